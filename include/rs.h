@@ -87,6 +87,10 @@ typedef enum {
 #define RS_DEV_ACCEPT 0x2u         /* accepted length outside 0..nd; clamped                     */
 #define RS_DEV_DRAFTS_PENDING 0x4u /* decode/verify/append with uncommitted drafts; drafts dropped */
 #define RS_DEV_TIMEOUT 0x8u        /* an in-kernel wait gave up after its time limit; results invalid */
+#define RS_DEV_LENGTH 0x10u        /* a request's length or context is out of range; request skipped      */
+#define RS_DEV_BLOCKS 0x20u        /* a state-cache block found no free slot or no place in the block table */
+#define RS_DEV_RECORDS 0x40u       /* a prefill continues a row with records buffered; request skipped    */
+#define RS_DEV_SLOT 0x80u          /* a row, start slot or block slot out of range; request (or block) skipped */
 
 /* RS_KDA: Gated DeltaNet with one decay per key channel, alpha_t in R^N
  * (a reading of Kimi Delta Attention, which [CSI] "Limits" names as
@@ -349,6 +353,143 @@ rs_status rs_eager_select(const rs_layer_desc *desc, int32_t *cur, const int32_t
 rs_status rs_decode_mamba2_noalloc(const rs_layer_desc *desc, const rs_state *st, const uint16_t *x,
                                    const float *dt, const float *A, const uint16_t *Bm,
                                    const uint16_t *Cm, const float *D, float *y, void *stream);
+
+/* ------------------------------------------------------------- ragged prefill
+ * Prompts reach the decode state through three calls, in this order:
+ *   rs_ragged_plan   once per batch: the packed rows' offsets, requests and
+ *                    positions, the chunks, and the state-cache blocks;
+ *   rs_qk_norm       per layer: norms (and rotates) the heads of q and k;
+ *   rs_prefill_gdn   per layer: the gated delta rule over all packed rows,
+ *                    ending in the checkpoints that rs_decode_gdn reads.
+ * A batch is R requests; request r brings lengths[r] new tokens (0 or more)
+ * after context[r] tokens that earlier calls have seen.  The rows of all
+ * requests are packed one after another, without padding between them.
+ * ctx/len below are context[r] and lengths[r].  Everything per request is
+ * known on the device only: no call waits for the GPU. */
+
+/* Tokens of one chunk.  Chunks are cut where a request's own position (context
+ * included) is a multiple of this, so a request of n tokens has at most
+ * n / 64 + 2 of them. */
+#define RS_CHUNK 64
+
+/* Shape of a ragged batch.  1 <= R <= 65535, 1 <= tokens_cap <= 2^30; block is
+ * 0 (no state cache) or a multiple of RS_CHUNK; max_blocks >= 1 and
+ * R * max_blocks <= 2^30 when block > 0; n_free >= 0. */
+typedef struct {
+    int32_t R;          /* requests                                             */
+    int32_t tokens_cap; /* rows of the packed arrays; a batch may fill fewer     */
+    int32_t block;      /* tokens between states that are kept for prefix reuse */
+    int32_t max_blocks; /* entries of one request's row of the block table       */
+    int32_t n_free;     /* entries of free_blocks                                */
+} rs_ragged_desc;
+
+/* A batch's plan; caller-allocated device arrays (rs_ragged_bytes_for). */
+typedef struct {
+    int32_t *cu_tokens;   /* [R+1] first packed row of each request              */
+    int32_t *cu_chunks;   /* [R+1] first chunk of each request                    */
+    int32_t *cu_blocks;   /* [R+1] blocks taken by the requests before            */
+    int32_t *token_req;   /* [tokens_cap] request of a row, -1 past the last row */
+    int32_t *token_pos;   /* [tokens_cap] ctx + index in the request, -1 past it */
+    int32_t *chunks;      /* [tokens_cap/64 + 2R][4] request, first row, rows,
+                             position / 64; {-1,0,0,0} past the last chunk        */
+    int32_t *block_table; /* [R][max_blocks] slot of the state after tokens
+                             [0, (j+1) block) of a request; NULL when block == 0  */
+    int32_t *counts;      /* [4] rows, chunks, blocks taken, requests with rows  */
+} rs_ragged;
+
+/* Byte sizes of the rs_ragged arrays (0 for an unused one). */
+typedef struct {
+    size_t cu_tokens, cu_chunks, cu_blocks, token_req, token_pos, chunks, block_table, counts;
+} rs_ragged_bytes;
+
+/* Validates the descriptor and fills the byte sizes.  Host only.
+ * Source: none (serving plumbing around the decode path). */
+rs_status rs_ragged_bytes_for(const rs_ragged_desc *rd, rs_ragged_bytes *out);
+
+/* Builds the plan from the requests' lengths, on the device.
+ * lengths, context: device int32 [R] (context NULL = all 0); free_blocks:
+ * device int32 [n_free], the state-cache slots that may be taken, used from
+ * the front in request order.  A block j is taken when its end lies in
+ * (ctx, ctx + len]; only the taken blocks' entries of block_table are written
+ * (-1 where free_blocks ran out, RS_DEV_BLOCKS).  A request with a negative
+ * length or context, or whose end passes 2^30 (RS_DEV_LENGTH), and every
+ * request from the first that does not fit into tokens_cap rows on
+ * (RS_DEV_CAPACITY), is planned with no rows.
+ * status: device word that receives RS_DEV_* bits.
+ * Source: none (serving plumbing around the decode path). */
+rs_status rs_ragged_plan(const rs_ragged_desc *rd, const int32_t *lengths, const int32_t *context,
+                         const int32_t *free_blocks, const rs_ragged *rg, uint32_t *status, void *stream);
+
+typedef enum {
+    RS_NORM_NONE = 0,
+    RS_NORM_L2 = 1, /* x / max(|x|, eps)                                  */
+    RS_NORM_RMS = 2 /* x / sqrt(mean(x^2) + eps), times the weight if any */
+} rs_norm;
+
+/* Heads to norm: T rows of Hq query heads and Hk key heads of D channels, bf16.
+ * D is 64, 128 or 256; Hq + Hk >= 1 (a side of no heads passes NULL); row
+ * strides in elements, multiples of 8 and at least heads * D. */
+typedef struct {
+    int32_t T, Hq, Hk, D;
+    int32_t norm;        /* rs_norm                                                    */
+    int32_t rot;         /* rotated leading channels: 0, or a multiple of 16 up to D    */
+    int32_t interleaved; /* 0: channel i turns with i + rot/2; 1: 2i turns with 2i + 1 */
+    float eps;
+    float weight_offset; /* the weight applied is wq + weight_offset                    */
+    float scale_q, scale_k;
+    int64_t ld_q, ld_k, ld_qo, ld_ko;
+} rs_qk_desc;
+
+/* Norms every head of q and k in fp32, applies weight (bf16 [D], NULL = none)
+ * and scale, turns the pairs (a, b) of the first rot channels by the angle
+ * t = positions[row] * inv_freq[pair], to (a cos t - b sin t, b cos t + a sin t),
+ * and rounds once.  positions: device int32 [T], any value (the angle is
+ * reduced exactly); inv_freq: device fp32 [rot/2], |inv_freq| < 2 pi.  A row's
+ * output may take its input's place (same pointer and stride).
+ * Source: [CSI] "How it works", Gated DeltaNet bullet (normed keys and
+ * queries are the inputs of a step); the rotation: none. */
+rs_status rs_qk_norm(const rs_qk_desc *desc, const uint16_t *q, const uint16_t *k, const uint16_t *wq,
+                     const uint16_t *wk, const float *inv_freq, const int32_t *positions, uint16_t *q_out,
+                     uint16_t *k_out, void *stream);
+
+/* Inputs of a prefill: packed rows q, k [rows][G][N] and v [rows][H][P] bf16
+ * with row strides in elements (multiples of 8), alpha >= 0 and beta fp32
+ * [rows][H]. */
+typedef struct {
+    const uint16_t *q, *k, *v;
+    const float *alpha, *beta;
+    int64_t ld_q, ld_k, ld_v;
+    const int32_t *rows;  /* device [R] state row of each request, all different; NULL: r      */
+    const int32_t *start; /* device [R] state to start from: a pool slot, -1 zeros, -2 the row's
+                             checkpoint; NULL: -2 for all                                     */
+    void *pool;           /* state-cache slots [n_pool][H][N][P], fp32 (bf16 with
+                             RS_PREC_SHARED_BF16); NULL with n_pool = 0                        */
+    int32_t n_pool;
+    int32_t max_len;      /* no request is longer (RS_DEV_LENGTH and skipped otherwise)         */
+} rs_prefill;
+
+/* Bytes of the scratch that rs_prefill_gdn needs (may be 0).  Host only.
+ * Source: none (library plumbing). */
+rs_status rs_prefill_bytes_for(const rs_layer_desc *desc, const rs_ragged_desc *rd, int32_t max_len, size_t *out);
+
+/* The gated delta rule over a planned batch: per request and head, from the
+ * starting state S and for each of its rows in order,
+ *   u_t = beta_t (v_t - alpha_t S k_t),  S <- alpha_t S + u_t k_t^T,  y_t = S q_t,
+ * the recurrence of rs_decode_gdn.  Writes y (bf16 [rows][H][P]), the final
+ * state to the request's checkpoint row (both copies in two-precision mode),
+ * with no records buffered, and the state at each taken block's end to its
+ * pool slot.  Requests without rows change nothing.  A row that continues its
+ * checkpoint must have no records or drafts buffered (rs_flush first;
+ * RS_DEV_RECORDS otherwise).  The plan must come from rs_ragged_plan with the
+ * same descriptor; block_table is read when rd->block > 0 and pool is given.
+ * RS_GDN only.  work: device scratch of rs_prefill_bytes_for bytes, 128-byte
+ * aligned.  States are accurate to fp32 rounding (operands of 22 bits, fp32 sums);
+ * y has fp16 operands beside fp32 sums and is rounded to bf16.  A NaN or an
+ * infinity stays in its request; there it may reach any row of its own chunk
+ * and all later ones.
+ * Source: [CSI] "How it works", Gated DeltaNet bullet (the recurrence). */
+rs_status rs_prefill_gdn(const rs_layer_desc *desc, const rs_state *st, const rs_ragged_desc *rd, const rs_ragged *rg,
+                         const rs_prefill *in, uint16_t *y, void *work, void *stream);
 
 #ifdef __cplusplus
 }

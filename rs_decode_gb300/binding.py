@@ -20,6 +20,9 @@ MAMBA2, GDN, KDA = 0, 1, 2
 PREC_FP32, PREC_TWO, PREC_SHARED_BF16 = 0, 1, 2
 U_BF16 = 0x10  # flag: GDN records keep u in bf16
 DEV_CAPACITY, DEV_ACCEPT, DEV_DRAFTS_PENDING = 0x1, 0x2, 0x4
+DEV_TIMEOUT, DEV_LENGTH, DEV_BLOCKS, DEV_RECORDS, DEV_SLOT = 0x8, 0x10, 0x20, 0x40, 0x80
+NORM_NONE, NORM_L2, NORM_RMS = 0, 1, 2
+CHUNK = 64  # rows of a chunk of the ragged prefill
 STATUS = {0: "RS_OK", 1: "RS_ERR_INVALID_ARG", 2: "RS_ERR_UNSUPPORTED", 3: "RS_ERR_CAPACITY",
           4: "RS_ERR_CUDA", 5: "RS_ERR_DEVICE", 6: "RS_ERR_STATIC_LIMIT"}
 STATIC_MAX_SEQS = 4096
@@ -47,6 +50,33 @@ class Inputs(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("x", "dt", "A", "Bm", "Cm", "D", "q", "k", "v", "alpha", "beta")]
 
 
+class RaggedDesc(ctypes.Structure):
+    _fields_ = [(n, _c_i32) for n in ("R", "tokens_cap", "block", "max_blocks", "n_free")]
+
+
+_RAGGED = ("cu_tokens", "cu_chunks", "cu_blocks", "token_req", "token_pos", "chunks", "block_table", "counts")
+
+
+class RaggedArrays(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in _RAGGED]
+
+
+class RaggedBytes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in _RAGGED]
+
+
+class QkDesc(ctypes.Structure):
+    _fields_ = [(n, _c_i32) for n in ("T", "Hq", "Hk", "D", "norm", "rot", "interleaved")] + \
+               [(n, ctypes.c_float) for n in ("eps", "weight_offset", "scale_q", "scale_k")] + \
+               [(n, ctypes.c_int64) for n in ("ld_q", "ld_k", "ld_qo", "ld_ko")]
+
+
+class Prefill(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("q", "k", "v", "alpha", "beta")] + \
+               [(n, ctypes.c_int64) for n in ("ld_q", "ld_k", "ld_v")] + \
+               [(n, _vp) for n in ("rows", "start", "pool")] + [("n_pool", _c_i32), ("max_len", _c_i32)]
+
+
 # name -> argtypes (restype is rs_status = int unless listed in _RESTYPE)
 _SIGS = {
     "rs_status_string": [ctypes.c_int],
@@ -72,6 +102,13 @@ _SIGS = {
     "rs_eager_verify_snapshots": [ctypes.POINTER(LayerDesc), _vp, _vp, ctypes.c_int,
                                   ctypes.POINTER(Inputs), _vp, _vp],
     "rs_eager_select": [ctypes.POINTER(LayerDesc), _vp, _vp, _vp, _vp],
+    "rs_ragged_bytes_for": [ctypes.POINTER(RaggedDesc), ctypes.POINTER(RaggedBytes)],
+    "rs_ragged_plan": [ctypes.POINTER(RaggedDesc), _vp, _vp, _vp, ctypes.POINTER(RaggedArrays), _vp, _vp],
+    "rs_qk_norm": [ctypes.POINTER(QkDesc)] + [_vp] * 9,
+    "rs_prefill_bytes_for": [ctypes.POINTER(LayerDesc), ctypes.POINTER(RaggedDesc), _c_i32,
+                             ctypes.POINTER(ctypes.c_size_t)],
+    "rs_prefill_gdn": [ctypes.POINTER(LayerDesc), ctypes.POINTER(State), ctypes.POINTER(RaggedDesc),
+                       ctypes.POINTER(RaggedArrays), ctypes.POINTER(Prefill), _vp, _vp, _vp],
     "rs_decode_mamba2_noalloc": [ctypes.POINTER(LayerDesc), ctypes.POINTER(State)] + [_vp] * 8,
 }
 _RESTYPE = {"rs_status_string": ctypes.c_char_p, "rs_version": ctypes.c_char_p,
@@ -252,3 +289,34 @@ def rs_decode_mamba2_noalloc(desc, state, x, dt, A, Bm, Cm, D, y, stream=None):
     _check("rs_decode_mamba2_noalloc", load().rs_decode_mamba2_noalloc(
         ctypes.byref(desc), ctypes.byref(state), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm),
         _ptr(D), _ptr(y), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- ragged prefill
+def rs_ragged_bytes_for(rd: RaggedDesc) -> RaggedBytes:
+    out = RaggedBytes()
+    _check("rs_ragged_bytes_for", load().rs_ragged_bytes_for(ctypes.byref(rd), ctypes.byref(out)))
+    return out
+
+
+def rs_ragged_plan(rd, lengths, context, free_blocks, arrays, status, stream=None):
+    _check("rs_ragged_plan", load().rs_ragged_plan(ctypes.byref(rd), _ptr(lengths), _ptr(context), _ptr(free_blocks),
+                                                   ctypes.byref(arrays), _ptr(status), _stream(stream)))
+
+
+def rs_qk_norm(desc, q, k, wq, wk, inv_freq, positions, q_out, k_out, stream=None):
+    """q, k, q_out, k_out are data pointers (their row strides are in desc)."""
+    _check("rs_qk_norm", load().rs_qk_norm(ctypes.byref(desc), q, k, _ptr(wq), _ptr(wk), _ptr(inv_freq),
+                                           _ptr(positions), q_out, k_out, _stream(stream)))
+
+
+def rs_prefill_bytes_for(desc, rd, max_len: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("rs_prefill_bytes_for", load().rs_prefill_bytes_for(ctypes.byref(desc), ctypes.byref(rd), max_len,
+                                                               ctypes.byref(out)))
+    return out.value
+
+
+def rs_prefill_gdn(desc, state, rd, arrays, prefill, y, work, stream=None):
+    _check("rs_prefill_gdn", load().rs_prefill_gdn(
+        ctypes.byref(desc), ctypes.byref(state), ctypes.byref(rd), ctypes.byref(arrays), ctypes.byref(prefill),
+        _ptr(y), _ptr(work), _stream(stream)))

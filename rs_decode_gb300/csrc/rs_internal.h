@@ -109,4 +109,16 @@ cudaError_t append_launch(const rs_layer_desc &d, const rs_state &st, int n, con
 cudaError_t select_launch(int B, int slots, int32_t *cur, const int32_t *accepted, uint32_t *status,
                           cudaStream_t s);
 
+// Ragged prefill (rs_ragged.cu, rs_qk.cu, rs_prefill.cu).
+// Entries of the chunk table: a request of n rows has at most n / 64 + 2 chunks.
+inline int ragged_chunks_cap(const rs_ragged_desc &rd) { return rd.tokens_cap / RS_CHUNK + 2 * rd.R; }
+cudaError_t ragged_plan_launch(const rs_ragged_desc &rd, const int32_t *lengths, const int32_t *context,
+                               const int32_t *free_blocks, const rs_ragged &rg, uint32_t *status, cudaStream_t s);
+cudaError_t qk_norm_launch(const rs_qk_desc &d, const uint16_t *q, const uint16_t *k, const uint16_t *wq,
+                           const uint16_t *wk, const float *inv_freq, const int32_t *positions, uint16_t *q_out,
+                           uint16_t *k_out, cudaStream_t s);
+size_t prefill_bytes(const rs_layer_desc &d, const rs_ragged_desc &rd, int max_len);
+cudaError_t prefill_launch(const rs_layer_desc &d, const rs_state &st, const rs_ragged_desc &rd, const rs_ragged &rg,
+                           const rs_prefill &in, uint16_t *y, void *work, cudaStream_t s);
+
 }  // namespace rs

@@ -1,0 +1,753 @@
+// The gated delta rule over a ragged batch of prompts (rs_prefill_gdn).
+//
+// Per request and value head, with state S [key n][value p] and rows t:
+//   u_t = beta_t (v_t - alpha_t S k_t),  S <- alpha_t S + u_t k_t^T,  y_t = S q_t.
+//
+// Chunked form.  Over the C = 64 rows of a chunk, with G_i the sum of
+// log alpha up to row i, the rows' u solve a unit lower triangular system and
+// everything else is a product:
+//   (I + A) u = diag(beta) R,  A_ij = beta_i e^(G_i - G_j) k_i.k_j  (j < i),
+//   R_i = v_i - e^(G_i) S k_i,
+//   y_i = e^(G_i) S q_i + sum_{j <= i} P_ij u_j,  P_ij = e^(G_i - G_j) q_i.k_j,
+//   S'  = e^(G_C) S + sum_j e^(G_C - G_j) u_j k_j^T.
+//
+// T = (I + A)^-1 diag(beta) and P do not depend on the state, so
+//   chunk_kernel  computes them for all chunks and heads at once, and
+//   scan_kernel   carries S through a request's chunks.
+// Decays enter as differences G_i - G_j only, so nothing overflows however
+// long a chunk's decay is; alpha = 0 is a decay of 2^-160, which is 0 in fp32.
+//
+// Precision.  The tensor cores multiply fp16 operands into fp32 sums.  Keys
+// and queries (bf16) are exact in fp16 once each row is scaled by a power of
+// two to a largest value in [1, 2).  What feeds the state (S, R, T, u) enters
+// as the sum of two fp16 terms, 22 bits, each row scaled by a power of two
+// likewise, so that states come out at fp32 accuracy (bf16 terms would leave
+// 16 bits at the same cost).  What feeds y alone (S and u once more, P) enters
+// as one fp16 term of 11 bits, below y's own rounding to 8.
+#include <cuda_fp16.h>
+
+#include "rs_common.cuh"
+#include "rs_internal.h"
+
+namespace rs {
+namespace {
+
+constexpr int C = RS_CHUNK;
+
+// What chunk_kernel leaves for scan_kernel.  All tiles have rows of 64 fp16
+// (128 bytes) with their 16-byte pieces in the order that shared-memory reads
+// want: piece c of row r at c ^ (r & 7).
+//
+// Per chunk and key head: keys, then queries, D / 64 tiles of 64 rows each.
+// Per chunk and value head:
+struct Record {
+    uint16_t t_hi[C * C], t_lo[C * C];  // T, row i scaled by 1 / (its power of two)
+    uint16_t p[C * C];                  // P without the rows' powers of two
+    float egk[C];  // e^(G_i) times key i's power of two
+    float eg[C];   // e^(G_i)
+    float su[C];   // T's and key i's powers of two: (T R)_i su_i = u_i times key i's power
+    float sq[C];   // query i's power of two
+    float ke[C];   // e^(G_C - G_i)
+};
+static_assert(sizeof(Record) == 25856, "records are copied in 16-byte pieces");
+
+struct PrefillParams {
+    int H, G, rep, prec;  // rep: value heads of a key head
+    int R, cap, ccap, block, max_blocks, n_pool, max_len, B;
+    float *hp;
+    uint16_t *lp;
+    int32_t *base, *h, *nd;
+    uint32_t *status;
+    rs_ragged rg;
+    const uint16_t *q, *k, *v;
+    const float *alpha, *beta;
+    long long ld_q, ld_k, ld_v;
+    const int32_t *rows, *start;
+    void *pool;
+    uint16_t *y;
+    Record *rec;  // [ccap][H]
+    unsigned char *tiles;  // [ccap][G] keys and queries of a chunk, fp16
+};
+
+// ---------------------------------------------------------------- warp matrix products
+// mma.sync m16n8k16: lane = 4 g + t.  A: rows g, g+8, columns 2t..2t+1 and
+// 2t+8..2t+9; B: rows (k) the same, column g; C: rows g, g+8, columns 2t..2t+1.
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r0), "r"(r1),
+                 "r"(r2), "r"(r3) : "memory");
+}
+// 16-byte copy global -> shared; zeros where `ok` is false (nothing is read).
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+
+// The power of two that brings a row whose largest magnitude is m into
+// [2^K, 2^(K+1)), and its inverse; 1 where m is not finite.
+template <int K>
+__device__ __forceinline__ void row_scale(float m, float &up, float &down) {
+    const int e = (int)(__float_as_uint(m) >> 23) & 255;
+    const int u = e == 255 ? 127 : min(254 + K - e, 253);  // biased exponent; its inverse is 254 - u >= 1
+    up = __uint_as_float((uint32_t)max(u, 1) << 23);
+    down = __uint_as_float((uint32_t)(254 - max(u, 1)) << 23);
+}
+
+// Two values as hi + lo: hi their fp16 rounding, lo the rounding of the rest.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack_h2(x, y);
+    const float2 h = unpack_h2(hi);
+    lo = pack_h2(x - h.x, y - h.y);
+}
+// The A fragment of 16 x 16 values held as two accumulator tiles, rows g and
+// g + 8 scaled by s0 and s1.
+__device__ __forceinline__ void split(const float (&c0)[4], const float (&c1)[4], float s0, float s1,
+                                      uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    split2(c0[0] * s0, c0[1] * s0, hi[0], lo[0]);
+    split2(c0[2] * s1, c0[3] * s1, hi[1], lo[1]);
+    split2(c1[0] * s0, c1[1] * s0, hi[2], lo[2]);
+    split2(c1[2] * s1, c1[3] * s1, hi[3], lo[3]);
+}
+// Largest magnitudes of rows g and g + 8 over N accumulator tiles.
+template <int N>
+__device__ __forceinline__ void row_max(const float (&c)[N][4], float &m0, float &m1) {
+    m0 = m1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        m0 = fmaxf(m0, fmaxf(fabsf(c[i][0]), fabsf(c[i][1])));
+        m1 = fmaxf(m1, fmaxf(fabsf(c[i][2]), fabsf(c[i][3])));
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        m0 = fmaxf(m0, __shfl_xor_sync(~0u, m0, o));
+        m1 = fmaxf(m1, __shfl_xor_sync(~0u, m1, o));
+    }
+}
+
+// Byte offset of 16-byte piece c (8 channels) of row r in 64-row tiles of 64 channels.
+__device__ __forceinline__ uint32_t piece(int r, int c) {
+    return (uint32_t)((c >> 3) * (C * 128) + r * 128 + (((c ^ r) & 7) << 4));
+}
+
+// Copies a chunk's 64 rows of D channels, zeros past the n rows it has.
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, long long ld, int n, int tid, int nt) {
+    constexpr int PIECES = D / 8;
+    for (int i = tid; i < C * PIECES; i += nt) {
+        const int r = i / PIECES, c = i % PIECES;
+        cp16(dst + piece(r, c), src + (r < n ? r : 0) * ld + c * 8, r < n);
+    }
+}
+
+// ---------------------------------------------------------------- chunk kernel
+// One CTA per chunk and key head: the products K K^T and Q K^T are shared by
+// the key head's value heads, whose decays and betas differ.  The triangular
+// inverse is fp32: four 16 x 16 diagonal blocks by substitution (a column per
+// thread), then twice  [[a,0],[c,b]]^-1 = [[a',0],[-b' c a', b']].
+constexpr int kChunkThreads = 128;
+constexpr int LDM = C + 4;  // fp32 matrices in shared memory: 16-byte rows, banks shifted by 4
+
+template <int D>
+struct ChunkSmem {
+    static constexpr int TILES = 2 * C * D * 2;
+    static constexpr int MATS = 2 * C * LDM * 4;
+    static constexpr int IMAGE = TILES > MATS ? TILES : MATS;  // the record's image after either
+    static constexpr int BYTES = IMAGE + (int)sizeof(Record) + 4 * C * 4;
+};
+
+// Sum of (value, error) pairs: the sum's rounding error goes into the error.
+__device__ __forceinline__ void add2(float &h, float &l, float h2, float l2) {
+    const float s = h + h2, b = s - h;
+    l = l + l2 + ((h - (s - b)) + (h2 - b));
+    h = s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_constant__ PrefillParams p) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int chunk = blockIdx.x / p.G, g = blockIdx.x - chunk * p.G;
+    if (chunk >= min(p.rg.counts[1], p.ccap)) return;
+    const int4 e = reinterpret_cast<const int4 *>(p.rg.chunks)[chunk];
+    const int n = e.z;
+    if (e.x < 0 || e.x >= p.R || n < 1 || n > C || e.y < 0 || e.y > p.cap - n) return;  // scan_kernel reports it
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t sK = smem_u32(smem), sQ = sK + C * D * 2;
+    load_tile<D>(sK, p.k + (long long)e.y * p.ld_k + g * D, p.ld_k, n, tid, kChunkThreads);
+    load_tile<D>(sQ, p.q + (long long)e.y * p.ld_q + g * D, p.ld_q, n, tid, kChunkThreads);
+    cp_async_wait_all();
+    __syncthreads();
+
+    // bf16 -> fp16 in place, two threads a row: each row scaled to [1, 2)
+    Record *image = reinterpret_cast<Record *>(smem + ChunkSmem<D>::IMAGE);
+    float *sk = reinterpret_cast<float *>(image + 1), *gh = sk + C, *gl = gh + C, *be = gl + C;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int row = tid >> 1, c0 = (tid & 1) * (D / 16);
+        uint4 v[D / 16];
+        float m = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            v[c] = *reinterpret_cast<const uint4 *>(smem + w * (C * D * 2) + piece(row, c0 + c));
+            float f[8];
+            unpack<uint16_t, 8>(v[c], f);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) m = fmaxf(m, fabsf(f[x]));
+        }
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+        float up, down;
+        row_scale<0>(m, up, down);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            float f[8];
+            unpack<uint16_t, 8>(v[c], f);
+            *reinterpret_cast<uint4 *>(smem + w * (C * D * 2) + piece(row, c0 + c)) =
+                make_uint4(pack_h2(f[0] * up, f[1] * up), pack_h2(f[2] * up, f[3] * up),
+                           pack_h2(f[4] * up, f[5] * up), pack_h2(f[6] * up, f[7] * up));
+        }
+        if ((tid & 1) == 0) (w ? image->sq : sk)[row] = down;
+    }
+    __syncthreads();
+    {
+        uint4 *out = reinterpret_cast<uint4 *>(p.tiles + ((size_t)chunk * p.G + g) * (2 * C * D * 2));
+        for (int i = tid; i < 2 * C * D * 2 / 16; i += kChunkThreads) out[i] = reinterpret_cast<const uint4 *>(smem)[i];
+    }
+
+    // rows 16 warp.. of K K^T and Q K^T, up to the diagonal
+    float kk[8][4] = {}, qk[8][4] = {};
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+        uint32_t a[4], b[4], w[4];
+        const int ar = warp * 16 + (lane & 15), ac = 2 * x + (lane >> 4);
+        ldsm4(a, sK + piece(ar, ac));
+        ldsm4(b, sQ + piece(ar, ac));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j <= warp) {
+                ldsm4(w, sK + piece(16 * j + (lane & 7) + ((lane & 16) >> 1), 2 * x + ((lane >> 3) & 1)));
+                mma_f16(kk[2 * j], a, w[0], w[1]);
+                mma_f16(kk[2 * j + 1], a, w[2], w[3]);
+                mma_f16(qk[2 * j], b, w[0], w[1]);
+                mma_f16(qk[2 * j + 1], b, w[2], w[3]);
+            }
+        }
+    }
+    __syncthreads();  // the tiles' place is the matrices' from here
+
+    float *A = reinterpret_cast<float *>(smem), *X = A + C * LDM;
+
+    for (int r = 0; r < p.rep; ++r) {
+        const int hv = g * p.rep + r;
+        if (warp == 0) {
+            // two rows a lane; sums of log2 alpha as (value, error) pairs, so
+            // that differences of large sums keep their low bits
+            float h[2], l[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                const bool in = t < n;
+                const float a = in ? p.alpha[(long long)(e.y + t) * p.H + hv] : 1.f;
+                be[t] = in ? p.beta[(long long)(e.y + t) * p.H + hv] : 0.f;
+                const float x = log2f(a);
+                h[i] = x < -160.f ? -160.f : x;
+            }
+            add2(h[1], l[1], h[0], l[0]);
+            float sh = h[1], sl = l[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float xh = __shfl_up_sync(~0u, sh, o), xl = __shfl_up_sync(~0u, sl, o);
+                if (lane >= o) add2(sh, sl, xh, xl);
+            }
+            float ph = __shfl_up_sync(~0u, sh, 1), pl = __shfl_up_sync(~0u, sl, 1);
+            if (lane == 0) ph = pl = 0.f;
+            add2(h[0], l[0], ph, pl);
+            const float ch = __shfl_sync(~0u, sh, 31), cl = __shfl_sync(~0u, sl, 31);
+            gh[2 * lane] = h[0], gl[2 * lane] = l[0], gh[2 * lane + 1] = sh, gl[2 * lane + 1] = sl;
+            const float e0 = exp2f(h[0] + l[0]), e1 = exp2f(sh + sl);
+            image->eg[2 * lane] = e0, image->eg[2 * lane + 1] = e1;
+            image->egk[2 * lane] = e0 * sk[2 * lane], image->egk[2 * lane + 1] = e1 * sk[2 * lane + 1];
+            image->ke[2 * lane] = exp2f((ch - h[0]) + (cl - l[0]));
+            image->ke[2 * lane + 1] = exp2f((ch - sh) + (cl - sl));
+        }
+        __syncthreads();
+        // A and P of this warp's rows
+        const int i0 = warp * 16 + (lane >> 2);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = i0 + 8 * hf, j = nt * 8 + (lane & 3) * 2;
+                float a[2] = {0.f, 0.f}, pv[2] = {0.f, 0.f};
+                if (nt <= 2 * warp + 1) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (j + x <= i) {
+                            const float d = exp2f((gh[i] - gh[j + x]) + (gl[i] - gl[j + x]));
+                            pv[x] = d * qk[nt][2 * hf + x];
+                            a[x] = j + x < i ? be[i] * d * (kk[nt][2 * hf + x] * sk[i] * sk[j + x]) : 0.f;
+                        }
+                    }
+                }
+                *reinterpret_cast<float2 *>(A + i * LDM + j) = make_float2(a[0], a[1]);
+                *reinterpret_cast<float2 *>(X + i * LDM + j) = make_float2(0.f, 0.f);
+                *reinterpret_cast<uint32_t *>(reinterpret_cast<unsigned char *>(image->p) + piece(i, nt) +
+                                              (lane & 3) * 4) = pack_h2(pv[0], pv[1]);
+            }
+        }
+        __syncthreads();
+        if (tid < C) {  // diagonal blocks: column tid of block tid / 16
+            const int b = tid & ~15, col = tid & 15;
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float s = i == col ? 1.f : 0.f;
+#pragma unroll
+                for (int m = 0; m < i; ++m) s = fmaf(-A[(b + i) * LDM + b + m], x[m], s);
+                x[i] = s;
+                X[(b + i) * LDM + b + col] = s;
+            }
+        }
+        __syncthreads();
+        {  // two 32 x 32 blocks; the product c a' waits in the zero block above the diagonal
+            const int pr = tid >> 6, t = tid & 63, i = t >> 2, c4 = (t & 3) * 4, o = 32 * pr;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int m = 0; m < 16; ++m) {
+                const float a = A[(o + 16 + i) * LDM + o + m];
+                const float4 x = *reinterpret_cast<const float4 *>(X + (o + m) * LDM + o + c4);
+                s.x = fmaf(a, x.x, s.x), s.y = fmaf(a, x.y, s.y), s.z = fmaf(a, x.z, s.z), s.w = fmaf(a, x.w, s.w);
+            }
+            *reinterpret_cast<float4 *>(X + (o + i) * LDM + o + 16 + c4) = s;
+            __syncthreads();
+            s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int m = 0; m < 16; ++m) {
+                const float a = -X[(o + 16 + i) * LDM + o + 16 + m];
+                const float4 x = *reinterpret_cast<const float4 *>(X + (o + m) * LDM + o + 16 + c4);
+                s.x = fmaf(a, x.x, s.x), s.y = fmaf(a, x.y, s.y), s.z = fmaf(a, x.z, s.z), s.w = fmaf(a, x.w, s.w);
+            }
+            *reinterpret_cast<float4 *>(X + (o + 16 + i) * LDM + o + c4) = s;
+            __syncthreads();
+            *reinterpret_cast<float4 *>(X + (o + i) * LDM + o + 16 + c4) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        __syncthreads();
+        {  // the 64 x 64 block, the same way
+            const int i = (tid >> 3) * 2, c4 = (tid & 7) * 4;
+            float4 s[2] = {};
+#pragma unroll 8
+            for (int m = 0; m < 32; ++m) {
+                const float4 x = *reinterpret_cast<const float4 *>(X + m * LDM + c4);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float a = A[(32 + i + y) * LDM + m];
+                    s[y].x = fmaf(a, x.x, s[y].x), s[y].y = fmaf(a, x.y, s[y].y);
+                    s[y].z = fmaf(a, x.z, s[y].z), s[y].w = fmaf(a, x.w, s[y].w);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) *reinterpret_cast<float4 *>(X + (i + y) * LDM + 32 + c4) = s[y];
+            __syncthreads();
+            s[0] = s[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int m = 0; m < 32; ++m) {
+                const float4 x = *reinterpret_cast<const float4 *>(X + m * LDM + 32 + c4);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float a = -X[(32 + i + y) * LDM + 32 + m];
+                    s[y].x = fmaf(a, x.x, s[y].x), s[y].y = fmaf(a, x.y, s[y].y);
+                    s[y].z = fmaf(a, x.z, s[y].z), s[y].w = fmaf(a, x.w, s[y].w);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) *reinterpret_cast<float4 *>(X + (32 + i + y) * LDM + c4) = s[y];
+        }
+        __syncthreads();
+        // T = X diag(beta), each row scaled and split in two; 8 threads a row
+        for (int i = tid; i < C * C / 8; i += kChunkThreads) {
+            const int row = i >> 3, c = i & 7;
+            float t[8], m = 0.f, up, down;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int j = c * 8 + x;
+                t[x] = j <= row ? X[row * LDM + j] * be[j] : 0.f;
+                m = fmaxf(m, fabsf(t[x]));
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+            row_scale<8>(m, up, down);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) split2(t[2 * x] * up, t[2 * x + 1] * up, hi[x], lo[x]);
+            *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(image->t_hi) + piece(row, c)) =
+                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(image->t_lo) + piece(row, c)) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (c == 0) image->su[row] = down * sk[row];
+        }
+        __syncthreads();
+        uint4 *out = reinterpret_cast<uint4 *>(p.rec + (size_t)chunk * p.H + hv);
+        const uint4 *img = reinterpret_cast<const uint4 *>(image);
+        for (int i = tid; i < (int)sizeof(Record) / 16; i += kChunkThreads) out[i] = img[i];
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- scan kernel
+// A warp owns 16 value columns of a head's state and carries them through the
+// request's chunks on its own: S^T (16 x D) lives in the accumulators of
+// m16n8k16 products, whose register layout is also that of their A operand, so
+//   S^T K^T, S^T Q^T  ->  R^T  ->  u^T = R^T T^T  ->  y^T += u^T P^T,  S^T += u^T K
+// pass from product to product without leaving the registers or meeting
+// another warp.  K, Q, T, P and V come through two shared-memory stages.
+// Operands that enter the state (S, R, T, u) are split in two bf16 terms; k, q
+// and v are bf16 inputs and exact.
+template <int D, int NW>
+struct ScanSmem {
+    static constexpr int TILE = C * D * 2;
+    static constexpr int VT = NW * C * 32;  // per warp: 64 rows of its 16 columns
+    static constexpr int REC = 2 * TILE + VT;
+    static constexpr int STAGE = REC + (int)sizeof(Record);
+    static constexpr int BYTES = 2 * STAGE;
+};
+
+struct Request {
+    int n, row0, ctx, chunk0, nch, srow, start;
+    bool ok;
+};
+
+// A request's facts, checked; bits of what is wrong go to the status word.
+__device__ __forceinline__ Request load_request(const PrefillParams &p, int r, bool report) {
+    Request q = {};
+    const int a = p.rg.cu_tokens[r], b = p.rg.cu_tokens[r + 1];
+    q.n = b - a;
+    q.row0 = a;
+    if (q.n == 0) return q;
+    unsigned bits = 0;
+    if (q.n < 0 || a < 0 || b > p.cap || q.n > p.max_len) {
+        bits = RS_DEV_LENGTH;
+    } else {
+        q.ctx = p.rg.token_pos[a];
+        q.chunk0 = p.rg.cu_chunks[r];
+        q.nch = p.rg.cu_chunks[r + 1] - q.chunk0;
+        if (q.ctx < 0 || q.ctx > (1 << 30) || q.chunk0 < 0 || q.chunk0 + q.nch > p.ccap ||
+            q.nch != (q.ctx + q.n + C - 1) / C - q.ctx / C)
+            bits = RS_DEV_LENGTH;
+    }
+    q.srow = p.rows ? p.rows[r] : r;
+    q.start = p.start ? p.start[r] : -2;
+    if (q.srow < 0 || q.srow >= p.B || q.start < -2 || q.start >= p.n_pool)
+        bits |= RS_DEV_SLOT;
+    else if (q.start == -2 && (p.h[q.srow] != 0 || p.nd[q.srow] != 0))
+        bits |= RS_DEV_RECORDS;
+    q.ok = bits == 0;
+    if (bits && report) atomicOr(p.status, bits);
+    return q;
+}
+
+template <int D, int NW>
+__global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ PrefillParams p) {
+    using M = ScanSmem<D, NW>;
+    constexpr int SPLIT = D / (16 * NW);  // CTAs of one head
+    constexpr int NT = NW * 32;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int part = blockIdx.x % SPLIT, hr = blockIdx.x / SPLIT;
+    const int h = hr % p.H, r = hr / p.H;
+    const Request rq = load_request(p, r, h == 0 && part == 0 && tid == 0);
+    if (!rq.ok) return;
+    const int g = h / p.rep;
+    const int col0 = (part * NW + warp) * 16;
+    const uint32_t s0 = smem_u32(smem);
+
+    // chunk i of the request: its first row and row count
+    const int head_rows = min(rq.n, C - rq.ctx % C);
+    auto first_row = [&](int i) { return i == 0 ? 0 : head_rows + (i - 1) * C; };
+    auto fetch = [&](int i, uint32_t st) {
+        const int at = first_row(i), n = min(i == 0 ? head_rows : C, rq.n - at);
+        const long long row = rq.row0 + at;
+        const unsigned char *kq = p.tiles + ((size_t)(rq.chunk0 + i) * p.G + g) * (2 * M::TILE);
+        for (int x = tid; x < 2 * M::TILE / 16; x += NT) cp16(st + x * 16, kq + x * 16, true);
+        const uint16_t *v = p.v + row * p.ld_v + h * D + part * NW * 16;
+        for (int x = tid; x < C * NW * 2; x += NT) {
+            const int t = x / (NW * 2), c = x % (NW * 2);
+            cp16(st + 2 * M::TILE + (c >> 1) * (C * 32) + t * 32 + (((c & 1) ^ ((t >> 2) & 1)) << 4),
+                 v + (t < n ? t : 0) * p.ld_v + c * 8, t < n);
+        }
+        const unsigned char *rec = reinterpret_cast<const unsigned char *>(p.rec + (size_t)(rq.chunk0 + i) * p.H + h);
+        for (int x = tid; x < (int)sizeof(Record) / 16; x += NT) cp16(st + M::REC + x * 16, rec + x * 16, true);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(0, s0);
+
+    // the starting state: S^T[p][n], rows p = col0 + gr (+8), columns n = 8 nt + 2 tq (+1)
+    const int gr = lane >> 2, tq = lane & 3;
+    float S[D / 8][4];
+    {
+        const bool cont = rq.start == -2, lowp = p.prec == RS_PREC_SHARED_BF16;
+        const size_t slab = (cont ? (size_t)rq.srow * p.H + h : (size_t)max(rq.start, 0) * p.H + h) * D * D;
+        const float *f = (cont ? p.hp : static_cast<const float *>(p.pool));
+        const uint16_t *b = (cont ? p.lp : static_cast<const uint16_t *>(p.pool));
+#pragma unroll
+        for (int nt = 0; nt < D / 8; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const size_t o = slab + (size_t)(nt * 8 + tq * 2 + (x & 1)) * D + col0 + gr + 8 * (x >> 1);
+                S[nt][x] = rq.start == -1 ? 0.f : lowp ? bf2f(b[o]) : f[o];
+            }
+    }
+    auto store_state = [&](float *f, uint16_t *b, size_t slab) {
+#pragma unroll
+        for (int nt = 0; nt < D / 8; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const size_t o = slab + (size_t)(nt * 8 + tq * 2 + (x & 1)) * D + col0 + gr + 8 * (x >> 1);
+                if (f) f[o] = S[nt][x];
+                if (b) b[o] = (uint16_t)f2bf(S[nt][x]);
+            }
+    };
+
+    for (int i = 0; i < rq.nch; ++i) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // this chunk's stage has landed, and every warp is done with the other one
+        const uint32_t st = s0 + (i & 1) * M::STAGE;
+        if (i + 1 < rq.nch) fetch(i + 1, s0 + ((i + 1) & 1) * M::STAGE);
+        const uint32_t sK = st, sQ = st + M::TILE, sV = st + 2 * M::TILE + warp * (C * 32);
+        const uint32_t sTh = st + M::REC, sTl = sTh + C * C * 2, sP = sTl + C * C * 2;
+        const Record *rec = reinterpret_cast<const Record *>(smem + (i & 1) * M::STAGE + M::REC);
+
+        // S^T K^T and S^T Q^T: columns are the chunk's rows
+        float X[8][4] = {}, Z[8][4] = {};
+        float ms0, ms1, su0, su1, sd0, sd1;
+        row_max(S, ms0, ms1);
+        row_scale<14>(ms0, su0, sd0);
+        row_scale<14>(ms1, su1, sd1);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+            uint32_t hi[4], lo[4], b[4];
+            split(S[2 * x], S[2 * x + 1], su0, su1, hi, lo);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t o = piece(16 * j + (lane & 7) + ((lane & 16) >> 1), 2 * x + ((lane >> 3) & 1));
+                ldsm4(b, sK + o);
+                mma_f16(X[2 * j], hi, b[0], b[1]);
+                mma_f16(X[2 * j + 1], hi, b[2], b[3]);
+                mma_f16(X[2 * j], lo, b[0], b[1]);
+                mma_f16(X[2 * j + 1], lo, b[2], b[3]);
+                ldsm4(b, sQ + o);
+                mma_f16(Z[2 * j], hi, b[0], b[1]);
+                mma_f16(Z[2 * j + 1], hi, b[2], b[3]);
+            }
+        }
+        // R^T = V^T - e^G S^T K^T, and the state's part of y
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t v[4];
+            const int t = 16 * j + (lane & 7) + ((lane & 16) >> 1), c = (lane >> 3) & 1;
+            ldsm4t(v, sV + t * 32 + ((c ^ ((t >> 2) & 1)) << 4));
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int nt = 2 * j + hf;
+                const float2 ek = *reinterpret_cast<const float2 *>(rec->egk + nt * 8 + tq * 2);
+                const float2 eg = *reinterpret_cast<const float2 *>(rec->eg + nt * 8 + tq * 2);
+                X[nt][0] = __uint_as_float(v[2 * hf] << 16) - ek.x * (X[nt][0] * sd0);
+                X[nt][1] = __uint_as_float(v[2 * hf] & 0xffff0000u) - ek.y * (X[nt][1] * sd0);
+                X[nt][2] = __uint_as_float(v[2 * hf + 1] << 16) - ek.x * (X[nt][2] * sd1);
+                X[nt][3] = __uint_as_float(v[2 * hf + 1] & 0xffff0000u) - ek.y * (X[nt][3] * sd1);
+                Z[nt][0] *= eg.x * sd0, Z[nt][1] *= eg.y * sd0, Z[nt][2] *= eg.x * sd1, Z[nt][3] *= eg.y * sd1;
+            }
+        }
+        // u^T = R^T T^T; T is lower triangular.  u carries its key's power of two.
+        float U[8][4] = {};
+        {
+            float m0, m1, u0, u1, d0, d1;
+            row_max(X, m0, m1);
+            row_scale<14>(m0, u0, d0);
+            row_scale<14>(m1, u1, d1);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t hi[4], lo[4], b[4];
+                split(X[2 * x], X[2 * x + 1], u0, u1, hi, lo);
+#pragma unroll
+                for (int j = x; j < 4; ++j) {
+                    const uint32_t o = piece(16 * j + (lane & 7) + ((lane & 16) >> 1), 2 * x + ((lane >> 3) & 1));
+                    ldsm4(b, sTh + o);
+                    mma_f16(U[2 * j], hi, b[0], b[1]);
+                    mma_f16(U[2 * j + 1], hi, b[2], b[3]);
+                    mma_f16(U[2 * j], lo, b[0], b[1]);
+                    mma_f16(U[2 * j + 1], lo, b[2], b[3]);
+                    ldsm4(b, sTl + o);
+                    mma_f16(U[2 * j], hi, b[0], b[1]);
+                    mma_f16(U[2 * j + 1], hi, b[2], b[3]);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                const float2 su = *reinterpret_cast<const float2 *>(rec->su + nt * 8 + tq * 2);
+                U[nt][0] *= su.x * d0, U[nt][1] *= su.y * d0, U[nt][2] *= su.x * d1, U[nt][3] *= su.y * d1;
+            }
+        }
+        // y^T = (e^G S^T Q^T + u^T P^T) with the queries' powers of two
+        {
+            float m0, m1, u0, u1, d0, d1;
+            row_max(U, m0, m1);
+            row_scale<14>(m0, u0, d0);
+            row_scale<14>(m1, u1, d1);
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) X[nt][0] = X[nt][1] = X[nt][2] = X[nt][3] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t a[4] = {pack_h2(U[2 * x][0] * u0, U[2 * x][1] * u0), pack_h2(U[2 * x][2] * u1, U[2 * x][3] * u1),
+                                       pack_h2(U[2 * x + 1][0] * u0, U[2 * x + 1][1] * u0),
+                                       pack_h2(U[2 * x + 1][2] * u1, U[2 * x + 1][3] * u1)};
+                uint32_t b[4];
+#pragma unroll
+                for (int j = x; j < 4; ++j) {
+                    ldsm4(b, sP + piece(16 * j + (lane & 7) + ((lane & 16) >> 1), 2 * x + ((lane >> 3) & 1)));
+                    mma_f16(X[2 * j], a, b[0], b[1]);
+                    mma_f16(X[2 * j + 1], a, b[2], b[3]);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                const float2 sq = *reinterpret_cast<const float2 *>(rec->sq + nt * 8 + tq * 2);
+                Z[nt][0] = (Z[nt][0] + X[nt][0] * d0) * sq.x, Z[nt][1] = (Z[nt][1] + X[nt][1] * d0) * sq.y;
+                Z[nt][2] = (Z[nt][2] + X[nt][2] * d1) * sq.x, Z[nt][3] = (Z[nt][3] + X[nt][3] * d1) * sq.y;
+            }
+        }
+        // S^T = e^(G_C) S^T + (e^(G_C - G) u)^T K, summed at u's row scale.  Where u is
+        // below 2^-30 of the row's state, the state's size sets the scale: at u's own
+        // the sum could overflow, and u's lost bits are far below the state's last one.
+        {
+            const float all = rec->eg[C - 1];
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                const float2 ke = *reinterpret_cast<const float2 *>(rec->ke + nt * 8 + tq * 2);
+                U[nt][0] *= ke.x, U[nt][1] *= ke.y, U[nt][2] *= ke.x, U[nt][3] *= ke.y;
+            }
+            float m0, m1, u0, u1, d0, d1;
+            row_max(U, m0, m1);
+            row_scale<14>(fmaxf(m0, all * ms0 * 9.31322574615478515625e-10f), u0, d0);
+            row_scale<14>(fmaxf(m1, all * ms1 * 9.31322574615478515625e-10f), u1, d1);
+#pragma unroll
+            for (int nt = 0; nt < D / 8; ++nt) {
+                S[nt][0] *= all * u0, S[nt][1] *= all * u0, S[nt][2] *= all * u1, S[nt][3] *= all * u1;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t hi[4], lo[4], b[4];
+                split(U[2 * x], U[2 * x + 1], u0, u1, hi, lo);
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    ldsm4t(b, sK + piece(16 * x + (lane & 15), 2 * j + (lane >> 4)));
+                    mma_f16(S[2 * j], hi, b[0], b[1]);
+                    mma_f16(S[2 * j + 1], hi, b[2], b[3]);
+                    mma_f16(S[2 * j], lo, b[0], b[1]);
+                    mma_f16(S[2 * j + 1], lo, b[2], b[3]);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < D / 8; ++nt) S[nt][0] *= d0, S[nt][1] *= d0, S[nt][2] *= d1, S[nt][3] *= d1;
+        }
+        // y through the warp's own V rows, to whole sectors
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = 16 * j + (lane & 7) + ((lane & 16) >> 1), c = (lane >> 3) & 1;
+            stsm4t(sV + t * 32 + ((c ^ ((t >> 2) & 1)) << 4), pack_bf2(Z[2 * j][0], Z[2 * j][1]),
+                   pack_bf2(Z[2 * j][2], Z[2 * j][3]), pack_bf2(Z[2 * j + 1][0], Z[2 * j + 1][1]),
+                   pack_bf2(Z[2 * j + 1][2], Z[2 * j + 1][3]));
+        }
+        __syncwarp();
+        const int at = first_row(i), n = min(i == 0 ? head_rows : C, rq.n - at);
+        uint16_t *y = p.y + ((long long)(rq.row0 + at) * p.H + h) * D + col0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int t = x * 16 + (lane >> 1), c = lane & 1;
+            if (t < n) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(smem + (sV - s0) + t * 32 + ((c ^ ((t >> 2) & 1)) << 4));
+                *reinterpret_cast<uint4 *>(y + (long long)t * p.H * D + c * 8) = w;
+            }
+        }
+        // the state at a block's end
+        if (p.block && p.pool) {
+            const int end = rq.ctx + at + n;
+            if (end % p.block == 0) {
+                const int j = end / p.block - 1;
+                const int slot = j < p.max_blocks ? p.rg.block_table[(size_t)r * p.max_blocks + j] : -1;
+                if (slot >= 0 && slot < p.n_pool) {
+                    const size_t slab = ((size_t)slot * p.H + h) * D * D;
+                    if (p.prec == RS_PREC_SHARED_BF16)
+                        store_state(nullptr, static_cast<uint16_t *>(p.pool), slab);
+                    else
+                        store_state(static_cast<float *>(p.pool), nullptr, slab);
+                } else if (slot != -1 && h == 0 && part == 0 && tid == 0) {
+                    atomicOr(p.status, RS_DEV_SLOT);
+                }
+            }
+        }
+    }
+    store_state(p.hp, p.lp, ((size_t)rq.srow * p.H + h) * D * D);
+    // a fresh start drops what the row had buffered (a continued row has nothing)
+    if (rq.start != -2 && h == 0 && part == 0 && tid == 0) p.base[rq.srow] = p.h[rq.srow] = p.nd[rq.srow] = 0;
+}
+
+template <int D, int NW>
+cudaError_t scan_launch(const PrefillParams &p, cudaStream_t s) {
+    static SmemGrants grants;
+    const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&scan_kernel<D, NW>), ScanSmem<D, NW>::BYTES, grants);
+    if (e != cudaSuccess) return e;
+    scan_kernel<D, NW><<<p.R * p.H * (D / (16 * NW)), NW * 32, ScanSmem<D, NW>::BYTES, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(const PrefillParams &p, cudaStream_t s) {
+    static SmemGrants grants;
+    cudaError_t e = grant_smem(reinterpret_cast<const void *>(&chunk_kernel<D>), ChunkSmem<D>::BYTES, grants);
+    if (e != cudaSuccess) return e;
+    chunk_kernel<D><<<p.ccap * p.G, kChunkThreads, ChunkSmem<D>::BYTES, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // a head on one CTA, or on two-warp CTAs where the heads alone would leave SMs idle
+    if (p.R * p.H <= 152) return scan_launch<D, 2>(p, s);
+    return scan_launch<D, D / 16>(p, s);
+}
+
+}  // namespace
+
+size_t prefill_bytes(const rs_layer_desc &d, const rs_ragged_desc &rd, int) {
+    return (size_t)ragged_chunks_cap(rd) * (d.H * sizeof(Record) + (size_t)d.G * 2 * C * d.N * 2);
+}
+
+cudaError_t prefill_launch(const rs_layer_desc &d, const rs_state &st, const rs_ragged_desc &rd, const rs_ragged &rg,
+                           const rs_prefill &in, uint16_t *y, void *work, cudaStream_t s) {
+    PrefillParams p = {};
+    p.H = d.H, p.G = d.G, p.rep = d.H / d.G, p.prec = d.precision & ~RS_U_BF16, p.B = d.B;
+    p.R = rd.R, p.cap = rd.tokens_cap, p.ccap = ragged_chunks_cap(rd), p.block = rd.block, p.max_blocks = rd.max_blocks;
+    p.n_pool = in.n_pool, p.max_len = in.max_len;
+    p.hp = st.ckpt_hp, p.lp = st.ckpt_lp, p.base = st.base, p.h = st.h, p.nd = st.nd, p.status = st.status;
+    p.rg = rg;
+    p.q = in.q, p.k = in.k, p.v = in.v, p.alpha = in.alpha, p.beta = in.beta;
+    p.ld_q = in.ld_q, p.ld_k = in.ld_k, p.ld_v = in.ld_v;
+    p.rows = in.rows, p.start = in.start, p.pool = in.pool, p.y = y, p.rec = static_cast<Record *>(work);
+    p.tiles = static_cast<unsigned char *>(work) + (size_t)p.ccap * d.H * sizeof(Record);
+    return d.P == 128 ? launch<128>(p, s) : launch<64>(p, s);
+}
+
+}  // namespace rs

@@ -24,6 +24,15 @@ def to_device(d: dict, device="cuda", non_blocking: bool = False) -> dict:
     return out
 
 
+def packed_stride(t: torch.Tensor, rows: int, heads: int, d: int, name: str) -> int:
+    """Row stride in elements of a packed [rows, heads, d] bf16 tensor whose heads lie side by side."""
+    if t.element_size() != 2 or t.dim() != 3 or t.shape[0] < rows or tuple(t.shape[1:]) != (heads, d):
+        raise ValueError(f"{name} must be bf16 [{rows}, {heads}, {d}], got {t.dtype} {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
 class Layer:
     def __init__(self, kind: str, B: int, H: int, G: int, P: int, N: int, L: int, T_max: int = 0,
                  capacity: int | None = None, precision: int = rb.PREC_FP32, device="cuda"):
@@ -99,6 +108,52 @@ class Layer:
             out = torch.empty(self.shape, dtype=torch.float32, device=self.base.device)
         rb.rs_materialize(self.desc, self.state, out, stream)
         return out
+
+    # ---------------------------------------------------------------- prefill
+    def prefill_workspace(self, ragged, max_len: int) -> torch.Tensor | None:
+        """Scratch of ``prefill`` for this plan shape; may serve many calls, one after another."""
+        n = rb.rs_prefill_bytes_for(self.desc, ragged.desc, max_len)
+        return torch.empty(n, dtype=torch.uint8, device=self.base.device) if n else None
+
+    def prefill(self, ragged, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Tensor,
+                beta: torch.Tensor, *, max_len: int, rows: torch.Tensor | None = None,
+                start: torch.Tensor | None = None, pool: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                work: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The gated delta rule over a planned batch (``prefill.Ragged``), into this layer's state.
+
+        q, k [rows, G, N], v [rows, H, P] bf16 (torch.bfloat16, or int16 bit
+        patterns), each head contiguous, rows at any stride; alpha, beta fp32
+        [rows, H].  rows, start: int32 [R] (see include/rs.h); pool
+        [n, H, N, P], fp32 or, for a shared-bf16 layer, bf16.  Returns y
+        torch.bfloat16 [rows, H, P].  Without y and work they are allocated
+        on the current stream, which then has to be the one the call runs on."""
+        T, H, G, N, P = ragged.desc.tokens_cap, self.H, self.G, self.desc.N, self.desc.P
+        lds = [packed_stride(t, T, heads, d, name)
+               for t, heads, d, name in ((q, G, N, "q"), (k, G, N, "k"), (v, H, P, "v"))]
+        for t, name in ((alpha, "alpha"), (beta, "beta")):
+            if t.dtype != torch.float32 or t.shape[0] < T or tuple(t.shape[1:]) != (H,):
+                raise ValueError(f"{name} must be float32 [{T}, {H}], got {t.dtype} {tuple(t.shape)}")
+        R = ragged.desc.R
+        for t, name in ((rows, "rows"), (start, "start")):
+            if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (R,)):
+                raise ValueError(f"{name} must be int32 [{R}]")
+        if pool is not None:
+            width = 2 if self.desc.precision & 0xf == rb.PREC_SHARED_BF16 else 4
+            if tuple(pool.shape[1:]) != (H, N, P) or pool.element_size() != width:
+                raise ValueError(f"pool must be [n, {H}, {N}, {P}] of {width}-byte values")
+        if y is None:
+            y = torch.empty(T, H, P, dtype=torch.bfloat16, device=self.base.device)
+        elif y.element_size() != 2 or y.shape[0] < T or tuple(y.shape[1:]) != (H, P):
+            raise ValueError(f"y must be bf16 [{T}, {H}, {P}]")
+        if work is None:
+            work = self.prefill_workspace(ragged, max_len)
+        elif work.numel() * work.element_size() < rb.rs_prefill_bytes_for(self.desc, ragged.desc, max_len):
+            raise ValueError("work is smaller than prefill_workspace() of this plan")
+        p = rb._ptr
+        args = rb.Prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), p(alpha), p(beta), *lds, p(rows), p(start),
+                          p(pool), 0 if pool is None else pool.shape[0], max_len)
+        rb.rs_prefill_gdn(self.desc, self.state, ragged.desc, ragged.arrays, args, y, work, stream)
+        return y
 
     def status(self, clear: bool = True, stream=None) -> int:
         return rb.rs_get_status(self.state, clear, stream)

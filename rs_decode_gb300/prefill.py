@@ -1,0 +1,99 @@
+"""What goes ahead of ``Layer.prefill``: the plan of a ragged batch and the
+norms of its query and key heads.
+
+    ragged = Ragged(R, tokens_cap, block=512, max_blocks=64, n_free=free.numel())
+    ragged.plan(lengths, context, free)                       # once per batch
+    q, k = qk_norm(q, k, norm="l2", scale_q=N ** -0.5)        # per layer
+    y = layer.prefill(ragged, q, k, v, alpha, beta, max_len=longest, start=start, pool=pool)
+
+Each call is one call of the binding and only enqueues work on the stream.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as rb
+from .layer import packed_stride
+
+NORMS = {"none": rb.NORM_NONE, "l2": rb.NORM_L2, "rms": rb.NORM_RMS}
+
+
+class Ragged:
+    """Owner of one batch plan's device arrays (see ``rs_ragged`` in include/rs.h)."""
+
+    def __init__(self, R: int, tokens_cap: int, block: int = 0, max_blocks: int = 0, n_free: int = 0, device="cuda"):
+        self.desc = rb.RaggedDesc(R, tokens_cap, block, max_blocks, n_free)
+        sz = rb.rs_ragged_bytes_for(self.desc)
+        dev = torch.device(device)
+        z = lambda n: torch.zeros(n // 4, dtype=torch.int32, device=dev)
+        self.cu_tokens, self.cu_chunks, self.cu_blocks = z(sz.cu_tokens), z(sz.cu_chunks), z(sz.cu_blocks)
+        self.token_req, self.token_pos = z(sz.token_req), z(sz.token_pos)
+        self.chunks = z(sz.chunks).view(-1, 4)
+        self.block_table = torch.full((R, max_blocks), -1, dtype=torch.int32, device=dev) if block else None
+        self.counts = z(sz.counts)
+        self.status_word = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.arrays = rb.RaggedArrays(*(rb._ptr(getattr(self, n)) for n in rb._RAGGED))
+
+    def plan(self, lengths: torch.Tensor, context: torch.Tensor | None = None,
+             free_blocks: torch.Tensor | None = None, stream=None) -> None:
+        """lengths, context: int32 [R]; free_blocks: int32, at least n_free slots."""
+        d = self.desc
+        for t, name, n in ((lengths, "lengths", d.R), (context, "context", d.R)):
+            if t is not None and (t.dtype != torch.int32 or t.numel() != n):
+                raise ValueError(f"{name} must be int32 [{n}]")
+        if d.block and d.n_free and (free_blocks is None or free_blocks.dtype != torch.int32
+                                     or free_blocks.numel() < d.n_free):
+            raise ValueError(f"free_blocks must be int32 [{d.n_free}]")
+        rb.rs_ragged_plan(d, lengths, context, free_blocks, self.arrays, self.status_word, stream)
+
+    def status(self, clear: bool = True) -> int:
+        """RS_DEV_* bits that plan() set; synchronises."""
+        bits = int(self.status_word.item()) & 0xffffffff
+        if clear:
+            self.status_word.zero_()
+        return bits
+
+
+def qk_norm(q: torch.Tensor | None, k: torch.Tensor | None, *, norm: str = "l2", eps: float = 1e-6,
+            wq: torch.Tensor | None = None, wk: torch.Tensor | None = None, weight_offset: float = 0.0,
+            scale_q: float = 1.0, scale_k: float = 1.0, positions: torch.Tensor | None = None,
+            inv_freq: torch.Tensor | None = None, interleaved: bool = False,
+            out: tuple | None = None, stream=None) -> tuple:
+    """Norms every head of q [T, Hq, D] and k [T, Hk, D] (bf16, rows at any
+    stride; either may be None) and rotates its first 2 * len(inv_freq)
+    channels by positions (int32 [T]) * inv_freq (float32).  Returns the two
+    results, torch.bfloat16, in ``out`` if given (in place: out=(q, k))."""
+    if norm not in NORMS:
+        raise ValueError(f"unknown norm {norm!r}")
+    one = q if q is not None else k
+    if one is None or one.dim() != 3:
+        raise ValueError("q or k must be a [T, heads, D] tensor")
+    T, D = one.shape[0], one.shape[2]
+    d = rb.QkDesc()
+    d.T, d.D, d.norm, d.interleaved = T, D, NORMS[norm], int(interleaved)
+    d.eps, d.weight_offset, d.scale_q, d.scale_k = eps, weight_offset, scale_q, scale_k
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or positions.dtype != torch.int32 or positions.numel() != T:
+            raise ValueError(f"inv_freq must be float32 and positions int32 [{T}]")
+        d.rot = 2 * inv_freq.numel()
+    for w in (wq, wk):
+        if w is not None and (w.element_size() != 2 or w.numel() != D):
+            raise ValueError(f"weights must be bf16 [{D}]")
+    qo, ko = out if out is not None else (None, None)
+    ptrs = [None] * 4
+    if q is not None:
+        d.Hq, d.ld_q = q.shape[1], packed_stride(q, T, q.shape[1], D, "q")
+        if qo is None:
+            qo = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        d.ld_qo = packed_stride(qo, T, d.Hq, D, "out[0]")
+        ptrs[0], ptrs[2] = q.data_ptr(), qo.data_ptr()
+    if k is not None:
+        d.Hk, d.ld_k = k.shape[1], packed_stride(k, T, k.shape[1], D, "k")
+        if ko is None:
+            ko = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+        d.ld_ko = packed_stride(ko, T, d.Hk, D, "out[1]")
+        ptrs[1], ptrs[3] = k.data_ptr(), ko.data_ptr()
+    rb.rs_qk_norm(d, ptrs[0], ptrs[1], wq, wk, inv_freq, positions, ptrs[2], ptrs[3], stream)
+    return qo, ko
