@@ -478,7 +478,8 @@ rs_status rs_prefill_bytes_for(const rs_layer_desc *desc, const rs_ragged_desc *
  * the recurrence of rs_decode_gdn.  Writes y (bf16 [rows][H][P]), the final
  * state to the request's checkpoint row (both copies in two-precision mode),
  * with no records buffered, and the state at each taken block's end to its
- * pool slot.  Requests without rows change nothing.  A row that continues its
+ * pool slot (which no request of the batch starts from).  Requests without
+ * rows change nothing.  A row that continues its
  * checkpoint must have no records or drafts buffered (rs_flush first;
  * RS_DEV_RECORDS otherwise).  The plan must come from rs_ragged_plan with the
  * same descriptor; block_table is read when rd->block > 0 and pool is given.

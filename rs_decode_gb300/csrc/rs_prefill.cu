@@ -14,6 +14,8 @@
 // T = (I + A)^-1 diag(beta) and P do not depend on the state, so
 //   chunk_kernel  computes them for all chunks and heads at once, and
 //   scan_kernel   carries S through a request's chunks.
+// Requests of at most kShort rows go through step_kernel instead, which runs
+// the recurrence row by row beside one read and one write of the state.
 // Decays enter as differences G_i - G_j only, so nothing overflows however
 // long a chunk's decay is; alpha = 0 is a decay of 2^-160, which is 0 in fp32.
 //
@@ -33,6 +35,10 @@ namespace rs {
 namespace {
 
 constexpr int C = RS_CHUNK;
+// Rows of the longest request that the recurrence serves.  256 cached requests of
+// 32 heads of 128, by rows (us): recurrence 165 (1), 227 (4), 341 (8), 582 (16),
+// 827 (24); chunks 746 (9) to 759 (33).
+constexpr int kShort = 16;
 
 // What chunk_kernel leaves for scan_kernel.  All tiles have rows of 64 fp16
 // (128 bytes) with their 16-byte pieces in the order that shared-memory reads
@@ -187,6 +193,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
     const int4 e = reinterpret_cast<const int4 *>(p.rg.chunks)[chunk];
     const int n = e.z;
     if (e.x < 0 || e.x >= p.R || n < 1 || n > C || e.y < 0 || e.y > p.cap - n) return;  // scan_kernel reports it
+    if (p.rg.cu_tokens[e.x + 1] - p.rg.cu_tokens[e.x] <= kShort) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t sK = smem_u32(smem), sQ = sK + C * D * 2;
     load_tile<D>(sK, p.k + (long long)e.y * p.ld_k + g * D, p.ld_k, n, tid, kChunkThreads);
@@ -408,24 +415,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
     }
 }
 
-// ---------------------------------------------------------------- scan kernel
-// A warp owns 16 value columns of a head's state and carries them through the
-// request's chunks on its own: S^T (16 x D) lives in the accumulators of
-// m16n8k16 products, whose register layout is also that of their A operand, so
-//   S^T K^T, S^T Q^T  ->  R^T  ->  u^T = R^T T^T  ->  y^T += u^T P^T,  S^T += u^T K
-// pass from product to product without leaving the registers or meeting
-// another warp.  K, Q, T, P and V come through two shared-memory stages.
-// Operands that enter the state (S, R, T, u) are split in two bf16 terms; k, q
-// and v are bf16 inputs and exact.
-template <int D, int NW>
-struct ScanSmem {
-    static constexpr int TILE = C * D * 2;
-    static constexpr int VT = NW * C * 32;  // per warp: 64 rows of its 16 columns
-    static constexpr int REC = 2 * TILE + VT;
-    static constexpr int STAGE = REC + (int)sizeof(Record);
-    static constexpr int BYTES = 2 * STAGE;
-};
-
+// ---------------------------------------------------------------- requests
 struct Request {
     int n, row0, ctx, chunk0, nch, srow, start;
     bool ok;
@@ -460,6 +450,149 @@ __device__ __forceinline__ Request load_request(const PrefillParams &p, int r, b
     return q;
 }
 
+// Pool slot of the state after the request's rows up to `end` (a position,
+// context included); -1 if it is not to be kept.
+__device__ __forceinline__ int block_slot(const PrefillParams &p, int r, int end, bool report) {
+    if (!p.block || !p.pool || end % p.block) return -1;
+    const int j = end / p.block - 1;
+    const int slot = j < p.max_blocks ? p.rg.block_table[(size_t)r * p.max_blocks + j] : -1;
+    if (slot >= 0 && slot < p.n_pool) return slot;
+    if (slot != -1 && report) atomicOr(p.status, RS_DEV_SLOT);
+    return -1;
+}
+
+// ---------------------------------------------------------------- step kernel
+// The recurrence for requests of a few rows.  A warp owns 16 value columns of
+// a head: lane = 4 rg + cg holds keys D/8 rg .. and values 4 cg .. of them in
+// registers, so that the state is read and written once, in 64-byte segments
+// with 8 KiB in flight per warp, and no warp waits for another.  One row's
+// S k, S q and k.q are summed over the lanes together; S_new q follows as
+// alpha S q + (k.q) u.  Bound by the state's bytes up to about a dozen rows.
+constexpr int kStepThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constant__ PrefillParams p) {
+    constexpr int ROWS = D / 8;                      // key rows of a lane
+    constexpr int SPLIT = D / 16 / (kStepThreads / 32);  // CTAs of a head
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = blockIdx.x % SPLIT, hr = blockIdx.x / SPLIT;
+    const int h = hr % p.H, r = hr / p.H;
+    const bool lead = h == 0 && part == 0 && threadIdx.x == 0;
+    // longer requests are scan_kernel's, where it runs at all
+    if (p.max_len > kShort && p.rg.cu_tokens[r + 1] - p.rg.cu_tokens[r] > kShort) return;
+    const Request rq = load_request(p, r, lead);
+    if (!rq.ok) return;
+    const int g = h / p.rep;
+    const int col = (part * (kStepThreads / 32) + warp) * 16 + (lane & 3) * 4, row0 = (lane >> 2) * ROWS;
+
+    float4 S[ROWS];
+    {
+        const bool cont = rq.start == -2;
+        const size_t slab = ((size_t)(cont ? rq.srow : max(rq.start, 0)) * p.H + h) * D * D + (size_t)row0 * D + col;
+        if (rq.start == -1) {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else if (p.prec == RS_PREC_SHARED_BF16) {
+            const uint16_t *b = (cont ? p.lp : static_cast<const uint16_t *>(p.pool)) + slab;
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(b + (size_t)i * D));
+                S[i] = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                                   __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+            }
+        } else {
+            const float *f = (cont ? p.hp : static_cast<const float *>(p.pool)) + slab;
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) S[i] = __ldcs(reinterpret_cast<const float4 *>(f + (size_t)i * D));
+        }
+    }
+    auto store_state = [&](float *f, uint16_t *b, size_t slab) {
+        slab += (size_t)row0 * D + col;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            if (f) __stcs(reinterpret_cast<float4 *>(f + slab + (size_t)i * D), S[i]);
+            if (b) st_stream2(b + slab + (size_t)i * D, make_uint2(pack_bf2(S[i].x, S[i].y), pack_bf2(S[i].z, S[i].w)));
+        }
+    };
+    for (int t = 0; t < rq.n; ++t) {
+        const long long row = rq.row0 + t;
+        const uint4 *kp = reinterpret_cast<const uint4 *>(p.k + row * p.ld_k + g * D + row0);
+        const uint4 *qp = reinterpret_cast<const uint4 *>(p.q + row * p.ld_q + g * D + row0);
+        const uint2 vp = *reinterpret_cast<const uint2 *>(p.v + row * p.ld_v + h * D + col);
+        const float alpha = p.alpha[row * p.H + h], beta = p.beta[row * p.H + h];
+        float k[ROWS];
+        float4 sk = make_float4(0.f, 0.f, 0.f, 0.f), sq = sk;
+        float kq = 0.f;
+#pragma unroll
+        for (int c = 0; c < ROWS / 8; ++c) {
+            float kk[8], qq[8];
+            unpack<uint16_t, 8>(kp[c], kk);
+            unpack<uint16_t, 8>(qp[c], qq);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 s = S[c * 8 + i];
+                sk.x = fmaf(kk[i], s.x, sk.x), sk.y = fmaf(kk[i], s.y, sk.y);
+                sk.z = fmaf(kk[i], s.z, sk.z), sk.w = fmaf(kk[i], s.w, sk.w);
+                sq.x = fmaf(qq[i], s.x, sq.x), sq.y = fmaf(qq[i], s.y, sq.y);
+                sq.z = fmaf(qq[i], s.z, sq.z), sq.w = fmaf(qq[i], s.w, sq.w);
+                kq = fmaf(kk[i], qq[i], kq);
+                k[c * 8 + i] = kk[i];
+            }
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            sk.x += __shfl_xor_sync(~0u, sk.x, o), sk.y += __shfl_xor_sync(~0u, sk.y, o);
+            sk.z += __shfl_xor_sync(~0u, sk.z, o), sk.w += __shfl_xor_sync(~0u, sk.w, o);
+            sq.x += __shfl_xor_sync(~0u, sq.x, o), sq.y += __shfl_xor_sync(~0u, sq.y, o);
+            sq.z += __shfl_xor_sync(~0u, sq.z, o), sq.w += __shfl_xor_sync(~0u, sq.w, o);
+            kq += __shfl_xor_sync(~0u, kq, o);
+        }
+        float4 u;
+        u.x = beta * (__uint_as_float(vp.x << 16) - alpha * sk.x);
+        u.y = beta * (__uint_as_float(vp.x & 0xffff0000u) - alpha * sk.y);
+        u.z = beta * (__uint_as_float(vp.y << 16) - alpha * sk.z);
+        u.w = beta * (__uint_as_float(vp.y & 0xffff0000u) - alpha * sk.w);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            S[i].x = fmaf(k[i], u.x, alpha * S[i].x), S[i].y = fmaf(k[i], u.y, alpha * S[i].y);
+            S[i].z = fmaf(k[i], u.z, alpha * S[i].z), S[i].w = fmaf(k[i], u.w, alpha * S[i].w);
+        }
+        if (lane < 4)
+            *reinterpret_cast<uint2 *>(p.y + (row * p.H + h) * D + col) =
+                make_uint2(pack_bf2(fmaf(kq, u.x, alpha * sq.x), fmaf(kq, u.y, alpha * sq.y)),
+                           pack_bf2(fmaf(kq, u.z, alpha * sq.z), fmaf(kq, u.w, alpha * sq.w)));
+        const int slot = block_slot(p, r, rq.ctx + t + 1, lead);
+        if (slot >= 0) {
+            const size_t slab = ((size_t)slot * p.H + h) * D * D;
+            if (p.prec == RS_PREC_SHARED_BF16)
+                store_state(nullptr, static_cast<uint16_t *>(p.pool), slab);
+            else
+                store_state(static_cast<float *>(p.pool), nullptr, slab);
+        }
+    }
+    store_state(p.hp, p.lp, ((size_t)rq.srow * p.H + h) * D * D);
+    if (rq.start != -2 && lead) p.base[rq.srow] = p.h[rq.srow] = p.nd[rq.srow] = 0;
+}
+
+// ---------------------------------------------------------------- scan kernel
+// A warp owns 16 value columns of a head's state and carries them through the
+// request's chunks on its own: S^T (16 x D) lives in the accumulators of
+// m16n8k16 products, whose register layout is also that of their A operand, so
+//   S^T K^T, S^T Q^T  ->  R^T  ->  u^T = R^T T^T  ->  y^T += u^T P^T,  S^T += u^T K
+// pass from product to product without leaving the registers or meeting
+// another warp.  K, Q, T, P and V come through two shared-memory stages.
+// Operands that enter the state (S, R, T, u) are split in two bf16 terms; k, q
+// and v are bf16 inputs and exact.
+template <int D, int NW>
+struct ScanSmem {
+    static constexpr int TILE = C * D * 2;
+    static constexpr int VT = NW * C * 32;  // per warp: 64 rows of its 16 columns
+    static constexpr int REC = 2 * TILE + VT;
+    static constexpr int STAGE = REC + (int)sizeof(Record);
+    static constexpr int BYTES = 2 * STAGE;
+};
+
+
 template <int D, int NW>
 __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ PrefillParams p) {
     using M = ScanSmem<D, NW>;
@@ -469,6 +602,7 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part = blockIdx.x % SPLIT, hr = blockIdx.x / SPLIT;
     const int h = hr % p.H, r = hr / p.H;
+    if (p.rg.cu_tokens[r + 1] - p.rg.cu_tokens[r] <= kShort) return;
     const Request rq = load_request(p, r, h == 0 && part == 0 && tid == 0);
     if (!rq.ok) return;
     const int g = h / p.rep;
@@ -684,22 +818,13 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
                 *reinterpret_cast<uint4 *>(y + (long long)t * p.H * D + c * 8) = w;
             }
         }
-        // the state at a block's end
-        if (p.block && p.pool) {
-            const int end = rq.ctx + at + n;
-            if (end % p.block == 0) {
-                const int j = end / p.block - 1;
-                const int slot = j < p.max_blocks ? p.rg.block_table[(size_t)r * p.max_blocks + j] : -1;
-                if (slot >= 0 && slot < p.n_pool) {
-                    const size_t slab = ((size_t)slot * p.H + h) * D * D;
-                    if (p.prec == RS_PREC_SHARED_BF16)
-                        store_state(nullptr, static_cast<uint16_t *>(p.pool), slab);
-                    else
-                        store_state(static_cast<float *>(p.pool), nullptr, slab);
-                } else if (slot != -1 && h == 0 && part == 0 && tid == 0) {
-                    atomicOr(p.status, RS_DEV_SLOT);
-                }
-            }
+        const int slot = block_slot(p, r, rq.ctx + at + n, h == 0 && part == 0 && tid == 0);
+        if (slot >= 0) {
+            const size_t slab = ((size_t)slot * p.H + h) * D * D;
+            if (p.prec == RS_PREC_SHARED_BF16)
+                store_state(nullptr, static_cast<uint16_t *>(p.pool), slab);
+            else
+                store_state(static_cast<float *>(p.pool), nullptr, slab);
         }
     }
     store_state(p.hp, p.lp, ((size_t)rq.srow * p.H + h) * D * D);
@@ -718,6 +843,8 @@ cudaError_t scan_launch(const PrefillParams &p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch(const PrefillParams &p, cudaStream_t s) {
+    step_kernel<D><<<p.R * p.H * (D / 16 / (kStepThreads / 32)), kStepThreads, 0, s>>>(p);
+    if (p.max_len <= kShort) return cudaGetLastError();
     static SmemGrants grants;
     cudaError_t e = grant_smem(reinterpret_cast<const void *>(&chunk_kernel<D>), ChunkSmem<D>::BYTES, grants);
     if (e != cudaSuccess) return e;
@@ -731,7 +858,8 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t s) {
 
 }  // namespace
 
-size_t prefill_bytes(const rs_layer_desc &d, const rs_ragged_desc &rd, int) {
+size_t prefill_bytes(const rs_layer_desc &d, const rs_ragged_desc &rd, int max_len) {
+    if (max_len <= kShort) return 0;
     return (size_t)ragged_chunks_cap(rd) * (d.H * sizeof(Record) + (size_t)d.G * 2 * C * d.N * 2);
 }
 
