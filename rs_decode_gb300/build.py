@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "librs.so")
 SOURCES = ["rs_api.cu", "rs_replay.cu", "rs_replay_m2.cu", "rs_replay_gdn.cu", "rs_replay_kda.cu", "rs_replay_direct.cu", "rs_eager.cu",
-           "rs_small.cu", "rs_noalloc.cu", "rs_ragged_api.cu", "rs_ragged.cu", "rs_qk.cu", "rs_prefill.cu"]
+           "rs_small.cu", "rs_noalloc.cu", "rs_ragged_api.cu", "rs_ragged.cu", "rs_qk.cu", "rs_prefill.cu",
+           "rs_prefill_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -26,54 +26,13 @@
 // likewise, so that states come out at fp32 accuracy (bf16 terms would leave
 // 16 bits at the same cost).  What feeds y alone (S and u once more, P) enters
 // as one fp16 term of 11 bits, below y's own rounding to 8.
-#include <cuda_fp16.h>
-
-#include "rs_common.cuh"
-#include "rs_internal.h"
+#include "rs_prefill.cuh"
 
 namespace rs {
+
+using namespace prefill;
+
 namespace {
-
-constexpr int C = RS_CHUNK;
-// Rows of the longest request that the recurrence serves.  256 cached requests of
-// 32 heads of 128, by rows (us): recurrence 165 (1), 227 (4), 341 (8), 582 (16),
-// 827 (24); chunks 746 (9) to 759 (33).
-constexpr int kShort = 16;
-
-// What chunk_kernel leaves for scan_kernel.  All tiles have rows of 64 fp16
-// (128 bytes) with their 16-byte pieces in the order that shared-memory reads
-// want: piece c of row r at c ^ (r & 7).
-//
-// Per chunk and key head: keys, then queries, D / 64 tiles of 64 rows each.
-// Per chunk and value head:
-struct Record {
-    uint16_t t_hi[C * C], t_lo[C * C];  // T, row i scaled by 1 / (its power of two)
-    uint16_t p[C * C];                  // P without the rows' powers of two
-    float egk[C];  // e^(G_i) times key i's power of two
-    float eg[C];   // e^(G_i)
-    float su[C];   // T's and key i's powers of two: (T R)_i su_i = u_i times key i's power
-    float sq[C];   // query i's power of two
-    float ke[C];   // e^(G_C - G_i)
-};
-static_assert(sizeof(Record) == 25856, "records are copied in 16-byte pieces");
-
-struct PrefillParams {
-    int H, G, rep, prec;  // rep: value heads of a key head
-    int R, cap, ccap, block, max_blocks, n_pool, max_len, B;
-    float *hp;
-    uint16_t *lp;
-    int32_t *base, *h, *nd;
-    uint32_t *status;
-    rs_ragged rg;
-    const uint16_t *q, *k, *v;
-    const float *alpha, *beta;
-    long long ld_q, ld_k, ld_v;
-    const int32_t *rows, *start;
-    void *pool;
-    uint16_t *y;
-    Record *rec;  // [ccap][H]
-    unsigned char *tiles;  // [ccap][G] keys and queries of a chunk, fp16
-};
 
 // ---------------------------------------------------------------- warp matrix products
 // mma.sync m16n8k16: lane = 4 g + t.  A: rows g, g+8, columns 2t..2t+1 and
@@ -100,28 +59,6 @@ __device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t r0, uint32_t r1, 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
-
-// The power of two that brings a row whose largest magnitude is m into
-// [2^K, 2^(K+1)), and its inverse; 1 where m is not finite.
-template <int K>
-__device__ __forceinline__ void row_scale(float m, float &up, float &down) {
-    const int e = (int)(__float_as_uint(m) >> 23) & 255;
-    const int u = e == 255 ? 127 : min(254 + K - e, 253);  // biased exponent; its inverse is 254 - u >= 1
-    up = __uint_as_float((uint32_t)max(u, 1) << 23);
-    down = __uint_as_float((uint32_t)(254 - max(u, 1)) << 23);
-}
-
-// Two values as hi + lo: hi their fp16 rounding, lo the rounding of the rest.
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-    hi = pack_h2(x, y);
-    const float2 h = unpack_h2(hi);
-    lo = pack_h2(x - h.x, y - h.y);
-}
 // The A fragment of 16 x 16 values held as two accumulator tiles, rows g and
 // g + 8 scaled by s0 and s1.
 __device__ __forceinline__ void split(const float (&c0)[4], const float (&c1)[4], float s0, float s1,
@@ -145,11 +82,6 @@ __device__ __forceinline__ void row_max(const float (&c)[N][4], float &m0, float
         m0 = fmaxf(m0, __shfl_xor_sync(~0u, m0, o));
         m1 = fmaxf(m1, __shfl_xor_sync(~0u, m1, o));
     }
-}
-
-// Byte offset of 16-byte piece c (8 channels) of row r in 64-row tiles of 64 channels.
-__device__ __forceinline__ uint32_t piece(int r, int c) {
-    return (uint32_t)((c >> 3) * (C * 128) + r * 128 + (((c ^ r) & 7) << 4));
 }
 
 // Copies a chunk's 64 rows of D channels, zeros past the n rows it has.
@@ -287,8 +219,15 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
             const float ch = __shfl_sync(~0u, sh, 31), cl = __shfl_sync(~0u, sl, 31);
             gh[2 * lane] = h[0], gl[2 * lane] = l[0], gh[2 * lane + 1] = sh, gl[2 * lane + 1] = sl;
             const float e0 = exp2f(h[0] + l[0]), e1 = exp2f(sh + sl);
-            image->eg[2 * lane] = e0, image->eg[2 * lane + 1] = e1;
-            image->egk[2 * lane] = e0 * sk[2 * lane], image->egk[2 * lane + 1] = e1 * sk[2 * lane + 1];
+            image->egq[2 * lane] = e0 * image->sq[2 * lane], image->egq[2 * lane + 1] = e1 * image->sq[2 * lane + 1];
+            if (lane == 31) image->all = e1;
+            const float k0 = e0 * sk[2 * lane], k1 = e1 * sk[2 * lane + 1];
+            image->egk[2 * lane] = k0, image->egk[2 * lane + 1] = k1;
+            float km = fmaxf(k0, k1);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) km = fmaxf(km, __shfl_xor_sync(~0u, km, o));
+            // D products of a state value and a key below 2
+            if (lane == 0) image->xmax = 2.f * D * km, image->umax = image->kmax = 0.f;
             image->ke[2 * lane] = exp2f((ch - h[0]) + (cl - l[0]));
             image->ke[2 * lane + 1] = exp2f((ch - sh) + (cl - sl));
         }
@@ -388,15 +327,19 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
         // T = X diag(beta), each row scaled and split in two; 8 threads a row
         for (int i = tid; i < C * C / 8; i += kChunkThreads) {
             const int row = i >> 3, c = i & 7;
-            float t[8], m = 0.f, up, down;
+            float t[8], m = 0.f, sum = 0.f, up, down;
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 const int j = c * 8 + x;
                 t[x] = j <= row ? X[row * LDM + j] * be[j] : 0.f;
                 m = fmaxf(m, fabsf(t[x]));
+                sum += fabsf(t[x]);
             }
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+            for (int o = 1; o < 8; o <<= 1) {
+                m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+                sum += __shfl_xor_sync(~0u, sum, o);
+            }
             row_scale<8>(m, up, down);
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -405,7 +348,12 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
                 make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(image->t_lo) + piece(row, c)) =
                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (c == 0) image->su[row] = down * sk[row];
+            if (c == 0) {
+                image->su[row] = down * sk[row];
+                // the order of the maxima does not matter: non-negative floats compare as integers
+                atomicMax(reinterpret_cast<int *>(&image->umax), __float_as_int(sum * sk[row]));
+                atomicMax(reinterpret_cast<int *>(&image->kmax), __float_as_int(sum * sk[row] * image->ke[row]));
+            }
         }
         __syncthreads();
         uint4 *out = reinterpret_cast<uint4 *>(p.rec + (size_t)chunk * p.H + hv);
@@ -413,52 +361,6 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
         for (int i = tid; i < (int)sizeof(Record) / 16; i += kChunkThreads) out[i] = img[i];
         __syncthreads();
     }
-}
-
-// ---------------------------------------------------------------- requests
-struct Request {
-    int n, row0, ctx, chunk0, nch, srow, start;
-    bool ok;
-};
-
-// A request's facts, checked; bits of what is wrong go to the status word.
-__device__ __forceinline__ Request load_request(const PrefillParams &p, int r, bool report) {
-    Request q = {};
-    const int a = p.rg.cu_tokens[r], b = p.rg.cu_tokens[r + 1];
-    q.n = b - a;
-    q.row0 = a;
-    if (q.n == 0) return q;
-    unsigned bits = 0;
-    if (q.n < 0 || a < 0 || b > p.cap || q.n > p.max_len) {
-        bits = RS_DEV_LENGTH;
-    } else {
-        q.ctx = p.rg.token_pos[a];
-        q.chunk0 = p.rg.cu_chunks[r];
-        q.nch = p.rg.cu_chunks[r + 1] - q.chunk0;
-        if (q.ctx < 0 || q.ctx > (1 << 30) || q.chunk0 < 0 || q.chunk0 + q.nch > p.ccap ||
-            q.nch != (q.ctx + q.n + C - 1) / C - q.ctx / C)
-            bits = RS_DEV_LENGTH;
-    }
-    q.srow = p.rows ? p.rows[r] : r;
-    q.start = p.start ? p.start[r] : -2;
-    if (q.srow < 0 || q.srow >= p.B || q.start < -2 || q.start >= p.n_pool)
-        bits |= RS_DEV_SLOT;
-    else if (q.start == -2 && (p.h[q.srow] != 0 || p.nd[q.srow] != 0))
-        bits |= RS_DEV_RECORDS;
-    q.ok = bits == 0;
-    if (bits && report) atomicOr(p.status, bits);
-    return q;
-}
-
-// Pool slot of the state after the request's rows up to `end` (a position,
-// context included); -1 if it is not to be kept.
-__device__ __forceinline__ int block_slot(const PrefillParams &p, int r, int end, bool report) {
-    if (!p.block || !p.pool || end % p.block) return -1;
-    const int j = end / p.block - 1;
-    const int slot = j < p.max_blocks ? p.rg.block_table[(size_t)r * p.max_blocks + j] : -1;
-    if (slot >= 0 && slot < p.n_pool) return slot;
-    if (slot != -1 && report) atomicOr(p.status, RS_DEV_SLOT);
-    return -1;
 }
 
 // ---------------------------------------------------------------- step kernel
@@ -698,7 +600,7 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
             for (int hf = 0; hf < 2; ++hf) {
                 const int nt = 2 * j + hf;
                 const float2 ek = *reinterpret_cast<const float2 *>(rec->egk + nt * 8 + tq * 2);
-                const float2 eg = *reinterpret_cast<const float2 *>(rec->eg + nt * 8 + tq * 2);
+                const float2 eg = *reinterpret_cast<const float2 *>(rec->egq + nt * 8 + tq * 2);
                 X[nt][0] = __uint_as_float(v[2 * hf] << 16) - ek.x * (X[nt][0] * sd0);
                 X[nt][1] = __uint_as_float(v[2 * hf] & 0xffff0000u) - ek.y * (X[nt][1] * sd0);
                 X[nt][2] = __uint_as_float(v[2 * hf + 1] << 16) - ek.x * (X[nt][2] * sd1);
@@ -760,15 +662,15 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
                 const float2 sq = *reinterpret_cast<const float2 *>(rec->sq + nt * 8 + tq * 2);
-                Z[nt][0] = (Z[nt][0] + X[nt][0] * d0) * sq.x, Z[nt][1] = (Z[nt][1] + X[nt][1] * d0) * sq.y;
-                Z[nt][2] = (Z[nt][2] + X[nt][2] * d1) * sq.x, Z[nt][3] = (Z[nt][3] + X[nt][3] * d1) * sq.y;
+                Z[nt][0] += X[nt][0] * d0 * sq.x, Z[nt][1] += X[nt][1] * d0 * sq.y;
+                Z[nt][2] += X[nt][2] * d1 * sq.x, Z[nt][3] += X[nt][3] * d1 * sq.y;
             }
         }
         // S^T = e^(G_C) S^T + (e^(G_C - G) u)^T K, summed at u's row scale.  Where u is
         // below 2^-30 of the row's state, the state's size sets the scale: at u's own
         // the sum could overflow, and u's lost bits are far below the state's last one.
         {
-            const float all = rec->eg[C - 1];
+            const float all = rec->all;
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
                 const float2 ke = *reinterpret_cast<const float2 *>(rec->ke + nt * 8 + tq * 2);
@@ -851,9 +753,13 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t s) {
     chunk_kernel<D><<<p.ccap * p.G, kChunkThreads, ChunkSmem<D>::BYTES, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // a head on one CTA, or on two-warp CTAs where the heads alone would leave SMs idle
-    if (p.R * p.H <= 152) return scan_launch<D, 2>(p, s);
-    return scan_launch<D, D / 16>(p, s);
+    if constexpr (D == 128) {
+        return scan_tc_launch(p, s);
+    } else {
+        // a head on one CTA, or on two-warp CTAs where the heads alone would leave SMs idle
+        if (p.R * p.H <= 152) return scan_launch<D, 2>(p, s);
+        return scan_launch<D, D / 16>(p, s);
+    }
 }
 
 }  // namespace

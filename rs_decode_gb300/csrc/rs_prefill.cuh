@@ -1,0 +1,140 @@
+// What the kernels of the ragged delta rule share: the chunk records, the
+// launch parameters, a request's facts, and the scaling of fp16 operands.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "rs_common.cuh"
+#include "rs_internal.h"
+
+namespace rs {
+namespace prefill {
+
+constexpr int C = RS_CHUNK;
+// Rows of the longest request that the recurrence serves.  256 cached requests of
+// 32 heads of 128, by rows (us): recurrence 165 (1), 227 (4), 341 (8), 582 (16),
+// 827 (24); chunks 746 (9) to 759 (33).
+constexpr int kShort = 16;
+
+// What chunk_kernel leaves for scan_kernel.  All tiles have rows of 64 fp16
+// (128 bytes) with their 16-byte pieces in the order that shared-memory reads
+// want: piece c of row r at c ^ (r & 7).
+//
+// Per chunk and key head: keys, then queries, D / 64 tiles of 64 rows each.
+// Per chunk and value head:
+struct Record {
+    uint16_t t_hi[C * C], t_lo[C * C];  // T, row i scaled by 1 / (its power of two)
+    uint16_t p[C * C];                  // P without the rows' powers of two
+    float egk[C];  // e^(G_i) times key i's power of two
+    float egq[C];  // e^(G_i) times query i's power of two
+    float su[C];   // T's and key i's powers of two: (T R)_i su_i = u_i times key i's power
+    float sq[C];   // query i's power of two
+    float ke[C];  // e^(G_C - G_i)
+    float all;     // e^(G_C)
+    // Bounds that size the scales of operands before the operands are known:
+    float xmax;  // |e^G S^T K^T| of a state row of largest magnitude 1
+    float umax;  // |u| (with its key's power of two) of an R row of largest magnitude 1
+    float kmax;  // the same of e^(G_C - G) u
+    float pad[28];
+};
+constexpr int kRecMats = 3 * C * C * 2;                   // bytes of the matrices, then
+constexpr int kRecVecs = (int)sizeof(Record) - kRecMats;  // of the vectors
+static_assert(sizeof(Record) == 25984, "records are copied in 16-byte pieces");
+
+struct PrefillParams {
+    int H, G, rep, prec;  // rep: value heads of a key head
+    int R, cap, ccap, block, max_blocks, n_pool, max_len, B;
+    float *hp;
+    uint16_t *lp;
+    int32_t *base, *h, *nd;
+    uint32_t *status;
+    rs_ragged rg;
+    const uint16_t *q, *k, *v;
+    const float *alpha, *beta;
+    long long ld_q, ld_k, ld_v;
+    const int32_t *rows, *start;
+    void *pool;
+    uint16_t *y;
+    Record *rec;  // [ccap][H]
+    unsigned char *tiles;  // [ccap][G] keys and queries of a chunk, fp16
+};
+
+// ---------------------------------------------------------------- fp16 operands
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+
+// The power of two that brings a row whose largest magnitude is m into
+// [2^K, 2^(K+1)), and its inverse; 1 where m is not finite.
+template <int K>
+__device__ __forceinline__ void row_scale(float m, float &up, float &down) {
+    const int e = (int)(__float_as_uint(m) >> 23) & 255;
+    const int u = e == 255 ? 127 : min(254 + K - e, 253);  // biased exponent; its inverse is 254 - u >= 1
+    up = __uint_as_float((uint32_t)max(u, 1) << 23);
+    down = __uint_as_float((uint32_t)(254 - max(u, 1)) << 23);
+}
+
+// Two values as hi + lo: hi their fp16 rounding, lo the rounding of the rest.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack_h2(x, y);
+    const float2 h = unpack_h2(hi);
+    lo = pack_h2(x - h.x, y - h.y);
+}
+// Byte offset of 16-byte piece c (8 channels) of row r in 64-row tiles of 64 channels.
+__device__ __forceinline__ uint32_t piece(int r, int c) {
+    return (uint32_t)((c >> 3) * (C * 128) + r * 128 + (((c ^ r) & 7) << 4));
+}
+
+// ---------------------------------------------------------------- requests
+struct Request {
+    int n, row0, ctx, chunk0, nch, srow, start;
+    bool ok;
+};
+
+// A request's facts, checked; bits of what is wrong go to the status word.
+__device__ __forceinline__ Request load_request(const PrefillParams &p, int r, bool report) {
+    Request q = {};
+    const int a = p.rg.cu_tokens[r], b = p.rg.cu_tokens[r + 1];
+    q.n = b - a;
+    q.row0 = a;
+    if (q.n == 0) return q;
+    unsigned bits = 0;
+    if (q.n < 0 || a < 0 || b > p.cap || q.n > p.max_len) {
+        bits = RS_DEV_LENGTH;
+    } else {
+        q.ctx = p.rg.token_pos[a];
+        q.chunk0 = p.rg.cu_chunks[r];
+        q.nch = p.rg.cu_chunks[r + 1] - q.chunk0;
+        if (q.ctx < 0 || q.ctx > (1 << 30) || q.chunk0 < 0 || q.chunk0 + q.nch > p.ccap ||
+            q.nch != (q.ctx + q.n + C - 1) / C - q.ctx / C)
+            bits = RS_DEV_LENGTH;
+    }
+    q.srow = p.rows ? p.rows[r] : r;
+    q.start = p.start ? p.start[r] : -2;
+    if (q.srow < 0 || q.srow >= p.B || q.start < -2 || q.start >= p.n_pool)
+        bits |= RS_DEV_SLOT;
+    else if (q.start == -2 && (p.h[q.srow] != 0 || p.nd[q.srow] != 0))
+        bits |= RS_DEV_RECORDS;
+    q.ok = bits == 0;
+    if (bits && report) atomicOr(p.status, bits);
+    return q;
+}
+
+// Pool slot of the state after the request's rows up to `end` (a position,
+// context included); -1 if it is not to be kept.
+__device__ __forceinline__ int block_slot(const PrefillParams &p, int r, int end, bool report) {
+    if (!p.block || !p.pool || end % p.block) return -1;
+    const int j = end / p.block - 1;
+    const int slot = j < p.max_blocks ? p.rg.block_table[(size_t)r * p.max_blocks + j] : -1;
+    if (slot >= 0 && slot < p.n_pool) return slot;
+    if (slot != -1 && report) atomicOr(p.status, RS_DEV_SLOT);
+    return -1;
+}
+
+// The scan of 128-wide heads on the fifth-generation tensor cores (rs_prefill_tc.cu).
+cudaError_t scan_tc_launch(const PrefillParams &p, cudaStream_t s);
+
+}  // namespace prefill
+}  // namespace rs

@@ -1,0 +1,644 @@
+// The chunk scan of the gated delta rule for 128-wide heads on the
+// fifth-generation tensor cores (tcgen05.mma, fp16 operands, fp32 sums in TMEM).
+//
+// A CTA carries one head of one request.  Everything is transposed so that the
+// M = 128 rows of every product are the head's value columns and a TMEM lane,
+// hence two of the CTA's 256 threads, own one of them (one thread the keys
+// 0..63 and the chunk's rows 0..31, the other the rest):
+//   X = S^T K^T, Z = S^T Q^T     A = S  (hi, lo in TMEM)  B = keys, queries
+//   R = V^T - e^G X              (threads)
+//   U = R T^T                    A = R  (hi, lo in TMEM)  B = T hi, lo; lower triangular
+//   D = (e^(G_C - G) u)^T K      A = u  (hi, lo in TMEM)  B = keys, the same tile read MN-major
+//   Y = u^T P^T                  A = u  (hi in shared memory)  B = P; lower triangular
+//   S <- e^(G_C) S + D, y = e^G Z + Y   (threads)
+// The state itself stays fp32 in the threads' registers, 64 keys each.
+//
+// A chunk is a chain of four products with register work between them, so one
+// head alone leaves the tensor cores idle half of the time: two CTAs share an
+// SM.  That fixes the budget: 256 TMEM columns (below), 128 registers, 94 KiB
+// of shared memory, in which only the keys and the vectors are double-buffered
+// (they are needed up to the chunk's end; everything else is refilled while
+// the chunk goes on).  Two threads a row, not one: the register work is
+// straight-line code of thousands of instructions, and two warps that run it
+// together on a scheduler share its fetches.
+//
+// TMEM columns, by phase of a chunk:
+//   [0, 64)     S lo  -> R hi, lo -> u hi, lo
+//   [64, 128)   X sums -> U sums -> Y sums
+//   [128, 192)  Z sums -> D sums, keys 0..63
+//   [192, 256)  S hi  -> D sums, keys 64..127
+// Z leaves early, packed to fp16 (y rounds to 8 bits, fp16 keeps 11).
+#include "rs_prefill.cuh"
+
+namespace rs {
+
+using namespace prefill;
+
+namespace {
+
+constexpr int D = 128;
+constexpr int kThreads = 256;
+constexpr int kTile = C * D * 2;      // keys or queries of a chunk
+constexpr int kHalf = C * 128;        // one 64 x 64 fp16 tile
+constexpr int kTmem = 256;
+
+// Shared memory: tiles on 1024-byte boundaries (the swizzle's period).
+struct Smem {
+    static constexpr int K = 0;                      // two buffers
+    static constexpr int Q = K + 2 * kTile;          // queries, then u
+    static constexpr int T = Q + kTile;              // hi, lo
+    static constexpr int P = T + 2 * kHalf;
+    static constexpr int V = P + kHalf;              // [64][128] bf16
+    static constexpr int VEC = V + C * D * 2;        // two buffers
+    static constexpr int MAX = VEC + 2 * kRecVecs;   // [2][2][128] row maxima of the state and of V
+    static constexpr int BAR = MAX + 4 * D * 4;
+    static constexpr int BYTES = BAR + 256 + 1024;   // and room to align
+};
+
+using f2 = unsigned long long;  // two fp32 values, the operand of paired arithmetic
+
+struct Bars {
+    uint64_t full_k[2], full_q, full_t, full_p;  // copies have landed
+    uint64_t mx, mz, mu, md, my, mend;                   // products are complete
+    uint32_t tmem, abort;
+    int nk, nq, nt;                                      // loads begun
+    const unsigned char *tiles;                          // the request's keys and queries of this head
+    unsigned long long tile_step;
+    const Record *rec;                                   // the request's records of this head, p.H apart
+};
+static_assert(sizeof(Bars) <= 256, "");
+
+struct Vecs {  // the vectors of a Record
+    float egk[C], egq[C], su[C], sq[C], ke[C], all, xmax, umax, kmax, pad[28];
+};
+static_assert(sizeof(Vecs) == kRecVecs, "");
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, Bars *b, uint32_t *status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    volatile uint32_t *abort = &b->abort;
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            atomicOr(status, RS_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// The same for a whole warp, with one answer for all lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, Bars *b, uint32_t *status) {
+    return __all_sync(~0u, wait_bar(bar, parity, b, status));
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, unsigned bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+        "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// Operands in shared memory are 128-byte-swizzled tiles: rows of 128 bytes,
+// 8-row groups 1024 bytes apart.  A descriptor's high word is the same for all.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr >> 4) | ((1024u >> 4) << 16); }
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\tmov.b64 bd, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\tmov.b64 ad, {%1, %3};\n\tmov.b64 bd, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+// fp16 A and B, fp32 sums, M = 128
+__host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn) {
+    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+#define R16(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), \
+    "=r"(v[o + 6]), "=r"(v[o + 7]), "=r"(v[o + 8]), "=r"(v[o + 9]), "=r"(v[o + 10]), "=r"(v[o + 11]),          \
+    "=r"(v[o + 12]), "=r"(v[o + 13]), "=r"(v[o + 14]), "=r"(v[o + 15])
+// 16 columns of the warp's 32 lanes, complete on return
+__device__ __forceinline__ void ld16(uint32_t addr, f2 (&f)[8]) {
+    uint32_t v[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : R16(v, 0)
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (f2)v[2 * i + 1] << 32 | v[2 * i];
+}
+#undef R16
+__device__ __forceinline__ void st8(uint32_t addr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 values of a row, scaled, as 8 packed hi and 8 packed lo columns.  hi is
+// the value cut to 11 bits, lo the fp16 rounding of the rest: 22 bits in all.
+__device__ __forceinline__ uint32_t pack_pair(f2 v) { return pack_h2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))); }
+__device__ __forceinline__ void put_split(uint32_t hi_addr, uint32_t lo_addr, const f2 *x, f2 up) {
+    uint32_t hi[8], lo[8];
+    const f2 minus = f2_pack(-1.f, -1.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const f2 v = f2_mul(x[i], up);
+        const f2 h = v & 0xffffe000ffffe000ull;
+        hi[i] = pack_pair(h);
+        lo[i] = pack_pair(f2_fma(h, minus, v));
+    }
+    st8(hi_addr, hi);
+    st8(lo_addr, lo);
+}
+// The largest magnitude of three.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pack_b2(f2 v) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float((uint32_t)(v >> 32))), "f"(__uint_as_float((uint32_t)v)));
+    return r;
+}
+
+struct Work {  // one request's head, as both sides see it
+    int n, head_rows;
+    __device__ int first(int i) const { return i == 0 ? 0 : head_rows + (i - 1) * C; }
+    __device__ int rows(int i) const { return min(i == 0 ? head_rows : C, n - first(i)); }
+};
+
+// Copies of one head's chunks into shared memory.  Each buffer has one warp
+// that refills it, once something that all threads waited for implies that the
+// buffer's readers are done: keys, vectors, queries and P warp 1, T warp 3.
+// (V's rows have the caller's stride: all threads copy them, 16 bytes each; one
+// bulk copy a row would hold up its warp for 45 clocks a copy.)
+// Where they come from, and how many were begun, is kept beside the barriers.
+__device__ __forceinline__ void load_k(Bars *b, uint32_t sm, int i, int heads) {
+    if (elect_one()) {
+        uint64_t *bar = b->full_k + (i & 1);
+        ++b->nk;
+        mbar_arrive_expect_tx(bar, kTile + kRecVecs);
+        bulk_load(sm + Smem::K + (i & 1) * kTile, b->tiles + (size_t)i * b->tile_step, kTile, bar);
+        bulk_load(sm + Smem::VEC + (i & 1) * kRecVecs,
+                  reinterpret_cast<const unsigned char *>(b->rec + (size_t)i * heads) + kRecMats, kRecVecs, bar);
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void load_qp(Bars *b, uint32_t sm, int i, int heads) {
+    if (elect_one()) {
+        ++b->nq;
+        mbar_arrive_expect_tx(&b->full_q, kTile);
+        bulk_load(sm + Smem::Q, b->tiles + (size_t)i * b->tile_step + kTile, kTile, &b->full_q);
+        mbar_arrive_expect_tx(&b->full_p, kHalf);
+        bulk_load(sm + Smem::P, b->rec[(size_t)i * heads].p, kHalf, &b->full_p);
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void load_t(Bars *b, uint32_t sm, int i, int heads) {
+    if (elect_one()) {
+        ++b->nt;
+        mbar_arrive_expect_tx(&b->full_t, 2 * kHalf);
+        bulk_load(sm + Smem::T, b->rec[(size_t)i * heads].t_hi, 2 * kHalf, &b->full_t);
+    }
+    __syncwarp();
+}
+// After giving up: wait (with a limit) for what is still in flight.
+__device__ __forceinline__ void drain(Bars *b) {
+    const int nk = b->nk, nq = b->nq, nt = b->nt;
+    for (int c = 0; c < 2; ++c)
+        if (nk > c) mbar_wait(b->full_k + c, ((nk + 1 - c) / 2 - 1) & 1);
+    if (nq) mbar_wait(&b->full_q, (nq - 1) & 1), mbar_wait(&b->full_p, (nq - 1) & 1);
+    if (nt) mbar_wait(&b->full_t, (nt - 1) & 1);
+}
+
+// Products, issued by one thread; k, q, t, u, pm: descriptors' low words.
+// Steps of 16 in a product's inner dimension are 32 bytes along a row (2 in a
+// descriptor), or 16 rows (128) where the tile is read MN-major.
+constexpr uint32_t kHalfD = kHalf >> 4;
+__device__ __forceinline__ void issue_x(uint32_t tm, uint32_t k, Bars *b) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+        mma_ts(tm + 64, tm + 192 + 8 * x, k + (x >> 2) * kHalfD + (x & 3) * 2, idesc_f16(64, false), x > 0);
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+        mma_ts(tm + 64, tm + 8 * x, k + (x >> 2) * kHalfD + (x & 3) * 2, idesc_f16(64, false), true);
+    umma_commit(&b->mx);
+}
+__device__ __forceinline__ void issue_z(uint32_t tm, uint32_t q, Bars *b) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+        mma_ts(tm + 128, tm + 192 + 8 * x, q + (x >> 2) * kHalfD + (x & 3) * 2, idesc_f16(64, false), x > 0);
+    umma_commit(&b->mz);
+}
+__device__ __forceinline__ void issue_u(uint32_t tm, uint32_t t, Bars *b) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {  // T is lower triangular: rows 16 x and on of its columns 16 x..
+        mma_ts(tm + 64 + 16 * x, tm + 8 * x, t + x * 130, idesc_f16(64 - 16 * x, false), x > 0);
+        mma_ts(tm + 64 + 16 * x, tm + 32 + 8 * x, t + x * 130, idesc_f16(64 - 16 * x, false), true);
+        mma_ts(tm + 64 + 16 * x, tm + 8 * x, t + kHalfD + x * 130, idesc_f16(64 - 16 * x, false), true);
+    }
+    umma_commit(&b->mu);
+}
+__device__ __forceinline__ void issue_d(uint32_t tm, uint32_t k, Bars *b) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {  // 16 rows of the chunk a step; keys 0..63, then 64..127
+        mma_ts(tm + 128, tm + 8 * x, k + x * 128, idesc_f16(64, true), x > 0);
+        mma_ts(tm + 192, tm + 8 * x, k + kHalfD + x * 128, idesc_f16(64, true), x > 0);
+        mma_ts(tm + 128, tm + 32 + 8 * x, k + x * 128, idesc_f16(64, true), true);
+        mma_ts(tm + 192, tm + 32 + 8 * x, k + kHalfD + x * 128, idesc_f16(64, true), true);
+    }
+    umma_commit(&b->md);
+}
+__device__ __forceinline__ void issue_y(uint32_t tm, uint32_t u, uint32_t pm, Bars *b) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        mma_ss(tm + 64 + 16 * x, u + x * 2, pm + x * 130, idesc_f16(64 - 16 * x, false), x > 0);
+    umma_commit(&b->my);
+}
+
+// The larger of the values of a row's two threads (warps w and w + 4).
+__device__ __forceinline__ float pair_max(float *m, int hf, int row, int warp, float x) {
+    m[hf * D + row] = x;
+    switch (warp & 3) {
+        case 0: asm volatile("bar.sync 1, 64;" ::: "memory"); break;
+        case 1: asm volatile("bar.sync 2, 64;" ::: "memory"); break;
+        case 2: asm volatile("bar.sync 3, 64;" ::: "memory"); break;
+        default: asm volatile("bar.sync 4, 64;" ::: "memory"); break;
+    }
+    return fmaxf(x, m[(hf ^ 1) * D + row]);
+}
+
+// A head of a request.  Every wait gives up after its time limit; the threads
+// learn of it together at the next barrier and leave.
+__device__ __forceinline__ void scan_head(const PrefillParams &p, const Request &rq, int h, int r, unsigned char *smem,
+                                          Bars *b) {
+    constexpr int DH = D / 2, CH = C / 2;
+    const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), hf = warp >> 2;
+    const int row = threadIdx.x & 127;  // value column of the head
+    const uint32_t base = b->tmem, sm = smem_u32(smem);
+    const uint32_t lanes = base + ((uint32_t)(warp & 3) << 21);
+    const uint32_t t_shi = lanes + 192 + 32 * hf, t_slo = lanes + 32 * hf;          // state
+    const uint32_t t_ohi = lanes + 16 * hf, t_olo = lanes + 32 + 16 * hf;           // R, u
+    const uint32_t t_sum = lanes + 64 + 32 * hf, t_z = lanes + 128 + 32 * hf, t_d = lanes + 128 + 64 * hf;
+    Work w;
+    w.n = rq.n;
+    w.head_rows = min(rq.n, C - rq.ctx % C);
+    const int nch = rq.nch;
+    const int vt = threadIdx.x >> 4, vc = threadIdx.x & 15;  // V: row vt + 16 j, 16-byte piece vc
+    const uint16_t *vsrc = p.v + ((long long)rq.row0 + vt) * p.ld_v + h * D + vc * 8;
+    auto load_v = [&](int i) {
+        if (i < nch) {
+            const int n = w.rows(i);
+            const uint16_t *src = vsrc + (long long)w.first(i) * p.ld_v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = vt + 16 * j < n;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm + Smem::V + (vt + 16 * j) * (D * 2) + vc * 16),
+                             "l"(in ? src + 16 * j * p.ld_v : p.v), "r"(in ? 16 : 0)
+                             : "memory");
+            }
+        }
+    };
+    if (warp == 1) {
+        load_k(b, sm, 0, p.H);
+        load_qp(b, sm, 0, p.H);
+        if (rq.nch > 1) load_k(b, sm, 1, p.H);
+    }
+    if (warp == 3) load_t(b, sm, 0, p.H);
+    load_v(0);
+
+    f2 S[DH / 2];
+    {
+        const bool cont = rq.start == -2;
+        const size_t slab = ((size_t)(cont ? rq.srow : max(rq.start, 0)) * p.H + h) * D * D + hf * DH * D + row;
+        if (rq.start == -1) {
+#pragma unroll
+            for (int n = 0; n < DH / 2; ++n) S[n] = 0;
+        } else if (p.prec == RS_PREC_SHARED_BF16) {
+            const uint16_t *src = (cont ? p.lp : static_cast<const uint16_t *>(p.pool)) + slab;
+#pragma unroll
+            for (int n = 0; n < DH / 2; ++n) S[n] = f2_pack(bf2f(src[2 * n * D]), bf2f(src[(2 * n + 1) * D]));
+        } else {
+            const float *src = (cont ? p.hp : static_cast<const float *>(p.pool)) + slab;
+#pragma unroll
+            for (int n = 0; n < DH / 2; ++n) S[n] = f2_pack(src[2 * n * D], src[(2 * n + 1) * D]);
+        }
+    }
+    auto store_state = [&](float *f, uint16_t *q, size_t slab) {
+        slab += hf * DH * D + row;
+        if (f) {
+#pragma unroll
+            for (int n = 0; n < DH / 2; ++n) {
+                float lo, hi;
+                f2_unpack(S[n], lo, hi);
+                f[slab + 2 * n * D] = lo, f[slab + (2 * n + 1) * D] = hi;
+            }
+        }
+        if (q) {
+#pragma unroll
+            for (int n = 0; n < DH / 2; ++n) {
+                float lo, hi;
+                f2_unpack(S[n], lo, hi);
+                q[slab + 2 * n * D] = (uint16_t)f2bf(lo), q[slab + (2 * n + 1) * D] = (uint16_t)f2bf(hi);
+            }
+        }
+    };
+
+    const long long ystep = (long long)p.H * D;
+    uint16_t *y = p.y + ((long long)rq.row0 * p.H + h) * D + (row & ~1) + (hf * CH + 16 * (row & 1)) * ystep;
+    float *rowmax = reinterpret_cast<float *>(smem + Smem::MAX);
+    bool ok = true;
+    for (int i = 0; i < nch; ++i) {
+        const unsigned ph = i & 1, kph = (i >> 1) & 1;
+        const int n = w.rows(i);
+        const uint32_t sk = desc_lo(sm + Smem::K + (i & 1) * kTile);
+        const Vecs &vec = *reinterpret_cast<const Vecs *>(smem + Smem::VEC + (i & 1) * kRecVecs);
+        // the state as an operand, its row scaled to fp16's range: the row's
+        // two threads agree on its largest magnitude
+        float smax = 0.f;
+#pragma unroll
+        for (int k = 0; k < DH / 2; ++k) {
+            float lo, hi;
+            f2_unpack(S[k], lo, hi);
+            smax = max_abs3(smax, lo, hi);
+        }
+        smax = pair_max(rowmax, hf, row, warp, smax);
+        float sup, sdown;
+        row_scale<14>(smax, sup, sdown);
+#pragma unroll
+        for (int k = 0; k < DH; k += 16) put_split(t_shi + k / 2, t_slo + k / 2, S + k / 2, f2_pack(sup, sup));
+        st_done();
+        asm volatile("cp.async.wait_all;" ::: "memory");  // this thread's part of V
+        tc_fence_before_sync();
+        if (__syncthreads_or(!ok)) break;
+        if (i > 0 && i + 1 < nch && warp == 1) load_k(b, sm, i + 1, p.H);  // the last chunk's are free: its y is done
+        ok = wait_warp(b->full_k + (i & 1), kph, b, p.status) && ok;
+        if (warp == 0) {
+            tc_fence_after_sync();
+            if (elect_one()) issue_x(base, sk, b);
+            __syncwarp();
+        }
+        // V's column, while X is computed
+        uint32_t v[CH / 2];
+        float vmax;
+        {
+            __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
+            const uint16_t *src = reinterpret_cast<const uint16_t *>(smem + Smem::V) + hf * CH * D + row;
+#pragma unroll
+            for (int t = 0; t < CH; t += 2) {
+                const uint32_t a = src[t * D], c = src[t * D + D];
+                v[t / 2] = __byte_perm(a, c, 0x5410);
+                const uint32_t mag = v[t / 2] & 0x7fff7fffu;
+                m2 = __hmax2(m2, *reinterpret_cast<const __nv_bfloat162 *>(&mag));
+            }
+            vmax = fmaxf(__low2float(m2), __high2float(m2));
+        }
+        vmax = pair_max(rowmax + 2 * D, hf, row, warp, vmax);
+        if (warp == 4) {  // Z, behind X
+            ok = wait_warp(&b->full_q, ph, b, p.status) && ok;
+            tc_fence_after_sync();
+            if (elect_one()) issue_z(base, desc_lo(sm + Smem::Q), b);
+            __syncwarp();
+        }
+        // |R| <= |V| + e^G |X|: the bound may be far above R; the split's low terms reach 2^-39 below it
+        const float rbound = fmaf(vec.xmax, smax, vmax);
+        float rup, rdown;
+        row_scale<14>(rbound, rup, rdown);
+        const unsigned long long nsdown = f2_pack(-sdown, -sdown);
+        ok = wait_warp(&b->mx, ph, b, p.status) && ok;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int t = 0; t < CH; t += 16) {
+            f2 x[8];
+            ld16(t_sum + t, x);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const ulonglong2 ek = *reinterpret_cast<const ulonglong2 *>(vec.egk + hf * CH + t + e);
+                const uint32_t v0 = v[(t + e) / 2], v1 = v[(t + e) / 2 + 1];
+                x[e / 2] = f2_fma(x[e / 2], f2_mul(ek.x, nsdown), (f2)(v0 & 0xffff0000u) << 32 | v0 << 16);
+                x[e / 2 + 1] = f2_fma(x[e / 2 + 1], f2_mul(ek.y, nsdown), (f2)(v1 & 0xffff0000u) << 32 | v1 << 16);
+            }
+            put_split(t_ohi + t / 2, t_olo + t / 2, x, f2_pack(rup, rup));
+        }
+        st_done();
+        tc_fence_before_sync();
+        if (__syncthreads_or(!ok)) { ok = false; break; }
+        load_v(i + 1);
+        if (warp == 0) {
+            ok = wait_warp(&b->full_t, ph, b, p.status) && ok;
+            tc_fence_after_sync();
+            if (elect_one()) issue_u(base, desc_lo(sm + Smem::T), b);
+            __syncwarp();
+        }
+        // u, with its key's power of two: fp16 for y, split with e^(G_C - G) for the state
+        const float ubound = vec.umax * rbound, kbound = vec.kmax * rbound;
+        float uup, udown, kup, kdown;
+        row_scale<14>(ubound, uup, udown);
+        row_scale<14>(kbound, kup, kdown);
+        const unsigned long long rd2 = f2_pack(rdown, rdown), uup2 = f2_pack(uup, uup);
+        ok = wait_warp(&b->mu, ph, b, p.status) && ok;
+        tc_fence_after_sync();
+        if (i + 1 < nch && warp == 3) load_t(b, sm, i + 1, p.H);
+        uint32_t z[CH / 2];  // u in fp16, then Z, then y
+#pragma unroll
+        for (int t = 0; t < CH; t += 16) {
+            f2 x[8];
+            ld16(t_sum + t, x);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const ulonglong2 su = *reinterpret_cast<const ulonglong2 *>(vec.su + hf * CH + t + e);
+                x[e / 2] = f2_mul(x[e / 2], f2_mul(su.x, rd2)), x[e / 2 + 1] = f2_mul(x[e / 2 + 1], f2_mul(su.y, rd2));
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[t / 2 + e] = pack_pair(f2_mul(x[e], uup2));
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const ulonglong2 ke = *reinterpret_cast<const ulonglong2 *>(vec.ke + hf * CH + t + e);
+                x[e / 2] = f2_mul(x[e / 2], ke.x), x[e / 2 + 1] = f2_mul(x[e / 2 + 1], ke.y);
+            }
+            put_split(t_ohi + t / 2, t_olo + t / 2, x, f2_pack(kup, kup));
+        }
+        // the queries' place takes u once Z is complete; Z leaves TMEM in fp16
+        // (2^-9 keeps its sums, below 2^24, in range)
+        ok = wait_warp(&b->mz, ph, b, p.status) && ok;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4 *>(smem + Smem::Q + (row * 128 + (((4 * hf + c) ^ (row & 7)) << 4))) =
+                make_uint4(z[4 * c], z[4 * c + 1], z[4 * c + 2], z[4 * c + 3]);
+#pragma unroll
+        for (int t = 0; t < CH; t += 16) {
+            f2 x[8];
+            ld16(t_z + t, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[t / 2 + e] = pack_pair(f2_mul(x[e], f2_pack(0.001953125f, 0.001953125f)));
+        }
+        st_done();
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        if (__syncthreads_or(!ok)) { ok = false; break; }
+        if (warp == 0) {
+            tc_fence_after_sync();
+            if (elect_one()) issue_d(base, sk, b);
+            __syncwarp();
+            ok = wait_warp(&b->full_p, ph, b, p.status) && ok;
+            if (elect_one()) issue_y(base, desc_lo(sm + Smem::Q), desc_lo(sm + Smem::P), b);
+            __syncwarp();
+        }
+        // S <- e^(G_C) S + D
+        ok = wait_warp(&b->md, ph, b, p.status) && ok;
+        tc_fence_after_sync();
+        {
+            const unsigned long long all = f2_pack(vec.all, vec.all), kd2 = f2_pack(kdown, kdown);
+#pragma unroll
+            for (int k = 0; k < DH; k += 16) {
+                f2 x[8];
+                ld16(t_d + k, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) S[k / 2 + e] = f2_fma(all, S[k / 2 + e], f2_mul(x[e], kd2));
+            }
+        }
+        // y = (e^G Z + Y) with the query's power of two
+        ok = wait_warp(&b->my, ph, b, p.status) && ok;
+        tc_fence_after_sync();
+        if (i + 1 < nch && warp == 1) load_qp(b, sm, i + 1, p.H);
+        const float zs = sdown * 512.f;
+        const unsigned long long zs2 = f2_pack(zs, zs), ud2 = f2_pack(udown, udown);
+#pragma unroll
+        for (int t = 0; t < CH; t += 16) {
+            f2 x[8];
+            ld16(t_sum + t, x);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const ulonglong2 eq = *reinterpret_cast<const ulonglong2 *>(vec.egq + hf * CH + t + e);
+                const ulonglong2 sq = *reinterpret_cast<const ulonglong2 *>(vec.sq + hf * CH + t + e);
+                const float2 z0 = unpack_h2(z[(t + e) / 2]), z1 = unpack_h2(z[(t + e) / 2 + 1]);
+                z[(t + e) / 2] = pack_b2(f2_fma(x[e / 2], f2_mul(sq.x, ud2), f2_mul(f2_mul(eq.x, zs2), f2_pack(z0.x, z0.y))));
+                z[(t + e) / 2 + 1] = pack_b2(f2_fma(x[e / 2 + 1], f2_mul(sq.y, ud2), f2_mul(f2_mul(eq.y, zs2), f2_pack(z1.x, z1.y))));
+            }
+        }
+        // Neighbouring lanes swap halves: an even lane stores its and its neighbour's
+        // columns of the first 16 of the thread's 32 rows, an odd lane those of the rest
+        {
+            const bool odd = row & 1;
+            const uint32_t sel0 = odd ? 0x1054 : 0x5410, sel1 = odd ? 0x3276 : 0x7632;
+            uint16_t *yc = y + w.first(i) * ystep;
+            const int m = n - hf * CH - 16 * odd;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t keep = odd ? z[8 + e] : z[e];
+                const uint32_t got = __shfl_xor_sync(~0u, odd ? z[e] : z[8 + e], 1);
+                z[e] = __byte_perm(keep, got, sel0);
+                z[8 + e] = __byte_perm(keep, got, sel1);
+            }
+            if (n == C) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    *reinterpret_cast<uint32_t *>(yc) = z[e];
+                    yc += ystep;
+                    *reinterpret_cast<uint32_t *>(yc) = z[8 + e];
+                    yc += ystep;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (2 * e < m) *reinterpret_cast<uint32_t *>(yc) = z[e];
+                    yc += ystep;
+                    if (2 * e + 1 < m) *reinterpret_cast<uint32_t *>(yc) = z[8 + e];
+                    yc += ystep;
+                }
+            }
+        }
+        const int slot = block_slot(p, r, rq.ctx + w.first(i) + n, h == 0 && threadIdx.x == 0);
+        if (slot >= 0) {
+            const size_t slab = ((size_t)slot * p.H + h) * D * D;
+            if (p.prec == RS_PREC_SHARED_BF16)
+                store_state(nullptr, static_cast<uint16_t *>(p.pool), slab);
+            else
+                store_state(static_cast<float *>(p.pool), nullptr, slab);
+        }
+    }
+    if (__syncthreads_or(!ok)) {
+        drain(b);
+        if (warp == 0 || warp == 4) {  // elect_one() names the same lane each time: the one that issued the products
+            if (elect_one()) umma_commit(&b->mend);
+            __syncwarp();
+            mbar_wait(&b->mend, 0);
+        }
+        return;
+    }
+    store_state(p.hp, p.lp, ((size_t)rq.srow * p.H + h) * D * D);
+    if (rq.start != -2 && h == 0 && threadIdx.x == 0) p.base[rq.srow] = p.h[rq.srow] = p.nd[rq.srow] = 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 2) scan_tc_kernel(const __grid_constant__ PrefillParams p) {
+    extern __shared__ unsigned char raw[];
+    const int h = blockIdx.x % p.H, r = blockIdx.x / p.H;
+    if (p.rg.cu_tokens[r + 1] - p.rg.cu_tokens[r] <= kShort) return;
+    const Request rq = load_request(p, r, h == 0 && threadIdx.x == 0);
+    if (!rq.ok) return;
+    unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    Bars *b = reinterpret_cast<Bars *>(smem + Smem::BAR);
+    if (threadIdx.x < 32) {
+        tmem_alloc(&b->tmem, kTmem);
+        if (threadIdx.x == 0) {
+            for (uint64_t *x : {b->full_k, b->full_k + 1, &b->full_q, &b->full_t, &b->full_p, &b->mx, &b->mz,
+                                &b->mu, &b->md, &b->my})
+                mbar_init(x, 1);
+            mbar_init(&b->mend, 2);
+            b->abort = 0;
+            b->nk = b->nq = b->nt = 0;
+            b->tiles = p.tiles + ((size_t)rq.chunk0 * p.G + h / p.rep) * (2 * kTile);
+            b->tile_step = (unsigned long long)p.G * (2 * kTile);
+            b->rec = p.rec + (size_t)rq.chunk0 * p.H + h;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
+        tc_fence_before_sync();
+    }
+    __syncthreads();
+    tc_fence_after_sync();
+    scan_head(p, rq, h, r, smem, b);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (threadIdx.x < 32) tmem_dealloc(b->tmem, kTmem);
+}
+
+}  // namespace
+
+namespace prefill {
+
+cudaError_t scan_tc_launch(const PrefillParams &p, cudaStream_t s) {
+    static SmemGrants grants;
+    const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&scan_tc_kernel), Smem::BYTES, grants);
+    if (e != cudaSuccess) return e;
+    scan_tc_kernel<<<p.R * p.H, kThreads, Smem::BYTES, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace prefill
+
+}  // namespace rs
