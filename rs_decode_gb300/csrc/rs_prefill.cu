@@ -96,18 +96,24 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
 
 // ---------------------------------------------------------------- chunk kernel
 // One CTA per chunk and key head: the products K K^T and Q K^T are shared by
-// the key head's value heads, whose decays and betas differ.  The triangular
-// inverse is fp32: four 16 x 16 diagonal blocks by substitution (a column per
-// thread), then twice  [[a,0],[c,b]]^-1 = [[a',0],[-b' c a', b']].
+// the key head's value heads, whose decays and betas differ and which are
+// served two at a time, 64 threads each.  The triangular inverse is fp32 and
+// in place: four 16 x 16 diagonal blocks by substitution (a column per thread),
+// then twice  [[a,0],[c,b]]^-1 = [[a',0],[-b' c a', b']]  with the product c a'
+// waiting in the unused block above the diagonal.  Substitution over the whole
+// 64 rows would be one dependent chain of 2016 steps; the two products are
+// register-tiled fp32 work (paired FMAs) that keeps the accuracy of T, which
+// every u of the chunk inherits.
 constexpr int kChunkThreads = 128;
 constexpr int LDM = C + 4;  // fp32 matrices in shared memory: 16-byte rows, banks shifted by 4
+constexpr int kMat = C * LDM;
 
 template <int D>
 struct ChunkSmem {
     static constexpr int TILES = 2 * C * D * 2;
-    static constexpr int MATS = 2 * C * LDM * 4;
-    static constexpr int IMAGE = TILES > MATS ? TILES : MATS;  // the record's image after either
-    static constexpr int BYTES = IMAGE + (int)sizeof(Record) + 4 * C * 4;
+    static constexpr int MATS = 2 * kMat * 4;
+    static constexpr int VECS = TILES > MATS ? TILES : MATS;  // after the tiles, or the matrices in their place
+    static constexpr int BYTES = VECS + (2 + 2 * 4) * C * 4 + 2 * 16;
 };
 
 // Sum of (value, error) pairs: the sum's rounding error goes into the error.
@@ -116,56 +122,147 @@ __device__ __forceinline__ void add2(float &h, float &l, float h2, float l2) {
     l = l + l2 + ((h - (s - b)) + (h2 - b));
     h = s;
 }
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// out[RI rows][4 columns] (+)= sgn * sum over m in [m0, m1) of a[row][m] x[m][column]; m0, m1 multiples of 4
+template <int RI, int CJ>
+__device__ __forceinline__ void tile_product(const float *a, const float *x, int m0, int m1, unsigned long long (&acc)[RI][CJ / 2]) {
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ / 2; ++j) acc[i][j] = 0;
+#pragma unroll 2
+    for (int m = m0; m < m1; m += 4) {
+        float av[RI][4];
+#pragma unroll
+        for (int i = 0; i < RI; ++i) {
+            const float4 v = *reinterpret_cast<const float4 *>(a + i * LDM + m);
+            av[i][0] = v.x, av[i][1] = v.y, av[i][2] = v.z, av[i][3] = v.w;
+        }
+#pragma unroll
+        for (int mm = 0; mm < 4; ++mm) {
+            unsigned long long xv[CJ / 2];
+#pragma unroll
+            for (int j = 0; j < CJ / 4; ++j) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(x + (m + mm) * LDM + 4 * j);
+                xv[2 * j] = v.x, xv[2 * j + 1] = v.y;
+            }
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                const unsigned long long w = f2_pack(av[i][mm], av[i][mm]);
+#pragma unroll
+                for (int j = 0; j < CJ / 2; ++j) acc[i][j] = f2_fma(w, xv[j], acc[i][j]);
+            }
+        }
+    }
+}
+template <int RI, int CJ>
+__device__ __forceinline__ void tile_store(float *out, const unsigned long long (&acc)[RI][CJ / 2], bool negate) {
+    const unsigned long long sign = negate ? 0x8000000080000000ull : 0;
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ / 4; ++j)
+            *reinterpret_cast<ulonglong2 *>(out + i * LDM + 4 * j) = make_ulonglong2(acc[i][2 * j] ^ sign, acc[i][2 * j + 1] ^ sign);
+}
+
+__device__ __forceinline__ void group_sync(int grp) {  // the 64 threads of one head
+    if (grp == 0)
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+    else
+        asm volatile("bar.sync 2, 64;" ::: "memory");
+}
 
 template <int D>
-__global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_constant__ PrefillParams p) {
+__global__ void __launch_bounds__(kChunkThreads, 4) chunk_kernel(const __grid_constant__ PrefillParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
     const int chunk = blockIdx.x / p.G, g = blockIdx.x - chunk * p.G;
     if (chunk >= min(p.rg.counts[1], p.ccap)) return;
     const int4 e = reinterpret_cast<const int4 *>(p.rg.chunks)[chunk];
     const int n = e.z;
-    if (e.x < 0 || e.x >= p.R || n < 1 || n > C || e.y < 0 || e.y > p.cap - n) return;  // scan_kernel reports it
+    if (e.x < 0 || e.x >= p.R || n < 1 || n > C || e.y < 0 || e.y > p.cap - n) return;  // the scan reports it
     if (p.rg.cu_tokens[e.x + 1] - p.rg.cu_tokens[e.x] <= kShort) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t sK = smem_u32(smem), sQ = sK + C * D * 2;
     load_tile<D>(sK, p.k + (long long)e.y * p.ld_k + g * D, p.ld_k, n, tid, kChunkThreads);
     load_tile<D>(sQ, p.q + (long long)e.y * p.ld_q + g * D, p.ld_q, n, tid, kChunkThreads);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+
+    float *sk = reinterpret_cast<float *>(smem + ChunkSmem<D>::VECS), *sq = sk + C;
+    float *vec = sq + C;                               // per head of a pair: gh, gl, beta, ke
+    float *bounds = vec + 2 * 4 * C;                   // per head of a pair: umax, kmax
+    // the first pair's decays are summed while the tiles are on their way
+    float h[2], l[2], cgh, cgl;
+    auto decays = [&](int hv, float *v) {
+        // two rows a lane; sums of log2 alpha as (value, error) pairs, so that
+        // differences of large sums keep their low bits
+        float *gh = v, *gl = gh + C, *be = gl + C;
+        l[0] = l[1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            const bool in = t < n;
+            const float a = in ? p.alpha[(long long)(e.y + t) * p.H + hv] : 1.f;
+            be[t] = in ? p.beta[(long long)(e.y + t) * p.H + hv] : 0.f;
+            const float x = log2f(a);
+            h[i] = x < -160.f ? -160.f : x;
+        }
+        add2(h[1], l[1], h[0], l[0]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float xh = __shfl_up_sync(~0u, h[1], o), xl = __shfl_up_sync(~0u, l[1], o);
+            if (lane >= o) add2(h[1], l[1], xh, xl);
+        }
+        float ph = __shfl_up_sync(~0u, h[1], 1), pl = __shfl_up_sync(~0u, l[1], 1);
+        if (lane == 0) ph = pl = 0.f;
+        add2(h[0], l[0], ph, pl);
+        cgh = __shfl_sync(~0u, h[1], 31), cgl = __shfl_sync(~0u, l[1], 31);
+        gh[2 * lane] = h[0], gl[2 * lane] = l[0], gh[2 * lane + 1] = h[1], gl[2 * lane + 1] = l[1];
+    };
+    if (warp < 2 && warp < p.rep) decays(g * p.rep + warp, vec + warp * 4 * C);
     cp_async_wait_all();
     __syncthreads();
 
     // bf16 -> fp16 in place, two threads a row: each row scaled to [1, 2)
-    Record *image = reinterpret_cast<Record *>(smem + ChunkSmem<D>::IMAGE);
-    float *sk = reinterpret_cast<float *>(image + 1), *gh = sk + C, *gl = gh + C, *be = gl + C;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         const int row = tid >> 1, c0 = (tid & 1) * (D / 16);
         uint4 v[D / 16];
-        float m = 0.f;
+        __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
             v[c] = *reinterpret_cast<const uint4 *>(smem + w * (C * D * 2) + piece(row, c0 + c));
-            float f[8];
-            unpack<uint16_t, 8>(v[c], f);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) m = fmaxf(m, fabsf(f[x]));
+            for (uint32_t x : {v[c].x, v[c].y, v[c].z, v[c].w}) {
+                const uint32_t mag = x & 0x7fff7fffu;
+                m2 = __hmax2(m2, *reinterpret_cast<const __nv_bfloat162 *>(&mag));
+            }
         }
+        float m = fmaxf(__low2float(m2), __high2float(m2));
         m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
         float up, down;
         row_scale<0>(m, up, down);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-            float f[8];
-            unpack<uint16_t, 8>(v[c], f);
+            auto half2 = [&](uint32_t x) {
+                return pack_h2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+            };
             *reinterpret_cast<uint4 *>(smem + w * (C * D * 2) + piece(row, c0 + c)) =
-                make_uint4(pack_h2(f[0] * up, f[1] * up), pack_h2(f[2] * up, f[3] * up),
-                           pack_h2(f[4] * up, f[5] * up), pack_h2(f[6] * up, f[7] * up));
+                make_uint4(half2(v[c].x), half2(v[c].y), half2(v[c].z), half2(v[c].w));
         }
-        if ((tid & 1) == 0) (w ? image->sq : sk)[row] = down;
+        if ((tid & 1) == 0) (w ? sq : sk)[row] = down;
     }
+    fence_proxy_async_smem();
     __syncthreads();
-    {
-        uint4 *out = reinterpret_cast<uint4 *>(p.tiles + ((size_t)chunk * p.G + g) * (2 * C * D * 2));
-        for (int i = tid; i < 2 * C * D * 2 / 16; i += kChunkThreads) out[i] = reinterpret_cast<const uint4 *>(smem)[i];
+    if (tid == 0) {  // both tiles, as they are, to the workspace
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(
+                         p.tiles + ((size_t)chunk * p.G + g) * (2 * C * D * 2)),
+                     "r"(sK), "r"(2 * C * D * 2)
+                     : "memory");
     }
 
     // rows 16 warp.. of K K^T and Q K^T, up to the diagonal
@@ -187,178 +284,167 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
             }
         }
     }
+    // keys' powers of two into K K^T
+    const int i0 = warp * 16 + (lane >> 2), j0 = (lane & 3) * 2;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+        const float2 s = *reinterpret_cast<const float2 *>(sk + nt * 8 + j0);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            kk[nt][2 * hf] *= s.x * sk[i0 + 8 * hf];
+            kk[nt][2 * hf + 1] *= s.y * sk[i0 + 8 * hf];
+        }
+    }
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncthreads();  // the tiles' place is the matrices' from here
 
-    float *A = reinterpret_cast<float *>(smem), *X = A + C * LDM;
-
-    for (int r = 0; r < p.rep; ++r) {
-        const int hv = g * p.rep + r;
-        if (warp == 0) {
-            // two rows a lane; sums of log2 alpha as (value, error) pairs, so
-            // that differences of large sums keep their low bits
-            float h[2], l[2] = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                const bool in = t < n;
-                const float a = in ? p.alpha[(long long)(e.y + t) * p.H + hv] : 1.f;
-                be[t] = in ? p.beta[(long long)(e.y + t) * p.H + hv] : 0.f;
-                const float x = log2f(a);
-                h[i] = x < -160.f ? -160.f : x;
-            }
-            add2(h[1], l[1], h[0], l[0]);
-            float sh = h[1], sl = l[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float xh = __shfl_up_sync(~0u, sh, o), xl = __shfl_up_sync(~0u, sl, o);
-                if (lane >= o) add2(sh, sl, xh, xl);
-            }
-            float ph = __shfl_up_sync(~0u, sh, 1), pl = __shfl_up_sync(~0u, sl, 1);
-            if (lane == 0) ph = pl = 0.f;
-            add2(h[0], l[0], ph, pl);
-            const float ch = __shfl_sync(~0u, sh, 31), cl = __shfl_sync(~0u, sl, 31);
-            gh[2 * lane] = h[0], gl[2 * lane] = l[0], gh[2 * lane + 1] = sh, gl[2 * lane + 1] = sl;
-            const float e0 = exp2f(h[0] + l[0]), e1 = exp2f(sh + sl);
-            image->egq[2 * lane] = e0 * image->sq[2 * lane], image->egq[2 * lane + 1] = e1 * image->sq[2 * lane + 1];
-            if (lane == 31) image->all = e1;
-            const float k0 = e0 * sk[2 * lane], k1 = e1 * sk[2 * lane + 1];
-            image->egk[2 * lane] = k0, image->egk[2 * lane + 1] = k1;
-            float km = fmaxf(k0, k1);
+    float *mats = reinterpret_cast<float *>(smem);
+    for (int r0 = 0; r0 < p.rep; r0 += 2) {
+        const int heads = min(2, p.rep - r0);
+        if (warp < heads) {
+            float *v = vec + warp * 4 * C;
+            if (r0 > 0) decays(g * p.rep + r0 + warp, v);
+            Record &out = p.rec[(size_t)chunk * p.H + g * p.rep + r0 + warp];
+            const float e0 = exp2f(h[0] + l[0]), e1 = exp2f(h[1] + l[1]);
+            const float k0 = exp2f((cgh - h[0]) + (cgl - l[0])), k1 = exp2f((cgh - h[1]) + (cgl - l[1]));
+            const float2 skl = *reinterpret_cast<const float2 *>(sk + 2 * lane), sql = *reinterpret_cast<const float2 *>(sq + 2 * lane);
+            *reinterpret_cast<float2 *>(out.egk + 2 * lane) = make_float2(e0 * skl.x, e1 * skl.y);
+            *reinterpret_cast<float2 *>(out.egq + 2 * lane) = make_float2(e0 * sql.x, e1 * sql.y);
+            *reinterpret_cast<float2 *>(out.sq + 2 * lane) = sql;
+            *reinterpret_cast<float2 *>(out.ke + 2 * lane) = make_float2(k0, k1);
+            *reinterpret_cast<float2 *>(v + 3 * C + 2 * lane) = make_float2(k0, k1);
+            float km = fmaxf(e0 * skl.x, e1 * skl.y);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) km = fmaxf(km, __shfl_xor_sync(~0u, km, o));
-            // D products of a state value and a key below 2
-            if (lane == 0) image->xmax = 2.f * D * km, image->umax = image->kmax = 0.f;
-            image->ke[2 * lane] = exp2f((ch - h[0]) + (cl - l[0]));
-            image->ke[2 * lane + 1] = exp2f((ch - sh) + (cl - sl));
+            if (lane == 31) out.all = e1;
+            if (lane == 0) {
+                out.xmax = 2.f * D * km;  // D products of a state value and a key below 2
+                bounds[2 * warp] = bounds[2 * warp + 1] = 0.f;
+            }
         }
         __syncthreads();
         // A and P of this warp's rows
-        const int i0 = warp * 16 + (lane >> 2);
+        for (int r = 0; r < heads; ++r) {
+            const float *gh = vec + r * 4 * C, *gl = gh + C, *be = gl + C;
+            float *A = mats + r * kMat;
+            unsigned char *pout = reinterpret_cast<unsigned char *>(p.rec[(size_t)chunk * p.H + g * p.rep + r0 + r].p);
+            const float hi[2] = {gh[i0], gh[i0 + 8]}, lo[2] = {gl[i0], gl[i0 + 8]}, bi[2] = {be[i0], be[i0 + 8]};
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
+            for (int nt = 0; nt < 8; ++nt) {
+                const int j = nt * 8 + j0;
+                const float2 hj = *reinterpret_cast<const float2 *>(gh + j), lj = *reinterpret_cast<const float2 *>(gl + j);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int i = i0 + 8 * hf, j = nt * 8 + (lane & 3) * 2;
-                float a[2] = {0.f, 0.f}, pv[2] = {0.f, 0.f};
-                if (nt <= 2 * warp + 1) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        if (j + x <= i) {
-                            const float d = exp2f((gh[i] - gh[j + x]) + (gl[i] - gl[j + x]));
-                            pv[x] = d * qk[nt][2 * hf + x];
-                            a[x] = j + x < i ? be[i] * d * (kk[nt][2 * hf + x] * sk[i] * sk[j + x]) : 0.f;
-                        }
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int i = i0 + 8 * hf;
+                    float2 av = make_float2(0.f, 0.f), pv = av;
+                    if (nt <= 2 * warp + 1) {
+                        const float d0 = j <= i ? exp2_fast((hi[hf] - hj.x) + (lo[hf] - lj.x)) : 0.f;
+                        const float d1 = j + 1 <= i ? exp2_fast((hi[hf] - hj.y) + (lo[hf] - lj.y)) : 0.f;
+                        pv = make_float2(j <= i ? d0 * qk[nt][2 * hf] : 0.f, j + 1 <= i ? d1 * qk[nt][2 * hf + 1] : 0.f);
+                        av = make_float2(j < i ? bi[hf] * d0 * kk[nt][2 * hf] : 0.f,
+                                         j + 1 < i ? bi[hf] * d1 * kk[nt][2 * hf + 1] : 0.f);
                     }
-                }
-                *reinterpret_cast<float2 *>(A + i * LDM + j) = make_float2(a[0], a[1]);
-                *reinterpret_cast<float2 *>(X + i * LDM + j) = make_float2(0.f, 0.f);
-                *reinterpret_cast<uint32_t *>(reinterpret_cast<unsigned char *>(image->p) + piece(i, nt) +
-                                              (lane & 3) * 4) = pack_h2(pv[0], pv[1]);
-            }
-        }
-        __syncthreads();
-        if (tid < C) {  // diagonal blocks: column tid of block tid / 16
-            const int b = tid & ~15, col = tid & 15;
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float s = i == col ? 1.f : 0.f;
-#pragma unroll
-                for (int m = 0; m < i; ++m) s = fmaf(-A[(b + i) * LDM + b + m], x[m], s);
-                x[i] = s;
-                X[(b + i) * LDM + b + col] = s;
-            }
-        }
-        __syncthreads();
-        {  // two 32 x 32 blocks; the product c a' waits in the zero block above the diagonal
-            const int pr = tid >> 6, t = tid & 63, i = t >> 2, c4 = (t & 3) * 4, o = 32 * pr;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const float a = A[(o + 16 + i) * LDM + o + m];
-                const float4 x = *reinterpret_cast<const float4 *>(X + (o + m) * LDM + o + c4);
-                s.x = fmaf(a, x.x, s.x), s.y = fmaf(a, x.y, s.y), s.z = fmaf(a, x.z, s.z), s.w = fmaf(a, x.w, s.w);
-            }
-            *reinterpret_cast<float4 *>(X + (o + i) * LDM + o + 16 + c4) = s;
-            __syncthreads();
-            s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const float a = -X[(o + 16 + i) * LDM + o + 16 + m];
-                const float4 x = *reinterpret_cast<const float4 *>(X + (o + m) * LDM + o + 16 + c4);
-                s.x = fmaf(a, x.x, s.x), s.y = fmaf(a, x.y, s.y), s.z = fmaf(a, x.z, s.z), s.w = fmaf(a, x.w, s.w);
-            }
-            *reinterpret_cast<float4 *>(X + (o + 16 + i) * LDM + o + c4) = s;
-            __syncthreads();
-            *reinterpret_cast<float4 *>(X + (o + i) * LDM + o + 16 + c4) = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        __syncthreads();
-        {  // the 64 x 64 block, the same way
-            const int i = (tid >> 3) * 2, c4 = (tid & 7) * 4;
-            float4 s[2] = {};
-#pragma unroll 8
-            for (int m = 0; m < 32; ++m) {
-                const float4 x = *reinterpret_cast<const float4 *>(X + m * LDM + c4);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float a = A[(32 + i + y) * LDM + m];
-                    s[y].x = fmaf(a, x.x, s[y].x), s[y].y = fmaf(a, x.y, s[y].y);
-                    s[y].z = fmaf(a, x.z, s[y].z), s[y].w = fmaf(a, x.w, s[y].w);
+                    *reinterpret_cast<float2 *>(A + i * LDM + j) = av;
+                    *reinterpret_cast<uint32_t *>(pout + piece(i, nt) + (lane & 3) * 4) = pack_h2(pv.x, pv.y);
                 }
             }
+        }
+        __syncthreads();
+        const int grp = tid >> 6, t = tid & 63;
+        if (grp < heads) {
+            float *A = mats + grp * kMat;
+            {  // diagonal blocks: column t of block t / 16
+                const int b = t & ~15, col = t & 15;
+                float x[16];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) *reinterpret_cast<float4 *>(X + (i + y) * LDM + 32 + c4) = s[y];
-            __syncthreads();
-            s[0] = s[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int m = 0; m < 32; ++m) {
-                const float4 x = *reinterpret_cast<const float4 *>(X + m * LDM + 32 + c4);
+                for (int i = 0; i < 16; ++i) {
+                    float s0 = i == col ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float a = -X[(32 + i + y) * LDM + 32 + m];
-                    s[y].x = fmaf(a, x.x, s[y].x), s[y].y = fmaf(a, x.y, s[y].y);
-                    s[y].z = fmaf(a, x.z, s[y].z), s[y].w = fmaf(a, x.w, s[y].w);
+                    for (int m = 0; m < i; m += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(A + (b + i) * LDM + b + m);
+                        s0 = fmaf(-v.x, x[m], s0);
+                        if (m + 1 < i) s1 = fmaf(-v.y, x[m + 1], s1);
+                        if (m + 2 < i) s0 = fmaf(-v.z, x[m + 2], s0);
+                        if (m + 3 < i) s1 = fmaf(-v.w, x[m + 3], s1);
+                    }
+                    x[i] = s0 + s1;
+                }
+                __syncwarp();  // a block's columns are one warp's: all of A's block is read
+#pragma unroll
+                for (int i = 0; i < 16; ++i) A[(b + i) * LDM + b + col] = x[i];
+                __syncwarp();
+            }
+            {  // the two 32 x 32 blocks, one a warp
+                const int o = 32 * (warp & 1), i = lane >> 1, c = (lane & 1) * 8;
+                unsigned long long acc[1][4];
+                tile_product<1, 8>(A + (o + 16 + i) * LDM + o, A + o * LDM + o + c, 0, 16, acc);
+                tile_store<1, 8>(A + (o + i) * LDM + o + 16 + c, acc, false);
+                __syncwarp();
+                tile_product<1, 8>(A + (o + 16 + i) * LDM + o + 16, A + o * LDM + o + 16 + c, 0, 16, acc);
+                tile_store<1, 8>(A + (o + 16 + i) * LDM + o + c, acc, true);
+            }
+            group_sync(grp);
+            {  // the 64 x 64 block; zero halves of the triangular factors are skipped
+                unsigned long long acc[4][2];
+                const int w = warp & 1;
+                {
+                    const int i = (lane >> 2) * 4, c = 16 * w + (lane & 3) * 4;
+                    tile_product<4, 4>(A + (32 + i) * LDM, A + c, 16 * w, 32, acc);
+                    tile_store<4, 4>(A + i * LDM + 32 + c, acc, false);
+                }
+                group_sync(grp);
+                {
+                    const int i = 16 * (1 - w) + (lane >> 3) * 4, c = (lane & 7) * 4;
+                    tile_product<4, 4>(A + (32 + i) * LDM + 32, A + 32 + c, 0, 32 - 16 * w, acc);
+                    tile_store<4, 4>(A + (32 + i) * LDM + c, acc, true);
                 }
             }
+            group_sync(grp);
+            // T = X diag(beta), each row scaled and split in two; 8 threads a row
+            Record &out = p.rec[(size_t)chunk * p.H + g * p.rep + r0 + grp];
+            const float *be = vec + grp * 4 * C + 2 * C, *ke = be + C;
+            const int c = t & 7;
+            float bj[8];
+            *reinterpret_cast<float4 *>(bj) = *reinterpret_cast<const float4 *>(be + c * 8);
+            *reinterpret_cast<float4 *>(bj + 4) = *reinterpret_cast<const float4 *>(be + c * 8 + 4);
+            float um = 0.f, kmx = 0.f;
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) {
+                const int row = i * 8 + (t >> 3);
+                float v[8], m = 0.f, sum = 0.f, up, down;
+                *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(A + row * LDM + c * 8);
+                *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(A + row * LDM + c * 8 + 4);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) *reinterpret_cast<float4 *>(X + (32 + i + y) * LDM + c4) = s[y];
+                for (int x = 0; x < 8; ++x) {
+                    v[x] = c * 8 + x <= row ? v[x] * bj[x] : 0.f;
+                    m = fmaxf(m, fabsf(v[x]));
+                    sum += fabsf(v[x]);
+                }
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) {
+                    m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+                    sum += __shfl_xor_sync(~0u, sum, o);
+                }
+                row_scale<8>(m, up, down);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) split2(v[2 * x] * up, v[2 * x + 1] * up, hi[x], lo[x]);
+                *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(out.t_hi) + piece(row, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(out.t_lo) + piece(row, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (c == 0) out.su[row] = down * sk[row];
+                um = fmaxf(um, sum * sk[row]);
+                kmx = fmaxf(kmx, sum * sk[row] * ke[row]);
+            }
+#pragma unroll
+            for (int o = 8; o < 32; o <<= 1) um = fmaxf(um, __shfl_xor_sync(~0u, um, o)), kmx = fmaxf(kmx, __shfl_xor_sync(~0u, kmx, o));
+            if (lane == 0) {
+                // non-negative floats compare as integers, so the order of the two warps does not matter
+                atomicMax(reinterpret_cast<int *>(bounds + 2 * grp), __float_as_int(um));
+                atomicMax(reinterpret_cast<int *>(bounds + 2 * grp + 1), __float_as_int(kmx));
+            }
+            group_sync(grp);
+            if (t == 0) out.umax = bounds[2 * grp], out.kmax = bounds[2 * grp + 1];
         }
-        __syncthreads();
-        // T = X diag(beta), each row scaled and split in two; 8 threads a row
-        for (int i = tid; i < C * C / 8; i += kChunkThreads) {
-            const int row = i >> 3, c = i & 7;
-            float t[8], m = 0.f, sum = 0.f, up, down;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int j = c * 8 + x;
-                t[x] = j <= row ? X[row * LDM + j] * be[j] : 0.f;
-                m = fmaxf(m, fabsf(t[x]));
-                sum += fabsf(t[x]);
-            }
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-                sum += __shfl_xor_sync(~0u, sum, o);
-            }
-            row_scale<8>(m, up, down);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) split2(t[2 * x] * up, t[2 * x + 1] * up, hi[x], lo[x]);
-            *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(image->t_hi) + piece(row, c)) =
-                make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(image->t_lo) + piece(row, c)) =
-                make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (c == 0) {
-                image->su[row] = down * sk[row];
-                // the order of the maxima does not matter: non-negative floats compare as integers
-                atomicMax(reinterpret_cast<int *>(&image->umax), __float_as_int(sum * sk[row]));
-                atomicMax(reinterpret_cast<int *>(&image->kmax), __float_as_int(sum * sk[row] * image->ke[row]));
-            }
-        }
-        __syncthreads();
-        uint4 *out = reinterpret_cast<uint4 *>(p.rec + (size_t)chunk * p.H + hv);
-        const uint4 *img = reinterpret_cast<const uint4 *>(image);
-        for (int i = tid; i < (int)sizeof(Record) / 16; i += kChunkThreads) out[i] = img[i];
         __syncthreads();
     }
 }
