@@ -237,6 +237,7 @@ __device__ __forceinline__ void drain(Bars *b) {
 // Steps of 16 in a product's inner dimension are 32 bytes along a row (2 in a
 // descriptor), or 16 rows (128) where the tile is read MN-major.
 constexpr uint32_t kHalfD = kHalf >> 4;
+constexpr uint32_t kHalfStride = ((kHalf >> 4) - (1024 >> 4)) << 16;  // leading offset: from one 64-wide tile to the next
 __device__ __forceinline__ void issue_x(uint32_t tm, uint32_t k, Bars *b) {
 #pragma unroll
     for (int x = 0; x < 8; ++x)
@@ -263,11 +264,9 @@ __device__ __forceinline__ void issue_u(uint32_t tm, uint32_t t, Bars *b) {
 }
 __device__ __forceinline__ void issue_d(uint32_t tm, uint32_t k, Bars *b) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {  // 16 rows of the chunk a step; keys 0..63, then 64..127
-        mma_ts(tm + 128, tm + 8 * x, k + x * 128, idesc_f16(64, true), x > 0);
-        mma_ts(tm + 192, tm + 8 * x, k + kHalfD + x * 128, idesc_f16(64, true), x > 0);
-        mma_ts(tm + 128, tm + 32 + 8 * x, k + x * 128, idesc_f16(64, true), true);
-        mma_ts(tm + 192, tm + 32 + 8 * x, k + kHalfD + x * 128, idesc_f16(64, true), true);
+    for (int x = 0; x < 4; ++x) {  // 16 rows of the chunk a step; two tiles of 64 keys side by side
+        mma_ts(tm + 128, tm + 8 * x, k + x * 128 + kHalfStride, idesc_f16(128, true), x > 0);
+        mma_ts(tm + 128, tm + 32 + 8 * x, k + x * 128 + kHalfStride, idesc_f16(128, true), true);
     }
     umma_commit(&b->md);
 }
@@ -297,7 +296,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
     constexpr int DH = D / 2, CH = C / 2;
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), hf = warp >> 2;
     const int row = threadIdx.x & 127;  // value column of the head
-    const uint32_t base = b->tmem, sm = smem_u32(smem);
+    const uint32_t base = __reduce_or_sync(~0u, b->tmem), sm = smem_u32(smem);  // the reduction makes it a uniform register
     const uint32_t lanes = base + ((uint32_t)(warp & 3) << 21);
     const uint32_t t_shi = lanes + 192 + 32 * hf, t_slo = lanes + 32 * hf;          // state
     const uint32_t t_ohi = lanes + 16 * hf, t_olo = lanes + 32 + 16 * hf;           // R, u
@@ -457,7 +456,8 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         float uup, udown, kup, kdown;
         row_scale<14>(ubound, uup, udown);
         row_scale<14>(kbound, kup, kdown);
-        const unsigned long long rd2 = f2_pack(rdown, rdown), uup2 = f2_pack(uup, uup);
+        const float uups = uup * rdown, kups = kup * rdown;  // from R's scale to u's
+        const f2 uup2 = f2_pack(uups, uups);
         ok = wait_warp(&b->mu, ph, b, p.status) && ok;
         tc_fence_after_sync();
         if (i + 1 < nch && warp == 3) load_t(b, sm, i + 1, p.H);
@@ -469,7 +469,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
                 const ulonglong2 su = *reinterpret_cast<const ulonglong2 *>(vec.su + hf * CH + t + e);
-                x[e / 2] = f2_mul(x[e / 2], f2_mul(su.x, rd2)), x[e / 2 + 1] = f2_mul(x[e / 2 + 1], f2_mul(su.y, rd2));
+                x[e / 2] = f2_mul(x[e / 2], su.x), x[e / 2 + 1] = f2_mul(x[e / 2 + 1], su.y);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[t / 2 + e] = pack_pair(f2_mul(x[e], uup2));
@@ -478,7 +478,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
                 const ulonglong2 ke = *reinterpret_cast<const ulonglong2 *>(vec.ke + hf * CH + t + e);
                 x[e / 2] = f2_mul(x[e / 2], ke.x), x[e / 2 + 1] = f2_mul(x[e / 2 + 1], ke.y);
             }
-            put_split(t_ohi + t / 2, t_olo + t / 2, x, f2_pack(kup, kup));
+            put_split(t_ohi + t / 2, t_olo + t / 2, x, f2_pack(kups, kups));
         }
         // the queries' place takes u once Z is complete; Z leaves TMEM in fp16
         // (2^-9 keeps its sums, below 2^24, in range)
