@@ -14,6 +14,8 @@
 // T = (I + A)^-1 diag(beta) and P do not depend on the state, so
 //   chunk_kernel  computes them for all chunks and heads at once, and
 //   scan_kernel   carries S through a request's chunks.
+// (Segments, rs_prefill.cuh, cut a long request's chunks where few chains would
+// leave the GPU idle.)
 // Requests of at most kShort rows go through step_kernel instead, which runs
 // the recurrence row by row beside one read and one write of the state.
 // Decays enter as differences G_i - G_j only, so nothing overflows however
@@ -581,18 +583,20 @@ struct ScanSmem {
 };
 
 
-template <int D, int NW>
-__global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ PrefillParams p) {
+template <int D, int NW, bool OUT>
+__global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ PrefillParams p, int units) {
     using M = ScanSmem<D, NW>;
     constexpr int SPLIT = D / (16 * NW);  // CTAs of one head
     constexpr int NT = NW * 32;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part = blockIdx.x % SPLIT, hr = blockIdx.x / SPLIT;
-    const int h = hr % p.H, r = hr / p.H;
+    const int h = hr % p.H, q = hr / p.H % units, r = hr / p.H / units;
     if (p.rg.cu_tokens[r + 1] - p.rg.cu_tokens[r] <= kShort) return;
-    const Request rq = load_request(p, r, h == 0 && part == 0 && tid == 0);
+    const Request rq = load_request(p, r, h == 0 && part == 0 && q == 0 && tid == 0);
     if (!rq.ok) return;
+    const Unit un = scan_unit<OUT>(p, hr, rq, r, q);
+    if (!un.ok) return;
     const int g = h / p.rep;
     const int col0 = (part * NW + warp) * 16;
     const uint32_t s0 = smem_u32(smem);
@@ -609,28 +613,25 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
         for (int x = tid; x < C * NW * 2; x += NT) {
             const int t = x / (NW * 2), c = x % (NW * 2);
             cp16(st + 2 * M::TILE + (c >> 1) * (C * 32) + t * 32 + (((c & 1) ^ ((t >> 2) & 1)) << 4),
-                 v + (t < n ? t : 0) * p.ld_v + c * 8, t < n);
+                 v + (t < n ? t : 0) * p.ld_v + c * 8, t < n && !un.map);
         }
         const unsigned char *rec = reinterpret_cast<const unsigned char *>(p.rec + (size_t)(rq.chunk0 + i) * p.H + h);
         for (int x = tid; x < (int)sizeof(Record) / 16; x += NT) cp16(st + M::REC + x * 16, rec + x * 16, true);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(0, s0);
+    fetch(un.c0, s0);
 
     // the starting state: S^T[p][n], rows p = col0 + gr (+8), columns n = 8 nt + 2 tq (+1)
     const int gr = lane >> 2, tq = lane & 3;
     float S[D / 8][4];
     {
-        const bool cont = rq.start == -2, lowp = p.prec == RS_PREC_SHARED_BF16;
-        const size_t slab = (cont ? (size_t)rq.srow * p.H + h : (size_t)max(rq.start, 0) * p.H + h) * D * D;
-        const float *f = (cont ? p.hp : static_cast<const float *>(p.pool));
-        const uint16_t *b = (cont ? p.lp : static_cast<const uint16_t *>(p.pool));
+        const StateSource from = unit_start<OUT, D>(p, rq, un);
 #pragma unroll
         for (int nt = 0; nt < D / 8; ++nt)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const size_t o = slab + (size_t)(nt * 8 + tq * 2 + (x & 1)) * D + col0 + gr + 8 * (x >> 1);
-                S[nt][x] = rq.start == -1 ? 0.f : lowp ? bf2f(b[o]) : f[o];
+                const int k = nt * 8 + tq * 2 + (x & 1), c = col0 + gr + 8 * (x >> 1);
+                S[nt][x] = from.kind == 0 ? 0.f : from.kind == 1 ? (k == c ? 1.f : 0.f) : from.kind == 2 ? from.f[k * D + c] : bf2f(from.b[k * D + c]);
             }
     }
     auto store_state = [&](float *f, uint16_t *b, size_t slab) {
@@ -644,14 +645,17 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
             }
     };
 
-    for (int i = 0; i < rq.nch; ++i) {
+    if (!OUT && un.seg == 0) store_state(p.segs, nullptr, seg_slab(p, un, 0, D * D));  // for the second pass
+
+    for (int i = un.c0; i < un.c1; ++i) {
+        const int odd = (i - un.c0) & 1;
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // this chunk's stage has landed, and every warp is done with the other one
-        const uint32_t st = s0 + (i & 1) * M::STAGE;
-        if (i + 1 < rq.nch) fetch(i + 1, s0 + ((i + 1) & 1) * M::STAGE);
+        const uint32_t st = s0 + odd * M::STAGE;
+        if (i + 1 < un.c1) fetch(i + 1, s0 + (odd ^ 1) * M::STAGE);
         const uint32_t sK = st, sQ = st + M::TILE, sV = st + 2 * M::TILE + warp * (C * 32);
         const uint32_t sTh = st + M::REC, sTl = sTh + C * C * 2, sP = sTl + C * C * 2;
-        const Record *rec = reinterpret_cast<const Record *>(smem + (i & 1) * M::STAGE + M::REC);
+        const Record *rec = reinterpret_cast<const Record *>(smem + odd * M::STAGE + M::REC);
 
         // S^T K^T and S^T Q^T: columns are the chunk's rows
         float X[8][4] = {}, Z[8][4] = {};
@@ -671,9 +675,11 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
                 mma_f16(X[2 * j + 1], hi, b[2], b[3]);
                 mma_f16(X[2 * j], lo, b[0], b[1]);
                 mma_f16(X[2 * j + 1], lo, b[2], b[3]);
-                ldsm4(b, sQ + o);
-                mma_f16(Z[2 * j], hi, b[0], b[1]);
-                mma_f16(Z[2 * j + 1], hi, b[2], b[3]);
+                if (OUT) {
+                    ldsm4(b, sQ + o);
+                    mma_f16(Z[2 * j], hi, b[0], b[1]);
+                    mma_f16(Z[2 * j + 1], hi, b[2], b[3]);
+                }
             }
         }
         // R^T = V^T - e^G S^T K^T, and the state's part of y
@@ -725,7 +731,7 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
             }
         }
         // y^T = (e^G S^T Q^T + u^T P^T) with the queries' powers of two
-        {
+        if (OUT) {
             float m0, m1, u0, u1, d0, d1;
             row_max(U, m0, m1);
             row_scale<14>(m0, u0, d0);
@@ -786,6 +792,7 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
 #pragma unroll
             for (int nt = 0; nt < D / 8; ++nt) S[nt][0] *= d0, S[nt][1] *= d0, S[nt][2] *= d1, S[nt][3] *= d1;
         }
+        if (!OUT) continue;
         // y through the warp's own V rows, to whole sectors
         __syncwarp();
 #pragma unroll
@@ -815,18 +822,120 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
                 store_state(static_cast<float *>(p.pool), nullptr, slab);
         }
     }
+    if (!OUT) {
+        if (un.map)
+            store_state(p.maps, nullptr, seg_slab(p, un, un.seg, D * D));
+        else
+            store_state(p.segs, nullptr, seg_slab(p, un, un.seg + 1, D * D));
+        return;
+    }
+    if (un.seg < un.nsegs - 1) return;
     store_state(p.hp, p.lp, ((size_t)rq.srow * p.H + h) * D * D);
     // a fresh start drops what the row had buffered (a continued row has nothing)
     if (rq.start != -2 && h == 0 && part == 0 && tid == 0) p.base[rq.srow] = p.h[rq.srow] = p.nd[rq.srow] = 0;
 }
 
-template <int D, int NW>
+// ---------------------------------------------------------------- combine kernel
+// S_(s+1) = M_s S_s + B_s over a request's segments, in order: per head and 32
+// value columns one CTA, which keeps S_s's columns in shared memory while the
+// next M_s is on its way.  fp32 throughout; bound by the maps' 64 KiB a step.
+template <int D>
+struct CombineSmem {
+    static constexpr int LD = D + 4;
+    static constexpr int MAP = D * LD * 4;
+    static constexpr int BYTES = 2 * MAP + 2 * D * 32 * 4;
+};
+
+template <int D>
+__global__ void __launch_bounds__(2 * D) combine_kernel(const __grid_constant__ PrefillParams p) {
+    using M = CombineSmem<D>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int part = blockIdx.x % (D / 32), hr = blockIdx.x / (D / 32);
+    const int tid = threadIdx.x;
+    Unit u;
+    u.h = hr % p.H, u.r = hr / p.H;
+    if (p.rg.cu_tokens[u.r + 1] - p.rg.cu_tokens[u.r] <= kShort) return;
+    const Request rq = load_request(p, u.r, false);
+    if (!rq.ok) return;
+    const int nsegs = (rq.nch + p.seglen - 1) / p.seglen;
+    if (nsegs < 3) return;
+    const uint32_t s0 = smem_u32(smem);
+    float *X = reinterpret_cast<float *>(smem + 2 * M::MAP);  // two buffers [D][32]
+    auto fetch = [&](int s) {
+        const float *src = p.maps + seg_slab(p, u, s, D * D);
+        const uint32_t dst = s0 + (s & 1) * M::MAP;
+        for (int i = tid; i < D * D / 4; i += 2 * D) cp16(dst + (i / (D / 4)) * (M::LD * 4) + (i % (D / 4)) * 16, src + i * 4, true);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(1);
+    for (int i = tid; i < D * 8; i += 2 * D)
+        reinterpret_cast<float4 *>(X)[i] = *reinterpret_cast<const float4 *>(p.segs + seg_slab(p, u, 1, D * D) + (i / 8) * D + part * 32 + (i % 8) * 4);
+    const int n = (tid >> 2) * 2, c = (tid & 3) * 8;  // rows n, n + 1, columns c..c + 7
+    for (int s = 1; s < nsegs - 1; ++s) {
+        if (s + 1 < nsegs - 1) {
+            fetch(s + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncthreads();
+        const float *m = reinterpret_cast<const float *>(smem + (s & 1) * M::MAP) + n * M::LD;
+        const float *x = X + ((s - 1) & 1) * (D * 32) + c;
+        float *out = p.segs + seg_slab(p, u, s + 1, D * D) + (size_t)n * D + part * 32 + c;
+        unsigned long long acc[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(out + i * D + 4 * j);
+                acc[i][2 * j] = v.x, acc[i][2 * j + 1] = v.y;
+            }
+#pragma unroll 4
+        for (int k = 0; k < D; k += 4) {
+            const float4 a0 = *reinterpret_cast<const float4 *>(m + k), a1 = *reinterpret_cast<const float4 *>(m + M::LD + k);
+            const float w0[4] = {a0.x, a0.y, a0.z, a0.w}, w1[4] = {a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const ulonglong2 x0 = *reinterpret_cast<const ulonglong2 *>(x + (k + kk) * 32);
+                const ulonglong2 x1 = *reinterpret_cast<const ulonglong2 *>(x + (k + kk) * 32 + 4);
+                const unsigned long long xv[4] = {x0.x, x0.y, x1.x, x1.y};
+                const unsigned long long p0 = f2_pack(w0[kk], w0[kk]), p1 = f2_pack(w1[kk], w1[kk]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[0][j] = f2_fma(p0, xv[j], acc[0][j]), acc[1][j] = f2_fma(p1, xv[j], acc[1][j]);
+            }
+        }
+        float *next = X + (s & 1) * (D * 32) + c;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const ulonglong2 v = make_ulonglong2(acc[i][2 * j], acc[i][2 * j + 1]);
+                *reinterpret_cast<ulonglong2 *>(out + i * D + 4 * j) = v;
+                *reinterpret_cast<ulonglong2 *>(next + (n + i) * 32 + 4 * j) = v;
+            }
+        __syncthreads();  // the next columns are complete, and this map's place is free
+    }
+}
+
+template <int D, int NW, bool OUT>
 cudaError_t scan_launch(const PrefillParams &p, cudaStream_t s) {
     static SmemGrants grants;
-    const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&scan_kernel<D, NW>), ScanSmem<D, NW>::BYTES, grants);
+    const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&scan_kernel<D, NW, OUT>), ScanSmem<D, NW>::BYTES, grants);
     if (e != cudaSuccess) return e;
-    scan_kernel<D, NW><<<p.R * p.H * (D / (16 * NW)), NW * 32, ScanSmem<D, NW>::BYTES, s>>>(p);
+    const int units = scan_units<OUT>(p);
+    scan_kernel<D, NW, OUT><<<p.R * p.H * units * (D / (16 * NW)), NW * 32, ScanSmem<D, NW>::BYTES, s>>>(p, units);
     return cudaGetLastError();
+}
+
+template <int D, bool OUT>
+cudaError_t scans(const PrefillParams &p, cudaStream_t s) {
+    if constexpr (D == 128) {
+        return scan_tc_launch<OUT>(p, s);
+    } else {
+        // a head on one CTA, or on two-warp CTAs where the heads alone would leave SMs idle
+        if (p.nseg == 1 && p.R * p.H <= 152) return scan_launch<D, 2, OUT>(p, s);
+        return scan_launch<D, D / 16, OUT>(p, s);
+    }
 }
 
 template <int D>
@@ -839,20 +948,42 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t s) {
     chunk_kernel<D><<<p.ccap * p.G, kChunkThreads, ChunkSmem<D>::BYTES, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if constexpr (D == 128) {
-        return scan_tc_launch(p, s);
-    } else {
-        // a head on one CTA, or on two-warp CTAs where the heads alone would leave SMs idle
-        if (p.R * p.H <= 152) return scan_launch<D, 2>(p, s);
-        return scan_launch<D, D / 16>(p, s);
+    if (p.nseg > 1) {
+        e = scans<D, false>(p, s);
+        if (e != cudaSuccess) return e;
+        static SmemGrants combine_grants;
+        e = grant_smem(reinterpret_cast<const void *>(&combine_kernel<D>), CombineSmem<D>::BYTES, combine_grants);
+        if (e != cudaSuccess) return e;
+        combine_kernel<D><<<p.R * p.H * (D / 32), 2 * D, CombineSmem<D>::BYTES, s>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
     }
+    return scans<D, true>(p, s);
+}
+
+// Segments of a request (1: none), from what the host knows: the chains alone,
+// requests x heads, against the 304 CTAs that the GPU holds at once.  The two
+// passes cost a little over twice the work and run at half a lone CTA's pace,
+// so fewer than five segments do not pay; one shorter than eight chunks would
+// spend its time on starting up.
+void plan_segments(const rs_layer_desc &d, const rs_ragged_desc &rd, int max_len, int &nseg, int &seglen) {
+    const int chunks = (max_len < rd.tokens_cap ? max_len : rd.tokens_cap) / C + 2;
+    const long long chains = (long long)rd.R * d.H;
+    long long want = chains < 304 ? 304 / chains : 1;
+    if (want > chunks / 8) want = chunks / 8;
+    nseg = want >= 5 ? (int)want : 1;
+    seglen = (chunks + nseg - 1) / nseg;
 }
 
 }  // namespace
 
+// The workspace: records, fp16 keys and queries, segments' states and maps.
 size_t prefill_bytes(const rs_layer_desc &d, const rs_ragged_desc &rd, int max_len) {
     if (max_len <= kShort) return 0;
-    return (size_t)ragged_chunks_cap(rd) * (d.H * sizeof(Record) + (size_t)d.G * 2 * C * d.N * 2);
+    int nseg, seglen;
+    plan_segments(d, rd, max_len, nseg, seglen);
+    return (size_t)ragged_chunks_cap(rd) * (d.H * sizeof(Record) + (size_t)d.G * 2 * C * d.N * 2) +
+           (nseg > 1 ? 2 * (size_t)rd.R * d.H * nseg * d.N * d.P * 4 : 0);
 }
 
 cudaError_t prefill_launch(const rs_layer_desc &d, const rs_state &st, const rs_ragged_desc &rd, const rs_ragged &rg,
@@ -867,6 +998,9 @@ cudaError_t prefill_launch(const rs_layer_desc &d, const rs_state &st, const rs_
     p.ld_q = in.ld_q, p.ld_k = in.ld_k, p.ld_v = in.ld_v;
     p.rows = in.rows, p.start = in.start, p.pool = in.pool, p.y = y, p.rec = static_cast<Record *>(work);
     p.tiles = static_cast<unsigned char *>(work) + (size_t)p.ccap * d.H * sizeof(Record);
+    plan_segments(d, rd, in.max_len, p.nseg, p.seglen);
+    p.segs = reinterpret_cast<float *>(p.tiles + (size_t)p.ccap * d.G * 2 * C * d.N * 2);
+    p.maps = p.segs + (size_t)rd.R * d.H * p.nseg * d.N * d.P;
     return d.P == 128 ? launch<128>(p, s) : launch<64>(p, s);
 }
 

@@ -57,6 +57,8 @@ struct PrefillParams {
     uint16_t *y;
     Record *rec;  // [ccap][H]
     unsigned char *tiles;  // [ccap][G] keys and queries of a chunk, fp16
+    int nseg, seglen;      // segments of a request at most, chunks of a segment
+    float *segs, *maps;    // [R][H][nseg][N][P] segments' starting states and transition maps
 };
 
 // ---------------------------------------------------------------- fp16 operands
@@ -133,7 +135,73 @@ __device__ __forceinline__ int block_slot(const PrefillParams &p, int r, int end
     return -1;
 }
 
+// ---------------------------------------------------------------- segments
+// A request's chunks form one chain per head.  Where requests and heads alone
+// leave most of the GPU idle, the chain is cut into segments.  A segment's final
+// state is linear in its starting state, S_out = M S_in + B (M acts on the key
+// index), so the segments run twice:
+//   first without outputs, from zero (giving B) and, with V = 0, from the
+//   identity (giving M), all at once; the first one runs from the request's
+//   starting state instead;
+//   then S_(s+1) = M_s S_s + B_s in order (combine_kernel), a small product a step;
+//   and again, with outputs, from those states.
+// That is a little over twice the work on a chain shorter by the number of
+// segments.
+struct Unit {          // what one CTA of a scan runs
+    int r, h, seg;
+    bool map;          // from the identity, without V
+    int c0, c1, nsegs;  // its chunks, and the request's segments
+    bool ok;
+};
+
+// The unit of a CTA (CTAs count heads first); OUT: the pass with outputs.
+template <bool OUT>
+__device__ __forceinline__ Unit scan_unit(const PrefillParams &p, int cta, const Request &rq, int r, int q) {
+    Unit u;
+    u.r = r;
+    u.h = cta % p.H;
+    u.seg = OUT ? q : q >> 1;
+    u.map = !OUT && (q & 1);
+    u.nsegs = p.nseg > 1 ? (rq.nch + p.seglen - 1) / p.seglen : 1;
+    u.c0 = u.seg * p.seglen;
+    u.c1 = min(u.c0 + p.seglen, rq.nch);
+    // the last segment's final state is the second pass's; the first needs no map
+    u.ok = OUT ? u.seg < u.nsegs : u.seg < u.nsegs - 1 && !(u.map && u.seg == 0);
+    return u;
+}
+template <bool OUT>
+inline int scan_units(const PrefillParams &p) { return OUT ? p.nseg : 2 * (p.nseg - 1); }
+
+__device__ __forceinline__ size_t seg_slab(const PrefillParams &p, const Unit &u, int seg, int n) {
+    return (((size_t)u.r * p.H + u.h) * p.nseg + seg) * n;
+}
+
+// Where a unit's state starts: kind 0 zeros, 1 the identity, 2 fp32, 3 bf16.
+struct StateSource {
+    int kind;
+    const float *f;
+    const uint16_t *b;
+};
+template <bool OUT, int D>
+__device__ __forceinline__ StateSource unit_start(const PrefillParams &p, const Request &rq, const Unit &u) {
+    StateSource s = {0, nullptr, nullptr};
+    if (u.map) {
+        s.kind = 1;
+    } else if (OUT ? u.nsegs > 1 : u.seg > 0) {
+        if (OUT) s.kind = 2, s.f = p.segs + seg_slab(p, u, u.seg, D * D);
+    } else if (rq.start != -1) {
+        const bool cont = rq.start == -2;
+        const size_t slab = ((size_t)(cont ? rq.srow : rq.start) * p.H + u.h) * D * D;
+        if (p.prec == RS_PREC_SHARED_BF16)
+            s.kind = 3, s.b = (cont ? p.lp : static_cast<const uint16_t *>(p.pool)) + slab;
+        else
+            s.kind = 2, s.f = (cont ? p.hp : static_cast<const float *>(p.pool)) + slab;
+    }
+    return s;
+}
+
 // The scan of 128-wide heads on the fifth-generation tensor cores (rs_prefill_tc.cu).
+template <bool OUT>
 cudaError_t scan_tc_launch(const PrefillParams &p, cudaStream_t s);
 
 }  // namespace prefill

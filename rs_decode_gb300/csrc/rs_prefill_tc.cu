@@ -291,7 +291,9 @@ __device__ __forceinline__ float pair_max(float *m, int hf, int row, int warp, f
 
 // A head of a request.  Every wait gives up after its time limit; the threads
 // learn of it together at the next barrier and leave.
-__device__ __forceinline__ void scan_head(const PrefillParams &p, const Request &rq, int h, int r, unsigned char *smem,
+// OUT: with y (otherwise the state alone).
+template <bool OUT>
+__device__ __forceinline__ void scan_head(const PrefillParams &p, const Request &rq, const Unit &u, unsigned char *smem,
                                           Bars *b) {
     constexpr int DH = D / 2, CH = C / 2;
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), hf = warp >> 2;
@@ -304,13 +306,13 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
     Work w;
     w.n = rq.n;
     w.head_rows = min(rq.n, C - rq.ctx % C);
-    const int nch = rq.nch;
+    const int nch = u.c1 - u.c0, h = u.h, r = u.r;
     const int vt = threadIdx.x >> 4, vc = threadIdx.x & 15;  // V: row vt + 16 j, 16-byte piece vc
     const uint16_t *vsrc = p.v + ((long long)rq.row0 + vt) * p.ld_v + h * D + vc * 8;
     auto load_v = [&](int i) {
         if (i < nch) {
-            const int n = w.rows(i);
-            const uint16_t *src = vsrc + (long long)w.first(i) * p.ld_v;
+            const int n = u.map ? 0 : w.rows(u.c0 + i);
+            const uint16_t *src = vsrc + (long long)w.first(u.c0 + i) * p.ld_v;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool in = vt + 16 * j < n;
@@ -322,27 +324,28 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
     };
     if (warp == 1) {
         load_k(b, sm, 0, p.H);
-        load_qp(b, sm, 0, p.H);
-        if (rq.nch > 1) load_k(b, sm, 1, p.H);
+        if (OUT) load_qp(b, sm, 0, p.H);
+        if (nch > 1) load_k(b, sm, 1, p.H);
     }
     if (warp == 3) load_t(b, sm, 0, p.H);
     load_v(0);
 
     f2 S[DH / 2];
     {
-        const bool cont = rq.start == -2;
-        const size_t slab = ((size_t)(cont ? rq.srow : max(rq.start, 0)) * p.H + h) * D * D + hf * DH * D + row;
-        if (rq.start == -1) {
+        const StateSource from = unit_start<OUT, D>(p, rq, u);
+        const int o = hf * DH * D + row;
+        if (from.kind == 2) {
 #pragma unroll
-            for (int n = 0; n < DH / 2; ++n) S[n] = 0;
-        } else if (p.prec == RS_PREC_SHARED_BF16) {
-            const uint16_t *src = (cont ? p.lp : static_cast<const uint16_t *>(p.pool)) + slab;
+            for (int n = 0; n < DH / 2; ++n) S[n] = f2_pack(from.f[o + 2 * n * D], from.f[o + (2 * n + 1) * D]);
+        } else if (from.kind == 3) {
 #pragma unroll
-            for (int n = 0; n < DH / 2; ++n) S[n] = f2_pack(bf2f(src[2 * n * D]), bf2f(src[(2 * n + 1) * D]));
+            for (int n = 0; n < DH / 2; ++n) S[n] = f2_pack(bf2f(from.b[o + 2 * n * D]), bf2f(from.b[o + (2 * n + 1) * D]));
         } else {
-            const float *src = (cont ? p.hp : static_cast<const float *>(p.pool)) + slab;
 #pragma unroll
-            for (int n = 0; n < DH / 2; ++n) S[n] = f2_pack(src[2 * n * D], src[(2 * n + 1) * D]);
+            for (int n = 0; n < DH / 2; ++n) {
+                const int k = hf * DH + 2 * n;
+                S[n] = f2_pack(from.kind == 1 && k == row ? 1.f : 0.f, from.kind == 1 && k + 1 == row ? 1.f : 0.f);
+            }
         }
     }
     auto store_state = [&](float *f, uint16_t *q, size_t slab) {
@@ -365,13 +368,15 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         }
     };
 
+    if (!OUT && u.seg == 0) store_state(p.segs, nullptr, seg_slab(p, u, 0, D * D));  // for the second pass
+
     const long long ystep = (long long)p.H * D;
     uint16_t *y = p.y + ((long long)rq.row0 * p.H + h) * D + (row & ~1) + (hf * CH + 16 * (row & 1)) * ystep;
     float *rowmax = reinterpret_cast<float *>(smem + Smem::MAX);
     bool ok = true;
     for (int i = 0; i < nch; ++i) {
         const unsigned ph = i & 1, kph = (i >> 1) & 1;
-        const int n = w.rows(i);
+        const int n = w.rows(u.c0 + i);
         const uint32_t sk = desc_lo(sm + Smem::K + (i & 1) * kTile);
         const Vecs &vec = *reinterpret_cast<const Vecs *>(smem + Smem::VEC + (i & 1) * kRecVecs);
         // the state as an operand, its row scaled to fp16's range: the row's
@@ -415,7 +420,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
             vmax = fmaxf(__low2float(m2), __high2float(m2));
         }
         vmax = pair_max(rowmax + 2 * D, hf, row, warp, vmax);
-        if (warp == 4) {  // Z, behind X
+        if (OUT && warp == 4) {  // Z, behind X
             ok = wait_warp(&b->full_q, ph, b, p.status) && ok;
             tc_fence_after_sync();
             if (elect_one()) issue_z(base, desc_lo(sm + Smem::Q), b);
@@ -471,8 +476,10 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
                 const ulonglong2 su = *reinterpret_cast<const ulonglong2 *>(vec.su + hf * CH + t + e);
                 x[e / 2] = f2_mul(x[e / 2], su.x), x[e / 2 + 1] = f2_mul(x[e / 2 + 1], su.y);
             }
+            if (OUT) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[t / 2 + e] = pack_pair(f2_mul(x[e], uup2));
+                for (int e = 0; e < 8; ++e) z[t / 2 + e] = pack_pair(f2_mul(x[e], uup2));
+            }
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
                 const ulonglong2 ke = *reinterpret_cast<const ulonglong2 *>(vec.ke + hf * CH + t + e);
@@ -482,6 +489,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         }
         // the queries' place takes u once Z is complete; Z leaves TMEM in fp16
         // (2^-9 keeps its sums, below 2^24, in range)
+        if (OUT) {
         ok = wait_warp(&b->mz, ph, b, p.status) && ok;
         tc_fence_after_sync();
 #pragma unroll
@@ -495,17 +503,20 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[t / 2 + e] = pack_pair(f2_mul(x[e], f2_pack(0.001953125f, 0.001953125f)));
         }
-        st_done();
         fence_proxy_async_smem();
+        }
+        st_done();
         tc_fence_before_sync();
         if (__syncthreads_or(!ok)) { ok = false; break; }
         if (warp == 0) {
             tc_fence_after_sync();
             if (elect_one()) issue_d(base, sk, b);
             __syncwarp();
-            ok = wait_warp(&b->full_p, ph, b, p.status) && ok;
-            if (elect_one()) issue_y(base, desc_lo(sm + Smem::Q), desc_lo(sm + Smem::P), b);
-            __syncwarp();
+            if (OUT) {
+                ok = wait_warp(&b->full_p, ph, b, p.status) && ok;
+                if (elect_one()) issue_y(base, desc_lo(sm + Smem::Q), desc_lo(sm + Smem::P), b);
+                __syncwarp();
+            }
         }
         // S <- e^(G_C) S + D
         ok = wait_warp(&b->md, ph, b, p.status) && ok;
@@ -520,6 +531,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
                 for (int e = 0; e < 8; ++e) S[k / 2 + e] = f2_fma(all, S[k / 2 + e], f2_mul(x[e], kd2));
             }
         }
+        if (!OUT) continue;
         // y = (e^G Z + Y) with the query's power of two
         ok = wait_warp(&b->my, ph, b, p.status) && ok;
         tc_fence_after_sync();
@@ -544,7 +556,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         {
             const bool odd = row & 1;
             const uint32_t sel0 = odd ? 0x1054 : 0x5410, sel1 = odd ? 0x3276 : 0x7632;
-            uint16_t *yc = y + w.first(i) * ystep;
+            uint16_t *yc = y + w.first(u.c0 + i) * ystep;
             const int m = n - hf * CH - 16 * odd;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -571,7 +583,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
                 }
             }
         }
-        const int slot = block_slot(p, r, rq.ctx + w.first(i) + n, h == 0 && threadIdx.x == 0);
+        const int slot = block_slot(p, r, rq.ctx + w.first(u.c0 + i) + n, h == 0 && threadIdx.x == 0);
         if (slot >= 0) {
             const size_t slab = ((size_t)slot * p.H + h) * D * D;
             if (p.prec == RS_PREC_SHARED_BF16)
@@ -589,16 +601,27 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         }
         return;
     }
+    if (!OUT) {
+        if (u.map)
+            store_state(p.maps, nullptr, seg_slab(p, u, u.seg, D * D));
+        else
+            store_state(p.segs, nullptr, seg_slab(p, u, u.seg + 1, D * D));
+        return;
+    }
+    if (u.seg < u.nsegs - 1) return;
     store_state(p.hp, p.lp, ((size_t)rq.srow * p.H + h) * D * D);
     if (rq.start != -2 && h == 0 && threadIdx.x == 0) p.base[rq.srow] = p.h[rq.srow] = p.nd[rq.srow] = 0;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) scan_tc_kernel(const __grid_constant__ PrefillParams p) {
+template <bool OUT>
+__global__ void __launch_bounds__(kThreads, 2) scan_tc_kernel(const __grid_constant__ PrefillParams p, int units) {
     extern __shared__ unsigned char raw[];
-    const int h = blockIdx.x % p.H, r = blockIdx.x / p.H;
+    const int h = blockIdx.x % p.H, q = blockIdx.x / p.H % units, r = blockIdx.x / p.H / units;
     if (p.rg.cu_tokens[r + 1] - p.rg.cu_tokens[r] <= kShort) return;
-    const Request rq = load_request(p, r, h == 0 && threadIdx.x == 0);
+    const Request rq = load_request(p, r, h == 0 && q == 0 && threadIdx.x == 0);
     if (!rq.ok) return;
+    const Unit u = scan_unit<OUT>(p, blockIdx.x, rq, r, q);
+    if (!u.ok) return;
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     Bars *b = reinterpret_cast<Bars *>(smem + Smem::BAR);
     if (threadIdx.x < 32) {
@@ -610,9 +633,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_tc_kernel(const __grid_const
             mbar_init(&b->mend, 2);
             b->abort = 0;
             b->nk = b->nq = b->nt = 0;
-            b->tiles = p.tiles + ((size_t)rq.chunk0 * p.G + h / p.rep) * (2 * kTile);
+            b->tiles = p.tiles + ((size_t)(rq.chunk0 + u.c0) * p.G + h / p.rep) * (2 * kTile);
             b->tile_step = (unsigned long long)p.G * (2 * kTile);
-            b->rec = p.rec + (size_t)rq.chunk0 * p.H + h;
+            b->rec = p.rec + (size_t)(rq.chunk0 + u.c0) * p.H + h;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         __syncwarp();
@@ -620,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_tc_kernel(const __grid_const
     }
     __syncthreads();
     tc_fence_after_sync();
-    scan_head(p, rq, h, r, smem, b);
+    scan_head<OUT>(p, rq, u, smem, b);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -631,13 +654,17 @@ __global__ void __launch_bounds__(kThreads, 2) scan_tc_kernel(const __grid_const
 
 namespace prefill {
 
+template <bool OUT>
 cudaError_t scan_tc_launch(const PrefillParams &p, cudaStream_t s) {
     static SmemGrants grants;
-    const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&scan_tc_kernel), Smem::BYTES, grants);
+    const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&scan_tc_kernel<OUT>), Smem::BYTES, grants);
     if (e != cudaSuccess) return e;
-    scan_tc_kernel<<<p.R * p.H, kThreads, Smem::BYTES, s>>>(p);
+    const int units = scan_units<OUT>(p);
+    scan_tc_kernel<OUT><<<p.R * p.H * units, kThreads, Smem::BYTES, s>>>(p, units);
     return cudaGetLastError();
 }
+template cudaError_t scan_tc_launch<true>(const PrefillParams &p, cudaStream_t s);
+template cudaError_t scan_tc_launch<false>(const PrefillParams &p, cudaStream_t s);
 
 }  // namespace prefill
 

@@ -271,6 +271,8 @@ class Case:
             self.alpha.fill_(1)
         elif alpha == "zeros":  # resets in the middle, and several in a row
             self.alpha[torch.rand(cap, H, generator=g, device="cuda") < 0.2] = 0
+        elif alpha == "slow":  # states that remember thousands of rows
+            self.alpha.pow_(0.01)
         elif alpha == "tiny":
             self.alpha.fill_(1e-30)
         if beta == "one":
@@ -388,6 +390,18 @@ def test_gdn_blocks_of_other_precisions(prec):
     c = Case(lengths, 4, 4, 128, prec, context=[128, 250, 0], block=128, seed=3)
     c.run([0, 1, -1])
     c.check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths,start,prec,block", [
+    ([2600], [-1], "fp32", 0), ([2600], [-2], "fp32", 256), ([3000, 1, 700, 2100], [-2, -1, 0, 1], "two", 512),
+    ([2113, 64], [0, -2], "shared_bf16", 64)])
+def test_gdn_long_requests(d, lengths, start, prec, block):
+    """Few chains of many chunks: these run in segments."""
+    c = Case(lengths, 2, 1, d, prec, context=[37] + [0] * (len(lengths) - 1), block=block, seed=len(lengths) + d, alpha="slow")
+    c.run(start)
+    c.check()
+    assert c.layer.status() == 0
 
 
 @pytest.mark.parametrize("alpha,beta,keys", [
