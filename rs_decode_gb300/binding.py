@@ -143,6 +143,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     return _lib
 
 
+# The current stream's handle without a Stream object around it: a decode step's
+# calls are short enough for that to count.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+if _current_stream is None or _current_device is None:
+    _current_device = torch.cuda.current_device
+
+    def _current_stream(device: int) -> int:
+        return torch.cuda.current_stream(device).cuda_stream
+
+
 def _ptr(t) -> int | None:
     if t is None:
         return None
@@ -155,7 +166,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -299,14 +310,16 @@ def rs_ragged_bytes_for(rd: RaggedDesc) -> RaggedBytes:
 
 
 def rs_ragged_plan(rd, lengths, context, free_blocks, arrays, status, stream=None):
-    _check("rs_ragged_plan", load().rs_ragged_plan(ctypes.byref(rd), _ptr(lengths), _ptr(context), _ptr(free_blocks),
-                                                   ctypes.byref(arrays), _ptr(status), _stream(stream)))
+    st = load().rs_ragged_plan(rd, _ptr(lengths), _ptr(context), _ptr(free_blocks), arrays, _ptr(status), _stream(stream))
+    if st:
+        _check("rs_ragged_plan", st)
 
 
 def rs_qk_norm(desc, q, k, wq, wk, inv_freq, positions, q_out, k_out, stream=None):
     """q, k, q_out, k_out are data pointers (their row strides are in desc)."""
-    _check("rs_qk_norm", load().rs_qk_norm(ctypes.byref(desc), q, k, _ptr(wq), _ptr(wk), _ptr(inv_freq),
-                                           _ptr(positions), q_out, k_out, _stream(stream)))
+    st = load().rs_qk_norm(desc, q, k, _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(positions), q_out, k_out, _stream(stream))
+    if st:
+        _check("rs_qk_norm", st)
 
 
 def rs_prefill_bytes_for(desc, rd, max_len: int) -> int:
@@ -317,6 +330,6 @@ def rs_prefill_bytes_for(desc, rd, max_len: int) -> int:
 
 
 def rs_prefill_gdn(desc, state, rd, arrays, prefill, y, work, stream=None):
-    _check("rs_prefill_gdn", load().rs_prefill_gdn(
-        ctypes.byref(desc), ctypes.byref(state), ctypes.byref(rd), ctypes.byref(arrays), ctypes.byref(prefill),
-        _ptr(y), _ptr(work), _stream(stream)))
+    st = load().rs_prefill_gdn(desc, state, rd, arrays, prefill, _ptr(y), _ptr(work), _stream(stream))
+    if st:
+        _check("rs_prefill_gdn", st)

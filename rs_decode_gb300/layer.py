@@ -26,11 +26,12 @@ def to_device(d: dict, device="cuda", non_blocking: bool = False) -> dict:
 
 def packed_stride(t: torch.Tensor, rows: int, heads: int, d: int, name: str) -> int:
     """Row stride in elements of a packed [rows, heads, d] bf16 tensor whose heads lie side by side."""
-    if t.element_size() != 2 or t.dim() != 3 or t.shape[0] < rows or tuple(t.shape[1:]) != (heads, d):
+    if t.dim() != 3 or t.size(0) < rows or t.size(1) != heads or t.size(2) != d or t.element_size() != 2:
         raise ValueError(f"{name} must be bf16 [{rows}, {heads}, {d}], got {t.dtype} {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    ld, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    return ld if t.size(0) > 1 else heads * d
 
 
 class Layer:
@@ -44,6 +45,7 @@ class Layer:
         sz = rb.rs_state_bytes_for(self.desc)
         self.B, self.H, self.G, self.P, self.N, self.L, self.T_max = B, H, G, P, N, L, T_max
         self.cap = self.desc.capacity
+        self._prefill_sizes: dict = {}  # workspace bytes by plan shape
         dev = torch.device(device)
         z = lambda n, dt: torch.zeros(n, dtype=dt, device=dev) if n else None
         self.ckpt_hp = z(sz.ckpt_hp // 4, torch.float32)
@@ -110,9 +112,16 @@ class Layer:
         return out
 
     # ---------------------------------------------------------------- prefill
+    def _prefill_bytes(self, rd, max_len: int) -> int:
+        key = (rd.R, rd.tokens_cap, rd.block, rd.max_blocks, rd.n_free, max_len)
+        n = self._prefill_sizes.get(key)
+        if n is None:
+            n = self._prefill_sizes[key] = rb.rs_prefill_bytes_for(self.desc, rd, max_len)
+        return n
+
     def prefill_workspace(self, ragged, max_len: int) -> torch.Tensor | None:
         """Scratch of ``prefill`` for this plan shape; may serve many calls, one after another."""
-        n = rb.rs_prefill_bytes_for(self.desc, ragged.desc, max_len)
+        n = self._prefill_bytes(ragged.desc, max_len)
         return torch.empty(n, dtype=torch.uint8, device=self.base.device) if n else None
 
     def prefill(self, ragged, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Tensor,
@@ -127,32 +136,33 @@ class Layer:
         [n, H, N, P], fp32 or, for a shared-bf16 layer, bf16.  Returns y
         torch.bfloat16 [rows, H, P].  Without y and work they are allocated
         on the current stream, which then has to be the one the call runs on."""
-        T, H, G, N, P = ragged.desc.tokens_cap, self.H, self.G, self.desc.N, self.desc.P
-        lds = [packed_stride(t, T, heads, d, name)
-               for t, heads, d, name in ((q, G, N, "q"), (k, G, N, "k"), (v, H, P, "v"))]
+        rd = ragged.desc
+        T, R, H, G, N, P = rd.tokens_cap, rd.R, self.H, self.G, self.N, self.P
+        ld_q, ld_k, ld_v = packed_stride(q, T, G, N, "q"), packed_stride(k, T, G, N, "k"), packed_stride(v, T, H, P, "v")
         for t, name in ((alpha, "alpha"), (beta, "beta")):
-            if t.dtype != torch.float32 or t.shape[0] < T or tuple(t.shape[1:]) != (H,):
+            if t.dtype is not torch.float32 or t.dim() != 2 or t.size(0) < T or t.size(1) != H:
                 raise ValueError(f"{name} must be float32 [{T}, {H}], got {t.dtype} {tuple(t.shape)}")
-        R = ragged.desc.R
         for t, name in ((rows, "rows"), (start, "start")):
-            if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (R,)):
+            if t is not None and (t.dtype is not torch.int32 or t.shape != (R,)):
                 raise ValueError(f"{name} must be int32 [{R}]")
+        n_pool = 0
         if pool is not None:
             width = 2 if self.desc.precision & 0xf == rb.PREC_SHARED_BF16 else 4
-            if tuple(pool.shape[1:]) != (H, N, P) or pool.element_size() != width:
+            n_pool = pool.size(0)
+            if pool.shape != (n_pool, H, N, P) or pool.element_size() != width:
                 raise ValueError(f"pool must be [n, {H}, {N}, {P}] of {width}-byte values")
         if y is None:
-            y = torch.empty(T, H, P, dtype=torch.bfloat16, device=self.base.device)
-        elif y.element_size() != 2 or y.shape[0] < T or tuple(y.shape[1:]) != (H, P):
+            y = torch.empty((T, H, P), dtype=torch.bfloat16, device=self.base.device)
+        elif y.element_size() != 2 or y.dim() != 3 or y.size(0) < T or y.size(1) != H or y.size(2) != P:
             raise ValueError(f"y must be bf16 [{T}, {H}, {P}]")
         if work is None:
             work = self.prefill_workspace(ragged, max_len)
-        elif work.numel() * work.element_size() < rb.rs_prefill_bytes_for(self.desc, ragged.desc, max_len):
+        elif work.nbytes < self._prefill_bytes(rd, max_len):
             raise ValueError("work is smaller than prefill_workspace() of this plan")
         p = rb._ptr
-        args = rb.Prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), p(alpha), p(beta), *lds, p(rows), p(start),
-                          p(pool), 0 if pool is None else pool.shape[0], max_len)
-        rb.rs_prefill_gdn(self.desc, self.state, ragged.desc, ragged.arrays, args, y, work, stream)
+        args = rb.Prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), p(alpha), p(beta), ld_q, ld_k, ld_v, p(rows), p(start),
+                          p(pool), n_pool, max_len)
+        rb.rs_prefill_gdn(self.desc, self.state, rd, ragged.arrays, args, y, work, stream)
         return y
 
     def status(self, clear: bool = True, stream=None) -> int:

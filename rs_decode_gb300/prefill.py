@@ -38,10 +38,10 @@ class Ragged:
              free_blocks: torch.Tensor | None = None, stream=None) -> None:
         """lengths, context: int32 [R]; free_blocks: int32, at least n_free slots."""
         d = self.desc
-        for t, name, n in ((lengths, "lengths", d.R), (context, "context", d.R)):
-            if t is not None and (t.dtype != torch.int32 or t.numel() != n):
-                raise ValueError(f"{name} must be int32 [{n}]")
-        if d.block and d.n_free and (free_blocks is None or free_blocks.dtype != torch.int32
+        for t, name in ((lengths, "lengths"), (context, "context")):
+            if t is not None and (t.dtype is not torch.int32 or t.numel() != d.R):
+                raise ValueError(f"{name} must be int32 [{d.R}]")
+        if d.block and d.n_free and (free_blocks is None or free_blocks.dtype is not torch.int32
                                      or free_blocks.numel() < d.n_free):
             raise ValueError(f"free_blocks must be int32 [{d.n_free}]")
         rb.rs_ragged_plan(d, lengths, context, free_blocks, self.arrays, self.status_word, stream)
@@ -63,37 +63,46 @@ def qk_norm(q: torch.Tensor | None, k: torch.Tensor | None, *, norm: str = "l2",
     stride; either may be None) and rotates its first 2 * len(inv_freq)
     channels by positions (int32 [T]) * inv_freq (float32).  Returns the two
     results, torch.bfloat16, in ``out`` if given (in place: out=(q, k))."""
-    if norm not in NORMS:
+    kind = NORMS.get(norm)
+    if kind is None:
         raise ValueError(f"unknown norm {norm!r}")
     one = q if q is not None else k
     if one is None or one.dim() != 3:
         raise ValueError("q or k must be a [T, heads, D] tensor")
-    T, D = one.shape[0], one.shape[2]
-    d = rb.QkDesc()
-    d.T, d.D, d.norm, d.interleaved = T, D, NORMS[norm], int(interleaved)
-    d.eps, d.weight_offset, d.scale_q, d.scale_k = eps, weight_offset, scale_q, scale_k
-    if (positions is None) != (inv_freq is None):
-        raise ValueError("positions and inv_freq go together")
+    T, D = one.size(0), one.size(2)
+    rot = 0
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float32 or positions.dtype != torch.int32 or positions.numel() != T:
+        if positions is None:
+            raise ValueError("positions and inv_freq go together")
+        rot = 2 * inv_freq.numel()
+        if inv_freq.dtype is not torch.float32 or positions.dtype is not torch.int32 or positions.numel() != T:
             raise ValueError(f"inv_freq must be float32 and positions int32 [{T}]")
-        d.rot = 2 * inv_freq.numel()
+    elif positions is not None:
+        raise ValueError("positions and inv_freq go together")
     for w in (wq, wk):
         if w is not None and (w.element_size() != 2 or w.numel() != D):
             raise ValueError(f"weights must be bf16 [{D}]")
     qo, ko = out if out is not None else (None, None)
-    ptrs = [None] * 4
+    Hq = Hk = ld_q = ld_k = ld_qo = ld_ko = 0
+    pq = pk = pqo = pko = None
     if q is not None:
-        d.Hq, d.ld_q = q.shape[1], packed_stride(q, T, q.shape[1], D, "q")
+        Hq = q.size(1)
+        ld_q = packed_stride(q, T, Hq, D, "q")
         if qo is None:
-            qo = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        d.ld_qo = packed_stride(qo, T, d.Hq, D, "out[0]")
-        ptrs[0], ptrs[2] = q.data_ptr(), qo.data_ptr()
+            qo = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            ld_qo = Hq * D
+        else:
+            ld_qo = packed_stride(qo, T, Hq, D, "out[0]")
+        pq, pqo = q.data_ptr(), qo.data_ptr()
     if k is not None:
-        d.Hk, d.ld_k = k.shape[1], packed_stride(k, T, k.shape[1], D, "k")
+        Hk = k.size(1)
+        ld_k = packed_stride(k, T, Hk, D, "k")
         if ko is None:
-            ko = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
-        d.ld_ko = packed_stride(ko, T, d.Hk, D, "out[1]")
-        ptrs[1], ptrs[3] = k.data_ptr(), ko.data_ptr()
-    rb.rs_qk_norm(d, ptrs[0], ptrs[1], wq, wk, inv_freq, positions, ptrs[2], ptrs[3], stream)
+            ko = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=k.device)
+            ld_ko = Hk * D
+        else:
+            ld_ko = packed_stride(ko, T, Hk, D, "out[1]")
+        pk, pko = k.data_ptr(), ko.data_ptr()
+    d = rb.QkDesc(T, Hq, Hk, D, kind, rot, interleaved, eps, weight_offset, scale_q, scale_k, ld_q, ld_k, ld_qo, ld_ko)
+    rb.rs_qk_norm(d, pq, pk, wq, wk, inv_freq, positions, pqo, pko, stream)
     return qo, ko
