@@ -3,17 +3,21 @@
 //
 // Each head is read once and written once (4 bytes a channel), so the kernel
 // is bound by HBM; the arithmetic only has to stay out of the way.  A head is
-// D / 8 lanes of 16 bytes each, its sum of squares a shuffle over those lanes,
-// and a thread has kRows heads in flight to cover the memory latency.  The
-// rotation's cosines and sines depend on the token and the pair alone: a CTA
-// computes them once for its tokens into shared memory and all their heads
-// read them.
+// D / 8 lanes of 16 bytes each, its sum of squares a shuffle over those lanes.
+// A warp takes a token's heads, or every hs-th group of them where tokens alone
+// are too few warps, four heads in flight per lane.  The cosines and sines of
+// a lane's pairs depend on the token alone: computed once, all its heads use
+// them, from registers.  Where channel i turns with i + rot/2, a lane of the
+// rotated part holds four channels of either half (8 bytes each), so that its
+// pairs are its own and no lane needs another's channels.
 //
 // The angle positions * inv_freq is reduced exactly: inv_freq / (2 pi) is held
 // as a 64-bit fraction of a turn, so the product with an integer position
 // modulo 2^64 is the fraction of a turn without any rounding of the product.
-// Its error is the position times 2^-54, where an fp32 product would be off by
-// 2^-25 of the angle (0.004 radians at position 100,000).
+// Its error is the position times 2^-64, where an fp32 product would be off by
+// 2^-25 of the angle (0.004 radians at position 100,000).  The reduced angle,
+// within half a turn, is what the fast sine and cosine are accurate for (2^-20
+// absolute, against the 2^-9 of a bf16 result).
 #include "rs_common.cuh"
 #include "rs_internal.h"
 
@@ -21,12 +25,12 @@ namespace rs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;       // heads that a thread has in flight
-constexpr int kMaxTokens = 16;  // tokens of one CTA
+
+enum Rot { ROT_NONE = 0, ROT_HALVES = 1, ROT_PAIRS = 2 };
 
 struct QkParams {
-    int T, Hq, Hk, norm, rot, interleaved, tokens;
-    float eps, w0, scale_q, scale_k;
+    int T, Hq, Hk, norm, rot, hs;
+    float eps, inv_eps, w0, scale_q, scale_k;
     long long ld_q, ld_k, ld_qo, ld_ko;
     const uint16_t *q, *k, *wq, *wk;
     const float *inv_freq;
@@ -34,110 +38,134 @@ struct QkParams {
     uint16_t *q_out, *k_out;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) qk_kernel(const __grid_constant__ QkParams p) {
-    constexpr int LPH = D / 8;             // lanes of a head
-    constexpr int SLOTS = kThreads / LPH;  // heads that the CTA takes at once
-    extern __shared__ float2 turn[];       // [tokens][rot / 2] cosine and sine
+// Turns per position as a 64-bit fraction: |f| / (2 pi) 2^64, from f's 24-bit
+// significand m and exponent: f = m 2^(e - 150), 1 / (2 pi) = c 2^-66.
+__device__ __forceinline__ unsigned long long turns(float f) {
+    const unsigned long long c = 0xA2F9836E4E44152Aull;  // 2^66 / (2 pi)
+    const uint32_t bits = __float_as_uint(f);
+    const int e = (bits >> 23) & 255, s = 152 - e;
+    const unsigned long long m = e ? (bits & 0x7fffffu) | 0x800000u : 0;
+    const unsigned long long lo = m * c, hi = __umul64hi(m, c);
+    const unsigned long long v = s >= 88 ? 0 : s >= 64 ? hi >> (s - 64) : s > 0 ? hi << (64 - s) | lo >> s : 0;
+    return bits >> 31 ? 0 - v : v;
+}
+
+template <int D, int ROT>
+__global__ void __launch_bounds__(kThreads, ROT == ROT_NONE ? 5 : 4) qk_kernel(const __grid_constant__ QkParams p) {
+    constexpr int kRows = 4;  // heads that a lane has in flight
+    constexpr int LPH = D / 8;       // lanes of a head
+    constexpr int SLOTS = 32 / LPH;  // heads that a warp takes at once
+    const int lane = threadIdx.x & 31, sub = lane % LPH;
     const int heads = p.Hq + p.Hk;
-    const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
-    const int half = p.rot >> 1;
-    if (half) {
-        for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-            const int t = i / half, j = i - t * half;
-            // turns per position as a 64-bit fraction; |inv_freq| < 2 pi keeps it below one turn
-            const double f = (double)p.inv_freq[j] * 0.15915494309189533577;
-            const long long frac = __double2ll_rn(f * 9223372036854775808.0);  // in 2^-63 turns
-            const unsigned long long ph = (unsigned long long)frac * 2ull *
-                                          (unsigned long long)(long long)p.positions[t0 + t];
-            float s, c;
-            sincospif((float)(int)(ph >> 32) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31: half turns
-            turn[i] = make_float2(c, s);
-        }
-        __syncthreads();
+    const bool turning = ROT != ROT_NONE && sub < p.rot / 8;
+    // the lane's channels: ch..ch+3 and ch+up..ch+up+3
+    const int ch = ROT == ROT_HALVES && turning ? sub * 4 : sub * 8, up = ROT == ROT_HALVES && turning ? p.rot / 2 : 4;
+    unsigned long long freq[4];
+    if (ROT != ROT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) freq[i] = turning ? turns(p.inv_freq[sub * 4 + i]) : 0;
     }
-    const int lane = threadIdx.x % LPH, slot = threadIdx.x / LPH;
-    const int ch = lane * 8;
-    const int total = nt * heads;
-    for (int r0 = slot; r0 < total + slot; r0 += SLOTS * kRows) {
-        uint4 raw[kRows];
-        int tok[kRows], head[kRows];
+    auto load8 = [&](const uint16_t *src) {
+        if (ROT != ROT_HALVES) return ld_stream(src);
+        const uint2 a = __ldcs(reinterpret_cast<const uint2 *>(src)), b = __ldcs(reinterpret_cast<const uint2 *>(src + up));
+        return make_uint4(a.x, a.y, b.x, b.y);
+    };
+    const int step = SLOTS * p.hs;
+    const long long units = (long long)p.T * p.hs, warps = (long long)gridDim.x * (kThreads / 32);
+    for (long long u = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+        const int t = p.hs == 1 ? (int)u : (int)(u / p.hs), part = p.hs == 1 ? 0 : (int)(u - (long long)t * p.hs);
+        const uint16_t *qs = p.q + t * p.ld_q + ch, *ks = p.k + t * p.ld_k + ch;
+        uint16_t *qd = p.q_out + t * p.ld_qo + ch, *kd = p.k_out + t * p.ld_ko + ch;
+        float cs[4], sn[4];
+        bool have = false;
+        for (int h0 = part * SLOTS + lane / LPH; h0 - lane / LPH < heads; h0 += step * kRows) {
+            uint4 raw[kRows];
 #pragma unroll
-        for (int e = 0; e < kRows; ++e) {
-            const int r = r0 + e * SLOTS;
-            tok[e] = r / heads;
-            head[e] = r - tok[e] * heads;
-            raw[e] = make_uint4(0, 0, 0, 0);
-            if (r < total) {
-                const long long t = t0 + tok[e];
-                const uint16_t *src = head[e] < p.Hq ? p.q + t * p.ld_q + (long long)head[e] * D
-                                                     : p.k + t * p.ld_k + (long long)(head[e] - p.Hq) * D;
-                raw[e] = ld_stream(src + ch);
+            for (int e = 0; e < kRows; ++e) {
+                const int h = h0 + e * step;
+                raw[e] = make_uint4(0, 0, 0, 0);
+                if (h < heads) raw[e] = load8(h < p.Hq ? qs + (long long)h * D : ks + (long long)(h - p.Hq) * D);
             }
-        }
+            if (ROT != ROT_NONE && !have) {  // behind the first loads
+                have = true;
+                const uint32_t pos = (uint32_t)p.positions[t];
 #pragma unroll
-        for (int e = 0; e < kRows; ++e) {
-            const int r = r0 + e * SLOTS;
-            const bool is_q = head[e] < p.Hq;
-            float x[8];
-            unpack<uint16_t, 8>(raw[e], x);
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-            for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-            float m = is_q ? p.scale_q : p.scale_k;
-            if (p.norm == RS_NORM_L2) {
-                const float n = sqrtf(ss);
-                m /= n < p.eps ? p.eps : n;  // a NaN norm stays one
-            } else if (p.norm == RS_NORM_RMS) {
-                m /= sqrtf(ss * (1.f / D) + p.eps);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t flo = (uint32_t)freq[i], fhi = (uint32_t)(freq[i] >> 32);
+                    const uint32_t ph = __umulhi(flo, pos) + fhi * pos - ((int)pos < 0 ? flo : 0);
+                    const float a = (float)(int)ph * 1.46291807926715968e-9f;  // 2 pi 2^-32
+                    cs[i] = __cosf(a), sn[i] = __sinf(a);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= m;
-            const uint16_t *w = is_q ? p.wq : p.wk;
-            if (w) {
-                float wf[8];
-                unpack<uint16_t, 8>(ld_u4(w + ch), wf);
+            for (int e = 0; e < kRows; ++e) {
+                const int h = h0 + e * step;
+                if (h - lane / LPH >= heads) break;  // the whole warp
+                const bool is_q = h < p.Hq;
+                float x[8];
+                unpack<uint16_t, 8>(raw[e], x);
+                float m = is_q ? p.scale_q : p.scale_k;
+                if (p.norm != RS_NORM_NONE) {
+                    float ss = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= wf[i] + p.w0;
-            }
-            if (half) {
-                if (p.interleaved) {
-                    if (ch < p.rot) {
-                        const float2 *cs = turn + (r < total ? tok[e] : 0) * half + ch / 2;
+                    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-                        for (int i = 0; i < 8; i += 2) {
-                            const float2 z = cs[i / 2];
-                            const float a = x[i], b = x[i + 1];
-                            x[i] = a * z.x - b * z.y;
-                            x[i + 1] = b * z.x + a * z.y;
-                        }
+                    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+                    if (p.norm == RS_NORM_L2) {
+                        const float r = rsqrtf(ss);
+                        m *= r > p.inv_eps ? p.inv_eps : r;  // x / max(|x|, eps); a NaN norm stays one
+                    } else {
+                        m *= rsqrtf(ss * (1.f / D) + p.eps);
                     }
-                } else {
-                    // lanes of the first and second half exchange their channels
-                    const bool lower = ch < half;
-                    const int other = lower ? lane + half / 8 : lane - half / 8;
-                    const float2 *cs = turn + (r < total ? tok[e] : 0) * half + (lower ? ch : ch - half);
-                    const int src = (threadIdx.x & 31) - lane + (ch < p.rot ? other : lane);
+                }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float y = __shfl_sync(~0u, x[i], src);
-                        if (ch < p.rot) {
-                            const float2 z = cs[i];
-                            x[i] = lower ? x[i] * z.x - y * z.y : x[i] * z.x + y * z.y;
-                        }
+                for (int i = 0; i < 8; ++i) x[i] *= m;
+                const uint16_t *w = is_q ? p.wq : p.wk;
+                if (w) {
+                    float wf[8];
+                    const uint2 wa = *reinterpret_cast<const uint2 *>(w + ch), wb = *reinterpret_cast<const uint2 *>(w + ch + up);
+                    unpack<uint16_t, 8>(make_uint4(wa.x, wa.y, wb.x, wb.y), wf);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] *= wf[i] + p.w0;
+                }
+                if (ROT != ROT_NONE && turning) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int ia = ROT == ROT_PAIRS ? 2 * i : i, ib = ROT == ROT_PAIRS ? 2 * i + 1 : i + 4;
+                        const float a = x[ia], b = x[ib];
+                        x[ia] = a * cs[i] - b * sn[i];
+                        x[ib] = b * cs[i] + a * sn[i];
+                    }
+                }
+                if (h < heads) {
+                    uint16_t *dst = is_q ? qd + (long long)h * D : kd + (long long)(h - p.Hq) * D;
+                    if (ROT == ROT_HALVES) {
+                        st_stream2(dst, make_uint2(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3])));
+                        st_stream2(dst + up, make_uint2(pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7])));
+                    } else {
+                        store_bf16<8>(dst, x);
                     }
                 }
             }
-            if (r < total) {
-                const long long t = t0 + tok[e];
-                uint16_t *dst = is_q ? p.q_out + t * p.ld_qo + (long long)head[e] * D
-                                     : p.k_out + t * p.ld_ko + (long long)(head[e] - p.Hq) * D;
-                store_bf16<8>(dst + ch, x);
-            }
         }
     }
+}
+
+template <int D>
+cudaError_t launch(QkParams &p, int interleaved, cudaStream_t s) {
+    // Where the tokens alone are fewer than 24 warps an SM, several warps a token
+    const int most = (p.Hq + p.Hk + 32 / (D / 8) - 1) / (32 / (D / 8));  // groups of heads of a token
+    p.hs = 1;
+    while (p.hs * 2 <= most && (long long)p.T * p.hs < 152 * 24) p.hs *= 2;
+    const long long ctas = ((long long)p.T * p.hs + kThreads / 32 - 1) / (kThreads / 32);
+    const int grid = (int)(ctas < 152 * 16 ? ctas : 152 * 16);
+    if (!p.rot)
+        qk_kernel<D, ROT_NONE><<<grid, kThreads, 0, s>>>(p);
+    else if (interleaved)
+        qk_kernel<D, ROT_PAIRS><<<grid, kThreads, 0, s>>>(p);
+    else
+        qk_kernel<D, ROT_HALVES><<<grid, kThreads, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -145,19 +173,13 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const __grid_constant__ Qk
 cudaError_t qk_norm_launch(const rs_qk_desc &d, const uint16_t *q, const uint16_t *k, const uint16_t *wq,
                            const uint16_t *wk, const float *inv_freq, const int32_t *positions, uint16_t *q_out,
                            uint16_t *k_out, cudaStream_t s) {
-    QkParams p = {d.T, d.Hq, d.Hk, d.norm, d.rot, d.interleaved, 1, d.eps, d.weight_offset, d.scale_q, d.scale_k,
+    QkParams p = {d.T, d.Hq, d.Hk, d.norm, d.rot, 1, d.eps, 1.f / d.eps, d.weight_offset, d.scale_q, d.scale_k,
                   d.ld_q, d.ld_k, d.ld_qo, d.ld_ko, q, k, wq, wk, inv_freq, positions, q_out, k_out};
-    // Tokens of a CTA: enough heads for one pass of all threads, as long as the grid still covers the SMs
-    const int slots = kThreads / (d.D / 8), heads = d.Hq + d.Hk;
-    while (p.tokens < kMaxTokens && p.tokens * heads < slots * kRows && d.T > p.tokens * 152 * 2) p.tokens *= 2;
-    const int grid = (d.T + p.tokens - 1) / p.tokens;
-    const size_t smem = (size_t)p.tokens * (d.rot / 2) * sizeof(float2);
     switch (d.D) {
-        case 64: qk_kernel<64><<<grid, kThreads, smem, s>>>(p); break;
-        case 128: qk_kernel<128><<<grid, kThreads, smem, s>>>(p); break;
-        default: qk_kernel<256><<<grid, kThreads, smem, s>>>(p); break;
+        case 64: return launch<64>(p, d.interleaved, s);
+        case 128: return launch<128>(p, d.interleaved, s);
+        default: return launch<256>(p, d.interleaved, s);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace rs
