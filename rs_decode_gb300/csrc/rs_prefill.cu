@@ -12,11 +12,11 @@
 //   S'  = e^(G_C) S + sum_j e^(G_C - G_j) u_j k_j^T.
 //
 // T = (I + A)^-1 diag(beta) and P do not depend on the state, so
-//   chunk_kernel  computes them for all chunks and heads at once, and
+//   chunk_cta     computes them for all chunks and heads at once, and
 //   scan_kernel   carries S through a request's chunks.
 // (Segments, rs_prefill.cuh, cut a long request's chunks where few chains would
 // leave the GPU idle.)
-// Requests of at most kShort rows go through step_kernel instead, which runs
+// Requests of at most kShort rows go through step_cta instead, which runs
 // the recurrence row by row beside one read and one write of the state.
 // Decays enter as differences G_i - G_j only, so nothing overflows however
 // long a chunk's decay is; alpha = 0 is a decay of 2^-160, which is 0 in fp32.
@@ -96,7 +96,7 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
     }
 }
 
-// ---------------------------------------------------------------- chunk kernel
+// ---------------------------------------------------------------- chunk matrices
 // One CTA per chunk and key head: the products K K^T and Q K^T are shared by
 // the key head's value heads, whose decays and betas differ and which are
 // served two at a time, 64 threads each.  The triangular inverse is fp32 and
@@ -180,9 +180,8 @@ __device__ __forceinline__ void group_sync(int grp) {  // the 64 threads of one 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kChunkThreads, 4) chunk_kernel(const __grid_constant__ PrefillParams p) {
-    extern __shared__ __align__(128) unsigned char smem[];
-    const int chunk = blockIdx.x / p.G, g = blockIdx.x - chunk * p.G;
+__device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsigned char *smem) {
+    const int chunk = cta / p.G, g = cta - chunk * p.G;
     if (chunk >= min(p.rg.counts[1], p.ccap)) return;
     const int4 e = reinterpret_cast<const int4 *>(p.rg.chunks)[chunk];
     const int n = e.z;
@@ -451,7 +450,7 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_kernel(const __grid_co
     }
 }
 
-// ---------------------------------------------------------------- step kernel
+// ---------------------------------------------------------------- short requests
 // The recurrence for requests of a few rows.  A warp owns 16 value columns of
 // a head: lane = 4 rg + cg holds keys D/8 rg .. and values 4 cg .. of them in
 // registers, so that the state is read and written once, in 64-byte segments
@@ -461,11 +460,13 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_kernel(const __grid_co
 constexpr int kStepThreads = 128;
 
 template <int D>
-__global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constant__ PrefillParams p) {
-    constexpr int ROWS = D / 8;                      // key rows of a lane
-    constexpr int SPLIT = D / 16 / (kStepThreads / 32);  // CTAs of a head
+constexpr int kStepSplit = D / 16 / (kStepThreads / 32);  // CTAs of a head
+
+template <int D>
+__device__ __forceinline__ void step_cta(const PrefillParams &p, int cta) {
+    constexpr int ROWS = D / 8;  // key rows of a lane
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int part = blockIdx.x % SPLIT, hr = blockIdx.x / SPLIT;
+    const int part = cta % kStepSplit<D>, hr = cta / kStepSplit<D>;
     const int h = hr % p.H, r = hr / p.H;
     const bool lead = h == 0 && part == 0 && threadIdx.x == 0;
     // longer requests are scan_kernel's, where it runs at all
@@ -475,6 +476,18 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
     const int g = h / p.rep;
     const int col = (part * (kStepThreads / 32) + warp) * 16 + (lane & 3) * 4, row0 = (lane >> 2) * ROWS;
 
+    // later rows' inputs on their way to the cache, a line or two a lane: rows
+    // follow one another too closely to wait for memory in between
+    for (int i = lane; i < (rq.n - 1) * 8; i += 32) {
+        const long long row = rq.row0 + 1 + (i >> 3);
+        const int w = i & 7;
+        const void *at = w < 2   ? (const void *)(p.k + row * p.ld_k + g * D + (w & 1) * (D / 2))
+                         : w < 4 ? (const void *)(p.q + row * p.ld_q + g * D + (w & 1) * (D / 2))
+                         : w < 5 ? (const void *)(p.v + row * p.ld_v + h * D + col)
+                         : w < 6 ? (const void *)(p.alpha + row * p.H + h)
+                                 : (const void *)(p.beta + row * p.H + h);
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+    }
     float4 S[ROWS];
     {
         const bool cont = rq.start == -2;
@@ -562,6 +575,24 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
     }
     store_state(p.hp, p.lp, ((size_t)rq.srow * p.H + h) * D * D);
     if (rq.start != -2 && lead) p.base[rq.srow] = p.h[rq.srow] = p.nd[rq.srow] = 0;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kStepThreads, 4) step_kernel(const __grid_constant__ PrefillParams p) {
+    step_cta<D>(p, blockIdx.x);
+}
+
+// ---------------------------------------------------------------- front kernel
+// What comes before the scan: the short requests' rows, bound by memory
+// latency, beside the long requests' chunk matrices, bound by issue.
+static_assert(kStepThreads == kChunkThreads, "one launch runs both");
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 4) front_kernel(const __grid_constant__ PrefillParams p, int steps) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    if ((int)blockIdx.x < steps)
+        step_cta<D>(p, blockIdx.x);
+    else
+        chunk_cta<D>(p, blockIdx.x - steps, smem);
 }
 
 // ---------------------------------------------------------------- scan kernel
@@ -940,12 +971,15 @@ cudaError_t scans(const PrefillParams &p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch(const PrefillParams &p, cudaStream_t s) {
-    step_kernel<D><<<p.R * p.H * (D / 16 / (kStepThreads / 32)), kStepThreads, 0, s>>>(p);
-    if (p.max_len <= kShort) return cudaGetLastError();
+    const int steps = p.R * p.H * kStepSplit<D>;
+    if (p.max_len <= kShort) {
+        step_kernel<D><<<steps, kStepThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    }
     static SmemGrants grants;
-    cudaError_t e = grant_smem(reinterpret_cast<const void *>(&chunk_kernel<D>), ChunkSmem<D>::BYTES, grants);
+    cudaError_t e = grant_smem(reinterpret_cast<const void *>(&front_kernel<D>), ChunkSmem<D>::BYTES, grants);
     if (e != cudaSuccess) return e;
-    chunk_kernel<D><<<p.ccap * p.G, kChunkThreads, ChunkSmem<D>::BYTES, s>>>(p);
+    front_kernel<D><<<steps + p.ccap * p.G, kChunkThreads, ChunkSmem<D>::BYTES, s>>>(p, steps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (p.nseg > 1) {

@@ -12,11 +12,12 @@ namespace prefill {
 
 constexpr int C = RS_CHUNK;
 // Rows of the longest request that the recurrence serves.  256 cached requests of
-// 32 heads of 128, by rows (us): recurrence 165 (1), 227 (4), 341 (8), 582 (16),
-// 827 (24); chunks 746 (9) to 759 (33).
-constexpr int kShort = 16;
+// 32 heads of 128 (us): recurrence 166 (1 row), 236 (4), 353 (8), 597 (16), chunks
+// 489 from 9 rows on; 4 requests of 8 heads: recurrence 8.4 (9 rows), 13 (16),
+// chunks 20.
+constexpr int kShort = 12;
 
-// What chunk_kernel leaves for scan_kernel.  All tiles have rows of 64 fp16
+// What chunk_cta leaves for the scans.  All tiles have rows of 64 fp16
 // (128 bytes) with their 16-byte pieces in the order that shared-memory reads
 // want: piece c of row r at c ^ (r & 7).
 //

@@ -41,12 +41,13 @@ struct QkParams {
 // Turns per position as a 64-bit fraction: |f| / (2 pi) 2^64, from f's 24-bit
 // significand m and exponent: f = m 2^(e - 150), 1 / (2 pi) = c 2^-66.
 __device__ __forceinline__ unsigned long long turns(float f) {
-    const unsigned long long c = 0xA2F9836E4E44152Aull;  // 2^66 / (2 pi)
+    constexpr unsigned long long c = 0xA2F9836E4E44152Aull;  // 2^66 / (2 pi)
     const uint32_t bits = __float_as_uint(f);
-    const int e = (bits >> 23) & 255, s = 152 - e;
+    const int e = (bits >> 23) & 255, s = 152 - e;  // s >= 23 for |f| < 2 pi
     const unsigned long long m = e ? (bits & 0x7fffffu) | 0x800000u : 0;
-    const unsigned long long lo = m * c, hi = __umul64hi(m, c);
-    const unsigned long long v = s >= 88 ? 0 : s >= 64 ? hi >> (s - 64) : s > 0 ? hi << (64 - s) | lo >> s : 0;
+    // m c = hi 2^32 + (low word of lo), 88 bits; shifted right by s
+    const unsigned long long lo = m * (uint32_t)c, hi = m * (uint32_t)(c >> 32) + (lo >> 32);
+    const unsigned long long v = s < 32 ? hi << (32 - s) | (uint32_t)lo >> s : s < 96 ? hi >> (s - 32) : 0;
     return bits >> 31 ? 0 - v : v;
 }
 

@@ -51,7 +51,7 @@ rs_status check_prefill(const rs_layer_desc *d, const rs_ragged_desc *rd, int ma
     RS_TRY(check_ragged(rd));
     if (max_len < 0) return RS_ERR_INVALID_ARG;
     // launch grids: chunks x key heads, requests x value heads x at most 8 column groups
-    if ((int64_t)ragged_chunks_cap(*rd) * d->H > kMaxGrid || (int64_t)rd->R * d->H * 8 > kMaxGrid)
+    if ((int64_t)ragged_chunks_cap(*rd) * d->H + (int64_t)rd->R * d->H * 8 > kMaxGrid)
         return RS_ERR_INVALID_ARG;
     return RS_OK;
 }
