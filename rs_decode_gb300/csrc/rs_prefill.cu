@@ -107,7 +107,7 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
 // register-tiled fp32 work (paired FMAs) that keeps the accuracy of T, which
 // every u of the chunk inherits.
 constexpr int kChunkThreads = 128;
-constexpr int LDM = C + 4;  // fp32 matrices in shared memory: 16-byte rows, banks shifted by 4
+constexpr int LDM = C + 8;  // fp32 matrices in shared memory: 16-byte rows, banks shifted by 8
 constexpr int kMat = C * LDM;
 
 template <int D>
@@ -130,8 +130,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// out[RI rows][4 columns] (+)= sgn * sum over m in [m0, m1) of a[row][m] x[m][column]; m0, m1 multiples of 4
-template <int RI, int CJ>
+// acc[RI rows, RS apart][CJ columns] = sum over m in [m0, m1) of a[row][m] x[m][column]; m0, m1 multiples of 4
+template <int RI, int RS, int CJ>
 __device__ __forceinline__ void tile_product(const float *a, const float *x, int m0, int m1, unsigned long long (&acc)[RI][CJ / 2]) {
 #pragma unroll
     for (int i = 0; i < RI; ++i)
@@ -142,7 +142,7 @@ __device__ __forceinline__ void tile_product(const float *a, const float *x, int
         float av[RI][4];
 #pragma unroll
         for (int i = 0; i < RI; ++i) {
-            const float4 v = *reinterpret_cast<const float4 *>(a + i * LDM + m);
+            const float4 v = *reinterpret_cast<const float4 *>(a + i * RS * LDM + m);
             av[i][0] = v.x, av[i][1] = v.y, av[i][2] = v.z, av[i][3] = v.w;
         }
 #pragma unroll
@@ -162,14 +162,14 @@ __device__ __forceinline__ void tile_product(const float *a, const float *x, int
         }
     }
 }
-template <int RI, int CJ>
+template <int RI, int RS, int CJ>
 __device__ __forceinline__ void tile_store(float *out, const unsigned long long (&acc)[RI][CJ / 2], bool negate) {
     const unsigned long long sign = negate ? 0x8000000080000000ull : 0;
 #pragma unroll
     for (int i = 0; i < RI; ++i)
 #pragma unroll
         for (int j = 0; j < CJ / 4; ++j)
-            *reinterpret_cast<ulonglong2 *>(out + i * LDM + 4 * j) = make_ulonglong2(acc[i][2 * j] ^ sign, acc[i][2 * j + 1] ^ sign);
+            *reinterpret_cast<ulonglong2 *>(out + i * RS * LDM + 4 * j) = make_ulonglong2(acc[i][2 * j] ^ sign, acc[i][2 * j + 1] ^ sign);
 }
 
 __device__ __forceinline__ void group_sync(int grp) {  // the 64 threads of one head
@@ -329,24 +329,43 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             const float *gh = vec + r * 4 * C, *gl = gh + C, *be = gl + C;
             float *A = mats + r * kMat;
             unsigned char *pout = reinterpret_cast<unsigned char *>(p.rec[(size_t)chunk * p.H + g * p.rep + r0 + r].p);
-            const float hi[2] = {gh[i0], gh[i0 + 8]}, lo[2] = {gl[i0], gl[i0 + 8]}, bi[2] = {be[i0], be[i0 + 8]};
+            using f2 = unsigned long long;
+            f2 hi[2], lo[2], bi[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = i0 + 8 * hf;
+                hi[hf] = f2_pack(gh[i], gh[i]), lo[hf] = f2_pack(gl[i], gl[i]), bi[hf] = f2_pack(be[i], be[i]);
+            }
+            const f2 one = f2_pack(1.f, 1.f), minus = f2_pack(-1.f, -1.f);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
                 const int j = nt * 8 + j0;
-                const float2 hj = *reinterpret_cast<const float2 *>(gh + j), lj = *reinterpret_cast<const float2 *>(gl + j);
+                if (nt > 2 * warp + 1) {  // above the diagonal
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        *reinterpret_cast<float2 *>(A + (i0 + 8 * hf) * LDM + j) = make_float2(0.f, 0.f);
+                        *reinterpret_cast<uint32_t *>(pout + piece(i0 + 8 * hf, nt) + (lane & 3) * 4) = 0;
+                    }
+                    continue;
+                }
+                const f2 hj = *reinterpret_cast<const f2 *>(gh + j), lj = *reinterpret_cast<const f2 *>(gl + j);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const int i = i0 + 8 * hf;
-                    float2 av = make_float2(0.f, 0.f), pv = av;
-                    if (nt <= 2 * warp + 1) {
-                        const float d0 = j <= i ? exp2_fast((hi[hf] - hj.x) + (lo[hf] - lj.x)) : 0.f;
-                        const float d1 = j + 1 <= i ? exp2_fast((hi[hf] - hj.y) + (lo[hf] - lj.y)) : 0.f;
-                        pv = make_float2(j <= i ? d0 * qk[nt][2 * hf] : 0.f, j + 1 <= i ? d1 * qk[nt][2 * hf + 1] : 0.f);
-                        av = make_float2(j < i ? bi[hf] * d0 * kk[nt][2 * hf] : 0.f,
-                                         j + 1 < i ? bi[hf] * d1 * kk[nt][2 * hf + 1] : 0.f);
+                    float x0, x1;
+                    f2_unpack(f2_fma(f2_fma(hj, minus, hi[hf]), one, f2_fma(lj, minus, lo[hf])), x0, x1);
+                    const f2 d = f2_pack(exp2_fast(x0), exp2_fast(x1));
+                    float p0, p1, a0, a1;
+                    f2_unpack(f2_mul(d, f2_pack(qk[nt][2 * hf], qk[nt][2 * hf + 1])), p0, p1);
+                    f2_unpack(f2_mul(f2_mul(d, bi[hf]), f2_pack(kk[nt][2 * hf], kk[nt][2 * hf + 1])), a0, a1);
+                    if (nt >= 2 * warp) {  // the diagonal's tiles
+                        if (j > i) p0 = 0.f;
+                        if (j + 1 > i) p1 = 0.f;
+                        if (j >= i) a0 = 0.f;
+                        if (j + 1 >= i) a1 = 0.f;
                     }
-                    *reinterpret_cast<float2 *>(A + i * LDM + j) = av;
-                    *reinterpret_cast<uint32_t *>(pout + piece(i, nt) + (lane & 3) * 4) = pack_h2(pv.x, pv.y);
+                    *reinterpret_cast<float2 *>(A + i * LDM + j) = make_float2(a0, a1);
+                    *reinterpret_cast<uint32_t *>(pout + piece(i, nt) + (lane & 3) * 4) = pack_h2(p0, p1);
                 }
             }
         }
@@ -378,26 +397,26 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             {  // the two 32 x 32 blocks, one a warp
                 const int o = 32 * (warp & 1), i = lane >> 1, c = (lane & 1) * 8;
                 unsigned long long acc[1][4];
-                tile_product<1, 8>(A + (o + 16 + i) * LDM + o, A + o * LDM + o + c, 0, 16, acc);
-                tile_store<1, 8>(A + (o + i) * LDM + o + 16 + c, acc, false);
+                tile_product<1, 1, 8>(A + (o + 16 + i) * LDM + o, A + o * LDM + o + c, 0, 16, acc);
+                tile_store<1, 1, 8>(A + (o + i) * LDM + o + 16 + c, acc, false);
                 __syncwarp();
-                tile_product<1, 8>(A + (o + 16 + i) * LDM + o + 16, A + o * LDM + o + 16 + c, 0, 16, acc);
-                tile_store<1, 8>(A + (o + 16 + i) * LDM + o + c, acc, true);
+                tile_product<1, 1, 8>(A + (o + 16 + i) * LDM + o + 16, A + o * LDM + o + 16 + c, 0, 16, acc);
+                tile_store<1, 1, 8>(A + (o + 16 + i) * LDM + o + c, acc, true);
             }
             group_sync(grp);
             {  // the 64 x 64 block; zero halves of the triangular factors are skipped
                 unsigned long long acc[4][2];
                 const int w = warp & 1;
                 {
-                    const int i = (lane >> 2) * 4, c = 16 * w + (lane & 3) * 4;
-                    tile_product<4, 4>(A + (32 + i) * LDM, A + c, 16 * w, 32, acc);
-                    tile_store<4, 4>(A + i * LDM + 32 + c, acc, false);
+                    const int i = lane >> 2, c = 16 * w + (lane & 3) * 4;  // rows i + 8 x
+                    tile_product<4, 8, 4>(A + (32 + i) * LDM, A + c, 16 * w, 32, acc);
+                    tile_store<4, 8, 4>(A + i * LDM + 32 + c, acc, false);
                 }
                 group_sync(grp);
                 {
                     const int i = 16 * (1 - w) + (lane >> 3) * 4, c = (lane & 7) * 4;
-                    tile_product<4, 4>(A + (32 + i) * LDM + 32, A + 32 + c, 0, 32 - 16 * w, acc);
-                    tile_store<4, 4>(A + (32 + i) * LDM + c, acc, true);
+                    tile_product<4, 1, 4>(A + (32 + i) * LDM + 32, A + 32 + c, 0, 32 - 16 * w, acc);
+                    tile_store<4, 1, 4>(A + (32 + i) * LDM + c, acc, true);
                 }
             }
             group_sync(grp);
@@ -405,28 +424,28 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             Record &out = p.rec[(size_t)chunk * p.H + g * p.rep + r0 + grp];
             const float *be = vec + grp * 4 * C + 2 * C, *ke = be + C;
             const int c = t & 7;
-            float bj[8];
-            *reinterpret_cast<float4 *>(bj) = *reinterpret_cast<const float4 *>(be + c * 8);
-            *reinterpret_cast<float4 *>(bj + 4) = *reinterpret_cast<const float4 *>(be + c * 8 + 4);
+            const ulonglong2 b0 = *reinterpret_cast<const ulonglong2 *>(be + c * 8), b1 = *reinterpret_cast<const ulonglong2 *>(be + c * 8 + 4);
+            const unsigned long long bj[4] = {b0.x, b0.y, b1.x, b1.y};
             float um = 0.f, kmx = 0.f;
 #pragma unroll 2
             for (int i = 0; i < 8; ++i) {
                 const int row = i * 8 + (t >> 3);
-                float v[8], m = 0.f, sum = 0.f, up, down;
-                *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(A + row * LDM + c * 8);
-                *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(A + row * LDM + c * 8 + 4);
+                // the row's sum of magnitudes sizes its scale and bounds what it can make of R
+                using f2 = unsigned long long;
+                const ulonglong2 v0 = *reinterpret_cast<const ulonglong2 *>(A + row * LDM + c * 8);
+                const ulonglong2 v1 = *reinterpret_cast<const ulonglong2 *>(A + row * LDM + c * 8 + 4);
+                const f2 w[4] = {f2_mul(v0.x, bj[0]), f2_mul(v0.y, bj[1]), f2_mul(v1.x, bj[2]), f2_mul(v1.y, bj[3])};
+                float v[8], sum = 0.f, up, down;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) f2_unpack(w[x], v[2 * x], v[2 * x + 1]);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    v[x] = c * 8 + x <= row ? v[x] * bj[x] : 0.f;
-                    m = fmaxf(m, fabsf(v[x]));
+                    if (c * 8 + x > row) v[x] = 0.f;
                     sum += fabsf(v[x]);
                 }
 #pragma unroll
-                for (int o = 1; o < 8; o <<= 1) {
-                    m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-                    sum += __shfl_xor_sync(~0u, sum, o);
-                }
-                row_scale<8>(m, up, down);
+                for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                row_scale<8>(sum, up, down);
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) split2(v[2 * x] * up, v[2 * x + 1] * up, hi[x], lo[x]);
