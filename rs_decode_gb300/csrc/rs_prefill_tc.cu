@@ -189,9 +189,13 @@ struct Work {  // one request's head, as both sides see it
     __device__ int rows(int i) const { return min(i == 0 ? head_rows : C, n - first(i)); }
 };
 
+// The copies and products of a chunk are issued by one warp each (X warp 0, U 1,
+// D 2, Y 3, Z 4, keys 5, queries and P 6, T 7): an issuing warp falls behind by
+// about 40 clocks an instruction, and the others wait for it at the next barrier.
+//
 // Copies of one head's chunks into shared memory.  Each buffer has one warp
 // that refills it, once something that all threads waited for implies that the
-// buffer's readers are done: keys, vectors, queries and P warp 1, T warp 3.
+// buffer's readers are done.
 // (V's rows have the caller's stride: all threads copy them, 16 bytes each; one
 // bulk copy a row would hold up its warp for 45 clocks a copy.)
 // Where they come from, and how many were begun, is kept beside the barriers.
@@ -322,12 +326,12 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
             }
         }
     };
-    if (warp == 1) {
+    if (warp == 5) {
         load_k(b, sm, 0, p.H);
-        if (OUT) load_qp(b, sm, 0, p.H);
         if (nch > 1) load_k(b, sm, 1, p.H);
     }
-    if (warp == 3) load_t(b, sm, 0, p.H);
+    if (OUT && warp == 6) load_qp(b, sm, 0, p.H);
+    if (warp == 7) load_t(b, sm, 0, p.H);
     load_v(0);
 
     f2 S[DH / 2];
@@ -373,6 +377,8 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
     const long long ystep = (long long)p.H * D;
     uint16_t *y = p.y + ((long long)rq.row0 * p.H + h) * D + (row & ~1) + (hf * CH + 16 * (row & 1)) * ystep;
     float *rowmax = reinterpret_cast<float *>(smem + Smem::MAX);
+    // the first position after the unit's start where a state is to be kept
+    int block_end = p.block && p.pool ? ((rq.ctx + w.first(u.c0)) / p.block + 1) * p.block : -1;
     bool ok = true;
     for (int i = 0; i < nch; ++i) {
         const unsigned ph = i & 1, kph = (i >> 1) & 1;
@@ -397,7 +403,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         asm volatile("cp.async.wait_all;" ::: "memory");  // this thread's part of V
         tc_fence_before_sync();
         if (__syncthreads_or(!ok)) break;
-        if (i > 0 && i + 1 < nch && warp == 1) load_k(b, sm, i + 1, p.H);  // the last chunk's are free: its y is done
+        if (i > 0 && i + 1 < nch && warp == 5) load_k(b, sm, i + 1, p.H);  // the last chunk's are free: its y is done
         ok = wait_warp(b->full_k + (i & 1), kph, b, p.status) && ok;
         if (warp == 0) {
             tc_fence_after_sync();
@@ -450,7 +456,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         tc_fence_before_sync();
         if (__syncthreads_or(!ok)) { ok = false; break; }
         load_v(i + 1);
-        if (warp == 0) {
+        if (warp == 1) {
             ok = wait_warp(&b->full_t, ph, b, p.status) && ok;
             tc_fence_after_sync();
             if (elect_one()) issue_u(base, desc_lo(sm + Smem::T), b);
@@ -465,7 +471,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         const f2 uup2 = f2_pack(uups, uups);
         ok = wait_warp(&b->mu, ph, b, p.status) && ok;
         tc_fence_after_sync();
-        if (i + 1 < nch && warp == 3) load_t(b, sm, i + 1, p.H);
+        if (i + 1 < nch && warp == 7) load_t(b, sm, i + 1, p.H);
         uint32_t z[CH / 2];  // u in fp16, then Z, then y
 #pragma unroll
         for (int t = 0; t < CH; t += 16) {
@@ -508,15 +514,16 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         st_done();
         tc_fence_before_sync();
         if (__syncthreads_or(!ok)) { ok = false; break; }
-        if (warp == 0) {
+        if (warp == 2) {
             tc_fence_after_sync();
             if (elect_one()) issue_d(base, sk, b);
             __syncwarp();
-            if (OUT) {
-                ok = wait_warp(&b->full_p, ph, b, p.status) && ok;
-                if (elect_one()) issue_y(base, desc_lo(sm + Smem::Q), desc_lo(sm + Smem::P), b);
-                __syncwarp();
-            }
+        }
+        if (OUT && warp == 3) {
+            ok = wait_warp(&b->full_p, ph, b, p.status) && ok;
+            tc_fence_after_sync();
+            if (elect_one()) issue_y(base, desc_lo(sm + Smem::Q), desc_lo(sm + Smem::P), b);
+            __syncwarp();
         }
         // S <- e^(G_C) S + D
         ok = wait_warp(&b->md, ph, b, p.status) && ok;
@@ -535,7 +542,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         // y = (e^G Z + Y) with the query's power of two
         ok = wait_warp(&b->my, ph, b, p.status) && ok;
         tc_fence_after_sync();
-        if (i + 1 < nch && warp == 1) load_qp(b, sm, i + 1, p.H);
+        if (i + 1 < nch && warp == 6) load_qp(b, sm, i + 1, p.H);
         const float zs = sdown * 512.f;
         const unsigned long long zs2 = f2_pack(zs, zs), ud2 = f2_pack(udown, udown);
 #pragma unroll
@@ -583,7 +590,10 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
                 }
             }
         }
-        const int slot = block_slot(p, r, rq.ctx + w.first(u.c0 + i) + n, h == 0 && threadIdx.x == 0);
+        const int end = rq.ctx + w.first(u.c0 + i) + n;
+        if (end != block_end) continue;
+        block_end += p.block;
+        const int slot = block_slot(p, r, end, h == 0 && threadIdx.x == 0);
         if (slot >= 0) {
             const size_t slab = ((size_t)slot * p.H + h) * D * D;
             if (p.prec == RS_PREC_SHARED_BF16)
@@ -594,7 +604,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
     }
     if (__syncthreads_or(!ok)) {
         drain(b);
-        if (warp == 0 || warp == 4) {  // elect_one() names the same lane each time: the one that issued the products
+        if (warp < 5) {  // elect_one() names the same lane each time: the one that issued the products
             if (elect_one()) umma_commit(&b->mend);
             __syncwarp();
             mbar_wait(&b->mend, 0);
@@ -630,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_tc_kernel(const __grid_const
             for (uint64_t *x : {b->full_k, b->full_k + 1, &b->full_q, &b->full_t, &b->full_p, &b->mx, &b->mz,
                                 &b->mu, &b->md, &b->my})
                 mbar_init(x, 1);
-            mbar_init(&b->mend, 2);
+            mbar_init(&b->mend, 5);
             b->abort = 0;
             b->nk = b->nq = b->nt = 0;
             b->tiles = p.tiles + ((size_t)(rq.chunk0 + u.c0) * p.G + h / p.rep) * (2 * kTile);
