@@ -608,6 +608,7 @@ static_assert(kStepThreads == kChunkThreads, "one launch runs both");
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 4) front_kernel(const __grid_constant__ PrefillParams p, int steps) {
     extern __shared__ __align__(128) unsigned char smem[];
+    let_next_launch();
     if ((int)blockIdx.x < steps)
         step_cta<D>(p, blockIdx.x);
     else
@@ -641,8 +642,10 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part = blockIdx.x % SPLIT, hr = blockIdx.x / SPLIT;
-    const int h = hr % p.H, q = hr / p.H % units, r = hr / p.H / units;
-    if (p.rg.cu_tokens[r + 1] - p.rg.cu_tokens[r] <= kShort) return;
+    if (blockIdx.x == 0) wait_for_launch();  // so that this launch does not end before the one it overlaps
+    int q;
+    const int h = hr % p.H, r = cta_request(p, hr / p.H, units, q);
+    if (r < 0) return;
     const Request rq = load_request(p, r, h == 0 && part == 0 && q == 0 && tid == 0);
     if (!rq.ok) return;
     const Unit un = scan_unit<OUT>(p, hr, rq, r, q);
@@ -669,7 +672,6 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
         for (int x = tid; x < (int)sizeof(Record) / 16; x += NT) cp16(st + M::REC + x * 16, rec + x * 16, true);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(un.c0, s0);
 
     // the starting state: S^T[p][n], rows p = col0 + gr (+8), columns n = 8 nt + 2 tq (+1)
     const int gr = lane >> 2, tq = lane & 3;
@@ -695,6 +697,8 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
             }
     };
 
+    wait_for_launch();  // for the chunks' records
+    fetch(un.c0, s0);
     if (!OUT && un.seg == 0) store_state(p.segs, nullptr, seg_slab(p, un, 0, D * D));  // for the second pass
 
     for (int i = un.c0; i < un.c1; ++i) {
@@ -973,8 +977,8 @@ cudaError_t scan_launch(const PrefillParams &p, cudaStream_t s) {
     const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&scan_kernel<D, NW, OUT>), ScanSmem<D, NW>::BYTES, grants);
     if (e != cudaSuccess) return e;
     const int units = scan_units<OUT>(p);
-    scan_kernel<D, NW, OUT><<<p.R * p.H * units * (D / (16 * NW)), NW * 32, ScanSmem<D, NW>::BYTES, s>>>(p, units);
-    return cudaGetLastError();
+    return launch_after(scan_kernel<D, NW, OUT>, p.classes * p.R * p.H * units * (D / (16 * NW)), NW * 32,
+                        ScanSmem<D, NW>::BYTES, s, start_early(p), p, units);
 }
 
 template <int D, bool OUT>
@@ -1052,6 +1056,10 @@ cudaError_t prefill_launch(const rs_layer_desc &d, const rs_state &st, const rs_
     p.rows = in.rows, p.start = in.start, p.pool = in.pool, p.y = y, p.rec = static_cast<Record *>(work);
     p.tiles = static_cast<unsigned char *>(work) + (size_t)p.ccap * d.H * sizeof(Record);
     plan_segments(d, rd, in.max_len, p.nseg, p.seglen);
+    // passes over the requests cost a CTA each that leaves at once: only where the
+    // units are few enough for the last chain to show
+    p.maxch = (in.max_len < rd.tokens_cap ? in.max_len : rd.tokens_cap) / C + 2;
+    p.classes = p.nseg == 1 && p.R > 1 && p.maxch > 4 && (long long)p.R * p.H <= 2048 ? 4 : 1;
     p.segs = reinterpret_cast<float *>(p.tiles + (size_t)p.ccap * d.G * 2 * C * d.N * 2);
     p.maps = p.segs + (size_t)rd.R * d.H * p.nseg * d.N * d.P;
     return d.P == 128 ? launch<128>(p, s) : launch<64>(p, s);

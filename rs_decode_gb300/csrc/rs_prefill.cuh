@@ -59,6 +59,7 @@ struct PrefillParams {
     Record *rec;  // [ccap][H]
     unsigned char *tiles;  // [ccap][G] keys and queries of a chunk, fp16
     int nseg, seglen;      // segments of a request at most, chunks of a segment
+    int classes, maxch;    // length classes of the scan's CTAs, chunks of the longest request
     float *segs, *maps;    // [R][H][nseg][N][P] segments' starting states and transition maps
 };
 
@@ -99,26 +100,23 @@ struct Request {
 // A request's facts, checked; bits of what is wrong go to the status word.
 __device__ __forceinline__ Request load_request(const PrefillParams &p, int r, bool report) {
     Request q = {};
+    // two rounds of independent loads
     const int a = p.rg.cu_tokens[r], b = p.rg.cu_tokens[r + 1];
+    const int c0 = p.rg.cu_chunks[r], c1 = p.rg.cu_chunks[r + 1];
+    const int srow = p.rows ? p.rows[r] : r, start = p.start ? p.start[r] : -2;
+    const bool in_cap = a >= 0 && b > a && b <= p.cap, in_rows = srow >= 0 && srow < p.B;
     q.n = b - a;
-    q.row0 = a;
     if (q.n == 0) return q;
+    q.ctx = in_cap ? p.rg.token_pos[a] : -1;
+    const int pending = in_rows ? p.h[srow] | p.nd[srow] : 0;
+    q.row0 = a, q.chunk0 = c0, q.nch = c1 - c0, q.srow = srow, q.start = start;
     unsigned bits = 0;
-    if (q.n < 0 || a < 0 || b > p.cap || q.n > p.max_len) {
+    if (!in_cap || q.n > p.max_len || q.ctx < 0 || q.ctx > (1 << 30) || c0 < 0 || c1 > p.ccap ||
+        q.nch != (q.ctx + q.n + C - 1) / C - q.ctx / C)
         bits = RS_DEV_LENGTH;
-    } else {
-        q.ctx = p.rg.token_pos[a];
-        q.chunk0 = p.rg.cu_chunks[r];
-        q.nch = p.rg.cu_chunks[r + 1] - q.chunk0;
-        if (q.ctx < 0 || q.ctx > (1 << 30) || q.chunk0 < 0 || q.chunk0 + q.nch > p.ccap ||
-            q.nch != (q.ctx + q.n + C - 1) / C - q.ctx / C)
-            bits = RS_DEV_LENGTH;
-    }
-    q.srow = p.rows ? p.rows[r] : r;
-    q.start = p.start ? p.start[r] : -2;
-    if (q.srow < 0 || q.srow >= p.B || q.start < -2 || q.start >= p.n_pool)
+    if (!in_rows || start < -2 || start >= p.n_pool)
         bits |= RS_DEV_SLOT;
-    else if (q.start == -2 && (p.h[q.srow] != 0 || p.nd[q.srow] != 0))
+    else if (start == -2 && pending != 0)
         bits |= RS_DEV_RECORDS;
     q.ok = bits == 0;
     if (bits && report) atomicOr(p.status, bits);
@@ -136,6 +134,27 @@ __device__ __forceinline__ int block_slot(const PrefillParams &p, int r, int end
     return -1;
 }
 
+// A scan's CTAs may start while the launch before it still runs (launch_after):
+// they fetch their starting state first and wait here for what that launch writes.
+__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next launch's CTAs start once all of this launch's have.
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <class... KArgs, class... Args>
+cudaError_t launch_after(void (*kernel)(KArgs...), int grid, int block, int smem, cudaStream_t s, bool early, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(block), cfg.dynamicSmemBytes = smem, cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr, cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// CTAs that start early are placed around what still runs, so two may share an SM
+// while others stay empty: only where the chains fill the GPU twice over anyway
+// (192 chains of 64-wide heads: 102 us early, 72 after the launch before).
+inline bool start_early(const PrefillParams &p) { return p.nseg == 1 && (long long)p.R * p.H >= 304; }
+
 // ---------------------------------------------------------------- segments
 // A request's chunks form one chain per head.  Where requests and heads alone
 // leave most of the GPU idle, the chain is cut into segments.  A segment's final
@@ -148,6 +167,21 @@ __device__ __forceinline__ int block_slot(const PrefillParams &p, int r, int end
 //   and again, with outputs, from those states.
 // That is a little over twice the work on a chain shorter by the number of
 // segments.
+// Without segments the CTAs come in up to four passes over the requests, longest
+// first: a CTA whose request is of another class leaves at once.  Started in the
+// requests' own order, a long chain that comes last would run alone at the end.
+__device__ __forceinline__ int length_class(const PrefillParams &p, int nch) {
+    return nch > p.maxch >> 1 ? 0 : nch > p.maxch >> 2 ? 1 : nch > p.maxch >> 3 ? 2 : 3;
+}
+// The request of a CTA (already without its head and part), -1 if it has nothing to do; q: its unit.
+__device__ __forceinline__ int cta_request(const PrefillParams &p, int cta, int units, int &q) {
+    q = cta % units;
+    const int cr = cta / units, r = cr % p.R;
+    if (p.rg.cu_tokens[r + 1] - p.rg.cu_tokens[r] <= kShort) return -1;
+    if (p.classes > 1 && length_class(p, p.rg.cu_chunks[r + 1] - p.rg.cu_chunks[r]) != cr / p.R) return -1;
+    return r;
+}
+
 struct Unit {          // what one CTA of a scan runs
     int r, h, seg;
     bool map;          // from the identity, without V

@@ -326,14 +326,6 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
             }
         }
     };
-    if (warp == 5) {
-        load_k(b, sm, 0, p.H);
-        if (nch > 1) load_k(b, sm, 1, p.H);
-    }
-    if (OUT && warp == 6) load_qp(b, sm, 0, p.H);
-    if (warp == 7) load_t(b, sm, 0, p.H);
-    load_v(0);
-
     f2 S[DH / 2];
     {
         const StateSource from = unit_start<OUT, D>(p, rq, u);
@@ -352,6 +344,14 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
             }
         }
     }
+    wait_for_launch();  // for the chunks' records
+    if (warp == 5) {
+        load_k(b, sm, 0, p.H);
+        if (nch > 1) load_k(b, sm, 1, p.H);
+    }
+    if (OUT && warp == 6) load_qp(b, sm, 0, p.H);
+    if (warp == 7) load_t(b, sm, 0, p.H);
+    load_v(0);
     auto store_state = [&](float *f, uint16_t *q, size_t slab) {
         slab += hf * DH * D + row;
         if (f) {
@@ -626,8 +626,10 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
 template <bool OUT>
 __global__ void __launch_bounds__(kThreads, 2) scan_tc_kernel(const __grid_constant__ PrefillParams p, int units) {
     extern __shared__ unsigned char raw[];
-    const int h = blockIdx.x % p.H, q = blockIdx.x / p.H % units, r = blockIdx.x / p.H / units;
-    if (p.rg.cu_tokens[r + 1] - p.rg.cu_tokens[r] <= kShort) return;
+    if (blockIdx.x == 0) wait_for_launch();  // so that this launch does not end before the one it overlaps
+    int q;
+    const int h = blockIdx.x % p.H, r = cta_request(p, blockIdx.x / p.H, units, q);
+    if (r < 0) return;
     const Request rq = load_request(p, r, h == 0 && q == 0 && threadIdx.x == 0);
     if (!rq.ok) return;
     const Unit u = scan_unit<OUT>(p, blockIdx.x, rq, r, q);
@@ -670,8 +672,7 @@ cudaError_t scan_tc_launch(const PrefillParams &p, cudaStream_t s) {
     const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&scan_tc_kernel<OUT>), Smem::BYTES, grants);
     if (e != cudaSuccess) return e;
     const int units = scan_units<OUT>(p);
-    scan_tc_kernel<OUT><<<p.R * p.H * units, kThreads, Smem::BYTES, s>>>(p, units);
-    return cudaGetLastError();
+    return launch_after(scan_tc_kernel<OUT>, p.classes * p.R * p.H * units, kThreads, Smem::BYTES, s, start_early(p), p, units);
 }
 template cudaError_t scan_tc_launch<true>(const PrefillParams &p, cudaStream_t s);
 template cudaError_t scan_tc_launch<false>(const PrefillParams &p, cudaStream_t s);
