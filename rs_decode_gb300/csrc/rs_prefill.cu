@@ -103,9 +103,9 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
 // in place: four 16 x 16 diagonal blocks by substitution (a column per thread),
 // then twice  [[a,0],[c,b]]^-1 = [[a',0],[-b' c a', b']]  with the product c a'
 // waiting in the unused block above the diagonal.  Substitution over the whole
-// 64 rows would be one dependent chain of 2016 steps; the two products are
-// register-tiled fp32 work (paired FMAs) that keeps the accuracy of T, which
-// every u of the chunk inherits.
+// 64 rows would be one dependent chain of 2016 steps; the products run on the
+// tensor cores with operands split to 22 bits, since every u of the chunk
+// inherits T's accuracy.
 constexpr int kChunkThreads = 128;
 constexpr int LDM = C + 8;  // fp32 matrices in shared memory: 16-byte rows, banks shifted by 8
 constexpr int kMat = C * LDM;
@@ -130,46 +130,63 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// acc[RI rows, RS apart][CJ columns] = sum over m in [m0, m1) of a[row][m] x[m][column]; m0, m1 multiples of 4
-template <int RI, int RS, int CJ>
-__device__ __forceinline__ void tile_product(const float *a, const float *x, int m0, int m1, unsigned long long (&acc)[RI][CJ / 2]) {
+// Products of fp32 blocks on the tensor cores: tf32 operands hold 11 bits, so an
+// operand enters as hi (cut to 11 bits) plus lo (what is left, which the
+// hardware cuts likewise) and a product takes three terms: 22 bits, without a
+// scale, since tf32 has fp32's exponent.
+// mma.sync m16n8k8: lane = 4 g + t.  A: rows g, g+8, columns t, t+4; B: rows (k)
+// t, t+4, column g; C as above.
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+template <int N>
+__device__ __forceinline__ void cut(const float (&x)[N], uint32_t (&hi)[N], uint32_t (&lo)[N]) {
 #pragma unroll
-    for (int i = 0; i < RI; ++i)
-#pragma unroll
-        for (int j = 0; j < CJ / 2; ++j) acc[i][j] = 0;
-#pragma unroll 2
-    for (int m = m0; m < m1; m += 4) {
-        float av[RI][4];
-#pragma unroll
-        for (int i = 0; i < RI; ++i) {
-            const float4 v = *reinterpret_cast<const float4 *>(a + i * RS * LDM + m);
-            av[i][0] = v.x, av[i][1] = v.y, av[i][2] = v.z, av[i][3] = v.w;
-        }
-#pragma unroll
-        for (int mm = 0; mm < 4; ++mm) {
-            unsigned long long xv[CJ / 2];
-#pragma unroll
-            for (int j = 0; j < CJ / 4; ++j) {
-                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(x + (m + mm) * LDM + 4 * j);
-                xv[2 * j] = v.x, xv[2 * j + 1] = v.y;
-            }
-#pragma unroll
-            for (int i = 0; i < RI; ++i) {
-                const unsigned long long w = f2_pack(av[i][mm], av[i][mm]);
-#pragma unroll
-                for (int j = 0; j < CJ / 2; ++j) acc[i][j] = f2_fma(w, xv[j], acc[i][j]);
-            }
-        }
+    for (int i = 0; i < N; ++i) {
+        hi[i] = __float_as_uint(x[i]) & 0xffffe000u;
+        lo[i] = __float_as_uint(x[i] - __uint_as_float(hi[i]));
     }
 }
-template <int RI, int RS, int CJ>
-__device__ __forceinline__ void tile_store(float *out, const unsigned long long (&acc)[RI][CJ / 2], bool negate) {
-    const unsigned long long sign = negate ? 0x8000000080000000ull : 0;
+// a, x: a block's first element, rows LDM apart
+__device__ __forceinline__ void frag_a(const float *a, int lane, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    const float *p = a + (lane >> 2) * LDM + (lane & 3);
+    const float v[4] = {p[0], p[8 * LDM], p[4], p[8 * LDM + 4]};
+    cut(v, hi, lo);
+}
+__device__ __forceinline__ void frag_b(const float *x, int lane, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+    const float *p = x + (lane & 3) * LDM + (lane >> 2);
+    const float v[2] = {p[0], p[4 * LDM]};
+    cut(v, hi, lo);
+}
+__device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh)[2],
+                                     const uint32_t (&bl)[2]) {
+    mma_tf32(c, al, bh);
+    mma_tf32(c, ah, bl);
+    mma_tf32(c, ah, bh);
+}
+__device__ __forceinline__ void put_c(float *out, int lane, const float (&c)[4], float sign) {
+    float *p = out + (lane >> 2) * LDM + (lane & 3) * 2;
+    *reinterpret_cast<float2 *>(p) = make_float2(sign * c[0], sign * c[1]);
+    *reinterpret_cast<float2 *>(p + 8 * LDM) = make_float2(sign * c[2], sign * c[3]);
+}
+// out = sign a x for 16 x 16 blocks, by one warp
+__device__ __forceinline__ void product16(const float *a, const float *x, float *out, int lane, float sign) {
+    float c[2][4] = {};
 #pragma unroll
-    for (int i = 0; i < RI; ++i)
+    for (int k = 0; k < 2; ++k) {
+        uint32_t ah[4], al[4], bh[2], bl[2];
+        frag_a(a + 8 * k, lane, ah, al);
 #pragma unroll
-        for (int j = 0; j < CJ / 4; ++j)
-            *reinterpret_cast<ulonglong2 *>(out + i * RS * LDM + 4 * j) = make_ulonglong2(acc[i][2 * j] ^ sign, acc[i][2 * j + 1] ^ sign);
+        for (int n = 0; n < 2; ++n) {
+            frag_b(x + 8 * k * LDM + 8 * n, lane, bh, bl);
+            mma3(c[n], ah, al, bh, bl);
+        }
+    }
+    put_c(out, lane, c[0], sign);
+    put_c(out + 8, lane, c[1], sign);
 }
 
 __device__ __forceinline__ void group_sync(int grp) {  // the 64 threads of one head
@@ -395,28 +412,48 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
                 __syncwarp();
             }
             {  // the two 32 x 32 blocks, one a warp
-                const int o = 32 * (warp & 1), i = lane >> 1, c = (lane & 1) * 8;
-                unsigned long long acc[1][4];
-                tile_product<1, 1, 8>(A + (o + 16 + i) * LDM + o, A + o * LDM + o + c, 0, 16, acc);
-                tile_store<1, 1, 8>(A + (o + i) * LDM + o + 16 + c, acc, false);
+                float *X = A + (32 * (warp & 1)) * (LDM + 1);
+                product16(X + 16 * LDM, X, X + 16, lane, 1.f);
                 __syncwarp();
-                tile_product<1, 1, 8>(A + (o + 16 + i) * LDM + o + 16, A + o * LDM + o + 16 + c, 0, 16, acc);
-                tile_store<1, 1, 8>(A + (o + 16 + i) * LDM + o + c, acc, true);
+                product16(X + 16 * LDM + 16, X + 16, X + 16 * LDM, lane, -1.f);
             }
             group_sync(grp);
-            {  // the 64 x 64 block; zero halves of the triangular factors are skipped
-                unsigned long long acc[4][2];
+            {  // the 64 x 64 block; zero tiles of the triangular factors are skipped
                 const int w = warp & 1;
-                {
-                    const int i = lane >> 2, c = 16 * w + (lane & 3) * 4;  // rows i + 8 x
-                    tile_product<4, 8, 4>(A + (32 + i) * LDM, A + c, 16 * w, 32, acc);
-                    tile_store<4, 8, 4>(A + i * LDM + 32 + c, acc, false);
+                {  // c a': 16 rows a warp
+                    float c[4][4] = {};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t ah[4], al[4], bh[2], bl[2];
+                        frag_a(A + (32 + 16 * w) * LDM + 8 * k, lane, ah, al);
+#pragma unroll
+                        for (int n = 0; n <= k; ++n) {
+                            frag_b(A + 8 * k * LDM + 8 * n, lane, bh, bl);
+                            mma3(c[n], ah, al, bh, bl);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) put_c(A + 16 * w * LDM + 32 + 8 * n, lane, c[n], 1.f);
                 }
                 group_sync(grp);
-                {
-                    const int i = 16 * (1 - w) + (lane >> 3) * 4, c = (lane & 7) * 4;
-                    tile_product<4, 1, 4>(A + (32 + i) * LDM + 32, A + 32 + c, 0, 32 - 16 * w, acc);
-                    tile_store<4, 1, 4>(A + (32 + i) * LDM + c, acc, true);
+                {  // -b' (c a'): 16 columns a warp
+                    float c[2][2][4] = {};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t ah[4], al[4], bh[2][2], bl[2][2];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) frag_b(A + 8 * k * LDM + 32 + 16 * w + 8 * n, lane, bh[n], bl[n]);
+#pragma unroll
+                        for (int m = k / 2; m < 2; ++m) {
+                            frag_a(A + (32 + 16 * m) * LDM + 32 + 8 * k, lane, ah, al);
+                            mma3(c[m][0], ah, al, bh[0], bl[0]);
+                            mma3(c[m][1], ah, al, bh[1], bl[1]);
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) put_c(A + (32 + 16 * m) * LDM + 16 * w + 8 * n, lane, c[m][n], -1.f);
                 }
             }
             group_sync(grp);
