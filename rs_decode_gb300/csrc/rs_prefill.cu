@@ -927,31 +927,35 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
 }
 
 // ---------------------------------------------------------------- combine kernel
-// S_(s+1) = M_s S_s + B_s over a request's segments, in order: per head and 32
+// S_(s+1) = M_s S_s + B_s over a request's segments, in order: per head and W
 // value columns one CTA, which keeps S_s's columns in shared memory while the
-// next M_s is on its way.  fp32 throughout; bound by the maps' 64 KiB a step.
-template <int D>
+// next M_s and B_s are on their way.  fp32 throughout.  A step reads a 64 KiB
+// map for few columns: narrow CTAs shorten the step, wide ones read the map
+// less often.
+template <int D, int W>
 struct CombineSmem {
     static constexpr int LD = D + 4;
     static constexpr int MAP = D * LD * 4;
-    static constexpr int BYTES = 2 * MAP + 2 * D * 32 * 4;
+    static constexpr int BYTES = 2 * MAP + 2 * D * W * 4;
 };
 
-template <int D>
+template <int D, int W>
 __global__ void __launch_bounds__(2 * D) combine_kernel(const __grid_constant__ PrefillParams p) {
-    using M = CombineSmem<D>;
+    using M = CombineSmem<D, W>;
+    using f2 = unsigned long long;
+    constexpr int NR = W / 8;  // rows of a thread, four columns each
     extern __shared__ __align__(128) unsigned char smem[];
-    const int part = blockIdx.x % (D / 32), hr = blockIdx.x / (D / 32);
+    const int part = blockIdx.x % (D / W), hr = blockIdx.x / (D / W);
     const int tid = threadIdx.x;
     Unit u;
     u.h = hr % p.H, u.r = hr / p.H;
     if (p.rg.cu_tokens[u.r + 1] - p.rg.cu_tokens[u.r] <= kShort) return;
     const Request rq = load_request(p, u.r, false);
     if (!rq.ok) return;
-    const int nsegs = (rq.nch + p.seglen - 1) / p.seglen;
-    if (nsegs < 3) return;
+    const int last = (rq.nch + p.seglen - 1) / p.seglen - 1;  // steps 1 .. last - 1
+    if (last < 2) return;
     const uint32_t s0 = smem_u32(smem);
-    float *X = reinterpret_cast<float *>(smem + 2 * M::MAP);  // two buffers [D][32]
+    float *X = reinterpret_cast<float *>(smem + 2 * M::MAP);  // two buffers [D][W]
     auto fetch = [&](int s) {
         const float *src = p.maps + seg_slab(p, u, s, D * D);
         const uint32_t dst = s0 + (s & 1) * M::MAP;
@@ -959,53 +963,70 @@ __global__ void __launch_bounds__(2 * D) combine_kernel(const __grid_constant__ 
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     fetch(1);
-    for (int i = tid; i < D * 8; i += 2 * D)
-        reinterpret_cast<float4 *>(X)[i] = *reinterpret_cast<const float4 *>(p.segs + seg_slab(p, u, 1, D * D) + (i / 8) * D + part * 32 + (i % 8) * 4);
-    const int n = (tid >> 2) * 2, c = (tid & 3) * 8;  // rows n, n + 1, columns c..c + 7
-    for (int s = 1; s < nsegs - 1; ++s) {
-        if (s + 1 < nsegs - 1) {
+    const int n = tid / (W / 4) * NR, c = tid % (W / 4) * 4;  // rows n.., columns c..c + 3
+    auto slab = [&](int s) { return p.segs + seg_slab(p, u, s, D * D) + (size_t)n * D + part * W + c; };
+    f2 next[NR][2];
+    auto load_b = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(slab(s) + i * D);
+            next[i][0] = v.x, next[i][1] = v.y;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+        *reinterpret_cast<float4 *>(X + (n + i) * W + c) = *reinterpret_cast<const float4 *>(slab(1) + i * D);
+    load_b(2);
+    for (int s = 1; s < last; ++s) {
+        f2 acc[NR][2];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) acc[i][0] = next[i][0], acc[i][1] = next[i][1];
+        if (s + 1 < last) {
             fetch(s + 1);
+            load_b(s + 2);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
         } else {
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         __syncthreads();
         const float *m = reinterpret_cast<const float *>(smem + (s & 1) * M::MAP) + n * M::LD;
-        const float *x = X + ((s - 1) & 1) * (D * 32) + c;
-        float *out = p.segs + seg_slab(p, u, s + 1, D * D) + (size_t)n * D + part * 32 + c;
-        unsigned long long acc[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(out + i * D + 4 * j);
-                acc[i][2 * j] = v.x, acc[i][2 * j + 1] = v.y;
-            }
+        const float *x = X + ((s - 1) & 1) * (D * W) + c;
 #pragma unroll 4
         for (int k = 0; k < D; k += 4) {
-            const float4 a0 = *reinterpret_cast<const float4 *>(m + k), a1 = *reinterpret_cast<const float4 *>(m + M::LD + k);
-            const float w0[4] = {a0.x, a0.y, a0.z, a0.w}, w1[4] = {a1.x, a1.y, a1.z, a1.w};
+            float w[NR][4];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const float4 a = *reinterpret_cast<const float4 *>(m + i * M::LD + k);
+                w[i][0] = a.x, w[i][1] = a.y, w[i][2] = a.z, w[i][3] = a.w;
+            }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                const ulonglong2 x0 = *reinterpret_cast<const ulonglong2 *>(x + (k + kk) * 32);
-                const ulonglong2 x1 = *reinterpret_cast<const ulonglong2 *>(x + (k + kk) * 32 + 4);
-                const unsigned long long xv[4] = {x0.x, x0.y, x1.x, x1.y};
-                const unsigned long long p0 = f2_pack(w0[kk], w0[kk]), p1 = f2_pack(w1[kk], w1[kk]);
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(x + (k + kk) * W);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[0][j] = f2_fma(p0, xv[j], acc[0][j]), acc[1][j] = f2_fma(p1, xv[j], acc[1][j]);
+                for (int i = 0; i < NR; ++i) {
+                    const f2 a = f2_pack(w[i][kk], w[i][kk]);
+                    acc[i][0] = f2_fma(a, v.x, acc[i][0]), acc[i][1] = f2_fma(a, v.y, acc[i][1]);
+                }
             }
         }
-        float *next = X + (s & 1) * (D * 32) + c;
+        float *y = X + (s & 1) * (D * W) + c;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const ulonglong2 v = make_ulonglong2(acc[i][2 * j], acc[i][2 * j + 1]);
-                *reinterpret_cast<ulonglong2 *>(out + i * D + 4 * j) = v;
-                *reinterpret_cast<ulonglong2 *>(next + (n + i) * 32 + 4 * j) = v;
-            }
+        for (int i = 0; i < NR; ++i) {
+            const ulonglong2 v = make_ulonglong2(acc[i][0], acc[i][1]);
+            *reinterpret_cast<ulonglong2 *>(slab(s + 1) + i * D) = v;
+            *reinterpret_cast<ulonglong2 *>(y + (n + i) * W) = v;
+        }
         __syncthreads();  // the next columns are complete, and this map's place is free
     }
+}
+
+template <int D, int W>
+cudaError_t combine_launch(const PrefillParams &p, cudaStream_t s) {
+    static SmemGrants grants;
+    const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&combine_kernel<D, W>), CombineSmem<D, W>::BYTES, grants);
+    if (e != cudaSuccess) return e;
+    combine_kernel<D, W><<<p.R * p.H * (D / W), 2 * D, CombineSmem<D, W>::BYTES, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <int D, int NW, bool OUT>
@@ -1045,11 +1066,10 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t s) {
     if (p.nseg > 1) {
         e = scans<D, false>(p, s);
         if (e != cudaSuccess) return e;
-        static SmemGrants combine_grants;
-        e = grant_smem(reinterpret_cast<const void *>(&combine_kernel<D>), CombineSmem<D>::BYTES, combine_grants);
-        if (e != cudaSuccess) return e;
-        combine_kernel<D><<<p.R * p.H * (D / 32), 2 * D, CombineSmem<D>::BYTES, s>>>(p);
-        e = cudaGetLastError();
+        // the narrowest columns that still run in one wave of a CTA an SM (32 heads of 128,
+        // 9 segments: 50 us at 32 columns, 63 at 16 in two waves)
+        const int slabs = p.R * p.H * D;
+        e = slabs / 8 <= 152 ? combine_launch<D, 8>(p, s) : slabs / 16 <= 152 ? combine_launch<D, 16>(p, s) : combine_launch<D, 32>(p, s);
         if (e != cudaSuccess) return e;
     }
     return scans<D, true>(p, s);
