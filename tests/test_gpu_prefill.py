@@ -548,3 +548,72 @@ def test_gdn_offsets_past_32_bits():
     y = c.layer.prefill(c.rg, c.q, c.k, c.v, c.alpha, c.beta, max_len=T, rows=c.rows, start=start, pool=c.pool)
     c.pool0, c.pool, c.start, c.y = small, small, [0, 1], y
     c.check()
+
+
+def test_gdn_scratch_needs_no_clearing():
+    """Whatever the workspace held before, also where segments are joined."""
+    for lengths in ([200, 64, 13], [3000]):
+        outs = []
+        for fill in (0, 255):
+            c = Case(lengths, 2, 1, 128, seed=1)
+            work = c.layer.prefill_workspace(c.rg, max(lengths))
+            work.fill_(fill)
+            c.run([-1] * len(lengths), work=work)
+            outs.append((c.y, c.state().clone()))
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("R,H,n", [(20, 16, 150), (10, 32, 20), (80, 32, 40)])
+def test_gdn_many_chains_back_to_back(R, H, n):
+    """Enough chains for the scan to start before the launch ahead of it ends, with short requests among
+    them, called twice in a row and from a graph, results read by the next kernel on the stream."""
+    rng = np.random.default_rng(R)
+    lengths = [int(x) for x in rng.integers(0, n, R)]
+    lengths[0] = 1
+    c = Case(lengths, H, H // 2, 64 if R == 10 else 128, seed=R)
+    start = [-1] * R
+    c.run(start)
+    first = (c.y.clone(), c.state().clone())
+    c.check()
+    work = c.layer.prefill_workspace(c.rg, n)
+    st, y = dev(np.array(start, np.int32)), torch.empty_like(c.y)
+    call = lambda: c.layer.prefill(c.rg, c.q, c.k, c.v, c.alpha, c.beta, max_len=n, rows=c.rows, start=st, pool=c.pool, y=y, work=work)
+    call()
+    call()
+    assert torch.equal(y, first[0]) and torch.equal(c.state(), first[1])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+        twice = y + y
+    y.zero_()
+    c.layer.ckpt_hp.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for r, m in enumerate(lengths):
+        if m:
+            assert torch.equal(c.state()[int(c.rows[r])], first[1][int(c.rows[r])])
+    assert torch.equal(y, first[0]) and torch.equal(twice, first[0] + first[0])
+
+
+def test_gdn_only_short_requests_where_long_ones_may_come():
+    """max_len allows chunks, no request has one: the recurrence alone, seen by the next kernel."""
+    c = Case([1, 3, 12, 0, 7] * 20, 16, 8, 128, seed=2)
+    y = c.run(max_len=500)
+    twice = y + y
+    torch.cuda.synchronize()
+    c.check()
+    assert torch.equal(twice, c.y + c.y)
+
+
+def test_example_runs():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "prefill_decode.py")
+    spec = importlib.util.spec_from_file_location("prefill_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    out = m.main()
+    assert out["taken"] == 2 + 0 + 5 + 1
+    assert out["prefix"] <= 2 * TOL_S       # two states within the tolerance of the same one
+    assert out["step"] <= TOL_Y + 2e-3      # a bf16 row against decode's fp32 one
