@@ -15,12 +15,9 @@
 namespace rs {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kItems = 4;                 // requests of one thread in one scan pass
-constexpr int kPass = kThreads * kItems;  // requests of one scan pass
-constexpr int kSmallReqs = 4000;          // requests of the one-launch form: three offset arrays in 48 KiB
-static_assert(kSmallReqs <= kPass, "the one-launch form scans in one pass");
-constexpr long long kMaxEnd = 1ll << 30;       // a request's largest position
+constexpr int kItems = 4;         // requests of one thread in one scan pass
+constexpr int kSmallReqs = 4000;  // requests of the one-launch form: three offset arrays in 48 KiB
+constexpr long long kMaxEnd = 1ll << 30;  // a request's largest position
 
 struct PlanParams {
     int R, cap, ccap, block, max_blocks, n_free;
@@ -30,6 +27,7 @@ struct PlanParams {
 };
 
 // Inclusive sum over the CTA of two values per thread; totals to all threads.
+template <int NT>
 __device__ __forceinline__ void cta_scan2(long long &a, long long &b, long long *warp_a, long long *warp_b,
                                           long long &tot_a, long long &tot_b) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -40,19 +38,16 @@ __device__ __forceinline__ void cta_scan2(long long &a, long long &b, long long 
     }
     if (lane == 31) warp_a[warp] = a, warp_b[warp] = b;
     __syncthreads();
-    if (warp == 0) {
-        long long x = warp_a[lane], y = warp_b[lane];
+    // every warp sums the warps' totals for itself
+    long long x = lane < NT / 32 ? warp_a[lane] : 0, y = lane < NT / 32 ? warp_b[lane] : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(~0u, x, o), v = __shfl_up_sync(~0u, y, o);
-            if (lane >= o) x += u, y += v;
-        }
-        warp_a[lane] = x, warp_b[lane] = y;
+    for (int o = 1; o < NT / 32; o <<= 1) {
+        const long long u = __shfl_up_sync(~0u, x, o), v = __shfl_up_sync(~0u, y, o);
+        if (lane >= o) x += u, y += v;
     }
-    __syncthreads();
-    if (warp > 0) a += warp_a[warp - 1], b += warp_b[warp - 1];
-    tot_a = warp_a[31], tot_b = warp_b[31];
-    __syncthreads();
+    tot_a = __shfl_sync(~0u, x, NT / 32 - 1), tot_b = __shfl_sync(~0u, y, NT / 32 - 1);
+    const long long pa = __shfl_sync(~0u, x, warp ? warp - 1 : 0), pb = __shfl_sync(~0u, y, warp ? warp - 1 : 0);
+    if (warp > 0) a += pa, b += pb;
 }
 
 struct Totals {
@@ -61,57 +56,83 @@ struct Totals {
     int chunks, blocks, active;
 };
 
-// Sums kPass requests starting at r0 and writes the offsets of each to
+// Sums NT * kItems requests starting at r0 and writes the offsets of each to
 // tok, chk, blk (at [r - r0 + 1] past the base; entry 0 is the caller's).
-// t carries the totals from pass to pass.
+// t carries the totals from pass to pass.  Rows, chunks and blocks are summed
+// together as if every request fitted into the capacity; only where the rows'
+// total says otherwise are the latter two summed again without those that do not.
+template <int NT>
 __device__ __forceinline__ void scan_pass(const PlanParams &p, int r0, Totals &t, int *tok, int *chk, int *blk,
                                           long long *wa, long long *wb, int *red, bool report) {
     int n[kItems], c[kItems];
     bool bad = false;
     const int first = r0 + threadIdx.x * kItems;
-    long long sum = 0, zero = 0;
+    long long rows = 0, packed = 0;
+    long long mine[kItems];
+    int active = 0;
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const int r = first + i;
         n[i] = r < p.R ? p.lengths[r] : 0;
         c[i] = r < p.R && p.context ? p.context[r] : 0;
+    }
+    auto chunks_blocks = [&](int i) {
+        const int chunks = n[i] ? (c[i] + n[i] + RS_CHUNK - 1) / RS_CHUNK - c[i] / RS_CHUNK : 0;
+        const int blocks = p.block && n[i] ? (c[i] + n[i]) / p.block - c[i] / p.block : 0;
+        return (long long)blocks << 32 | chunks;
+    };
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
         if (n[i] < 0 || c[i] < 0 || (long long)n[i] + c[i] > kMaxEnd) {
             bad = true;
             n[i] = c[i] = 0;
         }
-        sum += n[i];
-    }
-    long long at = sum, tot, dummy;
-    cta_scan2(at, zero, wa, wb, tot, dummy);
-    at += t.rows - sum;  // raw rows before this thread's requests
-    // a request fits if its end does; the rest are planned without rows
-    int end[kItems], active = 0, fit = 0;
-    long long packed = 0, mine[kItems];
-    bool over = false;
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        at += n[i];
-        if (at > p.cap) {
-            over = over || n[i] > 0;
-            n[i] = 0;
-        } else {
-            fit = (int)at;
-        }
-        end[i] = (int)(at > p.cap ? -1 : at);
-        active += n[i] > 0;
-        const int chunks = n[i] ? (c[i] + n[i] + RS_CHUNK - 1) / RS_CHUNK - c[i] / RS_CHUNK : 0;
-        const int blocks = p.block && n[i] ? (c[i] + n[i]) / p.block - c[i] / p.block : 0;
-        packed += (long long)blocks << 32 | chunks;
+        rows += n[i];
+        packed += chunks_blocks(i);
         mine[i] = packed;
+        active += n[i] > 0;
     }
-    long long pre = packed, act = active, tot_p, tot_a;
-    cta_scan2(pre, act, wa, wb, tot_p, tot_a);
+    long long at = rows, pre = packed, tot, tot_p;
+    cta_scan2<NT>(at, pre, wa, wb, tot, tot_p);
+    at += t.rows - rows;  // raw rows before this thread's requests
     pre -= packed;
-    // rows that fit: the largest fitting end so far
-    const int f = __reduce_max_sync(~0u, fit);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = f;
-    __syncthreads();
-    const int all = max(t.fit, __reduce_max_sync(~0u, red[threadIdx.x & 31]));
+    int end[kItems], all;
+    bool over = false;
+    if (t.rows + tot <= p.cap) {
+        all = (int)(t.rows + tot);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            at += n[i];
+            end[i] = (int)at;
+        }
+    } else {
+        // a request fits if its end does; the rest are planned without rows
+        int fit = 0;
+        packed = 0, active = 0;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            at += n[i];
+            if (at > p.cap) {
+                over = over || n[i] > 0;
+                n[i] = 0;
+                end[i] = -1;
+            } else {
+                end[i] = fit = (int)at;
+            }
+            active += n[i] > 0;
+            packed += chunks_blocks(i);
+            mine[i] = packed;
+        }
+        // rows that fit: the largest fitting end so far
+        const int f = __reduce_max_sync(~0u, fit);
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = f;
+        __syncthreads();
+        all = max(t.fit, __reduce_max_sync(~0u, red[threadIdx.x & (NT / 32 - 1)]));
+        pre = packed;
+        long long zero = 0, none;
+        cta_scan2<NT>(pre, zero, wa, wb, tot_p, none);
+        pre -= packed;
+    }
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         if (first + i >= p.R) continue;
@@ -126,7 +147,11 @@ __device__ __forceinline__ void scan_pass(const PlanParams &p, int r0, Totals &t
     t.fit = all;
     t.chunks += (int)(tot_p & 0xffffffffll);
     t.blocks += (int)(tot_p >> 32);
-    t.active += (int)tot_a;
+    __syncthreads();  // the scratch is free
+    const int warp_active = __reduce_add_sync(~0u, active);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = warp_active;
+    __syncthreads();
+    t.active += __reduce_add_sync(~0u, (threadIdx.x & 31) < NT / 32 ? red[threadIdx.x & 31] : 0);
     __syncthreads();
 }
 
@@ -141,10 +166,11 @@ __device__ __forceinline__ int find(const int *cu, int R, int x) {
 }
 
 // Fills rows, chunks and blocks, CTA `cta` of `ctas`.
+template <int NT>
 __device__ __forceinline__ void fill(const PlanParams &p, const int *tok, const int *chk, const int *blk, int cta,
                                      int ctas) {
     const int rows = tok[p.R], chunks = chk[p.R], blocks = blk[p.R];
-    const long long stride = (long long)ctas * kThreads, me = (long long)cta * kThreads + threadIdx.x;
+    const long long stride = (long long)ctas * NT, me = (long long)cta * NT + threadIdx.x;
     // four rows a thread: one search, then steps to the next request
     for (long long i = me; i * 4 < p.cap; i += stride) {
         const int x0 = (int)(i * 4);
@@ -199,38 +225,40 @@ __device__ __forceinline__ void write_counts(const PlanParams &p, const Totals &
     p.rg.counts[0] = t.fit, p.rg.counts[1] = t.chunks, p.rg.counts[2] = t.blocks, p.rg.counts[3] = t.active;
 }
 
-__global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ PlanParams p) {
-    __shared__ int tok[kSmallReqs + 1], chk[kSmallReqs + 1], blk[kSmallReqs + 1];
+template <int NT>
+__global__ void __launch_bounds__(NT) plan_kernel(const __grid_constant__ PlanParams p) {
+    constexpr int MAX = NT * kItems < kSmallReqs ? NT * kItems : kSmallReqs;
+    __shared__ int tok[MAX + 1], chk[MAX + 1], blk[MAX + 1];
     __shared__ long long wa[32], wb[32];
     __shared__ int red[32];
     if (threadIdx.x == 0) tok[0] = chk[0] = blk[0] = 0;
     Totals t = {};
-    scan_pass(p, 0, t, tok, chk, blk, wa, wb, red, blockIdx.x == 0);
+    scan_pass<NT>(p, 0, t, tok, chk, blk, wa, wb, red, blockIdx.x == 0);
     if (blockIdx.x == 0) {
-        for (int r = threadIdx.x; r < p.R; r += kThreads) {
+        for (int r = threadIdx.x; r < p.R; r += NT) {
             p.rg.cu_tokens[r + 1] = tok[r + 1];
             p.rg.cu_chunks[r + 1] = chk[r + 1];
             p.rg.cu_blocks[r + 1] = blk[r + 1];
         }
         if (threadIdx.x == 0) write_counts(p, t);
     }
-    fill(p, tok, chk, blk, blockIdx.x, gridDim.x);
+    fill<NT>(p, tok, chk, blk, blockIdx.x, gridDim.x);
 }
 
-__global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ PlanParams p) {
+constexpr int kScanThreads = 1024;
+__global__ void __launch_bounds__(kScanThreads) scan_kernel(const __grid_constant__ PlanParams p) {
     __shared__ long long wa[32], wb[32];
     __shared__ int red[32];
     Totals t = {};
-    for (int r0 = 0; r0 < p.R; r0 += kPass)
-        scan_pass(p, r0, t, p.rg.cu_tokens + r0, p.rg.cu_chunks + r0, p.rg.cu_blocks + r0, wa, wb, red, true);
+    for (int r0 = 0; r0 < p.R; r0 += kScanThreads * kItems)
+        scan_pass<kScanThreads>(p, r0, t, p.rg.cu_tokens + r0, p.rg.cu_chunks + r0, p.rg.cu_blocks + r0, wa, wb, red, true);
     if (threadIdx.x == 0) write_counts(p, t);
 }
 
-// A request planned without rows although its raw offset passed the capacity
-// keeps the offset of the rows that fit; scan_kernel writes that offset per
-// pass, so all later ones already carry it.
-__global__ void __launch_bounds__(kThreads) fill_kernel(const __grid_constant__ PlanParams p) {
-    fill(p, p.rg.cu_tokens, p.rg.cu_chunks, p.rg.cu_blocks, blockIdx.x, gridDim.x);
+// Requests planned without rows share the offset of the rows that fit: the pass
+// in which the capacity ran out and all later ones write it.
+__global__ void __launch_bounds__(kScanThreads) fill_kernel(const __grid_constant__ PlanParams p) {
+    fill<kScanThreads>(p, p.rg.cu_tokens, p.rg.cu_chunks, p.rg.cu_blocks, blockIdx.x, gridDim.x);
 }
 
 }  // namespace
@@ -239,18 +267,25 @@ cudaError_t ragged_plan_launch(const rs_ragged_desc &rd, const int32_t *lengths,
                                const int32_t *free_blocks, const rs_ragged &rg, uint32_t *status, cudaStream_t s) {
     PlanParams p = {rd.R, rd.tokens_cap, ragged_chunks_cap(rd), rd.block, rd.max_blocks, rd.n_free,
                     lengths, context, free_blocks, rg, status};
-    // a CTA for every 1024 groups of four rows and 1024 chunks, at most one per SM
+    // a thread for every four rows and every chunk, at most an SM's worth of CTAs an SM;
+    // small CTAs where the requests allow, whose barriers are cheaper
     const long long items = ((long long)p.cap + 3) / 4 + p.ccap;
-    int ctas = (int)((items + kThreads - 1) / kThreads);
-    if (ctas > 152) ctas = 152;
-    if (rd.R <= kSmallReqs) {
-        plan_kernel<<<ctas, kThreads, 0, s>>>(p);
+    auto ctas = [&](int nt, int most) {
+        const long long n = (items + nt - 1) / nt;
+        return (int)(n < most ? n : most);
+    };
+    if (rd.R <= 256 * kItems) {
+        plan_kernel<256><<<ctas(256, 152 * 4), 256, 0, s>>>(p);
         return cudaGetLastError();
     }
-    scan_kernel<<<1, kThreads, 0, s>>>(p);
+    if (rd.R <= kSmallReqs) {
+        plan_kernel<1024><<<ctas(1024, 152), 1024, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    scan_kernel<<<1, kScanThreads, 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    fill_kernel<<<ctas, kThreads, 0, s>>>(p);
+    fill_kernel<<<ctas(kScanThreads, 152), kScanThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 

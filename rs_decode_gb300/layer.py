@@ -26,12 +26,13 @@ def to_device(d: dict, device="cuda", non_blocking: bool = False) -> dict:
 
 def packed_stride(t: torch.Tensor, rows: int, heads: int, d: int, name: str) -> int:
     """Row stride in elements of a packed [rows, heads, d] bf16 tensor whose heads lie side by side."""
-    if t.dim() != 3 or t.size(0) < rows or t.size(1) != heads or t.size(2) != d or t.element_size() != 2:
-        raise ValueError(f"{name} must be bf16 [{rows}, {heads}, {d}], got {t.dtype} {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or shape[0] < rows or t.element_size() != 2:
+        raise ValueError(f"{name} must be bf16 [{rows}, {heads}, {d}], got {t.dtype} {tuple(shape)}")
     ld, head, one = t.stride()
-    if one != 1 or (heads > 1 and head != d):
+    if one != 1 or (head != d and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return ld if t.size(0) > 1 else heads * d
+    return ld if shape[0] > 1 else heads * d
 
 
 class Layer:
@@ -140,7 +141,8 @@ class Layer:
         T, R, H, G, N, P = rd.tokens_cap, rd.R, self.H, self.G, self.N, self.P
         ld_q, ld_k, ld_v = packed_stride(q, T, G, N, "q"), packed_stride(k, T, G, N, "k"), packed_stride(v, T, H, P, "v")
         for t, name in ((alpha, "alpha"), (beta, "beta")):
-            if t.dtype is not torch.float32 or t.dim() != 2 or t.size(0) < T or t.size(1) != H:
+            shape = t.shape
+            if t.dtype is not torch.float32 or len(shape) != 2 or shape[0] < T or shape[1] != H:
                 raise ValueError(f"{name} must be float32 [{T}, {H}], got {t.dtype} {tuple(t.shape)}")
         for t, name in ((rows, "rows"), (start, "start")):
             if t is not None and (t.dtype is not torch.int32 or t.shape != (R,)):
@@ -153,7 +155,7 @@ class Layer:
                 raise ValueError(f"pool must be [n, {H}, {N}, {P}] of {width}-byte values")
         if y is None:
             y = torch.empty((T, H, P), dtype=torch.bfloat16, device=self.base.device)
-        elif y.element_size() != 2 or y.dim() != 3 or y.size(0) < T or y.size(1) != H or y.size(2) != P:
+        elif y.element_size() != 2 or y.shape[1:] != (H, P) or y.shape[0] < T:
             raise ValueError(f"y must be bf16 [{T}, {H}, {P}]")
         if work is None:
             work = self.prefill_workspace(ragged, max_len)

@@ -54,6 +54,12 @@ class Ragged:
         return bits
 
 
+def _empty(like: torch.Tensor, shape: tuple) -> torch.Tensor:
+    if like.dtype is torch.bfloat16:
+        return like.new_empty(shape)
+    return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+
+
 def qk_norm(q: torch.Tensor | None, k: torch.Tensor | None, *, norm: str = "l2", eps: float = 1e-6,
             wq: torch.Tensor | None = None, wk: torch.Tensor | None = None, weight_offset: float = 0.0,
             scale_q: float = 1.0, scale_k: float = 1.0, positions: torch.Tensor | None = None,
@@ -67,9 +73,10 @@ def qk_norm(q: torch.Tensor | None, k: torch.Tensor | None, *, norm: str = "l2",
     if kind is None:
         raise ValueError(f"unknown norm {norm!r}")
     one = q if q is not None else k
-    if one is None or one.dim() != 3:
+    shape = one.shape if one is not None else ()
+    if len(shape) != 3:
         raise ValueError("q or k must be a [T, heads, D] tensor")
-    T, D = one.size(0), one.size(2)
+    T, _, D = shape
     rot = 0
     if inv_freq is not None:
         if positions is None:
@@ -86,19 +93,19 @@ def qk_norm(q: torch.Tensor | None, k: torch.Tensor | None, *, norm: str = "l2",
     Hq = Hk = ld_q = ld_k = ld_qo = ld_ko = 0
     pq = pk = pqo = pko = None
     if q is not None:
-        Hq = q.size(1)
+        Hq = shape[1]
         ld_q = packed_stride(q, T, Hq, D, "q")
         if qo is None:
-            qo = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            qo = _empty(q, (T, Hq, D))
             ld_qo = Hq * D
         else:
             ld_qo = packed_stride(qo, T, Hq, D, "out[0]")
         pq, pqo = q.data_ptr(), qo.data_ptr()
     if k is not None:
-        Hk = k.size(1)
+        Hk = k.shape[1]
         ld_k = packed_stride(k, T, Hk, D, "k")
         if ko is None:
-            ko = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=k.device)
+            ko = _empty(k, (T, Hk, D))
             ld_ko = Hk * D
         else:
             ld_ko = packed_stride(ko, T, Hk, D, "out[1]")
