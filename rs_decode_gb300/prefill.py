@@ -56,7 +56,7 @@ class Ragged:
 
 def _empty(like: torch.Tensor, shape: tuple) -> torch.Tensor:
     if like.dtype is torch.bfloat16:
-        return like.new_empty(shape)
+        return torch.empty_like(like)  # contiguous: like's heads lie side by side
     return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
 
 
