@@ -316,8 +316,8 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
     const int vt = threadIdx.x >> 4, vc = threadIdx.x & 15;  // V: row vt + 16 j, 16-byte piece vc
     const uint16_t *vsrc = p.v + ((long long)rq.row0 + vt) * p.ld_v + h * D + vc * 8;
     auto load_v = [&](int i) {
-        if (i < nch) {
-            const int n = u.map ? 0 : w.rows(u.c0 + i);
+        if (i < nch && !u.map) {
+            const int n = w.rows(u.c0 + i);
             const uint16_t *src = vsrc + (long long)w.first(u.c0 + i) * p.ld_v;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -414,8 +414,11 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         }
         // V's column, while X is computed
         uint32_t v[CH / 2];
-        float vmax;
-        {
+        float vmax = 0.f;
+        if (u.map) {
+#pragma unroll
+            for (int t = 0; t < CH / 2; ++t) v[t] = 0;
+        } else {
             __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
             const uint16_t *src = reinterpret_cast<const uint16_t *>(smem + Smem::V) + hf * CH * D + row;
 #pragma unroll
@@ -425,9 +428,8 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
                 const uint32_t mag = v[t / 2] & 0x7fff7fffu;
                 m2 = __hmax2(m2, *reinterpret_cast<const __nv_bfloat162 *>(&mag));
             }
-            vmax = fmaxf(__low2float(m2), __high2float(m2));
+            vmax = pair_max(rowmax + 2 * D, hf, row, warp, fmaxf(__low2float(m2), __high2float(m2)));
         }
-        vmax = pair_max(rowmax + 2 * D, hf, row, warp, vmax);
         if (OUT && warp == 4) {  // Z, behind X
             ok = wait_warp(&b->full_q, ph, b, p.status) && ok;
             tc_fence_after_sync();
