@@ -13,11 +13,19 @@
 //
 // T = (I + A)^-1 diag(beta) and P do not depend on the state, so
 //   chunk_cta     computes them for all chunks and heads at once, and
-//   scan_kernel   carries S through a request's chunks.
-// (Segments, rs_prefill.cuh, cut a long request's chunks where few chains would
-// leave the GPU idle.)
-// Requests of at most kShort rows go through step_cta instead, which runs
-// the recurrence row by row beside one read and one write of the state.
+//   the scans     carry S through a request's chunks: 128-wide heads on the
+//                 tcgen05 tensor cores (rs_prefill_tc.cu), 64-wide ones here.
+// Where few chains would leave the GPU idle, a request's chunks are cut into
+// segments (rs_prefill.cuh).  Requests of at most kShort rows go through step_cta
+// instead, which runs the recurrence row by row beside one read and one write of
+// the state.
+//
+// Measured on a GB300 with 32 value and 16 key heads of 128 (copy peak 6.78 TB/s):
+// 256 cached requests of one row 167 us (6.45 TB/s, the states' bytes); 16 prompts
+// of 26,458 rows 504 us (chunk matrices 183, scan 312); one request of 32,768 rows
+// 1033 us (chunk matrices 222, states and maps of 9 segments 415, joining them 50,
+// scan 347).  The latter two are bound by the scan's chains, not by their 0.8 GB.
+//
 // Decays enter as differences G_i - G_j only, so nothing overflows however
 // long a chunk's decay is; alpha = 0 is a decay of 2^-160, which is 0 in fp32.
 //
@@ -106,6 +114,9 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
 // 64 rows would be one dependent chain of 2016 steps; the products run on the
 // tensor cores with operands split to 22 bits, since every u of the chunk
 // inherits T's accuracy.
+// 26,458 rows of 32 value and 16 key heads: 183 us at four CTAs an SM, half of the
+// issue slots used: what bounds it is the latency of shared memory and of the
+// barriers between its short phases (five CTAs an SM, at 96 registers, run as long).
 constexpr int kChunkThreads = 128;
 constexpr int LDM = C + 8;  // fp32 matrices in shared memory: 16-byte rows, banks shifted by 8
 constexpr int kMat = C * LDM;
@@ -512,7 +523,9 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 // registers, so that the state is read and written once, in 64-byte segments
 // with 8 KiB in flight per warp, and no warp waits for another.  One row's
 // S k, S q and k.q are summed over the lanes together; S_new q follows as
-// alpha S q + (k.q) u.  Bound by the state's bytes up to about a dozen rows.
+// alpha S q + (k.q) u.  256 cached requests of 32 heads of 128: 167 us for one row,
+// 0.95 of the copy peak in the states' bytes, and 28 us more for each further row,
+// which is issue time.
 constexpr int kStepThreads = 128;
 
 template <int D>
@@ -525,7 +538,7 @@ __device__ __forceinline__ void step_cta(const PrefillParams &p, int cta) {
     const int part = cta % kStepSplit<D>, hr = cta / kStepSplit<D>;
     const int h = hr % p.H, r = hr / p.H;
     const bool lead = h == 0 && part == 0 && threadIdx.x == 0;
-    // longer requests are scan_kernel's, where it runs at all
+    // longer requests are the scan's, where it runs at all
     if (p.max_len > kShort && p.rg.cu_tokens[r + 1] - p.rg.cu_tokens[r] > kShort) return;
     const Request rq = load_request(p, r, lead);
     if (!rq.ok) return;
@@ -659,8 +672,10 @@ __global__ void __launch_bounds__(kChunkThreads, 4) front_kernel(const __grid_co
 //   S^T K^T, S^T Q^T  ->  R^T  ->  u^T = R^T T^T  ->  y^T += u^T P^T,  S^T += u^T K
 // pass from product to product without leaving the registers or meeting
 // another warp.  K, Q, T, P and V come through two shared-memory stages.
-// Operands that enter the state (S, R, T, u) are split in two bf16 terms; k, q
-// and v are bf16 inputs and exact.
+// It serves 64-wide heads, whose 64 rows would fill half of a tcgen05 product.
+// 24 requests with 2,419 rows in all, 8 heads of 64: 57 us, 2.3 us a chunk of the longest
+// chain; the warp's own products (240 of m16n8k16 a chunk, 8 clocks each) are about
+// half of that.
 template <int D, int NW>
 struct ScanSmem {
     static constexpr int TILE = C * D * 2;
@@ -931,7 +946,8 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
 // value columns one CTA, which keeps S_s's columns in shared memory while the
 // next M_s and B_s are on their way.  fp32 throughout.  A step reads a 64 KiB
 // map for few columns: narrow CTAs shorten the step, wide ones read the map
-// less often.
+// less often.  8 heads of 128, 31 segments: 8 columns a CTA took the whole call from
+// 326 us (32 columns) to 243.
 template <int D, int W>
 struct CombineSmem {
     static constexpr int LD = D + 4;
