@@ -18,6 +18,11 @@
 // 2^-25 of the angle (0.004 radians at position 100,000).  The reduced angle,
 // within half a turn, is what the fast sine and cosine are accurate for (2^-20
 // absolute, against the 2^-9 of a bf16 result).
+//
+// Measured: 32,768 rows of 32 heads of 128 in 84 us, 6.36 TB/s, 0.94 of the copy
+// peak; 8,191 rows of 36 heads with weights and 64 rotated channels in 37 us,
+// 4.1 TB/s: there one wave and two thirds of warps, and the rotation's arithmetic
+// between a warp's loads, are what is left.
 #include "rs_common.cuh"
 #include "rs_internal.h"
 
