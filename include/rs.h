@@ -373,7 +373,7 @@ rs_status rs_decode_mamba2_noalloc(const rs_layer_desc *desc, const rs_state *st
 #define RS_CHUNK 64
 
 /* Shape of a ragged batch.  1 <= R <= 65535, 1 <= tokens_cap <= 2^30; block is
- * 0 (no state cache) or a multiple of RS_CHUNK; max_blocks >= 1 and
+ * 0 (no state cache) or a multiple of RS_CHUNK up to 2^29; max_blocks >= 1 and
  * R * max_blocks <= 2^30 when block > 0; n_free >= 0. */
 typedef struct {
     int32_t R;          /* requests                                             */
@@ -483,8 +483,9 @@ rs_status rs_prefill_bytes_for(const rs_layer_desc *desc, const rs_ragged_desc *
  * checkpoint must have no records or drafts buffered (rs_flush first;
  * RS_DEV_RECORDS otherwise).  The plan must come from rs_ragged_plan with the
  * same descriptor; block_table is read when rd->block > 0 and pool is given.
- * RS_GDN only.  work: device scratch of rs_prefill_bytes_for bytes, 128-byte
- * aligned.  States are accurate to fp32 rounding (operands of 22 bits, fp32 sums);
+ * RS_GDN only.  work: device scratch, 128-byte aligned, of the bytes that
+ * rs_prefill_bytes_for gives for the same descriptors and max_len; it need not
+ * be cleared, and a call leaves nothing in it that another one needs.  States are accurate to fp32 rounding (operands of 22 bits, fp32 sums);
  * y has fp16 operands beside fp32 sums and is rounded to bf16.  A NaN or an
  * infinity stays in its request; there it may reach any row of its own chunk
  * and all later ones.

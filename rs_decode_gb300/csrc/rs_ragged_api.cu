@@ -27,7 +27,7 @@ inline bool aligned(const void *p, size_t a) { return p && (reinterpret_cast<uin
 rs_status check_ragged(const rs_ragged_desc *rd) {
     if (!rd) return RS_ERR_INVALID_ARG;
     if (rd->R < 1 || rd->R > 65535 || rd->tokens_cap < 1 || rd->tokens_cap > kMaxRows) return RS_ERR_INVALID_ARG;
-    if (rd->block < 0 || rd->block % RS_CHUNK || rd->n_free < 0) return RS_ERR_INVALID_ARG;
+    if (rd->block < 0 || rd->block > kMaxRows / 2 || rd->block % RS_CHUNK || rd->n_free < 0) return RS_ERR_INVALID_ARG;
     if (rd->block && (rd->max_blocks < 1 || (int64_t)rd->R * rd->max_blocks > kMaxRows)) return RS_ERR_INVALID_ARG;
     return RS_OK;
 }

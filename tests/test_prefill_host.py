@@ -36,7 +36,7 @@ def addresses(cls, **kw):
     ({}, 0), (dict(R=0), INVALID), (dict(R=65536), INVALID), (dict(R=65535), 0), (dict(tokens_cap=0), INVALID),
     (dict(tokens_cap=(1 << 30) + 1), INVALID), (dict(block=100), INVALID), (dict(block=-64), INVALID),
     (dict(max_blocks=0), INVALID), (dict(max_blocks=1 << 29), INVALID), (dict(block=0, max_blocks=0), 0),
-    (dict(n_free=-1), INVALID), (dict(n_free=0), 0)])
+    (dict(n_free=-1), INVALID), (dict(n_free=0), 0), (dict(block=1 << 29), 0), (dict(block=(1 << 29) + 64), INVALID)])
 def test_ragged_descriptor(lib, kw, status):
     out = rb.RaggedBytes()
     assert lib.rs_ragged_bytes_for(ctypes.byref(ragged(**kw)), ctypes.byref(out)) == status
@@ -170,3 +170,13 @@ def test_qk_norm_refuses_bad_calls():
             qk_norm(x, None, **kw)
     with pytest.raises(ValueError):
         qk_norm(None, None)
+
+
+def test_host_tensors_are_refused():
+    """A pointer to host memory would be read on the device."""
+    from rs_decode_gb300.prefill import qk_norm
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        qk_norm(x, x)
+    with pytest.raises(ValueError, match="CUDA"):
+        qk_norm(None, x)
