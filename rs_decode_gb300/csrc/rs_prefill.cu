@@ -22,8 +22,8 @@
 //
 // Measured on a GB300 with 32 value and 16 key heads of 128 (copy peak 6.78 TB/s):
 // 256 cached requests of one row 167 us (6.45 TB/s, the states' bytes); 16 prompts
-// of 26,458 rows 504 us (chunk matrices 183, scan 312); one request of 32,768 rows
-// 1033 us (chunk matrices 222, states and maps of 9 segments 415, joining them 50,
+// of 26,458 rows 498 us (chunk matrices 178, scan 312); one request of 32,768 rows
+// 1025 us (chunk matrices 213, states and maps of 9 segments 425, joining them 39,
 // scan 347).  The latter two are bound by the scan's chains, not by their 0.8 GB.
 //
 // Decays enter as differences G_i - G_j only, so nothing overflows however
@@ -114,7 +114,7 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
 // 64 rows would be one dependent chain of 2016 steps; the products run on the
 // tensor cores with operands split to 22 bits, since every u of the chunk
 // inherits T's accuracy.
-// 26,458 rows of 32 value and 16 key heads: 183 us at four CTAs an SM, half of the
+// 26,458 rows of 32 value and 16 key heads: 178 us at four CTAs an SM, half of the
 // issue slots used: what bounds it is the latency of shared memory and of the
 // barriers between its short phases (five CTAs an SM, at 96 registers, run as long).
 constexpr int kChunkThreads = 128;
@@ -294,17 +294,20 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
                      : "memory");
     }
 
-    // rows 16 warp.. of K K^T and Q K^T, up to the diagonal
+    // Rows 16 rb.. of K K^T and Q K^T, up to the diagonal: up to four times the work
+    // for the last of them, so the rows go around the warps (and with them the
+    // schedulers) from CTA to CTA.
+    const int rb = (warp + cta) & 3;
     float kk[8][4] = {}, qk[8][4] = {};
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
         uint32_t a[4], b[4], w[4];
-        const int ar = warp * 16 + (lane & 15), ac = 2 * x + (lane >> 4);
+        const int ar = rb * 16 + (lane & 15), ac = 2 * x + (lane >> 4);
         ldsm4(a, sK + piece(ar, ac));
         ldsm4(b, sQ + piece(ar, ac));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (j <= warp) {
+            if (j <= rb) {
                 ldsm4(w, sK + piece(16 * j + (lane & 7) + ((lane & 16) >> 1), 2 * x + ((lane >> 3) & 1)));
                 mma_f16(kk[2 * j], a, w[0], w[1]);
                 mma_f16(kk[2 * j + 1], a, w[2], w[3]);
@@ -314,7 +317,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
         }
     }
     // keys' powers of two into K K^T
-    const int i0 = warp * 16 + (lane >> 2), j0 = (lane & 3) * 2;
+    const int i0 = rb * 16 + (lane >> 2), j0 = (lane & 3) * 2;
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
         const float2 s = *reinterpret_cast<const float2 *>(sk + nt * 8 + j0);
@@ -368,7 +371,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
                 const int j = nt * 8 + j0;
-                if (nt > 2 * warp + 1) {  // above the diagonal
+                if (nt > 2 * rb + 1) {  // above the diagonal
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         *reinterpret_cast<float2 *>(A + (i0 + 8 * hf) * LDM + j) = make_float2(0.f, 0.f);
@@ -386,7 +389,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
                     float p0, p1, a0, a1;
                     f2_unpack(f2_mul(d, f2_pack(qk[nt][2 * hf], qk[nt][2 * hf + 1])), p0, p1);
                     f2_unpack(f2_mul(f2_mul(d, bi[hf]), f2_pack(kk[nt][2 * hf], kk[nt][2 * hf + 1])), a0, a1);
-                    if (nt >= 2 * warp) {  // the diagonal's tiles
+                    if (nt >= 2 * rb) {  // the diagonal's tiles
                         if (j > i) p0 = 0.f;
                         if (j + 1 > i) p1 = 0.f;
                         if (j >= i) a0 = 0.f;
@@ -466,6 +469,16 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 #pragma unroll
                         for (int n = 0; n < 2; ++n) put_c(A + (32 + 16 * m) * LDM + 16 * w + 8 * n, lane, c[m][n], -1.f);
                 }
+                group_sync(grp);
+                // what waited above the diagonal goes
+                const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = t + 64 * i;
+                    *reinterpret_cast<float4 *>(A + (e >> 3) * LDM + 32 + (e & 7) * 4) = zero;
+                }
+                *reinterpret_cast<float4 *>(A + (t >> 2) * LDM + 16 + (t & 3) * 4) = zero;
+                *reinterpret_cast<float4 *>(A + (32 + (t >> 2)) * LDM + 48 + (t & 3) * 4) = zero;
             }
             group_sync(grp);
             // T = X diag(beta), each row scaled and split in two; 8 threads a row
@@ -487,16 +500,13 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 #pragma unroll
                 for (int x = 0; x < 4; ++x) f2_unpack(w[x], v[2 * x], v[2 * x + 1]);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    if (c * 8 + x > row) v[x] = 0.f;
-                    sum += fabsf(v[x]);
-                }
+                for (int x = 0; x < 8; ++x) sum += fabsf(v[x]);
 #pragma unroll
                 for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
                 row_scale<8>(sum, up, down);
                 uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) split2(v[2 * x] * up, v[2 * x + 1] * up, hi[x], lo[x]);
+                for (int x = 0; x < 4; ++x) split_cut(v[2 * x] * up, v[2 * x + 1] * up, hi[x], lo[x]);
                 *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(out.t_hi) + piece(row, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(out.t_lo) + piece(row, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 if (c == 0) out.su[row] = down * sk[row];

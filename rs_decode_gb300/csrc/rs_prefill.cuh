@@ -86,6 +86,16 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     const float2 h = unpack_h2(hi);
     lo = pack_h2(x - h.x, y - h.y);
 }
+// The same with hi cut instead of rounded, its difference taken by mixed-precision
+// subtraction: fewer instructions, 22 bits as well.
+__device__ __forceinline__ void split_cut(float x, float y, uint32_t &hi, uint32_t &lo) {
+    float c, d;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
+    asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; sub.f32.f16 %0, l, %3; sub.f32.f16 %1, h, %4;}"
+        : "=f"(c), "=f"(d)
+        : "r"(hi), "f"(x), "f"(y));
+    lo = pack_h2(-c, -d);
+}
 // Byte offset of 16-byte piece c (8 channels) of row r in 64-row tiles of 64 channels.
 __device__ __forceinline__ uint32_t piece(int r, int c) {
     return (uint32_t)((c >> 3) * (C * 128) + r * 128 + (((c ^ r) & 7) << 4));

@@ -173,11 +173,9 @@ __device__ __forceinline__ void put_split(uint32_t hi_addr, uint32_t lo_addr, co
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const f2 v = f2_mul(x[i], up);
-        float a, b, c, d;
+        float a, b;
         f2_unpack(v, a, b);
-        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi[i]) : "f"(b), "f"(a));
-        asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; sub.f32.f16 %0, l, %3; sub.f32.f16 %1, h, %4;}" : "=f"(c), "=f"(d) : "r"(hi[i]), "f"(a), "f"(b));
-        lo[i] = pack_h2(-c, -d);
+        split_cut(a, b, hi[i], lo[i]);
     }
     st8(hi_addr, hi);
     st8(lo_addr, lo);
