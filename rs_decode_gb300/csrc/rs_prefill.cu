@@ -22,8 +22,8 @@
 //
 // Measured on a GB300 with 32 value and 16 key heads of 128 (copy peak 6.78 TB/s):
 // 256 cached requests of one row 167 us (6.45 TB/s, the states' bytes); 16 prompts
-// of 26,458 rows 498 us (chunk matrices 178, scan 312); one request of 32,768 rows
-// 1025 us (chunk matrices 213, states and maps of 9 segments 425, joining them 39,
+// of 26,458 rows 489 us (chunk matrices 169, scan 312); one request of 32,768 rows
+// 1013 us (chunk matrices 202, states and maps of 9 segments 425, joining them 39,
 // scan 347).  The latter two are bound by the scan's chains, not by their 0.8 GB.
 //
 // Decays enter as differences G_i - G_j only, so nothing overflows however
@@ -114,11 +114,15 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
 // 64 rows would be one dependent chain of 2016 steps; the products run on the
 // tensor cores with operands split to 22 bits, since every u of the chunk
 // inherits T's accuracy.
-// 26,458 rows of 32 value and 16 key heads: 178 us at four CTAs an SM, half of the
-// issue slots used: what bounds it is the latency of shared memory and of the
-// barriers between its short phases (five CTAs an SM, at 96 registers, run as long).
+// 26,458 rows of 32 value and 16 key heads: 169 us at four CTAs an SM, half of the
+// issue slots and three fifths of shared memory's bandwidth used: what bounds it is
+// the latency of shared memory and of the barriers between its short phases (five CTAs an SM, at 96 registers, run as long).
 constexpr int kChunkThreads = 128;
-constexpr int LDM = C + 8;  // fp32 matrices in shared memory: 16-byte rows, banks shifted by 8
+// fp32 matrices in shared memory: 16-byte rows, banks shifted by 12.  Rows 0, 2, 4, 6
+// and rows 1, 3, 5, 7 then start 8 banks apart, so a fragment whose 8 rows are taken in
+// the order of row_of() and whose columns go in pairs meets no bank twice.
+constexpr int LDM = C + 12;
+__device__ __forceinline__ int row_of(int g) { return (g & 3) << 1 | (g >> 2 & 1); }
 constexpr int kMat = C * LDM;
 
 template <int D>
@@ -146,7 +150,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // hardware cuts likewise) and a product takes three terms: 22 bits, without a
 // scale, since tf32 has fp32's exponent.
 // mma.sync m16n8k8: lane = 4 g + t.  A: rows g, g+8, columns t, t+4; B: rows (k)
-// t, t+4, column g; C as above.
+// t, t+4, column g; C: rows g, g+8, columns 2t, 2t+1.  Row g holds row_of(g) here, and
+// t, t+4 hold the k of 2t, 2t+1, for A and B alike.
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     asm volatile(
         "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -163,13 +168,14 @@ __device__ __forceinline__ void cut(const float (&x)[N], uint32_t (&hi)[N], uint
 }
 // a, x: a block's first element, rows LDM apart
 __device__ __forceinline__ void frag_a(const float *a, int lane, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-    const float *p = a + (lane >> 2) * LDM + (lane & 3);
-    const float v[4] = {p[0], p[8 * LDM], p[4], p[8 * LDM + 4]};
+    const float *p = a + row_of(lane >> 2) * LDM + (lane & 3) * 2;
+    const float2 x = *reinterpret_cast<const float2 *>(p), y = *reinterpret_cast<const float2 *>(p + 8 * LDM);
+    const float v[4] = {x.x, y.x, x.y, y.y};
     cut(v, hi, lo);
 }
 __device__ __forceinline__ void frag_b(const float *x, int lane, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
-    const float *p = x + (lane & 3) * LDM + (lane >> 2);
-    const float v[2] = {p[0], p[4 * LDM]};
+    const float *p = x + (lane & 3) * 2 * LDM + (lane >> 2);
+    const float v[2] = {p[0], p[LDM]};
     cut(v, hi, lo);
 }
 __device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh)[2],
@@ -179,7 +185,7 @@ __device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&ah)[4], con
     mma_tf32(c, ah, bh);
 }
 __device__ __forceinline__ void put_c(float *out, int lane, const float (&c)[4], float sign) {
-    float *p = out + (lane >> 2) * LDM + (lane & 3) * 2;
+    float *p = out + row_of(lane >> 2) * LDM + (lane & 3) * 2;
     *reinterpret_cast<float2 *>(p) = make_float2(sign * c[0], sign * c[1]);
     *reinterpret_cast<float2 *>(p + 8 * LDM) = make_float2(sign * c[2], sign * c[3]);
 }
@@ -256,15 +262,16 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
     cp_async_wait_all();
     __syncthreads();
 
-    // bf16 -> fp16 in place, two threads a row: each row scaled to [1, 2)
+    // bf16 -> fp16 in place, two threads a row: each row scaled to [1, 2).  A thread's
+    // pieces go by four, so that eight threads meet eight places of a 128-byte row.
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-        const int row = tid >> 1, c0 = (tid & 1) * (D / 16);
+        const int row = tid >> 1, c0 = (tid & 1) * 4;
         uint4 v[D / 16];
         __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-            v[c] = *reinterpret_cast<const uint4 *>(smem + w * (C * D * 2) + piece(row, c0 + c));
+            v[c] = *reinterpret_cast<const uint4 *>(smem + w * (C * D * 2) + piece(row, c0 | (c & 3)) + (c >> 2) * (C * 128));
 #pragma unroll
             for (uint32_t x : {v[c].x, v[c].y, v[c].z, v[c].w}) {
                 const uint32_t mag = x & 0x7fff7fffu;
@@ -280,7 +287,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             auto half2 = [&](uint32_t x) {
                 return pack_h2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
             };
-            *reinterpret_cast<uint4 *>(smem + w * (C * D * 2) + piece(row, c0 + c)) =
+            *reinterpret_cast<uint4 *>(smem + w * (C * D * 2) + piece(row, c0 | (c & 3)) + (c >> 2) * (C * 128)) =
                 make_uint4(half2(v[c].x), half2(v[c].y), half2(v[c].z), half2(v[c].w));
         }
         if ((tid & 1) == 0) (w ? sq : sk)[row] = down;
@@ -302,7 +309,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
         uint32_t a[4], b[4], w[4];
-        const int ar = rb * 16 + (lane & 15), ac = 2 * x + (lane >> 4);
+        const int ar = rb * 16 + (lane & 8) + row_of(lane), ac = 2 * x + (lane >> 4);
         ldsm4(a, sK + piece(ar, ac));
         ldsm4(b, sQ + piece(ar, ac));
 #pragma unroll
@@ -317,7 +324,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
         }
     }
     // keys' powers of two into K K^T
-    const int i0 = rb * 16 + (lane >> 2), j0 = (lane & 3) * 2;
+    const int i0 = rb * 16 + row_of(lane >> 2), j0 = (lane & 3) * 2;
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
         const float2 s = *reinterpret_cast<const float2 *>(sk + nt * 8 + j0);
@@ -371,12 +378,9 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
                 const int j = nt * 8 + j0;
-                if (nt > 2 * rb + 1) {  // above the diagonal
+                if (nt > 2 * rb + 1) {  // above the diagonal's blocks, where A is not read
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        *reinterpret_cast<float2 *>(A + (i0 + 8 * hf) * LDM + j) = make_float2(0.f, 0.f);
-                        *reinterpret_cast<uint32_t *>(pout + piece(i0 + 8 * hf, nt) + (lane & 3) * 4) = 0;
-                    }
+                    for (int hf = 0; hf < 2; ++hf) *reinterpret_cast<uint32_t *>(pout + piece(i0 + 8 * hf, nt) + (lane & 3) * 4) = 0;
                     continue;
                 }
                 const f2 hj = *reinterpret_cast<const f2 *>(gh + j), lj = *reinterpret_cast<const f2 *>(gl + j);
@@ -469,32 +473,26 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 #pragma unroll
                         for (int n = 0; n < 2; ++n) put_c(A + (32 + 16 * m) * LDM + 16 * w + 8 * n, lane, c[m][n], -1.f);
                 }
-                group_sync(grp);
-                // what waited above the diagonal goes
-                const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = t + 64 * i;
-                    *reinterpret_cast<float4 *>(A + (e >> 3) * LDM + 32 + (e & 7) * 4) = zero;
-                }
-                *reinterpret_cast<float4 *>(A + (t >> 2) * LDM + 16 + (t & 3) * 4) = zero;
-                *reinterpret_cast<float4 *>(A + (32 + (t >> 2)) * LDM + 48 + (t & 3) * 4) = zero;
             }
             group_sync(grp);
-            // T = X diag(beta), each row scaled and split in two; 8 threads a row
+            // T = X diag(beta), each row scaled and split in two; 8 threads a row, and in
+            // every eight lanes halves of two rows, which lie on different banks
             Record &out = p.rec[(size_t)chunk * p.H + g * p.rep + r0 + grp];
             const float *be = vec + grp * 4 * C + 2 * C, *ke = be + C;
-            const int c = t & 7;
+            const int c = (t & 3) | (t >> 1 & 4), rl = (t >> 2 & 1) | (t >> 3 & 6);
             const ulonglong2 b0 = *reinterpret_cast<const ulonglong2 *>(be + c * 8), b1 = *reinterpret_cast<const ulonglong2 *>(be + c * 8 + 4);
             const unsigned long long bj[4] = {b0.x, b0.y, b1.x, b1.y};
             float um = 0.f, kmx = 0.f;
 #pragma unroll 2
             for (int i = 0; i < 8; ++i) {
-                const int row = i * 8 + (t >> 3);
+                const int row = i * 8 + rl;
                 // the row's sum of magnitudes sizes its scale and bounds what it can make of R
                 using f2 = unsigned long long;
-                const ulonglong2 v0 = *reinterpret_cast<const ulonglong2 *>(A + row * LDM + c * 8);
-                const ulonglong2 v1 = *reinterpret_cast<const ulonglong2 *>(A + row * LDM + c * 8 + 4);
+                ulonglong2 v0 = make_ulonglong2(0, 0), v1 = v0;
+                if (c / 2 <= i / 2) {  // right of the diagonal's block another block has waited
+                    v0 = *reinterpret_cast<const ulonglong2 *>(A + row * LDM + c * 8);
+                    v1 = *reinterpret_cast<const ulonglong2 *>(A + row * LDM + c * 8 + 4);
+                }
                 const f2 w[4] = {f2_mul(v0.x, bj[0]), f2_mul(v0.y, bj[1]), f2_mul(v1.x, bj[2]), f2_mul(v1.y, bj[3])};
                 float v[8], sum = 0.f, up, down;
 #pragma unroll
@@ -502,7 +500,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 #pragma unroll
                 for (int x = 0; x < 8; ++x) sum += fabsf(v[x]);
 #pragma unroll
-                for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                for (int o : {1, 2, 8}) sum += __shfl_xor_sync(~0u, sum, o);
                 row_scale<8>(sum, up, down);
                 uint32_t hi[4], lo[4];
 #pragma unroll
@@ -514,7 +512,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
                 kmx = fmaxf(kmx, sum * sk[row] * ke[row]);
             }
 #pragma unroll
-            for (int o = 8; o < 32; o <<= 1) um = fmaxf(um, __shfl_xor_sync(~0u, um, o)), kmx = fmaxf(kmx, __shfl_xor_sync(~0u, kmx, o));
+            for (int o : {4, 16}) um = fmaxf(um, __shfl_xor_sync(~0u, um, o)), kmx = fmaxf(kmx, __shfl_xor_sync(~0u, kmx, o));
             if (lane == 0) {
                 // non-negative floats compare as integers, so the order of the two warps does not matter
                 atomicMax(reinterpret_cast<int *>(bounds + 2 * grp), __float_as_int(um));
