@@ -22,8 +22,8 @@
 //
 // Measured on a GB300 with 32 value and 16 key heads of 128 (copy peak 6.78 TB/s):
 // 256 cached requests of one row 167 us (6.45 TB/s, the states' bytes); 16 prompts
-// of 26,458 rows 489 us (chunk matrices 169, scan 312); one request of 32,768 rows
-// 1013 us (chunk matrices 202, states and maps of 9 segments 425, joining them 39,
+// of 26,458 rows 485 us (chunk matrices 163, scan 312); one request of 32,768 rows
+// 1006 us (chunk matrices 197, states and maps of 9 segments 425, joining them 39,
 // scan 347).  The latter two are bound by the scan's chains, not by their 0.8 GB.
 //
 // Decays enter as differences G_i - G_j only, so nothing overflows however
@@ -114,9 +114,9 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
 // 64 rows would be one dependent chain of 2016 steps; the products run on the
 // tensor cores with operands split to 22 bits, since every u of the chunk
 // inherits T's accuracy.
-// 26,458 rows of 32 value and 16 key heads: 169 us at four CTAs an SM, half of the
+// 26,458 rows of 32 value and 16 key heads: 163 us at four CTAs an SM, half of the
 // issue slots and three fifths of shared memory's bandwidth used: what bounds it is
-// the latency of shared memory and of the barriers between its short phases (five CTAs an SM, at 96 registers, run as long).
+// the latency of shared memory and of the barriers between its short phases (five CTAs an SM, at 96 registers, take 171 us).
 constexpr int kChunkThreads = 128;
 // fp32 matrices in shared memory: 16-byte rows, banks shifted by 12.  Rows 0, 2, 4, 6
 // and rows 1, 3, 5, 7 then start 8 banks apart, so a fragment whose 8 rows are taken in
@@ -301,37 +301,46 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
                      : "memory");
     }
 
-    // Rows 16 rb.. of K K^T and Q K^T, up to the diagonal: up to four times the work
-    // for the last of them, so the rows go around the warps (and with them the
-    // schedulers) from CTA to CTA.
-    const int rb = (warp + cta) & 3;
-    float kk[8][4] = {}, qk[8][4] = {};
+    // K K^T and Q K^T in 16 x 16 tiles up to the diagonal, three or two a warp: rows 3,
+    // 2 and 1 of the tiles from the left, and the corners (0, 0) and (3, 3).  The shares
+    // go around the warps (and with them the schedulers) from CTA to CTA.
+    const int share = (warp + cta) & 3, tiles = share < 2 ? 3 : 2, corners = share == 3;
+    auto tile_row = [&](int s) { return corners ? 3 * s : 3 - share; };
+    auto tile_col = [&](int s) { return corners ? 3 * s : s; };
+    float kk[3][2][4] = {}, qk[3][2][4] = {};
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
         uint32_t a[4], b[4], w[4];
-        const int ar = rb * 16 + (lane & 8) + row_of(lane), ac = 2 * x + (lane >> 4);
-        ldsm4(a, sK + piece(ar, ac));
-        ldsm4(b, sQ + piece(ar, ac));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j <= rb) {
-                ldsm4(w, sK + piece(16 * j + (lane & 7) + ((lane & 16) >> 1), 2 * x + ((lane >> 3) & 1)));
-                mma_f16(kk[2 * j], a, w[0], w[1]);
-                mma_f16(kk[2 * j + 1], a, w[2], w[3]);
-                mma_f16(qk[2 * j], b, w[0], w[1]);
-                mma_f16(qk[2 * j + 1], b, w[2], w[3]);
+        for (int s = 0; s < 3; ++s) {
+            if (s < tiles) {
+                if (s == 0 || (s == 1 && corners)) {
+                    const int ar = tile_row(s) * 16 + (lane & 8) + row_of(lane), ac = 2 * x + (lane >> 4);
+                    ldsm4(a, sK + piece(ar, ac));
+                    ldsm4(b, sQ + piece(ar, ac));
+                }
+                ldsm4(w, sK + piece(16 * tile_col(s) + (lane & 7) + ((lane & 16) >> 1), 2 * x + ((lane >> 3) & 1)));
+                mma_f16(kk[s][0], a, w[0], w[1]);
+                mma_f16(kk[s][1], a, w[2], w[3]);
+                mma_f16(qk[s][0], b, w[0], w[1]);
+                mma_f16(qk[s][1], b, w[2], w[3]);
             }
         }
     }
     // keys' powers of two into K K^T
-    const int i0 = rb * 16 + row_of(lane >> 2), j0 = (lane & 3) * 2;
+    const int i0 = row_of(lane >> 2), j0 = (lane & 3) * 2;
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-        const float2 s = *reinterpret_cast<const float2 *>(sk + nt * 8 + j0);
+    for (int s = 0; s < 3; ++s) {
+        if (s == 2 && tiles == 2) break;
+        const int i = tile_row(s) * 16 + i0;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            kk[nt][2 * hf] *= s.x * sk[i0 + 8 * hf];
-            kk[nt][2 * hf + 1] *= s.y * sk[i0 + 8 * hf];
+        for (int nt = 0; nt < 2; ++nt) {
+            const float2 sj = *reinterpret_cast<const float2 *>(sk + tile_col(s) * 16 + nt * 8 + j0);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                kk[s][nt][2 * hf] *= sj.x * sk[i + 8 * hf];
+                kk[s][nt][2 * hf + 1] *= sj.y * sk[i + 8 * hf];
+            }
         }
     }
     if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -362,45 +371,54 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             }
         }
         __syncthreads();
-        // A and P of this warp's rows
+        // this warp's tiles of A and P
         for (int r = 0; r < heads; ++r) {
             const float *gh = vec + r * 4 * C, *gl = gh + C, *be = gl + C;
             float *A = mats + r * kMat;
             unsigned char *pout = reinterpret_cast<unsigned char *>(p.rec[(size_t)chunk * p.H + g * p.rep + r0 + r].p);
             using f2 = unsigned long long;
             f2 hi[2], lo[2], bi[2];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int i = i0 + 8 * hf;
-                hi[hf] = f2_pack(gh[i], gh[i]), lo[hf] = f2_pack(gl[i], gl[i]), bi[hf] = f2_pack(be[i], be[i]);
-            }
             const f2 one = f2_pack(1.f, 1.f), minus = f2_pack(-1.f, -1.f);
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const int j = nt * 8 + j0;
-                if (nt > 2 * rb + 1) {  // above the diagonal's blocks, where A is not read
+            for (int s = 0; s < 3; ++s) {
+                if (s == 2 && tiles == 2) break;
+                if (s == 0 || (s == 1 && corners)) {
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) *reinterpret_cast<uint32_t *>(pout + piece(i0 + 8 * hf, nt) + (lane & 3) * 4) = 0;
-                    continue;
-                }
-                const f2 hj = *reinterpret_cast<const f2 *>(gh + j), lj = *reinterpret_cast<const f2 *>(gl + j);
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int i = i0 + 8 * hf;
-                    float x0, x1;
-                    f2_unpack(f2_fma(f2_fma(hj, minus, hi[hf]), one, f2_fma(lj, minus, lo[hf])), x0, x1);
-                    const f2 d = f2_pack(exp2_fast(x0), exp2_fast(x1));
-                    float p0, p1, a0, a1;
-                    f2_unpack(f2_mul(d, f2_pack(qk[nt][2 * hf], qk[nt][2 * hf + 1])), p0, p1);
-                    f2_unpack(f2_mul(f2_mul(d, bi[hf]), f2_pack(kk[nt][2 * hf], kk[nt][2 * hf + 1])), a0, a1);
-                    if (nt >= 2 * rb) {  // the diagonal's tiles
-                        if (j > i) p0 = 0.f;
-                        if (j + 1 > i) p1 = 0.f;
-                        if (j >= i) a0 = 0.f;
-                        if (j + 1 >= i) a1 = 0.f;
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int i = tile_row(s) * 16 + i0 + 8 * hf;
+                        hi[hf] = f2_pack(gh[i], gh[i]), lo[hf] = f2_pack(gl[i], gl[i]), bi[hf] = f2_pack(be[i], be[i]);
                     }
-                    *reinterpret_cast<float2 *>(A + i * LDM + j) = make_float2(a0, a1);
-                    *reinterpret_cast<uint32_t *>(pout + piece(i, nt) + (lane & 3) * 4) = pack_h2(p0, p1);
+                }
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const int j = tile_col(s) * 16 + nt * 8 + j0;
+                    const f2 hj = *reinterpret_cast<const f2 *>(gh + j), lj = *reinterpret_cast<const f2 *>(gl + j);
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int i = tile_row(s) * 16 + i0 + 8 * hf;
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_fma(hj, minus, hi[hf]), one, f2_fma(lj, minus, lo[hf])), x0, x1);
+                        const f2 d = f2_pack(exp2_fast(x0), exp2_fast(x1));
+                        float p0, p1, a0, a1;
+                        f2_unpack(f2_mul(d, f2_pack(qk[s][nt][2 * hf], qk[s][nt][2 * hf + 1])), p0, p1);
+                        f2_unpack(f2_mul(f2_mul(d, bi[hf]), f2_pack(kk[s][nt][2 * hf], kk[s][nt][2 * hf + 1])), a0, a1);
+                        if (tile_row(s) == tile_col(s)) {
+                            if (j > i) p0 = 0.f;
+                            if (j + 1 > i) p1 = 0.f;
+                            if (j >= i) a0 = 0.f;
+                            if (j + 1 >= i) a1 = 0.f;
+                        }
+                        *reinterpret_cast<float2 *>(A + i * LDM + j) = make_float2(a0, a1);
+                        *reinterpret_cast<uint32_t *>(pout + piece(i, j >> 3) + (lane & 3) * 4) = pack_h2(p0, p1);
+                    }
+                }
+            }
+            // P's zeros, 16 bytes a lane, by the warps of two tiles; A is not read up there
+            if (share >= 2) {
+#pragma unroll
+                for (int s = 0; s < 3; ++s) {  // tiles (0, 1), (0, 2), (0, 3) or (1, 2), (1, 3), (2, 3)
+                    const int row = share == 2 ? 0 : 1 + (s == 2), col = share == 2 ? s + 1 : 2 + (s > 0);
+                    *reinterpret_cast<uint4 *>(pout + piece(row * 16 + (lane >> 1), col * 2 + (lane & 1))) = make_uint4(0, 0, 0, 0);
                 }
             }
         }
