@@ -116,7 +116,8 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
 // inherits T's accuracy.
 // 26,458 rows of 32 value and 16 key heads: 163 us at four CTAs an SM, half of the
 // issue slots and three fifths of shared memory's bandwidth used: what bounds it is
-// the latency of shared memory and of the barriers between its short phases (five CTAs an SM, at 96 registers, take 171 us).
+// the latency of shared memory and of the barriers between its short phases (five
+// CTAs an SM, at 96 registers, take 171 us).
 constexpr int kChunkThreads = 128;
 // fp32 matrices in shared memory: 16-byte rows, banks shifted by 12.  Rows 0, 2, 4, 6
 // and rows 1, 3, 5, 7 then start 8 banks apart, so a fragment whose 8 rows are taken in
