@@ -538,7 +538,8 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
                 atomicMax(reinterpret_cast<int *>(bounds + 2 * grp + 1), __float_as_int(kmx));
             }
             group_sync(grp);
-            if (t == 0) out.umax = bounds[2 * grp], out.kmax = bounds[2 * grp + 1];
+            // 0 where nothing is written (beta = 0, or a reset after it): the scan divides by these
+            if (t == 0) out.umax = fmaxf(bounds[2 * grp], kLeastBound), out.kmax = fmaxf(bounds[2 * grp + 1], kLeastBound);
         }
         __syncthreads();
     }

@@ -38,6 +38,9 @@ struct Record {
     float kmax;  // the same of e^(G_C - G) u
     float pad[28];
 };
+// Least umax and kmax: the quotient of R's and u's scales stays finite in fp32
+// (at most 2^121), and what is below it is lost beside any R.
+constexpr float kLeastBound = 7.5231638452626401e-37f;  // 2^-120
 constexpr int kRecMats = 3 * C * C * 2;                   // bytes of the matrices, then
 constexpr int kRecVecs = (int)sizeof(Record) - kRecMats;  // of the vectors
 static_assert(sizeof(Record) == 25984, "records are copied in 16-byte pieces");
