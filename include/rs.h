@@ -485,10 +485,10 @@ rs_status rs_prefill_bytes_for(const rs_layer_desc *desc, const rs_ragged_desc *
  * same descriptor; block_table is read when rd->block > 0 and pool is given.
  * RS_GDN only.  work: device scratch, 128-byte aligned, of the bytes that
  * rs_prefill_bytes_for gives for the same descriptors and max_len; it need not
- * be cleared, and a call leaves nothing in it that another one needs.  States are accurate to fp32 rounding (operands of 22 bits, fp32 sums);
- * y has fp16 operands beside fp32 sums and is rounded to bf16.  A NaN or an
- * infinity stays in its request; there it may reach any row of its own chunk
- * and all later ones.
+ * be cleared, and a call leaves nothing in it that another one needs.  States,
+ * and y before its one rounding to bf16, are accurate to fp32 rounding (operands
+ * of 22 bits, fp32 sums).  A NaN or an infinity stays in its request; there it
+ * may reach any row of its own chunk and all later ones.
  * Source: [CSI] "How it works", Gated DeltaNet bullet (the recurrence). */
 rs_status rs_prefill_gdn(const rs_layer_desc *desc, const rs_state *st, const rs_ragged_desc *rd, const rs_ragged *rg,
                          const rs_prefill *in, uint16_t *y, void *work, void *stream);

@@ -30,12 +30,12 @@
 // long a chunk's decay is; alpha = 0 is a decay of 2^-160, which is 0 in fp32.
 //
 // Precision.  The tensor cores multiply fp16 operands into fp32 sums.  Keys
-// and queries (bf16) are exact in fp16 once each row is scaled by a power of
-// two to a largest value in [1, 2).  What feeds the state (S, R, T, u) enters
-// as the sum of two fp16 terms, 22 bits, each row scaled by a power of two
-// likewise, so that states come out at fp32 accuracy (bf16 terms would leave
-// 16 bits at the same cost).  What feeds y alone (S and u once more, P) enters
-// as one fp16 term of 11 bits, below y's own rounding to 8.
+// and queries (bf16) enter as one fp16 term, each row scaled by a power of two to
+// a largest value in [1, 2): exact down to 2^-17 of that value, and off by at most
+// 2^-25 of it below.  Everything else (S, R, T, P, u) enters as the sum of two fp16
+// terms, 22 bits, scaled by a power of two likewise, so that states and outputs come
+// out at fp32 accuracy (bf16 terms would leave 16 bits at the same cost), as those of
+// the recurrence for short requests do; y is rounded once, to bf16.
 #include "rs_prefill.cuh"
 
 namespace rs {
@@ -358,7 +358,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             const float k0 = exp2f((cgh - h[0]) + (cgl - l[0])), k1 = exp2f((cgh - h[1]) + (cgl - l[1]));
             const float2 skl = *reinterpret_cast<const float2 *>(sk + 2 * lane), sql = *reinterpret_cast<const float2 *>(sq + 2 * lane);
             *reinterpret_cast<float2 *>(out.egk + 2 * lane) = make_float2(e0 * skl.x, e1 * skl.y);
-            *reinterpret_cast<float2 *>(out.egq + 2 * lane) = make_float2(e0 * sql.x, e1 * sql.y);
+            *reinterpret_cast<float2 *>(out.eg + 2 * lane) = make_float2(e0, e1);
             *reinterpret_cast<float2 *>(out.sq + 2 * lane) = sql;
             *reinterpret_cast<float2 *>(out.ke + 2 * lane) = make_float2(k0, k1);
             *reinterpret_cast<float2 *>(v + 3 * C + 2 * lane) = make_float2(k0, k1);
@@ -376,7 +376,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
         for (int r = 0; r < heads; ++r) {
             const float *gh = vec + r * 4 * C, *gl = gh + C, *be = gl + C;
             float *A = mats + r * kMat;
-            unsigned char *pout = reinterpret_cast<unsigned char *>(p.rec[(size_t)chunk * p.H + g * p.rep + r0 + r].p);
+            unsigned char *pout = reinterpret_cast<unsigned char *>(p.rec[(size_t)chunk * p.H + g * p.rep + r0 + r].p_hi);
             using f2 = unsigned long long;
             f2 hi[2], lo[2], bi[2];
             const f2 one = f2_pack(1.f, 1.f), minus = f2_pack(-1.f, -1.f);
@@ -410,16 +410,12 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
                             if (j + 1 >= i) a1 = 0.f;
                         }
                         *reinterpret_cast<float2 *>(A + i * LDM + j) = make_float2(a0, a1);
-                        *reinterpret_cast<uint32_t *>(pout + piece(i, j >> 3) + (lane & 3) * 4) = pack_h2(p0, p1);
+                        uint32_t ph, pl;
+                        split_cut(p0, p1, ph, pl);
+                        unsigned char *at = pout + piece(i, j >> 3) + (lane & 3) * 4;
+                        *reinterpret_cast<uint32_t *>(at) = ph;
+                        *reinterpret_cast<uint32_t *>(at + C * C * 2) = pl;  // p_lo
                     }
-                }
-            }
-            // P's zeros, 16 bytes a lane, by the warps of two tiles; A is not read up there
-            if (share >= 2) {
-#pragma unroll
-                for (int s = 0; s < 3; ++s) {  // tiles (0, 1), (0, 2), (0, 3) or (1, 2), (1, 3), (2, 3)
-                    const int row = share == 2 ? 0 : 1 + (s == 2), col = share == 2 ? s + 1 : 2 + (s > 0);
-                    *reinterpret_cast<uint4 *>(pout + piece(row * 16 + (lane >> 1), col * 2 + (lane & 1))) = make_uint4(0, 0, 0, 0);
                 }
             }
         }
@@ -708,9 +704,11 @@ template <int D, int NW>
 struct ScanSmem {
     static constexpr int TILE = C * D * 2;
     static constexpr int VT = NW * C * 32;  // per warp: 64 rows of its 16 columns
-    static constexpr int REC = 2 * TILE + VT;
-    static constexpr int STAGE = REC + (int)sizeof(Record);
-    static constexpr int BYTES = 2 * STAGE;
+    static constexpr int T = 2 * TILE + VT;
+    static constexpr int VEC = T + 2 * C * C * 2;
+    static constexpr int STAGE = VEC + kRecVecs;
+    static constexpr int P = 2 * STAGE;  // one buffer: hi, lo
+    static constexpr int BYTES = P + 2 * C * C * 2;
 };
 
 
@@ -748,10 +746,16 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
             cp16(st + 2 * M::TILE + (c >> 1) * (C * 32) + t * 32 + (((c & 1) ^ ((t >> 2) & 1)) << 4),
                  v + (t < n ? t : 0) * p.ld_v + c * 8, t < n && !un.map);
         }
-        const unsigned char *rec = reinterpret_cast<const unsigned char *>(p.rec + (size_t)(rq.chunk0 + i) * p.H + h);
-        for (int x = tid; x < (int)sizeof(Record) / 16; x += NT) cp16(st + M::REC + x * 16, rec + x * 16, true);
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        const Record *rec = p.rec + (size_t)(rq.chunk0 + i) * p.H + h;
+        const unsigned char *t = reinterpret_cast<const unsigned char *>(rec->t_hi), *vec = reinterpret_cast<const unsigned char *>(rec->egk);
+        for (int x = tid; x < 2 * C * C * 2 / 16; x += NT) cp16(st + M::T + x * 16, t + x * 16, true);
+        for (int x = tid; x < kRecVecs / 16; x += NT) cp16(st + M::VEC + x * 16, vec + x * 16, true);
     };
+    auto fetch_p = [&](int i) {
+        const unsigned char *src = reinterpret_cast<const unsigned char *>(p.rec[(size_t)(rq.chunk0 + i) * p.H + h].p_hi);
+        for (int x = tid; x < 2 * C * C * 2 / 16; x += NT) cp16(s0 + M::P + x * 16, src + x * 16, true);
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
     // the starting state: S^T[p][n], rows p = col0 + gr (+8), columns n = 8 nt + 2 tq (+1)
     const int gr = lane >> 2, tq = lane & 3;
@@ -779,6 +783,7 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
 
     wait_for_launch();  // for the chunks' records
     fetch(un.c0, s0);
+    commit();
     if (!OUT && un.seg == 0) store_state(p.segs, nullptr, seg_slab(p, un, 0, D * D));  // for the second pass
 
     for (int i = un.c0; i < un.c1; ++i) {
@@ -786,10 +791,15 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // this chunk's stage has landed, and every warp is done with the other one
         const uint32_t st = s0 + odd * M::STAGE;
+        if (OUT) {
+            fetch_p(i);  // the last chunk's are used up as well
+            commit();
+        }
         if (i + 1 < un.c1) fetch(i + 1, s0 + (odd ^ 1) * M::STAGE);
+        commit();
         const uint32_t sK = st, sQ = st + M::TILE, sV = st + 2 * M::TILE + warp * (C * 32);
-        const uint32_t sTh = st + M::REC, sTl = sTh + C * C * 2, sP = sTl + C * C * 2;
-        const Record *rec = reinterpret_cast<const Record *>(smem + odd * M::STAGE + M::REC);
+        const uint32_t sTh = st + M::T, sTl = sTh + C * C * 2, sPh = s0 + M::P, sPl = sPh + C * C * 2;
+        const Vecs *rec = reinterpret_cast<const Vecs *>(smem + odd * M::STAGE + M::VEC);
 
         // S^T K^T and S^T Q^T: columns are the chunk's rows
         float X[8][4] = {}, Z[8][4] = {};
@@ -813,6 +823,8 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
                     ldsm4(b, sQ + o);
                     mma_f16(Z[2 * j], hi, b[0], b[1]);
                     mma_f16(Z[2 * j + 1], hi, b[2], b[3]);
+                    mma_f16(Z[2 * j], lo, b[0], b[1]);
+                    mma_f16(Z[2 * j + 1], lo, b[2], b[3]);
                 }
             }
         }
@@ -826,7 +838,7 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
             for (int hf = 0; hf < 2; ++hf) {
                 const int nt = 2 * j + hf;
                 const float2 ek = *reinterpret_cast<const float2 *>(rec->egk + nt * 8 + tq * 2);
-                const float2 eg = *reinterpret_cast<const float2 *>(rec->egq + nt * 8 + tq * 2);
+                const float2 eg = *reinterpret_cast<const float2 *>(rec->eg + nt * 8 + tq * 2);
                 X[nt][0] = __uint_as_float(v[2 * hf] << 16) - ek.x * (X[nt][0] * sd0);
                 X[nt][1] = __uint_as_float(v[2 * hf] & 0xffff0000u) - ek.y * (X[nt][1] * sd0);
                 X[nt][2] = __uint_as_float(v[2 * hf + 1] << 16) - ek.x * (X[nt][2] * sd1);
@@ -866,6 +878,8 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
         }
         // y^T = (e^G S^T Q^T + u^T P^T) with the queries' powers of two
         if (OUT) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();  // P has landed
             float m0, m1, u0, u1, d0, d1;
             row_max(U, m0, m1);
             row_scale<14>(m0, u0, d0);
@@ -874,22 +888,26 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
             for (int nt = 0; nt < 8; ++nt) X[nt][0] = X[nt][1] = X[nt][2] = X[nt][3] = 0.f;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const uint32_t a[4] = {pack_h2(U[2 * x][0] * u0, U[2 * x][1] * u0), pack_h2(U[2 * x][2] * u1, U[2 * x][3] * u1),
-                                       pack_h2(U[2 * x + 1][0] * u0, U[2 * x + 1][1] * u0),
-                                       pack_h2(U[2 * x + 1][2] * u1, U[2 * x + 1][3] * u1)};
-                uint32_t b[4];
+                uint32_t hi[4], lo[4], b[4];
+                split(U[2 * x], U[2 * x + 1], u0, u1, hi, lo);
 #pragma unroll
                 for (int j = x; j < 4; ++j) {
-                    ldsm4(b, sP + piece(16 * j + (lane & 7) + ((lane & 16) >> 1), 2 * x + ((lane >> 3) & 1)));
-                    mma_f16(X[2 * j], a, b[0], b[1]);
-                    mma_f16(X[2 * j + 1], a, b[2], b[3]);
+                    const uint32_t o = piece(16 * j + (lane & 7) + ((lane & 16) >> 1), 2 * x + ((lane >> 3) & 1));
+                    ldsm4(b, sPh + o);
+                    mma_f16(X[2 * j], hi, b[0], b[1]);
+                    mma_f16(X[2 * j + 1], hi, b[2], b[3]);
+                    mma_f16(X[2 * j], lo, b[0], b[1]);
+                    mma_f16(X[2 * j + 1], lo, b[2], b[3]);
+                    ldsm4(b, sPl + o);
+                    mma_f16(X[2 * j], hi, b[0], b[1]);
+                    mma_f16(X[2 * j + 1], hi, b[2], b[3]);
                 }
             }
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
                 const float2 sq = *reinterpret_cast<const float2 *>(rec->sq + nt * 8 + tq * 2);
-                Z[nt][0] += X[nt][0] * d0 * sq.x, Z[nt][1] += X[nt][1] * d0 * sq.y;
-                Z[nt][2] += X[nt][2] * d1 * sq.x, Z[nt][3] += X[nt][3] * d1 * sq.y;
+                Z[nt][0] = (Z[nt][0] + X[nt][0] * d0) * sq.x, Z[nt][1] = (Z[nt][1] + X[nt][1] * d0) * sq.y;
+                Z[nt][2] = (Z[nt][2] + X[nt][2] * d1) * sq.x, Z[nt][3] = (Z[nt][3] + X[nt][3] * d1) * sq.y;
             }
         }
         // S^T = e^(G_C) S^T + (e^(G_C - G) u)^T K, summed at u's row scale.  Where u is

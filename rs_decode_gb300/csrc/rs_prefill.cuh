@@ -25,9 +25,9 @@ constexpr int kShort = 12;
 // Per chunk and value head:
 struct Record {
     uint16_t t_hi[C * C], t_lo[C * C];  // T, row i scaled by 1 / (its power of two)
-    uint16_t p[C * C];                  // P without the rows' powers of two
+    uint16_t p_hi[C * C], p_lo[C * C];  // P without the rows' powers of two; nothing above the diagonal's 16 x 16 blocks
     float egk[C];  // e^(G_i) times key i's power of two
-    float egq[C];  // e^(G_i) times query i's power of two
+    float eg[C];   // e^(G_i)
     float su[C];   // T's and key i's powers of two: (T R)_i su_i = u_i times key i's power
     float sq[C];   // query i's power of two
     float ke[C];  // e^(G_C - G_i)
@@ -41,9 +41,13 @@ struct Record {
 // Least umax and kmax: the quotient of R's and u's scales stays finite in fp32
 // (at most 2^121), and what is below it is lost beside any R.
 constexpr float kLeastBound = 7.5231638452626401e-37f;  // 2^-120
-constexpr int kRecMats = 3 * C * C * 2;                   // bytes of the matrices, then
+constexpr int kRecMats = 4 * C * C * 2;                   // bytes of the matrices, then
 constexpr int kRecVecs = (int)sizeof(Record) - kRecMats;  // of the vectors
-static_assert(sizeof(Record) == 25984, "records are copied in 16-byte pieces");
+static_assert(sizeof(Record) == 34176, "records are copied in 16-byte pieces");
+struct Vecs {  // the vectors of a Record
+    float egk[C], eg[C], su[C], sq[C], ke[C], all, xmax, umax, kmax, pad[28];
+};
+static_assert(sizeof(Vecs) == kRecVecs, "");
 
 struct PrefillParams {
     int H, G, rep, prec;  // rep: value heads of a key head

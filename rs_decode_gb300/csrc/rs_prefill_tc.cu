@@ -9,13 +9,13 @@
 //   R = V^T - e^G X              (threads)
 //   U = R T^T                    A = R  (hi, lo in TMEM)  B = T hi, lo; lower triangular
 //   D = (e^(G_C - G) u)^T K      A = u  (hi, lo in TMEM)  B = keys, the same tile read MN-major
-//   Y = u^T P^T                  A = u  (hi in shared memory)  B = P; lower triangular
-//   S <- e^(G_C) S + D, y = e^G Z + Y   (threads)
+//   Y = e^G Z + u^T P^T          A = u  (hi, lo in shared memory)  B = P hi, lo; lower triangular
+//   S <- e^(G_C) S + D, y = Y    (threads)
 // The state itself stays fp32 in the threads' registers, 64 keys each.
 //
 // A chunk is a chain of four products with register work between them, so one
 // head alone leaves the tensor cores idle half of the time: two CTAs share an
-// SM.  That fixes the budget: 256 TMEM columns (below), 128 registers, 94 KiB
+// SM.  That fixes the budget: 256 TMEM columns (below), 128 registers, 102 KiB
 // of shared memory, in which only the keys and the vectors are double-buffered
 // (they are needed up to the chunk's end; everything else is refilled while
 // the chunk goes on).  Two threads a row, not one: the register work is
@@ -23,11 +23,16 @@
 // together on a scheduler share its fetches.
 //
 // TMEM columns, by phase of a chunk:
-//   [0, 64)     S lo  -> R hi, lo -> u hi, lo
-//   [64, 128)   X sums -> U sums -> Y sums
+//   [0, 64)     S lo  -> U sums -> u hi, lo
+//   [64, 128)   X sums -> R hi, lo -> Y sums, starting from e^G Z
 //   [128, 192)  Z sums -> D sums, keys 0..63
 //   [192, 256)  S hi  -> D sums, keys 64..127
-// Z leaves early, packed to fp16 (y rounds to 8 bits, fp16 keeps 11).
+// R and u take the place of the sums that they are made of, 16 rows of the chunk at a
+// time: 8 columns of hi and 8 of lo, a step of the product that reads them.
+//
+// y is held to fp32's accuracy like the state, not to bf16's: where a query meets
+// little of a large state, or small values overwrite large ones, the terms of y
+// cancel, and what is rounded off them would be left in it.
 //
 // Measured: 3.9 us a chunk for a CTA alone on its SM, 5.8 for each of two.  The
 // products are 1.6 us of the former at the tensor cores' rate (34 clocks for each
@@ -55,10 +60,10 @@ constexpr int kTmem = 256;
 // Shared memory: tiles on 1024-byte boundaries (the swizzle's period).
 struct Smem {
     static constexpr int K = 0;                      // two buffers
-    static constexpr int Q = K + 2 * kTile;          // queries, then u
-    static constexpr int T = Q + kTile;              // hi, lo
-    static constexpr int P = T + 2 * kHalf;
-    static constexpr int V = P + kHalf;              // [64][128] bf16
+    static constexpr int Q = K + 2 * kTile;          // queries, then u hi
+    static constexpr int T = Q + kTile;              // hi, lo, then u lo
+    static constexpr int P = T + 2 * kHalf;          // hi, lo
+    static constexpr int V = P + 2 * kHalf;          // [64][128] bf16
     static constexpr int VEC = V + C * D * 2;        // two buffers
     static constexpr int MAX = VEC + 2 * kRecVecs;   // [2][2][128] row maxima of the state and of V
     static constexpr int BAR = MAX + 4 * D * 4;
@@ -77,11 +82,6 @@ struct Bars {
     const Record *rec;                                   // the request's records of this head, p.H apart
 };
 static_assert(sizeof(Bars) <= 256, "");
-
-struct Vecs {  // the vectors of a Record
-    float egk[C], egq[C], su[C], sq[C], ke[C], all, xmax, umax, kmax, pad[28];
-};
-static_assert(sizeof(Vecs) == kRecVecs, "");
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, Bars *b, uint32_t *status) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -162,11 +162,19 @@ __device__ __forceinline__ void st8(uint32_t addr, const uint32_t (&v)[8]) {
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+__device__ __forceinline__ void st16(uint32_t addr, const f2 (&f)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"((uint32_t)f[0]), "r"((uint32_t)(f[0] >> 32)), "r"((uint32_t)f[1]), "r"((uint32_t)(f[1] >> 32)),
+        "r"((uint32_t)f[2]), "r"((uint32_t)(f[2] >> 32)), "r"((uint32_t)f[3]), "r"((uint32_t)(f[3] >> 32)),
+        "r"((uint32_t)f[4]), "r"((uint32_t)(f[4] >> 32)), "r"((uint32_t)f[5]), "r"((uint32_t)(f[5] >> 32)),
+        "r"((uint32_t)f[6]), "r"((uint32_t)(f[6] >> 32)), "r"((uint32_t)f[7]), "r"((uint32_t)(f[7] >> 32))
+        : "memory");
+}
 __device__ __forceinline__ void st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 16 values of a row, scaled, as 8 packed hi and 8 packed lo columns.  hi is
 // the value cut to 11 bits, lo the fp16 rounding of the rest: 22 bits in all.
-__device__ __forceinline__ uint32_t pack_pair(f2 v) { return pack_h2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))); }
 __device__ __forceinline__ void put_split(uint32_t hi_addr, uint32_t lo_addr, const f2 *x, f2 up) {
     uint32_t hi[8], lo[8];
     const f2 minus = f2_pack(-1.f, -1.f);
@@ -225,8 +233,8 @@ __device__ __forceinline__ void load_qp(Bars *b, uint32_t sm, int i, int heads) 
         ++b->nq;
         mbar_arrive_expect_tx(&b->full_q, kTile);
         bulk_load(sm + Smem::Q, b->tiles + (size_t)i * b->tile_step + kTile, kTile, &b->full_q);
-        mbar_arrive_expect_tx(&b->full_p, kHalf);
-        bulk_load(sm + Smem::P, b->rec[(size_t)i * heads].p, kHalf, &b->full_p);
+        mbar_arrive_expect_tx(&b->full_p, 2 * kHalf);
+        bulk_load(sm + Smem::P, b->rec[(size_t)i * heads].p_hi, 2 * kHalf, &b->full_p);
     }
     __syncwarp();
 }
@@ -265,29 +273,35 @@ __device__ __forceinline__ void issue_z(uint32_t tm, uint32_t q, Bars *b) {
 #pragma unroll
     for (int x = 0; x < 8; ++x)
         mma_ts(tm + 128, tm + 192 + 8 * x, q + (x >> 2) * kHalfD + (x & 3) * 2, idesc_f16(64, false), x > 0);
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+        mma_ts(tm + 128, tm + 8 * x, q + (x >> 2) * kHalfD + (x & 3) * 2, idesc_f16(64, false), true);
     umma_commit(&b->mz);
 }
 __device__ __forceinline__ void issue_u(uint32_t tm, uint32_t t, Bars *b) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {  // T is lower triangular: rows 16 x and on of its columns 16 x..
-        mma_ts(tm + 64 + 16 * x, tm + 8 * x, t + x * 130, idesc_f16(64 - 16 * x, false), x > 0);
-        mma_ts(tm + 64 + 16 * x, tm + 32 + 8 * x, t + x * 130, idesc_f16(64 - 16 * x, false), true);
-        mma_ts(tm + 64 + 16 * x, tm + 8 * x, t + kHalfD + x * 130, idesc_f16(64 - 16 * x, false), true);
+        mma_ts(tm + 16 * x, tm + 64 + 16 * x, t + x * 130, idesc_f16(64 - 16 * x, false), x > 0);
+        mma_ts(tm + 16 * x, tm + 64 + 16 * x + 8, t + x * 130, idesc_f16(64 - 16 * x, false), true);
+        mma_ts(tm + 16 * x, tm + 64 + 16 * x, t + kHalfD + x * 130, idesc_f16(64 - 16 * x, false), true);
     }
     umma_commit(&b->mu);
 }
 __device__ __forceinline__ void issue_d(uint32_t tm, uint32_t k, Bars *b) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {  // 16 rows of the chunk a step; two tiles of 64 keys side by side
-        mma_ts(tm + 128, tm + 8 * x, k + x * 128 + kHalfStride, idesc_f16(128, true), x > 0);
-        mma_ts(tm + 128, tm + 32 + 8 * x, k + x * 128 + kHalfStride, idesc_f16(128, true), true);
+        mma_ts(tm + 128, tm + 16 * x, k + x * 128 + kHalfStride, idesc_f16(128, true), x > 0);
+        mma_ts(tm + 128, tm + 16 * x + 8, k + x * 128 + kHalfStride, idesc_f16(128, true), true);
     }
     umma_commit(&b->md);
 }
-__device__ __forceinline__ void issue_y(uint32_t tm, uint32_t u, uint32_t pm, Bars *b) {
+__device__ __forceinline__ void issue_y(uint32_t tm, uint32_t uh, uint32_t ul, uint32_t pm, Bars *b) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-        mma_ss(tm + 64 + 16 * x, u + x * 2, pm + x * 130, idesc_f16(64 - 16 * x, false), x > 0);
+    for (int x = 0; x < 4; ++x) {  // onto e^G Z
+        mma_ss(tm + 64 + 16 * x, uh + x * 2, pm + x * 130, idesc_f16(64 - 16 * x, false), true);
+        mma_ss(tm + 64 + 16 * x, ul + x * 2, pm + x * 130, idesc_f16(64 - 16 * x, false), true);
+        mma_ss(tm + 64 + 16 * x, uh + x * 2, pm + kHalfD + x * 130, idesc_f16(64 - 16 * x, false), true);
+    }
     umma_commit(&b->my);
 }
 
@@ -315,8 +329,8 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
     const uint32_t base = __reduce_or_sync(~0u, b->tmem), sm = smem_u32(smem);  // the reduction makes it a uniform register
     const uint32_t lanes = base + ((uint32_t)(warp & 3) << 21);
     const uint32_t t_shi = lanes + 192 + 32 * hf, t_slo = lanes + 32 * hf;          // state
-    const uint32_t t_ohi = lanes + 16 * hf, t_olo = lanes + 32 + 16 * hf;           // R, u
-    const uint32_t t_sum = lanes + 64 + 32 * hf, t_z = lanes + 128 + 32 * hf, t_d = lanes + 128 + 64 * hf;
+    const uint32_t t_u = lanes + 32 * hf, t_r = lanes + 64 + 32 * hf;  // sums of U; of X and Y
+    const uint32_t t_z = lanes + 128 + 32 * hf, t_d = lanes + 128 + 64 * hf;
     Work w;
     w.n = rq.n;
     w.head_rows = min(rq.n, C - rq.ctx % C);
@@ -454,7 +468,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
 #pragma unroll
         for (int t = 0; t < CH; t += 16) {
             f2 x[8];
-            ld16(t_sum + t, x);
+            ld16(t_r + t, x);
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
                 const ulonglong2 ek = *reinterpret_cast<const ulonglong2 *>(vec.egk + hf * CH + t + e);
@@ -462,7 +476,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
                 x[e / 2] = f2_fma(x[e / 2], f2_mul(ek.x, nsdown), (f2)(v0 & 0xffff0000u) << 32 | v0 << 16);
                 x[e / 2 + 1] = f2_fma(x[e / 2 + 1], f2_mul(ek.y, nsdown), (f2)(v1 & 0xffff0000u) << 32 | v1 << 16);
             }
-            put_split(t_ohi + t / 2, t_olo + t / 2, x, f2_pack(rup, rup));
+            put_split(t_r + t, t_r + t + 8, x, f2_pack(rup, rup));
         }
         st_done();
         tc_fence_before_sync();
@@ -470,25 +484,31 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         load_v(i + 1);
         if (warp == 1) {
             ok = wait_warp(&b->full_t, ph, b, p.status) && ok;
+            if (OUT) ok = wait_warp(&b->mz, ph, b, p.status) && ok;  // Z reads S lo, where U goes
             tc_fence_after_sync();
             if (elect_one()) issue_u(base, desc_lo(sm + Smem::T), b);
             __syncwarp();
         }
-        // u, with its key's power of two: fp16 for y, split with e^(G_C - G) for the state
-        const float ubound = vec.umax * rbound, kbound = vec.kmax * rbound;
+        // u, with its key's power of two: for y, and with e^(G_C - G) for the state.  Y's
+        // sums start from e^G Z at u's scale: where u is below 2^-30 of the state, the
+        // state's size sets that scale, so that they stay in range.
+        const float ubound = fmaxf(vec.umax * rbound, smax * 9.31322574615478515625e-10f), kbound = vec.kmax * rbound;
         float uup, udown, kup, kdown;
         row_scale<14>(ubound, uup, udown);
         row_scale<14>(kbound, kup, kdown);
         const float uups = uup * rdown, kups = kup * rdown;  // from R's scale to u's
         const f2 uup2 = f2_pack(uups, uups);
         ok = wait_warp(&b->mu, ph, b, p.status) && ok;
+        if (OUT) ok = wait_warp(&b->mz, ph, b, p.status) && ok;
         tc_fence_after_sync();
-        if (i + 1 < nch && warp == 7) load_t(b, sm, i + 1, p.H);
-        uint32_t z[CH / 2];  // u in fp16, then Z, then y
+        if (!OUT && i + 1 < nch && warp == 7) load_t(b, sm, i + 1, p.H);
+        // u for Y takes the places of the queries and of T, whose products are complete
+        unsigned char *const urow = smem + Smem::Q + row * 128;
+        static_assert(Smem::T == Smem::Q + kTile, "u lo lies behind u hi");
 #pragma unroll
         for (int t = 0; t < CH; t += 16) {
             f2 x[8];
-            ld16(t_sum + t, x);
+            ld16(t_u + t, x);
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
                 const ulonglong2 su = *reinterpret_cast<const ulonglong2 *>(vec.su + hf * CH + t + e);
@@ -496,32 +516,41 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
             }
             if (OUT) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[t / 2 + e] = pack_pair(f2_mul(x[e], uup2));
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float a, d;
+                        f2_unpack(f2_mul(x[4 * c + e], uup2), a, d);
+                        split_cut(a, d, hi[e], lo[e]);
+                    }
+                    unsigned char *const at = urow + (((4 * hf + t / 8 + c) ^ (row & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(at + kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
             }
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
                 const ulonglong2 ke = *reinterpret_cast<const ulonglong2 *>(vec.ke + hf * CH + t + e);
                 x[e / 2] = f2_mul(x[e / 2], ke.x), x[e / 2 + 1] = f2_mul(x[e / 2 + 1], ke.y);
             }
-            put_split(t_ohi + t / 2, t_olo + t / 2, x, f2_pack(kups, kups));
+            put_split(t_u + t, t_u + t + 8, x, f2_pack(kups, kups));
         }
-        // the queries' place takes u once Z is complete; Z leaves TMEM in fp16
-        // (2^-9 keeps its sums, below 2^24, in range)
         if (OUT) {
-        ok = wait_warp(&b->mz, ph, b, p.status) && ok;
-        tc_fence_after_sync();
+            const float zs = sdown * uup;
+            const f2 zs2 = f2_pack(zs, zs);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4 *>(smem + Smem::Q + (row * 128 + (((4 * hf + c) ^ (row & 7)) << 4))) =
-                make_uint4(z[4 * c], z[4 * c + 1], z[4 * c + 2], z[4 * c + 3]);
+            for (int t = 0; t < CH; t += 16) {
+                f2 x[8];
+                ld16(t_z + t, x);
 #pragma unroll
-        for (int t = 0; t < CH; t += 16) {
-            f2 x[8];
-            ld16(t_z + t, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[t / 2 + e] = pack_pair(f2_mul(x[e], f2_pack(0.001953125f, 0.001953125f)));
-        }
-        fence_proxy_async_smem();
+                for (int e = 0; e < 16; e += 4) {
+                    const ulonglong2 eg = *reinterpret_cast<const ulonglong2 *>(vec.eg + hf * CH + t + e);
+                    x[e / 2] = f2_mul(x[e / 2], f2_mul(eg.x, zs2)), x[e / 2 + 1] = f2_mul(x[e / 2 + 1], f2_mul(eg.y, zs2));
+                }
+                st16(t_r + t, x);
+            }
+            fence_proxy_async_smem();
         }
         st_done();
         tc_fence_before_sync();
@@ -534,7 +563,7 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         if (OUT && warp == 3) {
             ok = wait_warp(&b->full_p, ph, b, p.status) && ok;
             tc_fence_after_sync();
-            if (elect_one()) issue_y(base, desc_lo(sm + Smem::Q), desc_lo(sm + Smem::P), b);
+            if (elect_one()) issue_y(base, desc_lo(sm + Smem::Q), desc_lo(sm + Smem::T), desc_lo(sm + Smem::P), b);
             __syncwarp();
         }
         // S <- e^(G_C) S + D
@@ -551,23 +580,22 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
             }
         }
         if (!OUT) continue;
-        // y = (e^G Z + Y) with the query's power of two
+        // y = Y with the query's power of two
         ok = wait_warp(&b->my, ph, b, p.status) && ok;
         tc_fence_after_sync();
         if (i + 1 < nch && warp == 6) load_qp(b, sm, i + 1, p.H);
-        const float zs = sdown * 512.f;
-        const unsigned long long zs2 = f2_pack(zs, zs), ud2 = f2_pack(udown, udown);
+        if (i + 1 < nch && warp == 7) load_t(b, sm, i + 1, p.H);
+        const f2 ud2 = f2_pack(udown, udown);
+        uint32_t z[CH / 2];
 #pragma unroll
         for (int t = 0; t < CH; t += 16) {
             f2 x[8];
-            ld16(t_sum + t, x);
+            ld16(t_r + t, x);
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-                const ulonglong2 eq = *reinterpret_cast<const ulonglong2 *>(vec.egq + hf * CH + t + e);
                 const ulonglong2 sq = *reinterpret_cast<const ulonglong2 *>(vec.sq + hf * CH + t + e);
-                const float2 z0 = unpack_h2(z[(t + e) / 2]), z1 = unpack_h2(z[(t + e) / 2 + 1]);
-                z[(t + e) / 2] = pack_b2(f2_fma(x[e / 2], f2_mul(sq.x, ud2), f2_mul(f2_mul(eq.x, zs2), f2_pack(z0.x, z0.y))));
-                z[(t + e) / 2 + 1] = pack_b2(f2_fma(x[e / 2 + 1], f2_mul(sq.y, ud2), f2_mul(f2_mul(eq.y, zs2), f2_pack(z1.x, z1.y))));
+                z[(t + e) / 2] = pack_b2(f2_mul(x[e / 2], f2_mul(sq.x, ud2)));
+                z[(t + e) / 2 + 1] = pack_b2(f2_mul(x[e / 2 + 1], f2_mul(sq.y, ud2)));
             }
         }
         // Neighbouring lanes swap halves: an even lane stores its and its neighbour's

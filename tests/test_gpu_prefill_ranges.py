@@ -11,7 +11,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_prefill import Case
+from test_gpu_prefill import TOL_BF16, Case, gdn_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,69 @@ def test_large_states_where_nothing_is_written(d, what):
         c.beta[at[:-1] + 1] = keep
     c.run()
     c.check()
+
+
+# ----------------------------------------------------------------------------- outputs beside what enters them
+# An output is a sum of terms of S q and P u.  Its error besides the rounding to
+# bf16 is that of fp32 sums and of operands held to 22 bits, 5e-6 of the terms'
+# magnitudes in the 2-norm as for the states, times 4 for the largest of a row
+# against its mean.
+TOL_TERMS = 2e-5
+
+
+def rows_near(c):
+    """Every output for itself, beside the magnitudes of the terms that it is the sum of."""
+    rep, at = c.H // c.G, 0
+    for r, n in enumerate(c.lengths):
+        s = slice(at, at + n)
+        q, k = (x[s].double().repeat_interleave(rep, 1) for x in (c.q, c.k))
+        v, alpha, beta = c.v[s].double(), c.alpha[s].double(), c.beta[s].double()
+        y = gdn_ref(c.first_state(r), q, k, v, alpha, beta)[0]
+        S, A, terms = c.first_state(r), c.first_state(r).abs(), []
+        for t in range(n):
+            S, A = alpha[t][:, None, None] * S, alpha[t][:, None, None] * A
+            u = beta[t][:, None] * (v[t] - torch.einsum("hn,hnp->hp", k[t], S))
+            S, A = S + k[t][:, :, None] * u[:, None, :], A + k[t].abs()[:, :, None] * u.abs()[:, None, :]
+            terms.append(torch.einsum("hn,hnp->hp", q[t].abs(), A))
+        err = (c.y[s].double() - y).abs()
+        over = (err - TOL_BF16 * y.abs()) / torch.stack(terms)
+        assert bool(err.isfinite().all()) and float(over.max()) <= TOL_TERMS, f"request {r}: {float(over.max()):.1e}"
+        at += n
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths", [[5, 12], [13, 64, 200], [2200]])
+def test_queries_that_meet_little_of_a_large_state(d, lengths):
+    """The state's largest part, on two keys, is at right angles to every query."""
+    c = Case(lengths, 2, 1, d, alpha="one", beta="zero", seed=23)
+    w = torch.randn(c.S0.shape[0], 2, d, device="cuda")
+    c.S0[:, :, 0] -= 3000 * w
+    c.S0[:, :, 1] += 1000 * w
+    c.layer.init(c.S0)
+    c.q[..., 0], c.q[..., 1] = 0.125, 0.375
+    c.run()
+    rows_near(c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths", [[12], [13, 64, 200], [2200]])
+def test_large_values_overwritten_by_small_ones(d, lengths):
+    """One key all along, written in full: every other row takes a value a thousand times its own out again."""
+    c = Case(lengths, 2, 1, d, alpha="one", beta="one", keys="same", seed=24)
+    c.v[::2] = (c.v[::2].float() * 1000).bfloat16()
+    c.run()
+    rows_near(c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_are_not_biased(d):
+    """Roundings to bf16 cancel over 2.6 million outputs (2^-9 / sqrt(2.6e6), 1.2e-6); 3e-5 leaves the sums' own."""
+    c = Case([640] * 8, 4, 2, d, alpha="slow", seed=25)
+    c.run()
+    at, dot, square = 0, 0.0, 0.0
+    for r, n in enumerate(c.lengths):
+        s = slice(at, at + n)
+        q, k = (x[s].double().repeat_interleave(2, 1) for x in (c.q, c.k))
+        y = gdn_ref(c.first_state(r), q, k, c.v[s].double(), c.alpha[s].double(), c.beta[s].double())[0]
+        dot, square, at = dot + float((c.y[s].double() * y).sum()), square + float(y.square().sum()), at + n
+    assert abs(dot / square - 1) <= 3e-5
