@@ -839,11 +839,14 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
                 const int nt = 2 * j + hf;
                 const float2 ek = *reinterpret_cast<const float2 *>(rec->egk + nt * 8 + tq * 2);
                 const float2 eg = *reinterpret_cast<const float2 *>(rec->eg + nt * 8 + tq * 2);
-                X[nt][0] = __uint_as_float(v[2 * hf] << 16) - ek.x * (X[nt][0] * sd0);
-                X[nt][1] = __uint_as_float(v[2 * hf] & 0xffff0000u) - ek.y * (X[nt][1] * sd0);
-                X[nt][2] = __uint_as_float(v[2 * hf + 1] << 16) - ek.x * (X[nt][2] * sd1);
-                X[nt][3] = __uint_as_float(v[2 * hf + 1] & 0xffff0000u) - ek.y * (X[nt][3] * sd1);
-                Z[nt][0] *= eg.x * sd0, Z[nt][1] *= eg.y * sd0, Z[nt][2] *= eg.x * sd1, Z[nt][3] *= eg.y * sd1;
+                // the vectors' powers of two and the rows' first: their product is near 1, the sums alone may not fit
+                X[nt][0] = __uint_as_float(v[2 * hf] << 16) - ek.x * sd0 * X[nt][0];
+                X[nt][1] = __uint_as_float(v[2 * hf] & 0xffff0000u) - ek.y * sd0 * X[nt][1];
+                X[nt][2] = __uint_as_float(v[2 * hf + 1] << 16) - ek.x * sd1 * X[nt][2];
+                X[nt][3] = __uint_as_float(v[2 * hf + 1] & 0xffff0000u) - ek.y * sd1 * X[nt][3];
+                const float2 sq = *reinterpret_cast<const float2 *>(rec->sq + nt * 8 + tq * 2);
+                Z[nt][0] *= eg.x * sq.x * sd0, Z[nt][1] *= eg.y * sq.y * sd0;
+                Z[nt][2] *= eg.x * sq.x * sd1, Z[nt][3] *= eg.y * sq.y * sd1;
             }
         }
         // u^T = R^T T^T; T is lower triangular.  u carries its key's power of two.
@@ -906,8 +909,8 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
                 const float2 sq = *reinterpret_cast<const float2 *>(rec->sq + nt * 8 + tq * 2);
-                Z[nt][0] = (Z[nt][0] + X[nt][0] * d0) * sq.x, Z[nt][1] = (Z[nt][1] + X[nt][1] * d0) * sq.y;
-                Z[nt][2] = (Z[nt][2] + X[nt][2] * d1) * sq.x, Z[nt][3] = (Z[nt][3] + X[nt][3] * d1) * sq.y;
+                Z[nt][0] += d0 * sq.x * X[nt][0], Z[nt][1] += d0 * sq.y * X[nt][1];
+                Z[nt][2] += d1 * sq.x * X[nt][2], Z[nt][3] += d1 * sq.y * X[nt][3];
             }
         }
         // S^T = e^(G_C) S^T + (e^(G_C - G) u)^T K, summed at u's row scale.  Where u is

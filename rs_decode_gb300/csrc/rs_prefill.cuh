@@ -78,11 +78,12 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
 
 // The power of two that brings a row whose largest magnitude is m into
-// [2^K, 2^(K+1)), and its inverse; 1 where m is not finite.
+// [2^K, 2^(K+1)), and its inverse.  A bound that is no longer finite counts as 2^128,
+// which no finite value reaches; a value that is not finite stays so at any scale.
 template <int K>
 __device__ __forceinline__ void row_scale(float m, float &up, float &down) {
     const int e = (int)(__float_as_uint(m) >> 23) & 255;
-    const int u = e == 255 ? 127 : min(254 + K - e, 253);  // biased exponent; its inverse is 254 - u >= 1
+    const int u = min(254 + K - e, 253);  // biased exponent; its inverse is 254 - u >= 1
     up = __uint_as_float((uint32_t)max(u, 1) << 23);
     down = __uint_as_float((uint32_t)(254 - max(u, 1)) << 23);
 }

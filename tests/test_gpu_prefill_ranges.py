@@ -48,6 +48,14 @@ def test_large_states_where_nothing_is_written(d, what):
     c.check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_states_near_the_end_of_fp32(d):
+    """The bound of |S k| passes what fp32 holds, the products themselves do not."""
+    c = scaled(Case([200, 13], 4, 2, d, alpha="slow", seed=22), 2e38)
+    c.run()
+    c.check()
+
+
 # ----------------------------------------------------------------------------- outputs beside what enters them
 # An output is a sum of terms of S q and P u.  Its error besides the rounding to
 # bf16 is that of fp32 sums and of operands held to 22 bits, 5e-6 of the terms'
