@@ -91,6 +91,7 @@ typedef enum {
 #define RS_DEV_BLOCKS 0x20u        /* a state-cache block found no free slot or no place in the block table */
 #define RS_DEV_RECORDS 0x40u       /* a prefill continues a row with records buffered; request skipped    */
 #define RS_DEV_SLOT 0x80u          /* a row, start slot or block slot out of range; request (or block) skipped */
+#define RS_DEV_GATE 0x100u         /* a prefill's gates grow too much within a chunk; request's results invalid  */
 
 /* RS_KDA: Gated DeltaNet with one decay per key channel, alpha_t in R^N
  * (a reading of Kimi Delta Attention, which [CSI] "Limits" names as
@@ -454,7 +455,10 @@ rs_status rs_qk_norm(const rs_qk_desc *desc, const uint16_t *q, const uint16_t *
 
 /* Inputs of a prefill: packed rows q, k [rows][G][N] and v [rows][H][P] bf16
  * with row strides in elements (multiples of 8), alpha >= 0 and beta fp32
- * [rows][H]. */
+ * [rows][H].  alpha is at most 1 in a decaying layer.  Above it, requests of up
+ * to 12 rows take any value; in longer ones the products of consecutive rows'
+ * alpha may reach 2^6 within a chunk (RS_DEV_GATE otherwise, and what the call
+ * writes for that request is not to be used). */
 typedef struct {
     const uint16_t *q, *k, *v;
     const float *alpha, *beta;

@@ -20,7 +20,7 @@ MAMBA2, GDN, KDA = 0, 1, 2
 PREC_FP32, PREC_TWO, PREC_SHARED_BF16 = 0, 1, 2
 U_BF16 = 0x10  # flag: GDN records keep u in bf16
 DEV_CAPACITY, DEV_ACCEPT, DEV_DRAFTS_PENDING = 0x1, 0x2, 0x4
-DEV_TIMEOUT, DEV_LENGTH, DEV_BLOCKS, DEV_RECORDS, DEV_SLOT = 0x8, 0x10, 0x20, 0x40, 0x80
+DEV_TIMEOUT, DEV_LENGTH, DEV_BLOCKS, DEV_RECORDS, DEV_SLOT, DEV_GATE = 0x8, 0x10, 0x20, 0x40, 0x80, 0x100
 NORM_NONE, NORM_L2, NORM_RMS = 0, 1, 2
 CHUNK = 64  # rows of a chunk of the ragged prefill
 STATUS = {0: "RS_OK", 1: "RS_ERR_INVALID_ARG", 2: "RS_ERR_UNSUPPORTED", 3: "RS_ERR_CAPACITY",

@@ -28,6 +28,8 @@
 //
 // Decays enter as differences G_i - G_j only, so nothing overflows however
 // long a chunk's decay is; alpha = 0 is a decay of 2^-160, which is 0 in fp32.
+// Growth (alpha > 1) by more than 2^6 within a chunk would pass fp16's range in P and
+// leave R and u too few bits in rows before it: it is reported.
 //
 // Precision.  The tensor cores multiply fp16 operands into fp32 sums.  Keys
 // and queries (bf16) enter as one fp16 term, each row scaled by a power of two to
@@ -247,6 +249,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             const float x = log2f(a);
             h[i] = x < -160.f ? -160.f : x;
         }
+        const bool rises = __any_sync(~0u, h[0] > 0.f || h[1] > 0.f);
         add2(h[1], l[1], h[0], l[0]);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -258,6 +261,17 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
         add2(h[0], l[0], ph, pl);
         cgh = __shfl_sync(~0u, h[1], 31), cgl = __shfl_sync(~0u, l[1], 31);
         gh[2 * lane] = h[0], gl[2 * lane] = l[0], gh[2 * lane + 1] = h[1], gl[2 * lane + 1] = l[1];
+        if (rises) {  // how far a row's sum stands above the least before it: P is below 4 D 2^6
+            float low = fminf(h[0], h[1]);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float x = __shfl_up_sync(~0u, low, o);
+                if (lane >= o) low = fminf(low, x);
+            }
+            low = __shfl_up_sync(~0u, low, 1);
+            low = lane == 0 ? 0.f : fminf(low, 0.f);
+            if (fmaxf(h[0] - low, h[1] - fminf(low, h[0])) > 6.f) atomicOr(p.status, RS_DEV_GATE);
+        }
     };
     if (warp < 2 && warp < p.rep) decays(g * p.rep + warp, vec + warp * 4 * C);
     cp_async_wait_all();

@@ -11,6 +11,7 @@ import numpy as np
 import pytest
 import torch
 
+from rs_decode_gb300 import binding as rb
 from test_gpu_prefill import TOL_BF16, Case, gdn_ref
 
 pytestmark = pytest.mark.gpu
@@ -120,3 +121,47 @@ def test_outputs_are_not_biased(d):
         y = gdn_ref(c.first_state(r), q, k, c.v[s].double(), c.alpha[s].double(), c.beta[s].double())[0]
         dot, square, at = dot + float((c.y[s].double() * y).sum()), square + float(y.square().sum()), at + n
     assert abs(dot / square - 1) <= 3e-5
+
+
+# ----------------------------------------------------------------------------- growing states
+def growing(lengths, d, alpha):
+    c = Case(lengths, 4, 2, d, seed=26)
+    if alpha == "steps":  # up and down by 2^3, twice up in a row
+        c.alpha.copy_(torch.tensor([8, 8, 1 / 64], device="cuda").repeat(c.cap // 3 + 1)[:c.cap, None].expand_as(c.alpha))
+    elif alpha == "runs":  # 2^-52 down, 2^47 up
+        c.alpha.copy_(torch.where((torch.arange(c.cap, device="cuda") // 30 % 2 == 0)[:, None], 0.3, 3.0).expand_as(c.alpha))
+    else:
+        c.alpha.fill_(alpha)
+    c.q.copy_(c.k)
+    c.run()
+    return c
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("alpha", [1.0001, 1.05, "steps"])
+def test_growth_within_a_chunk(d, alpha):
+    c = growing([100, 12, 64, 13], d, alpha)
+    c.check()
+    rows_near(c)
+    assert c.layer.status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("alpha", [1.2, 2.0, "runs"])
+def test_too_much_growth_within_a_chunk_is_reported(d, alpha):
+    c = growing([90, 64], d, alpha)
+    assert c.layer.status() == rb.DEV_GATE
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("alpha", [1.2, 4.0, "runs"])
+def test_growth_in_short_requests(d, alpha):
+    """The recurrence has no such limit, also beside a chunk that does not grow."""
+    c = growing([12, 5, 1], d, alpha)
+    c.check()
+    rows_near(c)
+    c = Case([12, 64], 4, 2, d, seed=27)
+    c.alpha[:12] = 4
+    c.run()
+    c.check()
+    assert c.layer.status() == 0
