@@ -24,10 +24,13 @@ def to_device(d: dict, device="cuda", non_blocking: bool = False) -> dict:
     return out
 
 
+BF16 = (torch.bfloat16, torch.int16)  # values, or their bit patterns
+
+
 def packed_stride(t: torch.Tensor, rows: int, heads: int, d: int, name: str) -> int:
     """Row stride in elements of a packed [rows, heads, d] bf16 tensor whose heads lie side by side."""
     shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != d or shape[0] < rows or t.element_size() != 2:
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or shape[0] < rows or t.dtype not in BF16:
         raise ValueError(f"{name} must be bf16 [{rows}, {heads}, {d}], got {t.dtype} {tuple(shape)}")
     ld, head, one = t.stride()
     if one != 1 or (head != d and heads > 1):
@@ -151,14 +154,14 @@ class Layer:
                 raise ValueError(f"{name} must be CUDA int32 [{R}]")
         n_pool = 0
         if pool is not None:
-            width = 2 if self.desc.precision & 0xf == rb.PREC_SHARED_BF16 else 4
+            types = BF16 if self.desc.precision & 0xf == rb.PREC_SHARED_BF16 else (torch.float32,)
             n_pool = pool.size(0)
-            if pool.shape != (n_pool, H, N, P) or pool.element_size() != width or not pool.is_cuda:
-                raise ValueError(f"pool must be CUDA [n, {H}, {N}, {P}] of {width}-byte values")
+            if pool.shape != (n_pool, H, N, P) or pool.dtype not in types or not pool.is_cuda:
+                raise ValueError(f"pool must be CUDA {types[0]} [n, {H}, {N}, {P}], got {pool.dtype} {tuple(pool.shape)}")
         if y is None:
             y = torch.empty((T, H, P), dtype=torch.bfloat16, device=self.base.device)
-        elif y.element_size() != 2 or y.shape[1:] != (H, P) or y.shape[0] < T:
-            raise ValueError(f"y must be bf16 [{T}, {H}, {P}]")
+        elif y.dtype not in BF16 or y.shape[1:] != (H, P) or y.shape[0] < T:
+            raise ValueError(f"y must be bf16 [{T}, {H}, {P}], got {y.dtype} {tuple(y.shape)}")
         if work is None:
             work = self.prefill_workspace(ragged, max_len)
         elif work.nbytes < self._prefill_bytes(rd, max_len):

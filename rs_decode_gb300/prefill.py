@@ -13,7 +13,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as rb
-from .layer import packed_stride
+from .layer import BF16, packed_stride
 
 NORMS = {"none": rb.NORM_NONE, "l2": rb.NORM_L2, "rms": rb.NORM_RMS}
 
@@ -89,8 +89,8 @@ def qk_norm(q: torch.Tensor | None, k: torch.Tensor | None, *, norm: str = "l2",
     elif positions is not None:
         raise ValueError("positions and inv_freq go together")
     for w in (wq, wk):
-        if w is not None and (w.element_size() != 2 or w.numel() != D or not w.is_cuda):
-            raise ValueError(f"weights must be CUDA bf16 [{D}]")
+        if w is not None and (w.dtype not in BF16 or w.numel() != D or not w.is_cuda):
+            raise ValueError(f"weights must be CUDA bf16 [{D}], got {w.dtype} {tuple(w.shape)}")
     qo, ko = out if out is not None else (None, None)
     Hq = Hk = ld_q = ld_k = ld_qo = ld_ko = 0
     pq = pk = pqo = pko = None
