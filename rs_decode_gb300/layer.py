@@ -142,22 +142,25 @@ class Layer:
         on the current stream, which then has to be the one the call runs on."""
         rd = ragged.desc
         T, R, H, G, N, P = rd.tokens_cap, rd.R, self.H, self.G, self.N, self.P
-        if not (q.is_cuda and k.is_cuda and v.is_cuda and alpha.is_cuda and beta.is_cuda):
-            raise ValueError("q, k, v, alpha and beta must be CUDA tensors")
+        dev = self.base.get_device()
+        for t, name in ((q, "q"), (k, "k"), (v, "v"), (alpha, "alpha"), (beta, "beta"), (rows, "rows"), (start, "start"),
+                        (pool, "pool"), (y, "y"), (work, "work"), (ragged.counts, "the plan")):
+            if t is not None and (dev < 0 or t.get_device() != dev):
+                raise ValueError(f"{name} must be on the layer's CUDA device")
         ld_q, ld_k, ld_v = packed_stride(q, T, G, N, "q"), packed_stride(k, T, G, N, "k"), packed_stride(v, T, H, P, "v")
         for t, name in ((alpha, "alpha"), (beta, "beta")):
             shape = t.shape
             if t.dtype is not torch.float32 or len(shape) != 2 or shape[0] < T or shape[1] != H:
                 raise ValueError(f"{name} must be float32 [{T}, {H}], got {t.dtype} {tuple(t.shape)}")
         for t, name in ((rows, "rows"), (start, "start")):
-            if t is not None and (t.dtype is not torch.int32 or t.shape != (R,) or not t.is_cuda):
-                raise ValueError(f"{name} must be CUDA int32 [{R}]")
+            if t is not None and (t.dtype is not torch.int32 or t.shape != (R,)):
+                raise ValueError(f"{name} must be int32 [{R}]")
         n_pool = 0
         if pool is not None:
             types = BF16 if self.desc.precision & 0xf == rb.PREC_SHARED_BF16 else (torch.float32,)
             n_pool = pool.size(0)
-            if pool.shape != (n_pool, H, N, P) or pool.dtype not in types or not pool.is_cuda:
-                raise ValueError(f"pool must be CUDA {types[0]} [n, {H}, {N}, {P}], got {pool.dtype} {tuple(pool.shape)}")
+            if pool.shape != (n_pool, H, N, P) or pool.dtype not in types:
+                raise ValueError(f"pool must be {types[0]} [n, {H}, {N}, {P}], got {pool.dtype} {tuple(pool.shape)}")
         if y is None:
             y = torch.empty((T, H, P), dtype=torch.bfloat16, device=self.base.device)
         elif y.dtype not in BF16 or y.shape[1:] != (H, P) or y.shape[0] < T:

@@ -37,13 +37,13 @@ class Ragged:
     def plan(self, lengths: torch.Tensor, context: torch.Tensor | None = None,
              free_blocks: torch.Tensor | None = None, stream=None) -> None:
         """lengths, context: int32 [R]; free_blocks: int32, at least n_free slots."""
-        d = self.desc
+        d, dev = self.desc, self.counts.get_device()
         for t, name in ((lengths, "lengths"), (context, "context")):
-            if t is not None and (t.dtype is not torch.int32 or t.numel() != d.R or not t.is_cuda):
-                raise ValueError(f"{name} must be CUDA int32 [{d.R}]")
+            if t is not None and (t.dtype is not torch.int32 or t.numel() != d.R or t.get_device() != dev or dev < 0):
+                raise ValueError(f"{name} must be int32 [{d.R}] on the plan's CUDA device")
         if d.block and d.n_free and (free_blocks is None or free_blocks.dtype is not torch.int32
-                                     or free_blocks.numel() < d.n_free or not free_blocks.is_cuda):
-            raise ValueError(f"free_blocks must be CUDA int32 [{d.n_free}]")
+                                     or free_blocks.numel() < d.n_free or free_blocks.get_device() != dev):
+            raise ValueError(f"free_blocks must be int32 [{d.n_free}] on the plan's CUDA device")
         rb.rs_ragged_plan(d, lengths, context, free_blocks, self.arrays, self.status_word, stream)
 
     def status(self, clear: bool = True) -> int:
@@ -74,9 +74,14 @@ def qk_norm(q: torch.Tensor | None, k: torch.Tensor | None, *, norm: str = "l2",
         raise ValueError(f"unknown norm {norm!r}")
     one = q if q is not None else k
     shape = one.shape if one is not None else ()
-    if len(shape) != 3 or not one.is_cuda or not (k is None or k.is_cuda):
+    dev = one.get_device() if one is not None else -1
+    if len(shape) != 3 or dev < 0:
         raise ValueError("q or k must be a CUDA [T, heads, D] tensor")
     T, _, D = shape
+    qo, ko = out if out is not None else (None, None)
+    for t in (k, wq, wk, positions, inv_freq, qo, ko):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors must be on one CUDA device, got {t.device} beside {one.device}")
     rot = 0
     if inv_freq is not None:
         if positions is None:
@@ -84,14 +89,11 @@ def qk_norm(q: torch.Tensor | None, k: torch.Tensor | None, *, norm: str = "l2",
         rot = 2 * inv_freq.numel()
         if inv_freq.dtype is not torch.float32 or positions.dtype is not torch.int32 or positions.numel() != T:
             raise ValueError(f"inv_freq must be float32 and positions int32 [{T}]")
-        if not (inv_freq.is_cuda and positions.is_cuda):
-            raise ValueError("inv_freq and positions must be CUDA tensors")
     elif positions is not None:
         raise ValueError("positions and inv_freq go together")
     for w in (wq, wk):
-        if w is not None and (w.dtype not in BF16 or w.numel() != D or not w.is_cuda):
-            raise ValueError(f"weights must be CUDA bf16 [{D}], got {w.dtype} {tuple(w.shape)}")
-    qo, ko = out if out is not None else (None, None)
+        if w is not None and (w.dtype not in BF16 or w.numel() != D):
+            raise ValueError(f"weights must be bf16 [{D}], got {w.dtype} {tuple(w.shape)}")
     Hq = Hk = ld_q = ld_k = ld_qo = ld_ko = 0
     pq = pk = pqo = pko = None
     if q is not None:

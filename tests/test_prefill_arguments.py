@@ -1,5 +1,5 @@
 """CPU checks that the Python calls of the ragged prefill refuse tensors that the
-kernels would misread, before anything is enqueued.
+kernels would misread or could not reach, before anything is enqueued.
 
 The tensors are fakes that say they are on a GPU; the binding's functions are
 replaced by recorders, so no call reaches the library."""
@@ -46,13 +46,14 @@ def norm_args(**kw):
 
 
 NORM_WRONG = {
-    "q": lambda: [fake(T, H, D, dtype=F16), fake(T, H, D, dtype=torch.uint16)],
-    "k": lambda: [fake(T, G, D, dtype=F16)],
-    "wq": lambda: [fake(D, dtype=F16)],
-    "wk": lambda: [fake(D, dtype=F16)],
-    "positions": lambda: [fake(T, dtype=torch.int64)],
-    "inv_freq": lambda: [fake(32, dtype=F16)],
-    "out": lambda: [(fake(T, H, D, dtype=F16), None), (None, fake(T, G, D, dtype=F16))],
+    "q": lambda: [fake(T, H, D, dtype=F16), fake(T, H, D, device="cpu"), fake(T, H, D, dtype=torch.uint16)],
+    "k": lambda: [fake(T, G, D, dtype=F16), fake(T, G, D, device="cpu")],
+    "wq": lambda: [fake(D, dtype=F16), fake(D, device="cpu")],
+    "wk": lambda: [fake(D, dtype=F16), fake(D, device="cpu")],
+    "positions": lambda: [fake(T, dtype=torch.int64), fake(T, dtype=I32, device="cpu")],
+    "inv_freq": lambda: [fake(32, dtype=F16), fake(32, dtype=F32, device="cpu")],
+    "out": lambda: [(fake(T, H, D, device="cpu"), None), (None, fake(T, G, D, device="cpu")), (fake(T, H, D, dtype=F16), None),
+                    (None, fake(T, G, D, dtype=F16)), (fake(T, H, D, device="cuda:1"), None)],
 }
 
 
@@ -87,9 +88,12 @@ def test_plan_refusals(calls):
     i = lambda n, **kw: fake(n, **{"dtype": I32, **kw})
     ragged().plan(i(R), i(R), i(5))
     assert calls == ["rs_ragged_plan"]
-    for a in ((i(R, dtype=torch.int64), i(R), i(5)), (i(R), i(R), i(4)), (i(R), i(R), None)):
+    for a in ((i(R, device="cpu"), i(R), i(5)), (i(R), i(R, device="cpu"), i(5)), (i(R), i(R), i(5, device="cpu")),
+              (i(R, dtype=torch.int64), i(R), i(5)), (i(R, device="cuda:1"), i(R), i(5)), (i(R), i(R), i(4)), (i(R), i(R), None)):
         with pytest.raises(ValueError):
             ragged().plan(*a)
+    with pytest.raises(ValueError):
+        ragged(counts=fake(4, dtype=I32, device="cpu")).plan(i(R, device="cpu"), None, i(5, device="cpu"))
     assert calls == ["rs_ragged_plan"]
 
 
@@ -111,16 +115,17 @@ def prefill_args(**kw):
 
 
 PREFILL_WRONG = {
-    "q": lambda: [fake(T, G, D, dtype=F16)],
-    "k": lambda: [fake(T, G, D, dtype=F16)],
-    "v": lambda: [fake(T, H, D, dtype=F16)],
-    "alpha": lambda: [fake(T, H)],
-    "beta": lambda: [fake(T, H, dtype=I32)],
-    "rows": lambda: [fake(R, dtype=torch.int64)],
-    "start": lambda: [fake(R + 1, dtype=I32)],
-    "pool": lambda: [fake(5, H, D, D, dtype=I32), fake(5, H, D, D)],
-    "y": lambda: [fake(T, H, D, dtype=F16), fake(T - 1, H, D)],
-    "work": lambda: [fake(1023, dtype=torch.uint8)],
+    "ragged": lambda: [ragged(counts=fake(4, dtype=I32, device="cuda:1"))],
+    "q": lambda: [fake(T, G, D, dtype=F16), fake(T, G, D, device="cpu"), fake(T, G, D, device="cuda:1")],
+    "k": lambda: [fake(T, G, D, dtype=F16), fake(T, G, D, device="cpu")],
+    "v": lambda: [fake(T, H, D, dtype=F16), fake(T, H, D, device="cpu")],
+    "alpha": lambda: [fake(T, H), fake(T, H, dtype=F32, device="cpu")],
+    "beta": lambda: [fake(T, H, dtype=I32), fake(T, H, dtype=F32, device="cpu")],
+    "rows": lambda: [fake(R, dtype=torch.int64), fake(R, dtype=I32, device="cpu")],
+    "start": lambda: [fake(R + 1, dtype=I32), fake(R, dtype=I32, device="cpu")],
+    "pool": lambda: [fake(5, H, D, D, dtype=I32), fake(5, H, D, D), fake(5, H, D, D, dtype=F32, device="cpu")],
+    "y": lambda: [fake(T, H, D, dtype=F16), fake(T, H, D, device="cpu"), fake(T, H, D, device="cuda:1"), fake(T - 1, H, D)],
+    "work": lambda: [fake(1024, dtype=torch.uint8, device="cpu"), fake(1023, dtype=torch.uint8)],
 }
 
 
@@ -143,4 +148,11 @@ def test_prefill_pool_of_a_bf16_layer(calls):
     for bad in (fake(5, H, D, D, dtype=F16), fake(5, H, D, D, dtype=F32)):
         with pytest.raises(ValueError):
             layer(rb.PREC_SHARED_BF16).prefill(**prefill_args(pool=bad))
+    assert calls == []
+
+
+def test_layer_on_the_host_is_refused(calls):
+    cpu = {k: v.cpu() if isinstance(v, torch.Tensor) else v for k, v in prefill_args().items()}
+    with pytest.raises(ValueError, match="CUDA"):
+        layer(device="cpu").prefill(**{**cpu, "ragged": ragged(counts=fake(4, dtype=I32, device="cpu"))})
     assert calls == []
