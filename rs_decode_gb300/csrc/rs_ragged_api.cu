@@ -91,6 +91,7 @@ rs_status rs_qk_norm(const rs_qk_desc *d, const uint16_t *q, const uint16_t *k, 
     if (d->rot < 0 || d->rot > d->D) return RS_ERR_INVALID_ARG;
     if (d->rot % 16) return RS_ERR_UNSUPPORTED;
     if (!(d->eps >= 0.f) || !isfinite(d->eps)) return RS_ERR_INVALID_ARG;
+    if (d->T == 0) return RS_OK;  // whose arrays may have no address
     if (d->rot && (!aligned(inv_freq, 4) || !aligned(positions, 4))) return RS_ERR_INVALID_ARG;
     if (d->Hq && (!aligned(q, 16) || !aligned(q_out, 16) || !stride_ok(d->ld_q, (int64_t)d->Hq * d->D) ||
                   !stride_ok(d->ld_qo, (int64_t)d->Hq * d->D)))
@@ -99,7 +100,6 @@ rs_status rs_qk_norm(const rs_qk_desc *d, const uint16_t *q, const uint16_t *k, 
                   !stride_ok(d->ld_ko, (int64_t)d->Hk * d->D)))
         return RS_ERR_INVALID_ARG;
     if ((wq && !aligned(wq, 16)) || (wk && !aligned(wk, 16))) return RS_ERR_INVALID_ARG;
-    if (d->T == 0) return RS_OK;
     return cuda_status(qk_norm_launch(*d, q, k, wq, wk, inv_freq, positions, q_out, k_out, (cudaStream_t)stream));
 }
 

@@ -156,3 +156,19 @@ def test_layer_on_the_host_is_refused(calls):
     with pytest.raises(ValueError, match="CUDA"):
         layer(device="cpu").prefill(**{**cpu, "ragged": ragged(counts=fake(4, dtype=I32, device="cpu"))})
     assert calls == []
+
+
+# ----------------------------------------------------------------------------- nothing to do
+def test_norm_of_no_rows():
+    """An empty tensor has no address; the descriptor is still checked."""
+    import ctypes
+
+    from rs_decode_gb300 import build
+    build.build()
+    d = rb.QkDesc(0, 4, 2, 128, rb.NORM_L2, 64, 0, 1e-6, 0.0, 1.0, 1.0, 512, 256, 512, 256)
+    assert rb.load().rs_qk_norm(ctypes.byref(d), *[None] * 9) == 0
+    d.D = 96
+    assert rb.load().rs_qk_norm(ctypes.byref(d), *[None] * 9) == 2
+    with FakeTensorMode():
+        q, k = qk_norm(fake(0, H, D), fake(0, G, D), positions=fake(0, dtype=I32), inv_freq=fake(32, dtype=F32), stream=0)
+        assert q.shape == (0, H, D) and k.shape == (0, G, D)
