@@ -49,7 +49,7 @@ class Layer:
         sz = rb.rs_state_bytes_for(self.desc)
         self.B, self.H, self.G, self.P, self.N, self.L, self.T_max = B, H, G, P, N, L, T_max
         self.cap = self.desc.capacity
-        self._prefill_sizes: dict = {}  # workspace bytes by plan shape
+        self._prefill_size = (None, 0)  # the last plan shape and its workspace bytes
         dev = torch.device(device)
         z = lambda n, dt: torch.zeros(n, dtype=dt, device=dev) if n else None
         self.ckpt_hp = z(sz.ckpt_hp // 4, torch.float32)
@@ -118,10 +118,9 @@ class Layer:
     # ---------------------------------------------------------------- prefill
     def _prefill_bytes(self, rd, max_len: int) -> int:
         key = (rd.R, rd.tokens_cap, rd.block, rd.max_blocks, rd.n_free, max_len)
-        n = self._prefill_sizes.get(key)
-        if n is None:
-            n = self._prefill_sizes[key] = rb.rs_prefill_bytes_for(self.desc, rd, max_len)
-        return n
+        if self._prefill_size[0] != key:
+            self._prefill_size = (key, rb.rs_prefill_bytes_for(self.desc, rd, max_len))
+        return self._prefill_size[1]
 
     def prefill_workspace(self, ragged, max_len: int) -> torch.Tensor | None:
         """Scratch of ``prefill`` for this plan shape; may serve many calls, one after another."""

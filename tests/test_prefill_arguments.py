@@ -172,3 +172,16 @@ def test_norm_of_no_rows():
     with FakeTensorMode():
         q, k = qk_norm(fake(0, H, D), fake(0, G, D), positions=fake(0, dtype=I32), inv_freq=fake(32, dtype=F32), stream=0)
         assert q.shape == (0, H, D) and k.shape == (0, G, D)
+
+
+# ----------------------------------------------------------------------------- what a layer keeps
+def test_a_layer_keeps_no_size_for_every_length():
+    """Servers meet any longest length; the sizes stay right, and nothing grows with their number."""
+    from rs_decode_gb300 import build
+    build.build()
+    x = Layer("gdn", 2, H, G, D, D, 16, device="cpu")
+    rd = rb.RaggedDesc(R, 5000, 0, 0, 0)
+    for n in [1, 12, 13, *range(100, 1100), 1, 13, 100]:
+        assert x._prefill_bytes(rd, n) == rb.rs_prefill_bytes_for(x.desc, rd, n)
+    kept = sum(len(v) for v in vars(x).values() if isinstance(v, (dict, list, set, tuple)))
+    assert kept < 20
