@@ -423,7 +423,7 @@ rs_status rs_ragged_plan(const rs_ragged_desc *rd, const int32_t *lengths, const
 
 typedef enum {
     RS_NORM_NONE = 0,
-    RS_NORM_L2 = 1, /* x / max(|x|, eps)                                  */
+    RS_NORM_L2 = 1, /* x / max(|x|, eps); eps below 2^-100 counts as that */
     RS_NORM_RMS = 2 /* x / sqrt(mean(x^2) + eps), times the weight if any */
 } rs_norm;
 

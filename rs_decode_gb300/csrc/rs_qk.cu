@@ -179,7 +179,10 @@ cudaError_t launch(QkParams &p, int interleaved, cudaStream_t s) {
 cudaError_t qk_norm_launch(const rs_qk_desc &d, const uint16_t *q, const uint16_t *k, const uint16_t *wq,
                            const uint16_t *wk, const float *inv_freq, const int32_t *positions, uint16_t *q_out,
                            uint16_t *k_out, cudaStream_t s) {
-    QkParams p = {d.T, d.Hq, d.Hk, d.norm, d.rot, 1, d.eps, 1.f / d.eps, d.weight_offset, d.scale_q, d.scale_k,
+    // below 2^-75 a head's squares vanish in fp32, so a smaller eps than 2^-100 decides
+    // nothing but heads of zero, which its reciprocal must not turn into 0 times infinity
+    const float inv_eps = d.eps > 0x1p-100f ? 1.f / d.eps : 0x1p100f;
+    QkParams p = {d.T, d.Hq, d.Hk, d.norm, d.rot, 1, d.eps, inv_eps, d.weight_offset, d.scale_q, d.scale_k,
                   d.ld_q, d.ld_k, d.ld_qo, d.ld_ko, q, k, wq, wk, inv_freq, positions, q_out, k_out};
     switch (d.D) {
         case 64: return launch<64>(p, d.interleaved, s);

@@ -12,6 +12,7 @@ import pytest
 import torch
 
 from rs_decode_gb300 import binding as rb
+from rs_decode_gb300.prefill import qk_norm
 from test_gpu_prefill import TOL_BF16, Case, gdn_ref
 
 pytestmark = pytest.mark.gpu
@@ -165,3 +166,14 @@ def test_growth_in_short_requests(d, alpha):
     c.run()
     c.check()
     assert c.layer.status() == 0
+
+
+# ----------------------------------------------------------------------------- norms
+@pytest.mark.parametrize("eps", [1e-39, 0.0])
+def test_norm_of_a_zero_head_with_the_smallest_eps(eps):
+    q = torch.zeros(3, 2, 128, dtype=torch.bfloat16, device="cuda")
+    q[1, 0] = 2.0
+    out, _ = qk_norm(q, None, norm="l2", eps=eps, scale_q=3.0)
+    ref = torch.zeros_like(q)
+    ref[1, 0] = 3.0 * 128 ** -0.5
+    assert torch.equal(out, ref)
