@@ -714,8 +714,9 @@ __global__ void __launch_bounds__(kChunkThreads, 4) front_kernel(const __grid_co
 // 24 requests with 2,419 rows in all, 8 heads of 64: 57 us, 2.3 us a chunk of the longest
 // chain; the warp's own products (240 of m16n8k16 a chunk, 8 clocks each) are about
 // half of that.
-template <int D, int NW>
+template <int D>
 struct ScanSmem {
+    static constexpr int NW = D / 16;  // warps of a head
     static constexpr int TILE = C * D * 2;
     static constexpr int VT = NW * C * 32;  // per warp: 64 rows of its 16 columns
     static constexpr int T = 2 * TILE + VT;
@@ -725,25 +726,23 @@ struct ScanSmem {
     static constexpr int BYTES = P + 2 * C * C * 2;
 };
 
-
-template <int D, int NW, bool OUT>
-__global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ PrefillParams p, int units) {
-    using M = ScanSmem<D, NW>;
-    constexpr int SPLIT = D / (16 * NW);  // CTAs of one head
-    constexpr int NT = NW * 32;
+template <int D, bool OUT>
+__global__ void __launch_bounds__(2 * D) scan_kernel(const __grid_constant__ PrefillParams p, int units) {
+    using M = ScanSmem<D>;
+    constexpr int NW = M::NW, NT = NW * 32;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int part = blockIdx.x % SPLIT, hr = blockIdx.x / SPLIT;
+    const int hr = blockIdx.x;
     if (blockIdx.x == 0) wait_for_launch();  // so that this launch does not end before the one it overlaps
     int q;
     const int h = hr % p.H, r = cta_request(p, hr / p.H, units, q);
     if (r < 0) return;
-    const Request rq = load_request(p, r, h == 0 && part == 0 && q == 0 && tid == 0);
+    const Request rq = load_request(p, r, h == 0 && q == 0 && tid == 0);
     if (!rq.ok) return;
     const Unit un = scan_unit<OUT>(p, hr, rq, r, q);
     if (!un.ok) return;
     const int g = h / p.rep;
-    const int col0 = (part * NW + warp) * 16;
+    const int col0 = warp * 16;
     const uint32_t s0 = smem_u32(smem);
 
     // chunk i of the request: its first row and row count
@@ -754,7 +753,7 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
         const long long row = rq.row0 + at;
         const unsigned char *kq = p.tiles + ((size_t)(rq.chunk0 + i) * p.G + g) * (2 * M::TILE);
         for (int x = tid; x < 2 * M::TILE / 16; x += NT) cp16(st + x * 16, kq + x * 16, true);
-        const uint16_t *v = p.v + row * p.ld_v + h * D + part * NW * 16;
+        const uint16_t *v = p.v + row * p.ld_v + h * D;
         for (int x = tid; x < C * NW * 2; x += NT) {
             const int t = x / (NW * 2), c = x % (NW * 2);
             cp16(st + 2 * M::TILE + (c >> 1) * (C * 32) + t * 32 + (((c & 1) ^ ((t >> 2) & 1)) << 4),
@@ -982,7 +981,7 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
                 *reinterpret_cast<uint4 *>(y + (long long)t * p.H * D + c * 8) = w;
             }
         }
-        const int slot = block_slot(p, r, rq.ctx + at + n, h == 0 && part == 0 && tid == 0);
+        const int slot = block_slot(p, r, rq.ctx + at + n, h == 0 && tid == 0);
         if (slot >= 0) {
             const size_t slab = ((size_t)slot * p.H + h) * D * D;
             if (p.prec == RS_PREC_SHARED_BF16)
@@ -1001,7 +1000,7 @@ __global__ void __launch_bounds__(NW * 32) scan_kernel(const __grid_constant__ P
     if (un.seg < un.nsegs - 1) return;
     store_state(p.hp, p.lp, ((size_t)rq.srow * p.H + h) * D * D);
     // a fresh start drops what the row had buffered (a continued row has nothing)
-    if (rq.start != -2 && h == 0 && part == 0 && tid == 0) p.base[rq.srow] = p.h[rq.srow] = p.nd[rq.srow] = 0;
+    if (rq.start != -2 && h == 0 && tid == 0) p.base[rq.srow] = p.h[rq.srow] = p.nd[rq.srow] = 0;
 }
 
 // ---------------------------------------------------------------- combine kernel
@@ -1108,24 +1107,16 @@ cudaError_t combine_launch(const PrefillParams &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int D, int NW, bool OUT>
-cudaError_t scan_launch(const PrefillParams &p, cudaStream_t s) {
-    static SmemGrants grants;
-    const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&scan_kernel<D, NW, OUT>), ScanSmem<D, NW>::BYTES, grants);
-    if (e != cudaSuccess) return e;
-    const int units = scan_units<OUT>(p);
-    return launch_after(scan_kernel<D, NW, OUT>, p.classes * p.R * p.H * units * (D / (16 * NW)), NW * 32,
-                        ScanSmem<D, NW>::BYTES, s, start_early(p), p, units);
-}
-
 template <int D, bool OUT>
 cudaError_t scans(const PrefillParams &p, cudaStream_t s) {
     if constexpr (D == 128) {
         return scan_tc_launch<OUT>(p, s);
     } else {
-        // a head on one CTA, or on two-warp CTAs where the heads alone would leave SMs idle
-        if (p.nseg == 1 && p.R * p.H <= 152) return scan_launch<D, 2, OUT>(p, s);
-        return scan_launch<D, D / 16, OUT>(p, s);
+        static SmemGrants grants;
+        const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&scan_kernel<D, OUT>), ScanSmem<D>::BYTES, grants);
+        if (e != cudaSuccess) return e;
+        const int units = scan_units<OUT>(p);
+        return launch_after(scan_kernel<D, OUT>, p.classes * p.R * p.H * units, 2 * D, ScanSmem<D>::BYTES, s, start_early(p), p, units);
     }
 }
 
