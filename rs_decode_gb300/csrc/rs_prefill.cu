@@ -1146,10 +1146,14 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t s) {
 }
 
 // Segments of a request (1: none), from what the host knows: the chains alone,
-// requests x heads, against the 304 CTAs that the GPU holds at once.  The two
-// passes cost a little over twice the work and run at half a lone CTA's pace,
-// so fewer than five segments do not pay; one shorter than eight chunks would
-// spend its time on starting up.
+// requests x heads, against the 304 CTAs that the GPU holds at once; a segment is
+// eight chunks at least, or it would spend its time on starting up.  Segmented
+// against one chain each, requests of 16,384 rows and 128-wide heads (us): 9
+// segments (32 chains) 555 and 1,200, 5 (60) 883 and 1,270, 4 (76) 1,066 and 1,332,
+// 3 (96) 1,190 and 1,400, 2 (128) 1,682 and 1,488; of 64-wide heads 432 and 789, 668
+// and 889, 826 and 934, 933 and 979, 1,318 and 1,064.  They start at five, where
+// requests of 4,096 rows gain a seventh too (4: 321 and 349, 239 and 246).  Short
+// requests beside a long one count as chains as well: the host does not know them.
 void plan_segments(const rs_layer_desc &d, const rs_ragged_desc &rd, int max_len, int &nseg, int &seglen) {
     const int chunks = (max_len < rd.tokens_cap ? max_len : rd.tokens_cap) / C + 2;
     const long long chains = (long long)rd.R * d.H;
@@ -1183,10 +1187,14 @@ cudaError_t prefill_launch(const rs_layer_desc &d, const rs_state &st, const rs_
     p.rows = in.rows, p.start = in.start, p.pool = in.pool, p.y = y, p.rec = static_cast<Record *>(work);
     p.tiles = static_cast<unsigned char *>(work) + (size_t)p.ccap * d.H * sizeof(Record);
     plan_segments(d, rd, in.max_len, p.nseg, p.seglen);
-    // passes over the requests cost a CTA each that leaves at once: only where the
-    // units are few enough for the last chain to show
+    // Passes over the requests, longest first, where the chains fill the GPU, but not so
+    // often that the last one does not show.  Prompts of 300 to 4,000 rows, four passes
+    // against one (us): 512 chains of 128-wide heads 482 and 543, 1,952 chains 1,712 and
+    // 1,812; 1,024 of 64-wide heads 696 and 827.  Below 304 they only move chains together
+    // on some SMs: 128 chains 328 and 311, of 64-wide heads 233 and 212.  A pass costs a
+    // CTA for each chain that leaves at once: 4,096 chains of 1 to 900 rows 511 and 501.
     p.maxch = (in.max_len < rd.tokens_cap ? in.max_len : rd.tokens_cap) / C + 2;
-    p.classes = p.nseg == 1 && p.R > 1 && p.maxch > 4 && (long long)p.R * p.H <= 2048 ? 4 : 1;
+    p.classes = p.nseg == 1 && p.R > 1 && p.maxch > 4 && fills_gpu(p) && (long long)p.R * p.H <= 2048 ? 4 : 1;
     p.segs = reinterpret_cast<float *>(p.tiles + (size_t)p.ccap * d.G * 2 * C * d.N * 2);
     p.maps = p.segs + (size_t)rd.R * d.H * p.nseg * d.N * d.P;
     return d.P == 128 ? launch<128>(p, s) : launch<64>(p, s);

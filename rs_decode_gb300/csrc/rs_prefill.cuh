@@ -168,10 +168,14 @@ cudaError_t launch_after(void (*kernel)(KArgs...), int grid, int block, int smem
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Requests and heads alone make a chain for each place on the GPU, two an SM.
+inline bool fills_gpu(const PrefillParams &p) { return (long long)p.R * p.H >= 304; }
+
 // CTAs that start early are placed around what still runs, so two may share an SM
-// while others stay empty: only where the chains fill the GPU twice over anyway
-// (192 chains of 64-wide heads: 102 us early, 72 after the launch before).
-inline bool start_early(const PrefillParams &p) { return p.nseg == 1 && (long long)p.R * p.H >= 304; }
+// while others stay empty: only where the chains fill the GPU anyway (192 chains of
+// 64-wide heads, 100 to 900 rows: 93 us early, 85 after the launch before; 320 of
+// 128-wide heads 115 and 121, 1,952 of 1 to 200 rows 143 and 149).
+inline bool start_early(const PrefillParams &p) { return p.nseg == 1 && fills_gpu(p); }
 
 // ---------------------------------------------------------------- segments
 // A request's chunks form one chain per head.  Where requests and heads alone
