@@ -216,6 +216,27 @@ __device__ __forceinline__ void group_sync(int grp) {  // the 64 threads of one 
         asm volatile("bar.sync 2, 64;" ::: "memory");
 }
 
+// By a warp, two rows a lane: reports a chunk whose summed log2 alpha stands more than 6
+// above the least before it, below which P stays under 4 D 2^6.
+__device__ __noinline__ void report_growth(float x0, float x1, uint32_t *status) {
+    const int lane = threadIdx.x & 31;
+    x0 = fmaxf(log2f(x0), -160.f), x1 = fmaxf(log2f(x1), -160.f) + x0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_up_sync(~0u, x1, o);
+        if (lane >= o) x0 += x, x1 += x;
+    }
+    float low = fminf(x0, x1);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_up_sync(~0u, low, o);
+        if (lane >= o) low = fminf(low, x);
+    }
+    low = __shfl_up_sync(~0u, low, 1);
+    low = lane == 0 ? 0.f : fminf(low, 0.f);
+    if (fmaxf(x0 - low, x1 - fminf(low, x0)) > 6.f) atomicOr(status, RS_DEV_GATE);
+}
+
 template <int D>
 __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsigned char *smem) {
     const int chunk = cta / p.G, g = cta - chunk * p.G;
@@ -249,7 +270,6 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             const float x = log2f(a);
             h[i] = x < -160.f ? -160.f : x;
         }
-        const bool rises = __any_sync(~0u, h[0] > 0.f || h[1] > 0.f);
         add2(h[1], l[1], h[0], l[0]);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -261,19 +281,15 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
         add2(h[0], l[0], ph, pl);
         cgh = __shfl_sync(~0u, h[1], 31), cgl = __shfl_sync(~0u, l[1], 31);
         gh[2 * lane] = h[0], gl[2 * lane] = l[0], gh[2 * lane + 1] = h[1], gl[2 * lane + 1] = l[1];
-        if (rises) {  // how far a row's sum stands above the least before it: P is below 4 D 2^6
-            float low = fminf(h[0], h[1]);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float x = __shfl_up_sync(~0u, low, o);
-                if (lane >= o) low = fminf(low, x);
-            }
-            low = __shfl_up_sync(~0u, low, 1);
-            low = lane == 0 ? 0.f : fminf(low, 0.f);
-            if (fmaxf(h[0] - low, h[1] - fminf(low, h[0])) > 6.f) atomicOr(p.status, RS_DEV_GATE);
-        }
+    };
+    // the other two warps look whether any alpha is above 1
+    auto watch = [&](int hv) {
+        const float *a = p.alpha + (long long)e.y * p.H + hv;
+        const float a0 = 2 * lane < n ? a[(long long)(2 * lane) * p.H] : 1.f, a1 = 2 * lane + 1 < n ? a[(long long)(2 * lane + 1) * p.H] : 1.f;
+        if (__any_sync(~0u, fmaxf(a0, a1) > 1.f)) report_growth(a0, a1, p.status);
     };
     if (warp < 2 && warp < p.rep) decays(g * p.rep + warp, vec + warp * 4 * C);
+    if (warp >= 2 && warp - 2 < p.rep) watch(g * p.rep + warp - 2);
     cp_async_wait_all();
     __syncthreads();
 
@@ -384,6 +400,8 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
                 out.xmax = 2.f * D * km;  // D products of a state value and a key below 2
                 bounds[2 * warp] = bounds[2 * warp + 1] = 0.f;
             }
+        } else if (r0 > 0 && warp >= 2 && warp - 2 < heads) {
+            watch(g * p.rep + r0 + warp - 2);
         }
         __syncthreads();
         // this warp's tiles of A and P
