@@ -424,7 +424,9 @@ rs_status rs_ragged_plan(const rs_ragged_desc *rd, const int32_t *lengths, const
 typedef enum {
     RS_NORM_NONE = 0,
     RS_NORM_L2 = 1, /* x / max(|x|, eps); eps below 2^-100 counts as that */
-    RS_NORM_RMS = 2 /* x / sqrt(mean(x^2) + eps), times the weight if any */
+    RS_NORM_RMS = 2 /* x / sqrt(mean(x^2) + eps), times the weight if any.
+                     * x / sqrt(sum(x^2) + e), an L2 norm with its eps inside the
+                     * root, is this with eps = e / D and a scale of D^-1/2.    */
 } rs_norm;
 
 /* Heads to norm: T rows of Hq query heads and Hk key heads of D channels, bf16.
@@ -444,7 +446,7 @@ typedef struct {
 /* Norms every head of q and k in fp32, applies weight (bf16 [D], NULL = none)
  * and scale, turns the pairs (a, b) of the first rot channels by the angle
  * t = positions[row] * inv_freq[pair], to (a cos t - b sin t, b cos t + a sin t),
- * and rounds once.  positions: device int32 [T], any value (the angle is
+ * and rounds once (a sum of squares past fp32 gives 0).  positions: device int32 [T], any value (the angle is
  * reduced exactly); inv_freq: device fp32 [rot/2], |inv_freq| < 2 pi.  A row's
  * output may take its input's place (same pointer and stride).
  * Source: [CSI] "How it works", Gated DeltaNet bullet (normed keys and
@@ -491,7 +493,10 @@ rs_status rs_prefill_bytes_for(const rs_layer_desc *desc, const rs_ragged_desc *
  * rs_prefill_bytes_for gives for the same descriptors and max_len; it need not
  * be cleared, and a call leaves nothing in it that another one needs.  States,
  * and y before its one rounding to bf16, are accurate to fp32 rounding (operands
- * of 22 bits, fp32 sums).  A NaN or an infinity stays in its request; there it
+ * of 22 bits, fp32 sums).  In requests of more than 12 rows and heads of 128
+ * the operands' bits count from a chunk's largest state and value: a state that
+ * replaces one 2^12 times as large within a chunk is 3e-6 off, 2^16 times 5e-5.
+ * A NaN or an infinity stays in its request; there it
  * may reach any row of its own chunk and all later ones.
  * Source: [CSI] "How it works", Gated DeltaNet bullet (the recurrence). */
 rs_status rs_prefill_gdn(const rs_layer_desc *desc, const rs_state *st, const rs_ragged_desc *rd, const rs_ragged *rg,

@@ -21,10 +21,14 @@
 // the state.
 //
 // Measured on a GB300 with 32 value and 16 key heads of 128 (copy peak 6.78 TB/s):
-// 256 cached requests of one row 167 us (6.45 TB/s, the states' bytes); 16 prompts
-// of 26,458 rows 485 us (chunk matrices 163, scan 312); one request of 32,768 rows
-// 1006 us (chunk matrices 197, states and maps of 9 segments 425, joining them 39,
-// scan 347).  The latter two are bound by the scan's chains, not by their 0.8 GB.
+// 256 cached requests of one row 166 us (6.5 TB/s, the states' bytes); 16 prompts
+// of 26,458 rows 485 us (chunk matrices 172, scan 317); one request of 32,768 rows
+// 1022 us (chunk matrices 205, states and maps of 9 segments 427, joining them 39,
+// scan 353).  Besides the 0.79 GB that the prompts cannot do without, the chunk
+// matrices leave 0.60 GB (26 to 34 KiB a chunk and head, 32 KiB a chunk and key head)
+// which the scan reads again: together 2.6 times the necessary bytes, at 0.63 and 0.50
+// of the copy peak in the two kernels, one after the other.  Those bytes and the
+// latency within a chunk (rs_prefill_tc.cu) bound them.
 //
 // Decays enter as differences G_i - G_j only, so nothing overflows however
 // long a chunk's decay is; alpha = 0 is a decay of 2^-160, which is 0 in fp32.
@@ -38,6 +42,12 @@
 // terms, 22 bits, scaled by a power of two likewise, so that states and outputs come
 // out at fp32 accuracy (bf16 terms would leave 16 bits at the same cost), as those of
 // the recurrence for short requests do; y is rounded once, to bf16.
+// The rows of a chunk share a scale for R and u in each value column.  In the
+// 128-wide scan it comes from a bound, some 2^8 above R, and the low terms reach 2^-39
+// below it: values that follow a far larger state which they replace within one chunk
+// keep fewer bits.  A state forgotten at row 20 of 64, 2^k times the values: the new
+// one is 3.3e-7 off for k = 6, 8.8e-7 (10), 3.3e-6 (12), 5.2e-5 (16), 8.5e-4 (20);
+// 2.8e-7 at any of these in the 64-wide scan, which scales by R itself.
 #include "rs_prefill.cuh"
 
 namespace rs {
@@ -116,10 +126,11 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
 // 64 rows would be one dependent chain of 2016 steps; the products run on the
 // tensor cores with operands split to 22 bits, since every u of the chunk
 // inherits T's accuracy.
-// 26,458 rows of 32 value and 16 key heads: 163 us at four CTAs an SM, half of the
-// issue slots and three fifths of shared memory's bandwidth used: what bounds it is
-// the latency of shared memory and of the barriers between its short phases (five
-// CTAs an SM, at 96 registers, take 171 us).
+// 26,458 rows of 32 value and 16 key heads: 172 us at four CTAs an SM, with half of the
+// issue slots, 0.65 of shared memory's bandwidth and 0.63 of the copy peak (its records
+// and tiles, 0.60 GB, and 0.2 GB of rows) in use: its writes and the latency of shared
+// memory and of the barriers between its short phases bound it together.  (Before P had
+// two terms: 163 us, and 171 at five CTAs an SM with 96 registers.)
 constexpr int kChunkThreads = 128;
 // fp32 matrices in shared memory: 16-byte rows, banks shifted by 12.  Rows 0, 2, 4, 6
 // and rows 1, 3, 5, 7 then start 8 banks apart, so a fragment whose 8 rows are taken in
@@ -579,9 +590,10 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 // registers, so that the state is read and written once, in 64-byte segments
 // with 8 KiB in flight per warp, and no warp waits for another.  One row's
 // S k, S q and k.q are summed over the lanes together; S_new q follows as
-// alpha S q + (k.q) u.  256 cached requests of 32 heads of 128: 167 us for one row,
-// 0.95 of the copy peak in the states' bytes, and 28 us more for each further row,
-// which is issue time.
+// alpha S q + (k.q) u.  256 cached requests of 32 heads of 128: 166 us for one row,
+// 0.95 of the copy peak in the states' bytes (two-precision checkpoints 204 us, 0.97;
+// bf16 135, 0.59: its loads and stores are 8 bytes a lane), and 28 us more for each
+// further row, which is issue time.
 constexpr int kStepThreads = 128;
 
 template <int D>
@@ -727,11 +739,12 @@ __global__ void __launch_bounds__(kChunkThreads, 4) front_kernel(const __grid_co
 // m16n8k16 products, whose register layout is also that of their A operand, so
 //   S^T K^T, S^T Q^T  ->  R^T  ->  u^T = R^T T^T  ->  y^T += u^T P^T,  S^T += u^T K
 // pass from product to product without leaving the registers or meeting
-// another warp.  K, Q, T, P and V come through two shared-memory stages.
+// another warp.  K, Q, T and V come through two shared-memory stages; P, needed last,
+// through one, so that two CTAs fit an SM.
 // It serves 64-wide heads, whose 64 rows would fill half of a tcgen05 product.
-// 24 requests with 2,419 rows in all, 8 heads of 64: 57 us, 2.3 us a chunk of the longest
-// chain; the warp's own products (240 of m16n8k16 a chunk, 8 clocks each) are about
-// half of that.
+// 24 requests with 2,419 rows in all, 8 heads of 64: 68 us, 2.7 us a chunk of the longest
+// chain (4.9 for each of two CTAs on an SM); the warp's own products (312 of m16n8k16 a
+// chunk, 8 clocks each) are about half of that.
 template <int D>
 struct ScanSmem {
     static constexpr int NW = D / 16;  // warps of a head

@@ -12,9 +12,9 @@ namespace prefill {
 
 constexpr int C = RS_CHUNK;
 // Rows of the longest request that the recurrence serves.  256 cached requests of
-// 32 heads of 128 (us): recurrence 166 (1 row), 236 (4), 353 (8), 597 (16), chunks
-// 489 from 9 rows on; 4 requests of 8 heads: recurrence 8.4 (9 rows), 13 (16),
-// chunks 20.
+// 32 heads of 128 (us): recurrence 166 (1 row), 247 (4), 362 (8), 471 (12), 597 (16),
+// chunks 469 from 13 rows on; with a bf16 state 135, 232, 357, 475 and 419.  4 requests
+// of 8 heads: recurrence 8.4 (9 rows), 13 (16), chunks 20.
 constexpr int kShort = 12;
 
 // What chunk_cta leaves for the scans.  All tiles have rows of 64 fp16

@@ -34,15 +34,16 @@
 // little of a large state, or small values overwrite large ones, the terms of y
 // cancel, and what is rounded off them would be left in it.
 //
-// Measured: 3.9 us a chunk for a CTA alone on its SM, 5.8 for each of two.  The
-// products are 1.6 us of the former at the tensor cores' rate (34 clocks for each
-// 128 x 64 x 16); the rest is register work, about 1,400 instructions a warp and
-// chunk at half of the issue slots, waiting on TMEM and shared-memory latency and on
-// the barriers between phases.  Tried and slower: warps specialised into a state
-// chain and outputs (4.8 us a chunk alone: one warp a scheduler hides no latency), y
-// of a chunk deferred behind the next one's X (4.9 us: Z then waits for it).  Against
-// the register-resident form of the 64-wide scan at 128 columns: 16 prompts 0.31 ms
-// instead of 0.58.
+// Measured: 4.25 us a chunk for a CTA alone on its SM, 5.95 for each of two.  The
+// tensor cores are at work for 1.3 us of it (34 clocks for each 128 x 64 x 16 product,
+// 50 where both operands are in shared memory); the rest is register work, about 1,630
+// instructions a warp and chunk at half of the issue slots, waiting on TMEM and
+// shared-memory latency and on the barriers between phases.  At 128 registers the
+// form with outputs spills 24 bytes a thread.  Tried in the first form, with y's operands as single terms (3.9 and
+// 5.8 us), and slower: warps specialised into a state chain and outputs (4.8 us a chunk
+// alone: one warp a scheduler hides no latency), y of a chunk deferred behind the next
+// one's X (4.9 us: Z then waits for it).  Against the register-resident form of the
+// 64-wide scan at 128 columns: 16 prompts 0.31 ms instead of 0.58.
 #include "rs_prefill.cuh"
 
 namespace rs {

@@ -20,9 +20,12 @@
 // absolute, against the 2^-9 of a bf16 result).
 //
 // Measured: 32,768 rows of 32 heads of 128 in 84 us, 6.36 TB/s, 0.94 of the copy
-// peak; 8,191 rows of 36 heads with weights and 64 rotated channels in 37 us,
-// 4.1 TB/s: there one wave and two thirds of warps, and the rotation's arithmetic
-// between a warp's loads, are what is left.
+// peak, and 64 heads of 64 the same; 8,192 rows of 32 heads of 256 52 us, 5.2 TB/s.
+// 8,191 rows of 36 heads of 128 with weights and 64 rotated channels 37 us, 4.1 TB/s
+// (interleaved pairs 35; heads of 64 58 us for 32,768 rows of 32, heads of 256 60 us for
+// 8,192): there one wave and two thirds of warps, and the rotation's arithmetic between
+// a warp's loads, are what is left.  Every form spills 8 to 32 bytes a thread at its
+// 48 or 64 registers.
 #include "rs_common.cuh"
 #include "rs_internal.h"
 

@@ -11,7 +11,8 @@
 // second launch.
 //
 // Measured: 256 requests of one token 6.1 us a call, 1,021 requests with 462,000
-// rows 8.2 us.
+// rows 8.2 us; 4,000 requests of one launch 13 us, 4,096 of two 21, 16,384 41 and
+// 65,535 113: there the one CTA's passes of 4,096 requests, about 6 us each, are the time.
 #include "rs_common.cuh"
 #include "rs_internal.h"
 

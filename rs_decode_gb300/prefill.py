@@ -68,7 +68,12 @@ def qk_norm(q: torch.Tensor | None, k: torch.Tensor | None, *, norm: str = "l2",
     """Norms every head of q [T, Hq, D] and k [T, Hk, D] (bf16, rows at any
     stride; either may be None) and rotates its first 2 * len(inv_freq)
     channels by positions (int32 [T]) * inv_freq (float32).  Returns the two
-    results, torch.bfloat16, in ``out`` if given (in place: out=(q, k))."""
+    results, torch.bfloat16, in ``out`` if given (in place: out=(q, k)).
+    Without out they are allocated on the current stream, which then has to be
+    the one the call runs on.
+
+    Delta-rule layers norm by x / sqrt(sum(x^2) + e): norm="rms" with
+    eps=e / D and scales of D ** -0.5 (times the query's own)."""
     kind = NORMS.get(norm)
     if kind is None:
         raise ValueError(f"unknown norm {norm!r}")
