@@ -446,9 +446,10 @@ typedef struct {
 /* Norms every head of q and k in fp32, applies weight (bf16 [D], NULL = none)
  * and scale, turns the pairs (a, b) of the first rot channels by the angle
  * t = positions[row] * inv_freq[pair], to (a cos t - b sin t, b cos t + a sin t),
- * and rounds once (a sum of squares past fp32 gives 0).  positions: device int32 [T], any value (the angle is
- * reduced exactly); inv_freq: device fp32 [rot/2], |inv_freq| < 2 pi.  A row's
- * output may take its input's place (same pointer and stride).
+ * and rounds once (a head whose squares sum past fp32's range gives 0).
+ * positions: device int32 [T], any value (the angle is reduced exactly);
+ * inv_freq: device fp32 [rot/2], |inv_freq| < 2 pi.  A row's output may take its
+ * input's place (same pointer and stride).
  * Source: [CSI] "How it works", Gated DeltaNet bullet (normed keys and
  * queries are the inputs of a step); the rotation: none. */
 rs_status rs_qk_norm(const rs_qk_desc *desc, const uint16_t *q, const uint16_t *k, const uint16_t *wq,
@@ -496,8 +497,8 @@ rs_status rs_prefill_bytes_for(const rs_layer_desc *desc, const rs_ragged_desc *
  * of 22 bits, fp32 sums).  In requests of more than 12 rows and heads of 128
  * the operands' bits count from a chunk's largest state and value: a state that
  * replaces one 2^12 times as large within a chunk is 3e-6 off, 2^16 times 5e-5.
- * A NaN or an infinity stays in its request; there it
- * may reach any row of its own chunk and all later ones.
+ * A NaN or an infinity stays in its request; there it may reach any row of its
+ * own chunk and all later ones.
  * Source: [CSI] "How it works", Gated DeltaNet bullet (the recurrence). */
 rs_status rs_prefill_gdn(const rs_layer_desc *desc, const rs_state *st, const rs_ragged_desc *rd, const rs_ragged *rg,
                          const rs_prefill *in, uint16_t *y, void *work, void *stream);
