@@ -144,7 +144,7 @@ struct ChunkSmem {
     static constexpr int TILES = 2 * C * D * 2;
     static constexpr int MATS = 2 * kMat * 4;
     static constexpr int VECS = TILES > MATS ? TILES : MATS;  // after the tiles, or the matrices in their place
-    static constexpr int BYTES = VECS + (2 + 2 * 4) * C * 4 + 2 * 16;
+    static constexpr int BYTES = VECS + (2 + 2 * 3) * C * 4;
 };
 
 // Sum of (value, error) pairs: the sum's rounding error goes into the error.
@@ -263,8 +263,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
     asm volatile("cp.async.commit_group;" ::: "memory");
 
     float *sk = reinterpret_cast<float *>(smem + ChunkSmem<D>::VECS), *sq = sk + C;
-    float *vec = sq + C;                               // per head of a pair: gh, gl, beta, ke
-    float *bounds = vec + 2 * 4 * C;                   // per head of a pair: umax, kmax
+    float *vec = sq + C;                               // per head of a pair: gh, gl, beta
     // the first pair's decays are summed while the tiles are on their way
     float h[2], l[2], cgh, cgl;
     auto decays = [&](int hv, float *v) {
@@ -299,7 +298,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
         const float a0 = 2 * lane < n ? a[(long long)(2 * lane) * p.H] : 1.f, a1 = 2 * lane + 1 < n ? a[(long long)(2 * lane + 1) * p.H] : 1.f;
         if (__any_sync(~0u, fmaxf(a0, a1) > 1.f)) report_growth(a0, a1, p.status);
     };
-    if (warp < 2 && warp < p.rep) decays(g * p.rep + warp, vec + warp * 4 * C);
+    if (warp < 2 && warp < p.rep) decays(g * p.rep + warp, vec + warp * 3 * C);
     if (warp >= 2 && warp - 2 < p.rep) watch(g * p.rep + warp - 2);
     cp_async_wait_all();
     __syncthreads();
@@ -392,7 +391,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
     for (int r0 = 0; r0 < p.rep; r0 += 2) {
         const int heads = min(2, p.rep - r0);
         if (warp < heads) {
-            float *v = vec + warp * 4 * C;
+            float *v = vec + warp * 3 * C;
             if (r0 > 0) decays(g * p.rep + r0 + warp, v);
             Record &out = p.rec[(size_t)chunk * p.H + g * p.rep + r0 + warp];
             const float e0 = exp2f(h[0] + l[0]), e1 = exp2f(h[1] + l[1]);
@@ -402,22 +401,14 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             *reinterpret_cast<float2 *>(out.eg + 2 * lane) = make_float2(e0, e1);
             *reinterpret_cast<float2 *>(out.sq + 2 * lane) = sql;
             *reinterpret_cast<float2 *>(out.ke + 2 * lane) = make_float2(k0, k1);
-            *reinterpret_cast<float2 *>(v + 3 * C + 2 * lane) = make_float2(k0, k1);
-            float km = fmaxf(e0 * skl.x, e1 * skl.y);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) km = fmaxf(km, __shfl_xor_sync(~0u, km, o));
             if (lane == 31) out.all = e1;
-            if (lane == 0) {
-                out.xmax = 2.f * D * km;  // D products of a state value and a key below 2
-                bounds[2 * warp] = bounds[2 * warp + 1] = 0.f;
-            }
         } else if (r0 > 0 && warp >= 2 && warp - 2 < heads) {
             watch(g * p.rep + r0 + warp - 2);
         }
         __syncthreads();
         // this warp's tiles of A and P
         for (int r = 0; r < heads; ++r) {
-            const float *gh = vec + r * 4 * C, *gl = gh + C, *be = gl + C;
+            const float *gh = vec + r * 3 * C, *gl = gh + C, *be = gl + C;
             float *A = mats + r * kMat;
             unsigned char *pout = reinterpret_cast<unsigned char *>(p.rec[(size_t)chunk * p.H + g * p.rep + r0 + r].p_hi);
             using f2 = unsigned long long;
@@ -536,15 +527,14 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             // T = X diag(beta), each row scaled and split in two; 8 threads a row, and in
             // every eight lanes halves of two rows, which lie on different banks
             Record &out = p.rec[(size_t)chunk * p.H + g * p.rep + r0 + grp];
-            const float *be = vec + grp * 4 * C + 2 * C, *ke = be + C;
+            const float *be = vec + grp * 3 * C + 2 * C;
             const int c = (t & 3) | (t >> 1 & 4), rl = (t >> 2 & 1) | (t >> 3 & 6);
             const ulonglong2 b0 = *reinterpret_cast<const ulonglong2 *>(be + c * 8), b1 = *reinterpret_cast<const ulonglong2 *>(be + c * 8 + 4);
             const unsigned long long bj[4] = {b0.x, b0.y, b1.x, b1.y};
-            float um = 0.f, kmx = 0.f;
 #pragma unroll 2
             for (int i = 0; i < 8; ++i) {
                 const int row = i * 8 + rl;
-                // the row's sum of magnitudes sizes its scale and bounds what it can make of R
+                // the row's sum of magnitudes sizes its scale
                 using f2 = unsigned long long;
                 ulonglong2 v0 = make_ulonglong2(0, 0), v1 = v0;
                 if (c / 2 <= i / 2) {  // right of the diagonal's block another block has waited
@@ -566,19 +556,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
                 *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(out.t_hi) + piece(row, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(out.t_lo) + piece(row, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 if (c == 0) out.su[row] = down * sk[row];
-                um = fmaxf(um, sum * sk[row]);
-                kmx = fmaxf(kmx, sum * sk[row] * ke[row]);
             }
-#pragma unroll
-            for (int o : {4, 16}) um = fmaxf(um, __shfl_xor_sync(~0u, um, o)), kmx = fmaxf(kmx, __shfl_xor_sync(~0u, kmx, o));
-            if (lane == 0) {
-                // non-negative floats compare as integers, so the order of the two warps does not matter
-                atomicMax(reinterpret_cast<int *>(bounds + 2 * grp), __float_as_int(um));
-                atomicMax(reinterpret_cast<int *>(bounds + 2 * grp + 1), __float_as_int(kmx));
-            }
-            group_sync(grp);
-            // 0 where nothing is written (beta = 0, or a reset after it): the scan divides by these
-            if (t == 0) out.umax = fmaxf(bounds[2 * grp], kLeastBound), out.kmax = fmaxf(bounds[2 * grp + 1], kLeastBound);
         }
         __syncthreads();
     }

@@ -32,20 +32,13 @@ struct Record {
     float sq[C];   // query i's power of two
     float ke[C];  // e^(G_C - G_i)
     float all;     // e^(G_C)
-    // Bounds that size the scales of operands before the operands are known:
-    float xmax;  // |e^G S^T K^T| of a state row of largest magnitude 1
-    float umax;  // |u| (with its key's power of two) of an R row of largest magnitude 1
-    float kmax;  // the same of e^(G_C - G) u
-    float pad[28];
+    float pad[31];
 };
-// Least umax and kmax: the quotient of R's and u's scales stays finite in fp32
-// (at most 2^121), and what is below it is lost beside any R.
-constexpr float kLeastBound = 7.5231638452626401e-37f;  // 2^-120
 constexpr int kRecMats = 4 * C * C * 2;                   // bytes of the matrices, then
 constexpr int kRecVecs = (int)sizeof(Record) - kRecMats;  // of the vectors
 static_assert(sizeof(Record) == 34176, "records are copied in 16-byte pieces");
 struct Vecs {  // the vectors of a Record
-    float egk[C], eg[C], su[C], sq[C], ke[C], all, xmax, umax, kmax, pad[28];
+    float egk[C], eg[C], su[C], sq[C], ke[C], all, pad[31];
 };
 static_assert(sizeof(Vecs) == kRecVecs, "");
 

@@ -306,15 +306,18 @@ __device__ __forceinline__ void issue_y(uint32_t tm, uint32_t uh, uint32_t ul, u
     umma_commit(&b->my);
 }
 
-// The larger of the values of a row's two threads (warps w and w + 4).
-__device__ __forceinline__ float pair_max(float *m, int hf, int row, int warp, float x) {
-    m[hf * D + row] = x;
+// A barrier of a row's two threads (warps w and w + 4), and the larger of their values.
+__device__ __forceinline__ void pair_sync(int warp) {
     switch (warp & 3) {
         case 0: asm volatile("bar.sync 1, 64;" ::: "memory"); break;
         case 1: asm volatile("bar.sync 2, 64;" ::: "memory"); break;
         case 2: asm volatile("bar.sync 3, 64;" ::: "memory"); break;
         default: asm volatile("bar.sync 4, 64;" ::: "memory"); break;
     }
+}
+__device__ __forceinline__ float pair_max(float *m, int hf, int row, int warp, float x) {
+    m[hf * D + row] = x;
+    pair_sync(warp);
     return fmaxf(x, m[(hf ^ 1) * D + row]);
 }
 
@@ -437,21 +440,13 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
         }
         // V's column, while X is computed
         uint32_t v[CH / 2];
-        float vmax = 0.f;
         if (u.map) {
 #pragma unroll
             for (int t = 0; t < CH / 2; ++t) v[t] = 0;
         } else {
-            __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
             const uint16_t *src = reinterpret_cast<const uint16_t *>(smem + Smem::V) + hf * CH * D + row;
 #pragma unroll
-            for (int t = 0; t < CH; t += 2) {
-                const uint32_t a = src[t * D], c = src[t * D + D];
-                v[t / 2] = __byte_perm(a, c, 0x5410);
-                const uint32_t mag = v[t / 2] & 0x7fff7fffu;
-                m2 = __hmax2(m2, *reinterpret_cast<const __nv_bfloat162 *>(&mag));
-            }
-            vmax = pair_max(rowmax + 2 * D, hf, row, warp, fmaxf(__low2float(m2), __high2float(m2)));
+            for (int t = 0; t < CH; t += 2) v[t / 2] = __byte_perm(src[t * D], src[t * D + D], 0x5410);
         }
         if (OUT && warp == 4) {  // Z, behind X
             ok = wait_warp(&b->full_q, ph, b, p.status) && ok;
@@ -459,26 +454,35 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
             if (elect_one()) issue_z(base, desc_lo(sm + Smem::Q), b);
             __syncwarp();
         }
-        // |R| <= |V| + e^G |X|: the bound may be far above R; the split's low terms reach 2^-39 below it
-        const float rbound = fmaf(vec.xmax, smax, vmax);
-        float rup, rdown;
-        row_scale<14>(rbound, rup, rdown);
-        const unsigned long long nsdown = f2_pack(-sdown, -sdown);
         ok = wait_warp(&b->mx, ph, b, p.status) && ok;
         tc_fence_after_sync();
+        // R, at a scale from its own largest magnitude: a bound from |S| and |k| is 2^6 and more
+        // above it, and a small R behind a large one would lose those bits
+        const unsigned long long nsdown = f2_pack(-sdown, -sdown);
+        f2 R[CH / 2];
+        float rmax = 0.f;
 #pragma unroll
         for (int t = 0; t < CH; t += 16) {
             f2 x[8];
             ld16(t_r + t, x);
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const ulonglong2 ek = *reinterpret_cast<const ulonglong2 *>(vec.egk + hf * CH + t + e);
-                const uint32_t v0 = v[(t + e) / 2], v1 = v[(t + e) / 2 + 1];
-                x[e / 2] = f2_fma(x[e / 2], f2_mul(ek.x, nsdown), (f2)(v0 & 0xffff0000u) << 32 | v0 << 16);
-                x[e / 2 + 1] = f2_fma(x[e / 2 + 1], f2_mul(ek.y, nsdown), (f2)(v1 & 0xffff0000u) << 32 | v1 << 16);
+            for (int e = 0; e < 8; e += 2) {
+                const ulonglong2 ek = *reinterpret_cast<const ulonglong2 *>(vec.egk + hf * CH + t + 2 * e);
+                const uint32_t v0 = v[t / 2 + e], v1 = v[t / 2 + e + 1];
+                R[t / 2 + e] = f2_fma(x[e], f2_mul(ek.x, nsdown), (f2)(v0 & 0xffff0000u) << 32 | v0 << 16);
+                R[t / 2 + e + 1] = f2_fma(x[e + 1], f2_mul(ek.y, nsdown), (f2)(v1 & 0xffff0000u) << 32 | v1 << 16);
+                float a, c;
+                f2_unpack(R[t / 2 + e], a, c);
+                rmax = max_abs3(rmax, a, c);
+                f2_unpack(R[t / 2 + e + 1], a, c);
+                rmax = max_abs3(rmax, a, c);
             }
-            put_split(t_r + t, t_r + t + 8, x, f2_pack(rup, rup));
         }
+        rmax = pair_max(rowmax + 2 * D, hf, row, warp, rmax);
+        float rup, rdown;
+        row_scale<14>(rmax, rup, rdown);
+#pragma unroll
+        for (int t = 0; t < CH; t += 16) put_split(t_r + t, t_r + t + 8, R + t / 2, f2_pack(rup, rup));
         st_done();
         tc_fence_before_sync();
         if (__syncthreads_or(!ok)) { ok = false; break; }
@@ -490,31 +494,55 @@ __device__ __forceinline__ void scan_head(const PrefillParams &p, const Request 
             if (elect_one()) issue_u(base, desc_lo(sm + Smem::T), b);
             __syncwarp();
         }
-        // u, with its key's power of two: for y, and with e^(G_C - G) for the state.  Y's
-        // sums start from e^G Z at u's scale: where u is below 2^-30 of the state, the
-        // state's size sets that scale, so that they stay in range.
-        const float ubound = fmaxf(vec.umax * rbound, smax * 9.31322574615478515625e-10f), kbound = vec.kmax * rbound;
-        float uup, udown, kup, kdown;
-        row_scale<14>(ubound, uup, udown);
-        row_scale<14>(kbound, kup, kdown);
-        const float uups = uup * rdown, kups = kup * rdown;  // from R's scale to u's
-        const f2 uup2 = f2_pack(uups, uups);
         ok = wait_warp(&b->mu, ph, b, p.status) && ok;
         if (OUT) ok = wait_warp(&b->mz, ph, b, p.status) && ok;
         tc_fence_after_sync();
+        // u, with its key's power of two: for y, and with e^(G_C - G) for the state, each at a
+        // scale from its own largest magnitude, as R
+        f2 U[CH / 2];
+        float umax = 0.f, kmax = 0.f;
+#pragma unroll
+        for (int t = 0; t < CH; t += 16) {
+            f2 x[8];
+            ld16(t_u + t, x);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const ulonglong2 su = *reinterpret_cast<const ulonglong2 *>(vec.su + hf * CH + t + 2 * e);
+                const ulonglong2 ke = *reinterpret_cast<const ulonglong2 *>(vec.ke + hf * CH + t + 2 * e);
+                const f2 u0 = U[t / 2 + e] = f2_mul(x[e], su.x), u1 = U[t / 2 + e + 1] = f2_mul(x[e + 1], su.y);
+                float a, c;
+                if (OUT) {
+                    f2_unpack(u0, a, c);
+                    umax = max_abs3(umax, a, c);
+                    f2_unpack(u1, a, c);
+                    umax = max_abs3(umax, a, c);
+                }
+                f2_unpack(f2_mul(u0, ke.x), a, c);
+                kmax = max_abs3(kmax, a, c);
+                f2_unpack(f2_mul(u1, ke.y), a, c);
+                kmax = max_abs3(kmax, a, c);
+            }
+        }
+        // (the state's and R's maxima are read by now, by all threads)
+        if (OUT) rowmax[hf * D + row] = umax;
+        kmax = pair_max(rowmax + 2 * D, hf, row, warp, kmax);
+        if (OUT) umax = fmaxf(umax, rowmax[(hf ^ 1) * D + row]);
+        // Where nothing is written u is 0: a least bound keeps the quotients of the scales
+        // in range.  Y's sums start from e^G Z at u's scale: where u is below 2^-30 of the
+        // state, the state's size sets it, so that they stay in range too.
+        const float least = rmax * 7.88860905221011805411728565283e-31f;  // 2^-100
+        float uup, udown, kup, kdown;
+        row_scale<14>(fmaxf(umax * rdown, fmaxf(least, smax * 9.31322574615478515625e-10f)), uup, udown);
+        row_scale<14>(fmaxf(kmax * rdown, least), kup, kdown);
+        const float uups = uup * rdown, kups = kup * rdown;  // from R's scale to u's
+        const f2 uup2 = f2_pack(uups, uups);
         if (!OUT && i + 1 < nch && warp == 7) load_t(b, sm, i + 1, p.H);
         // u for Y takes the places of the queries and of T, whose products are complete
         unsigned char *const urow = smem + Smem::Q + row * 128;
         static_assert(Smem::T == Smem::Q + kTile, "u lo lies behind u hi");
 #pragma unroll
         for (int t = 0; t < CH; t += 16) {
-            f2 x[8];
-            ld16(t_u + t, x);
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const ulonglong2 su = *reinterpret_cast<const ulonglong2 *>(vec.su + hf * CH + t + e);
-                x[e / 2] = f2_mul(x[e / 2], su.x), x[e / 2 + 1] = f2_mul(x[e / 2 + 1], su.y);
-            }
+            f2 *const x = U + t / 2;
             if (OUT) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {

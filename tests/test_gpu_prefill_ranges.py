@@ -58,6 +58,18 @@ def test_states_near_the_end_of_fp32(d):
     c.check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("k,rows", [(12, 1), (16, 1), (20, 1), (12, 8), (16, 8)])
+def test_states_that_replace_far_larger_ones(d, k, rows):
+    """A state 2^k times the values, forgotten in the middle of a chunk, at once or over eight rows:
+    what is written behind it is as accurate as ever."""
+    c = scaled(Case([64, 150], 4, 2, d, alpha="slow", seed=3), 10 * 2.0 ** k)
+    for at in (20, 64 + 20, 64 + 100):
+        c.alpha[at:at + rows] = 0 if rows == 1 else 2.0 ** (-2 * k / rows)
+    c.run()
+    c.check()
+
+
 # ----------------------------------------------------------------------------- outputs beside what enters them
 # An output is a sum of terms of S q and P u.  Its error besides the rounding to
 # bf16 is that of fp32 sums and of operands held to 22 bits, 5e-6 of the terms'
