@@ -22,11 +22,11 @@
 //
 // Measured on a GB300 with 32 value and 16 key heads of 128 (copy peak 6.78 TB/s):
 // 256 cached requests of one row 166 us (6.5 TB/s, the states' bytes); 16 prompts
-// of 26,458 rows 485 us (chunk matrices 172, scan 317); one request of 32,768 rows
-// 1022 us (chunk matrices 205, states and maps of 9 segments 427, joining them 39,
-// scan 353).  Besides the 0.79 GB that the prompts cannot do without, the chunk
+// of 26,458 rows 496 us (chunk matrices 166, scan 335); one request of 32,768 rows
+// 1078 us (chunk matrices 198, states and maps of 9 segments 469, joining them 39,
+// scan 374).  Besides the 0.79 GB that the prompts cannot do without, the chunk
 // matrices leave 0.60 GB (26 to 34 KiB a chunk and head, 32 KiB a chunk and key head)
-// which the scan reads again: together 2.6 times the necessary bytes, at 0.63 and 0.50
+// which the scan reads again: together 2.6 times the necessary bytes, at 0.65 and 0.48
 // of the copy peak in the two kernels, one after the other.  Those bytes and the
 // latency within a chunk (rs_prefill_tc.cu) bound them.
 //
@@ -42,12 +42,11 @@
 // terms, 22 bits, scaled by a power of two likewise, so that states and outputs come
 // out at fp32 accuracy (bf16 terms would leave 16 bits at the same cost), as those of
 // the recurrence for short requests do; y is rounded once, to bf16.
-// The rows of a chunk share a scale for R and u in each value column.  In the
-// 128-wide scan it comes from a bound, some 2^8 above R, and the low terms reach 2^-39
-// below it: values that follow a far larger state which they replace within one chunk
-// keep fewer bits.  A state forgotten at row 20 of 64, 2^k times the values: the new
-// one is 3.3e-7 off for k = 6, 8.8e-7 (10), 3.3e-6 (12), 5.2e-5 (16), 8.5e-4 (20);
-// 2.8e-7 at any of these in the 64-wide scan, which scales by R itself.
+// The rows of a chunk share a scale for R and u in each value column, from its largest
+// magnitude; the low terms reach 2^-39 below it, so values that follow a far larger
+// state which they replace within one chunk keep fewer bits in the end.  A state
+// forgotten at row 20 of 64, 2^k times the values: the new one is 3.3e-7 off up to
+// k = 20, 4.1e-6 at 24, 2.2e-4 at 28.
 #include "rs_prefill.cuh"
 
 namespace rs {
@@ -126,8 +125,8 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const uint16_t *src, lon
 // 64 rows would be one dependent chain of 2016 steps; the products run on the
 // tensor cores with operands split to 22 bits, since every u of the chunk
 // inherits T's accuracy.
-// 26,458 rows of 32 value and 16 key heads: 172 us at four CTAs an SM, with half of the
-// issue slots, 0.65 of shared memory's bandwidth and 0.63 of the copy peak (its records
+// 26,458 rows of 32 value and 16 key heads: 166 us at four CTAs an SM, with half of the
+// issue slots, 0.65 of shared memory's bandwidth and 0.65 of the copy peak (its records
 // and tiles, 0.60 GB, and 0.2 GB of rows) in use: its writes and the latency of shared
 // memory and of the barriers between its short phases bound it together.  (Before P had
 // two terms: 163 us, and 171 at five CTAs an SM with 96 registers.)
@@ -1158,10 +1157,10 @@ cudaError_t launch(const PrefillParams &p, cudaStream_t s) {
 // requests x heads, against the 304 CTAs that the GPU holds at once; a segment is
 // eight chunks at least, or it would spend its time on starting up.  Segmented
 // against one chain each, requests of 16,384 rows and 128-wide heads (us): 9
-// segments (32 chains) 555 and 1,200, 5 (60) 883 and 1,270, 4 (76) 1,066 and 1,332,
-// 3 (96) 1,190 and 1,400, 2 (128) 1,682 and 1,488; of 64-wide heads 432 and 789, 668
-// and 889, 826 and 934, 933 and 979, 1,318 and 1,064.  They start at five, where
-// requests of 4,096 rows gain a seventh too (4: 321 and 349, 239 and 246).  Short
+// segments (32 chains) 579 and 1,244, 5 (60) 918 and 1,322, 4 (76) 1,117 and 1,365,
+// 3 (96) 1,229 and 1,422, 2 (128) 1,744 and 1,513; of 64-wide heads 425 and 770, 660
+// and 843, 811 and 882, 919 and 928, 1,301 and 1,008.  They start at five, where
+// requests of 4,096 rows gain a tenth and more too (4: 335 and 358, 237 and 233).  Short
 // requests beside a long one count as chains as well: the host does not know them.
 void plan_segments(const rs_layer_desc &d, const rs_ragged_desc &rd, int max_len, int &nseg, int &seglen) {
     const int chunks = (max_len < rd.tokens_cap ? max_len : rd.tokens_cap) / C + 2;
@@ -1198,10 +1197,10 @@ cudaError_t prefill_launch(const rs_layer_desc &d, const rs_state &st, const rs_
     plan_segments(d, rd, in.max_len, p.nseg, p.seglen);
     // Passes over the requests, longest first, where the chains fill the GPU, but not so
     // often that the last one does not show.  Prompts of 300 to 4,000 rows, four passes
-    // against one (us): 512 chains of 128-wide heads 482 and 543, 1,952 chains 1,712 and
-    // 1,812; 1,024 of 64-wide heads 696 and 827.  Below 304 they only move chains together
-    // on some SMs: 128 chains 328 and 311, of 64-wide heads 233 and 212.  A pass costs a
-    // CTA for each chain that leaves at once: 4,096 chains of 1 to 900 rows 511 and 501.
+    // against one (us): 512 chains of 128-wide heads 483 and 547, 1,952 chains 1,727 and
+    // 1,833; 1,024 of 64-wide heads 684 and 807.  Below 304 they only move chains together
+    // on some SMs: 128 chains 332 and 315, of 64-wide heads 230 and 207.  A pass costs a
+    // CTA for each chain that leaves at once: 4,096 chains of 1 to 900 rows 516 and 507.
     p.maxch = (in.max_len < rd.tokens_cap ? in.max_len : rd.tokens_cap) / C + 2;
     p.classes = p.nseg == 1 && p.R > 1 && p.maxch > 4 && fills_gpu(p) && (long long)p.R * p.H <= 2048 ? 4 : 1;
     p.segs = reinterpret_cast<float *>(p.tiles + (size_t)p.ccap * d.G * 2 * C * d.N * 2);

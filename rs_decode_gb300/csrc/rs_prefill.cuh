@@ -13,7 +13,7 @@ namespace prefill {
 constexpr int C = RS_CHUNK;
 // Rows of the longest request that the recurrence serves.  256 cached requests of
 // 32 heads of 128 (us): recurrence 166 (1 row), 247 (4), 362 (8), 471 (12), 597 (16),
-// chunks 469 from 13 rows on; with a bf16 state 135, 232, 357, 475 and 419.  4 requests
+// chunks 474 from 13 rows on; with a bf16 state 135, 232, 358, 475 (12), chunks 424.  4 requests
 // of 8 heads: recurrence 8.4 (9 rows), 13 (16), chunks 20.
 constexpr int kShort = 12;
 
@@ -166,8 +166,8 @@ inline bool fills_gpu(const PrefillParams &p) { return (long long)p.R * p.H >= 3
 
 // CTAs that start early are placed around what still runs, so two may share an SM
 // while others stay empty: only where the chains fill the GPU anyway (192 chains of
-// 64-wide heads, 100 to 900 rows: 93 us early, 85 after the launch before; 320 of
-// 128-wide heads 115 and 121, 1,952 of 1 to 200 rows 143 and 149).
+// 64-wide heads, 100 to 900 rows: 92 us early, 84 after the launch before; 320 of
+// 128-wide heads 119 and 124, 1,952 of 1 to 200 rows 145 and 151).
 inline bool start_early(const PrefillParams &p) { return p.nseg == 1 && fills_gpu(p); }
 
 // ---------------------------------------------------------------- segments

@@ -34,16 +34,18 @@
 // little of a large state, or small values overwrite large ones, the terms of y
 // cancel, and what is rounded off them would be left in it.
 //
-// Measured: 4.25 us a chunk for a CTA alone on its SM, 5.95 for each of two.  The
+// Measured: 4.46 us a chunk for a CTA alone on its SM, 6.29 for each of two.  The
 // tensor cores are at work for 1.3 us of it (34 clocks for each 128 x 64 x 16 product,
-// 50 where both operands are in shared memory); the rest is register work, about 1,630
+// 50 where both operands are in shared memory); the rest is register work, about 1,700
 // instructions a warp and chunk at half of the issue slots, waiting on TMEM and
-// shared-memory latency and on the barriers between phases.  At 128 registers the
-// form with outputs spills 24 bytes a thread.  Tried in the first form, with y's operands as single terms (3.9 and
-// 5.8 us), and slower: warps specialised into a state chain and outputs (4.8 us a chunk
-// alone: one warp a scheduler hides no latency), y of a chunk deferred behind the next
-// one's X (4.9 us: Z then waits for it).  Against the register-resident form of the
-// 64-wide scan at 128 columns: 16 prompts 0.31 ms instead of 0.58.
+// shared-memory latency and on the barriers between phases.  At 128 registers 12 bytes
+// a thread spill, 32 in the form with outputs.  Scales of R and u from bounds that are
+// known before their values (4.25 and 5.95 us) cost small values their bits.  Tried in
+// the first form, with those and y's operands as single terms (3.9 and 5.8 us), and
+// slower: warps specialised into a state chain and outputs (4.8 us a chunk alone: one
+// warp a scheduler hides no latency), y of a chunk deferred behind the next one's X
+// (4.9 us: Z then waits for it).  Against the register-resident form of the 64-wide
+// scan at 128 columns: 16 prompts 0.31 ms instead of 0.58.
 #include "rs_prefill.cuh"
 
 namespace rs {
