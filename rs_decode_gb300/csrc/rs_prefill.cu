@@ -533,7 +533,8 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 #pragma unroll 2
             for (int i = 0; i < 8; ++i) {
                 const int row = i * 8 + rl;
-                // the row's sum of magnitudes sizes its scale
+                // the row's sum of magnitudes sizes its scale: no element passes 2^15, and those
+                // that a decay has made small keep their bits, as what they multiply may be large
                 using f2 = unsigned long long;
                 ulonglong2 v0 = make_ulonglong2(0, 0), v1 = v0;
                 if (c / 2 <= i / 2) {  // right of the diagonal's block another block has waited
@@ -548,7 +549,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
                 for (int x = 0; x < 8; ++x) sum += fabsf(v[x]);
 #pragma unroll
                 for (int o : {1, 2, 8}) sum += __shfl_xor_sync(~0u, sum, o);
-                row_scale<8>(sum, up, down);
+                row_scale<14>(sum, up, down);
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) split_cut(v[2 * x] * up, v[2 * x + 1] * up, hi[x], lo[x]);

@@ -70,6 +70,19 @@ def test_states_that_replace_far_larger_ones(d, k, rows):
     c.check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("k,rows", [(13, 8), (14, 8), (14, 30), (18, 12)])
+def test_large_states_that_fade(d, k, rows):
+    """A state 2^k times the values that fades by 2^-2k within a chunk: rows on the way down are sums of
+    small multiples of large values."""
+    c = scaled(Case([64], 4, 2, d, alpha="slow", seed=3), 10 * 2.0 ** k)
+    c.alpha[20:20 + rows] = 2.0 ** (-2 * k / rows)
+    c.run()
+    row = int(c.rows[0])
+    x = [t.double() for t in (c.q.repeat_interleave(2, 1), c.k.repeat_interleave(2, 1), c.v, c.alpha, c.beta)]
+    c.near(c.state()[row].double(), gdn_ref(c.first_state(0), *x)[1], 5e-6, "state")
+
+
 # ----------------------------------------------------------------------------- outputs beside what enters them
 # An output is a sum of terms of S q and P u.  Its error besides the rounding to
 # bf16 is that of fp32 sums and of operands held to 22 bits, 5e-6 of the terms'
