@@ -495,8 +495,9 @@ rs_status rs_prefill_bytes_for(const rs_layer_desc *desc, const rs_ragged_desc *
  * be cleared, and a call leaves nothing in it that another one needs.  States,
  * and y before its one rounding to bf16, are accurate to fp32 rounding (operands
  * of 22 bits, fp32 sums).  In requests of more than 12 rows those bits count from
- * the largest u of a value column in a chunk: a state that replaces one 2^24 times
- * as large within a chunk is 4e-6 off.
+ * the largest u of a value column in a chunk: a state that replaces one up to 2^20
+ * times as large within a chunk is 1.2e-6 off, 2^24 times 5e-6; y keeps its own
+ * rounding up to 2^20.
  * A NaN or an infinity stays in its request; there it may reach any row of its
  * own chunk and all later ones.
  * Source: [CSI] "How it works", Gated DeltaNet bullet (the recurrence). */

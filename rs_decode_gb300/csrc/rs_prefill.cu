@@ -37,16 +37,18 @@
 //
 // Precision.  The tensor cores multiply fp16 operands into fp32 sums.  Keys
 // and queries (bf16) enter as one fp16 term, each row scaled by a power of two to
-// a largest value in [1, 2): exact down to 2^-17 of that value, and off by at most
-// 2^-25 of it below.  Everything else (S, R, T, P, u) enters as the sum of two fp16
-// terms, 22 bits, scaled by a power of two likewise, so that states and outputs come
-// out at fp32 accuracy (bf16 terms would leave 16 bits at the same cost), as those of
-// the recurrence for short requests do; y is rounded once, to bf16.
+// a largest value in [1, 2) (queries [64, 128)): exact down to 2^-17 of that value,
+// and off by at most 2^-25 of it below.  Everything else (S, R, T, P, u) enters as the
+// sum of two fp16 terms, 22 bits, scaled by a power of two likewise, so that states and
+// outputs come out at fp32 accuracy (bf16 terms would leave 16 bits at the same cost),
+// as those of the recurrence for short requests do; y is rounded once, to bf16.
 // The rows of a chunk share a scale for R and u in each value column, from its largest
-// magnitude; the low terms reach 2^-39 below it, so values that follow a far larger
-// state which they replace within one chunk keep fewer bits in the end.  A state
-// forgotten at row 20 of 64, 2^k times the values: the new one is 3.3e-7 off up to
-// k = 20, 4.1e-6 at 24, 2.2e-4 at 28.
+// magnitude, and P has a fixed one; their low terms reach 2^-39 and 2^-40 below those,
+// so that what replaces a far larger state within one chunk keeps fewer bits in the end.
+// A state 2^k times the values, forgotten at row 20 of 64: the new one is 3.3e-7 off up
+// to k = 20, 4.1e-6 at 24, 2.2e-4 at 28; fading over 8 to 30 rows, 1.2e-6 at most up to
+// 20, 4.6e-6 at 24.  On the way down y is off, beside the terms that it is the sum of,
+// by 5e-6 at k = 12, 6e-5 at 14, 1e-3 at 18, and passes its own rounding from 2^20 on.
 #include "rs_prefill.cuh"
 
 namespace rs {
@@ -143,7 +145,7 @@ struct ChunkSmem {
     static constexpr int TILES = 2 * C * D * 2;
     static constexpr int MATS = 2 * kMat * 4;
     static constexpr int VECS = TILES > MATS ? TILES : MATS;  // after the tiles, or the matrices in their place
-    static constexpr int BYTES = VECS + (2 + 2 * 3) * C * 4;
+    static constexpr int BYTES = VECS + (2 + 2 * 3) * C * 4 + 16;
 };
 
 // Sum of (value, error) pairs: the sum's rounding error goes into the error.
@@ -263,6 +265,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
 
     float *sk = reinterpret_cast<float *>(smem + ChunkSmem<D>::VECS), *sq = sk + C;
     float *vec = sq + C;                               // per head of a pair: gh, gl, beta
+    int *grows = reinterpret_cast<int *>(vec + 2 * 3 * C);  // an alpha above 1 in the odd heads, in the even ones
     // the first pair's decays are summed while the tiles are on their way
     float h[2], l[2], cgh, cgl;
     auto decays = [&](int hv, float *v) {
@@ -291,18 +294,24 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
         cgh = __shfl_sync(~0u, h[1], 31), cgl = __shfl_sync(~0u, l[1], 31);
         gh[2 * lane] = h[0], gl[2 * lane] = l[0], gh[2 * lane + 1] = h[1], gl[2 * lane + 1] = l[1];
     };
-    // the other two warps look whether any alpha is above 1
-    auto watch = [&](int hv) {
-        const float *a = p.alpha + (long long)e.y * p.H + hv;
-        const float a0 = 2 * lane < n ? a[(long long)(2 * lane) * p.H] : 1.f, a1 = 2 * lane + 1 < n ? a[(long long)(2 * lane + 1) * p.H] : 1.f;
-        if (__any_sync(~0u, fmaxf(a0, a1) > 1.f)) report_growth(a0, a1, p.status);
-    };
-    if (warp < 2 && warp < p.rep) decays(g * p.rep + warp, vec + warp * 3 * C);
-    if (warp >= 2 && warp - 2 < p.rep) watch(g * p.rep + warp - 2);
+    if (warp < 2) {
+        if (warp < p.rep) decays(g * p.rep + warp, vec + warp * 3 * C);
+    } else {  // the other two look whether any alpha of the key head's is above 1
+        bool any = false;
+        for (int r = warp - 2; r < p.rep; r += 2) {
+            const float *a = p.alpha + (long long)e.y * p.H + g * p.rep + r;
+            const float a0 = 2 * lane < n ? a[(long long)(2 * lane) * p.H] : 1.f;
+            const float a1 = 2 * lane + 1 < n ? a[(long long)(2 * lane + 1) * p.H] : 1.f;
+            if (__any_sync(~0u, fmaxf(a0, a1) > 1.f)) report_growth(a0, a1, p.status), any = true;
+        }
+        if (lane == 0) grows[warp - 2] = any;
+    }
     cp_async_wait_all();
     __syncthreads();
 
-    // bf16 -> fp16 in place, two threads a row: each row scaled to [1, 2).  A thread's
+    // bf16 -> fp16 in place, two threads a row: each row scaled to [1, 2), and queries to
+    // [64, 128) where no alpha is above 1: P, which has no scale of its own, is then below
+    // 2^15, and what a decay leaves of it keeps more bits, as u may be large.  A thread's
     // pieces go by four, so that eight threads meet eight places of a 128-byte row.
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -321,7 +330,7 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
         float m = fmaxf(__low2float(m2), __high2float(m2));
         m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
         float up, down;
-        row_scale<0>(m, up, down);
+        row_scale(w && !(grows[0] | grows[1]) ? 6 : 0, m, up, down);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
             auto half2 = [&](uint32_t x) {
@@ -401,8 +410,6 @@ __device__ __forceinline__ void chunk_cta(const PrefillParams &p, int cta, unsig
             *reinterpret_cast<float2 *>(out.sq + 2 * lane) = sql;
             *reinterpret_cast<float2 *>(out.ke + 2 * lane) = make_float2(k0, k1);
             if (lane == 31) out.all = e1;
-        } else if (r0 > 0 && warp >= 2 && warp - 2 < heads) {
-            watch(g * p.rep + r0 + warp - 2);
         }
         __syncthreads();
         // this warp's tiles of A and P

@@ -25,7 +25,7 @@ constexpr int kShort = 12;
 // Per chunk and value head:
 struct Record {
     uint16_t t_hi[C * C], t_lo[C * C];  // T, row i scaled by 1 / (its power of two)
-    uint16_t p_hi[C * C], p_lo[C * C];  // P without the rows' powers of two; nothing above the diagonal's 16 x 16 blocks
+    uint16_t p_hi[C * C], p_lo[C * C];  // P without the queries' powers of two; nothing above the diagonal's 16 x 16 blocks
     float egk[C];  // e^(G_i) times key i's power of two
     float eg[C];   // e^(G_i)
     float su[C];   // T's and key i's powers of two: (T R)_i su_i = u_i times key i's power
@@ -73,13 +73,14 @@ __device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(
 // The power of two that brings a row whose largest magnitude is m into
 // [2^K, 2^(K+1)), and its inverse.  A bound that is no longer finite counts as 2^128,
 // which no finite value reaches; a value that is not finite stays so at any scale.
-template <int K>
-__device__ __forceinline__ void row_scale(float m, float &up, float &down) {
+__device__ __forceinline__ void row_scale(int K, float m, float &up, float &down) {
     const int e = (int)(__float_as_uint(m) >> 23) & 255;
     const int u = min(254 + K - e, 253);  // biased exponent; its inverse is 254 - u >= 1
     up = __uint_as_float((uint32_t)max(u, 1) << 23);
     down = __uint_as_float((uint32_t)(254 - max(u, 1)) << 23);
 }
+template <int K>
+__device__ __forceinline__ void row_scale(float m, float &up, float &down) { row_scale(K, m, up, down); }
 
 // Two values as hi + lo: hi their fp16 rounding, lo the rounding of the rest.
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {

@@ -202,3 +202,14 @@ def test_norm_of_a_zero_head_with_the_smallest_eps(eps):
     ref = torch.zeros_like(q)
     ref[1, 0] = 3.0 * 128 ** -0.5
     assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("k,rows", [(8, 8), (12, 8), (12, 30)])
+def test_outputs_while_a_large_state_fades(d, k, rows):
+    """Every output for itself, beside its terms, while a state 2^k times the values fades by 2^-2k."""
+    c = scaled(Case([64, 150], 4, 2, d, alpha="slow", seed=3), 10 * 2.0 ** k)
+    for at in (20, 64 + 20, 64 + 80):
+        c.alpha[at:at + rows] = 2.0 ** (-2 * k / rows)
+    c.run()
+    rows_near(c)
