@@ -504,6 +504,118 @@ rs_status rs_prefill_bytes_for(const rs_layer_desc *desc, const rs_ragged_desc *
 rs_status rs_prefill_gdn(const rs_layer_desc *desc, const rs_state *st, const rs_ragged_desc *rd, const rs_ragged *rg,
                          const rs_prefill *in, uint16_t *y, void *work, void *stream);
 
+/* --------------------------------------------------- attention over a paged cache
+ * The attention layers between the recurrent ones of a hybrid model, for the
+ * batches that rs_ragged_plan plans: new tokens, drafts and prompts alike.
+ *   rs_attn_plan   once per batch, after rs_ragged_plan: shares of the work;
+ *   rs_qk_norm     per layer: norms and rotates the heads of q and k;
+ *   rs_kv_write    per layer: the batch's keys and values into the cache;
+ *   rs_attend      per layer: attention of the batch's rows over the cache.
+ * A token at position t of request r lives in slot t % page of page
+ * pages[r][t / page]; which pages a request has is the caller's business. */
+
+typedef enum {
+    RS_KV_BF16 = 0,
+    RS_KV_E4M3 = 1 /* per token and head, e4m3 codes and one power of two 2^(byte - 127): the least
+                    * (from 2^-60 to 2^119) with which the head's largest magnitude is at most 448.
+                    * Code times power is exact in bf16.  A head with an infinity or a NaN has
+                    * byte 255 and reads as NaN.                                             */
+} rs_kv_type;
+
+/* Shape of a layer's cache.  D is 64 or 128; page a power of two from 16 to
+ * 256; Hq a multiple of Hk, at most 128 times it, Hq <= 65535; n_pages, max_pages >= 1,
+ * n_pages * Hk < 2^31 and max_pages * page <= 2^30. */
+typedef struct {
+    int32_t Hq, Hk, D; /* query heads, key and value heads, channels; query head h reads key head h / (Hq / Hk) */
+    int32_t type;      /* rs_kv_type                                            */
+    int32_t page;      /* tokens of a page                                      */
+    int32_t n_pages;   /* pages of the cache                                    */
+    int32_t max_pages; /* entries of a request's row of the page table          */
+} rs_kv_desc;
+
+/* A layer's cache; caller-allocated device arrays (rs_kv_bytes_for). */
+typedef struct {
+    void *k, *v;       /* [n_pages][Hk][page][D] bf16, or e4m3 codes            */
+    uint8_t *ks, *vs;  /* [n_pages][Hk][page] powers' bytes; NULL for RS_KV_BF16 */
+} rs_kv;
+
+/* Byte sizes of the rs_kv arrays (0 for an unused one). */
+typedef struct {
+    size_t k, v, ks, vs;
+} rs_kv_bytes;
+
+/* Validates the descriptor and fills the byte sizes.  Host only.
+ * Source: none (the pages treat the recurrent layers alone). */
+rs_status rs_kv_bytes_for(const rs_kv_desc *d, rs_kv_bytes *out);
+
+/* Writes the planned rows' keys and values, k, v [rows][Hk][D] bf16 with row
+ * strides in elements (multiples of 8; tokens_cap rows), to their places in
+ * the cache.  pages: device int32 [R][max_pages].  A row whose page is not in
+ * the table's row (RS_DEV_LENGTH) or whose entry is outside 0..n_pages-1
+ * (RS_DEV_SLOT) is left out.  Two rows of a batch must not share a place.
+ * status: device word that receives RS_DEV_* bits.
+ * Source: none (the pages treat the recurrent layers alone). */
+rs_status rs_kv_write(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *rd, const rs_ragged *rg,
+                      const int32_t *pages, const uint16_t *k, const uint16_t *v, int64_t ld_k, int64_t ld_v,
+                      uint32_t *status, void *stream);
+
+/* The reverse: the planned rows' keys and values out of the cache, to k, v
+ * [tokens_cap][Hk][D] bf16 (8-bit heads as code times power, exactly).  Rows
+ * that the batch does not fill, or that have no page (status bits as for
+ * rs_kv_write), are left as they are.
+ * Source: none (the pages treat the recurrent layers alone). */
+rs_status rs_kv_read(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *rd, const rs_ragged *rg,
+                     const int32_t *pages, uint16_t *k, uint16_t *v, uint32_t *status, void *stream);
+
+/* Bytes of a batch's attention plan, and of the scratch of rs_attend. */
+typedef struct {
+    size_t plan, work;
+} rs_attn_bytes;
+
+/* Validates and fills the sizes, for batches whose requests bring at most
+ * max_len rows each.  Host only.
+ * Source: none (library plumbing). */
+rs_status rs_attn_bytes_for(const rs_kv_desc *d, const rs_ragged_desc *rd, int32_t max_len, rs_attn_bytes *out);
+
+/* Shares out the attention of a planned batch, on the device; for every layer
+ * with the same Hq, Hk, page and max_pages.  plan: device memory, 128-byte
+ * aligned, which rs_attend only reads.  A request with more than max_len rows,
+ * or whose end passes max_pages * page, gets no attention (RS_DEV_LENGTH).
+ * Source: none (library plumbing). */
+rs_status rs_attn_plan(const rs_kv_desc *d, const rs_ragged_desc *rd, const rs_ragged *rg, int32_t max_len, void *plan,
+                       uint32_t *status, void *stream);
+
+/* Inputs of rs_attend. */
+typedef struct {
+    const uint16_t *q;    /* [rows][Hq][D] bf16, row stride ld_q in elements (a multiple of 8; tokens_cap rows) */
+    int64_t ld_q;
+    const int32_t *pages; /* device [R][max_pages]                                            */
+    float scale;          /* of the scores, often D^-1/2; finite, not negative               */
+    int32_t max_len;      /* as given to rs_attn_plan                                         */
+} rs_attn;
+
+/* Causal attention of the planned rows over the cache: for row t of a request
+ * with position p (its context included) and query head h,
+ *   y = sum_j e^(s_j - max s) v_j / sum_j e^(s_j - max s),  s_j = scale q.k_j,
+ * over the request's cached positions j = 0 .. p; y bf16 [rows][Hq][D].  The
+ * batch's own rows have to be in the cache (rs_kv_write before, on the same
+ * stream).  Scores, sums and their joining are fp32; the weights are rounded to
+ * bf16 (fp16 for few rows on an 8-bit cache) before they meet the values, y
+ * once.  Rows of requests without attention in the plan, and rows past the
+ * batch, are left as they are.  plan: from rs_attn_plan for the same Hq, Hk, R
+ * and max_len (RS_DEV_LENGTH otherwise, and y is left).  An entry of the page
+ * table that is outside 0..n_pages-1 reads as zeros (RS_DEV_SLOT).
+ * work: device scratch of rs_attn_bytes_for's bytes, 128-byte aligned; not
+ * cleared, and a call leaves nothing in it that another one needs; calls that
+ * may overlap need one each.  Results are the same from run to run; the batch
+ * around a request may change the order of its sums.
+ * What lies in a page behind a request's last key is never used, whatever it
+ * holds.  A NaN or an infinity in k or q reaches the rows that see it; one in v
+ * may, besides them, reach the request's own rows up to 127 positions before it.
+ * Source: none (the pages treat the recurrent layers alone). */
+rs_status rs_attend(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *rd, const rs_ragged *rg, const rs_attn *in,
+                    const void *plan, uint16_t *y, void *work, uint32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,6 +23,7 @@ DEV_CAPACITY, DEV_ACCEPT, DEV_DRAFTS_PENDING = 0x1, 0x2, 0x4
 DEV_TIMEOUT, DEV_LENGTH, DEV_BLOCKS, DEV_RECORDS, DEV_SLOT, DEV_GATE = 0x8, 0x10, 0x20, 0x40, 0x80, 0x100
 NORM_NONE, NORM_L2, NORM_RMS = 0, 1, 2
 CHUNK = 64  # rows of a chunk of the ragged prefill
+KV_BF16, KV_E4M3 = 0, 1
 STATUS = {0: "RS_OK", 1: "RS_ERR_INVALID_ARG", 2: "RS_ERR_UNSUPPORTED", 3: "RS_ERR_CAPACITY",
           4: "RS_ERR_CUDA", 5: "RS_ERR_DEVICE", 6: "RS_ERR_STATIC_LIMIT"}
 STATIC_MAX_SEQS = 4096
@@ -77,6 +78,26 @@ class Prefill(ctypes.Structure):
                [(n, _vp) for n in ("rows", "start", "pool")] + [("n_pool", _c_i32), ("max_len", _c_i32)]
 
 
+class KvDesc(ctypes.Structure):
+    _fields_ = [(n, _c_i32) for n in ("Hq", "Hk", "D", "type", "page", "n_pages", "max_pages")]
+
+
+class Kv(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("k", "v", "ks", "vs")]
+
+
+class KvBytes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("k", "v", "ks", "vs")]
+
+
+class AttnBytes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("plan", "work")]
+
+
+class Attn(ctypes.Structure):
+    _fields_ = [("q", _vp), ("ld_q", ctypes.c_int64), ("pages", _vp), ("scale", ctypes.c_float), ("max_len", _c_i32)]
+
+
 # name -> argtypes (restype is rs_status = int unless listed in _RESTYPE)
 _SIGS = {
     "rs_status_string": [ctypes.c_int],
@@ -109,6 +130,15 @@ _SIGS = {
                              ctypes.POINTER(ctypes.c_size_t)],
     "rs_prefill_gdn": [ctypes.POINTER(LayerDesc), ctypes.POINTER(State), ctypes.POINTER(RaggedDesc),
                        ctypes.POINTER(RaggedArrays), ctypes.POINTER(Prefill), _vp, _vp, _vp],
+    "rs_kv_bytes_for": [ctypes.POINTER(KvDesc), ctypes.POINTER(KvBytes)],
+    "rs_kv_write": [ctypes.POINTER(KvDesc), ctypes.POINTER(Kv), ctypes.POINTER(RaggedDesc), ctypes.POINTER(RaggedArrays),
+                    _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int64, _vp, _vp],
+    "rs_kv_read": [ctypes.POINTER(KvDesc), ctypes.POINTER(Kv), ctypes.POINTER(RaggedDesc), ctypes.POINTER(RaggedArrays)] +
+                  [_vp] * 5,
+    "rs_attn_bytes_for": [ctypes.POINTER(KvDesc), ctypes.POINTER(RaggedDesc), _c_i32, ctypes.POINTER(AttnBytes)],
+    "rs_attn_plan": [ctypes.POINTER(KvDesc), ctypes.POINTER(RaggedDesc), ctypes.POINTER(RaggedArrays), _c_i32, _vp, _vp, _vp],
+    "rs_attend": [ctypes.POINTER(KvDesc), ctypes.POINTER(Kv), ctypes.POINTER(RaggedDesc), ctypes.POINTER(RaggedArrays),
+                  ctypes.POINTER(Attn)] + [_vp] * 5,
     "rs_decode_mamba2_noalloc": [ctypes.POINTER(LayerDesc), ctypes.POINTER(State)] + [_vp] * 8,
 }
 _RESTYPE = {"rs_status_string": ctypes.c_char_p, "rs_version": ctypes.c_char_p,
@@ -333,3 +363,41 @@ def rs_prefill_gdn(desc, state, rd, arrays, prefill, y, work, stream=None):
     st = load().rs_prefill_gdn(desc, state, rd, arrays, prefill, _ptr(y), _ptr(work), _stream(stream))
     if st:
         _check("rs_prefill_gdn", st)
+
+
+# ----------------------------------------------------------------------------- attention over a paged cache
+def rs_kv_bytes_for(desc: KvDesc) -> KvBytes:
+    out = KvBytes()
+    _check("rs_kv_bytes_for", load().rs_kv_bytes_for(ctypes.byref(desc), ctypes.byref(out)))
+    return out
+
+
+def rs_kv_write(desc, kv, rd, rg, pages, k, v, ld_k, ld_v, status, stream=None):
+    """k, v are data pointers (their row strides are ld_k, ld_v)."""
+    st = load().rs_kv_write(desc, kv, rd, rg, _ptr(pages), k, v, ld_k, ld_v, _ptr(status), _stream(stream))
+    if st:
+        _check("rs_kv_write", st)
+
+
+def rs_kv_read(desc, kv, rd, rg, pages, k, v, status, stream=None):
+    st = load().rs_kv_read(desc, kv, rd, rg, _ptr(pages), _ptr(k), _ptr(v), _ptr(status), _stream(stream))
+    if st:
+        _check("rs_kv_read", st)
+
+
+def rs_attn_bytes_for(desc, rd, max_len: int) -> AttnBytes:
+    out = AttnBytes()
+    _check("rs_attn_bytes_for", load().rs_attn_bytes_for(ctypes.byref(desc), ctypes.byref(rd), max_len, ctypes.byref(out)))
+    return out
+
+
+def rs_attn_plan(desc, rd, rg, max_len: int, plan, status, stream=None):
+    st = load().rs_attn_plan(desc, rd, rg, max_len, _ptr(plan), _ptr(status), _stream(stream))
+    if st:
+        _check("rs_attn_plan", st)
+
+
+def rs_attend(desc, kv, rd, rg, attn, plan, y, work, status, stream=None):
+    st = load().rs_attend(desc, kv, rd, rg, attn, _ptr(plan), _ptr(y), _ptr(work), _ptr(status), _stream(stream))
+    if st:
+        _check("rs_attend", st)

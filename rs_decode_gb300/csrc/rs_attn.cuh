@@ -1,0 +1,197 @@
+// What the kernels of the attention over a paged cache share: the plan's
+// layout, the launch parameters, the walk over a CTA's pieces, page look-ups
+// and the copies of keys and values.
+//
+// A batch's work is laid end to end, request after request, and cut into one
+// equal share for each CTA (one an SM).  A share is a run of pieces: whole
+// heads of requests, and parts of one at either end.  A part leaves its
+// unnormalised sums, its largest score and its sum of weights in the
+// workspace; join_kernel puts the parts of a head together, in order.  So the
+// shares are equal whatever the lengths are, few rows on a long cache spread
+// over the GPU, and results do not change from run to run.
+#pragma once
+
+#include <cuda.h>
+
+#include "rs_common.cuh"
+#include "rs_internal.h"
+
+namespace rs {
+namespace attn {
+
+constexpr int kKeys = 64;        // keys of a block of the short form
+constexpr int kTileKeys = 128;   // keys of a tile of the long form
+constexpr int kTileRows = 128;   // query rows (token x head of the group) of a tile
+constexpr int kMaxCtas = 512;    // shares at most
+// What starting a piece costs, in keys' blocks or tiles: its queries, its epilogue.
+constexpr int kShortStart = 1;
+constexpr int kLongStart = 2;
+
+// The head of a plan's buffer.  Lists and starts follow it, see PlanView.
+struct PlanHead {
+    int n_short, n_long;    // requests of either form
+    int short_rows;         // a request of at most this many rows of a key head's group is short
+    int ctas, max_len;      // what the plan was made for
+    int Hq, Hk, R;
+    int pad[8];
+};
+static_assert(sizeof(PlanHead) == 64, "");
+
+// A share's first piece.  Short: part = key block, item unused.  Long: item = the
+// request's item of two query tiles, part = key tile.
+struct Start {
+    int idx, item, head, part;
+};
+
+struct PlanView {
+    PlanHead *head;
+    int4 *shorts, *longs;           // [R] request, first row, rows, context
+    Start *short_start, *long_start;  // [ctas + 1]
+    long long *short_cu, *long_cu;  // [R + 1] work before each listed request
+};
+inline size_t plan_bytes(int R, int ctas) {
+    return sizeof(PlanHead) + 32 * (size_t)R + 2 * sizeof(Start) * (size_t)(ctas + 1) + 16 * ((size_t)R + 1);
+}
+__host__ __device__ inline PlanView plan_view(void *plan, int R, int ctas) {
+    unsigned char *p = static_cast<unsigned char *>(plan);
+    PlanView v;
+    v.head = reinterpret_cast<PlanHead *>(p);
+    p += sizeof(PlanHead);
+    v.shorts = reinterpret_cast<int4 *>(p);
+    v.longs = v.shorts + R;
+    v.short_start = reinterpret_cast<Start *>(v.longs + R);
+    v.long_start = v.short_start + ctas + 1;
+    v.short_cu = reinterpret_cast<long long *>(v.long_start + ctas + 1);
+    v.long_cu = v.short_cu + R + 1;
+    return v;
+}
+
+// How a batch is run, decided on the host from what it knows.
+struct Form {
+    int short_rows;   // 0, 16 or 32
+    bool any_long;    // requests longer than that are possible
+};
+// Up to 32 rows of a group (a token's heads that share a key head, or a few drafts')
+// stay in the registers of one warp's matrix instructions.  Drafts alone in a batch may
+// fill them; where longer requests are expected too, 16.
+inline Form form_of(int g, int max_len) {
+    Form f;
+    const long long rows = (long long)g * max_len;
+    if (rows <= 32)
+        f.short_rows = rows <= 16 ? 16 : 32;
+    else
+        f.short_rows = g <= 16 ? 16 : g <= 32 ? 32 : 0;
+    f.any_long = rows > f.short_rows;
+    return f;
+}
+
+__host__ __device__ inline int tile_tokens(int g) { return kTileRows / g; }  // of one query tile
+
+struct Params {
+    int Hq, Hk, g, page, page_log, n_pages, max_pages, R, cap, ctas, max_len, short_rows;
+    const int32_t *pages;
+    const uint16_t *q;
+    long long ld_q;
+    float c;  // scale * log2(e)
+    uint16_t *y;
+    void *plan;
+    const uint8_t *ks, *vs;
+    uint32_t *status;
+    float *short_parts, *long_parts;  // the workspace's two halves
+};
+
+// A part's place in the workspace: two a CTA (the end of a head that the CTA before began,
+// and the beginning of one that the next CTA goes on with), rows of D sums, then rows of
+// (largest score, sum of weights), scores in units of log2.
+__host__ __device__ inline size_t part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
+
+// ---------------------------------------------------------------- waits
+struct Abort {
+    uint32_t flag;
+};
+// As mbar_wait, but any wait of the CTA that gives up ends the others too.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, volatile uint32_t *abort, uint32_t *status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            atomicOr(status, RS_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+// The same for a whole warp, with one answer for all lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volatile uint32_t *abort, uint32_t *status) {
+    return __all_sync(~0u, wait_bar(bar, parity, abort, status));
+}
+
+// A position in a ring of n barriers, with the parity of its current round.
+struct Ring {
+    int at = 0;
+    unsigned parity = 0;
+    __device__ __forceinline__ void step(int n) {
+        if (++at == n) at = 0, parity ^= 1;
+    }
+};
+
+// ---------------------------------------------------------------- copies
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int c0, int c1, int c2, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, unsigned bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The power of two of an 8-bit head's scale byte (255, of a head that is not finite, gives infinity).
+__device__ __forceinline__ float pow2_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Place n of a paged row of pages, -1 (and a status bit) if the entry names no page.
+__device__ __forceinline__ int page_of(const Params &p, int r, int j) {
+    const int at = j < p.max_pages ? p.pages[(size_t)r * p.max_pages + j] : -1;
+    if (at >= 0 && at < p.n_pages) return at;
+    atomicOr(p.status, RS_DEV_SLOT);
+    return -1;
+}
+
+__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <class... KArgs, class... Args>
+cudaError_t launch(void (*kernel)(KArgs...), int grid, int block, int smem, cudaStream_t s, bool early, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(block), cfg.dynamicSmemBytes = smem, cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr, cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// ---------------------------------------------------------------- launches
+cudaError_t plan_launch(const rs_kv_desc &d, const rs_ragged_desc &rd, const rs_ragged &rg, int max_len, int ctas,
+                        const Form &f, void *plan, uint32_t *status, cudaStream_t s);
+// early: the launch may begin while the one before it in the stream still runs.
+cudaError_t short_launch(const Params &p, int D, bool e4m3, const CUtensorMap &k, const CUtensorMap &v, bool early,
+                         cudaStream_t s);
+cudaError_t long_launch(const Params &p, int D, bool e4m3, const CUtensorMap &q, const CUtensorMap &k,
+                        const CUtensorMap &v, cudaStream_t s);
+cudaError_t join_launch(const Params &p, int D, bool any_long, cudaStream_t s);
+cudaError_t kv_write_launch(const rs_kv_desc &d, const rs_kv &kv, const rs_ragged_desc &rd, const rs_ragged &rg,
+                            const int32_t *pages, const uint16_t *k, const uint16_t *v, long long ld_k, long long ld_v,
+                            uint32_t *status, cudaStream_t s);
+cudaError_t kv_read_launch(const rs_kv_desc &d, const rs_kv &kv, const rs_ragged_desc &rd, const rs_ragged &rg,
+                           const int32_t *pages, uint16_t *k, uint16_t *v, uint32_t *status, cudaStream_t s);
+
+}  // namespace attn
+}  // namespace rs

@@ -1,0 +1,597 @@
+// Attention of many rows over a paged cache on the fifth-generation tensor
+// cores: prompts, and turns behind a cached context.
+//
+// The rows of a product are tokens x the query heads of one key head, token after
+// token, so that a tile of 128 rows reads each key and value once for all heads of the
+// group, and a causal edge is 128 / g tokens wide.  A CTA holds two such tiles:
+//   S_i = Q_i K_j^T                128 x 128, fp32 in TMEM     (i = 0, 1: the tile)
+//   P_i = 2^(c (S_i - m))          bf16, in S's place, by a thread a row
+//   O_i (+)= P_i V_j               128 x D, fp32 in TMEM
+// The tensor cores work on one tile while the threads work on the other: the order of
+// products is P_0 V, Q_0 K, P_1 V, Q_1 K.  A step of a tile is 8 D x 128 x 128 / 2 operations
+// to 128 x 128 exponentials, so at D = 128 the products bound it as long as a tile's
+// register work hides behind the other tile's two products.
+//
+// The weights are relative to a reference that follows a row's maximum only when it is
+// 2^8 behind: then the row's O is read, scaled and written back before the next product
+// (otherwise O never leaves TMEM before the end).  Weights are rounded to bf16, which the product with bf16 values
+// asks for: 2^-9 of each, no more than y's own rounding and on average less.  Their
+// sum is that of the unrounded weights, fp32.
+//
+// Warps: 0-3 and 4-7 a thread a row of either tile; 8 issues the products; 9 the copies
+// (TMA, 128-byte swizzle, keys and values by turns in one ring).  From an 8-bit cache the codes are
+// copied, and warps 12-15 turn them into bf16 tiles, code times power of two, exactly.
+//
+// TMEM columns: S_0 [0, 128), S_1 [128, 256), O_0 [256, 256 + D), O_1 after it.
+#include "rs_attn.cuh"
+
+namespace rs {
+namespace attn {
+namespace {
+
+using f2 = unsigned long long;  // two fp32 values, the operand of paired arithmetic
+
+template <int D_, bool E4M3_>
+struct Cfg {
+    static constexpr int D = D_;
+    static constexpr bool E4M3 = E4M3_;
+    static constexpr int THREADS = E4M3 ? 512 : 384;
+    static constexpr int HALF = 128 * 128;                 // 128 rows of 128 bytes
+    static constexpr int TILE = (D / 64) * HALF;           // 128 rows of Q, K or V
+    static constexpr int STAGES = D == 64 ? 8 : E4M3 ? 3 : 5;
+    static constexpr int RAWS = E4M3 ? 4 : 0;              // tiles of codes
+    static constexpr int RAW = 128 * D;
+    static constexpr int Q = 0;
+    static constexpr int RING = 2 * TILE;
+    static constexpr int CODES = RING + STAGES * TILE;
+    static constexpr int SCALES = CODES + RAWS * RAW;      // [RAWS][128]
+    static constexpr int BARS = SCALES + RAWS * 128;
+    static constexpr int BYTES = BARS + 512 + 1024;        // and room to align
+    static_assert(BYTES <= 227 * 1024, "");
+};
+
+constexpr int kMaxStages = 8, kMaxRaws = 4;
+struct Bars {
+    uint64_t full[kMaxStages], empty[kMaxStages];         // tiles of keys and values
+    uint64_t raw_full[kMaxRaws], raw_empty[kMaxRaws];     // tiles of codes
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_ready[2], pv_done[2], end;
+    uint32_t tmem, abort, begun, begun_q;                 // begun: copied tiles, of codes or not
+};
+static_assert(sizeof(Bars) <= 512, "");
+
+// ---------------------------------------------------------------- tensor cores
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// Tiles are 128-byte-swizzled: rows of 128 bytes, groups of 8 rows 1024 bytes apart; LBO: from
+// one half of 64 columns to the next, where a tile is read MN-major.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\tmov.b64 ad, {%1, %3};\n\tmov.b64 bd, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\tmov.b64 bd, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+
+#define RS_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
+#define RS_U8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+#define RS_32 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}"
+// 32 columns of the warp's 32 lanes; complete after ld_done()
+__device__ __forceinline__ void ld32(uint32_t addr, uint32_t *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " RS_32 ", [%32];"
+                 : RS_R8(v, 0), RS_R8(v, 8), RS_R8(v, 16), RS_R8(v, 24)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ld_done() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st32(uint32_t addr, const uint32_t *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " RS_32 ";" ::RS_U8(v, 0), RS_U8(v, 8), RS_U8(v, 16), RS_U8(v, 24),
+                 "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+#undef RS_R8
+#undef RS_U8
+#undef RS_32
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ---------------------------------------------------------------- a CTA's walk over its share
+struct Walk {
+    Start at, end;
+    int n, Hk, tokens;  // tokens of a query tile
+    const int4 *list;
+    int4 q, next;
+    int items, t0, tn;      // the request's items; the piece's first token and tokens
+    int keys;               // of the whole request
+    int tiles, last;        // key tiles that the item sees, the piece's end among them
+    int need[2];            // key tiles that either query tile sees
+    __device__ __forceinline__ void begin(const Params &p, const PlanView &v) {
+        at = v.long_start[blockIdx.x], end = v.long_start[blockIdx.x + 1];
+        n = v.head->n_long, list = v.longs, Hk = p.Hk, tokens = tile_tokens(p.g);
+        if (at.idx < n) q = list[at.idx];
+        if (at.idx + 1 < n) next = list[at.idx + 1];
+    }
+    __device__ __forceinline__ bool piece() {
+        const bool same = at.idx == end.idx && at.item == end.item && at.head == end.head;
+        if (at.idx >= n || (same && at.part == end.part)) return false;
+        items = (q.z + 2 * tokens - 1) / (2 * tokens);
+        t0 = at.item * 2 * tokens, tn = min(2 * tokens, q.z - t0);
+        keys = q.z + q.w;
+        need[0] = (q.w + t0 + min(tn, tokens) + kTileKeys - 1) / kTileKeys;
+        tiles = (q.w + t0 + tn + kTileKeys - 1) / kTileKeys;
+        need[1] = tn > tokens ? tiles : 0;
+        last = same ? end.part : tiles;
+        return true;
+    }
+    __device__ __forceinline__ bool whole() const { return at.part == 0 && last == tiles; }
+    __device__ __forceinline__ void step() {
+        at.part = 0;
+        if (++at.head < Hk) return;
+        at.head = 0;
+        if (++at.item < items) return;
+        at.item = 0, ++at.idx;
+        q = next;
+        if (at.idx + 1 < n) next = list[at.idx + 1];
+    }
+};
+
+// ---------------------------------------------------------------- copies
+template <class C>
+__device__ __forceinline__ void copy_role(const Params &p, const PlanView &v, const CUtensorMap *qm, const CUtensorMap *km,
+                                          const CUtensorMap *vm, uint32_t sm, Bars *b) {
+    constexpr int ROWB = C::E4M3 ? C::D : C::D * 2, HALVES = ROWB > 128 ? 2 : 1;
+    constexpr int UNIT = C::E4M3 ? C::RAW : C::TILE, UNITS = C::E4M3 ? C::RAWS : C::STAGES;
+    uint64_t *const full = C::E4M3 ? b->raw_full : b->full, *const empty = C::E4M3 ? b->raw_empty : b->empty;
+    const int lane = threadIdx.x & 31;
+    const int rows = min(p.page, 64), boxes = kTileKeys / rows;
+    const bool scales = C::E4M3 && lane >= 16 && lane < 16 + boxes;
+    const bool copier = lane < boxes * HALVES;
+    const int half = scales ? 0 : lane % HALVES, box = scales ? lane - 16 : lane / HALVES;
+    Ring ring;
+    bool first_round = true, first_piece = true;
+    unsigned q_parity = 0;
+    Walk w;
+    w.begin(p, v);
+    for (; w.piece(); w.step()) {
+        auto page_at = [&](int j) {
+            const int key = j * kTileKeys + box * rows;
+            return (copier || scales) && j < w.last && key < w.keys ? page_of(p, w.q.x, key >> p.page_log) : -1;
+        };
+        int page = page_at(w.at.part);
+        if (!first_piece) {
+            if (!wait_warp(&b->q_empty, q_parity, &b->abort, p.status)) return;
+            q_parity ^= 1;
+        }
+        first_piece = false;
+        if (lane == 0) {
+            const int tiles = w.need[1] ? 2 : 1;
+            ++*const_cast<volatile uint32_t *>(&b->begun_q);
+            mbar_arrive_expect_tx(&b->q_full, tiles * (C::D / 64) * w.tokens * p.g * 128);
+            for (int i = 0; i < tiles; ++i)
+                for (int h = 0; h < C::D / 64; ++h)
+                    tma_load_3d(sm + C::Q + i * C::TILE + h * C::HALF, qm, h * 64, w.at.head * p.g, w.q.y + w.t0 + i * w.tokens, &b->q_full);
+        }
+        __syncwarp();
+        for (int j = w.at.part; j < w.last; ++j) {
+            const int next = page_at(j + 1);  // in flight while this tile waits for its place
+            const int row = (j * kTileKeys + box * rows) & (p.page - 1);
+            const unsigned with_scales = __ballot_sync(~0u, scales && page >= 0);
+            const int slab = page >= 0 ? page * p.Hk + w.at.head : p.n_pages * p.Hk;  // past the cache: zeros
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                if (!first_round && !wait_warp(empty + ring.at, ring.parity ^ 1, &b->abort, p.status)) return;
+                if (lane == 0) {
+                    ++*const_cast<volatile uint32_t *>(&b->begun);
+                    mbar_arrive_expect_tx(full + ring.at, UNIT + __popc(with_scales) * rows);
+                }
+                __syncwarp();
+                const uint32_t to = sm + (C::E4M3 ? C::CODES : C::RING) + ring.at * UNIT;
+                if (copier)
+                    tma_load_3d(to + half * C::HALF + box * rows * min(ROWB, 128), kv ? vm : km, half * 64, row, slab, full + ring.at);
+                else if (scales && page >= 0)
+                    bulk_load(sm + C::SCALES + ring.at * 128 + box * rows,
+                              (kv ? p.vs : p.ks) + (((size_t)page * p.Hk + w.at.head) << p.page_log) + row, rows, full + ring.at);
+                ring.step(UNITS);
+                if (ring.at == 0) first_round = false;
+            }
+            page = next;
+        }
+    }
+    // the last arrivals on the barriers that this warp waits on
+    if (!first_piece) wait_warp(&b->q_empty, q_parity, &b->abort, p.status);
+    for (int i = 0; i < UNITS; ++i) {
+        if (!first_round || i < ring.at) wait_warp(empty + i, first_round ? 0 : i < ring.at ? ring.parity : ring.parity ^ 1, &b->abort, p.status);
+    }
+}
+
+// After giving up: wait (with a limit) for the copies still in flight.
+template <class C>
+__device__ __forceinline__ void drain(Bars *b) {
+    constexpr int UNITS = C::E4M3 ? C::RAWS : C::STAGES;
+    uint64_t *const full = C::E4M3 ? b->raw_full : b->full;
+    const int begun = *const_cast<volatile uint32_t *>(&b->begun), q = *const_cast<volatile uint32_t *>(&b->begun_q);
+    for (int s = 0; s < UNITS; ++s) {
+        const int rounds = begun > s ? (begun - s + UNITS - 1) / UNITS : 0;
+        if (rounds) mbar_wait(full + s, (rounds - 1) & 1);
+    }
+    if (q) mbar_wait(&b->q_full, (q - 1) & 1);
+}
+
+// Codes into bf16 tiles, a thread a key.
+template <class C>
+__device__ __forceinline__ void convert_role(const Params &p, const PlanView &v, uint32_t sm, Bars *b) {
+    const int lane = threadIdx.x & 31, row = threadIdx.x & 127;
+    Ring ring, raw;
+    bool first_round = true;
+    Walk w;
+    w.begin(p, v);
+    for (; w.piece(); w.step()) {
+        for (int j = w.at.part; j < w.last; ++j) {
+            const bool live = j * kTileKeys + row < w.keys;
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+                if (!wait_warp(b->raw_full + raw.at, raw.parity, &b->abort, p.status)) return;
+                if (!first_round && !wait_warp(b->empty + ring.at, ring.parity ^ 1, &b->abort, p.status)) return;
+                const uint32_t from = sm + C::CODES + raw.at * C::RAW, to = sm + C::RING + ring.at * C::TILE;
+                uint32_t byte;
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(sm + C::SCALES + raw.at * 128 + row) : "memory");
+                const float up = pow2_of(byte);
+#pragma unroll
+                for (int c = 0; c < C::D / 16; ++c) {
+                    const uint32_t at = C::D == 64 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4) : row * 128 + ((c ^ (row & 7)) << 4);
+                    uint32_t x[4], o[8];
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(from + at) : "memory");
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t h;
+                        float lo, hi;
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(x[e >> 1] >> (16 * (e & 1)))));
+                        asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(lo), "=f"(hi) : "r"(h));
+                        o[e] = live ? pack_bf(lo * up, hi * up) : 0;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int piece = 2 * c + e;
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (piece >> 3) * C::HALF + row * 128 + (((piece ^ row) & 7) << 4)),
+                                     "r"(o[4 * e]), "r"(o[4 * e + 1]), "r"(o[4 * e + 2]), "r"(o[4 * e + 3])
+                                     : "memory");
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b->full + ring.at), mbar_arrive(b->raw_empty + raw.at);
+                raw.step(C::RAWS);
+                ring.step(C::STAGES);
+                if (ring.at == 0) first_round = false;
+            }
+        }
+    }
+    for (int i = 0; i < C::STAGES; ++i)
+        if (!first_round || i < ring.at) wait_warp(b->empty + i, first_round ? 0 : i < ring.at ? ring.parity : ring.parity ^ 1, &b->abort, p.status);
+}
+
+// ---------------------------------------------------------------- products
+template <class C>
+__device__ __forceinline__ bool product_role(const Params &p, const PlanView &v, uint32_t sm, Bars *b) {
+    constexpr int D = C::D;
+    constexpr uint32_t kIdescS = umma_idesc_bf16(128, 128, false, false), kIdescO = umma_idesc_bf16(128, D, false, true);
+    const int lane = threadIdx.x & 31;
+    const uint32_t tmem = b->tmem;
+    Ring ring;
+    unsigned q_parity = 0, p_parity[2] = {0, 0};
+    auto wait = [&](uint64_t *bar, unsigned parity) {
+        const bool ok = wait_warp(bar, parity, &b->abort, p.status);
+        tc_fence_after_sync();
+        return ok;
+    };
+    auto scores = [&](int i, int stage) {
+        if (elect_one()) {
+            const uint32_t a = desc_lo(sm + C::Q + i * C::TILE, 16), k = desc_lo(sm + C::RING + stage * C::TILE, 16);
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x)
+                mma_ss(tmem + i * 128, a + (x >> 2) * (C::HALF >> 4) + (x & 3) * 2, k + (x >> 2) * (C::HALF >> 4) + (x & 3) * 2, kIdescS, x > 0);
+            umma_commit(b->s_full + i);
+        }
+        __syncwarp();
+    };
+    auto values = [&](int i, int stage, bool acc) {
+        if (elect_one()) {
+            const uint32_t vd = desc_lo(sm + C::RING + stage * C::TILE, C::HALF);
+#pragma unroll
+            for (int x = 0; x < kTileKeys / 16; ++x)
+                mma_ts(tmem + 256 + i * D, tmem + i * 128 + x * 8, vd + x * 128, kIdescO, acc || x > 0);
+            umma_commit(b->pv_done + i);
+        }
+        __syncwarp();
+    };
+    auto release = [&](uint64_t *bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
+    };
+    // What lies in the tile behind the request's last key is not part of the cache: zeros
+    // meet its zero weights.  (8-bit tiles are written so.)
+    auto clear = [&](int stage, int from) {
+        if (C::E4M3 || from >= kTileKeys) return;
+        const int rows = min(p.page, 64), to = (from + rows - 1) / rows * rows;  // copies past the last page's are zeros already
+        for (int i = lane; i < (to - from) * (D / 8); i += 32) {
+            const int r = from + i / (D / 8), c = i % (D / 8);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(sm + C::RING + stage * C::TILE + (c >> 3) * C::HALF + r * 128 + (((c ^ r) & 7) << 4)),
+                         "r"(0)
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+    };
+    Walk w;
+    w.begin(p, v);
+    for (; w.piece(); w.step()) {
+        if (!wait(&b->q_full, q_parity)) return false;
+        q_parity ^= 1;
+        int v_stage = 0;
+        for (int j = w.at.part; j <= w.last; ++j) {
+            // K_j at the ring's place, V_j behind it; V_(j-1) at v_stage
+            const int k_stage = ring.at;
+            if (j < w.last) {
+                if (!wait(b->full + k_stage, ring.parity)) return false;
+                ring.step(C::STAGES);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (j > w.at.part && j - 1 < w.need[i]) {
+                    if (!wait(b->p_ready + i, p_parity[i])) return false;
+                    p_parity[i] ^= 1;
+                    values(i, v_stage, j - 1 > w.at.part);
+                }
+                if (j < w.last && j < w.need[i]) scores(i, k_stage);
+            }
+            if (j > w.at.part) release(b->empty + v_stage);
+            if (j < w.last) {
+                release(b->empty + k_stage);
+                if (j == w.last - 1) release(&b->q_empty);
+                v_stage = ring.at;
+                if (!wait(b->full + v_stage, ring.parity)) return false;
+                ring.step(C::STAGES);
+                clear(v_stage, w.keys - j * kTileKeys);
+            }
+        }
+    }
+    return true;
+}
+
+// ---------------------------------------------------------------- a thread a row
+template <class C>
+__device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int i, Bars *b) {
+    constexpr int D = C::D;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t t_s = b->tmem + lanes + i * 128, t_o = b->tmem + lanes + 256 + i * D;
+    const f2 c2 = f2_pack(p.c, p.c);
+    unsigned count = 0;  // key tiles of this query tile so far
+    Walk w;
+    w.begin(p, v);
+    const int token_in = row / p.g, head_in = row - token_in * p.g;
+    for (; w.piece(); w.step()) {
+        if (i == 1 && !w.need[1]) continue;
+        const int token = w.t0 + i * w.tokens + token_in;
+        const bool real = token_in < w.tokens && token < w.q.z;
+        const int first = w.q.w + w.t0 + i * w.tokens, limit = w.q.w + min(token, w.q.z - 1);  // last keys that the tile's first row and this one see
+        const int end = min(w.last, w.need[i]);
+        float m = -INFINITY;
+        f2 l2 = 0;
+        for (int j = w.at.part; j < end; ++j, ++count) {
+            if (!wait_warp(b->s_full + i, count & 1, &b->abort, p.status)) return false;
+            tc_fence_after_sync();
+            uint32_t s[128];
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) ld32(t_s + c, s + c);
+            ld_done();
+            if (j * kTileKeys + kTileKeys - 1 > first) {
+                const int seen = limit - j * kTileKeys;
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (c > seen) s[c] = 0xff800000u;
+            }
+            float top[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(s[c]);
+#pragma unroll
+            for (int c = 4; c < 124; c += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(s[124 + e]));
+            const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+            if (j == w.at.part) {
+                m = most;
+            } else {
+                const bool behind = (most - m) * p.c > 8.f;
+                if (__any_sync(~0u, behind)) {
+                    // O waits for its last product, then takes the new reference
+                    if (!wait_warp(b->pv_done + i, (count - 1) & 1, &b->abort, p.status)) return false;
+                    tc_fence_after_sync();
+                    const float f = behind ? ex2((m - most) * p.c) : 1.f;
+                    if (behind) m = most;
+                    const f2 ff = f2_pack(f, f);
+                    l2 = f2_mul(l2, ff);
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        ld32(t_o + c, o);
+                        ld_done();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        st32(t_o + c, o);
+                    }
+                }
+            }
+            // a row that has seen no key yet has no weights
+            const float mc = m == -INFINITY ? 0.f : -m * p.c;
+            const f2 mc2 = f2_pack(mc, mc);
+            f2 sum[2] = {0, 0};
+#pragma unroll
+            for (int c = 0; c < 128; c += 64) {
+                uint32_t w32[32];
+#pragma unroll
+                for (int e = 0; e < 64; e += 2) {
+                    const f2 x = f2_fma((f2)s[c + e + 1] << 32 | s[c + e], c2, mc2);
+                    float lo, hi;
+                    f2_unpack(x, lo, hi);
+                    lo = ex2(lo), hi = ex2(hi);
+                    sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2_pack(lo, hi));
+                    w32[e / 2] = pack_bf(lo, hi);
+                }
+                st32(t_s + c / 2, w32);
+            }
+            l2 = f2_add(l2, f2_add(sum[0], sum[1]));
+            st_done();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b->p_ready + i);
+        }
+        float l, l_hi;
+        f2_unpack(l2, l, l_hi);
+        l += l_hi;
+        const bool any = end > w.at.part;
+        if (any) {
+            if (!wait_warp(b->pv_done + i, (count - 1) & 1, &b->abort, p.status)) return false;
+            tc_fence_after_sync();
+        }
+        const bool whole = w.whole();
+        const float inv = 1.f / l;
+        uint16_t *const y = p.y + ((long long)(w.q.y + token) * p.Hq + w.at.head * p.g + head_in) * D;
+        float *const part = p.long_parts + (size_t)(2 * blockIdx.x + (w.at.part > 0 ? 0 : 1)) * part_floats(2 * kTileRows, D);
+        const int x = i * kTileRows + row;
+        if (!whole && real) reinterpret_cast<float2 *>(part + (size_t)2 * kTileRows * D)[x] = make_float2(m == -INFINITY ? m : m * p.c, l);
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            if (any) {
+                ld32(t_o + c, o);
+                ld_done();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0;
+            }
+            if (!real) continue;
+            if (whole) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint4 u;
+                    u.x = pack_bf(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                    u.y = pack_bf(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                    u.z = pack_bf(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                    u.w = pack_bf(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                    *reinterpret_cast<uint4 *>(y + c + e) = u;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<uint4 *>(part + (size_t)x * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+        }
+        tc_fence_before_sync();  // O is read before the next piece's first product
+    }
+    return true;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
+            const __grid_constant__ CUtensorMap vm) {
+    extern __shared__ unsigned char raw[];
+    let_next_launch();
+    unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    const uint32_t sm = smem_u32(smem);
+    Bars *b = reinterpret_cast<Bars *>(smem + C::BARS);
+    const PlanView v = plan_view(p.plan, p.R, p.ctas);
+    const bool mine = v.head->short_rows == p.short_rows && v.head->max_len == p.max_len && v.head->ctas == p.ctas &&
+                      v.head->Hq == p.Hq && v.head->Hk == p.Hk && v.head->R == p.R;
+    const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
+    if (warp == 8) {
+        tmem_alloc(&b->tmem, 512);
+        if ((threadIdx.x & 31) == 0) {
+            if (!mine && blockIdx.x == 0) atomicOr(p.status, RS_DEV_LENGTH);
+            for (int i = 0; i < C::STAGES; ++i) mbar_init(b->full + i, C::E4M3 ? 4 : 1), mbar_init(b->empty + i, 1);
+            for (int i = 0; i < C::RAWS; ++i) mbar_init(b->raw_full + i, 1), mbar_init(b->raw_empty + i, 4);
+            mbar_init(&b->q_full, 1), mbar_init(&b->q_empty, 1);
+            for (int i = 0; i < 2; ++i) mbar_init(b->s_full + i, 1), mbar_init(b->p_ready + i, 4), mbar_init(b->pv_done + i, 1);
+            mbar_init(&b->end, 1);
+            b->abort = b->begun = b->begun_q = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
+        tc_fence_before_sync();
+    }
+    __syncthreads();
+    tc_fence_after_sync();
+    if (mine) {
+        bool ok = true;
+        if (warp < 8) {
+            row_role<C>(p, v, warp >> 2, b);
+        } else if (warp == 8) {
+            ok = product_role<C>(p, v, sm, b);
+        } else if (warp == 9) {
+            copy_role<C>(p, v, &qm, &km, &vm, sm, b);
+        } else if (C::E4M3 && warp >= 12) {
+            convert_role<C>(p, v, sm, b);
+        }
+        if (warp == 8 && !ok) {  // products still in flight; elect_one() names the lane that issued them
+            if (elect_one()) umma_commit(&b->end);
+            __syncwarp();
+            mbar_wait(&b->end, 0);
+        }
+    }
+    tc_fence_before_sync();
+    if (__syncthreads_or(*const_cast<volatile uint32_t *>(&b->abort)) && threadIdx.x == 0) drain<C>(b);
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 8) tmem_dealloc(b->tmem, 512);
+}
+
+template <class C>
+cudaError_t launch_cfg(const Params &p, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
+    static SmemGrants grants;
+    const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&long_kernel<C>), C::BYTES, grants);
+    if (e != cudaSuccess) return e;
+    return launch(long_kernel<C>, p.ctas, C::THREADS, C::BYTES, s, false, p, q, k, v);
+}
+
+}  // namespace
+
+cudaError_t long_launch(const Params &p, int D, bool e4m3, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                        cudaStream_t s) {
+    if (D == 64) return e4m3 ? launch_cfg<Cfg<64, true>>(p, q, k, v, s) : launch_cfg<Cfg<64, false>>(p, q, k, v, s);
+    return e4m3 ? launch_cfg<Cfg<128, true>>(p, q, k, v, s) : launch_cfg<Cfg<128, false>>(p, q, k, v, s);
+}
+
+}  // namespace attn
+}  // namespace rs

@@ -1,0 +1,738 @@
+// Attention of few rows over a paged cache (one new token a request, or a few
+// drafts), and the kernel that joins the parts of heads that several CTAs shared.
+//
+// For each row x of a request's group of heads on a key head, over its keys j:
+//   s_j = c q.k_j,  m = max s_j,  y = sum 2^(s_j - m) v_j / sum 2^(s_j - m)
+// with c = scale log2(e).  Every key and value is read once for 16 or 32 rows, so HBM
+// bounds it: 2 D bytes of K and of V a key are 4 g D operations, a few tens a byte.
+//
+// A CTA an SM walks its share of the batch's blocks of 64 keys.  A producer warp
+// copies them by TMA into a ring (128-byte swizzle), as far ahead as shared memory
+// allows: the copies of the next head or request are under way while the last one's
+// sums are joined.  Eight warps in two groups of four take the blocks in turns, a
+// warp 16 keys of a block, each for itself: its own running maximum, sum of
+// weights and sums of values in registers, so that no barrier falls between blocks.
+// The matrix instructions (mma.sync, 16 rows x 8 x 16) are as many rows as a
+// token has heads on a key head; tcgen05's 128 rows would be mostly empty.  The reference
+// that weights are relative to follows the maximum only when it is 2^8 behind (2^1 with
+// 8 bits), since a step of it costs a pass over the sums.
+//
+// From a bf16 cache the weights are rounded to bf16 for their product with the values,
+// which the product's types ask for: 2^-9 of each weight, as large as y's own rounding
+// at most and on average less.  From an 8-bit cache the codes become fp16, exactly, and so
+// queries (scaled row by row by a power of two: bf16's 8 bits fit) and weights: relative to
+// m' = max(s_j + e_j), with e_j the exponent of value j's scale, and times 2^14, so that
+// the weight times 2^e_j uses fp16's whole range: what lies 2^-28 below the
+// largest loses bits.  The sum of weights itself stays fp32 and unrounded in both.
+#include "rs_attn.cuh"
+
+namespace rs {
+namespace attn {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32 + 32;
+constexpr int kPass = 32;        // channels joined at a time
+constexpr int kPitch = kPass + 8;  // floats between rows of the joining area: conflict-free pairs
+
+template <int D_, bool E4M3_, int MT_>
+struct Cfg {
+    static constexpr int D = D_, MT = MT_, ROWS = 16 * MT;
+    static constexpr bool E4M3 = E4M3_;
+    static constexpr int ROWB = D * (E4M3 ? 1 : 2);           // bytes of a key
+    static constexpr int HALVES = ROWB > 128 ? 2 : 1;         // tiles of 128-byte rows side by side
+    static constexpr int TILE = kKeys * ROWB;
+    // whole rounds of both groups of warps: a stage always meets the same group, which
+    // then waits on its barriers in every round
+    static constexpr int STAGES = 2 * TILE >= 32768 ? 6 : 12;
+    static constexpr int SCALES = STAGES * 2 * TILE;          // [STAGES][2][kKeys]
+    static constexpr int JOIN = SCALES + (E4M3 ? STAGES * 2 * kKeys : 0);
+    static constexpr int ML = JOIN + kWarps * 16 * kPitch * 4;  // [kWarps][ROWS] (maximum, sum)
+    static constexpr int BARS = ML + kWarps * ROWS * 8;
+    static constexpr int BYTES = BARS + 2 * STAGES * 8 + 16 + 1024;  // and room to align
+    static_assert(BYTES <= 227 * 1024, "");
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <bool E4M3>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (E4M3)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_h(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t two_halves(uint32_t codes16) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes16));
+    return r;
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Byte of 16-byte piece c of key r in a tile as the copies leave it.
+template <class C>
+__device__ __forceinline__ uint32_t piece(int r, int c) {
+    if constexpr (C::ROWB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    return (c >> 3) * (kKeys * 128) + r * 128 + (((c ^ r) & 7) << 4);
+}
+
+// A CTA's walk over its share: piece after piece.
+struct Walk {
+    Start at, end;
+    int n, Hk;
+    const int4 *list;
+    int4 q, next;  // the request (index, first row, rows, context), and the one after it
+    int keys, blocks, last;
+    __device__ __forceinline__ void begin(const Params &p, const PlanView &v) {
+        at = v.short_start[blockIdx.x], end = v.short_start[blockIdx.x + 1];
+        n = v.head->n_short, list = v.shorts, Hk = p.Hk;
+        if (at.idx < n) q = list[at.idx];
+        if (at.idx + 1 < n) next = list[at.idx + 1];
+    }
+    __device__ __forceinline__ bool piece() {
+        if (at.idx >= n || (at.idx == end.idx && at.head == end.head && at.part == end.part)) return false;
+        keys = q.z + q.w;
+        blocks = (keys + kKeys - 1) / kKeys;
+        last = at.idx == end.idx && at.head == end.head ? end.part : blocks;
+        return true;
+    }
+    __device__ __forceinline__ void step() {
+        at.part = 0;
+        if (++at.head < Hk) return;
+        at.head = 0, ++at.idx;
+        q = next;
+        if (at.idx + 1 < n) next = list[at.idx + 1];
+    }
+};
+
+// ---------------------------------------------------------------- copies
+template <class C>
+__device__ __forceinline__ void produce(const Params &p, const PlanView &v, const CUtensorMap *km, const CUtensorMap *vm,
+                                        uint32_t sm, uint64_t *full, uint64_t *empty, volatile uint32_t *abort) {
+    volatile uint32_t *const begun = abort + 1;  // blocks, for drain()
+    const int lane = threadIdx.x & 31;
+    const int rows = min(p.page, kKeys), boxes = kKeys / rows;  // of one copy; copies to a block's 64 keys
+    // lane -> one copy: box, half of the channels, keys or values; then (8 bits) a box's scales
+    const int copies = boxes * C::HALVES * 2;
+    const bool copies_scales = C::E4M3 && lane >= 16 && lane < 16 + 2 * boxes;
+    const bool is_v = lane & 1;
+    const int half = copies_scales ? 0 : (lane >> 1) % C::HALVES;
+    const int box = copies_scales ? (lane - 16) >> 1 : (lane >> 1) / C::HALVES;
+    const bool copier = lane < copies;
+    const CUtensorMap *const map = is_v ? vm : km;
+    const uint8_t *const scales = is_v ? p.vs : p.ks;
+    Ring ring;
+    bool first_round = true;
+    Walk w;
+    w.begin(p, v);
+    for (; w.piece(); w.step()) {
+        auto page_at = [&](int b) {  // -1: past the request's keys, or no page
+            const int key = b * kKeys + box * rows;
+            return (copier || copies_scales) && b < w.last && key < w.keys ? page_of(p, w.q.x, key >> p.page_log) : -1;
+        };
+        int page = page_at(w.at.part), page1 = page_at(w.at.part + 1);
+        for (int b = w.at.part; b < w.last; ++b) {
+            const int page2 = page_at(b + 2);  // in flight while this block waits for its stage
+            if (!first_round && !wait_warp(empty + ring.at, ring.parity ^ 1, abort, p.status)) return;
+            const int row = (b * kKeys + box * rows) & (p.page - 1);
+            const unsigned with_scales = __ballot_sync(~0u, copies_scales && page >= 0);
+            if (lane == 0) {
+                *begun += 1;
+                mbar_arrive_expect_tx(full + ring.at, 2 * C::TILE + __popc(with_scales) * rows);
+            }
+            __syncwarp();
+            const uint32_t stage = sm + ring.at * 2 * C::TILE;
+            if (copier) {  // a coordinate past the cache fills in zeros
+                const int slab = page >= 0 ? page * p.Hk + w.at.head : p.n_pages * p.Hk;
+                tma_load_3d(stage + (is_v ? C::TILE : 0) + half * (kKeys * 128) + box * rows * min(C::ROWB, 128), map,
+                            half * 64, row, slab, full + ring.at);
+            } else if (copies_scales && page >= 0) {
+                bulk_load(sm + C::SCALES + (ring.at * 2 + is_v) * kKeys + box * rows,
+                          scales + (((size_t)page * p.Hk + w.at.head) << p.page_log) + row, rows, full + ring.at);
+            }
+            ring.step(C::STAGES);
+            if (ring.at == 0) first_round = false;
+            page = page1, page1 = page2;
+        }
+    }
+}
+
+// After giving up: wait (with a limit) for the copies still in flight.
+template <class C>
+__device__ __forceinline__ void drain(uint64_t *full, int begun) {
+    for (int s = 0; s < C::STAGES; ++s) {
+        const int rounds = begun > s ? (begun - s + C::STAGES - 1) / C::STAGES : 0;
+        if (rounds) mbar_wait(full + s, (rounds - 1) & 1);
+    }
+}
+
+// ---------------------------------------------------------------- arithmetic
+template <class C>
+struct Sums {
+    float o[C::MT][C::D / 8][4];  // 16 rows x D, as the products leave them
+    float m[C::MT][2], l[C::MT][2];
+};
+
+// The queries of a piece as operands; with 8 bits scaled to fp16, and c times what undoes it in cq.
+template <class C>
+__device__ __forceinline__ void load_queries(const Params &p, const int4 &rq, int head, uint32_t (&q)[C::MT][C::D / 16][4],
+                                             float (&cq)[C::MT][2]) {
+    const int lane = threadIdx.x & 31, t = lane & 3, rows = rq.z * p.g;
+#pragma unroll
+    for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int row = mt * 16 + hf * 8 + (lane >> 2);
+            const bool in = row < rows;
+            const uint16_t *src = p.q + (long long)(rq.y + (in ? row / p.g : 0)) * p.ld_q + (head * p.g + (in ? row % p.g : 0)) * C::D;
+            cq[mt][hf] = p.c;
+            if constexpr (!C::E4M3) {
+#pragma unroll
+                for (int k = 0; k < C::D / 16; ++k) {
+                    q[mt][k][hf] = in ? *reinterpret_cast<const uint32_t *>(src + k * 16 + 2 * t) : 0;
+                    q[mt][k][2 + hf] = in ? *reinterpret_cast<const uint32_t *>(src + k * 16 + 8 + 2 * t) : 0;
+                }
+            } else {
+                // a lane's channels are those of its 16 bytes of codes: 16 t, and 64 + 16 t
+                uint32_t x[C::D / 8];
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < C::D / 64; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint4 u = in ? *reinterpret_cast<const uint4 *>(src + k * 64 + t * 16 + e * 8) : make_uint4(0, 0, 0, 0);
+                        x[8 * k + 4 * e] = u.x, x[8 * k + 4 * e + 1] = u.y, x[8 * k + 4 * e + 2] = u.z, x[8 * k + 4 * e + 3] = u.w;
+                    }
+#pragma unroll
+                for (int i = 0; i < C::D / 8; ++i) top = __vmaxu2(top, x[i] & 0x7fff7fffu);
+                top = max(top & 0xffffu, top >> 16);
+                top = max(top, __shfl_xor_sync(~0u, top, 1));
+                top = max(top, __shfl_xor_sync(~0u, top, 2));
+                // the power of two that brings the row's largest magnitude to [2^14, 2^15)
+                const int up = min(max(254 + 14 - (int)(top >> 7), 1), 253);
+                const float fu = __uint_as_float((uint32_t)up << 23);
+                cq[mt][hf] = p.c * __uint_as_float((uint32_t)(254 - up) << 23);
+#pragma unroll
+                for (int s = 0; s < C::D / 16; ++s)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t u = x[2 * s + e];
+                        q[mt][s][2 * e + hf] = pack_h(bf2f(u & 0xffffu) * fu, __uint_as_float(u & 0xffff0000u) * fu);
+                    }
+            }
+        }
+}
+
+// One warp's 16 keys of a staged block.  key0: position of the first; limit: the
+// last key that each of the lane's rows sees.
+template <class C>
+__device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C::D / 16][4], const float (&cq)[C::MT][2],
+                                        uint32_t k_tile, uint32_t v_tile, uint32_t scales, int slice, int key0, int keys,
+                                        int seen, const int (&limit)[C::MT][2]) {
+    constexpr int MT = C::MT, D = C::D;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float s[MT][2][4] = {};
+    if constexpr (!C::E4M3) {
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) {
+            uint32_t b[2][4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) ldmatrix4(b[nt], k_tile + piece<C>(slice + nt * 8 + (lane & 7), 4 * kk + (lane >> 3)));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    mma<false>(s[mt][nt], q[mt][2 * kk], b[nt][0], b[nt][1]);
+                    mma<false>(s[mt][nt], q[mt][2 * kk + 1], b[nt][2], b[nt][3]);
+                }
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+            uint4 b[2];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) b[nt] = lds128(k_tile + piece<C>(slice + nt * 8 + g, t + 4 * h));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const uint32_t w = k == 0 ? b[nt].x : k == 1 ? b[nt].y : k == 2 ? b[nt].z : b[nt].w;
+                    const uint32_t b0 = two_halves(w), b1 = two_halves(w >> 16);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) mma<true>(s[mt][nt], q[mt][4 * h + k], b0, b1);
+                }
+        }
+    }
+    // scores in units of log2; with 8 bits ev is the power of two of each key's values
+    float ev[2][2];
+    if constexpr (C::E4M3) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float up = pow2_of(lds_u8(scales + slice + nt * 8 + 2 * t + e));
+                const uint32_t vb = lds_u8(scales + kKeys + slice + nt * 8 + 2 * t + e);
+                ev[nt][e] = (float)((int)vb - 127);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    s[mt][nt][e] *= up * cq[mt][0];
+                    s[mt][nt][2 + e] *= up * cq[mt][1];
+                }
+            }
+    } else {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[mt][nt][e] *= cq[mt][e >> 1];
+    }
+    const bool masked = key0 + 15 > seen;  // some row does not see all 16
+    if (masked) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (key0 + nt * 8 + 2 * t + (e & 1) > limit[mt][e >> 1]) s[mt][nt][e] = -INFINITY;
+        // What lies behind the last key is not part of the cache: as zeros it meets its zero weights
+        if (!C::E4M3 && key0 + 16 > keys) {
+            for (int i = lane; i < (16 - max(keys - key0, 0)) * (D / 8); i += 32) {
+                const int r = slice + 15 - i / (D / 8), c = i % (D / 8);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(v_tile + piece<C>(r, c)), "r"(0) : "memory");
+            }
+            __syncwarp();
+        }
+    }
+    // the largest score so far; the reference follows it only when far behind
+    constexpr float kBehind = C::E4M3 ? 1.f : 8.f;
+    bool behind = false;
+    float top[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            float x;
+            if constexpr (C::E4M3) {
+                x = fmaxf(fmaxf(s[mt][0][2 * hf] + ev[0][0], s[mt][0][2 * hf + 1] + ev[0][1]),
+                          fmaxf(s[mt][1][2 * hf] + ev[1][0], s[mt][1][2 * hf + 1] + ev[1][1]));
+            } else {
+                x = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]), fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+            }
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+            top[mt][hf] = x;
+            behind = behind || x > a.m[mt][hf] + kBehind;
+        }
+    if (__any_sync(~0u, behind)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const float m = fmaxf(a.m[mt][hf], top[mt][hf]);
+                const float f = m == -INFINITY ? 1.f : ex2(a.m[mt][hf] - m);
+                a.m[mt][hf] = m;
+                a.l[mt][hf] *= f;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) a.o[mt][n][2 * hf] *= f, a.o[mt][n][2 * hf + 1] *= f;
+            }
+    }
+    uint32_t w[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        float x[2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // a row that has seen no key yet has no weights
+                const float below = s[mt][nt][e] - (a.m[mt][e >> 1] == -INFINITY ? 0.f : a.m[mt][e >> 1]);
+                x[nt][e] = ex2(below);
+                a.l[mt][e >> 1] += x[nt][e];
+                // at most 2^15: the reference may be 2^1 behind
+                if constexpr (C::E4M3) x[nt][e] = ex2(below + (ev[nt][e & 1] + 14.f));
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // rows g and g + 8 of the first eight keys, then of the others
+            const float lo = x[i >> 1][2 * (i & 1)], hi = x[i >> 1][2 * (i & 1) + 1];
+            w[mt][i] = C::E4M3 ? pack_h(lo, hi) : pack_bf(lo, hi);
+        }
+    }
+    if constexpr (!C::E4M3) {
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+            uint32_t b[4];
+            ldmatrix4_trans(b, v_tile + piece<C>(slice + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * n + (lane >> 4)));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                mma<false>(a.o[mt][2 * n], w[mt], b[0], b[1]);
+                mma<false>(a.o[mt][2 * n + 1], w[mt], b[2], b[3]);
+            }
+        }
+    } else {
+        // a lane's D / 8 channels from four keys: bytes of two keys side by side are one operand
+        uint32_t r[4][D / 32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = slice + 2 * t + (i & 1) + 8 * (i >> 1);
+            if constexpr (D == 128) {
+                const uint4 u = lds128(v_tile + piece<C>(key, g));
+                r[i][0] = u.x, r[i][1] = u.y, r[i][2] = u.z, r[i][3] = u.w;
+            } else {
+                const uint2 u = lds64(v_tile + piece<C>(key, g >> 1) + (g & 1) * 8);
+                r[i][0] = u.x, r[i][1] = u.y;
+            }
+            if (masked && key0 + 2 * t + (i & 1) + 8 * (i >> 1) >= keys)
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) r[i][e] = 0;
+        }
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t x = __byte_perm(r[0][e], r[1][e], h ? 0x7362 : 0x5140);
+                const uint32_t y = __byte_perm(r[2][e], r[3][e], h ? 0x7362 : 0x5140);
+                const uint32_t x0 = two_halves(x), x1 = two_halves(x >> 16), y0 = two_halves(y), y1 = two_halves(y >> 16);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    mma<true>(a.o[mt][4 * e + 2 * h], w[mt], x0, y0);
+                    mma<true>(a.o[mt][4 * e + 2 * h + 1], w[mt], x1, y1);
+                }
+            }
+    }
+}
+
+// The eight warps' sums of a piece, joined; whole heads go to y, parts to the workspace.
+template <class C>
+__device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &rq, int head, bool whole, int slot,
+                                       unsigned char *smem) {
+    constexpr int MT = C::MT, D = C::D;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float2 *const ml = reinterpret_cast<float2 *>(smem + C::ML);
+    float *const area = reinterpret_cast<float *>(smem + C::JOIN);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            float l = a.l[mt][hf];
+            l += __shfl_xor_sync(~0u, l, 1);
+            l += __shfl_xor_sync(~0u, l, 2);
+            if (t == 0) ml[warp * C::ROWS + mt * 16 + hf * 8 + g] = make_float2(a.m[mt][hf], l);
+        }
+    consumers_sync();
+    const int rows = rq.z * p.g;
+    float *const part = p.short_parts + (size_t)(2 * blockIdx.x + slot) * part_floats(C::ROWS, D);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        // weights of this warp's two rows
+        float f[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * C::ROWS + mt * 16 + hf * 8 + g].x);
+            f[hf] = a.m[mt][hf] == -INFINITY ? 0.f : ex2(a.m[mt][hf] - m);
+            if (C::E4M3) f[hf] *= 6.103515625e-5f;  // 2^-14
+        }
+        // a thread's row and pair of channels of what is joined
+        const int row = threadIdx.x >> 4, col = (threadIdx.x & 15) * 2, x = mt * 16 + row;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * C::ROWS + x].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float2 v = ml[w * C::ROWS + x];
+            // a sum that is not a number stays one
+            l += v.x == -INFINITY ? v.y : v.y * ex2(v.x - m);
+        }
+        const float inv = 1.f / l;
+        const int token = x / p.g, in_group = x - token * p.g;
+        uint16_t *const y = p.y + ((long long)(rq.y + token) * p.Hq + head * p.g + in_group) * D;
+        if (!whole && col == 0 && x < rows) reinterpret_cast<float2 *>(part + (size_t)C::ROWS * D)[x] = make_float2(m, l);
+#pragma unroll
+        for (int c = 0; c < D / kPass; ++c) {
+            float *const to = area + (warp * 16 + g) * kPitch;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        // 8 bits: sums n of a lane are channels (D / 8) (2 t + k) + n
+                        const float2 v = C::E4M3 ? make_float2(a.o[mt][4 * c + 2 * i][2 * hf + k] * f[hf], a.o[mt][4 * c + 2 * i + 1][2 * hf + k] * f[hf])
+                                                 : make_float2(a.o[mt][4 * c + 2 * i + k][2 * hf] * f[hf], a.o[mt][4 * c + 2 * i + k][2 * hf + 1] * f[hf]);
+                        const int at = C::E4M3 ? (2 * t + k) * 4 + 2 * i : (2 * i + k) * 8 + 2 * t;
+                        *reinterpret_cast<float2 *>(to + hf * 8 * kPitch + at) = v;
+                    }
+            consumers_sync();
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 v = *reinterpret_cast<const float2 *>(area + (w * 16 + row) * kPitch + col);
+                sum.x += v.x, sum.y += v.y;
+            }
+            const int d = C::E4M3 ? (D / 8) * (col >> 2) + 4 * c + (col & 3) : c * kPass + col;
+            if (x < rows) {
+                if (whole)
+                    *reinterpret_cast<uint32_t *>(y + d) = pack_bf(sum.x * inv, sum.y * inv);
+                else
+                    *reinterpret_cast<float2 *>(part + (size_t)x * D + d) = sum;
+            }
+            consumers_sync();
+        }
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void consume(const Params &p, const PlanView &v, unsigned char *smem, uint64_t *full, uint64_t *empty,
+                                        volatile uint32_t *abort) {
+    constexpr int MT = C::MT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, slice = (warp & 3) * 16;
+    const uint32_t sm = smem_u32(smem);
+    Ring ring;
+    ring.at = group;
+    bool ok = true;
+    Walk w;
+    w.begin(p, v);
+    int turn = 0;  // the group that takes the next block
+    for (; w.piece(); w.step()) {
+        uint32_t q[MT][C::D / 16][4];
+        float cq[MT][2];
+        load_queries<C>(p, w.q, w.at.head, q, cq);
+        int limit[MT][2];
+        const int rows = w.q.z * p.g;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) limit[mt][hf] = w.q.w + min(mt * 16 + hf * 8 + (lane >> 2), rows - 1) / p.g;
+        Sums<C> a;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) a.m[mt][hf] = -INFINITY, a.l[mt][hf] = 0.f;
+#pragma unroll
+            for (int n = 0; n < C::D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a.o[mt][n][e] = 0.f;
+        }
+        for (int b = w.at.part; b < w.last; ++b, turn ^= 1) {
+            if (turn != group || !ok) continue;
+            ok = wait_warp(full + ring.at, ring.parity, abort, p.status);
+            const int key0 = b * kKeys + slice;
+            if (ok && key0 < w.keys) {
+                const uint32_t stage = sm + ring.at * 2 * C::TILE;
+                compute<C>(a, q, cq, stage, stage + C::TILE, sm + C::SCALES + ring.at * 2 * kKeys, slice, key0, w.keys, w.q.w, limit);
+                if (!C::E4M3 && key0 + 16 > w.keys) fence_proxy_async_smem();  // zeros written before the next copy
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + ring.at);
+            ring.step(C::STAGES), ring.step(C::STAGES);
+        }
+        if (named_sync_or(2, kWarps * 32, !ok)) return;
+        finish<C>(p, a, w.q, w.at.head, w.at.part == 0 && w.last == w.blocks, w.at.part > 0 ? 0 : 1, smem);
+    }
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1)
+short_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
+    extern __shared__ unsigned char raw[];
+    let_next_launch();
+    unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BARS), *empty = full + C::STAGES;
+    uint32_t *abort = reinterpret_cast<uint32_t *>(empty + C::STAGES);
+    const PlanView v = plan_view(p.plan, p.R, p.ctas);
+    const bool mine = v.head->short_rows == p.short_rows && v.head->max_len == p.max_len && v.head->ctas == p.ctas &&
+                      v.head->Hq == p.Hq && v.head->Hk == p.Hk && v.head->R == p.R;
+    if (threadIdx.x == 0) {
+        if (!mine && blockIdx.x == 0) atomicOr(p.status, RS_DEV_LENGTH);
+        for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, 1), mbar_init(empty + i, kWarps / 2);
+        abort[0] = abort[1] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    if (mine) {
+        if (threadIdx.x >= kWarps * 32)
+            produce<C>(p, v, &km, &vm, smem_u32(smem), full, empty, abort);
+        else
+            consume<C>(p, v, smem, full, empty, abort);
+    }
+    // Every block that was copied has been waited for, but for a wait that gave up
+    if (__syncthreads_or(*reinterpret_cast<volatile uint32_t *>(abort)) && threadIdx.x == 0)
+        drain<C>(full, (int)reinterpret_cast<volatile uint32_t *>(abort)[1]);
+    if (blockIdx.x == 0) wait_for_launch();  // this launch does not end before the one that it overlaps
+}
+
+// ---------------------------------------------------------------- parts of a head
+// Row x of a head that the CTAs from c - 1 on shared: a warp's work, D / 32 channels a lane.
+// part_of(cta, slot): its sums.  Parts come in the order of the keys.
+template <int D>
+__device__ __forceinline__ void join_row(const float *parts, size_t stride, int rows, int c, int n, const Start *start, int x,
+                                         uint16_t *y) {
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    auto part_at = [&](int k) -> const float * {  // part k: the first is the end of CTA c - 1's share
+        if (k == 0) return parts + (size_t)(2 * (c - 1) + 1) * stride;
+        const Start a = start[c + k - 1], b = start[c + k];
+        const bool none = a.idx == b.idx && a.item == b.item && a.head == b.head && a.part == b.part;
+        return none ? nullptr : parts + (size_t)(2 * (c + k - 1)) * stride;
+    };
+    float m = -INFINITY;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        const float *at = k0 + lane < n ? part_at(k0 + lane) : nullptr;
+        float x_m = at ? at[(size_t)rows * D + 2 * x] : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x_m = fmaxf(x_m, __shfl_xor_sync(~0u, x_m, o));
+        m = fmaxf(m, x_m);
+    }
+    float l = 0.f, sum[V] = {};
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        const float *at = k0 + lane < n ? part_at(k0 + lane) : nullptr;
+        float f = 0.f, mine = 0.f;
+        if (at) {
+            const float2 v = reinterpret_cast<const float2 *>(at + (size_t)rows * D)[x];
+            f = v.x == -INFINITY ? 1.f : ex2(v.x - m);  // a part without keys that the row sees has sums of zero
+            mine = v.y * f;
+        }
+        l += mine;
+        unsigned live = __ballot_sync(~0u, at != nullptr);
+        const unsigned long long addr = reinterpret_cast<unsigned long long>(at);
+        for (int k = 0; k < min(32, n - k0); ++k) {
+            const float fk = __shfl_sync(~0u, f, k);
+            const float *pk = reinterpret_cast<const float *>(__shfl_sync(~0u, addr, k));
+            if (!(live >> k & 1)) continue;
+            float v[V];
+            if constexpr (V == 4) {
+                const float4 u = *reinterpret_cast<const float4 *>(pk + (size_t)x * D + lane * 4);
+                v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+            } else {
+                const float2 u = *reinterpret_cast<const float2 *>(pk + (size_t)x * D + lane * 2);
+                v[0] = u.x, v[1] = u.y;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] = fmaf(fk, v[i], sum[i]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    const float inv = 1.f / l;
+    if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(y + lane * 4) = make_uint2(pack_bf(sum[0] * inv, sum[1] * inv), pack_bf(sum[2] * inv, sum[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(y + lane * 2) = pack_bf(sum[0] * inv, sum[1] * inv);
+}
+
+constexpr int kJoinWarps = 8;
+constexpr int kLongBlocks = 8;  // CTAs to a long item's 256 rows
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
+    wait_for_launch();
+    const PlanView v = plan_view(p.plan, p.R, p.ctas);
+    const bool lng = blockIdx.y > 0;
+    const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Start *start = lng ? v.long_start : v.short_start;
+    const Start s = start[c], before = start[c - 1];
+    const int listed = lng ? v.head->n_long : v.head->n_short;
+    if (v.head->short_rows != p.short_rows || v.head->max_len != p.max_len || v.head->ctas != p.ctas || v.head->R != p.R) return;
+    if (s.idx >= listed || s.part == 0) return;  // this share begins with a head
+    auto same = [&](const Start &o) { return o.idx == s.idx && o.item == s.item && o.head == s.head && o.part > 0; };
+    if (same(before)) return;  // an earlier boundary's
+    // this head's parts: CTA c - 1's, and those of the shares that begin within it
+    int n = 1;
+    for (int k = c;; k += 32) {
+        const unsigned more = __ballot_sync(~0u, k + lane < p.ctas && same(start[min(k + lane, p.ctas)]));
+        n += more == ~0u ? 32 : __ffs(~more) - 1;
+        if (more != ~0u) break;
+    }
+    const int4 q = (lng ? v.longs : v.shorts)[s.idx];
+    if (!lng) {
+        for (int x = warp; x < q.z * p.g; x += kJoinWarps) {
+            const int token = x / p.g;
+            join_row<D>(p.short_parts, part_floats(p.short_rows, D), p.short_rows, c, n, start, x,
+                        p.y + ((long long)(q.y + token) * p.Hq + s.head * p.g + x - token * p.g) * D);
+        }
+        return;
+    }
+    const int tokens = tile_tokens(p.g);
+    for (int x = (blockIdx.y - 1) * kJoinWarps + warp; x < 2 * kTileRows; x += kLongBlocks * kJoinWarps) {
+        const int in = x & (kTileRows - 1), token = s.item * 2 * tokens + (x / kTileRows) * tokens + in / p.g;
+        if (in >= tokens * p.g || token >= q.z) continue;
+        join_row<D>(p.long_parts, part_floats(2 * kTileRows, D), 2 * kTileRows, c, n, start, x,
+                    p.y + ((long long)(q.y + token) * p.Hq + s.head * p.g + in % p.g) * D);
+    }
+}
+
+template <class C>
+cudaError_t launch_cfg(const Params &p, const CUtensorMap &k, const CUtensorMap &v, bool early, cudaStream_t s) {
+    static SmemGrants grants;
+    const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&short_kernel<C>), C::BYTES, grants);
+    if (e != cudaSuccess) return e;
+    return launch(short_kernel<C>, p.ctas, kThreads, C::BYTES, s, early, p, k, v);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_rows(const Params &p, const CUtensorMap &k, const CUtensorMap &v, bool early, cudaStream_t s) {
+    return p.short_rows == 16 ? launch_cfg<Cfg<D, E4M3, 1>>(p, k, v, early, s) : launch_cfg<Cfg<D, E4M3, 2>>(p, k, v, early, s);
+}
+
+}  // namespace
+
+cudaError_t short_launch(const Params &p, int D, bool e4m3, const CUtensorMap &k, const CUtensorMap &v, bool early,
+                         cudaStream_t s) {
+    if (D == 64) return e4m3 ? launch_rows<64, true>(p, k, v, early, s) : launch_rows<64, false>(p, k, v, early, s);
+    return e4m3 ? launch_rows<128, true>(p, k, v, early, s) : launch_rows<128, false>(p, k, v, early, s);
+}
+
+cudaError_t join_launch(const Params &p, int D, bool any_long, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.ctas - 1, any_long ? 1 + kLongBlocks : 1), cfg.blockDim = dim3(kJoinWarps * 32), cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr, cfg.numAttrs = 1;
+    return D == 64 ? cudaLaunchKernelEx(&cfg, join_kernel<64>, p) : cudaLaunchKernelEx(&cfg, join_kernel<128>, p);
+}
+
+}  // namespace attn
+}  // namespace rs
