@@ -106,14 +106,14 @@ struct Params {
 __host__ __device__ inline size_t part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
 
 // ---------------------------------------------------------------- waits
-struct Abort {
-    uint32_t flag;
-};
-// As mbar_wait, but any wait of the CTA that gives up ends the others too.
+// As mbar_wait, but any wait of the CTA that gives up ends the others too.  A waiting
+// thread sleeps (mbar_try_wait_sleep) between its looks at the time: hundreds of threads that
+// read the global timer in a loop hold up each other.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, volatile uint32_t *abort, uint32_t *status) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_sleep(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try_wait_sleep(bar, parity)) {
         if (*abort) return false;
         if (global_ns() - t0 > kWaitLimitNs) {
             *abort = 1;

@@ -36,6 +36,9 @@ struct Cfg {
     static constexpr int D = D_;
     static constexpr bool E4M3 = E4M3_;
     static constexpr int THREADS = E4M3 ? 512 : 384;
+    // Registers a thread by role, out of those of the launch (168 or 128 each)
+    static constexpr int ROW_REGS = E4M3 ? 184 : 216, ISSUE_REGS = E4M3 ? 56 : 64, CONVERT_REGS = 88;
+    static_assert(256 * ROW_REGS + 128 * ISSUE_REGS + (E4M3 ? 128 * CONVERT_REGS : 0) <= THREADS * (E4M3 ? 128 : 168), "");
     static constexpr int HALF = 128 * 128;                 // 128 rows of 128 bytes
     static constexpr int TILE = (D / 64) * HALF;           // 128 rows of Q, K or V
     static constexpr int STAGES = D == 64 ? 8 : E4M3 ? 3 : 5;
@@ -133,7 +136,7 @@ struct Walk {
     int items, t0, tn;      // the request's items; the piece's first token and tokens
     int keys;               // of the whole request
     int tiles, last;        // key tiles that the item sees, the piece's end among them
-    int need[2];            // key tiles that either query tile sees
+    int need0, need1;       // key tiles that either query tile sees
     __device__ __forceinline__ void begin(const Params &p, const PlanView &v) {
         at = v.long_start[blockIdx.x], end = v.long_start[blockIdx.x + 1];
         n = v.head->n_long, list = v.longs, Hk = p.Hk, tokens = tile_tokens(p.g);
@@ -146,14 +149,19 @@ struct Walk {
         items = (q.z + 2 * tokens - 1) / (2 * tokens);
         t0 = at.item * 2 * tokens, tn = min(2 * tokens, q.z - t0);
         keys = q.z + q.w;
-        need[0] = (q.w + t0 + min(tn, tokens) + kTileKeys - 1) / kTileKeys;
+        need0 = (q.w + t0 + min(tn, tokens) + kTileKeys - 1) / kTileKeys;
         tiles = (q.w + t0 + tn + kTileKeys - 1) / kTileKeys;
-        need[1] = tn > tokens ? tiles : 0;
+        need1 = tn > tokens ? tiles : 0;
         last = same ? end.part : tiles;
         return true;
     }
+    __device__ __forceinline__ int need(int i) const { return i ? need1 : need0; }
     __device__ __forceinline__ bool whole() const { return at.part == 0 && last == tiles; }
     __device__ __forceinline__ void step() {
+        if (at.idx == end.idx && at.item == end.item && at.head == end.head) {  // the share ends within this head
+            at = end;
+            return;
+        }
         at.part = 0;
         if (++at.head < Hk) return;
         at.head = 0;
@@ -193,7 +201,7 @@ __device__ __forceinline__ void copy_role(const Params &p, const PlanView &v, co
         }
         first_piece = false;
         if (lane == 0) {
-            const int tiles = w.need[1] ? 2 : 1;
+            const int tiles = w.need1 ? 2 : 1;
             ++*const_cast<volatile uint32_t *>(&b->begun_q);
             mbar_arrive_expect_tx(&b->q_full, tiles * (C::D / 64) * w.tokens * p.g * 128);
             for (int i = 0; i < tiles; ++i)
@@ -366,12 +374,12 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (j > w.at.part && j - 1 < w.need[i]) {
+                if (j > w.at.part && j - 1 < w.need(i)) {
                     if (!wait(b->p_ready + i, p_parity[i])) return false;
                     p_parity[i] ^= 1;
                     values(i, v_stage, j - 1 > w.at.part);
                 }
-                if (j < w.last && j < w.need[i]) scores(i, k_stage);
+                if (j < w.last && j < w.need(i)) scores(i, k_stage);
             }
             if (j > w.at.part) release(b->empty + v_stage);
             if (j < w.last) {
@@ -400,11 +408,11 @@ __device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int
     w.begin(p, v);
     const int token_in = row / p.g, head_in = row - token_in * p.g;
     for (; w.piece(); w.step()) {
-        if (i == 1 && !w.need[1]) continue;
+        if (i == 1 && !w.need1) continue;
         const int token = w.t0 + i * w.tokens + token_in;
         const bool real = token_in < w.tokens && token < w.q.z;
         const int first = w.q.w + w.t0 + i * w.tokens, limit = w.q.w + min(token, w.q.z - 1);  // last keys that the tile's first row and this one see
-        const int end = min(w.last, w.need[i]);
+        const int end = min(w.last, w.need(i));
         float m = -INFINITY;
         f2 l2 = 0;
         for (int j = w.at.part; j < end; ++j, ++count) {
@@ -556,12 +564,14 @@ long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
     if (mine) {
         bool ok = true;
         if (warp < 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::ROW_REGS));
             row_role<C>(p, v, warp >> 2, b);
-        } else if (warp == 8) {
-            ok = product_role<C>(p, v, sm, b);
-        } else if (warp == 9) {
-            copy_role<C>(p, v, &qm, &km, &vm, sm, b);
-        } else if (C::E4M3 && warp >= 12) {
+        } else if (warp < 12) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::ISSUE_REGS));
+            if (warp == 8) ok = product_role<C>(p, v, sm, b);
+            if (warp == 9) copy_role<C>(p, v, &qm, &km, &vm, sm, b);
+        } else if constexpr (C::E4M3) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONVERT_REGS));
             convert_role<C>(p, v, sm, b);
         }
         if (warp == 8 && !ok) {  // products still in flight; elect_one() names the lane that issued them

@@ -136,6 +136,10 @@ struct Walk {
         return true;
     }
     __device__ __forceinline__ void step() {
+        if (at.idx == end.idx && at.head == end.head) {  // the share ends within this head
+            at = end;
+            return;
+        }
         at.part = 0;
         if (++at.head < Hk) return;
         at.head = 0, ++at.idx;
@@ -158,7 +162,6 @@ __device__ __forceinline__ void produce(const Params &p, const PlanView &v, cons
     const int half = copies_scales ? 0 : (lane >> 1) % C::HALVES;
     const int box = copies_scales ? (lane - 16) >> 1 : (lane >> 1) / C::HALVES;
     const bool copier = lane < copies;
-    const CUtensorMap *const map = is_v ? vm : km;
     const uint8_t *const scales = is_v ? p.vs : p.ks;
     Ring ring;
     bool first_round = true;
@@ -183,8 +186,11 @@ __device__ __forceinline__ void produce(const Params &p, const PlanView &v, cons
             const uint32_t stage = sm + ring.at * 2 * C::TILE;
             if (copier) {  // a coordinate past the cache fills in zeros
                 const int slab = page >= 0 ? page * p.Hk + w.at.head : p.n_pages * p.Hk;
-                tma_load_3d(stage + (is_v ? C::TILE : 0) + half * (kKeys * 128) + box * rows * min(C::ROWB, 128), map,
-                            half * 64, row, slab, full + ring.at);
+                const uint32_t to = stage + half * (kKeys * 128) + box * rows * min(C::ROWB, 128);
+                if (is_v)
+                    tma_load_3d(to + C::TILE, vm, half * 64, row, slab, full + ring.at);
+                else
+                    tma_load_3d(to, km, half * 64, row, slab, full + ring.at);
             } else if (copies_scales && page >= 0) {
                 bulk_load(sm + C::SCALES + (ring.at * 2 + is_v) * kKeys + box * rows,
                           scales + (((size_t)page * p.Hk + w.at.head) << p.page_log) + row, rows, full + ring.at);
