@@ -19,8 +19,11 @@
 // sum is that of the unrounded weights, fp32.
 //
 // Warps: 0-3 and 4-7 a thread a row of either tile; 8 issues the products; 9 the copies
-// (TMA, 128-byte swizzle, keys and values by turns in one ring).  From an 8-bit cache the codes are
+// (TMA, 128-byte swizzle, keys and values by turns in one ring); 12-15 take O out at the end of a piece,
+// while the next one's first products and weights are under way.  From an 8-bit cache the codes are
 // copied, and warps 12-15 turn them into bf16 tiles, code times power of two, exactly.
+// A piece of a single query tile (few tokens) takes its key tiles by turns as tile 0 and tile 1,
+// with sums and references of their own, which its end puts together.
 //
 // TMEM columns: S_0 [0, 128), S_1 [128, 256), O_0 [256, 256 + D), O_1 after it.
 #include "rs_attn.cuh"
@@ -31,37 +34,41 @@ namespace {
 
 using f2 = unsigned long long;  // two fp32 values, the operand of paired arithmetic
 
+constexpr int kThreads = 512;
+
 template <int D_, bool E4M3_>
 struct Cfg {
     static constexpr int D = D_;
     static constexpr bool E4M3 = E4M3_;
-    static constexpr int THREADS = E4M3 ? 512 : 384;
-    // Registers a thread by role, out of those of the launch (168 or 128 each)
-    static constexpr int ROW_REGS = E4M3 ? 184 : 216, ISSUE_REGS = E4M3 ? 56 : 64, CONVERT_REGS = 88;
-    static_assert(256 * ROW_REGS + 128 * ISSUE_REGS + (E4M3 ? 128 * CONVERT_REGS : 0) <= THREADS * (E4M3 ? 128 : 168), "");
     static constexpr int HALF = 128 * 128;                 // 128 rows of 128 bytes
     static constexpr int TILE = (D / 64) * HALF;           // 128 rows of Q, K or V
-    static constexpr int STAGES = D == 64 ? 8 : E4M3 ? 3 : 5;
+    static constexpr int QS = E4M3 ? 2 : 3;                // places for query tiles
+    static constexpr int STAGES = D == 64 ? 8 : E4M3 ? 3 : 4;
     static constexpr int RAWS = E4M3 ? 4 : 0;              // tiles of codes
     static constexpr int RAW = 128 * D;
     static constexpr int Q = 0;
-    static constexpr int RING = 2 * TILE;
+    static constexpr int RING = QS * TILE;
     static constexpr int CODES = RING + STAGES * TILE;
-    static constexpr int SCALES = CODES + RAWS * RAW;      // [RAWS][128]
-    static constexpr int BARS = SCALES + RAWS * 128;
-    static constexpr int BYTES = BARS + 512 + 1024;        // and room to align
+    static constexpr int TILES = CODES + RAWS * RAW;       // bytes of all tiles, from a multiple of 1024 on
+    static constexpr int SMALL = 3072;                     // what lies before them
+    static constexpr int BYTES = SMALL + TILES;
     static_assert(BYTES <= 227 * 1024, "");
+    // Registers a thread by role, out of the launch's 128 each
+    static constexpr int ROW_REGS = 184, ISSUE_REGS = 56, HELP_REGS = 88;
+    static_assert(256 * ROW_REGS + 128 * ISSUE_REGS + 128 * HELP_REGS <= kThreads * 128, "");
 };
 
-constexpr int kMaxStages = 8, kMaxRaws = 4;
-struct Bars {
+constexpr int kMaxStages = 8, kMaxRaws = 4, kMaxQs = 3;
+struct Shared {
+    float2 ml[2][kTileRows];                              // a piece's largest scores (in log2) and sums of weights
+    uint8_t scales[kMaxRaws][kTileKeys];
     uint64_t full[kMaxStages], empty[kMaxStages];         // tiles of keys and values
     uint64_t raw_full[kMaxRaws], raw_empty[kMaxRaws];     // tiles of codes
-    uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_ready[2], pv_done[2], end;
-    uint32_t tmem, abort, begun, begun_q;                 // begun: copied tiles, of codes or not
+    uint64_t q_full[kMaxQs], q_empty[kMaxQs];
+    uint64_t s_full[2], p_ready[2], pv_done[2], o_full[2], o_free[2], end;
+    uint32_t tmem, abort, begun, begun_q[kMaxQs];         // begun: copied tiles, of codes or not
 };
-static_assert(sizeof(Bars) <= 512, "");
+static_assert(sizeof(Shared) <= 3072, "");
 
 // ---------------------------------------------------------------- tensor cores
 __device__ __forceinline__ bool elect_one() {
@@ -136,7 +143,8 @@ struct Walk {
     int items, t0, tn;      // the request's items; the piece's first token and tokens
     int keys;               // of the whole request
     int tiles, last;        // key tiles that the item sees, the piece's end among them
-    int need0, need1;       // key tiles that either query tile sees
+    int need0;              // key tiles that the first query tile sees
+    bool one;               // a single query tile
     __device__ __forceinline__ void begin(const Params &p, const PlanView &v) {
         at = v.long_start[blockIdx.x], end = v.long_start[blockIdx.x + 1];
         n = v.head->n_long, list = v.longs, Hk = p.Hk, tokens = tile_tokens(p.g);
@@ -151,11 +159,14 @@ struct Walk {
         keys = q.z + q.w;
         need0 = (q.w + t0 + min(tn, tokens) + kTileKeys - 1) / kTileKeys;
         tiles = (q.w + t0 + tn + kTileKeys - 1) / kTileKeys;
-        need1 = tn > tokens ? tiles : 0;
+        one = tn <= tokens;
         last = same ? end.part : tiles;
         return true;
     }
-    __device__ __forceinline__ int need(int i) const { return i ? need1 : need0; }
+    // The key tiles of place i: first(i), first(i) + stride() .. below end_of(i)
+    __device__ __forceinline__ int first(int i) const { return at.part + (one ? i : 0); }
+    __device__ __forceinline__ int end_of(int i) const { return one || i ? last : min(last, need0); }
+    __device__ __forceinline__ int stride() const { return one ? 2 : 1; }
     __device__ __forceinline__ bool whole() const { return at.part == 0 && last == tiles; }
     __device__ __forceinline__ void step() {
         if (at.idx == end.idx && at.item == end.item && at.head == end.head) {  // the share ends within this head
@@ -175,7 +186,7 @@ struct Walk {
 // ---------------------------------------------------------------- copies
 template <class C>
 __device__ __forceinline__ void copy_role(const Params &p, const PlanView &v, const CUtensorMap *qm, const CUtensorMap *km,
-                                          const CUtensorMap *vm, uint32_t sm, Bars *b) {
+                                          const CUtensorMap *vm, uint32_t sm, Shared *b) {
     constexpr int ROWB = C::E4M3 ? C::D : C::D * 2, HALVES = ROWB > 128 ? 2 : 1;
     constexpr int UNIT = C::E4M3 ? C::RAW : C::TILE, UNITS = C::E4M3 ? C::RAWS : C::STAGES;
     uint64_t *const full = C::E4M3 ? b->raw_full : b->full, *const empty = C::E4M3 ? b->raw_empty : b->empty;
@@ -184,9 +195,8 @@ __device__ __forceinline__ void copy_role(const Params &p, const PlanView &v, co
     const bool scales = C::E4M3 && lane >= 16 && lane < 16 + boxes;
     const bool copier = lane < boxes * HALVES;
     const int half = scales ? 0 : lane % HALVES, box = scales ? lane - 16 : lane / HALVES;
-    Ring ring;
-    bool first_round = true, first_piece = true;
-    unsigned q_parity = 0;
+    Ring ring, qs;
+    bool first_round = true, first_q = true;
     Walk w;
     w.begin(p, v);
     for (; w.piece(); w.step()) {
@@ -194,21 +204,22 @@ __device__ __forceinline__ void copy_role(const Params &p, const PlanView &v, co
             const int key = j * kTileKeys + box * rows;
             return (copier || scales) && j < w.last && key < w.keys ? page_of(p, w.q.x, key >> p.page_log) : -1;
         };
-        int page = page_at(w.at.part);
-        if (!first_piece) {
-            if (!wait_warp(&b->q_empty, q_parity, &b->abort, p.status)) return;
-            q_parity ^= 1;
-        }
-        first_piece = false;
-        if (lane == 0) {
-            const int tiles = w.need1 ? 2 : 1;
-            ++*const_cast<volatile uint32_t *>(&b->begun_q);
-            mbar_arrive_expect_tx(&b->q_full, tiles * (C::D / 64) * w.tokens * p.g * 128);
-            for (int i = 0; i < tiles; ++i)
+        auto queries = [&](int i) {
+            if (!first_q && !wait_warp(b->q_empty + qs.at, qs.parity ^ 1, &b->abort, p.status)) return false;
+            if (lane == 0) {
+                ++*const_cast<volatile uint32_t *>(b->begun_q + qs.at);
+                mbar_arrive_expect_tx(b->q_full + qs.at, (C::D / 64) * w.tokens * p.g * 128);
                 for (int h = 0; h < C::D / 64; ++h)
-                    tma_load_3d(sm + C::Q + i * C::TILE + h * C::HALF, qm, h * 64, w.at.head * p.g, w.q.y + w.t0 + i * w.tokens, &b->q_full);
-        }
-        __syncwarp();
+                    tma_load_3d(sm + C::Q + qs.at * C::TILE + h * C::HALF, qm, h * 64, w.at.head * p.g, w.q.y + w.t0 + i * w.tokens,
+                                b->q_full + qs.at);
+            }
+            __syncwarp();
+            qs.step(C::QS);
+            if (qs.at == 0) first_q = false;
+            return true;
+        };
+        int page = page_at(w.at.part);
+        if (!queries(0)) return;
         for (int j = w.at.part; j < w.last; ++j) {
             const int next = page_at(j + 1);  // in flight while this tile waits for its place
             const int row = (j * kTileKeys + box * rows) & (p.page - 1);
@@ -226,74 +237,178 @@ __device__ __forceinline__ void copy_role(const Params &p, const PlanView &v, co
                 if (copier)
                     tma_load_3d(to + half * C::HALF + box * rows * min(ROWB, 128), kv ? vm : km, half * 64, row, slab, full + ring.at);
                 else if (scales && page >= 0)
-                    bulk_load(sm + C::SCALES + ring.at * 128 + box * rows,
+                    bulk_load(smem_u32(b->scales[ring.at % kMaxRaws]) + box * rows,
                               (kv ? p.vs : p.ks) + (((size_t)page * p.Hk + w.at.head) << p.page_log) + row, rows, full + ring.at);
                 ring.step(UNITS);
                 if (ring.at == 0) first_round = false;
+                // the second query tile behind the first keys: its place is free last
+                if (kv == 0 && j == w.at.part && !w.one && !queries(1)) return;
             }
             page = next;
         }
     }
     // the last arrivals on the barriers that this warp waits on
-    if (!first_piece) wait_warp(&b->q_empty, q_parity, &b->abort, p.status);
-    for (int i = 0; i < UNITS; ++i) {
+    for (int i = 0; i < C::QS; ++i)
+        if (!first_q || i < qs.at) wait_warp(b->q_empty + i, first_q ? 0 : i < qs.at ? qs.parity : qs.parity ^ 1, &b->abort, p.status);
+    for (int i = 0; i < UNITS; ++i)
         if (!first_round || i < ring.at) wait_warp(empty + i, first_round ? 0 : i < ring.at ? ring.parity : ring.parity ^ 1, &b->abort, p.status);
-    }
 }
 
 // After giving up: wait (with a limit) for the copies still in flight.
 template <class C>
-__device__ __forceinline__ void drain(Bars *b) {
+__device__ __forceinline__ void drain(Shared *b) {
     constexpr int UNITS = C::E4M3 ? C::RAWS : C::STAGES;
     uint64_t *const full = C::E4M3 ? b->raw_full : b->full;
-    const int begun = *const_cast<volatile uint32_t *>(&b->begun), q = *const_cast<volatile uint32_t *>(&b->begun_q);
+    const int begun = *const_cast<volatile uint32_t *>(&b->begun);
     for (int s = 0; s < UNITS; ++s) {
         const int rounds = begun > s ? (begun - s + UNITS - 1) / UNITS : 0;
         if (rounds) mbar_wait(full + s, (rounds - 1) & 1);
     }
-    if (q) mbar_wait(&b->q_full, (q - 1) & 1);
+    for (int i = 0; i < C::QS; ++i) {
+        const int q = *const_cast<volatile uint32_t *>(b->begun_q + i);
+        if (q) mbar_wait(b->q_full + i, (q - 1) & 1);
+    }
 }
 
-// Codes into bf16 tiles, a thread a key.
+// ---------------------------------------------------------------- conversion, and the end of a piece
+// A tile of codes into a bf16 tile, a thread a key; rows behind the last key become zeros.
 template <class C>
-__device__ __forceinline__ void convert_role(const Params &p, const PlanView &v, uint32_t sm, Bars *b) {
+__device__ __forceinline__ void convert_tile(uint32_t from, uint32_t to, uint32_t byte, int row, bool live) {
+    const float up = pow2_of(byte);
+#pragma unroll
+    for (int c = 0; c < C::D / 16; ++c) {
+        const uint32_t at = C::D == 64 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4) : row * 128 + ((c ^ (row & 7)) << 4);
+        uint32_t x[4], o[8];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(from + at) : "memory");
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t h;
+            float lo, hi;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(x[e >> 1] >> (16 * (e & 1)))));
+            asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(lo), "=f"(hi) : "r"(h));
+            o[e] = live ? pack_bf(lo * up, hi * up) : 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int piece = 2 * c + e;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (piece >> 3) * C::HALF + row * 128 + (((piece ^ row) & 7) << 4)),
+                         "r"(o[4 * e]), "r"(o[4 * e + 1]), "r"(o[4 * e + 2]), "r"(o[4 * e + 3])
+                         : "memory");
+        }
+    }
+}
+
+// The end of a piece, a thread a row: O out of TMEM, to y or to the workspace.  The next piece's
+// scores and weights go on meanwhile.
+template <class C>
+__device__ __forceinline__ bool end_piece(const Params &p, const Walk &w, Shared *b, unsigned (&parity)[2]) {
+    constexpr int D = C::D;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127;
+    const uint32_t t_o = b->tmem + ((uint32_t)(warp & 3) << 21) + 256;
+    const int token_in = row / p.g, head_in = row - token_in * p.g;
+    const bool whole = w.whole();
+    float *const part = p.long_parts + (size_t)(2 * blockIdx.x + (w.at.part > 0 ? 0 : 1)) * part_floats(2 * kTileRows, D);
+#pragma unroll 1
+    for (int i = 0; i < (w.one ? 1 : 2); ++i) {
+        const int token = w.t0 + i * w.tokens + token_in;
+        const bool real = token_in < w.tokens && token < w.q.z;
+        // the places whose sums these rows have: 0 and 1 both where one tile took both
+        const int places = w.one ? (w.first(1) < w.end_of(1) ? 2 : 1) : w.first(i) < w.end_of(i) ? 1 : 0;
+        float2 v = make_float2(-INFINITY, 0.f), v1 = v;
+        if (places) {
+            if (!wait_warp(b->o_full + i, i ? parity[1] : parity[0], &b->abort, p.status)) return false;
+            if (places == 2 && !wait_warp(b->o_full + 1, parity[1], &b->abort, p.status)) return false;
+            if (i || places == 2) parity[1] ^= 1;
+            if (!i) parity[0] ^= 1;
+            tc_fence_after_sync();
+            v = b->ml[i][row];
+            if (places == 2) v1 = b->ml[1][row];
+        }
+        const float m = fmaxf(v.x, v1.x);
+        // a row that has seen no key in a place: sums of zero there
+        const float f0 = v.x == -INFINITY ? 1.f : ex2(v.x - m), f1 = v1.x == -INFINITY ? 1.f : ex2(v1.x - m);
+        const float l = v.y * f0 + v1.y * f1;
+        const float s0 = whole ? f0 / l : f0, s1 = whole ? f1 / l : f1;
+        uint16_t *const y = p.y + ((long long)(w.q.y + token) * p.Hq + w.at.head * p.g + head_in) * D;
+        const int x = i * kTileRows + row;
+        if (!whole && real) reinterpret_cast<float2 *>(part + (size_t)2 * kTileRows * D)[x] = make_float2(m, l);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            if (places) {
+                ld32(t_o + i * D + c, o);
+                ld_done();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s0);
+            if (places == 2) {
+                uint32_t o1[32];
+                ld32(t_o + D + c, o1);
+                ld_done();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), s1, __uint_as_float(o[e])));
+            }
+            if (c + 32 == D && places) {  // O is free
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(b->o_free + i);
+                    if (places == 2) mbar_arrive(b->o_free + 1);
+                }
+            }
+            if (!real) continue;
+            if (whole) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint4 u;
+                    u.x = pack_bf(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+                    u.y = pack_bf(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                    u.z = pack_bf(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
+                    u.w = pack_bf(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
+                    *reinterpret_cast<uint4 *>(y + c + e) = u;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<uint4 *>(part + (size_t)x * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+        }
+    }
+    return true;
+}
+
+// Tiles of codes become bf16 tiles, pieces are ended.  With codes, a piece is ended when the next
+// one's first tiles are there, as many as the ring holds: the products need those first.
+template <class C>
+__device__ __forceinline__ void help_role(const Params &p, const PlanView &v, uint32_t sm, Shared *b) {
     const int lane = threadIdx.x & 31, row = threadIdx.x & 127;
-    Ring ring, raw;
-    bool first_round = true;
+    unsigned parity[2] = {0, 0};
     Walk w;
     w.begin(p, v);
-    for (; w.piece(); w.step()) {
-        for (int j = w.at.part; j < w.last; ++j) {
-            const bool live = j * kTileKeys + row < w.keys;
+    if constexpr (!C::E4M3) {
+        for (; w.piece(); w.step())
+            if (!end_piece<C>(p, w, b, parity)) return;
+    } else {
+        Ring ring, raw;
+        bool first_round = true, to_end = false;
+        Walk before = w;
+        for (; w.piece(); w.step()) {
+            const int units = 2 * (w.last - w.at.part);
 #pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
+            for (int u = 0; u < units || to_end; ++u) {
+                if (to_end && (u == C::STAGES || u == units)) {
+                    if (!end_piece<C>(p, before, b, parity)) return;
+                    to_end = false;
+                    if (u == units) break;
+                }
+                const int j = w.at.part + (u >> 1);
                 if (!wait_warp(b->raw_full + raw.at, raw.parity, &b->abort, p.status)) return;
                 if (!first_round && !wait_warp(b->empty + ring.at, ring.parity ^ 1, &b->abort, p.status)) return;
-                const uint32_t from = sm + C::CODES + raw.at * C::RAW, to = sm + C::RING + ring.at * C::TILE;
-                uint32_t byte;
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(sm + C::SCALES + raw.at * 128 + row) : "memory");
-                const float up = pow2_of(byte);
-#pragma unroll
-                for (int c = 0; c < C::D / 16; ++c) {
-                    const uint32_t at = C::D == 64 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4) : row * 128 + ((c ^ (row & 7)) << 4);
-                    uint32_t x[4], o[8];
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(from + at) : "memory");
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint32_t h;
-                        float lo, hi;
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(x[e >> 1] >> (16 * (e & 1)))));
-                        asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(lo), "=f"(hi) : "r"(h));
-                        o[e] = live ? pack_bf(lo * up, hi * up) : 0;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int piece = 2 * c + e;
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (piece >> 3) * C::HALF + row * 128 + (((piece ^ row) & 7) << 4)),
-                                     "r"(o[4 * e]), "r"(o[4 * e + 1]), "r"(o[4 * e + 2]), "r"(o[4 * e + 3])
-                                     : "memory");
-                    }
-                }
+                convert_tile<C>(sm + C::CODES + raw.at * C::RAW, sm + C::RING + ring.at * C::TILE, b->scales[raw.at][row], row,
+                                j * kTileKeys + row < w.keys);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b->full + ring.at), mbar_arrive(b->raw_empty + raw.at);
@@ -301,29 +416,33 @@ __device__ __forceinline__ void convert_role(const Params &p, const PlanView &v,
                 ring.step(C::STAGES);
                 if (ring.at == 0) first_round = false;
             }
+            before = w, to_end = true;
         }
+        if (to_end && !end_piece<C>(p, before, b, parity)) return;
+        for (int i = 0; i < C::STAGES; ++i)
+            if (!first_round || i < ring.at)
+                wait_warp(b->empty + i, first_round ? 0 : i < ring.at ? ring.parity : ring.parity ^ 1, &b->abort, p.status);
     }
-    for (int i = 0; i < C::STAGES; ++i)
-        if (!first_round || i < ring.at) wait_warp(b->empty + i, first_round ? 0 : i < ring.at ? ring.parity : ring.parity ^ 1, &b->abort, p.status);
 }
 
 // ---------------------------------------------------------------- products
 template <class C>
-__device__ __forceinline__ bool product_role(const Params &p, const PlanView &v, uint32_t sm, Bars *b) {
+__device__ __forceinline__ bool product_role(const Params &p, const PlanView &v, uint32_t sm, Shared *b) {
     constexpr int D = C::D;
     constexpr uint32_t kIdescS = umma_idesc_bf16(128, 128, false, false), kIdescO = umma_idesc_bf16(128, D, false, true);
     const int lane = threadIdx.x & 31;
     const uint32_t tmem = b->tmem;
-    Ring ring;
-    unsigned q_parity = 0, p_parity[2] = {0, 0};
+    Ring ring, qs;
+    unsigned p_parity = 0, o_parity = 0, o_used = 0;  // a bit for each place
     auto wait = [&](uint64_t *bar, unsigned parity) {
         const bool ok = wait_warp(bar, parity, &b->abort, p.status);
         tc_fence_after_sync();
         return ok;
     };
-    auto scores = [&](int i, int stage) {
+    // S_i = Q K^T
+    auto scores = [&](int i, int q, int stage) {
         if (elect_one()) {
-            const uint32_t a = desc_lo(sm + C::Q + i * C::TILE, 16), k = desc_lo(sm + C::RING + stage * C::TILE, 16);
+            const uint32_t a = desc_lo(sm + C::Q + q * C::TILE, 16), k = desc_lo(sm + C::RING + stage * C::TILE, 16);
 #pragma unroll
             for (int x = 0; x < D / 16; ++x)
                 mma_ss(tmem + i * 128, a + (x >> 2) * (C::HALF >> 4) + (x & 3) * 2, k + (x >> 2) * (C::HALF >> 4) + (x & 3) * 2, kIdescS, x > 0);
@@ -331,15 +450,27 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
         }
         __syncwarp();
     };
-    auto values = [&](int i, int stage, bool acc) {
+    // O_i (+)= P_i V; first: of the piece, when the last one's O_i has to be out of its place
+    auto values = [&](int i, int stage, bool first, bool last) {
+        if (!wait(b->p_ready + i, p_parity >> i & 1)) return false;
+        p_parity ^= 1u << i;
+        if (first) {
+            if (o_used >> i & 1) {
+                if (!wait(b->o_free + i, o_parity >> i & 1)) return false;
+                o_parity ^= 1u << i;
+            }
+            o_used |= 1u << i;
+        }
         if (elect_one()) {
             const uint32_t vd = desc_lo(sm + C::RING + stage * C::TILE, C::HALF);
 #pragma unroll
             for (int x = 0; x < kTileKeys / 16; ++x)
-                mma_ts(tmem + 256 + i * D, tmem + i * 128 + x * 8, vd + x * 128, kIdescO, acc || x > 0);
+                mma_ts(tmem + 256 + i * D, tmem + i * 128 + x * 8, vd + x * 128, kIdescO, !first || x > 0);
             umma_commit(b->pv_done + i);
+            if (last) umma_commit(b->o_full + i);
         }
         __syncwarp();
+        return true;
     };
     auto release = [&](uint64_t *bar) {
         if (elect_one()) umma_commit(bar);
@@ -362,9 +493,41 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
     Walk w;
     w.begin(p, v);
     for (; w.piece(); w.step()) {
-        if (!wait(&b->q_full, q_parity)) return false;
-        q_parity ^= 1;
+        const int q0 = qs.at;
+        if (!wait(b->q_full + q0, qs.parity)) return false;
+        qs.step(C::QS);
+        if (w.one) {
+            // a single query tile: key tiles by turns in both places, so that the products of one
+            // run beside the register work of the other
+            int v0 = 0, v1 = 0;  // the places' values
+            for (int j = w.at.part; j < w.last + 2; ++j) {
+                const int i = (j - w.at.part) & 1;
+                if (j - 2 >= w.at.part) {
+                    const int stage = i ? v1 : v0;
+                    if (!values(i, stage, j - 2 < w.at.part + 2, j >= w.last)) return false;
+                    release(b->empty + stage);
+                }
+                if (j >= w.last) continue;
+                const int k_stage = ring.at;
+                if (!wait(b->full + k_stage, ring.parity)) return false;
+                ring.step(C::STAGES);
+                scores(i, q0, k_stage);
+                release(b->empty + k_stage);
+                if (j == w.last - 1) release(b->q_empty + q0);
+                const int stage = ring.at;
+                if (!wait(b->full + stage, ring.parity)) return false;
+                ring.step(C::STAGES);
+                clear(stage, w.keys - j * kTileKeys);
+                if (i) v1 = stage; else v0 = stage;
+            }
+            continue;
+        }
+        const int q1 = qs.at;
+        const unsigned q1_parity = qs.parity;
+        qs.step(C::QS);
         int v_stage = 0;
+        const int end0 = w.end_of(0);
+        if (end0 <= w.at.part) release(b->q_empty + q0);  // the first tile's rows see none of these keys
         for (int j = w.at.part; j <= w.last; ++j) {
             // K_j at the ring's place, V_j behind it; V_(j-1) at v_stage
             const int k_stage = ring.at;
@@ -372,19 +535,20 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
                 if (!wait(b->full + k_stage, ring.parity)) return false;
                 ring.step(C::STAGES);
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (j > w.at.part && j - 1 < w.need(i)) {
-                    if (!wait(b->p_ready + i, p_parity[i])) return false;
-                    p_parity[i] ^= 1;
-                    values(i, v_stage, j - 1 > w.at.part);
-                }
-                if (j < w.last && j < w.need(i)) scores(i, k_stage);
+            if (j > w.at.part && j <= end0 && !values(0, v_stage, j - 1 == w.at.part, j == end0)) return false;
+            if (j < end0) {
+                scores(0, q0, k_stage);
+                if (j == end0 - 1) release(b->q_empty + q0);
             }
-            if (j > w.at.part) release(b->empty + v_stage);
+            if (j > w.at.part) {
+                if (!values(1, v_stage, j - 1 == w.at.part, j == w.last)) return false;
+                release(b->empty + v_stage);
+            }
             if (j < w.last) {
+                if (j == w.at.part && !wait(b->q_full + q1, q1_parity)) return false;
+                scores(1, q1, k_stage);
                 release(b->empty + k_stage);
-                if (j == w.last - 1) release(&b->q_empty);
+                if (j == w.last - 1) release(b->q_empty + q1);
                 v_stage = ring.at;
                 if (!wait(b->full + v_stage, ring.parity)) return false;
                 ring.step(C::STAGES);
@@ -397,33 +561,32 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
 
 // ---------------------------------------------------------------- a thread a row
 template <class C>
-__device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int i, Bars *b) {
+__device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int i, Shared *b) {
     constexpr int D = C::D;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t t_s = b->tmem + lanes + i * 128, t_o = b->tmem + lanes + 256 + i * D;
     const f2 c2 = f2_pack(p.c, p.c);
-    unsigned count = 0;  // key tiles of this query tile so far
+    unsigned count = 0, ended = 0;  // key tiles of this place so far, pieces
     Walk w;
     w.begin(p, v);
-    const int token_in = row / p.g, head_in = row - token_in * p.g;
+    const int token_in = row / p.g;
     for (; w.piece(); w.step()) {
-        if (i == 1 && !w.need1) continue;
-        const int token = w.t0 + i * w.tokens + token_in;
-        const bool real = token_in < w.tokens && token < w.q.z;
-        const int first = w.q.w + w.t0 + i * w.tokens, limit = w.q.w + min(token, w.q.z - 1);  // last keys that the tile's first row and this one see
-        const int end = min(w.last, w.need(i));
+        const int t0 = w.t0 + (w.one ? 0 : i * w.tokens), token = t0 + token_in;
+        const int first = w.q.w + t0, limit = w.q.w + min(token, w.q.z - 1);  // last keys that the tile's first row and this one see
+        const int begin = w.first(i), end = w.end_of(i), stride = w.stride();
         float m = -INFINITY;
         f2 l2 = 0;
-        for (int j = w.at.part; j < end; ++j, ++count) {
+        for (int j = begin; j < end; j += stride, ++count) {
             if (!wait_warp(b->s_full + i, count & 1, &b->abort, p.status)) return false;
             tc_fence_after_sync();
             uint32_t s[128];
 #pragma unroll
             for (int c = 0; c < 128; c += 32) ld32(t_s + c, s + c);
             ld_done();
-            if (j * kTileKeys + kTileKeys - 1 > first) {
-                const int seen = limit - j * kTileKeys;
+            const bool masked = j * kTileKeys + kTileKeys - 1 > first;
+            const int seen = limit - j * kTileKeys;
+            if (masked) {
 #pragma unroll
                 for (int c = 0; c < 128; ++c)
                     if (c > seen) s[c] = 0xff800000u;
@@ -438,7 +601,7 @@ __device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int
 #pragma unroll
             for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(s[124 + e]));
             const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-            if (j == w.at.part) {
+            if (j == begin) {
                 m = most;
             } else {
                 const bool behind = (most - m) * p.c > 8.f;
@@ -467,6 +630,16 @@ __device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int
             f2 sum[2] = {0, 0};
 #pragma unroll
             for (int c = 0; c < 128; c += 64) {
+                if (c) {  // the second half again: its registers held the first half's weights
+                    ld32(t_s + 64, s + 64);
+                    ld32(t_s + 96, s + 96);
+                    ld_done();
+                    if (masked) {
+#pragma unroll
+                        for (int k = 64; k < 128; ++k)
+                            if (k > seen) s[k] = 0xff800000u;
+                    }
+                }
                 uint32_t w32[32];
 #pragma unroll
                 for (int e = 0; e < 64; e += 2) {
@@ -480,69 +653,36 @@ __device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int
                 st32(t_s + c / 2, w32);
             }
             l2 = f2_add(l2, f2_add(sum[0], sum[1]));
+            if (j + stride >= end) {
+                // the last piece's are read when its O is out (a piece may have one key tile)
+                if (ended > 0 && !wait_warp(b->o_free + i, (ended - 1) & 1, &b->abort, p.status)) return false;
+                ++ended;
+                float l, l_hi;
+                f2_unpack(l2, l, l_hi);
+                b->ml[i][row] = make_float2(m == -INFINITY ? m : m * p.c, l + l_hi);
+            }
             st_done();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(b->p_ready + i);
         }
-        float l, l_hi;
-        f2_unpack(l2, l, l_hi);
-        l += l_hi;
-        const bool any = end > w.at.part;
-        if (any) {
-            if (!wait_warp(b->pv_done + i, (count - 1) & 1, &b->abort, p.status)) return false;
-            tc_fence_after_sync();
-        }
-        const bool whole = w.whole();
-        const float inv = 1.f / l;
-        uint16_t *const y = p.y + ((long long)(w.q.y + token) * p.Hq + w.at.head * p.g + head_in) * D;
-        float *const part = p.long_parts + (size_t)(2 * blockIdx.x + (w.at.part > 0 ? 0 : 1)) * part_floats(2 * kTileRows, D);
-        const int x = i * kTileRows + row;
-        if (!whole && real) reinterpret_cast<float2 *>(part + (size_t)2 * kTileRows * D)[x] = make_float2(m == -INFINITY ? m : m * p.c, l);
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            if (any) {
-                ld32(t_o + c, o);
-                ld_done();
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0;
-            }
-            if (!real) continue;
-            if (whole) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint4 u;
-                    u.x = pack_bf(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                    u.y = pack_bf(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                    u.z = pack_bf(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                    u.w = pack_bf(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                    *reinterpret_cast<uint4 *>(y + c + e) = u;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<uint4 *>(part + (size_t)x * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            }
-        }
-        tc_fence_before_sync();  // O is read before the next piece's first product
     }
     return true;
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
             const __grid_constant__ CUtensorMap vm) {
-    extern __shared__ unsigned char raw[];
+    extern __shared__ __align__(1024) unsigned char raw[];
     let_next_launch();
-    unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    const uint32_t sm = smem_u32(smem);
-    Bars *b = reinterpret_cast<Bars *>(smem + C::BARS);
+    // the tiles begin on a multiple of 1024 bytes, the swizzle's period
+    const uint32_t sm = (smem_u32(raw) + (uint32_t)sizeof(Shared) + 1023) & ~1023u;
+    Shared *b = reinterpret_cast<Shared *>(raw);
     const PlanView v = plan_view(p.plan, p.R, p.ctas);
-    const bool mine = v.head->short_rows == p.short_rows && v.head->max_len == p.max_len && v.head->ctas == p.ctas &&
-                      v.head->Hq == p.Hq && v.head->Hk == p.Hk && v.head->R == p.R;
+    const bool mine = sm + C::TILES <= smem_u32(raw) + C::BYTES && v.head->short_rows == p.short_rows &&
+                      v.head->max_len == p.max_len && v.head->ctas == p.ctas && v.head->Hq == p.Hq && v.head->Hk == p.Hk &&
+                      v.head->R == p.R;
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
     if (warp == 8) {
         tmem_alloc(&b->tmem, 512);
@@ -550,10 +690,11 @@ long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
             if (!mine && blockIdx.x == 0) atomicOr(p.status, RS_DEV_LENGTH);
             for (int i = 0; i < C::STAGES; ++i) mbar_init(b->full + i, C::E4M3 ? 4 : 1), mbar_init(b->empty + i, 1);
             for (int i = 0; i < C::RAWS; ++i) mbar_init(b->raw_full + i, 1), mbar_init(b->raw_empty + i, 4);
-            mbar_init(&b->q_full, 1), mbar_init(&b->q_empty, 1);
+            for (int i = 0; i < C::QS; ++i) mbar_init(b->q_full + i, 1), mbar_init(b->q_empty + i, 1), b->begun_q[i] = 0;
             for (int i = 0; i < 2; ++i) mbar_init(b->s_full + i, 1), mbar_init(b->p_ready + i, 4), mbar_init(b->pv_done + i, 1);
+            for (int i = 0; i < 2; ++i) mbar_init(b->o_full + i, 1), mbar_init(b->o_free + i, 4);
             mbar_init(&b->end, 1);
-            b->abort = b->begun = b->begun_q = 0;
+            b->abort = b->begun = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         __syncwarp();
@@ -570,9 +711,9 @@ long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::ISSUE_REGS));
             if (warp == 8) ok = product_role<C>(p, v, sm, b);
             if (warp == 9) copy_role<C>(p, v, &qm, &km, &vm, sm, b);
-        } else if constexpr (C::E4M3) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CONVERT_REGS));
-            convert_role<C>(p, v, sm, b);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::HELP_REGS));
+            help_role<C>(p, v, sm, b);
         }
         if (warp == 8 && !ok) {  // products still in flight; elect_one() names the lane that issued them
             if (elect_one()) umma_commit(&b->end);
@@ -592,7 +733,7 @@ cudaError_t launch_cfg(const Params &p, const CUtensorMap &q, const CUtensorMap 
     static SmemGrants grants;
     const cudaError_t e = grant_smem(reinterpret_cast<const void *>(&long_kernel<C>), C::BYTES, grants);
     if (e != cudaSuccess) return e;
-    return launch(long_kernel<C>, p.ctas, C::THREADS, C::BYTES, s, false, p, q, k, v);
+    return launch(long_kernel<C>, p.ctas, kThreads, C::BYTES, s, false, p, q, k, v);
 }
 
 }  // namespace
