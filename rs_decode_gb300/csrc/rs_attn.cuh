@@ -106,22 +106,23 @@ struct Params {
 __host__ __device__ inline size_t part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
 
 // ---------------------------------------------------------------- waits
-// As mbar_wait, but any wait of the CTA that gives up ends the others too.  A waiting
-// thread sleeps (mbar_try_wait_sleep) between its looks at the time: hundreds of threads that
-// read the global timer in a loop hold up each other.
+// As mbar_wait, but any wait of the CTA that gives up ends the others too.  The time is
+// looked at once in a while only.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, volatile uint32_t *abort, uint32_t *status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (mbar_try_wait_sleep(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait_sleep(bar, parity)) {
+    unsigned long long t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 256; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
+        const unsigned long long t = global_ns();
+        if (!t0) t0 = t;
+        if (t - t0 > kWaitLimitNs) {
             *abort = 1;
             atomicOr(status, RS_DEV_TIMEOUT);
             return false;
         }
     }
-    return true;
 }
 // The same for a whole warp, with one answer for all lanes.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volatile uint32_t *abort, uint32_t *status) {
@@ -157,13 +158,31 @@ __device__ __forceinline__ float ex2(float x) {
 // The power of two of an 8-bit head's scale byte (255, of a head that is not finite, gives infinity).
 __device__ __forceinline__ float pow2_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Place n of a paged row of pages, -1 (and a status bit) if the entry names no page.
-__device__ __forceinline__ int page_of(const Params &p, int r, int j) {
-    const int at = j < p.max_pages ? p.pages[(size_t)r * p.max_pages + j] : -1;
-    if (at >= 0 && at < p.n_pages) return at;
-    atomicOr(p.status, RS_DEV_SLOT);
-    return -1;
-}
+// A request's entries of the page table as a copying warp walks along them: a lane
+// holds one of 32, and of the 32 after them, which are loaded long before they are asked for.
+struct PageWindow {
+    int r = -1, first = 0;  // the request, its first entry held
+    int now, next;
+    __device__ __forceinline__ int load(const Params &p, int entries, int e) const {
+        return e < entries ? __ldg(p.pages + (size_t)r * p.max_pages + e) : -1;
+    }
+    // Moves to the 32 entries that hold entry e; entries: those that the request uses.  Whole warps.
+    __device__ __forceinline__ void at(const Params &p, int request, int entries, int e) {
+        const int lane = threadIdx.x & 31, from = e & ~31;
+        if (request == r && from == first) return;
+        const bool on = request == r && from == first + 32;
+        r = request, first = from;
+        now = on ? next : load(p, entries, from + lane);
+        next = load(p, entries, from + 32 + lane);
+    }
+    // The page of entry e for each lane's e in the window, -1 (and a status bit) if it is none of the cache's.
+    __device__ __forceinline__ int page(const Params &p, int e, bool wanted) const {
+        const int got = __shfl_sync(~0u, now, e & 31);
+        if (got >= 0 && got < p.n_pages) return wanted ? got : -1;
+        if (wanted) atomicOr(p.status, RS_DEV_SLOT);
+        return -1;
+    }
+};
 
 __device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -18,7 +18,7 @@
 // asks for: 2^-9 of each, no more than y's own rounding and on average less.  Their
 // sum is that of the unrounded weights, fp32.
 //
-// Warps: 0-3 and 4-7 a thread a row of either tile; 8 issues the products; 9 the copies
+// Warps: 0-3 and 4-7 a thread a row of either tile; 8 issues the products; 9 and 10 the copies
 // (TMA, 128-byte swizzle, keys and values by turns in one ring); 12-15 take O out at the end of a piece,
 // while the next one's first products and weights are under way.  From an 8-bit cache the codes are
 // copied, and warps 12-15 turn them into bf16 tiles, code times power of two, exactly.
@@ -66,7 +66,7 @@ struct Shared {
     uint64_t raw_full[kMaxRaws], raw_empty[kMaxRaws];     // tiles of codes
     uint64_t q_full[kMaxQs], q_empty[kMaxQs];
     uint64_t s_full[2], p_ready[2], pv_done[2], o_full[2], o_free[2], end;
-    uint32_t tmem, abort, begun, begun_q[kMaxQs];         // begun: copied tiles, of codes or not
+    uint32_t tmem, abort, begun[2], begun_q[kMaxQs];      // begun: tiles of keys, of values, of codes or not
 };
 static_assert(sizeof(Shared) <= 3072, "");
 
@@ -184,26 +184,29 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------- copies
+// One warp copies the queries and the keys, another the values.  Keys and values take the
+// places of one ring by turns; their number is even, so that a place always meets the same
+// warp, which then waits on its barriers in every round.
 template <class C>
 __device__ __forceinline__ void copy_role(const Params &p, const PlanView &v, const CUtensorMap *qm, const CUtensorMap *km,
-                                          const CUtensorMap *vm, uint32_t sm, Shared *b) {
+                                          const CUtensorMap *vm, uint32_t sm, Shared *b, int is_v) {
     constexpr int ROWB = C::E4M3 ? C::D : C::D * 2, HALVES = ROWB > 128 ? 2 : 1;
     constexpr int UNIT = C::E4M3 ? C::RAW : C::TILE, UNITS = C::E4M3 ? C::RAWS : C::STAGES;
+    static_assert(UNITS % 2 == 0, "");
     uint64_t *const full = C::E4M3 ? b->raw_full : b->full, *const empty = C::E4M3 ? b->raw_empty : b->empty;
     const int lane = threadIdx.x & 31;
     const int rows = min(p.page, 64), boxes = kTileKeys / rows;
+    // lane -> one copy: 64 channels of a box; then (8 bits) a box's scales
     const bool scales = C::E4M3 && lane >= 16 && lane < 16 + boxes;
     const bool copier = lane < boxes * HALVES;
-    const int half = scales ? 0 : lane % HALVES, box = scales ? lane - 16 : lane / HALVES;
+    const int half = scales ? 0 : lane % HALVES, box = scales ? lane - 16 : min(lane / HALVES, boxes - 1);
     Ring ring, qs;
+    ring.at = is_v;
     bool first_round = true, first_q = true;
+    PageWindow pages;
     Walk w;
     w.begin(p, v);
     for (; w.piece(); w.step()) {
-        auto page_at = [&](int j) {
-            const int key = j * kTileKeys + box * rows;
-            return (copier || scales) && j < w.last && key < w.keys ? page_of(p, w.q.x, key >> p.page_log) : -1;
-        };
         auto queries = [&](int i) {
             if (!first_q && !wait_warp(b->q_empty + qs.at, qs.parity ^ 1, &b->abort, p.status)) return false;
             if (lane == 0) {
@@ -218,39 +221,41 @@ __device__ __forceinline__ void copy_role(const Params &p, const PlanView &v, co
             if (qs.at == 0) first_q = false;
             return true;
         };
-        int page = page_at(w.at.part);
-        if (!queries(0)) return;
+        if (!is_v && !queries(0)) return;
+        const int entries = min((w.keys + p.page - 1) >> p.page_log, p.max_pages);
         for (int j = w.at.part; j < w.last; ++j) {
-            const int next = page_at(j + 1);  // in flight while this tile waits for its place
-            const int row = (j * kTileKeys + box * rows) & (p.page - 1);
+            const int key = j * kTileKeys + box * rows, row = key & (p.page - 1);
+            pages.at(p, w.q.x, entries, (j * kTileKeys) >> p.page_log);
+            const int page = pages.page(p, key >> p.page_log, (copier || scales) && key < w.keys);
             const unsigned with_scales = __ballot_sync(~0u, scales && page >= 0);
             const int slab = page >= 0 ? page * p.Hk + w.at.head : p.n_pages * p.Hk;  // past the cache: zeros
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                if (!first_round && !wait_warp(empty + ring.at, ring.parity ^ 1, &b->abort, p.status)) return;
-                if (lane == 0) {
-                    ++*const_cast<volatile uint32_t *>(&b->begun);
-                    mbar_arrive_expect_tx(full + ring.at, UNIT + __popc(with_scales) * rows);
-                }
-                __syncwarp();
-                const uint32_t to = sm + (C::E4M3 ? C::CODES : C::RING) + ring.at * UNIT;
-                if (copier)
-                    tma_load_3d(to + half * C::HALF + box * rows * min(ROWB, 128), kv ? vm : km, half * 64, row, slab, full + ring.at);
-                else if (scales && page >= 0)
-                    bulk_load(smem_u32(b->scales[ring.at % kMaxRaws]) + box * rows,
-                              (kv ? p.vs : p.ks) + (((size_t)page * p.Hk + w.at.head) << p.page_log) + row, rows, full + ring.at);
-                ring.step(UNITS);
-                if (ring.at == 0) first_round = false;
-                // the second query tile behind the first keys: its place is free last
-                if (kv == 0 && j == w.at.part && !w.one && !queries(1)) return;
+            if (!first_round && !wait_warp(empty + ring.at, ring.parity ^ 1, &b->abort, p.status)) return;
+            if (lane == 0) {
+                ++*const_cast<volatile uint32_t *>(b->begun + is_v);
+                mbar_arrive_expect_tx(full + ring.at, UNIT + __popc(with_scales) * rows);
             }
-            page = next;
+            __syncwarp();
+            const uint32_t to = sm + (C::E4M3 ? C::CODES : C::RING) + ring.at * UNIT + half * C::HALF + box * rows * min(ROWB, 128);
+            if (copier) {
+                if (is_v)
+                    tma_load_3d(to, vm, half * 64, row, slab, full + ring.at);
+                else
+                    tma_load_3d(to, km, half * 64, row, slab, full + ring.at);
+            } else if (scales && page >= 0) {
+                bulk_load(smem_u32(b->scales[ring.at % kMaxRaws]) + box * rows,
+                          (is_v ? p.vs : p.ks) + (((size_t)page * p.Hk + w.at.head) << p.page_log) + row, rows, full + ring.at);
+            }
+            ring.step(UNITS), ring.step(UNITS);
+            if (ring.at == is_v) first_round = false;
+            // the second query tile behind the first keys: its place is free last
+            if (!is_v && j == w.at.part && !w.one && !queries(1)) return;
         }
     }
     // the last arrivals on the barriers that this warp waits on
-    for (int i = 0; i < C::QS; ++i)
-        if (!first_q || i < qs.at) wait_warp(b->q_empty + i, first_q ? 0 : i < qs.at ? qs.parity : qs.parity ^ 1, &b->abort, p.status);
-    for (int i = 0; i < UNITS; ++i)
+    if (!is_v)
+        for (int i = 0; i < C::QS; ++i)
+            if (!first_q || i < qs.at) wait_warp(b->q_empty + i, first_q ? 0 : i < qs.at ? qs.parity : qs.parity ^ 1, &b->abort, p.status);
+    for (int i = is_v; i < UNITS; i += 2)
         if (!first_round || i < ring.at) wait_warp(empty + i, first_round ? 0 : i < ring.at ? ring.parity : ring.parity ^ 1, &b->abort, p.status);
 }
 
@@ -259,8 +264,8 @@ template <class C>
 __device__ __forceinline__ void drain(Shared *b) {
     constexpr int UNITS = C::E4M3 ? C::RAWS : C::STAGES;
     uint64_t *const full = C::E4M3 ? b->raw_full : b->full;
-    const int begun = *const_cast<volatile uint32_t *>(&b->begun);
     for (int s = 0; s < UNITS; ++s) {
+        const int begun = 2 * *const_cast<volatile uint32_t *>(b->begun + (s & 1)) + (s & 1);  // past the warp's last place
         const int rounds = begun > s ? (begun - s + UNITS - 1) / UNITS : 0;
         if (rounds) mbar_wait(full + s, (rounds - 1) & 1);
     }
@@ -271,29 +276,54 @@ __device__ __forceinline__ void drain(Shared *b) {
 }
 
 // ---------------------------------------------------------------- conversion, and the end of a piece
-// A tile of codes into a bf16 tile, a thread a key; rows behind the last key become zeros.
+// A tile of codes into a bf16 tile, a thread a key; rows behind the last key become zeros.  A code's
+// bits moved to bf16's places are its value times 2^-120 (subnormal ones too), and products with powers of two
+// are exact: fewer and faster instructions than conversions by way of fp16 and fp32.
 template <class C>
 __device__ __forceinline__ void convert_tile(uint32_t from, uint32_t to, uint32_t byte, int row, bool live) {
-    const float up = pow2_of(byte);
+    // 2^(120 + byte - 127), in two factors where one is past bf16's range; NaN for a head that is not finite
+    const uint32_t e1 = min(byte + 120u, 254u), e2 = byte + 120u - e1 + 127u;
+    const uint32_t up1 = live ? (byte == 255 ? 0x7fc0u : e1 << 7) * 0x10001u : 0, up2 = (e2 << 7) * 0x10001u;
+    const bool twice = __any_sync(~0u, e2 != 127);
+    uint32_t x[C::D / 16][4];
 #pragma unroll
     for (int c = 0; c < C::D / 16; ++c) {
         const uint32_t at = C::D == 64 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4) : row * 128 + ((c ^ (row & 7)) << 4);
-        uint32_t x[4], o[8];
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(from + at) : "memory");
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[c][0]), "=r"(x[c][1]), "=r"(x[c][2]), "=r"(x[c][3]) : "r"(from + at) : "memory");
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t h;
-            float lo, hi;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(x[e >> 1] >> (16 * (e & 1)))));
-            asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(lo), "=f"(hi) : "r"(h));
-            o[e] = live ? pack_bf(lo * up, hi * up) : 0;
+    for (int piece = 0; piece < C::D / 8; ++piece) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t h = __byte_perm(x[piece >> 1][2 * (piece & 1) + (e >> 1)], 0, e & 1 ? 0x3424 : 0x1404);  // two codes, in the high bytes
+            const uint32_t bits = (h & 0x80008000u) | ((h >> 4) & 0x07f007f0u);
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[e]) : "r"(bits), "r"(up1));
         }
+        if (twice) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int piece = 2 * c + e;
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (piece >> 3) * C::HALF + row * 128 + (((piece ^ row) & 7) << 4)),
-                         "r"(o[4 * e]), "r"(o[4 * e + 1]), "r"(o[4 * e + 2]), "r"(o[4 * e + 3])
-                         : "memory");
+            for (int e = 0; e < 4; ++e) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[e]) : "r"(up2));
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (piece >> 3) * C::HALF + row * 128 + (((piece ^ row) & 7) << 4)),
+                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                     : "memory");
+    }
+}
+
+// Four lanes have four 16-byte pieces each, of a row of their own; after this lane q has piece q of each row:
+// what they store side by side is contiguous, a quarter of the lines to a store instruction.
+__device__ __forceinline__ void swap_pieces(uint32_t (&r)[4][4], int lane) {
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        const bool odd = lane & d;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & d) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t got = __shfl_xor_sync(~0u, odd ? r[k][e] : r[k | d][e], d);
+                if (odd) r[k][e] = got; else r[k | d][e] = got;
+            }
         }
     }
 }
@@ -329,7 +359,14 @@ __device__ __forceinline__ bool end_piece(const Params &p, const Walk &w, Shared
         const float f0 = v.x == -INFINITY ? 1.f : ex2(v.x - m), f1 = v1.x == -INFINITY ? 1.f : ex2(v1.x - m);
         const float l = v.y * f0 + v1.y * f1;
         const float s0 = whole ? f0 / l : f0, s1 = whole ? f1 / l : f1;
-        uint16_t *const y = p.y + ((long long)(w.q.y + token) * p.Hq + w.at.head * p.g + head_in) * D;
+        // y's rows of four lanes, and where this lane's 16 bytes of each go
+        const unsigned long long y = real ? reinterpret_cast<unsigned long long>(p.y + ((long long)(w.q.y + token) * p.Hq + w.at.head * p.g + head_in) * D) : 0;
+        uint16_t *to[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned long long at = __shfl_sync(~0u, y, (lane & ~3) + k);
+            to[k] = at ? reinterpret_cast<uint16_t *>(at) + (lane & 3) * 8 : nullptr;
+        }
         const int x = i * kTileRows + row;
         if (!whole && real) reinterpret_cast<float2 *>(part + (size_t)2 * kTileRows * D)[x] = make_float2(m, l);
 #pragma unroll 1
@@ -359,18 +396,15 @@ __device__ __forceinline__ bool end_piece(const Params &p, const Walk &w, Shared
                     if (places == 2) mbar_arrive(b->o_free + 1);
                 }
             }
-            if (!real) continue;
             if (whole) {
+                uint32_t r[4][4];
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint4 u;
-                    u.x = pack_bf(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
-                    u.y = pack_bf(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                    u.z = pack_bf(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
-                    u.w = pack_bf(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
-                    *reinterpret_cast<uint4 *>(y + c + e) = u;
-                }
-            } else {
+                for (int e = 0; e < 16; ++e) r[e >> 2][e & 3] = pack_bf(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                swap_pieces(r, lane);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (to[k]) *reinterpret_cast<uint4 *>(to[k] + c) = make_uint4(r[k][0], r[k][1], r[k][2], r[k][3]);
+            } else if (real) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<uint4 *>(part + (size_t)x * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -694,7 +728,7 @@ long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
             for (int i = 0; i < 2; ++i) mbar_init(b->s_full + i, 1), mbar_init(b->p_ready + i, 4), mbar_init(b->pv_done + i, 1);
             for (int i = 0; i < 2; ++i) mbar_init(b->o_full + i, 1), mbar_init(b->o_free + i, 4);
             mbar_init(&b->end, 1);
-            b->abort = b->begun = 0;
+            b->abort = b->begun[0] = b->begun[1] = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         __syncwarp();
@@ -710,7 +744,7 @@ long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
         } else if (warp < 12) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::ISSUE_REGS));
             if (warp == 8) ok = product_role<C>(p, v, sm, b);
-            if (warp == 9) copy_role<C>(p, v, &qm, &km, &vm, sm, b);
+            if (warp == 9 || warp == 10) copy_role<C>(p, v, &qm, &km, &vm, sm, b, warp - 9);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::HELP_REGS));
             help_role<C>(p, v, sm, b);

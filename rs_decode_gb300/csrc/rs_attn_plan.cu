@@ -22,9 +22,9 @@ struct PlanParams {
 };
 
 // Work of a long request's first i items on one key head; tq tokens an item of two query
-// tiles.  All of them but the request's last are full: they take two tile products for each of
-// ceil((ctx + (i + 1) tq) / 128) key tiles.  The sum of those is taken from the sum of the
-// numerators, less the remainders of 128, which repeat after 128 / gcd(tq, 128) items.
+// tiles.  All of them but the request's last are full: they see ceil((ctx + (i + 1) tq) / 128)
+// key tiles.  The sum of those is taken from the sum of the numerators, less the remainders
+// of 128, which repeat after 128 / gcd(tq, 128) items.
 __device__ __forceinline__ long long items_before(int ctx, int tq, int i) {
     const long long first = (long long)ctx + tq + kTileKeys - 1;
     const int low = tq & -tq, period = low >= kTileKeys ? 1 : kTileKeys / low;
@@ -40,12 +40,7 @@ __device__ __forceinline__ long long items_before(int ctx, int tq, int i) {
     long long rest = remainders(i % period);
     if (i >= period) rest += (i / period) * remainders(period);
     const long long sum = i * first + (long long)tq * ((long long)i * (i - 1) / 2);
-    return (sum - rest) / kTileKeys * 2 + (long long)i * kLongStart;
-}
-// The last item's, whose second query tile may have no rows.
-__device__ __forceinline__ int last_tiles(int n, int tq) {
-    const int rest = n - (n - 1) / tq * tq;
-    return rest > tq / 2 ? 2 : 1;
+    return (sum - rest) / kTileKeys + (long long)i * kLongStart;
 }
 
 __device__ __forceinline__ void scan3(long long &a, long long &b, long long &c, long long (*part)[32], long long *tot) {
@@ -111,8 +106,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const __grid_consta
         if (is_short) ws = (long long)p.Hk * ((ctx + n + kKeys - 1) / kKeys + kShortStart);
         if (is_long) {
             const int items = (n + tq - 1) / tq;
-            wl = p.Hk * (items_before(ctx, tq, items - 1) + kLongStart +
-                         (long long)last_tiles(n, tq) * ((ctx + n + kTileKeys - 1) / kTileKeys));
+            wl = p.Hk * (items_before(ctx, tq, items - 1) + kLongStart + (ctx + n + kTileKeys - 1) / kTileKeys);
         }
         long long tot[3];
         scan3(count, ws, wl, part, tot);
@@ -160,11 +154,9 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const __grid_consta
             }
             s.item = lo;
             const long long in = at - p.Hk * items_before(q.w, tq, lo);
-            const int tiles = lo == items - 1 ? last_tiles(q.z, tq) : 2;
-            const int keys = (q.w + min(q.z, (lo + 1) * tq) + kTileKeys - 1) / kTileKeys;
-            const int one = kLongStart + tiles * keys;
+            const int one = kLongStart + (q.w + min(q.z, (lo + 1) * tq) + kTileKeys - 1) / kTileKeys;
             s.head = (int)(in / one);
-            s.part = max(0, (int)(in % one) - kLongStart) / tiles;
+            s.part = max(0, (int)(in % one) - kLongStart);
         }
         (lng ? v.long_start : v.short_start)[c] = s;
     }

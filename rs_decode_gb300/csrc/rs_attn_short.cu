@@ -6,8 +6,8 @@
 // with c = scale log2(e).  Every key and value is read once for 16 or 32 rows, so HBM
 // bounds it: 2 D bytes of K and of V a key are 4 g D operations, a few tens a byte.
 //
-// A CTA an SM walks its share of the batch's blocks of 64 keys.  A producer warp
-// copies them by TMA into a ring (128-byte swizzle), as far ahead as shared memory
+// A CTA an SM walks its share of the batch's blocks of 64 keys.  Copying
+// warps bring them by TMA into a ring (128-byte swizzle), as far ahead as shared memory
 // allows: the copies of the next head or request are under way while the last one's
 // sums are joined.  Eight warps in two groups of four take the blocks in turns, a
 // warp 16 keys of a block, each for itself: its own running maximum, sum of
@@ -31,7 +31,8 @@ namespace attn {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32 + 32;
+constexpr int kCopiers = 4;  // warps
+constexpr int kThreads = (kWarps + kCopiers) * 32;
 constexpr int kPass = 32;        // channels joined at a time
 constexpr int kPitch = kPass + 8;  // floats between rows of the joining area: conflict-free pairs
 
@@ -42,6 +43,8 @@ struct Cfg {
     static constexpr int ROWB = D * (E4M3 ? 1 : 2);           // bytes of a key
     static constexpr int HALVES = ROWB > 128 ? 2 : 1;         // tiles of 128-byte rows side by side
     static constexpr int TILE = kKeys * ROWB;
+    // copying warps at work: halves of keys and of values, or keys, values and the scales of both
+    static constexpr int COPIERS = E4M3 ? 4 : 2 * HALVES;
     // whole rounds of both groups of warps: a stage always meets the same group, which
     // then waits on its barriers in every round
     static constexpr int STAGES = 2 * TILE >= 32768 ? 6 : 12;
@@ -49,7 +52,7 @@ struct Cfg {
     static constexpr int JOIN = SCALES + (E4M3 ? STAGES * 2 * kKeys : 0);
     static constexpr int ML = JOIN + kWarps * 16 * kPitch * 4;  // [kWarps][ROWS] (maximum, sum)
     static constexpr int BARS = ML + kWarps * ROWS * 8;
-    static constexpr int BYTES = BARS + 2 * STAGES * 8 + 16 + 1024;  // and room to align
+    static constexpr int BYTES = BARS + 2 * STAGES * 8 + 32 + 1024;  // and room to align
     static_assert(BYTES <= 227 * 1024, "");
 };
 
@@ -152,61 +155,58 @@ struct Walk {
 template <class C>
 __device__ __forceinline__ void produce(const Params &p, const PlanView &v, const CUtensorMap *km, const CUtensorMap *vm,
                                         uint32_t sm, uint64_t *full, uint64_t *empty, volatile uint32_t *abort) {
-    volatile uint32_t *const begun = abort + 1;  // blocks, for drain()
-    const int lane = threadIdx.x & 31;
-    const int rows = min(p.page, kKeys), boxes = kKeys / rows;  // of one copy; copies to a block's 64 keys
-    // lane -> one copy: box, half of the channels, keys or values; then (8 bits) a box's scales
-    const int copies = boxes * C::HALVES * 2;
-    const bool copies_scales = C::E4M3 && lane >= 16 && lane < 16 + 2 * boxes;
-    const bool is_v = lane & 1;
-    const int half = copies_scales ? 0 : (lane >> 1) % C::HALVES;
-    const int box = copies_scales ? (lane - 16) >> 1 : (lane >> 1) / C::HALVES;
-    const bool copier = lane < copies;
-    const uint8_t *const scales = is_v ? p.vs : p.ks;
+    const int lane = threadIdx.x & 31, role = (threadIdx.x >> 5) - kWarps;
+    if (role >= C::COPIERS) return;
+    volatile uint32_t *const begun = abort + 1 + role;  // blocks, for drain()
+    const int rows = min(p.page, kKeys), boxes = kKeys / rows;  // keys of one copy; copies to a block, a lane each
+    const bool scales = C::E4M3 && role >= 2, is_v = C::E4M3 ? role & 1 : role >= C::HALVES;
+    const int half = C::E4M3 ? 0 : role % C::HALVES;
     Ring ring;
     bool first_round = true;
+    PageWindow pages;
     Walk w;
     w.begin(p, v);
     for (; w.piece(); w.step()) {
-        auto page_at = [&](int b) {  // -1: past the request's keys, or no page
-            const int key = b * kKeys + box * rows;
-            return (copier || copies_scales) && b < w.last && key < w.keys ? page_of(p, w.q.x, key >> p.page_log) : -1;
-        };
-        int page = page_at(w.at.part), page1 = page_at(w.at.part + 1);
+        const int entries = min((w.keys + p.page - 1) >> p.page_log, p.max_pages);
         for (int b = w.at.part; b < w.last; ++b) {
-            const int page2 = page_at(b + 2);  // in flight while this block waits for its stage
+            const int key = b * kKeys + lane * rows;
+            pages.at(p, w.q.x, entries, (b * kKeys) >> p.page_log);
+            const bool mine = lane < boxes;
+            const int page = pages.page(p, key >> p.page_log, mine && key < w.keys);
             if (!first_round && !wait_warp(empty + ring.at, ring.parity ^ 1, abort, p.status)) return;
-            const int row = (b * kKeys + box * rows) & (p.page - 1);
-            const unsigned with_scales = __ballot_sync(~0u, copies_scales && page >= 0);
+            const int row = key & (p.page - 1);
+            const unsigned there = __ballot_sync(~0u, page >= 0);
             if (lane == 0) {
                 *begun += 1;
-                mbar_arrive_expect_tx(full + ring.at, 2 * C::TILE + __popc(with_scales) * rows);
+                mbar_arrive_expect_tx(full + ring.at, scales ? __popc(there) * rows : C::TILE / C::HALVES);
             }
             __syncwarp();
-            const uint32_t stage = sm + ring.at * 2 * C::TILE;
-            if (copier) {  // a coordinate past the cache fills in zeros
+            if (scales) {
+                if (page >= 0)
+                    bulk_load(sm + C::SCALES + (ring.at * 2 + is_v) * kKeys + lane * rows,
+                              (is_v ? p.vs : p.ks) + (((size_t)page * p.Hk + w.at.head) << p.page_log) + row, rows, full + ring.at);
+            } else if (mine) {  // a coordinate past the cache fills in zeros
                 const int slab = page >= 0 ? page * p.Hk + w.at.head : p.n_pages * p.Hk;
-                const uint32_t to = stage + half * (kKeys * 128) + box * rows * min(C::ROWB, 128);
+                const uint32_t to = sm + ring.at * 2 * C::TILE + half * (kKeys * 128) + lane * rows * min(C::ROWB, 128);
                 if (is_v)
                     tma_load_3d(to + C::TILE, vm, half * 64, row, slab, full + ring.at);
                 else
                     tma_load_3d(to, km, half * 64, row, slab, full + ring.at);
-            } else if (copies_scales && page >= 0) {
-                bulk_load(sm + C::SCALES + (ring.at * 2 + is_v) * kKeys + box * rows,
-                          scales + (((size_t)page * p.Hk + w.at.head) << p.page_log) + row, rows, full + ring.at);
             }
             ring.step(C::STAGES);
             if (ring.at == 0) first_round = false;
-            page = page1, page1 = page2;
         }
     }
 }
 
 // After giving up: wait (with a limit) for the copies still in flight.
 template <class C>
-__device__ __forceinline__ void drain(uint64_t *full, int begun) {
+__device__ __forceinline__ void drain(uint64_t *full, const volatile uint32_t *begun) {
+    // a block that only some of the warps began cannot complete: the limit ends that wait
+    int most = 0;
+    for (int i = 0; i < C::COPIERS; ++i) most = max(most, (int)begun[i]);
     for (int s = 0; s < C::STAGES; ++s) {
-        const int rounds = begun > s ? (begun - s + C::STAGES - 1) / C::STAGES : 0;
+        const int rounds = most > s ? (most - s + C::STAGES - 1) / C::STAGES : 0;
         if (rounds) mbar_wait(full + s, (rounds - 1) & 1);
     }
 }
@@ -592,8 +592,8 @@ short_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorM
                       v.head->Hq == p.Hq && v.head->Hk == p.Hk && v.head->R == p.R;
     if (threadIdx.x == 0) {
         if (!mine && blockIdx.x == 0) atomicOr(p.status, RS_DEV_LENGTH);
-        for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, 1), mbar_init(empty + i, kWarps / 2);
-        abort[0] = abort[1] = 0;
+        for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, C::COPIERS), mbar_init(empty + i, kWarps / 2);
+        for (int i = 0; i <= kCopiers; ++i) abort[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -605,7 +605,7 @@ short_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorM
     }
     // Every block that was copied has been waited for, but for a wait that gave up
     if (__syncthreads_or(*reinterpret_cast<volatile uint32_t *>(abort)) && threadIdx.x == 0)
-        drain<C>(full, (int)reinterpret_cast<volatile uint32_t *>(abort)[1]);
+        drain<C>(full, abort + 1);
     if (blockIdx.x == 0) wait_for_launch();  // this launch does not end before the one that it overlaps
 }
 
