@@ -80,22 +80,32 @@ __device__ __forceinline__ bool elect_one() {
 // one half of 64 columns to the next, where a tile is read MN-major.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
-// D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+// D[tmem] (+)= A[smem] B[smem], and A[tmem] below, by the lane of a converged warp that lead is set in.  The
+// operands are the same in all lanes and stay in uniform registers: in a branch that one lane takes,
+// moving them there took 45 clocks a product, and a tile's 16 of them longer than the products.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\tmov.b64 ad, {%1, %3};\n\tmov.b64 bd, {%2, %3};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 ad, bd;\n\tmov.b64 ad, {%1, %3};\n\tmov.b64 bd, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc), "r"(lead)
         : "memory");
 }
-// D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\tmov.b64 bd, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 bd;\n\tmov.b64 bd, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc), "r"(lead)
         : "memory");
 }
+__device__ __forceinline__ void commit(uint64_t *bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+// A value that is the same in all lanes, as a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(~0u, x); }
 
 #define RS_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
 #define RS_U8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
@@ -310,24 +320,6 @@ __device__ __forceinline__ void convert_tile(uint32_t from, uint32_t to, uint32_
     }
 }
 
-// Four lanes have four 16-byte pieces each, of a row of their own; after this lane q has piece q of each row:
-// what they store side by side is contiguous, a quarter of the lines to a store instruction.
-__device__ __forceinline__ void swap_pieces(uint32_t (&r)[4][4], int lane) {
-#pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-        const bool odd = lane & d;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (k & d) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t got = __shfl_xor_sync(~0u, odd ? r[k][e] : r[k | d][e], d);
-                if (odd) r[k][e] = got; else r[k | d][e] = got;
-            }
-        }
-    }
-}
-
 // The end of a piece, a thread a row: O out of TMEM, to y or to the workspace.  The next piece's
 // scores and weights go on meanwhile.
 template <class C>
@@ -359,14 +351,7 @@ __device__ __forceinline__ bool end_piece(const Params &p, const Walk &w, Shared
         const float f0 = v.x == -INFINITY ? 1.f : ex2(v.x - m), f1 = v1.x == -INFINITY ? 1.f : ex2(v1.x - m);
         const float l = v.y * f0 + v1.y * f1;
         const float s0 = whole ? f0 / l : f0, s1 = whole ? f1 / l : f1;
-        // y's rows of four lanes, and where this lane's 16 bytes of each go
-        const unsigned long long y = real ? reinterpret_cast<unsigned long long>(p.y + ((long long)(w.q.y + token) * p.Hq + w.at.head * p.g + head_in) * D) : 0;
-        uint16_t *to[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const unsigned long long at = __shfl_sync(~0u, y, (lane & ~3) + k);
-            to[k] = at ? reinterpret_cast<uint16_t *>(at) + (lane & 3) * 8 : nullptr;
-        }
+        uint16_t *const y = p.y + ((long long)(w.q.y + token) * p.Hq + w.at.head * p.g + head_in) * D;
         const int x = i * kTileRows + row;
         if (!whole && real) reinterpret_cast<float2 *>(part + (size_t)2 * kTileRows * D)[x] = make_float2(m, l);
 #pragma unroll 1
@@ -396,15 +381,18 @@ __device__ __forceinline__ bool end_piece(const Params &p, const Walk &w, Shared
                     if (places == 2) mbar_arrive(b->o_free + 1);
                 }
             }
+            if (!real) continue;
             if (whole) {
-                uint32_t r[4][4];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e >> 2][e & 3] = pack_bf(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-                swap_pieces(r, lane);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (to[k]) *reinterpret_cast<uint4 *>(to[k] + c) = make_uint4(r[k][0], r[k][1], r[k][2], r[k][3]);
-            } else if (real) {
+                for (int e = 0; e < 32; e += 8) {
+                    uint4 u;
+                    u.x = pack_bf(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+                    u.y = pack_bf(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                    u.z = pack_bf(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
+                    u.w = pack_bf(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
+                    *reinterpret_cast<uint4 *>(y + c + e) = u;
+                }
+            } else {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<uint4 *>(part + (size_t)x * D + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -465,7 +453,8 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
     constexpr int D = C::D;
     constexpr uint32_t kIdescS = umma_idesc_bf16(128, 128, false, false), kIdescO = umma_idesc_bf16(128, D, false, true);
     const int lane = threadIdx.x & 31;
-    const uint32_t tmem = b->tmem;
+    const uint32_t tmem = uniform(b->tmem), lead = elect_one();
+    const uint32_t q_desc = uniform(desc_lo(sm + C::Q, 16)), k_desc = uniform(desc_lo(sm + C::RING, 16)), v_desc = uniform(desc_lo(sm + C::RING, C::HALF));
     Ring ring, qs;
     unsigned p_parity = 0, o_parity = 0, o_used = 0;  // a bit for each place
     auto wait = [&](uint64_t *bar, unsigned parity) {
@@ -475,14 +464,13 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
     };
     // S_i = Q K^T
     auto scores = [&](int i, int q, int stage) {
-        if (elect_one()) {
-            const uint32_t a = desc_lo(sm + C::Q + q * C::TILE, 16), k = desc_lo(sm + C::RING + stage * C::TILE, 16);
+        const uint32_t a = q_desc + uniform(q) * (C::TILE >> 4), k = k_desc + uniform(stage) * (C::TILE >> 4), s = tmem + uniform(i) * 128;
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x)
-                mma_ss(tmem + i * 128, a + (x >> 2) * (C::HALF >> 4) + (x & 3) * 2, k + (x >> 2) * (C::HALF >> 4) + (x & 3) * 2, kIdescS, x > 0);
-            umma_commit(b->s_full + i);
+        for (int x = 0; x < D / 16; ++x) {
+            const uint32_t at = (x >> 2) * (C::HALF >> 4) + (x & 3) * 2;
+            mma_ss(s, a + at, k + at, kIdescS, x > 0, lead);
         }
-        __syncwarp();
+        commit(b->s_full + i, lead);
     };
     // O_i (+)= P_i V; first: of the piece, when the last one's O_i has to be out of its place
     auto values = [&](int i, int stage, bool first, bool last) {
@@ -495,21 +483,14 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
             }
             o_used |= 1u << i;
         }
-        if (elect_one()) {
-            const uint32_t vd = desc_lo(sm + C::RING + stage * C::TILE, C::HALF);
+        const uint32_t vd = v_desc + uniform(stage) * (C::TILE >> 4), o = tmem + 256 + uniform(i) * D, w = tmem + uniform(i) * 128;
 #pragma unroll
-            for (int x = 0; x < kTileKeys / 16; ++x)
-                mma_ts(tmem + 256 + i * D, tmem + i * 128 + x * 8, vd + x * 128, kIdescO, !first || x > 0);
-            umma_commit(b->pv_done + i);
-            if (last) umma_commit(b->o_full + i);
-        }
-        __syncwarp();
+        for (int x = 0; x < kTileKeys / 16; ++x) mma_ts(o, w + x * 8, vd + x * 128, kIdescO, !first || x > 0, lead);
+        commit(b->pv_done + i, lead);
+        if (last) commit(b->o_full + i, lead);
         return true;
     };
-    auto release = [&](uint64_t *bar) {
-        if (elect_one()) umma_commit(bar);
-        __syncwarp();
-    };
+    auto release = [&](uint64_t *bar) { commit(bar, lead); };
     // What lies in the tile behind the request's last key is not part of the cache: zeros
     // meet its zero weights.  (8-bit tiles are written so.)
     auto clear = [&](int stage, int from) {
@@ -750,8 +731,7 @@ long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
             help_role<C>(p, v, sm, b);
         }
         if (warp == 8 && !ok) {  // products still in flight; elect_one() names the lane that issued them
-            if (elect_one()) umma_commit(&b->end);
-            __syncwarp();
+            commit(&b->end, elect_one());
             mbar_wait(&b->end, 0);
         }
     }
