@@ -578,7 +578,7 @@ typedef struct {
 rs_status rs_attn_bytes_for(const rs_kv_desc *d, const rs_ragged_desc *rd, int32_t max_len, rs_attn_bytes *out);
 
 /* Shares out the attention of a planned batch, on the device; for every layer
- * with the same Hq, Hk, page and max_pages.  plan: device memory, 128-byte
+ * with the same Hq, Hk, type, page and max_pages.  plan: device memory, 128-byte
  * aligned, which rs_attend only reads.  A request with more than max_len rows,
  * or whose end passes max_pages * page, gets no attention (RS_DEV_LENGTH).
  * Source: none (library plumbing). */
@@ -602,7 +602,7 @@ typedef struct {
  * stream).  Scores, sums and their joining are fp32; the weights are rounded to
  * bf16 (fp16 for few rows on an 8-bit cache) before they meet the values, y
  * once.  Rows of requests without attention in the plan, and rows past the
- * batch, are left as they are.  plan: from rs_attn_plan for the same Hq, Hk, R
+ * batch, are left as they are.  plan: from rs_attn_plan for the same Hq, Hk, type, R
  * and max_len (RS_DEV_LENGTH otherwise, and y is left).  An entry of the page
  * table that is outside 0..n_pages-1 reads as zeros (RS_DEV_SLOT).
  * work: device scratch of rs_attn_bytes_for's bytes, 128-byte aligned; not

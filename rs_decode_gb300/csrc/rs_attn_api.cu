@@ -139,7 +139,7 @@ rs_status rs_attn_bytes_for(const rs_kv_desc *d, const rs_ragged_desc *rd, int32
     RS_TRY(check_kv_desc(d));
     RS_TRY(check_batch(d, rd));
     if (max_len < 1 || !o) return RS_ERR_INVALID_ARG;
-    const Form f = form_of(d->Hq / d->Hk, max_len);
+    const Form f = form_of(d->Hq / d->Hk, max_len, d->type == RS_KV_E4M3);
     o->plan = plan_bytes(rd->R, kCtas);
     o->work = (short_floats(*d, f) + long_floats(*d, f)) * 4;
     return RS_OK;
@@ -152,7 +152,7 @@ rs_status rs_attn_plan(const rs_kv_desc *d, const rs_ragged_desc *rd, const rs_r
     RS_TRY(check_rows(rg));
     if (max_len < 1 || !aligned(plan, 128) || !aligned(status, 4)) return RS_ERR_INVALID_ARG;
     return cuda_status(
-        plan_launch(*d, *rd, *rg, max_len, kCtas, form_of(d->Hq / d->Hk, max_len), plan, status, (cudaStream_t)stream));
+        plan_launch(*d, *rd, *rg, max_len, kCtas, form_of(d->Hq / d->Hk, max_len, d->type == RS_KV_E4M3), plan, status, (cudaStream_t)stream));
 }
 
 rs_status rs_attend(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *rd, const rs_ragged *rg, const rs_attn *in,
@@ -165,7 +165,7 @@ rs_status rs_attend(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *
     if (!stride_ok(in->ld_q, (int64_t)d->Hq * d->D)) return RS_ERR_INVALID_ARG;
     if (!aligned(plan, 128) || !aligned(y, 16) || !aligned(work, 128) || !aligned(status, 4)) return RS_ERR_INVALID_ARG;
     const int g = d->Hq / d->Hk;
-    const Form f = form_of(g, in->max_len);
+    const Form f = form_of(g, in->max_len, d->type == RS_KV_E4M3);
     Params p = {};
     p.Hq = d->Hq, p.Hk = d->Hk, p.g = g, p.page = d->page, p.page_log = ilog2(d->page);
     p.n_pages = d->n_pages, p.max_pages = d->max_pages, p.R = rd->R, p.cap = rd->tokens_cap;

@@ -455,27 +455,28 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
     const int lane = threadIdx.x & 31;
     const uint32_t tmem = uniform(b->tmem), lead = elect_one();
     const uint32_t q_desc = uniform(desc_lo(sm + C::Q, 16)), k_desc = uniform(desc_lo(sm + C::RING, 16)), v_desc = uniform(desc_lo(sm + C::RING, C::HALF));
+    constexpr uint32_t kStep = C::TILE >> 4;  // from place to place, in descriptors
     Ring ring, qs;
     unsigned p_parity = 0, o_parity = 0, o_used = 0;  // a bit for each place
+    // The products' pace is this warp's: what it waits for is mostly there, and operands are
+    // worked out before the waits.
     auto wait = [&](uint64_t *bar, unsigned parity) {
-        const bool ok = wait_warp(bar, parity, &b->abort, p.status);
+        bool ok = __all_sync(~0u, mbar_try_wait(bar, parity));
+        if (!ok) ok = wait_warp(bar, parity, &b->abort, p.status);
         tc_fence_after_sync();
         return ok;
     };
-    // S_i = Q K^T
-    auto scores = [&](int i, int q, int stage) {
-        const uint32_t a = q_desc + uniform(q) * (C::TILE >> 4), k = k_desc + uniform(stage) * (C::TILE >> 4), s = tmem + uniform(i) * 128;
+    // S_i = Q K^T; q, k: descriptors
+    auto scores = [&](int i, uint32_t q, uint32_t k) {
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
             const uint32_t at = (x >> 2) * (C::HALF >> 4) + (x & 3) * 2;
-            mma_ss(s, a + at, k + at, kIdescS, x > 0, lead);
+            mma_ss(tmem + i * 128, q + at, k + at, kIdescS, x > 0, lead);
         }
         commit(b->s_full + i, lead);
     };
     // O_i (+)= P_i V; first: of the piece, when the last one's O_i has to be out of its place
-    auto values = [&](int i, int stage, bool first, bool last) {
-        if (!wait(b->p_ready + i, p_parity >> i & 1)) return false;
-        p_parity ^= 1u << i;
+    auto values = [&](int i, uint32_t vd, bool first, bool last) {
         if (first) {
             if (o_used >> i & 1) {
                 if (!wait(b->o_free + i, o_parity >> i & 1)) return false;
@@ -483,9 +484,11 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
             }
             o_used |= 1u << i;
         }
-        const uint32_t vd = v_desc + uniform(stage) * (C::TILE >> 4), o = tmem + 256 + uniform(i) * D, w = tmem + uniform(i) * 128;
+        if (!wait(b->p_ready + i, p_parity >> i & 1)) return false;
+        p_parity ^= 1u << i;
+        mma_ts(tmem + 256 + i * D, tmem + i * 128, vd, kIdescO, !first, lead);
 #pragma unroll
-        for (int x = 0; x < kTileKeys / 16; ++x) mma_ts(o, w + x * 8, vd + x * 128, kIdescO, !first || x > 0, lead);
+        for (int x = 1; x < kTileKeys / 16; ++x) mma_ts(tmem + 256 + i * D, tmem + i * 128 + x * 8, vd + x * 128, kIdescO, true, lead);
         commit(b->pv_done + i, lead);
         if (last) commit(b->o_full + i, lead);
         return true;
@@ -509,6 +512,7 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
     w.begin(p, v);
     for (; w.piece(); w.step()) {
         const int q0 = qs.at;
+        const uint32_t q0_desc = q_desc + uniform(q0) * kStep;
         if (!wait(b->q_full + q0, qs.parity)) return false;
         qs.step(C::QS);
         if (w.one) {
@@ -516,28 +520,28 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
             // run beside the register work of the other
             int v0 = 0, v1 = 0;  // the places' values
             for (int j = w.at.part; j < w.last + 2; ++j) {
-                const int i = (j - w.at.part) & 1;
+                const int i = uniform((j - w.at.part) & 1), stage = i ? v1 : v0, k_stage = ring.at;
+                const uint32_t vd = v_desc + uniform(stage) * kStep, kd = k_desc + uniform(k_stage) * kStep;
                 if (j - 2 >= w.at.part) {
-                    const int stage = i ? v1 : v0;
-                    if (!values(i, stage, j - 2 < w.at.part + 2, j >= w.last)) return false;
+                    if (!values(i, vd, j - 2 < w.at.part + 2, j >= w.last)) return false;
                     release(b->empty + stage);
                 }
                 if (j >= w.last) continue;
-                const int k_stage = ring.at;
                 if (!wait(b->full + k_stage, ring.parity)) return false;
                 ring.step(C::STAGES);
-                scores(i, q0, k_stage);
+                scores(i, q0_desc, kd);
                 release(b->empty + k_stage);
                 if (j == w.last - 1) release(b->q_empty + q0);
-                const int stage = ring.at;
-                if (!wait(b->full + stage, ring.parity)) return false;
+                const int next = ring.at;
+                if (!wait(b->full + next, ring.parity)) return false;
                 ring.step(C::STAGES);
-                clear(stage, w.keys - j * kTileKeys);
-                if (i) v1 = stage; else v0 = stage;
+                clear(next, w.keys - j * kTileKeys);
+                if (i) v1 = next; else v0 = next;
             }
             continue;
         }
         const int q1 = qs.at;
+        const uint32_t q1_desc = q_desc + uniform(q1) * kStep;
         const unsigned q1_parity = qs.parity;
         qs.step(C::QS);
         int v_stage = 0;
@@ -546,22 +550,23 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
         for (int j = w.at.part; j <= w.last; ++j) {
             // K_j at the ring's place, V_j behind it; V_(j-1) at v_stage
             const int k_stage = ring.at;
+            const uint32_t kd = k_desc + uniform(k_stage) * kStep, vd = v_desc + uniform(v_stage) * kStep;
             if (j < w.last) {
                 if (!wait(b->full + k_stage, ring.parity)) return false;
                 ring.step(C::STAGES);
             }
-            if (j > w.at.part && j <= end0 && !values(0, v_stage, j - 1 == w.at.part, j == end0)) return false;
+            if (j > w.at.part && j <= end0 && !values(0, vd, j - 1 == w.at.part, j == end0)) return false;
             if (j < end0) {
-                scores(0, q0, k_stage);
+                scores(0, q0_desc, kd);
                 if (j == end0 - 1) release(b->q_empty + q0);
             }
             if (j > w.at.part) {
-                if (!values(1, v_stage, j - 1 == w.at.part, j == w.last)) return false;
+                if (!values(1, vd, j - 1 == w.at.part, j == w.last)) return false;
                 release(b->empty + v_stage);
             }
             if (j < w.last) {
                 if (j == w.at.part && !wait(b->q_full + q1, q1_parity)) return false;
-                scores(1, q1, k_stage);
+                scores(1, q1_desc, kd);
                 release(b->empty + k_stage);
                 if (j == w.last - 1) release(b->q_empty + q1);
                 v_stage = ring.at;

@@ -39,6 +39,11 @@ constexpr int kPitch = kPass + 8;  // floats between rows of the joining area: c
 template <int D_, bool E4M3_, int MT_>
 struct Cfg {
     static constexpr int D = D_, MT = MT_, ROWS = 16 * MT;
+    // 16 rows: two groups of four warps take the blocks in turns, a warp 16 keys.  32 rows: all eight
+    // take every block, two of them the same keys and half of the channels of their values each, since
+    // a warp's registers hold the sums of 16 rows (with those of both halves 700 bytes a thread
+    // spilled, and four drafts of 64 requests took 250 us).
+    static constexpr int GROUPS = 2 / MT, PARTS = MT, N = D / 8 / PARTS;  // N: a warp's tiles of eight channels
     static constexpr bool E4M3 = E4M3_;
     static constexpr int ROWB = D * (E4M3 ? 1 : 2);           // bytes of a key
     static constexpr int HALVES = ROWB > 128 ? 2 : 1;         // tiles of 128-byte rows side by side
@@ -87,6 +92,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
@@ -214,7 +224,7 @@ __device__ __forceinline__ void drain(uint64_t *full, const volatile uint32_t *b
 // ---------------------------------------------------------------- arithmetic
 template <class C>
 struct Sums {
-    float o[C::MT][C::D / 8][4];  // 16 rows x D, as the products leave them
+    float o[C::MT][C::N][4];  // 16 rows x (D or half of it), as the products leave them
     float m[C::MT][2], l[C::MT][2];
 };
 
@@ -273,8 +283,8 @@ __device__ __forceinline__ void load_queries(const Params &p, const int4 &rq, in
 template <class C>
 __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C::D / 16][4], const float (&cq)[C::MT][2],
                                         uint32_t k_tile, uint32_t v_tile, uint32_t scales, int slice, int key0, int keys,
-                                        int seen, const int (&limit)[C::MT][2]) {
-    constexpr int MT = C::MT, D = C::D;
+                                        int seen, const int (&limit)[C::MT][2], int part) {
+    constexpr int MT = C::MT, D = C::D, N = C::N;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float s[MT][2][4] = {};
     if constexpr (!C::E4M3) {
@@ -343,8 +353,8 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
                     if (key0 + nt * 8 + 2 * t + (e & 1) > limit[mt][e >> 1]) s[mt][nt][e] = -INFINITY;
         // What lies behind the last key is not part of the cache: as zeros it meets its zero weights
         if (!C::E4M3 && key0 + 16 > keys) {
-            for (int i = lane; i < (16 - max(keys - key0, 0)) * (D / 8); i += 32) {
-                const int r = slice + 15 - i / (D / 8), c = i % (D / 8);
+            for (int i = lane; i < (16 - max(keys - key0, 0)) * N; i += 32) {
+                const int r = slice + 15 - i / N, c = part * N + i % N;
                 asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(v_tile + piece<C>(r, c)), "r"(0) : "memory");
             }
             __syncwarp();
@@ -380,7 +390,7 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
                 a.m[mt][hf] = m;
                 a.l[mt][hf] *= f;
 #pragma unroll
-                for (int n = 0; n < D / 8; ++n) a.o[mt][n][2 * hf] *= f, a.o[mt][n][2 * hf + 1] *= f;
+                for (int n = 0; n < N; ++n) a.o[mt][n][2 * hf] *= f, a.o[mt][n][2 * hf + 1] *= f;
             }
     }
     uint32_t w[MT][4];
@@ -406,9 +416,9 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
     }
     if constexpr (!C::E4M3) {
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
+        for (int n = 0; n < N / 2; ++n) {
             uint32_t b[4];
-            ldmatrix4_trans(b, v_tile + piece<C>(slice + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * n + (lane >> 4)));
+            ldmatrix4_trans(b, v_tile + piece<C>(slice + ((lane >> 3) & 1) * 8 + (lane & 7), part * N + 2 * n + (lane >> 4)));
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 mma<false>(a.o[mt][2 * n], w[mt], b[0], b[1]);
@@ -416,24 +426,27 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
             }
         }
     } else {
-        // a lane's D / 8 channels from four keys: bytes of two keys side by side are one operand
-        uint32_t r[4][D / 32];
+        // a lane's N channels from four keys, of the D / 8 that begin at (D / 8) g: bytes of two keys side by side are one operand
+        uint32_t r[4][N / 4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int key = slice + 2 * t + (i & 1) + 8 * (i >> 1);
-            if constexpr (D == 128) {
-                const uint4 u = lds128(v_tile + piece<C>(key, g));
+            const int key = slice + 2 * t + (i & 1) + 8 * (i >> 1), at = g * (D / 8) + part * N;  // byte in the row
+            const uint32_t from = v_tile + piece<C>(key, at >> 4) + (at & 15);
+            if constexpr (N == 16) {
+                const uint4 u = lds128(from);
                 r[i][0] = u.x, r[i][1] = u.y, r[i][2] = u.z, r[i][3] = u.w;
-            } else {
-                const uint2 u = lds64(v_tile + piece<C>(key, g >> 1) + (g & 1) * 8);
+            } else if constexpr (N == 8) {
+                const uint2 u = lds64(from);
                 r[i][0] = u.x, r[i][1] = u.y;
+            } else {
+                r[i][0] = lds32(from);
             }
             if (masked && key0 + 2 * t + (i & 1) + 8 * (i >> 1) >= keys)
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e) r[i][e] = 0;
+                for (int e = 0; e < N / 4; ++e) r[i][e] = 0;
         }
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e)
+        for (int e = 0; e < N / 4; ++e)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t x = __byte_perm(r[0][e], r[1][e], h ? 0x7362 : 0x5140);
@@ -452,7 +465,7 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
 template <class C>
 __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &rq, int head, bool whole, int slot,
                                        unsigned char *smem) {
-    constexpr int MT = C::MT, D = C::D;
+    constexpr int MT = C::MT, D = C::D, SUMS = kWarps / C::PARTS;  // warps whose sums of a channel are joined
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float2 *const ml = reinterpret_cast<float2 *>(smem + C::ML);
     float *const area = reinterpret_cast<float *>(smem + C::JOIN);
@@ -463,11 +476,12 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
             float l = a.l[mt][hf];
             l += __shfl_xor_sync(~0u, l, 1);
             l += __shfl_xor_sync(~0u, l, 2);
-            if (t == 0) ml[warp * C::ROWS + mt * 16 + hf * 8 + g] = make_float2(a.m[mt][hf], l);
+            // two warps of the same keys have the same
+            if (t == 0 && warp < SUMS) ml[warp * C::ROWS + mt * 16 + hf * 8 + g] = make_float2(a.m[mt][hf], l);
         }
     consumers_sync();
     const int rows = rq.z * p.g;
-    float *const part = p.short_parts + (size_t)(2 * blockIdx.x + slot) * part_floats(C::ROWS, D);
+    float *const to_parts = p.short_parts + (size_t)(2 * blockIdx.x + slot) * part_floats(C::ROWS, D);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         // weights of this warp's two rows
@@ -476,7 +490,7 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
         for (int hf = 0; hf < 2; ++hf) {
             float m = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * C::ROWS + mt * 16 + hf * 8 + g].x);
+            for (int w = 0; w < SUMS; ++w) m = fmaxf(m, ml[w * C::ROWS + mt * 16 + hf * 8 + g].x);
             f[hf] = a.m[mt][hf] == -INFINITY ? 0.f : ex2(a.m[mt][hf] - m);
             if (C::E4M3) f[hf] *= 6.103515625e-5f;  // 2^-14
         }
@@ -484,9 +498,9 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
         const int row = threadIdx.x >> 4, col = (threadIdx.x & 15) * 2, x = mt * 16 + row;
         float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * C::ROWS + x].x);
+        for (int w = 0; w < SUMS; ++w) m = fmaxf(m, ml[w * C::ROWS + x].x);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < SUMS; ++w) {
             const float2 v = ml[w * C::ROWS + x];
             // a sum that is not a number stays one
             l += v.x == -INFINITY ? v.y : v.y * ex2(v.x - m);
@@ -494,9 +508,9 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
         const float inv = 1.f / l;
         const int token = x / p.g, in_group = x - token * p.g;
         uint16_t *const y = p.y + ((long long)(rq.y + token) * p.Hq + head * p.g + in_group) * D;
-        if (!whole && col == 0 && x < rows) reinterpret_cast<float2 *>(part + (size_t)C::ROWS * D)[x] = make_float2(m, l);
+        if (!whole && col == 0 && x < rows) reinterpret_cast<float2 *>(to_parts + (size_t)C::ROWS * D)[x] = make_float2(m, l);
 #pragma unroll
-        for (int c = 0; c < D / kPass; ++c) {
+        for (int c = 0; c < C::N / 4; ++c) {  // 32 channels of each part of the channels at a time
             float *const to = area + (warp * 16 + g) * kPitch;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
@@ -504,25 +518,28 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        // 8 bits: sums n of a lane are channels (D / 8) (2 t + k) + n
+                        // 8 bits: sums n of a lane are channels (D / 8) (2 t + k) + part N + n
                         const float2 v = C::E4M3 ? make_float2(a.o[mt][4 * c + 2 * i][2 * hf + k] * f[hf], a.o[mt][4 * c + 2 * i + 1][2 * hf + k] * f[hf])
                                                  : make_float2(a.o[mt][4 * c + 2 * i + k][2 * hf] * f[hf], a.o[mt][4 * c + 2 * i + k][2 * hf + 1] * f[hf]);
                         const int at = C::E4M3 ? (2 * t + k) * 4 + 2 * i : (2 * i + k) * 8 + 2 * t;
                         *reinterpret_cast<float2 *>(to + hf * 8 * kPitch + at) = v;
                     }
             consumers_sync();
-            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 v = *reinterpret_cast<const float2 *>(area + (w * 16 + row) * kPitch + col);
-                sum.x += v.x, sum.y += v.y;
-            }
-            const int d = C::E4M3 ? (D / 8) * (col >> 2) + 4 * c + (col & 3) : c * kPass + col;
-            if (x < rows) {
-                if (whole)
-                    *reinterpret_cast<uint32_t *>(y + d) = pack_bf(sum.x * inv, sum.y * inv);
-                else
-                    *reinterpret_cast<float2 *>(part + (size_t)x * D + d) = sum;
+            for (int part = 0; part < C::PARTS; ++part) {
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < SUMS; ++w) {
+                    const float2 v = *reinterpret_cast<const float2 *>(area + ((part * SUMS + w) * 16 + row) * kPitch + col);
+                    sum.x += v.x, sum.y += v.y;
+                }
+                const int d = C::E4M3 ? (D / 8) * (col >> 2) + part * C::N + 4 * c + (col & 3) : part * (D / C::PARTS) + c * kPass + col;
+                if (x < rows) {
+                    if (whole)
+                        *reinterpret_cast<uint32_t *>(y + d) = pack_bf(sum.x * inv, sum.y * inv);
+                    else
+                        *reinterpret_cast<float2 *>(to_parts + (size_t)x * D + d) = sum;
+                }
             }
             consumers_sync();
         }
@@ -533,7 +550,8 @@ template <class C>
 __device__ __forceinline__ void consume(const Params &p, const PlanView &v, unsigned char *smem, uint64_t *full, uint64_t *empty,
                                         volatile uint32_t *abort) {
     constexpr int MT = C::MT;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, slice = (warp & 3) * 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = C::GROUPS == 2 ? warp >> 2 : 0, slice = (warp & 3) * 16;
+    const int part = C::GROUPS == 2 ? 0 : warp >> 2;
     const uint32_t sm = smem_u32(smem);
     Ring ring;
     ring.at = group;
@@ -557,22 +575,23 @@ __device__ __forceinline__ void consume(const Params &p, const PlanView &v, unsi
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) a.m[mt][hf] = -INFINITY, a.l[mt][hf] = 0.f;
 #pragma unroll
-            for (int n = 0; n < C::D / 8; ++n)
+            for (int n = 0; n < C::N; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a.o[mt][n][e] = 0.f;
         }
-        for (int b = w.at.part; b < w.last; ++b, turn ^= 1) {
+        for (int b = w.at.part; b < w.last; ++b, turn ^= C::GROUPS - 1) {
             if (turn != group || !ok) continue;
             ok = wait_warp(full + ring.at, ring.parity, abort, p.status);
             const int key0 = b * kKeys + slice;
             if (ok && key0 < w.keys) {
                 const uint32_t stage = sm + ring.at * 2 * C::TILE;
-                compute<C>(a, q, cq, stage, stage + C::TILE, sm + C::SCALES + ring.at * 2 * kKeys, slice, key0, w.keys, w.q.w, limit);
+                compute<C>(a, q, cq, stage, stage + C::TILE, sm + C::SCALES + ring.at * 2 * kKeys, slice, key0, w.keys, w.q.w, limit, part);
                 if (!C::E4M3 && key0 + 16 > w.keys) fence_proxy_async_smem();  // zeros written before the next copy
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + ring.at);
-            ring.step(C::STAGES), ring.step(C::STAGES);
+            ring.step(C::STAGES);
+            if (C::GROUPS == 2) ring.step(C::STAGES);
         }
         if (named_sync_or(2, kWarps * 32, !ok)) return;
         finish<C>(p, a, w.q, w.at.head, w.at.part == 0 && w.last == w.blocks, w.at.part > 0 ? 0 : 1, smem);
@@ -592,16 +611,20 @@ short_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorM
                       v.head->Hq == p.Hq && v.head->Hk == p.Hk && v.head->R == p.R;
     if (threadIdx.x == 0) {
         if (!mine && blockIdx.x == 0) atomicOr(p.status, RS_DEV_LENGTH);
-        for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, C::COPIERS), mbar_init(empty + i, kWarps / 2);
+        for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, C::COPIERS), mbar_init(empty + i, kWarps / C::GROUPS);
         for (int i = 0; i <= kCopiers; ++i) abort[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
     if (mine) {
-        if (threadIdx.x >= kWarps * 32)
+        // registers of the launch's 168 a thread: the copying warps leave most of theirs to the others
+        if (threadIdx.x >= kWarps * 32) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
             produce<C>(p, v, &km, &vm, smem_u32(smem), full, empty, abort);
-        else
+        } else {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
             consume<C>(p, v, smem, full, empty, abort);
+        }
     }
     // Every block that was copied has been waited for, but for a wait that gave up
     if (__syncthreads_or(*reinterpret_cast<volatile uint32_t *>(abort)) && threadIdx.x == 0)
@@ -641,22 +664,30 @@ __device__ __forceinline__ void join_row(const float *parts, size_t stride, int 
             mine = v.y * f;
         }
         l += mine;
-        unsigned live = __ballot_sync(~0u, at != nullptr);
+        const unsigned live = __ballot_sync(~0u, at != nullptr);
         const unsigned long long addr = reinterpret_cast<unsigned long long>(at);
-        for (int k = 0; k < min(32, n - k0); ++k) {
-            const float fk = __shfl_sync(~0u, f, k);
-            const float *pk = reinterpret_cast<const float *>(__shfl_sync(~0u, addr, k));
-            if (!(live >> k & 1)) continue;
-            float v[V];
-            if constexpr (V == 4) {
-                const float4 u = *reinterpret_cast<const float4 *>(pk + (size_t)x * D + lane * 4);
-                v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-            } else {
-                const float2 u = *reinterpret_cast<const float2 *>(pk + (size_t)x * D + lane * 2);
-                v[0] = u.x, v[1] = u.y;
+        for (int k = 0; k < min(32, n - k0); k += 8) {
+            float v[8][V], fk[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {  // independent loads; a part that is none counts nothing
+                fk[u] = __shfl_sync(~0u, f, k + u);
+                const float *pk = reinterpret_cast<const float *>(__shfl_sync(~0u, addr, k + u));
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[u][i] = 0.f;
+                if (live >> (k + u) & 1) {
+                    if constexpr (V == 4) {
+                        const float4 y = *reinterpret_cast<const float4 *>(pk + (size_t)x * D + lane * 4);
+                        v[u][0] = y.x, v[u][1] = y.y, v[u][2] = y.z, v[u][3] = y.w;
+                    } else {
+                        const float2 y = *reinterpret_cast<const float2 *>(pk + (size_t)x * D + lane * 2);
+                        v[u][0] = y.x, v[u][1] = y.y;
+                    }
+                }
             }
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] = fmaf(fk, v[i], sum[i]);
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] = fmaf(fk[u], v[u][i], sum[i]);
         }
     }
 #pragma unroll
