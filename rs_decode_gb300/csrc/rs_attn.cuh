@@ -131,6 +131,36 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity, volati
     return __all_sync(~0u, wait_bar(bar, parity, abort, status));
 }
 
+// The same where what is waited for is mostly there: one look and a vote.  (The short form from an 8-bit
+// cache 272 against 290 us; the long form's 8-bit prompts are a tenth slower with it.)
+__device__ __forceinline__ bool wait_long(uint32_t bar, unsigned parity, volatile uint32_t *abort, uint32_t *status) {
+    unsigned long long t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 256; ++i) {
+            unsigned ok;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
+            if (__all_sync(~0u, ok)) return true;
+        }
+        if (__any_sync(~0u, *abort != 0)) return false;
+        const unsigned long long t = global_ns();
+        if (!t0) t0 = t;
+        if (__any_sync(~0u, t - t0 > kWaitLimitNs)) {
+            *abort = 1;
+            atomicOr(status, RS_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_ready(uint64_t *bar, unsigned parity, volatile uint32_t *abort, uint32_t *status) {
+    if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+    return wait_long(smem_u32(bar), parity, abort, status);
+}
+
 // A position in a ring of n barriers, with the parity of its current round.
 struct Ring {
     int at = 0;

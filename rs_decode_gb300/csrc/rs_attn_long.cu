@@ -54,7 +54,7 @@ struct Cfg {
     static constexpr int BYTES = SMALL + TILES;
     static_assert(BYTES <= 227 * 1024, "");
     // Registers a thread by role, out of the launch's 128 each
-    static constexpr int ROW_REGS = 184, ISSUE_REGS = 56, HELP_REGS = 88;
+    static constexpr int ROW_REGS = 176, ISSUE_REGS = 56, HELP_REGS = 104;
     static_assert(256 * ROW_REGS + 128 * ISSUE_REGS + 128 * HELP_REGS <= kThreads * 128, "");
 };
 
@@ -458,11 +458,9 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
     constexpr uint32_t kStep = C::TILE >> 4;  // from place to place, in descriptors
     Ring ring, qs;
     unsigned p_parity = 0, o_parity = 0, o_used = 0;  // a bit for each place
-    // The products' pace is this warp's: what it waits for is mostly there, and operands are
-    // worked out before the waits.
+    // The products' pace is this warp's: operands are worked out before the waits.
     auto wait = [&](uint64_t *bar, unsigned parity) {
-        bool ok = __all_sync(~0u, mbar_try_wait(bar, parity));
-        if (!ok) ok = wait_warp(bar, parity, &b->abort, p.status);
+        const bool ok = wait_warp(bar, parity, &b->abort, p.status);
         tc_fence_after_sync();
         return ok;
     };

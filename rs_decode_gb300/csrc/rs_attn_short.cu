@@ -183,7 +183,7 @@ __device__ __forceinline__ void produce(const Params &p, const PlanView &v, cons
             pages.at(p, w.q.x, entries, (b * kKeys) >> p.page_log);
             const bool mine = lane < boxes;
             const int page = pages.page(p, key >> p.page_log, mine && key < w.keys);
-            if (!first_round && !wait_warp(empty + ring.at, ring.parity ^ 1, abort, p.status)) return;
+            if (!first_round && !wait_ready(empty + ring.at, ring.parity ^ 1, abort, p.status)) return;
             const int row = key & (p.page - 1);
             const unsigned there = __ballot_sync(~0u, page >= 0);
             if (lane == 0) {
@@ -581,7 +581,7 @@ __device__ __forceinline__ void consume(const Params &p, const PlanView &v, unsi
         }
         for (int b = w.at.part; b < w.last; ++b, turn ^= C::GROUPS - 1) {
             if (turn != group || !ok) continue;
-            ok = wait_warp(full + ring.at, ring.parity, abort, p.status);
+            ok = wait_ready(full + ring.at, ring.parity, abort, p.status);
             const int key0 = b * kKeys + slice;
             if (ok && key0 < w.keys) {
                 const uint32_t stage = sm + ring.at * 2 * C::TILE;
