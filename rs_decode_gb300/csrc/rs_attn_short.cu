@@ -39,18 +39,20 @@ constexpr int kPitch = kPass + 8;  // floats between rows of the joining area: c
 template <int D_, bool E4M3_, int MT_>
 struct Cfg {
     static constexpr int D = D_, MT = MT_, ROWS = 16 * MT;
-    // 16 rows: two groups of four warps take the blocks in turns, a warp 16 keys.  32 rows: all eight
-    // take every block, two of them the same keys and half of the channels of their values each, since
-    // a warp's registers hold the sums of 16 rows (with those of both halves 700 bytes a thread
-    // spilled, and four drafts of 64 requests took 250 us).
-    static constexpr int GROUPS = 2 / MT, PARTS = MT, N = D / 8 / PARTS;  // N: a warp's tiles of eight channels
+    // A warp takes 16 keys of a block, or 32, where its chain of products, maximum and exponentials
+    // would be longer than the block's time: with 8 bits and with 32 rows.  With 32 rows two warps take
+    // the same keys and half of the channels of their values each, since a warp's registers hold the
+    // sums of 16 rows.  As many warps as a block needs are a group; groups take the blocks in turns.
+    static constexpr int NT = E4M3_ || MT == 2 ? 4 : 2;   // tiles of eight keys of a warp
+    static constexpr int SLICES = kKeys / (8 * NT), PARTS = MT, GROUPS = kWarps / (SLICES * PARTS);
+    static constexpr int N = D / 8 / PARTS;               // tiles of eight channels of a warp
     static constexpr bool E4M3 = E4M3_;
     static constexpr int ROWB = D * (E4M3 ? 1 : 2);           // bytes of a key
     static constexpr int HALVES = ROWB > 128 ? 2 : 1;         // tiles of 128-byte rows side by side
     static constexpr int TILE = kKeys * ROWB;
     // copying warps at work: halves of keys and of values, or keys, values and the scales of both
     static constexpr int COPIERS = E4M3 ? 4 : 2 * HALVES;
-    // whole rounds of both groups of warps: a stage always meets the same group, which
+    // whole rounds of all groups of warps: a stage always meets the same group, which
     // then waits on its barriers in every round
     static constexpr int STAGES = 2 * TILE >= 32768 ? 6 : 12;
     static constexpr int SCALES = STAGES * 2 * TILE;          // [STAGES][2][kKeys]
@@ -58,7 +60,7 @@ struct Cfg {
     static constexpr int ML = JOIN + kWarps * 16 * kPitch * 4;  // [kWarps][ROWS] (maximum, sum)
     static constexpr int BARS = ML + kWarps * ROWS * 8;
     static constexpr int BYTES = BARS + 2 * STAGES * 8 + 32 + 1024;  // and room to align
-    static_assert(BYTES <= 227 * 1024, "");
+    static_assert(BYTES <= 227 * 1024 && STAGES % GROUPS == 0, "");
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -99,9 +101,9 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
@@ -126,6 +128,21 @@ template <class C>
 __device__ __forceinline__ uint32_t piece(int r, int c) {
     if constexpr (C::ROWB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
     return (c >> 3) * (kKeys * 128) + r * 128 + (((c ^ r) & 7) << 4);
+}
+
+// Where a lane finds the keys (and the values) of its warp's slice of 16 in a tile.  Pieces further
+// along a row, and rows further down, are exclusive-ors and sums of constants away, see compute().
+template <class C>
+__device__ __forceinline__ uint32_t key_place(int slice) {
+    const int lane = threadIdx.x & 31;
+    return C::E4M3 ? piece<C>(slice + (lane >> 2), lane & 3) : piece<C>(slice + (lane & 7), lane >> 3);
+}
+template <class C>
+__device__ __forceinline__ uint32_t value_place(int slice, int part) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (!C::E4M3) return piece<C>(slice + (lane & 15), part * C::N + (lane >> 4));
+    const int at = (lane >> 2) * (C::D / 8) + part * C::N;  // byte in the row
+    return piece<C>(slice + 2 * (lane & 3), at >> 4) + (at & 15);
 }
 
 // A CTA's walk over its share: piece after piece.
@@ -278,25 +295,25 @@ __device__ __forceinline__ void load_queries(const Params &p, const int4 &rq, in
         }
 }
 
-// One warp's 16 keys of a staged block.  key0: position of the first; limit: the
+// One warp's 8 NT keys of a staged block.  key0: position of the first; limit: the
 // last key that each of the lane's rows sees.
 template <class C>
 __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C::D / 16][4], const float (&cq)[C::MT][2],
-                                        uint32_t k_tile, uint32_t v_tile, uint32_t scales, int slice, int key0, int keys,
+                                        uint32_t k_at, uint32_t v_at, uint32_t v_tile, uint32_t scales, int slice, int key0, int keys,
                                         int seen, const int (&limit)[C::MT][2], int part) {
-    constexpr int MT = C::MT, D = C::D, N = C::N;
+    constexpr int MT = C::MT, D = C::D, N = C::N, NT = C::NT;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float s[MT][2][4] = {};
+    float s[MT][NT][4] = {};
     if constexpr (!C::E4M3) {
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk) {
-            uint32_t b[2][4];
+            uint32_t b[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) ldmatrix4(b[nt], k_tile + piece<C>(slice + nt * 8 + (lane & 7), 4 * kk + (lane >> 3)));
+            for (int nt = 0; nt < NT; ++nt) ldmatrix4(b[nt], (k_at ^ (kk & 1) << 6) + (kk >> 1) * (kKeys * 128) + nt * 1024);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+                for (int nt = 0; nt < NT; ++nt) {
                     mma<false>(s[mt][nt], q[mt][2 * kk], b[nt][0], b[nt][1]);
                     mma<false>(s[mt][nt], q[mt][2 * kk + 1], b[nt][2], b[nt][3]);
                 }
@@ -304,13 +321,13 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
     } else {
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-            uint4 b[2];
+            uint4 b[NT];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) b[nt] = lds128(k_tile + piece<C>(slice + nt * 8 + g, t + 4 * h));
+            for (int nt = 0; nt < NT; ++nt) b[nt] = lds128((k_at ^ h << 6) + nt * 8 * C::ROWB);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+                for (int nt = 0; nt < NT; ++nt) {
                     const uint32_t w = k == 0 ? b[nt].x : k == 1 ? b[nt].y : k == 2 ? b[nt].z : b[nt].w;
                     const uint32_t b0 = two_halves(w), b1 = two_halves(w >> 16);
 #pragma unroll
@@ -319,42 +336,43 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
         }
     }
     // scores in units of log2; with 8 bits ev is the power of two of each key's values
-    float ev[2][2];
+    float ev[NT][2];
     if constexpr (C::E4M3) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t kb = lds_u16(scales + slice + nt * 8 + 2 * t), vb = lds_u16(scales + kKeys + slice + nt * 8 + 2 * t);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float up = pow2_of(lds_u8(scales + slice + nt * 8 + 2 * t + e));
-                const uint32_t vb = lds_u8(scales + kKeys + slice + nt * 8 + 2 * t + e);
-                ev[nt][e] = (float)((int)vb - 127);
+                const float up = __uint_as_float(e ? (kb & 0xff00u) << 15 : (kb & 0xffu) << 23);
+                ev[nt][e] = (float)(e ? vb >> 8 : vb & 0xffu) - 127.f;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     s[mt][nt][e] *= up * cq[mt][0];
                     s[mt][nt][2 + e] *= up * cq[mt][1];
                 }
             }
+        }
     } else {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[mt][nt][e] *= cq[mt][e >> 1];
     }
-    const bool masked = key0 + 15 > seen;  // some row does not see all 16
+    const bool masked = key0 + 8 * NT - 1 > seen;  // some row does not see all of them
     if (masked) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (key0 + nt * 8 + 2 * t + (e & 1) > limit[mt][e >> 1]) s[mt][nt][e] = -INFINITY;
         // What lies behind the last key is not part of the cache: as zeros it meets its zero weights
-        if (!C::E4M3 && key0 + 16 > keys) {
-            for (int i = lane; i < (16 - max(keys - key0, 0)) * N; i += 32) {
-                const int r = slice + 15 - i / N, c = part * N + i % N;
+        if (!C::E4M3 && key0 + 8 * NT > keys) {
+            for (int i = lane; i < (8 * NT - max(keys - key0, 0)) * N; i += 32) {
+                const int r = slice + 8 * NT - 1 - i / N, c = part * N + i % N;
                 asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(v_tile + piece<C>(r, c)), "r"(0) : "memory");
             }
             __syncwarp();
@@ -368,13 +386,11 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-            float x;
-            if constexpr (C::E4M3) {
-                x = fmaxf(fmaxf(s[mt][0][2 * hf] + ev[0][0], s[mt][0][2 * hf + 1] + ev[0][1]),
-                          fmaxf(s[mt][1][2 * hf] + ev[1][0], s[mt][1][2 * hf + 1] + ev[1][1]));
-            } else {
-                x = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]), fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
-            }
+            float x = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                x = C::E4M3 ? fmaxf(x, fmaxf(s[mt][nt][2 * hf] + ev[nt][0], s[mt][nt][2 * hf + 1] + ev[nt][1]))
+                            : fmaxf(x, fmaxf(s[mt][nt][2 * hf], s[mt][nt][2 * hf + 1]));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
             top[mt][hf] = x;
@@ -393,12 +409,12 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
                 for (int n = 0; n < N; ++n) a.o[mt][n][2 * hf] *= f, a.o[mt][n][2 * hf + 1] *= f;
             }
     }
-    uint32_t w[MT][4];
+    uint32_t w[NT / 2][MT][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        float x[2][4];
+        float x[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 // a row that has seen no key yet has no weights
@@ -409,20 +425,24 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
                 if constexpr (C::E4M3) x[nt][e] = ex2(below + (ev[nt][e & 1] + 14.f));
             }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // rows g and g + 8 of the first eight keys, then of the others
-            const float lo = x[i >> 1][2 * (i & 1)], hi = x[i >> 1][2 * (i & 1) + 1];
-            w[mt][i] = C::E4M3 ? pack_h(lo, hi) : pack_bf(lo, hi);
-        }
+        for (int kk = 0; kk < NT / 2; ++kk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // rows g and g + 8 of the first eight keys, then of the others
+                const float lo = x[2 * kk + (i >> 1)][2 * (i & 1)], hi = x[2 * kk + (i >> 1)][2 * (i & 1) + 1];
+                w[kk][mt][i] = C::E4M3 ? pack_h(lo, hi) : pack_bf(lo, hi);
+            }
     }
+#pragma unroll
+    for (int kk = 0; kk < NT / 2; ++kk)
     if constexpr (!C::E4M3) {
 #pragma unroll
         for (int n = 0; n < N / 2; ++n) {
             uint32_t b[4];
-            ldmatrix4_trans(b, v_tile + piece<C>(slice + ((lane >> 3) & 1) * 8 + (lane & 7), part * N + 2 * n + (lane >> 4)));
+            ldmatrix4_trans(b, (v_at ^ (n & 3) << 5) + (n >> 2) * (kKeys * 128) + kk * 2048);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                mma<false>(a.o[mt][2 * n], w[mt], b[0], b[1]);
-                mma<false>(a.o[mt][2 * n + 1], w[mt], b[2], b[3]);
+                mma<false>(a.o[mt][2 * n], w[kk][mt], b[0], b[1]);
+                mma<false>(a.o[mt][2 * n + 1], w[kk][mt], b[2], b[3]);
             }
         }
     } else {
@@ -430,8 +450,7 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
         uint32_t r[4][N / 4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int key = slice + 2 * t + (i & 1) + 8 * (i >> 1), at = g * (D / 8) + part * N;  // byte in the row
-            const uint32_t from = v_tile + piece<C>(key, at >> 4) + (at & 15);
+            const uint32_t from = (D == 128 ? (v_at + (i & 1) * 128) ^ (i & 1) << 4 : v_at + (i & 1) * 64) + ((i >> 1) + 2 * kk) * 8 * C::ROWB;
             if constexpr (N == 16) {
                 const uint4 u = lds128(from);
                 r[i][0] = u.x, r[i][1] = u.y, r[i][2] = u.z, r[i][3] = u.w;
@@ -441,7 +460,7 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
             } else {
                 r[i][0] = lds32(from);
             }
-            if (masked && key0 + 2 * t + (i & 1) + 8 * (i >> 1) >= keys)
+            if (masked && key0 + 16 * kk + 2 * t + (i & 1) + 8 * (i >> 1) >= keys)
 #pragma unroll
                 for (int e = 0; e < N / 4; ++e) r[i][e] = 0;
         }
@@ -454,8 +473,8 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
                 const uint32_t x0 = two_halves(x), x1 = two_halves(x >> 16), y0 = two_halves(y), y1 = two_halves(y >> 16);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    mma<true>(a.o[mt][4 * e + 2 * h], w[mt], x0, y0);
-                    mma<true>(a.o[mt][4 * e + 2 * h + 1], w[mt], x1, y1);
+                    mma<true>(a.o[mt][4 * e + 2 * h], w[kk][mt], x0, y0);
+                    mma<true>(a.o[mt][4 * e + 2 * h + 1], w[kk][mt], x1, y1);
                 }
             }
     }
@@ -463,10 +482,10 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
 
 // The eight warps' sums of a piece, joined; whole heads go to y, parts to the workspace.
 template <class C>
-__device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &rq, int head, bool whole, int slot,
+__device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &rq, int head, bool whole, int slot, int place,
                                        unsigned char *smem) {
     constexpr int MT = C::MT, D = C::D, SUMS = kWarps / C::PARTS;  // warps whose sums of a channel are joined
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float2 *const ml = reinterpret_cast<float2 *>(smem + C::ML);
     float *const area = reinterpret_cast<float *>(smem + C::JOIN);
 #pragma unroll
@@ -477,7 +496,7 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
             l += __shfl_xor_sync(~0u, l, 1);
             l += __shfl_xor_sync(~0u, l, 2);
             // two warps of the same keys have the same
-            if (t == 0 && warp < SUMS) ml[warp * C::ROWS + mt * 16 + hf * 8 + g] = make_float2(a.m[mt][hf], l);
+            if (t == 0 && place < SUMS) ml[place * C::ROWS + mt * 16 + hf * 8 + g] = make_float2(a.m[mt][hf], l);
         }
     consumers_sync();
     const int rows = rq.z * p.g;
@@ -511,7 +530,7 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
         if (!whole && col == 0 && x < rows) reinterpret_cast<float2 *>(to_parts + (size_t)C::ROWS * D)[x] = make_float2(m, l);
 #pragma unroll
         for (int c = 0; c < C::N / 4; ++c) {  // 32 channels of each part of the channels at a time
-            float *const to = area + (warp * 16 + g) * kPitch;
+            float *const to = area + (place * 16 + g) * kPitch;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
@@ -550,9 +569,11 @@ template <class C>
 __device__ __forceinline__ void consume(const Params &p, const PlanView &v, unsigned char *smem, uint64_t *full, uint64_t *empty,
                                         volatile uint32_t *abort) {
     constexpr int MT = C::MT;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = C::GROUPS == 2 ? warp >> 2 : 0, slice = (warp & 3) * 16;
-    const int part = C::GROUPS == 2 ? 0 : warp >> 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = warp / (C::SLICES * C::PARTS), part = warp / C::SLICES % C::PARTS, slice = warp % C::SLICES * (8 * C::NT);
+    const int place = part * (kWarps / C::PARTS) + group * C::SLICES + warp % C::SLICES;  // among the sums to be joined
     const uint32_t sm = smem_u32(smem);
+    const uint32_t k_at = sm + key_place<C>(slice), v_at = sm + C::TILE + value_place<C>(slice, part);
     Ring ring;
     ring.at = group;
     bool ok = true;
@@ -579,22 +600,22 @@ __device__ __forceinline__ void consume(const Params &p, const PlanView &v, unsi
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a.o[mt][n][e] = 0.f;
         }
-        for (int b = w.at.part; b < w.last; ++b, turn ^= C::GROUPS - 1) {
+        for (int b = w.at.part; b < w.last; ++b, turn = (turn + 1) % C::GROUPS) {
             if (turn != group || !ok) continue;
             ok = wait_ready(full + ring.at, ring.parity, abort, p.status);
             const int key0 = b * kKeys + slice;
             if (ok && key0 < w.keys) {
-                const uint32_t stage = sm + ring.at * 2 * C::TILE;
-                compute<C>(a, q, cq, stage, stage + C::TILE, sm + C::SCALES + ring.at * 2 * kKeys, slice, key0, w.keys, w.q.w, limit, part);
-                if (!C::E4M3 && key0 + 16 > w.keys) fence_proxy_async_smem();  // zeros written before the next copy
+                const uint32_t stage = ring.at * 2 * C::TILE;
+                compute<C>(a, q, cq, k_at + stage, v_at + stage, sm + stage + C::TILE, sm + C::SCALES + ring.at * 2 * kKeys, slice, key0, w.keys, w.q.w, limit, part);
+                if (!C::E4M3 && key0 + 8 * C::NT > w.keys) fence_proxy_async_smem();  // zeros written before the next copy
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + ring.at);
-            ring.step(C::STAGES);
-            if (C::GROUPS == 2) ring.step(C::STAGES);
+#pragma unroll
+            for (int i = 0; i < C::GROUPS; ++i) ring.step(C::STAGES);
         }
         if (named_sync_or(2, kWarps * 32, !ok)) return;
-        finish<C>(p, a, w.q, w.at.head, w.at.part == 0 && w.last == w.blocks, w.at.part > 0 ? 0 : 1, smem);
+        finish<C>(p, a, w.q, w.at.head, w.at.part == 0 && w.last == w.blocks, w.at.part > 0 ? 0 : 1, place, smem);
     }
 }
 
@@ -633,54 +654,59 @@ short_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorM
 }
 
 // ---------------------------------------------------------------- parts of a head
-// Row x of a head that the CTAs from c - 1 on shared: a warp's work, D / 32 channels a lane.
-// part_of(cta, slot): its sums.  Parts come in the order of the keys.
+// The parts of a head that several CTAs shared, in the order of its keys, a lane each (32 at a time): the
+// first is the end of CTA c - 1's share, the others begin the shares c, c + 1 ..
+struct Parts {
+    const float *base;
+    size_t stride;
+    int c, n;
+    const Start *start;
+    __device__ __forceinline__ const float *at(int k) const {
+        if (k >= n) return nullptr;
+        if (k == 0) return base + (size_t)(2 * (c - 1) + 1) * stride;
+        const Start a = start[c + k - 1], b = start[c + k];
+        const bool none = a.idx == b.idx && a.item == b.item && a.head == b.head && a.part == b.part;  // an empty share
+        return none ? nullptr : base + (size_t)(2 * (c + k - 1)) * stride;
+    }
+};
+
+// Row x of such a head, a warp's work, D / 32 channels a lane.  mine: the lane's of the first 32 parts.
 template <int D>
-__device__ __forceinline__ void join_row(const float *parts, size_t stride, int rows, int c, int n, const Start *start, int x,
-                                         uint16_t *y) {
+__device__ __forceinline__ void join_row(const Parts &parts, const float *mine, int rows, int x, uint16_t *y) {
     constexpr int V = D / 32;
     const int lane = threadIdx.x & 31;
-    auto part_at = [&](int k) -> const float * {  // part k: the first is the end of CTA c - 1's share
-        if (k == 0) return parts + (size_t)(2 * (c - 1) + 1) * stride;
-        const Start a = start[c + k - 1], b = start[c + k];
-        const bool none = a.idx == b.idx && a.item == b.item && a.head == b.head && a.part == b.part;
-        return none ? nullptr : parts + (size_t)(2 * (c + k - 1)) * stride;
-    };
-    float m = -INFINITY;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-        const float *at = k0 + lane < n ? part_at(k0 + lane) : nullptr;
-        float x_m = at ? at[(size_t)rows * D + 2 * x] : -INFINITY;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x_m = fmaxf(x_m, __shfl_xor_sync(~0u, x_m, o));
-        m = fmaxf(m, x_m);
+    float2 ml = mine ? reinterpret_cast<const float2 *>(mine + (size_t)rows * D)[x] : make_float2(-INFINITY, 0.f);
+    float m = ml.x;
+    for (int k0 = 32; k0 < parts.n; k0 += 32) {
+        const float *at = parts.at(k0 + lane);
+        if (at) m = fmaxf(m, at[(size_t)rows * D + 2 * x]);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     float l = 0.f, sum[V] = {};
-    for (int k0 = 0; k0 < n; k0 += 32) {
-        const float *at = k0 + lane < n ? part_at(k0 + lane) : nullptr;
-        float f = 0.f, mine = 0.f;
-        if (at) {
-            const float2 v = reinterpret_cast<const float2 *>(at + (size_t)rows * D)[x];
-            f = v.x == -INFINITY ? 1.f : ex2(v.x - m);  // a part without keys that the row sees has sums of zero
-            mine = v.y * f;
-        }
-        l += mine;
+    for (int k0 = 0; k0 < parts.n; k0 += 32) {
+        const float *at = k0 ? parts.at(k0 + lane) : mine;
+        if (k0) ml = at ? reinterpret_cast<const float2 *>(at + (size_t)rows * D)[x] : make_float2(-INFINITY, 0.f);
+        // a part without keys that the row sees has sums of zero
+        const float f = !at ? 0.f : ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+        if (at) l += ml.y * f;
         const unsigned live = __ballot_sync(~0u, at != nullptr);
         const unsigned long long addr = reinterpret_cast<unsigned long long>(at);
-        for (int k = 0; k < min(32, n - k0); k += 8) {
+        for (int k = 0; k < min(32, parts.n - k0); k += 8) {
             float v[8][V], fk[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {  // independent loads; a part that is none counts nothing
+            for (int u = 0; u < 8; ++u) {  // independent loads
                 fk[u] = __shfl_sync(~0u, f, k + u);
                 const float *pk = reinterpret_cast<const float *>(__shfl_sync(~0u, addr, k + u));
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[u][i] = 0.f;
                 if (live >> (k + u) & 1) {
                     if constexpr (V == 4) {
-                        const float4 y = *reinterpret_cast<const float4 *>(pk + (size_t)x * D + lane * 4);
-                        v[u][0] = y.x, v[u][1] = y.y, v[u][2] = y.z, v[u][3] = y.w;
+                        const float4 y4 = *reinterpret_cast<const float4 *>(pk + (size_t)x * D + lane * 4);
+                        v[u][0] = y4.x, v[u][1] = y4.y, v[u][2] = y4.z, v[u][3] = y4.w;
                     } else {
-                        const float2 y = *reinterpret_cast<const float2 *>(pk + (size_t)x * D + lane * 2);
-                        v[u][0] = y.x, v[u][1] = y.y;
+                        const float2 y2 = *reinterpret_cast<const float2 *>(pk + (size_t)x * D + lane * 2);
+                        v[u][0] = y2.x, v[u][1] = y2.y;
                     }
                 }
             }
@@ -700,43 +726,42 @@ __device__ __forceinline__ void join_row(const float *parts, size_t stride, int 
 }
 
 constexpr int kJoinWarps = 8;
-constexpr int kLongBlocks = 8;  // CTAs to a long item's 256 rows
+constexpr int kShortBlocks = 2, kLongBlocks = 16;  // CTAs to a head's 32 rows, or an item's 256
 
+// A CTA to a boundary between two shares, and to some of its head's rows; latency bounds it.
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
-    wait_for_launch();
-    const PlanView v = plan_view(p.plan, p.R, p.ctas);
-    const bool lng = blockIdx.y > 0;
     const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool lng = blockIdx.y >= (p.short_rows ? kShortBlocks : 0);
+    const int first = (lng ? blockIdx.y - (p.short_rows ? kShortBlocks : 0) : blockIdx.y) * kJoinWarps + warp;
+    if (blockIdx.x == 0 && blockIdx.y == 0) wait_for_launch();  // this launch does not end before the one that it overlaps
+    // the plan was there before the launch that this one waits for
+    const PlanView v = plan_view(p.plan, p.R, p.ctas);
     const Start *start = lng ? v.long_start : v.short_start;
     const Start s = start[c], before = start[c - 1];
-    const int listed = lng ? v.head->n_long : v.head->n_short;
-    if (v.head->short_rows != p.short_rows || v.head->max_len != p.max_len || v.head->ctas != p.ctas || v.head->R != p.R) return;
-    if (s.idx >= listed || s.part == 0) return;  // this share begins with a head
+    const PlanHead &h = *v.head;
+    const bool mine = h.short_rows == p.short_rows && h.max_len == p.max_len && h.ctas == p.ctas && h.Hq == p.Hq && h.Hk == p.Hk && h.R == p.R;
+    if (!mine || s.idx >= (lng ? h.n_long : h.n_short) || s.part == 0) return;  // this share begins with a head
     auto same = [&](const Start &o) { return o.idx == s.idx && o.item == s.item && o.head == s.head && o.part > 0; };
     if (same(before)) return;  // an earlier boundary's
-    // this head's parts: CTA c - 1's, and those of the shares that begin within it
-    int n = 1;
+    Parts parts;
+    parts.n = 1;
     for (int k = c;; k += 32) {
         const unsigned more = __ballot_sync(~0u, k + lane < p.ctas && same(start[min(k + lane, p.ctas)]));
-        n += more == ~0u ? 32 : __ffs(~more) - 1;
+        parts.n += more == ~0u ? 32 : __ffs(~more) - 1;
         if (more != ~0u) break;
     }
+    const int rows = lng ? 2 * kTileRows : p.short_rows, tokens = tile_tokens(p.g);
+    parts.base = lng ? p.long_parts : p.short_parts;
+    parts.stride = part_floats(rows, D), parts.c = c, parts.start = start;
+    const float *at = parts.at(lane);
     const int4 q = (lng ? v.longs : v.shorts)[s.idx];
-    if (!lng) {
-        for (int x = warp; x < q.z * p.g; x += kJoinWarps) {
-            const int token = x / p.g;
-            join_row<D>(p.short_parts, part_floats(p.short_rows, D), p.short_rows, c, n, start, x,
-                        p.y + ((long long)(q.y + token) * p.Hq + s.head * p.g + x - token * p.g) * D);
-        }
-        return;
-    }
-    const int tokens = tile_tokens(p.g);
-    for (int x = (blockIdx.y - 1) * kJoinWarps + warp; x < 2 * kTileRows; x += kLongBlocks * kJoinWarps) {
-        const int in = x & (kTileRows - 1), token = s.item * 2 * tokens + (x / kTileRows) * tokens + in / p.g;
-        if (in >= tokens * p.g || token >= q.z) continue;
-        join_row<D>(p.long_parts, part_floats(2 * kTileRows, D), 2 * kTileRows, c, n, start, x,
-                    p.y + ((long long)(q.y + token) * p.Hq + s.head * p.g + in % p.g) * D);
+    wait_for_launch();
+    for (int x = first; x < rows; x += (lng ? kLongBlocks : kShortBlocks) * kJoinWarps) {
+        const int tile = lng ? x / kTileRows : 0, in = lng ? x & (kTileRows - 1) : x, token_in = in / p.g;
+        const int token = lng ? (2 * s.item + tile) * tokens + token_in : token_in;
+        if (token >= q.z || (lng && token_in >= tokens)) continue;
+        join_row<D>(parts, at, rows, x, p.y + ((long long)(q.y + token) * p.Hq + s.head * p.g + in - token_in * p.g) * D);
     }
 }
 
@@ -763,7 +788,7 @@ cudaError_t short_launch(const Params &p, int D, bool e4m3, const CUtensorMap &k
 
 cudaError_t join_launch(const Params &p, int D, bool any_long, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.ctas - 1, any_long ? 1 + kLongBlocks : 1), cfg.blockDim = dim3(kJoinWarps * 32), cfg.stream = s;
+    cfg.gridDim = dim3(p.ctas - 1, (p.short_rows ? kShortBlocks : 0) + (any_long ? kLongBlocks : 0)), cfg.blockDim = dim3(kJoinWarps * 32), cfg.stream = s;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
