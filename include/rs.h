@@ -590,7 +590,7 @@ typedef struct {
     const uint16_t *q;    /* [rows][Hq][D] bf16, row stride ld_q in elements (a multiple of 8; tokens_cap rows) */
     int64_t ld_q;
     const int32_t *pages; /* device [R][max_pages]                                            */
-    float scale;          /* of the scores, often D^-1/2; finite, not negative               */
+    float scale;          /* of the scores, often D^-1/2; finite and above 0                 */
     int32_t max_len;      /* as given to rs_attn_plan                                         */
 } rs_attn;
 

@@ -161,7 +161,7 @@ rs_status rs_attend(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *
     RS_TRY(check_batch(d, rd));
     RS_TRY(check_kv(d, kv));
     RS_TRY(check_rows(rg));
-    if (!in || in->max_len < 1 || !(in->scale >= 0.f) || !isfinite(in->scale) || !aligned(in->q, 16) || !aligned(in->pages, 4)) return RS_ERR_INVALID_ARG;
+    if (!in || in->max_len < 1 || !(in->scale > 0.f) || !isfinite(in->scale) || !aligned(in->q, 16) || !aligned(in->pages, 4)) return RS_ERR_INVALID_ARG;
     if (!stride_ok(in->ld_q, (int64_t)d->Hq * d->D)) return RS_ERR_INVALID_ARG;
     if (!aligned(plan, 128) || !aligned(y, 16) || !aligned(work, 128) || !aligned(status, 4)) return RS_ERR_INVALID_ARG;
     const int g = d->Hq / d->Hk;
