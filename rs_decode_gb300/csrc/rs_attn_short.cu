@@ -8,10 +8,10 @@
 //
 // A CTA an SM walks its share of the batch's blocks of 64 keys.  Copying
 // warps bring them by TMA into a ring (128-byte swizzle), as far ahead as shared memory
-// allows: the copies of the next head or request are under way while the last one's
-// sums are joined.  Eight warps in two groups of four take the blocks in turns, a
-// warp 16 keys of a block, each for itself: its own running maximum, sum of
-// weights and sums of values in registers, so that no barrier falls between blocks.
+// allows, and each piece's queries: the copies of the next head or request are under way while
+// the last one's sums are joined.  Eight warps in groups take the blocks in turns, a warp 16 or 32
+// keys of a block, each for itself: its own running maximum, sum of weights and sums of
+// values in registers, so that no barrier falls between blocks.
 // The matrix instructions (mma.sync, 16 rows x 8 x 16) are as many rows as a
 // token has heads on a key head; tcgen05's 128 rows would be mostly empty.  The reference
 // that weights are relative to follows the maximum only when it is 2^8 behind (2^1 with
@@ -58,8 +58,10 @@ struct Cfg {
     static constexpr int SCALES = STAGES * 2 * TILE;          // [STAGES][2][kKeys]
     static constexpr int JOIN = SCALES + (E4M3 ? STAGES * 2 * kKeys : 0);
     static constexpr int ML = JOIN + kWarps * 16 * kPitch * 4;  // [kWarps][ROWS] (maximum, sum)
-    static constexpr int BARS = ML + kWarps * ROWS * 8;
-    static constexpr int BYTES = BARS + 2 * STAGES * 8 + 32 + 1024;  // and room to align
+    static constexpr int Q = ML + kWarps * ROWS * 8;            // [ROWS] queries of a piece
+    static constexpr int QROW = 2 * D + 16;                     // their pitch: conflict-free
+    static constexpr int BARS = Q + ROWS * QROW;
+    static constexpr int BYTES = BARS + (2 * STAGES + 2) * 8 + 32 + 1024;  // and room to align
     static_assert(BYTES <= 227 * 1024 && STAGES % GROUPS == 0, "");
 };
 
@@ -188,12 +190,31 @@ __device__ __forceinline__ void produce(const Params &p, const PlanView &v, cons
     const int rows = min(p.page, kKeys), boxes = kKeys / rows;  // keys of one copy; copies to a block, a lane each
     const bool scales = C::E4M3 && role >= 2, is_v = C::E4M3 ? role & 1 : role >= C::HALVES;
     const int half = C::E4M3 ? 0 : role % C::HALVES;
+    uint64_t *const q_full = empty + C::STAGES, *const q_empty = q_full + 1;
+    const bool queries = role == C::COPIERS - 1;  // this warp brings the pieces' queries too, a row a lane
+    unsigned q_parity = 0;
     Ring ring;
-    bool first_round = true;
+    bool first_round = true, first_piece = true;
     PageWindow pages;
     Walk w;
     w.begin(p, v);
     for (; w.piece(); w.step()) {
+        if (queries) {
+            if (!first_piece) {
+                if (!wait_ready(q_empty, q_parity, abort, p.status)) return;
+                q_parity ^= 1;
+            }
+            const int rows = w.q.z * p.g, token = lane / p.g;
+            if (lane == 0) {
+                abort[1 + kCopiers] += 1;
+                mbar_arrive_expect_tx(q_full, rows * 2 * C::D);
+            }
+            __syncwarp();
+            if (lane < rows)
+                bulk_load(sm + C::Q + lane * C::QROW, p.q + (long long)(w.q.y + token) * p.ld_q + (w.at.head * p.g + lane - token * p.g) * C::D,
+                          2 * C::D, q_full);
+            first_piece = false;
+        }
         const int entries = min((w.keys + p.page - 1) >> p.page_log, p.max_pages);
         for (int b = w.at.part; b < w.last; ++b) {
             const int key = b * kKeys + lane * rows;
@@ -236,6 +257,7 @@ __device__ __forceinline__ void drain(uint64_t *full, const volatile uint32_t *b
         const int rounds = most > s ? (most - s + C::STAGES - 1) / C::STAGES : 0;
         if (rounds) mbar_wait(full + s, (rounds - 1) & 1);
     }
+    if (begun[kCopiers]) mbar_wait(full + 2 * C::STAGES, (begun[kCopiers] - 1) & 1);
 }
 
 // ---------------------------------------------------------------- arithmetic
@@ -246,23 +268,26 @@ struct Sums {
 };
 
 // The queries of a piece as operands; with 8 bits scaled to fp16, and c times what undoes it in cq.
+// Rows that the piece does not have are zeros.
 template <class C>
-__device__ __forceinline__ void load_queries(const Params &p, const int4 &rq, int head, uint32_t (&q)[C::MT][C::D / 16][4],
+__device__ __forceinline__ void load_queries(const Params &p, int rows, uint32_t from, uint32_t (&q)[C::MT][C::D / 16][4],
                                              float (&cq)[C::MT][2]) {
-    const int lane = threadIdx.x & 31, t = lane & 3, rows = rq.z * p.g;
+    const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt)
+    for (int mt = 0; mt < C::MT; ++mt) {
+        if constexpr (!C::E4M3) {
+#pragma unroll
+            for (int k = 0; k < C::D / 16; ++k) ldmatrix4(q[mt][k], from + (mt * 16 + (lane & 15)) * C::QROW + (2 * k + (lane >> 4)) * 16);
+        }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const int row = mt * 16 + hf * 8 + (lane >> 2);
             const bool in = row < rows;
-            const uint16_t *src = p.q + (long long)(rq.y + (in ? row / p.g : 0)) * p.ld_q + (head * p.g + (in ? row % p.g : 0)) * C::D;
             cq[mt][hf] = p.c;
             if constexpr (!C::E4M3) {
 #pragma unroll
                 for (int k = 0; k < C::D / 16; ++k) {
-                    q[mt][k][hf] = in ? *reinterpret_cast<const uint32_t *>(src + k * 16 + 2 * t) : 0;
-                    q[mt][k][2 + hf] = in ? *reinterpret_cast<const uint32_t *>(src + k * 16 + 8 + 2 * t) : 0;
+                    if (!in) q[mt][k][hf] = q[mt][k][2 + hf] = 0;
                 }
             } else {
                 // a lane's channels are those of its 16 bytes of codes: 16 t, and 64 + 16 t
@@ -272,8 +297,9 @@ __device__ __forceinline__ void load_queries(const Params &p, const int4 &rq, in
                 for (int k = 0; k < C::D / 64; ++k)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint4 u = in ? *reinterpret_cast<const uint4 *>(src + k * 64 + t * 16 + e * 8) : make_uint4(0, 0, 0, 0);
-                        x[8 * k + 4 * e] = u.x, x[8 * k + 4 * e + 1] = u.y, x[8 * k + 4 * e + 2] = u.z, x[8 * k + 4 * e + 3] = u.w;
+                        const uint4 u = lds128(from + row * C::QROW + (k * 64 + t * 16 + e * 8) * 2);
+                        x[8 * k + 4 * e] = in ? u.x : 0, x[8 * k + 4 * e + 1] = in ? u.y : 0;
+                        x[8 * k + 4 * e + 2] = in ? u.z : 0, x[8 * k + 4 * e + 3] = in ? u.w : 0;
                     }
 #pragma unroll
                 for (int i = 0; i < C::D / 8; ++i) top = __vmaxu2(top, x[i] & 0x7fff7fffu);
@@ -293,6 +319,7 @@ __device__ __forceinline__ void load_queries(const Params &p, const int4 &rq, in
                     }
             }
         }
+    }
 }
 
 // One warp's 8 NT keys of a staged block.  key0: position of the first; limit: the
@@ -302,7 +329,7 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
                                         uint32_t k_at, uint32_t v_at, uint32_t v_tile, uint32_t scales, int slice, int key0, int keys,
                                         int seen, const int (&limit)[C::MT][2], int part) {
     constexpr int MT = C::MT, D = C::D, N = C::N, NT = C::NT;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, t = lane & 3;
     float s[MT][NT][4] = {};
     if constexpr (!C::E4M3) {
 #pragma unroll
@@ -580,10 +607,15 @@ __device__ __forceinline__ void consume(const Params &p, const PlanView &v, unsi
     Walk w;
     w.begin(p, v);
     int turn = 0;  // the group that takes the next block
+    unsigned q_parity = 0;
     for (; w.piece(); w.step()) {
         uint32_t q[MT][C::D / 16][4];
         float cq[MT][2];
-        load_queries<C>(p, w.q, w.at.head, q, cq);
+        ok = wait_ready(empty + C::STAGES, q_parity, abort, p.status) && ok;
+        q_parity ^= 1;
+        if (ok) load_queries<C>(p, w.q.z * p.g, sm + C::Q, q, cq);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + C::STAGES + 1);
         int limit[MT][2];
         const int rows = w.q.z * p.g;
 #pragma unroll
@@ -626,14 +658,16 @@ short_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorM
     let_next_launch();
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BARS), *empty = full + C::STAGES;
-    uint32_t *abort = reinterpret_cast<uint32_t *>(empty + C::STAGES);
+    uint64_t *q_full = empty + C::STAGES, *q_empty = q_full + 1;
+    uint32_t *abort = reinterpret_cast<uint32_t *>(q_empty + 1);  // and what was begun: blocks by warp, queries
     const PlanView v = plan_view(p.plan, p.R, p.ctas);
     const bool mine = v.head->short_rows == p.short_rows && v.head->max_len == p.max_len && v.head->ctas == p.ctas &&
                       v.head->Hq == p.Hq && v.head->Hk == p.Hk && v.head->R == p.R;
     if (threadIdx.x == 0) {
         if (!mine && blockIdx.x == 0) atomicOr(p.status, RS_DEV_LENGTH);
         for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, C::COPIERS), mbar_init(empty + i, kWarps / C::GROUPS);
-        for (int i = 0; i <= kCopiers; ++i) abort[i] = 0;
+        mbar_init(q_full, 1), mbar_init(q_empty, kWarps);
+        for (int i = 0; i < 2 + kCopiers; ++i) abort[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
