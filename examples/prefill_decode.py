@@ -1,5 +1,6 @@
 """Prompts into the decode state, then decoding, then a second batch that reuses
-a cached prefix: the calls of one Gated DeltaNet layer in a serving loop.
+a cached prefix: the calls of one Gated DeltaNet layer in a serving loop, and of
+one attention layer beside it.
 
     python examples/prefill_decode.py
 
@@ -9,6 +10,10 @@ and the delta rule over all packed rows (``Layer.prefill``), which leaves each
 request's state where ``Layer.decode`` continues it and keeps the state after
 every ``BLOCK`` tokens in a pool.  A later request that starts with the same
 tokens begins from such a state instead of from nothing.
+
+The attention layer takes the same batches: the norms with rotation, the new rows'
+keys and values into the pages of a cache (``KVCache.write``), and the attention over
+it (``KVCache.attend``), for prompts and single tokens alike.
 """
 from __future__ import annotations
 
@@ -20,10 +25,12 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from rs_decode_gb300 import build  # noqa: E402
+from rs_decode_gb300.attention import KVCache  # noqa: E402
 from rs_decode_gb300.layer import Layer  # noqa: E402
 from rs_decode_gb300.prefill import Ragged, qk_norm  # noqa: E402
 
 H, G, D, WINDOW, BLOCK = 32, 16, 128, 16, 256
+HQ, HK, ROT, PAGE = 32, 4, 64, 64  # the attention layer: query heads, key heads, rotated channels, tokens of a page
 
 
 def project(tokens: torch.Tensor, seed: int = 0) -> dict:
@@ -60,6 +67,22 @@ def decode(layer: Layer, tokens: torch.Tensor) -> torch.Tensor:
     q, k = qk_norm(p["q"], p["k"], norm="l2", scale_q=D ** -0.5)
     d = dict(q=q, k=k, v=p["v"].contiguous(), alpha=p["alpha"], beta=p["beta"])
     return layer.decode({n: t.view(torch.int16) if t.dtype == torch.bfloat16 else t for n, t in d.items()}, {})
+
+
+def attend(cache: KVCache, pages: torch.Tensor, requests: list, context: list) -> torch.Tensor:
+    """One batch of the attention layer: requests' new tokens behind the tokens before them."""
+    lengths = [len(t) for t in requests]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rows = torch.randn(1000, (HQ + 2 * HK) * D, generator=g, device="cuda", dtype=torch.bfloat16)[torch.cat(requests)]
+    inv_freq = 10000.0 ** (-torch.arange(0, ROT, 2, device="cuda", dtype=torch.float32) / ROT)
+    ragged = Ragged(len(requests), sum(lengths))
+    ragged.plan(i32(lengths), i32(context))
+    plan = cache.plan(ragged, max(lengths))  # serves all attention layers of the batch
+    q, k = qk_norm(rows[:, :HQ * D].unflatten(1, (HQ, D)), rows[:, HQ * D:(HQ + HK) * D].unflatten(1, (HK, D)), norm="rms",
+                   positions=ragged.token_pos, inv_freq=inv_freq)
+    cache.write(ragged, k, rows[:, (HQ + HK) * D:].unflatten(1, (HK, D)), pages)
+    return cache.attend(ragged, q, pages, plan, max_len=max(lengths))
 
 
 def main() -> dict:
@@ -99,7 +122,26 @@ def main() -> dict:
     y2, _ = prefill(layer2, [torch.cat([prompts[0], ten])], [0], [-1], [0], pool, list(range(24, 32)))
     step_apart = float((y2[-1].float() - out[0]).norm() / out[0].norm())
     print(f"the last decoded row against the same row of a prefill: {step_apart:.1e}")
-    return {"prefix": apart, "step": step_apart, "taken": taken}
+
+    # the attention layer: the same prompts, then the same ten tokens each, one at a time; the last of
+    # them against the same row of one pass over the whole request
+    cache = KVCache(HQ, HK, D, 100, 30, page=PAGE)
+    pages = torch.randperm(100, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((4, 30), -1, dtype=torch.int32, device="cuda")
+    used = 0
+    for r, p in enumerate(prompts):
+        need = (len(p) + len(steps) + PAGE - 1) // PAGE
+        table[r, :need] = pages[used:used + need]
+        used += need
+    attend(cache, table, prompts, [0] * 4)
+    for i, t in enumerate(steps):
+        last = attend(cache, table, list(t.view(4, 1)), [len(p) + i for p in prompts])
+    whole = attend(cache, table, [torch.cat([p, torch.stack([t[r] for t in steps])]) for r, p in enumerate(prompts)], [0] * 4)
+    ends = torch.tensor([len(p) + len(steps) for p in prompts], device="cuda").cumsum(0) - 1
+    attention_apart = float((whole[ends].float() - last.float()).norm() / last.float().norm())
+    print(f"attention: {used} pages; the last token's rows against those of one pass over the prompts: {attention_apart:.1e}")
+    assert cache.status() == 0
+    return {"prefix": apart, "step": step_apart, "taken": taken, "attention": attention_apart}
 
 
 if __name__ == "__main__":

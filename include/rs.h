@@ -602,9 +602,10 @@ typedef struct {
  * stream).  Scores, sums and their joining are fp32; the weights are rounded to
  * bf16 (fp16 for few rows on an 8-bit cache) before they meet the values, y
  * once.  Rows of requests without attention in the plan, and rows past the
- * batch, are left as they are.  plan: from rs_attn_plan for the same Hq, Hk, type, R
- * and max_len (RS_DEV_LENGTH otherwise, and y is left).  An entry of the page
- * table that is outside 0..n_pages-1 reads as zeros (RS_DEV_SLOT).
+ * batch, are left as they are.  plan: from rs_attn_plan for the same Hq, Hk, type, R,
+ * tokens_cap and max_len (RS_DEV_LENGTH otherwise, and y is left).  Where an entry of
+ * a request's page table is outside 0..n_pages-1 (RS_DEV_SLOT), the request's
+ * rows are not to be used.
  * work: device scratch of rs_attn_bytes_for's bytes, 128-byte aligned; not
  * cleared, and a call leaves nothing in it that another one needs; calls that
  * may overlap need one each.  Results are the same from run to run; the batch

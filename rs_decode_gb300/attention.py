@@ -42,14 +42,18 @@ class KVCache:
         self.k, self.v = (z((*shape, D), torch.uint8 if e4m3 else torch.bfloat16) for _ in range(2))
         self.k_exp, self.v_exp = (z(shape, torch.uint8) if e4m3 else None for _ in range(2))
         self.status_word = z(1, torch.int32)
+        self._dev = self.status_word.get_device()
         self.kv = rb.Kv(*(rb._ptr(t) for t in (self.k, self.v, self.k_exp, self.v_exp)))
 
     # ------------------------------------------------------------------ checks
-    def _on_device(self, *tensors) -> None:
-        dev = self.status_word.get_device()
-        for t, name in tensors:
+    def _on_device(self, names: str, *tensors) -> None:
+        dev = self._dev
+        for t in tensors:
             if t is not None and (dev < 0 or t.get_device() != dev):
-                raise ValueError(f"{name} must be on the cache's CUDA device")
+                which = names.split()[next(i for i, x in enumerate(tensors) if x is t)]
+                raise ValueError(f"{which} must be on the cache's CUDA device")
+        if rb._current_device() != dev:  # the library launches on it
+            raise ValueError(f"the cache's CUDA device ({dev}) must be the current one")
 
     def _pages(self, ragged, pages: torch.Tensor) -> None:
         if pages.dtype is not torch.int32 or pages.shape != (ragged.desc.R, self.max_pages):
@@ -66,9 +70,10 @@ class KVCache:
         """The planned rows' keys and values, [rows, Hk, D] bf16 (torch.bfloat16, or int16 bit
         patterns; rows at any stride), to their places in the cache."""
         rd = ragged.desc
-        self._on_device((k, "k"), (v, "v"), (pages, "pages"), (ragged.counts, "the plan"))
+        self._on_device("k v pages ragged", k, v, pages, ragged.counts)
         self._pages(ragged, pages)
-        ld_k, ld_v = (packed_stride(t, rd.tokens_cap, self.Hk, self.D, n) for t, n in ((k, "k"), (v, "v")))
+        T, Hk, D = rd.tokens_cap, self.Hk, self.D
+        ld_k, ld_v = packed_stride(k, T, Hk, D, "k"), packed_stride(v, T, Hk, D, "v")
         rb.rs_kv_write(self.desc, self.kv, rd, ragged.arrays, pages, k.data_ptr(), v.data_ptr(), ld_k, ld_v,
                        self.status_word, stream)
 
@@ -80,13 +85,14 @@ class KVCache:
         rd = ragged.desc
         shape = (rd.tokens_cap, self.Hk, self.D)
         if out is None:
-            out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=self.status_word.device) for _ in range(2))
-        k, v = out
-        self._on_device((k, "out[0]"), (v, "out[1]"), (pages, "pages"), (ragged.counts, "the plan"))
+            k, v = torch.empty((2, *shape), dtype=torch.bfloat16, device=self.status_word.device).unbind(0)
+        else:
+            k, v = out
+            for t in out:
+                if t.dtype not in BF16 or t.shape[1:] != shape[1:] or t.shape[0] < shape[0]:
+                    raise ValueError(f"out must be bf16 {list(shape)}, got {t.dtype} {tuple(t.shape)}")
+        self._on_device("out[0] out[1] pages ragged", k, v, pages, ragged.counts)
         self._pages(ragged, pages)
-        for t in out:
-            if t.dtype not in BF16 or t.shape[1:] != shape[1:] or t.shape[0] < shape[0]:
-                raise ValueError(f"out must be bf16 {list(shape)}, got {t.dtype} {tuple(t.shape)}")
         rb.rs_kv_read(self.desc, self.kv, rd, ragged.arrays, pages, k, v, self.status_word, stream)
         return k, v
 
@@ -97,7 +103,7 @@ class KVCache:
         n = self._bytes(ragged.desc, max_len).plan
         if out is None:
             out = torch.empty(n, dtype=torch.uint8, device=self.status_word.device)
-        self._on_device((out, "out"), (ragged.counts, "the batch's plan"))
+        self._on_device("out ragged", out, ragged.counts)
         if out.nbytes < n:
             raise ValueError("out is smaller than a plan of this batch")
         rb.rs_attn_plan(self.desc, ragged.desc, ragged.arrays, max_len, out, self.status_word, stream)
@@ -116,7 +122,7 @@ class KVCache:
         they are allocated on the current stream, which then has to be the one the call runs on."""
         rd = ragged.desc
         T, Hq, D = rd.tokens_cap, self.Hq, self.D
-        self._on_device((q, "q"), (pages, "pages"), (plan, "plan"), (y, "y"), (work, "work"), (ragged.counts, "the batch's plan"))
+        self._on_device("q pages plan ragged y work", q, pages, plan, ragged.counts, y, work)
         self._pages(ragged, pages)
         ld_q = packed_stride(q, T, Hq, D, "q")
         sizes = self._bytes(rd, max_len)

@@ -32,8 +32,8 @@ struct PlanHead {
     int n_short, n_long;    // requests of either form
     int short_rows;         // a request of at most this many rows of a key head's group is short
     int ctas, max_len;      // what the plan was made for
-    int Hq, Hk, R;
-    int pad[8];
+    int Hq, Hk, R, cap;
+    int pad[7];
 };
 static_assert(sizeof(PlanHead) == 64, "");
 
@@ -101,6 +101,12 @@ struct Params {
     uint32_t *status;
     float *short_parts, *long_parts;  // the workspace's two halves
 };
+
+// Whether a plan is one for this call.
+__device__ __forceinline__ bool plan_fits(const PlanHead &h, const Params &p) {
+    return h.short_rows == p.short_rows && h.max_len == p.max_len && h.ctas == p.ctas && h.Hq == p.Hq && h.Hk == p.Hk && h.R == p.R &&
+           h.cap == p.cap;
+}
 
 // A part's place in the workspace: two a CTA (the end of a head that the CTA before began,
 // and the beginning of one that the next CTA goes on with), rows of D sums, then rows of

@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t kMaxRows = 1ll << 30;
 constexpr int64_t kMaxStride = 1ll << 31;
+constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kCtas = 152;  // shares of the work: one CTA for each SM of the GPU
 
 inline bool aligned(const void *p, size_t a) { return p && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -161,7 +162,7 @@ rs_status rs_attend(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *
     RS_TRY(check_batch(d, rd));
     RS_TRY(check_kv(d, kv));
     RS_TRY(check_rows(rg));
-    if (!in || in->max_len < 1 || !(in->scale > 0.f) || !isfinite(in->scale) || !aligned(in->q, 16) || !aligned(in->pages, 4)) return RS_ERR_INVALID_ARG;
+    if (!in || in->max_len < 1 || !(in->scale > 0.f) || !isfinite(in->scale * kLog2e) || !aligned(in->q, 16) || !aligned(in->pages, 4)) return RS_ERR_INVALID_ARG;
     if (!stride_ok(in->ld_q, (int64_t)d->Hq * d->D)) return RS_ERR_INVALID_ARG;
     if (!aligned(plan, 128) || !aligned(y, 16) || !aligned(work, 128) || !aligned(status, 4)) return RS_ERR_INVALID_ARG;
     const int g = d->Hq / d->Hk;
@@ -171,7 +172,7 @@ rs_status rs_attend(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *
     p.n_pages = d->n_pages, p.max_pages = d->max_pages, p.R = rd->R, p.cap = rd->tokens_cap;
     p.ctas = kCtas, p.max_len = in->max_len, p.short_rows = f.short_rows;
     p.pages = in->pages, p.q = in->q, p.ld_q = in->ld_q;
-    p.c = in->scale * 1.44269504088896341f;
+    p.c = in->scale * kLog2e;
     p.y = y, p.plan = const_cast<void *>(plan), p.ks = kv->ks, p.vs = kv->vs, p.status = status;
     p.short_parts = static_cast<float *>(work), p.long_parts = p.short_parts + short_floats(*d, f);
     const bool e4m3 = d->type == RS_KV_E4M3;

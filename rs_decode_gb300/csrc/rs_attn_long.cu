@@ -698,9 +698,7 @@ long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
     const uint32_t sm = (smem_u32(raw) + (uint32_t)sizeof(Shared) + 1023) & ~1023u;
     Shared *b = reinterpret_cast<Shared *>(raw);
     const PlanView v = plan_view(p.plan, p.R, p.ctas);
-    const bool mine = sm + C::TILES <= smem_u32(raw) + C::BYTES && v.head->short_rows == p.short_rows &&
-                      v.head->max_len == p.max_len && v.head->ctas == p.ctas && v.head->Hq == p.Hq && v.head->Hk == p.Hk &&
-                      v.head->R == p.R;
+    const bool mine = sm + C::TILES <= smem_u32(raw) + C::BYTES && plan_fits(*v.head, p);
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
     if (warp == 8) {
         tmem_alloc(&b->tmem, 512);

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         PlanHead h = {};
         h.n_short = n_short, h.n_long = n_long, h.short_rows = p.short_rows, h.ctas = p.ctas, h.max_len = p.max_len;
-        h.Hq = p.Hq, h.Hk = p.Hk, h.R = p.R;
+        h.Hq = p.Hq, h.Hk = p.Hk, h.R = p.R, h.cap = p.cap;
         *v.head = h;
     }
     for (int i = threadIdx.x; i < 2 * (p.ctas + 1); i += kThreads) {

@@ -50,11 +50,10 @@ struct Cfg {
     static constexpr int ROWB = D * (E4M3 ? 1 : 2);           // bytes of a key
     static constexpr int HALVES = ROWB > 128 ? 2 : 1;         // tiles of 128-byte rows side by side
     static constexpr int TILE = kKeys * ROWB;
-    // copying warps at work: halves of keys and of values, or keys, values and the scales of both
-    static constexpr int COPIERS = E4M3 ? 4 : 2 * HALVES;
     // whole rounds of all groups of warps: a stage always meets the same group, which
     // then waits on its barriers in every round
     static constexpr int STAGES = 2 * TILE >= 32768 ? 6 : 12;
+    static constexpr int COPIERS = STAGES % 4 ? 3 : 4;        // copying warps at work, each every third or fourth block
     static constexpr int SCALES = STAGES * 2 * TILE;          // [STAGES][2][kKeys]
     static constexpr int JOIN = SCALES + (E4M3 ? STAGES * 2 * kKeys : 0);
     static constexpr int ML = JOIN + kWarps * 16 * kPitch * 4;  // [kWarps][ROWS] (maximum, sum)
@@ -62,7 +61,7 @@ struct Cfg {
     static constexpr int QROW = 2 * D + 16;                     // their pitch: conflict-free
     static constexpr int BARS = Q + ROWS * QROW;
     static constexpr int BYTES = BARS + (2 * STAGES + 2) * 8 + 32 + 1024;  // and room to align
-    static_assert(BYTES <= 227 * 1024 && STAGES % GROUPS == 0, "");
+    static_assert(BYTES <= 227 * 1024 && STAGES % GROUPS == 0 && STAGES % COPIERS == 0, "");
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -187,14 +186,19 @@ __device__ __forceinline__ void produce(const Params &p, const PlanView &v, cons
     const int lane = threadIdx.x & 31, role = (threadIdx.x >> 5) - kWarps;
     if (role >= C::COPIERS) return;
     volatile uint32_t *const begun = abort + 1 + role;  // blocks, for drain()
-    const int rows = min(p.page, kKeys), boxes = kKeys / rows;  // keys of one copy; copies to a block, a lane each
-    const bool scales = C::E4M3 && role >= 2, is_v = C::E4M3 ? role & 1 : role >= C::HALVES;
-    const int half = C::E4M3 ? 0 : role % C::HALVES;
+    // A block is one warp's: one that issues every copy of every block would take longer than the copies.  A lane
+    // to a copy: keys or values, half of the channels, up to 64 keys; then (8 bits) scales of as many keys.
+    const int rows = min(p.page, kKeys), boxes = kKeys / rows;
+    const bool scales = C::E4M3 && lane >= 16 && lane < 16 + 2 * boxes, is_v = lane & 1;
+    const bool tiles = lane < 2 * C::HALVES * boxes;
+    const int half = scales ? 0 : (lane >> 1) % C::HALVES, box = scales ? (lane - 16) >> 1 : min((lane >> 1) / C::HALVES, boxes - 1);
     uint64_t *const q_full = empty + C::STAGES, *const q_empty = q_full + 1;
     const bool queries = role == C::COPIERS - 1;  // this warp brings the pieces' queries too, a row a lane
     unsigned q_parity = 0;
     Ring ring;
+    ring.at = role;
     bool first_round = true, first_piece = true;
+    int skip = role;  // blocks until this warp's next
     PageWindow pages;
     Walk w;
     w.begin(p, v);
@@ -216,46 +220,44 @@ __device__ __forceinline__ void produce(const Params &p, const PlanView &v, cons
             first_piece = false;
         }
         const int entries = min((w.keys + p.page - 1) >> p.page_log, p.max_pages);
-        for (int b = w.at.part; b < w.last; ++b) {
-            const int key = b * kKeys + lane * rows;
+        int b = w.at.part + skip;
+        for (; b < w.last; b += C::COPIERS) {
+            const int key = b * kKeys + box * rows, row = key & (p.page - 1);
             pages.at(p, w.q.x, entries, (b * kKeys) >> p.page_log);
-            const bool mine = lane < boxes;
-            const int page = pages.page(p, key >> p.page_log, mine && key < w.keys);
+            const int page = pages.page(p, key >> p.page_log, (tiles || scales) && key < w.keys);
             if (!first_round && !wait_ready(empty + ring.at, ring.parity ^ 1, abort, p.status)) return;
-            const int row = key & (p.page - 1);
-            const unsigned there = __ballot_sync(~0u, page >= 0);
+            const unsigned there = __ballot_sync(~0u, scales && page >= 0);
             if (lane == 0) {
                 *begun += 1;
-                mbar_arrive_expect_tx(full + ring.at, scales ? __popc(there) * rows : C::TILE / C::HALVES);
+                mbar_arrive_expect_tx(full + ring.at, 2 * C::TILE + __popc(there) * rows);
             }
             __syncwarp();
-            if (scales) {
-                if (page >= 0)
-                    bulk_load(sm + C::SCALES + (ring.at * 2 + is_v) * kKeys + lane * rows,
-                              (is_v ? p.vs : p.ks) + (((size_t)page * p.Hk + w.at.head) << p.page_log) + row, rows, full + ring.at);
-            } else if (mine) {  // a coordinate past the cache fills in zeros
+            if (tiles) {  // a coordinate past the cache fills in zeros
                 const int slab = page >= 0 ? page * p.Hk + w.at.head : p.n_pages * p.Hk;
-                const uint32_t to = sm + ring.at * 2 * C::TILE + half * (kKeys * 128) + lane * rows * min(C::ROWB, 128);
+                const uint32_t to = sm + ring.at * 2 * C::TILE + half * (kKeys * 128) + box * rows * min(C::ROWB, 128);
                 if (is_v)
                     tma_load_3d(to + C::TILE, vm, half * 64, row, slab, full + ring.at);
                 else
                     tma_load_3d(to, km, half * 64, row, slab, full + ring.at);
+            } else if (scales && page >= 0) {
+                bulk_load(sm + C::SCALES + (ring.at * 2 + is_v) * kKeys + box * rows,
+                          (is_v ? p.vs : p.ks) + (((size_t)page * p.Hk + w.at.head) << p.page_log) + row, rows, full + ring.at);
             }
-            ring.step(C::STAGES);
-            if (ring.at == 0) first_round = false;
+#pragma unroll
+            for (int i = 0; i < C::COPIERS; ++i) ring.step(C::STAGES);
+            if (ring.at == role) first_round = false;
         }
+        skip = b - w.last;
     }
 }
 
 // After giving up: wait (with a limit) for the copies still in flight.
 template <class C>
 __device__ __forceinline__ void drain(uint64_t *full, const volatile uint32_t *begun) {
-    // a block that only some of the warps began cannot complete: the limit ends that wait
-    int most = 0;
-    for (int i = 0; i < C::COPIERS; ++i) most = max(most, (int)begun[i]);
+    constexpr int PLACES = C::STAGES / C::COPIERS;  // a warp's
     for (int s = 0; s < C::STAGES; ++s) {
-        const int rounds = most > s ? (most - s + C::STAGES - 1) / C::STAGES : 0;
-        if (rounds) mbar_wait(full + s, (rounds - 1) & 1);
+        const int n = (int)begun[s % C::COPIERS], first = s / C::COPIERS;
+        if (n > first) mbar_wait(full + s, ((n - first + PLACES - 1) / PLACES - 1) & 1);
     }
     if (begun[kCopiers]) mbar_wait(full + 2 * C::STAGES, (begun[kCopiers] - 1) & 1);
 }
@@ -661,11 +663,10 @@ short_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorM
     uint64_t *q_full = empty + C::STAGES, *q_empty = q_full + 1;
     uint32_t *abort = reinterpret_cast<uint32_t *>(q_empty + 1);  // and what was begun: blocks by warp, queries
     const PlanView v = plan_view(p.plan, p.R, p.ctas);
-    const bool mine = v.head->short_rows == p.short_rows && v.head->max_len == p.max_len && v.head->ctas == p.ctas &&
-                      v.head->Hq == p.Hq && v.head->Hk == p.Hk && v.head->R == p.R;
+    const bool mine = plan_fits(*v.head, p);
     if (threadIdx.x == 0) {
         if (!mine && blockIdx.x == 0) atomicOr(p.status, RS_DEV_LENGTH);
-        for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, C::COPIERS), mbar_init(empty + i, kWarps / C::GROUPS);
+        for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, 1), mbar_init(empty + i, kWarps / C::GROUPS);
         mbar_init(q_full, 1), mbar_init(q_empty, kWarps);
         for (int i = 0; i < 2 + kCopiers; ++i) abort[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const Start *start = lng ? v.long_start : v.short_start;
     const Start s = start[c], before = start[c - 1];
     const PlanHead &h = *v.head;
-    const bool mine = h.short_rows == p.short_rows && h.max_len == p.max_len && h.ctas == p.ctas && h.Hq == p.Hq && h.Hk == p.Hk && h.R == p.R;
+    const bool mine = plan_fits(h, p);
     if (!mine || s.idx >= (lng ? h.n_long : h.n_short) || s.part == 0) return;  // this share begins with a head
     auto same = [&](const Start &o) { return o.idx == s.idx && o.item == s.item && o.head == s.head && o.part > 0; };
     if (same(before)) return;  // an earlier boundary's

@@ -133,7 +133,7 @@ def test_attend_refusals(lib):
         return lib.rs_attend(ctypes.byref(d or desc()), ctypes.byref(cache or kv()), ctypes.byref(rd or ragged()),
                              ctypes.byref(rg or addresses(rb.RaggedArrays)), None if none else ctypes.byref(x), plan, y, work, st, None)
     for a in (dict(q=None), dict(q=0x1008), dict(ld_q=1016), dict(ld_q=1028), dict(pages=None), dict(pages=0x2002), dict(scale=-1.0), dict(scale=0.0),
-              dict(scale=float("nan")), dict(scale=float("inf")), dict(max_len=0), dict(max_len=-3), dict(ld_q=(1 << 31) + 8)):
+              dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(max_len=0), dict(max_len=-3), dict(ld_q=(1 << 31) + 8)):
         assert call(a) == INVALID, a
     for kw in (dict(none=True), dict(plan=None), dict(plan=0x4040), dict(y=None), dict(y=0x5008), dict(work=None), dict(work=0x6010),
                dict(st=None), dict(cache=addresses(rb.Kv)), dict(rd=ragged(tokens_cap=0)), dict(rg=addresses(rb.RaggedArrays, cu_tokens=0x100002)),
@@ -152,6 +152,7 @@ def calls(monkeypatch, lib):
     seen = []
     for name in ("rs_kv_write", "rs_kv_read", "rs_attn_plan", "rs_attend"):
         monkeypatch.setattr(rb, name, lambda *a, _n=name, **k: seen.append(_n))
+    monkeypatch.setattr(rb, "_current_device", lambda: 0)
     with FakeTensorMode():
         yield seen
 
@@ -234,6 +235,17 @@ def test_attend_tensors(calls):
         c.plan(plan_of("cuda:1"), T)
     with pytest.raises(rb.RsError):
         c.plan(plan_of(), 0)
+    assert calls == []
+
+
+def test_another_current_device_is_refused(calls, monkeypatch):
+    c = cache()
+    k = fake(T, HK, D)
+    monkeypatch.setattr(rb, "_current_device", lambda: 1)
+    for call in (lambda: c.write(plan_of(), k, k, pages()), lambda: c.read(plan_of(), pages()), lambda: c.plan(plan_of(), T),
+                 lambda: c.attend(plan_of(), fake(T, HQ, D), pages(), fake(100_000, dtype=U8), max_len=T)):
+        with pytest.raises(ValueError, match="current"):
+            call()
     assert calls == []
 
 

@@ -138,6 +138,10 @@ def test_plan_of_another_shape_is_refused():
     assert b.cache.status() == rb.DEV_LENGTH and bool((y == 4.0).all())
     b.cache.attend(b.ragged, q, b.pages, torch.zeros_like(plan), max_len=200, y=y)
     assert b.cache.status() == rb.DEV_LENGTH and bool((y == 4.0).all())
+    wider = Ragged(len(b.lengths), b.cap + 100)  # as many requests, more rows
+    wider.plan(i32([min(200, n + 10) for n in b.lengths]), i32([0] * len(b.lengths)))
+    b.cache.attend(b.ragged, q, b.pages, b.cache.plan(wider, 200), max_len=200, y=y)
+    assert b.cache.status() == rb.DEV_LENGTH and bool((y == 4.0).all())
     b.cache.attend(b.ragged, q, b.pages, plan, max_len=200, y=y)
     b.check(q, y)
 
@@ -351,3 +355,14 @@ def test_a_prompt_in_pieces(type):
     b.k = [k[a: a + n].to(F64).transpose(0, 1) for a, n in zip((0, total[0]), total)]
     b.v = [v[a: a + n].to(F64).transpose(0, 1) for a, n in zip((0, total[0]), total)]
     b.check(torch.cat(rows[0]), torch.cat([torch.cat(o) for o in out]))
+
+
+def test_the_example_s_attention_layer():
+    """Ten tokens after a prompt, one at a time and in one pass: two results within 3e-3 of the same values."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "prefill_decode.py")
+    spec = importlib.util.spec_from_file_location("prefill_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    assert m.main()["attention"] <= 2 * 3e-3
