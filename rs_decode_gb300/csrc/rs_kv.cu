@@ -10,6 +10,10 @@
 //
 // Each value is read once and written once, so HBM bounds a batch of prompts,
 // and a launch's latency a step of single tokens.
+//
+// Measured: 29,871 rows of 4 + 4 heads of 128 into a bf16 cache 21.6 us, 5.7 TB/s, 0.84 of the copy peak (17.9 where the
+// caches hold part of it); 39,602 such rows out of an 8-bit cache 27.7 us, 4.4 TB/s, out of a bf16 one 29.8, 5.4 TB/s;
+// 256 rows 2.5 us, a launch.  Two or four heads a lane, to have more look-ups in flight: no faster (21.6 to 23.7, 27.7 to 30.8).
 #include <cuda_fp16.h>
 
 #include "rs_attn.cuh"
