@@ -22,7 +22,7 @@ namespace attn {
 constexpr int kKeys = 64;        // keys of a block of the short form
 constexpr int kTileKeys = 128;   // keys of a tile of the long form
 constexpr int kTileRows = 128;   // query rows (token x head of the group) of a tile
-constexpr int kMaxCtas = 512;    // shares at most
+constexpr int kCtas = 152;       // shares of the work: one CTA for each SM of the GPU
 // What starting a piece costs, in keys' blocks or tiles: its queries, its epilogue.
 constexpr int kShortStart = 1;
 constexpr int kLongStart = 2;
@@ -43,14 +43,21 @@ struct Start {
     int idx, item, head, part;
 };
 
+// A head that several shares have parts of, at the first of them that begins within it (n 0 at the
+// others): how many parts there are, and its rows.
+struct Join {
+    int n, head, row, tokens;  // parts, key head, packed row of the first token, tokens
+};
+
 struct PlanView {
     PlanHead *head;
     int4 *shorts, *longs;           // [R] request, first row, rows, context
     Start *short_start, *long_start;  // [ctas + 1]
+    Join *short_join, *long_join;     // [ctas]
     long long *short_cu, *long_cu;  // [R + 1] work before each listed request
 };
 inline size_t plan_bytes(int R, int ctas) {
-    return sizeof(PlanHead) + 32 * (size_t)R + 2 * sizeof(Start) * (size_t)(ctas + 1) + 16 * ((size_t)R + 1);
+    return sizeof(PlanHead) + 32 * (size_t)R + 2 * sizeof(Start) * (size_t)(ctas + 1) + 2 * sizeof(Join) * (size_t)ctas + 16 * ((size_t)R + 1);
 }
 __host__ __device__ inline PlanView plan_view(void *plan, int R, int ctas) {
     unsigned char *p = static_cast<unsigned char *>(plan);
@@ -61,7 +68,9 @@ __host__ __device__ inline PlanView plan_view(void *plan, int R, int ctas) {
     v.longs = v.shorts + R;
     v.short_start = reinterpret_cast<Start *>(v.longs + R);
     v.long_start = v.short_start + ctas + 1;
-    v.short_cu = reinterpret_cast<long long *>(v.long_start + ctas + 1);
+    v.short_join = reinterpret_cast<Join *>(v.long_start + ctas + 1);
+    v.long_join = v.short_join + ctas;
+    v.short_cu = reinterpret_cast<long long *>(v.long_join + ctas);
     v.long_cu = v.short_cu + R + 1;
     return v;
 }

@@ -13,7 +13,6 @@ namespace {
 constexpr int64_t kMaxRows = 1ll << 30;
 constexpr int64_t kMaxStride = 1ll << 31;
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr int kCtas = 152;  // shares of the work: one CTA for each SM of the GPU
 
 inline bool aligned(const void *p, size_t a) { return p && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool stride_ok(int64_t ld, int64_t row) { return ld >= row && ld % 8 == 0 && ld <= kMaxStride; }

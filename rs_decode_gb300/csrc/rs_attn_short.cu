@@ -695,114 +695,144 @@ short_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorM
 }
 
 // ---------------------------------------------------------------- parts of a head
-// The parts of a head that several CTAs shared, in the order of its keys, a lane each (32 at a time): the
-// first is the end of CTA c - 1's share, the others begin the shares c, c + 1 ..
-struct Parts {
-    const float *base;
-    size_t stride;
-    int c, n;
-    const Start *start;
-    __device__ __forceinline__ const float *at(int k) const {
-        if (k >= n) return nullptr;
-        if (k == 0) return base + (size_t)(2 * (c - 1) + 1) * stride;
-        const Start a = start[c + k - 1], b = start[c + k];
-        const bool none = a.idx == b.idx && a.item == b.item && a.head == b.head && a.part == b.part;  // an empty share
-        return none ? nullptr : base + (size_t)(2 * (c + k - 1)) * stride;
-    }
-};
-
-// Row x of such a head, a warp's work, D / 32 channels a lane.  mine: the lane's of the first 32 parts.
-template <int D>
-__device__ __forceinline__ void join_row(const Parts &parts, const float *mine, int rows, int x, uint16_t *y) {
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31;
-    float2 ml = mine ? reinterpret_cast<const float2 *>(mine + (size_t)rows * D)[x] : make_float2(-INFINITY, 0.f);
-    float m = ml.x;
-    for (int k0 = 32; k0 < parts.n; k0 += 32) {
-        const float *at = parts.at(k0 + lane);
-        if (at) m = fmaxf(m, at[(size_t)rows * D + 2 * x]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    float l = 0.f, sum[V] = {};
-    for (int k0 = 0; k0 < parts.n; k0 += 32) {
-        const float *at = k0 ? parts.at(k0 + lane) : mine;
-        if (k0) ml = at ? reinterpret_cast<const float2 *>(at + (size_t)rows * D)[x] : make_float2(-INFINITY, 0.f);
-        // a part without keys that the row sees has sums of zero
-        const float f = !at ? 0.f : ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
-        if (at) l += ml.y * f;
-        const unsigned live = __ballot_sync(~0u, at != nullptr);
-        const unsigned long long addr = reinterpret_cast<unsigned long long>(at);
-        for (int k = 0; k < min(32, parts.n - k0); k += 8) {
-            float v[8][V], fk[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {  // independent loads
-                fk[u] = __shfl_sync(~0u, f, k + u);
-                const float *pk = reinterpret_cast<const float *>(__shfl_sync(~0u, addr, k + u));
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[u][i] = 0.f;
-                if (live >> (k + u) & 1) {
-                    if constexpr (V == 4) {
-                        const float4 y4 = *reinterpret_cast<const float4 *>(pk + (size_t)x * D + lane * 4);
-                        v[u][0] = y4.x, v[u][1] = y4.y, v[u][2] = y4.z, v[u][3] = y4.w;
-                    } else {
-                        const float2 y2 = *reinterpret_cast<const float2 *>(pk + (size_t)x * D + lane * 2);
-                        v[u][0] = y2.x, v[u][1] = y2.y;
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-#pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] = fmaf(fk[u], v[u][i], sum[i]);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    const float inv = 1.f / l;
-    if constexpr (V == 4)
-        *reinterpret_cast<uint2 *>(y + lane * 4) = make_uint2(pack_bf(sum[0] * inv, sum[1] * inv), pack_bf(sum[2] * inv, sum[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(y + lane * 2) = pack_bf(sum[0] * inv, sum[1] * inv);
-}
-
 constexpr int kJoinWarps = 8;
 constexpr int kShortBlocks = 2, kLongBlocks = 16;  // CTAs to a head's 32 rows, or an item's 256
 
-// A CTA to a boundary between two shares, and to some of its head's rows; latency bounds it.
+// Rows x0, x0 + dx .. (NR of them, those with y) of a head that CTA c - 1's share ends with and the
+// shares c, c + 1 .. begin with: n parts in the order of its keys, stride floats from CTA to CTA.  A warp's
+// work, D / 32 channels a lane, the sums of U parts in flight, the first of them with the maxima.
+template <int D, int NR, int U>
+__device__ __forceinline__ void join_rows(const float *parts, size_t stride, int c, int n, int rows, int x0, int dx, uint16_t *const (&y)[NR]) {
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    auto part = [&](int k) { return parts + (size_t)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c + k - 1)) * stride; };
+    float o[NR][U][V];
+    auto load = [&](int k) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[r][u][i] = 0.f;
+                if (k + u < n && y[r]) {
+                    const float *at = part(k + u) + (size_t)(x0 + r * dx) * D + lane * V;
+                    if constexpr (V == 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(at);
+                        o[r][u][0] = v.x, o[r][u][1] = v.y, o[r][u][2] = v.z, o[r][u][3] = v.w;
+                    } else {
+                        const float2 v = *reinterpret_cast<const float2 *>(at);
+                        o[r][u][0] = v.x, o[r][u][1] = v.y;
+                    }
+                }
+            }
+    };
+    auto max_sum = [&](int k, int r) {
+        return k < n && y[r] ? reinterpret_cast<const float2 *>(part(k) + (size_t)rows * D)[x0 + r * dx] : make_float2(-INFINITY, 0.f);
+    };
+    auto put = [&](const float (&sum)[V], float l, uint16_t *to) {
+        const float inv = 1.f / l;
+        if constexpr (V == 4)
+            *reinterpret_cast<uint2 *>(to + lane * 4) = make_uint2(pack_bf(sum[0] * inv, sum[1] * inv), pack_bf(sum[2] * inv, sum[3] * inv));
+        else
+            *reinterpret_cast<uint32_t *>(to + lane * 2) = pack_bf(sum[0] * inv, sum[1] * inv);
+    };
+    if (n <= U) {  // most heads: every lane reads all maxima
+        float2 ml[NR][U];
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int u = 0; u < U; ++u) ml[r][u] = max_sum(u, r);
+        load(0);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            float m = -INFINITY, l = 0.f, sum[V] = {};
+#pragma unroll
+            for (int u = 0; u < U; ++u) m = fmaxf(m, ml[r][u].x);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float f = ml[r][u].x == -INFINITY ? 1.f : ex2(ml[r][u].x - m);
+                l = fmaf(ml[r][u].y, f, l);
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] = fmaf(f, o[r][u][i], sum[i]);
+            }
+            if (y[r]) put(sum, l, y[r]);
+        }
+        return;
+    }
+    float2 ml[NR];
+    float m[NR], l[NR], sum[NR][V];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) ml[r] = max_sum(lane, r);
+    load(0);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        m[r] = ml[r].x, l[r] = 0.f;
+        for (int k = 32 + lane; k < n; k += 32) m[r] = fmaxf(m[r], max_sum(k, r).x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m[r] = fmaxf(m[r], __shfl_xor_sync(~0u, m[r], d));
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[r][i] = 0.f;
+    }
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        float f[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            if (k0) ml[r] = max_sum(k0 + lane, r);
+            // a part without keys that the row sees has sums of zero
+            f[r] = k0 + lane >= n ? 0.f : ml[r].x == -INFINITY ? 1.f : ex2(ml[r].x - m[r]);
+            l[r] += ml[r].y * f[r];
+        }
+        for (int k = k0; k < min(k0 + 32, n); k += U) {
+            if (k) load(k);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float fu = __shfl_sync(~0u, f[r], (k + u) & 31);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[r][i] = fmaf(fu, o[r][u][i], sum[r][i]);
+                }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l[r] += __shfl_xor_sync(~0u, l[r], d);
+        if (y[r]) put(sum[r], l[r], y[r]);
+    }
+}
+
+// A CTA to a boundary between two shares, and to some of its head's rows.  Latency bounds it: one look
+// into the plan, then the maxima and the first sums.  151 items of 256 rows, two parts each, take 13 us
+// on a cold L2; four parts of one row in flight, two of each of a long form's two rows (64 registers)
+// against 16 of one row (124): 16 prompts 417 against 437 us.
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
-    const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool lng = blockIdx.y >= (p.short_rows ? kShortBlocks : 0);
-    const int first = (lng ? blockIdx.y - (p.short_rows ? kShortBlocks : 0) : blockIdx.y) * kJoinWarps + warp;
+    const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, shorts = p.short_rows ? kShortBlocks : 0;
+    const bool lng = blockIdx.y >= shorts;
     if (blockIdx.x == 0 && blockIdx.y == 0) wait_for_launch();  // this launch does not end before the one that it overlaps
     // the plan was there before the launch that this one waits for
     const PlanView v = plan_view(p.plan, p.R, p.ctas);
-    const Start *start = lng ? v.long_start : v.short_start;
-    const Start s = start[c], before = start[c - 1];
-    const PlanHead &h = *v.head;
-    const bool mine = plan_fits(h, p);
-    if (!mine || s.idx >= (lng ? h.n_long : h.n_short) || s.part == 0) return;  // this share begins with a head
-    auto same = [&](const Start &o) { return o.idx == s.idx && o.item == s.item && o.head == s.head && o.part > 0; };
-    if (same(before)) return;  // an earlier boundary's
-    Parts parts;
-    parts.n = 1;
-    for (int k = c;; k += 32) {
-        const unsigned more = __ballot_sync(~0u, k + lane < p.ctas && same(start[min(k + lane, p.ctas)]));
-        parts.n += more == ~0u ? 32 : __ffs(~more) - 1;
-        if (more != ~0u) break;
-    }
-    const int rows = lng ? 2 * kTileRows : p.short_rows, tokens = tile_tokens(p.g);
-    parts.base = lng ? p.long_parts : p.short_parts;
-    parts.stride = part_floats(rows, D), parts.c = c, parts.start = start;
-    const float *at = parts.at(lane);
-    const int4 q = (lng ? v.longs : v.shorts)[s.idx];
+    const Join j = (lng ? v.long_join : v.short_join)[c];
+    if (!plan_fits(*v.head, p) || j.n == 0) return;
+    const int tile_toks = tile_tokens(p.g);
+    // row `in` of query tile t
+    auto row = [&](int t, int in) -> uint16_t * {
+        const int i = in / p.g, token = t * tile_toks + i;
+        const bool live = token < j.tokens && (!lng || i < tile_toks);
+        return live ? p.y + ((long long)(j.row + token) * p.Hq + j.head * p.g + in - i * p.g) * D : nullptr;
+    };
     wait_for_launch();
-    for (int x = first; x < rows; x += (lng ? kLongBlocks : kShortBlocks) * kJoinWarps) {
-        const int tile = lng ? x / kTileRows : 0, in = lng ? x & (kTileRows - 1) : x, token_in = in / p.g;
-        const int token = lng ? (2 * s.item + tile) * tokens + token_in : token_in;
-        if (token >= q.z || (lng && token_in >= tokens)) continue;
-        join_row<D>(parts, at, rows, x, p.y + ((long long)(q.y + token) * p.Hq + s.head * p.g + in - token_in * p.g) * D);
+    if (lng) {
+        for (int x = (blockIdx.y - shorts) * kJoinWarps + warp; x < kTileRows; x += kLongBlocks * kJoinWarps) {
+            uint16_t *const y[2] = {row(0, x), row(1, x)};
+            if (y[0]) join_rows<D, 2, 2>(p.long_parts, part_floats(2 * kTileRows, D), c, j.n, 2 * kTileRows, x, kTileRows, y);
+        }
+    } else {
+        for (int x = blockIdx.y * kJoinWarps + warp; x < p.short_rows; x += kShortBlocks * kJoinWarps) {
+            uint16_t *const y[1] = {row(0, x)};
+            if (y[0]) join_rows<D, 1, 4>(p.short_parts, part_floats(p.short_rows, D), c, j.n, p.short_rows, x, 0, y);
+        }
     }
 }
 
