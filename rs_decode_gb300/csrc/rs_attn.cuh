@@ -23,8 +23,10 @@ constexpr int kKeys = 64;        // keys of a block of the short form
 constexpr int kTileKeys = 128;   // keys of a tile of the long form
 constexpr int kTileRows = 128;   // query rows (token x head of the group) of a tile
 constexpr int kCtas = 152;       // shares of the work: one CTA for each SM of the GPU
-// What starting a piece costs, in keys' blocks or tiles: its queries, its epilogue.
-constexpr int kShortStart = 1;
+// What starting a piece costs, in keys' blocks or tiles: its queries, its epilogue.  With 1, 4 and 7 blocks
+// 256 requests on an 8-bit cache took 216, 204 and 196 us, one on 131,072 keys 56, 56 and 59, 64 of four drafts 97, 88
+// and 89; with 1, 2, 3 and 4 tiles 16 prompts took 476, 417, 431 and 443.
+constexpr int kShortStart = 4;
 constexpr int kLongStart = 2;
 
 // The head of a plan's buffer.  Lists and starts follow it, see PlanView.
@@ -57,7 +59,8 @@ struct PlanView {
     long long *short_cu, *long_cu;  // [R + 1] work before each listed request
 };
 inline size_t plan_bytes(int R, int ctas) {
-    return sizeof(PlanHead) + 32 * (size_t)R + 2 * sizeof(Start) * (size_t)(ctas + 1) + 2 * sizeof(Join) * (size_t)ctas + 16 * ((size_t)R + 1);
+    return sizeof(PlanHead) + 32 * (size_t)R + 2 * sizeof(Start) * (size_t)(ctas + 1) + 2 * sizeof(Join) * (size_t)ctas +
+           16 * ((size_t)R + 1);
 }
 __host__ __device__ inline PlanView plan_view(void *plan, int R, int ctas) {
     unsigned char *p = static_cast<unsigned char *>(plan);

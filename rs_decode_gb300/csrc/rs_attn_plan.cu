@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const __grid_consta
         (lng ? v.long_start : v.short_start)[c] = starts[i] = s;
     }
     __syncthreads();
-    // Heads that are cut, so that the join does not have to search for them (3 us).  No share that begins
+    // Heads that are cut, so that the join does not have to search for them (2 us).  No share that begins
     // within a head is empty: shares are whole units of work, of which each part of a head is one.
     for (int i = threadIdx.x; i < 2 * p.ctas; i += kThreads) {
         const bool lng = i >= p.ctas;

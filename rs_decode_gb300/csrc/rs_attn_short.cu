@@ -26,9 +26,9 @@
 // largest loses bits.  The sum of weights itself stays fp32 and unrounded in both.
 //
 // Measured (32 query heads on 4 key heads of 128): 256 tokens behind 20 to 8,000 keys each, 2.1 GB of bf16 cache,
-// 315 us, 6.7 TB/s, 0.99 of the copy peak; from an 8-bit cache 217 us, 5.0 TB/s, where the conversion and
+// 315 us, 6.7 TB/s, 0.99 of the copy peak; from an 8-bit cache 204 us, 5.3 TB/s, where the conversion and
 // the products' own chain bound it (0.43 us a block of 64 keys against 0.37 at the copy's rate); four drafts of 64
-// requests 100 us, 4.2 TB/s.  One token behind 131,071 keys 58 us and four behind 50 to 900 each 11 to 15 us: there
+// requests 88 us, 4.8 TB/s.  One token behind 131,071 keys 56 us and four behind 50 to 900 each 10 to 15 us: there
 // the launches, a start of dependent loads, and the joining of parts.
 #include "rs_attn.cuh"
 
@@ -803,7 +803,7 @@ __device__ __forceinline__ void join_rows(const float *parts, size_t stride, int
 }
 
 // A CTA to a boundary between two shares, and to some of its head's rows.  Latency bounds it: one look
-// into the plan, then the maxima and the first sums.  151 items of 256 rows, two parts each, take 13 us
+// into the plan, then the maxima and the first sums.  151 items of 256 rows, two parts each, take 11 us
 // on a cold L2; four parts of one row in flight, two of each of a long form's two rows (64 registers)
 // against 16 of one row (124): 16 prompts 417 against 437 us.
 template <int D>
