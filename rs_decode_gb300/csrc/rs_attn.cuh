@@ -23,10 +23,11 @@ constexpr int kKeys = 64;        // keys of a block of the short form
 constexpr int kTileKeys = 128;   // keys of a tile of the long form
 constexpr int kTileRows = 128;   // query rows (token x head of the group) of a tile
 constexpr int kCtas = 152;       // shares of the work: one CTA for each SM of the GPU
-// What starting a piece costs, in keys' blocks or tiles: its queries, its epilogue.  With 1, 4 and 7 blocks
-// 256 requests on an 8-bit cache took 216, 204 and 196 us, one on 131,072 keys 56, 56 and 59, 64 of four drafts 97, 88
-// and 89; with 1, 2, 3 and 4 tiles 16 prompts took 476, 417, 431 and 443.
-constexpr int kShortStart = 4;
+// What starting a piece costs, in keys' blocks or tiles: its queries, its epilogue.  About 3 us in the short form, four
+// blocks of bf16 and seven of 8 bits: with 1, 4 and 7 blocks 64 requests of four drafts took 97, 88 and 89 us and one
+// request on 131,072 keys 56, 56 and 59; 256 requests on an 8-bit cache 216, 204 and 196, 33 of 64 heads on 8 there 89, 87
+// and 79.  With 1, 2, 3 and 4 tiles 16 prompts took 476, 417, 431 and 443.
+inline int short_start(bool e4m3) { return e4m3 ? 7 : 4; }
 constexpr int kLongStart = 2;
 
 // The head of a plan's buffer.  Lists and starts follow it, see PlanView.

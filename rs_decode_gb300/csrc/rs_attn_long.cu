@@ -15,7 +15,7 @@
 // The weights are relative to a reference that follows a row's maximum only when it is
 // 2^8 behind: then the row's O is read, scaled and written back before the next product
 // (otherwise O never leaves TMEM before the end).  Weights are rounded to bf16, which the product with bf16 values
-// asks for: 2^-9 of each, no more than y's own rounding and on average less.  Their
+// asks for: 2^-8 of each at most, no more than y's own rounding and on average less.  Their
 // sum is that of the unrounded weights, fp32.
 //
 // Warps: 0-3 and 4-7 a thread a row of either tile; 8 issues the products; 9 and 10 the copies

@@ -14,7 +14,7 @@ namespace {
 constexpr int kThreads = 1024;
 
 struct PlanParams {
-    int Hq, Hk, g, R, cap, max_len, short_rows, ctas;
+    int Hq, Hk, g, R, cap, max_len, short_rows, short_start, ctas;
     long long keys_cap;  // keys that a request's row of the page table has room for
     rs_ragged rg;
     void *plan;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const __grid_consta
         }
         const bool is_short = n > 0 && (long long)n * p.g <= p.short_rows, is_long = n > 0 && !is_short;
         long long count = (is_short ? 1ll : 0) | (is_long ? 1ll << 32 : 0), ws = 0, wl = 0;
-        if (is_short) ws = (long long)p.Hk * ((ctx + n + kKeys - 1) / kKeys + kShortStart);
+        if (is_short) ws = (long long)p.Hk * ((ctx + n + kKeys - 1) / kKeys + p.short_start);
         if (is_long) {
             const int items = (n + tq - 1) / tq;
             wl = p.Hk * (items_before(ctx, tq, items - 1) + kLongStart + (ctx + n + kTileKeys - 1) / kTileKeys);
@@ -140,9 +140,9 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const __grid_consta
             s.idx = find(v.short_cu, n_short, x);
             const int4 q = v.shorts[s.idx];
             const long long at = x - v.short_cu[s.idx];
-            const int one = (q.w + q.z + kKeys - 1) / kKeys + kShortStart;
+            const int one = (q.w + q.z + kKeys - 1) / kKeys + p.short_start;
             s.head = (int)(at / one);
-            s.part = max(0, (int)(at % one) - kShortStart);
+            s.part = max(0, (int)(at % one) - p.short_start);
         } else if (x < all) {
             s.idx = find(v.long_cu, n_long, x);
             const int4 q = v.longs[s.idx];
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const __grid_consta
 
 cudaError_t plan_launch(const rs_kv_desc &d, const rs_ragged_desc &rd, const rs_ragged &rg, int max_len, int ctas,
                         const Form &f, void *plan, uint32_t *status, cudaStream_t s) {
-    PlanParams p = {d.Hq, d.Hk, d.Hq / d.Hk, rd.R, rd.tokens_cap, max_len, f.short_rows, ctas,
+    PlanParams p = {d.Hq, d.Hk, d.Hq / d.Hk, rd.R, rd.tokens_cap, max_len, f.short_rows, short_start(d.type == RS_KV_E4M3), ctas,
                     (long long)d.max_pages * d.page, rg, plan, status};
     attn_plan_kernel<<<1, kThreads, 0, s>>>(p);
     return cudaGetLastError();
