@@ -280,6 +280,38 @@ def test_shares_cover_the_work_once(lengths, context, Hq, Hk):
         assert biggest <= 2 * (len(places) + 4 * len(lst) * Hk * max(items_of(n) for _, _, n, _ in lst)) // 152 + 4
 
 
+@pytest.mark.parametrize("lengths,context,Hq,Hk", [
+    ([1], [0], 4, 4), ([1], [9000], 8, 2), ([1] * 7, [0, 5000, 3, 640, 64, 2000, 1], 32, 4), ([3000, 40, 1], [0, 700, 9], 6, 2),
+    ([33] * 3, [20_000, 10, 4000], 16, 1), ([1] * 200, list(range(0, 2000, 10)), 16, 2)])
+@pytest.mark.parametrize("type", ["bf16", "e4m3"])
+def test_cut_heads_are_listed_once(lengths, context, Hq, Hk, type):
+    b = Batch.__new__(Batch)
+    R, g = len(lengths), Hq // Hk
+    b.lengths = lengths
+    b.ragged = Ragged(R, sum(lengths))
+    b.ragged.plan(i32(lengths), i32(context))
+    b.cache = KVCache(Hq, Hk, 64, 10, 20_000, page=16, type=type)
+    shorts, longs, _, s_start, l_start = shares(b, max(lengths))
+    raw = b.cache.plan(b.ragged, max(lengths)).cpu().numpy()
+    ctas = len(s_start) - 1
+    at = 64 + 32 * R + 32 * (ctas + 1)
+    joins = raw[at: at + 32 * ctas].view(np.int32).reshape(2, ctas, 4)
+    tq = 2 * (128 // g)
+    for starts, lst, got, is_long in ((s_start, shorts, joins[0], False), (l_start, longs, joins[1], True)):
+        heads = {}  # of each head that a share begins within: the shares that do
+        for c in range(ctas):
+            idx, item, head, part = (int(x) for x in starts[c])
+            if idx < len(lst) and part:
+                heads.setdefault((idx, item, head), []).append(c)
+        want = np.zeros((ctas, 4), np.int32)
+        for (idx, item, head), cs in heads.items():
+            assert cs == list(range(cs[0], cs[-1] + 1)) and len({int(starts[c][3]) for c in cs}) == len(cs)
+            _, row, n, _ = (int(x) for x in lst[idx])
+            want[cs[0]] = (1 + len(cs), head, row + item * tq, min(tq, n - item * tq) if is_long else n)
+        assert np.array_equal(got[:, 0], want[:, 0])
+        assert np.array_equal(got[got[:, 0] > 0], want[want[:, 0] > 0])
+
+
 # ----------------------------------------------------------------------------- attention
 CASES = {  # lengths, context, Hq, Hk, D, page
     "one token of one": ([1], [0], 1, 1, 64, 16),
