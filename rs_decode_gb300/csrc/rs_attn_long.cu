@@ -57,7 +57,7 @@ struct Cfg {
     static constexpr int RING = QS * TILE;
     static constexpr int CODES = RING + STAGES * TILE;
     static constexpr int TILES = CODES + RAWS * RAW;       // bytes of all tiles, from a multiple of 1024 on
-    static constexpr int SMALL = 3072;                     // what lies before them
+    static constexpr int SMALL = 3 * 1024;                 // what lies before them
     static constexpr int BYTES = SMALL + TILES;
     static_assert(BYTES <= 227 * 1024, "");
     // Registers a thread by role, out of the launch's 128 each
@@ -75,7 +75,7 @@ struct Shared {
     uint64_t s_full[2], p_ready[2], pv_done[2], o_full[2], o_free[2], end;
     uint32_t tmem, abort, begun[2], begun_q[kMaxQs];      // begun: tiles of keys, of values, of codes or not
 };
-static_assert(sizeof(Shared) <= 3072, "");
+static_assert(sizeof(Shared) <= 3 * 1024, "");
 
 // ---------------------------------------------------------------- tensor cores
 __device__ __forceinline__ bool elect_one() {
