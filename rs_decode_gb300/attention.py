@@ -61,9 +61,10 @@ class KVCache:
 
     def _bytes(self, rd, max_len: int) -> rb.AttnBytes:
         key = (rd.R, rd.tokens_cap, max_len)
-        if self._sizes[0] != key:
-            self._sizes = (key, rb.rs_attn_bytes_for(self.desc, rd, max_len))
-        return self._sizes[1]
+        sizes = self._sizes  # read once: another thread may put another shape's there
+        if sizes[0] != key:
+            self._sizes = sizes = (key, rb.rs_attn_bytes_for(self.desc, rd, max_len))
+        return sizes[1]
 
     # ------------------------------------------------------------------ calls
     def write(self, ragged, k: torch.Tensor, v: torch.Tensor, pages: torch.Tensor, stream=None) -> None:
