@@ -118,9 +118,10 @@ class Layer:
     # ---------------------------------------------------------------- prefill
     def _prefill_bytes(self, rd, max_len: int) -> int:
         key = (rd.R, rd.tokens_cap, rd.block, rd.max_blocks, rd.n_free, max_len)
-        if self._prefill_size[0] != key:
-            self._prefill_size = (key, rb.rs_prefill_bytes_for(self.desc, rd, max_len))
-        return self._prefill_size[1]
+        size = self._prefill_size  # read once: another thread may put another shape's there
+        if size[0] != key:
+            self._prefill_size = size = (key, rb.rs_prefill_bytes_for(self.desc, rd, max_len))
+        return size[1]
 
     def prefill_workspace(self, ragged, max_len: int) -> torch.Tensor | None:
         """Scratch of ``prefill`` for this plan shape; may serve many calls, one after another."""

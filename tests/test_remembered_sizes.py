@@ -1,4 +1,4 @@
-"""The workspace sizes that a cache remembers from call to call, while another thread
+"""The workspace sizes that a cache or a layer remembers from call to call, while another thread
 asks the same object about another shape: each call gets its own shape's sizes."""
 from __future__ import annotations
 
@@ -8,6 +8,7 @@ import pytest
 
 from rs_decode_gb300 import binding as rb
 from rs_decode_gb300.attention import KVCache
+from rs_decode_gb300.layer import Layer
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -51,3 +52,15 @@ def test_attention_sizes(type, first):
     c.meanwhile = lambda: c._bytes(small, 1)
     got = c._bytes(large, 1000)
     assert (got.plan, got.work) == (want.plan, want.work)
+
+
+@pytest.mark.parametrize("first", [False, True])
+def test_prefill_size(first):
+    small, large = rb.RaggedDesc(2, 64, 0, 0, 0), rb.RaggedDesc(2, 4000, 0, 0, 0)
+    x = interrupted(Layer, "_prefill_size")("gdn", 2, 4, 2, 128, 128, 16, device="cpu")
+    want = rb.rs_prefill_bytes_for(x.desc, large, 4000)
+    assert want > rb.rs_prefill_bytes_for(x.desc, small, 1)
+    if not first:
+        x._prefill_bytes(large, 4000)
+    x.meanwhile = lambda: x._prefill_bytes(small, 1)
+    assert x._prefill_bytes(large, 4000) == want
