@@ -802,8 +802,8 @@ __device__ __forceinline__ void join_rows(const float *parts, size_t stride, int
     }
 }
 
-// A CTA to a boundary between two shares, and to some of its head's rows.  Latency bounds it: one look
-// into the plan, then the maxima and the first sums.  151 items of 256 rows, two parts each, take 11 us
+// A CTA to a boundary between two shares, and to some of its head's rows.  Latency bounds it: two looks
+// into the plan, beside the launch before, then the maxima and the first sums.  151 items of 256 rows, two parts each, take 11 us
 // on a cold L2; four parts of one row in flight, two of each of a long form's two rows (64 registers)
 // against 16 of one row (124): 16 prompts 417 against 437 us.
 template <int D>
@@ -813,8 +813,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     if (blockIdx.x == 0 && blockIdx.y == 0) wait_for_launch();  // this launch does not end before the one that it overlaps
     // the plan was there before the launch that this one waits for
     const PlanView v = plan_view(p.plan, p.R, p.ctas);
+    if (!plan_fits(*v.head, p)) return;  // the lists lie where this call's R says: a smaller plan ends before them
     const Join j = (lng ? v.long_join : v.short_join)[c];
-    if (!plan_fits(*v.head, p) || j.n == 0) return;
+    if (j.n == 0) return;
     const int tile_toks = tile_tokens(p.g);
     // row `in` of query tile t
     auto row = [&](int t, int in) -> uint16_t * {
