@@ -99,8 +99,8 @@ class KVCache:
 
     def plan(self, ragged, max_len: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Shares of a planned batch's attention, in ``out`` if given (an earlier plan of the
-        same shape); for all layers with these heads and page tables of this size.  No request
-        of the batch may bring more than max_len rows."""
+        same shape); for all layers with these heads, this type and page tables of this size.  No
+        request of the batch may bring more than max_len rows."""
         n = self._bytes(ragged.desc, max_len).plan
         if out is None:
             out = torch.empty(n, dtype=torch.uint8, device=self.status_word.device)

@@ -35,8 +35,8 @@ struct PlanHead {
     int n_short, n_long;    // requests of either form
     int short_rows;         // a request of at most this many rows of a key head's group is short
     int ctas, max_len;      // what the plan was made for
-    int Hq, Hk, R, cap;
-    int pad[7];
+    int Hq, Hk, R, cap, type;
+    int pad[6];
 };
 static_assert(sizeof(PlanHead) == 64, "");
 
@@ -103,7 +103,7 @@ inline Form form_of(int g, int max_len, bool e4m3) {
 __host__ __device__ inline int tile_tokens(int g) { return kTileRows / g; }  // of one query tile
 
 struct Params {
-    int Hq, Hk, g, page, page_log, n_pages, max_pages, R, cap, ctas, max_len, short_rows;
+    int Hq, Hk, g, type, page, page_log, n_pages, max_pages, R, cap, ctas, max_len, short_rows;
     const int32_t *pages;
     const uint16_t *q;
     long long ld_q;
@@ -118,7 +118,7 @@ struct Params {
 // Whether a plan is one for this call.
 __device__ __forceinline__ bool plan_fits(const PlanHead &h, const Params &p) {
     return h.short_rows == p.short_rows && h.max_len == p.max_len && h.ctas == p.ctas && h.Hq == p.Hq && h.Hk == p.Hk && h.R == p.R &&
-           h.cap == p.cap;
+           h.cap == p.cap && h.type == p.type;
 }
 
 // A part's place in the workspace: two a CTA (the end of a head that the CTA before began,

@@ -167,7 +167,7 @@ rs_status rs_attend(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *
     const int g = d->Hq / d->Hk;
     const Form f = form_of(g, in->max_len, d->type == RS_KV_E4M3);
     Params p = {};
-    p.Hq = d->Hq, p.Hk = d->Hk, p.g = g, p.page = d->page, p.page_log = ilog2(d->page);
+    p.Hq = d->Hq, p.Hk = d->Hk, p.g = g, p.type = d->type, p.page = d->page, p.page_log = ilog2(d->page);
     p.n_pages = d->n_pages, p.max_pages = d->max_pages, p.R = rd->R, p.cap = rd->tokens_cap;
     p.ctas = kCtas, p.max_len = in->max_len, p.short_rows = f.short_rows;
     p.pages = in->pages, p.q = in->q, p.ld_q = in->ld_q;

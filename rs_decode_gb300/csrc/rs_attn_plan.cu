@@ -14,7 +14,7 @@ namespace {
 constexpr int kThreads = 1024;
 
 struct PlanParams {
-    int Hq, Hk, g, R, cap, max_len, short_rows, short_start, ctas;
+    int Hq, Hk, g, type, R, cap, max_len, short_rows, short_start, ctas;
     long long keys_cap;  // keys that a request's row of the page table has room for
     rs_ragged rg;
     void *plan;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         PlanHead h = {};
         h.n_short = n_short, h.n_long = n_long, h.short_rows = p.short_rows, h.ctas = p.ctas, h.max_len = p.max_len;
-        h.Hq = p.Hq, h.Hk = p.Hk, h.R = p.R, h.cap = p.cap;
+        h.Hq = p.Hq, h.Hk = p.Hk, h.R = p.R, h.cap = p.cap, h.type = p.type;
         *v.head = h;
     }
     for (int i = threadIdx.x; i < 2 * (p.ctas + 1); i += kThreads) {
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(const __grid_consta
 
 cudaError_t plan_launch(const rs_kv_desc &d, const rs_ragged_desc &rd, const rs_ragged &rg, int max_len, int ctas,
                         const Form &f, void *plan, uint32_t *status, cudaStream_t s) {
-    PlanParams p = {d.Hq, d.Hk, d.Hq / d.Hk, rd.R, rd.tokens_cap, max_len, f.short_rows, short_start(d.type == RS_KV_E4M3), ctas,
+    PlanParams p = {d.Hq, d.Hk, d.Hq / d.Hk, d.type, rd.R, rd.tokens_cap, max_len, f.short_rows, short_start(d.type == RS_KV_E4M3), ctas,
                     (long long)d.max_pages * d.page, rg, plan, status};
     attn_plan_kernel<<<1, kThreads, 0, s>>>(p);
     return cudaGetLastError();

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from rs_decode_gb300 import binding as rb
+from rs_decode_gb300.attention import KVCache
 from rs_decode_gb300.prefill import Ragged
 from test_gpu_attention import BF16, Batch, i32
 
@@ -38,4 +39,17 @@ def test_plan_of_another_number_of_requests(type, n, small, large):
         own[: plan.numel()] = plan
         attend(b, own, q, y, n)
         assert b.cache.status() == rb.DEV_LENGTH and bool((y == 4.0).all())
+    b.check(q, b.attend(q, y=y))
+
+
+@pytest.mark.parametrize("type,other", [("bf16", "e4m3"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("Hq,Hk,n", [(8, 2, 1), (8, 2, 8), (8, 2, 9), (16, 1, 2), (40, 1, 1), (128, 2, 30)])
+def test_plan_for_a_cache_of_another_type(type, other, Hq, Hk, n):
+    """Also where both types run the same form: up to 32 rows of a group, or more than 32 heads in it."""
+    b = Batch([n, 1, 0], [300, 5, 0], Hq, Hk, 64, type, 16)
+    q = b.randn(b.cap, Hq, 64).to(BF16)
+    y = torch.full((b.cap, Hq, 64), 4.0, dtype=BF16, device="cuda")
+    plan = KVCache(Hq, Hk, 64, b.n_pages, b.max_pages, page=16, type=other).plan(b.ragged, n)
+    b.cache.attend(b.ragged, q, b.pages, plan, max_len=n, y=y)
+    assert b.cache.status() == rb.DEV_LENGTH and bool((y == 4.0).all())
     b.check(q, b.attend(q, y=y))
