@@ -123,7 +123,8 @@ __device__ __forceinline__ bool plan_fits(const PlanHead &h, const Params &p) {
 
 // A part's place in the workspace: two a CTA (the end of a head that the CTA before began,
 // and the beginning of one that the next CTA goes on with), rows of D sums, then rows of
-// (largest score, sum of weights), scores in units of log2.
+// (largest score, sum of weights), scores in units of log2.  The short form with 8 bits has the largest of
+// score plus value's exponent there, and the logarithm of the sum relative to it.
 __host__ __device__ inline size_t part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
 
 // ---------------------------------------------------------------- waits
@@ -206,6 +207,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+using f2 = unsigned long long;  // two fp32 values, the operand of paired arithmetic
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 // The power of two of an 8-bit head's scale byte (255, of a head that is not finite, gives infinity).
 __device__ __forceinline__ float pow2_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
@@ -256,7 +263,7 @@ cudaError_t short_launch(const Params &p, int D, bool e4m3, const CUtensorMap &k
                          cudaStream_t s);
 cudaError_t long_launch(const Params &p, int D, bool e4m3, const CUtensorMap &q, const CUtensorMap &k,
                         const CUtensorMap &v, cudaStream_t s);
-cudaError_t join_launch(const Params &p, int D, bool any_long, cudaStream_t s);
+cudaError_t join_launch(const Params &p, int D, bool e4m3, bool any_long, cudaStream_t s);
 cudaError_t kv_write_launch(const rs_kv_desc &d, const rs_kv &kv, const rs_ragged_desc &rd, const rs_ragged &rg,
                             const int32_t *pages, const uint16_t *k, const uint16_t *v, long long ld_k, long long ld_v,
                             uint32_t *status, cudaStream_t s);

@@ -184,7 +184,7 @@ rs_status rs_attend(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *
         e = long_launch(p, d->D, e4m3, qm, km, vm, s);
     }
     if (e == cudaSuccess && f.short_rows) e = short_launch(p, d->D, e4m3, km, vm, f.any_long, s);
-    if (e == cudaSuccess) e = join_launch(p, d->D, f.any_long, s);
+    if (e == cudaSuccess) e = join_launch(p, d->D, e4m3, f.any_long, s);
     return cuda_status(e);
 }
 

@@ -39,8 +39,6 @@ namespace rs {
 namespace attn {
 namespace {
 
-using f2 = unsigned long long;  // two fp32 values, the operand of paired arithmetic
-
 constexpr int kThreads = 512;
 
 template <int D_, bool E4M3_>
@@ -138,11 +136,6 @@ __device__ __forceinline__ void st_done() { asm volatile("tcgen05.wait::st.sync.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-    f2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {

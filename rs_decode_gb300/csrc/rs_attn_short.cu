@@ -23,7 +23,11 @@
 // queries (scaled row by row by a power of two: bf16's 8 bits fit) and weights: relative to
 // m' = max(s_j + e_j), with e_j the exponent of value j's scale, and times 2^14, so that
 // the weight times 2^e_j uses fp16's whole range: what lies 2^-28 below the
-// largest loses bits.  The sum of weights itself stays fp32 and unrounded in both.
+// largest loses bits.  The sum of weights itself stays fp32 and unrounded in both.  With 8 bits it is of
+// 2^(s_j - m' + 25), since e_j is -60 to 119: the largest of them is then 2^-94 to 2^86, and what is 2^-32 of
+// the largest still counts.  (Of 2^(s_j - m') those a little below the largest vanished beside values of 2^119.)
+// Where such sums are joined they are logarithms relative to their m', which may be far apart.  (A maximum of the scores
+// alone, kept beside m', as their reference: four drafts of 64 requests 125 us against 109, 256 tokens 196 against 185.)
 //
 // Measured (32 query heads on 4 key heads of 128): 256 tokens behind 20 to 8,000 keys each, 2.1 GB of bf16 cache,
 // 315 us, 6.7 TB/s, 0.99 of the copy peak; from an 8-bit cache 196 us, 5.5 TB/s, where the conversion and
@@ -274,6 +278,16 @@ struct Sums {
     float o[C::MT][C::N][4];  // 16 rows x (D or half of it), as the products leave them
     float m[C::MT][2], l[C::MT][2];
 };
+constexpr float kUp = 25.f;  // 8 bits: while keys are gone over, l is of weights times 2^kUp
+
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 8 bits: a part's (m', logarithm of its sum of weights), the latter relative to another m'.  A part without
+// keys has -inf for both; what is not a number stays one.
+__device__ __forceinline__ float log_sum_at(float2 part, float m) { return part.x == -INFINITY ? part.y : part.y + (part.x - m); }
 
 // The queries of a piece as operands; with 8 bits scaled to fp16, and c times what undoes it in cq.
 // Rows that the piece does not have are zeros.
@@ -438,8 +452,13 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
             for (int hf = 0; hf < 2; ++hf) {
                 const float m = fmaxf(a.m[mt][hf], top[mt][hf]);
                 const float f = m == -INFINITY ? 1.f : ex2(a.m[mt][hf] - m);
+                if constexpr (C::E4M3) {  // m' may move by more than one factor's range
+                    const float root = m == -INFINITY ? 1.f : ex2(0.5f * (a.m[mt][hf] - m));
+                    a.l[mt][hf] = a.l[mt][hf] * root * root;
+                } else {
+                    a.l[mt][hf] *= f;
+                }
                 a.m[mt][hf] = m;
-                a.l[mt][hf] *= f;
 #pragma unroll
                 for (int n = 0; n < N; ++n) a.o[mt][n][2 * hf] *= f, a.o[mt][n][2 * hf + 1] *= f;
             }
@@ -449,16 +468,34 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
     for (int mt = 0; mt < MT; ++mt) {
         float x[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int hf = 0; hf < 2; ++hf) {
+            // a row that has seen no key yet has no weights
+            const float m = a.m[mt][hf] == -INFINITY ? 0.f : a.m[mt][hf];
+            if constexpr (!C::E4M3) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // a row that has seen no key yet has no weights
-                const float below = s[mt][nt][e] - (a.m[mt][e >> 1] == -INFINITY ? 0.f : a.m[mt][e >> 1]);
-                x[nt][e] = ex2(below);
-                a.l[mt][e >> 1] += x[nt][e];
-                // at most 2^15: the reference may be 2^1 behind
-                if constexpr (C::E4M3) x[nt][e] = ex2(below + (ev[nt][e & 1] + 14.f));
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 2 * hf; e < 2 * hf + 2; ++e) {
+                        x[nt][e] = ex2(s[mt][nt][e] - m);
+                        a.l[mt][hf] += x[nt][e];
+                    }
+            } else {
+                f2 sum = 0;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const f2 below = f2_add(f2_pack(s[mt][nt][2 * hf], s[mt][nt][2 * hf + 1]), f2_pack(-m, -m));
+                    float lo, hi;
+                    f2_unpack(f2_add(below, f2_pack(kUp, kUp)), lo, hi);
+                    sum = f2_add(sum, f2_pack(ex2(lo), ex2(hi)));
+                    // at most 2^15: the reference may be 2^1 behind
+                    f2_unpack(f2_add(below, f2_pack(ev[nt][0] + 14.f, ev[nt][1] + 14.f)), lo, hi);
+                    x[nt][2 * hf] = ex2(lo), x[nt][2 * hf + 1] = ex2(hi);
+                }
+                float lo, hi;
+                f2_unpack(sum, lo, hi);
+                a.l[mt][hf] += lo + hi;
             }
+        }
 #pragma unroll
         for (int kk = 0; kk < NT / 2; ++kk)
 #pragma unroll
@@ -530,6 +567,7 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
             float l = a.l[mt][hf];
             l += __shfl_xor_sync(~0u, l, 1);
             l += __shfl_xor_sync(~0u, l, 2);
+            if constexpr (C::E4M3) l = lg2(l) - kUp;
             // two warps of the same keys have the same
             if (t == 0 && place < SUMS) ml[place * C::ROWS + mt * 16 + hf * 8 + g] = make_float2(a.m[mt][hf], l);
         }
@@ -553,13 +591,23 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
         float m = -INFINITY, l = 0.f;
 #pragma unroll
         for (int w = 0; w < SUMS; ++w) m = fmaxf(m, ml[w * C::ROWS + x].x);
+        float most = -INFINITY;  // 8 bits: the largest logarithm, which l is relative to
+        if constexpr (C::E4M3) {
+#pragma unroll
+            for (int w = 0; w < SUMS; ++w) most = fmaxf(most, log_sum_at(ml[w * C::ROWS + x], m));
+            if (most == -INFINITY) most = 0.f;  // no weights: a sum of 0, not of what -inf less -inf is
+        }
 #pragma unroll
         for (int w = 0; w < SUMS; ++w) {
             const float2 v = ml[w * C::ROWS + x];
             // a sum that is not a number stays one
-            l += v.x == -INFINITY ? v.y : v.y * ex2(v.x - m);
+            if constexpr (C::E4M3)
+                l += ex2(log_sum_at(v, m) - most);
+            else
+                l += v.x == -INFINITY ? v.y : v.y * ex2(v.x - m);
         }
-        const float inv = 1.f / l;
+        const float inv = 1.f / l, back = C::E4M3 ? ex2(-most) : 1.f;
+        if constexpr (C::E4M3) l = lg2(l) + most;
         const int token = x / p.g, in_group = x - token * p.g;
         uint16_t *const y = p.y + ((long long)(rq.y + token) * p.Hq + head * p.g + in_group) * D;
         if (!whole && col == 0 && x < rows) reinterpret_cast<float2 *>(to_parts + (size_t)C::ROWS * D)[x] = make_float2(m, l);
@@ -590,7 +638,7 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
                 const int d = C::E4M3 ? (D / 8) * (col >> 2) + part * C::N + 4 * c + (col & 3) : part * (D / C::PARTS) + c * kPass + col;
                 if (x < rows) {
                     if (whole)
-                        *reinterpret_cast<uint32_t *>(y + d) = pack_bf(sum.x * inv, sum.y * inv);
+                        *reinterpret_cast<uint32_t *>(y + d) = pack_bf(sum.x * inv * back, sum.y * inv * back);
                     else
                         *reinterpret_cast<float2 *>(to_parts + (size_t)x * D + d) = sum;
                 }
@@ -701,7 +749,8 @@ constexpr int kShortBlocks = 2, kLongBlocks = 16;  // CTAs to a head's 32 rows, 
 // Rows x0, x0 + dx .. (NR of them, those with y) of a head that CTA c - 1's share ends with and the
 // shares c, c + 1 .. begin with: n parts in the order of its keys, stride floats from CTA to CTA.  A warp's
 // work, D / 32 channels a lane, the sums of U parts in flight, the first of them with the maxima.
-template <int D, int NR, int U>
+// LOG: with logarithms of the sums of weights (the short form's with 8 bits).
+template <int D, int NR, int U, bool LOG>
 __device__ __forceinline__ void join_rows(const float *parts, size_t stride, int c, int n, int rows, int x0, int dx, uint16_t *const (&y)[NR]) {
     constexpr int V = D / 32;
     const int lane = threadIdx.x & 31;
@@ -727,14 +776,17 @@ __device__ __forceinline__ void join_rows(const float *parts, size_t stride, int
             }
     };
     auto max_sum = [&](int k, int r) {
-        return k < n && y[r] ? reinterpret_cast<const float2 *>(part(k) + (size_t)rows * D)[x0 + r * dx] : make_float2(-INFINITY, 0.f);
+        return k < n && y[r] ? reinterpret_cast<const float2 *>(part(k) + (size_t)rows * D)[x0 + r * dx] : make_float2(-INFINITY, LOG ? -INFINITY : 0.f);
     };
-    auto put = [&](const float (&sum)[V], float l, uint16_t *to) {
-        const float inv = 1.f / l;
+    // most: the logarithm that l is relative to
+    auto put = [&](float (&sum)[V], float l, float most, uint16_t *to) {
+        const float inv = 1.f / l, back = LOG ? ex2(-most) : 1.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] = sum[i] * inv * back;
         if constexpr (V == 4)
-            *reinterpret_cast<uint2 *>(to + lane * 4) = make_uint2(pack_bf(sum[0] * inv, sum[1] * inv), pack_bf(sum[2] * inv, sum[3] * inv));
+            *reinterpret_cast<uint2 *>(to + lane * 4) = make_uint2(pack_bf(sum[0], sum[1]), pack_bf(sum[2], sum[3]));
         else
-            *reinterpret_cast<uint32_t *>(to + lane * 2) = pack_bf(sum[0] * inv, sum[1] * inv);
+            *reinterpret_cast<uint32_t *>(to + lane * 2) = pack_bf(sum[0], sum[1]);
     };
     if (n <= U) {  // most heads: every lane reads all maxima
         float2 ml[NR][U];
@@ -745,22 +797,29 @@ __device__ __forceinline__ void join_rows(const float *parts, size_t stride, int
         load(0);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            float m = -INFINITY, l = 0.f, sum[V] = {};
+            float m = -INFINITY, most = -INFINITY, l = 0.f, sum[V] = {};
 #pragma unroll
             for (int u = 0; u < U; ++u) m = fmaxf(m, ml[r][u].x);
+            if constexpr (LOG) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) most = fmaxf(most, log_sum_at(ml[r][u], m));
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const float f = ml[r][u].x == -INFINITY ? 1.f : ex2(ml[r][u].x - m);
-                l = fmaf(ml[r][u].y, f, l);
+                if constexpr (LOG)
+                    l += ex2(log_sum_at(ml[r][u], m) - most);
+                else
+                    l = fmaf(ml[r][u].y, f, l);
 #pragma unroll
                 for (int i = 0; i < V; ++i) sum[i] = fmaf(f, o[r][u][i], sum[i]);
             }
-            if (y[r]) put(sum, l, y[r]);
+            if (y[r]) put(sum, l, most, y[r]);
         }
         return;
     }
     float2 ml[NR];
-    float m[NR], l[NR], sum[NR][V];
+    float m[NR], most[NR], l[NR], sum[NR][V];
 #pragma unroll
     for (int r = 0; r < NR; ++r) ml[r] = max_sum(lane, r);
     load(0);
@@ -770,6 +829,12 @@ __device__ __forceinline__ void join_rows(const float *parts, size_t stride, int
         for (int k = 32 + lane; k < n; k += 32) m[r] = fmaxf(m[r], max_sum(k, r).x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m[r] = fmaxf(m[r], __shfl_xor_sync(~0u, m[r], d));
+        most[r] = -INFINITY;
+        if constexpr (LOG) {
+            for (int k = lane; k < n; k += 32) most[r] = fmaxf(most[r], log_sum_at(k < 32 ? ml[r] : max_sum(k, r), m[r]));
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) most[r] = fmaxf(most[r], __shfl_xor_sync(~0u, most[r], d));
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) sum[r][i] = 0.f;
     }
@@ -780,7 +845,10 @@ __device__ __forceinline__ void join_rows(const float *parts, size_t stride, int
             if (k0) ml[r] = max_sum(k0 + lane, r);
             // a part without keys that the row sees has sums of zero
             f[r] = k0 + lane >= n ? 0.f : ml[r].x == -INFINITY ? 1.f : ex2(ml[r].x - m[r]);
-            l[r] += ml[r].y * f[r];
+            if constexpr (LOG)
+                l[r] += k0 + lane >= n ? 0.f : ex2(log_sum_at(ml[r], m[r]) - most[r]);
+            else
+                l[r] += ml[r].y * f[r];
         }
         for (int k = k0; k < min(k0 + 32, n); k += U) {
             if (k) load(k);
@@ -798,7 +866,7 @@ __device__ __forceinline__ void join_rows(const float *parts, size_t stride, int
     for (int r = 0; r < NR; ++r) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) l[r] += __shfl_xor_sync(~0u, l[r], d);
-        if (y[r]) put(sum[r], l[r], y[r]);
+        if (y[r]) put(sum[r], l[r], most[r], y[r]);
     }
 }
 
@@ -806,7 +874,7 @@ __device__ __forceinline__ void join_rows(const float *parts, size_t stride, int
 // into the plan, beside the launch before, then the maxima and the first sums.  151 items of 256 rows, two parts each, take 11 us
 // on a cold L2; four parts of one row in flight, two of each of a long form's two rows (64 registers)
 // against 16 of one row (124): 16 prompts 417 against 437 us.
-template <int D>
+template <int D, bool E4M3>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
     const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, shorts = p.short_rows ? kShortBlocks : 0;
     const bool lng = blockIdx.y >= shorts;
@@ -827,12 +895,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     if (lng) {
         for (int x = (blockIdx.y - shorts) * kJoinWarps + warp; x < kTileRows; x += kLongBlocks * kJoinWarps) {
             uint16_t *const y[2] = {row(0, x), row(1, x)};
-            if (y[0]) join_rows<D, 2, 2>(p.long_parts, part_floats(2 * kTileRows, D), c, j.n, 2 * kTileRows, x, kTileRows, y);
+            if (y[0]) join_rows<D, 2, 2, false>(p.long_parts, part_floats(2 * kTileRows, D), c, j.n, 2 * kTileRows, x, kTileRows, y);
         }
     } else {
         for (int x = blockIdx.y * kJoinWarps + warp; x < p.short_rows; x += kShortBlocks * kJoinWarps) {
             uint16_t *const y[1] = {row(0, x)};
-            if (y[0]) join_rows<D, 1, 4>(p.short_parts, part_floats(p.short_rows, D), c, j.n, p.short_rows, x, 0, y);
+            if (y[0]) join_rows<D, 1, 4, E4M3>(p.short_parts, part_floats(p.short_rows, D), c, j.n, p.short_rows, x, 0, y);
         }
     }
 }
@@ -858,14 +926,15 @@ cudaError_t short_launch(const Params &p, int D, bool e4m3, const CUtensorMap &k
     return e4m3 ? launch_rows<128, true>(p, k, v, early, s) : launch_rows<128, false>(p, k, v, early, s);
 }
 
-cudaError_t join_launch(const Params &p, int D, bool any_long, cudaStream_t s) {
+cudaError_t join_launch(const Params &p, int D, bool e4m3, bool any_long, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.ctas - 1, (p.short_rows ? kShortBlocks : 0) + (any_long ? kLongBlocks : 0)), cfg.blockDim = dim3(kJoinWarps * 32), cfg.stream = s;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr, cfg.numAttrs = 1;
-    return D == 64 ? cudaLaunchKernelEx(&cfg, join_kernel<64>, p) : cudaLaunchKernelEx(&cfg, join_kernel<128>, p);
+    if (D == 64) return cudaLaunchKernelEx(&cfg, e4m3 ? join_kernel<64, true> : join_kernel<64, false>, p);
+    return cudaLaunchKernelEx(&cfg, e4m3 ? join_kernel<128, true> : join_kernel<128, false>, p);
 }
 
 }  // namespace attn
