@@ -612,7 +612,8 @@ typedef struct {
  * around a request may change the order of its sums.
  * What lies in a page behind a request's last key is never used, whatever it
  * holds.  A NaN or an infinity in k or q reaches the rows that see it; one in v
- * may, besides them, reach the request's own rows up to 127 positions before it.
+ * may, besides them, reach the request's own rows up to 126 + T positions before
+ * it, T = 128 / (Hq / Hk) rounded down (254 with a query head to each key head).
  * Source: none (the pages treat the recurrent layers alone). */
 rs_status rs_attend(const rs_kv_desc *d, const rs_kv *kv, const rs_ragged_desc *rd, const rs_ragged *rg, const rs_attn *in,
                     const void *plan, uint16_t *y, void *work, uint32_t *status, void *stream);
