@@ -278,7 +278,10 @@ struct Sums {
     float o[C::MT][C::N][4];  // 16 rows x (D or half of it), as the products leave them
     float m[C::MT][2], l[C::MT][2];
 };
-constexpr float kUp = 25.f;  // 8 bits: while keys are gone over, l is of weights times 2^kUp
+// 8 bits: exponents of values' scales are held less 16, so that m' of scores far from 0, where it can only be rounded (up),
+// is a score itself for values up to 2^25: the products' weights then lose range, not their meaning.
+constexpr float kBias = 127.f + 16.f;
+constexpr float kUp = 9.f;  // while keys are gone over, l is of weights times 2^kUp, 2^25 without that 16
 
 __device__ __forceinline__ float lg2(float x) {
     float y;
@@ -393,7 +396,7 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float up = __uint_as_float(e ? (kb & 0xff00u) << 15 : (kb & 0xffu) << 23);
-                ev[nt][e] = (float)(e ? vb >> 8 : vb & 0xffu) - 127.f;
+                ev[nt][e] = (float)(e ? vb >> 8 : vb & 0xffu) - kBias;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     s[mt][nt][e] *= up * cq[mt][0];
@@ -438,12 +441,12 @@ __device__ __forceinline__ void compute(Sums<C> &a, const uint32_t (&q)[C::MT][C
             float x = -INFINITY;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                x = C::E4M3 ? fmaxf(x, fmaxf(s[mt][nt][2 * hf] + ev[nt][0], s[mt][nt][2 * hf + 1] + ev[nt][1]))
+                x = C::E4M3 ? fmaxf(x, fmaxf(__fadd_ru(s[mt][nt][2 * hf], ev[nt][0]), __fadd_ru(s[mt][nt][2 * hf + 1], ev[nt][1])))
                             : fmaxf(x, fmaxf(s[mt][nt][2 * hf], s[mt][nt][2 * hf + 1]));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
             top[mt][hf] = x;
-            behind = behind || x > a.m[mt][hf] + kBehind;
+            behind = behind || x - a.m[mt][hf] > kBehind;
         }
     if (__any_sync(~0u, behind)) {
 #pragma unroll
@@ -584,7 +587,7 @@ __device__ __forceinline__ void finish(const Params &p, Sums<C> &a, const int4 &
 #pragma unroll
             for (int w = 0; w < SUMS; ++w) m = fmaxf(m, ml[w * C::ROWS + mt * 16 + hf * 8 + g].x);
             f[hf] = a.m[mt][hf] == -INFINITY ? 0.f : ex2(a.m[mt][hf] - m);
-            if (C::E4M3) f[hf] *= 6.103515625e-5f;  // 2^-14
+            if (C::E4M3) f[hf] *= 4.f;  // 2^16 of the values' exponents, 2^-14 of the weights
         }
         // a thread's row and pair of channels of what is joined
         const int row = threadIdx.x >> 4, col = (threadIdx.x & 15) * 2, x = mt * 16 + row;
