@@ -578,13 +578,17 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
 }
 
 // ---------------------------------------------------------------- a thread a row
+// A row's weights are 2^(c s - M), M = c m rounded up: 1 at most, all of them relative to the M that there is.  From here
+// on the rounding could leave nothing of the largest.  But there scores that are not equal lie 2^6 and more apart (2^-24 of
+// themselves): with c rounded down to a power of two c m is exact, the largest weight 1, and others 2^-32 at most.
+constexpr float kFar = 1073741824.f;  // 2^30
 template <class C>
 __device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int i, Shared *b) {
     constexpr int D = C::D;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t t_s = b->tmem + lanes + i * 128, t_o = b->tmem + lanes + 256 + i * D;
-    const f2 c2 = f2_pack(p.c, p.c);
+    auto is_far = [&](float m) { return fabsf(m) * p.c >= kFar; };
     unsigned count = 0, ended = 0;  // key tiles of this place so far, pieces
     Walk w;
     w.begin(p, v);
@@ -627,7 +631,8 @@ __device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int
                     // O waits for its last product, then takes the new reference
                     if (!wait_warp(b->pv_done + i, (count - 1) & 1, &b->abort, p.status)) return false;
                     tc_fence_after_sync();
-                    const float f = behind ? ex2((m - most) * p.c) : 1.f;
+                    const float by = is_far(m) || is_far(most) ? (m - most) * p.c : __fmul_ru(m, p.c) - __fmul_ru(most, p.c);
+                    const float f = behind ? ex2(by) : 1.f;
                     if (behind) m = most;
                     const f2 ff = f2_pack(f, f);
                     l2 = f2_mul(l2, ff);
@@ -643,8 +648,9 @@ __device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int
                 }
             }
             // a row that has seen no key yet has no weights
-            const float mc = m == -INFINITY ? 0.f : -m * p.c;
-            const f2 mc2 = f2_pack(mc, mc);
+            const float cr = is_far(m) ? __uint_as_float(__float_as_uint(p.c) & 0x7f800000u) : p.c;
+            const float mc = m == -INFINITY ? 0.f : -__fmul_ru(m, cr);
+            const f2 c2 = f2_pack(cr, cr), mc2 = f2_pack(mc, mc);
             f2 sum[2] = {0, 0};
 #pragma unroll
             for (int c = 0; c < 128; c += 64) {
@@ -677,7 +683,7 @@ __device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int
                 ++ended;
                 float l, l_hi;
                 f2_unpack(l2, l, l_hi);
-                b->ml[i][row] = make_float2(m == -INFINITY ? m : m * p.c, l + l_hi);
+                b->ml[i][row] = make_float2(__fmul_ru(m, p.c), l + l_hi);
             }
             st_done();
             tc_fence_before_sync();

@@ -18,6 +18,9 @@ pytestmark = pytest.mark.gpu
 BATCHES = {  # new rows and keys before them of each request
     "tokens": ([1, 1, 1], [3000, 70, 900]),
     "drafts": ([4, 3, 4], [5000, 70, 300]),
+    "a turn": ([40], [9000]),
+    "turns": ([90, 40, 3, 130], [700, 3000, 1000, 0]),
+    "a prompt": ([1500], [0]),
 }
 
 
