@@ -725,25 +725,26 @@ long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
     __syncthreads();
     tc_fence_after_sync();
     if (mine) {
-        bool ok = true;
         if (warp < 8) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::ROW_REGS));
             row_role<C>(p, v, warp >> 2, b);
         } else if (warp < 12) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::ISSUE_REGS));
-            if (warp == 8) ok = product_role<C>(p, v, sm, b);
+            if (warp == 8) product_role<C>(p, v, sm, b);
             if (warp == 9 || warp == 10) copy_role<C>(p, v, &qm, &km, &vm, sm, b, warp - 9);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::HELP_REGS));
             help_role<C>(p, v, sm, b);
         }
-        if (warp == 8 && !ok) {  // products still in flight; elect_one() names the lane that issued them
+    }
+    tc_fence_before_sync();
+    if (__syncthreads_or(*const_cast<volatile uint32_t *>(&b->abort))) {
+        if (warp == 8) {  // products still in flight, also where their warp did not give up; elect_one() names the lane that issued them
             commit(&b->end, elect_one());
             mbar_wait(&b->end, 0);
         }
+        if (threadIdx.x == 0) drain<C>(b);
     }
-    tc_fence_before_sync();
-    if (__syncthreads_or(*const_cast<volatile uint32_t *>(&b->abort)) && threadIdx.x == 0) drain<C>(b);
     __syncthreads();
     tc_fence_after_sync();
     if (warp == 8) tmem_dealloc(b->tmem, 512);
