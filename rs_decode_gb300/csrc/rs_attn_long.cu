@@ -71,7 +71,7 @@ struct Shared {
     uint64_t raw_full[kMaxRaws], raw_empty[kMaxRaws];     // tiles of codes
     uint64_t q_full[kMaxQs], q_empty[kMaxQs];
     uint64_t s_full[2], p_ready[2], pv_done[2], o_full[2], o_free[2], end;
-    uint32_t tmem, abort, begun[2], begun_q[kMaxQs];      // begun: tiles of keys, of values, of codes or not
+    uint32_t tmem, abort, ended, begun[2], begun_q[kMaxQs];  // ended: no product in flight; begun: tiles of keys, of values, of codes or not
 };
 static_assert(sizeof(Shared) <= 3 * 1024, "");
 
@@ -725,21 +725,27 @@ long_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMa
     __syncthreads();
     tc_fence_after_sync();
     if (mine) {
+        bool ok = true;
         if (warp < 8) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::ROW_REGS));
             row_role<C>(p, v, warp >> 2, b);
         } else if (warp < 12) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::ISSUE_REGS));
-            if (warp == 8) product_role<C>(p, v, sm, b);
+            if (warp == 8) ok = product_role<C>(p, v, sm, b);
             if (warp == 9 || warp == 10) copy_role<C>(p, v, &qm, &km, &vm, sm, b, warp - 9);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::HELP_REGS));
             help_role<C>(p, v, sm, b);
         }
+        if (warp == 8 && !ok) {  // products still in flight; elect_one() names the lane that issued them
+            commit(&b->end, elect_one());
+            mbar_wait(&b->end, 0);
+        }
+        if (warp == 8) b->ended = !ok;  // (with the wait for all of them behind the barrier the product role spills: 16 prompts 487 us)
     }
     tc_fence_before_sync();
     if (__syncthreads_or(*const_cast<volatile uint32_t *>(&b->abort))) {
-        if (warp == 8) {  // products still in flight, also where their warp did not give up; elect_one() names the lane that issued them
+        if (warp == 8 && !b->ended) {  // another warp gave up: the last products may be in flight all the same
             commit(&b->end, elect_one());
             mbar_wait(&b->end, 0);
         }
