@@ -601,7 +601,10 @@ typedef struct {
  * batch's own rows have to be in the cache (rs_kv_write before, on the same
  * stream).  Scores, sums and their joining are fp32; the weights are rounded to
  * bf16 (fp16 for few rows on an 8-bit cache) before they meet the values, y
- * once.  Rows of requests without attention in the plan, and rows past the
+ * once.  Weights go up to 2^8 within the sums: where values add up to 2^119 and more
+ * y may not be finite (few rows on an 8-bit cache take values to the end of the range).
+ * The batch is the plan's, and rg only checked: after another rs_ragged_plan a
+ * new plan is needed.  Rows of requests without attention in the plan, and rows past the
  * batch, are left as they are.  plan: from rs_attn_plan for the same Hq, Hk, type, R,
  * tokens_cap and max_len (RS_DEV_LENGTH otherwise, and y is left).  Where an entry of
  * a request's page table is outside 0..n_pages-1 (RS_DEV_SLOT), the request's

@@ -120,7 +120,9 @@ class KVCache:
         """Causal attention of the planned rows, q [rows, Hq, D] bf16 (rows at any stride), over
         their requests' cached keys, the batch's own among them (``write`` comes first).  scale
         is D ** -0.5 unless given.  Returns y torch.bfloat16 [rows, Hq, D].  Without y and work
-        they are allocated on the current stream, which then has to be the one the call runs on."""
+        they are allocated on the current stream, which then has to be the one the call runs on;
+        rows that the batch does not fill are then undefined.  The batch is the plan's: after
+        another ``ragged.plan`` it has to be made anew."""
         rd = ragged.desc
         T, Hq, D = rd.tokens_cap, self.Hq, self.D
         self._on_device("q pages plan ragged y work", q, pages, plan, ragged.counts, y, work)

@@ -26,7 +26,7 @@ constexpr int kCtas = 152;       // shares of the work: one CTA for each SM of t
 // What starting a piece costs, in keys' blocks or tiles: its queries, its epilogue.  About 3 us in the short form, four
 // blocks of bf16 and seven of 8 bits: with 1, 4 and 7 blocks 64 requests of four drafts took 97, 88 and 89 us and one
 // request on 131,072 keys 56, 56 and 59; 256 requests on an 8-bit cache 216, 204 and 196, 33 of 64 heads on 8 there 89, 87
-// and 79.  With 1, 2, 3 and 4 tiles 16 prompts took 476, 417, 431 and 443.
+// and 79.  With 1, 2 and 3 tiles, timed in turns, 16 prompts took 535, 457 and 465 us, a mixed batch of 40 262, 257 and 260.
 inline int short_start(bool e4m3) { return e4m3 ? 7 : 4; }
 constexpr int kLongStart = 2;
 
@@ -86,9 +86,11 @@ struct Form {
 };
 // Up to 32 rows of a group (a token's heads that share a key head, or a few drafts') stay in
 // the registers of warps' matrix instructions.  Where longer requests are expected beside them, a bf16
-// cache's tokens run as tiles too: a key tile of a single query tile is bound by HBM there
-// (1.7 us against 1.4 at the copy's rate), and a launch is saved.  With 8 bits the tiles are bound by
-// the conversion of the codes (2.1 us a key tile against 0.7), and the short form is kept.
+// cache's tokens run as tiles too, which saves a launch: 16 tokens beside 8 prompts of 900 107 us against 109 with
+// both forms, a mixed batch of 40 257 against 258.  But a key tile of a single query tile takes 1.7 us, 1.4 at the copy's
+// rate: 255 tokens behind 20 to 8,000 keys beside a chunk of 512 rows take 411 us so and 356 with both, which a rule that
+// counts the requests could have.  With 8 bits the tiles are bound by the conversion of the codes (2.1 us a key tile
+// against 0.7), and the short form is kept.
 inline Form form_of(int g, int max_len, bool e4m3) {
     Form f;
     const long long rows = (long long)g * max_len;

@@ -27,9 +27,9 @@
 //
 // TMEM columns: S_0 [0, 128), S_1 [128, 256), O_0 [256, 256 + D), O_1 after it.
 //
-// Measured (D = 128): a prompt of 32,768 tokens, 16 query heads on 2 key heads, 2.6 ms, 1,690 TFLOP/s, 0.86 of the measured
-// product rate; 16 prompts of 27,711 tokens in all, 32 on 4 heads, 417 us, 1,280 TFLOP/s (about 4 us of each
-// item of 32 tokens and a key head are its start and end).  A key tile of two query tiles takes 2,900 clocks: the products
+// Measured (D = 128): a prompt of 32,768 tokens, 16 query heads on 2 key heads, 2.74 to 2.82 ms, 1,560 to 1,600 TFLOP/s, 0.80 to
+// 0.82 of the measured product rate; 16 prompts of 27,711 tokens in all, 32 on 4 heads, 434 to 455 us, 1,170 to 1,230 TFLOP/s
+// (both go with the card's power; about 4 us of each item of 32 tokens and a key head are its start and end).  A key tile of two query tiles takes 2,900 clocks: the products
 // 2,600 of them (34 clocks for each 64 columns, 50 where both operands are in shared memory), the rest the
 // product warp's waits and commits.  A row's register work is 1,500 clocks a tile.  Where one query tile is all, 1.7 us a key
 // tile of 64 KiB from HBM (1.4 at the copy's rate); from an 8-bit cache 2.0, which the conversion takes.

@@ -19,7 +19,8 @@
 //
 // From a bf16 cache the weights are rounded to bf16 for their product with the values,
 // which the product's types ask for: 2^-8 of each weight at most, as y's own rounding,
-// and on average less.  From an 8-bit cache the codes become fp16, exactly, and so
+// and on average less.  (What is left of them as a second bf16 term would leave y's own rounding alone, but four drafts of
+// 64 requests take 99 us with it against 85, 256 tokens 318 against 313.)  From an 8-bit cache the codes become fp16, exactly, and so
 // queries (scaled row by row by a power of two: bf16's 8 bits fit) and weights: relative to
 // m' = max(s_j + e_j), with e_j the exponent of value j's scale, and times 2^14, so that
 // the weight times 2^e_j uses fp16's whole range: what lies 2^-28 below the
@@ -30,9 +31,9 @@
 // alone, kept beside m', as their reference: four drafts of 64 requests 125 us against 109, 256 tokens 196 against 185.)
 //
 // Measured (32 query heads on 4 key heads of 128): 256 tokens behind 20 to 8,000 keys each, 2.1 GB of bf16 cache,
-// 315 us, 6.7 TB/s, 0.99 of the copy peak; from an 8-bit cache 196 us, 5.5 TB/s, where the conversion and
+// 312 us, 6.8 TB/s, the copy peak; from an 8-bit cache 193 us, 5.6 TB/s, where the conversion and
 // the products' own chain bound it (0.43 us a block of 64 keys against 0.37 at the copy's rate); four drafts of 64
-// requests 88 us, 4.8 TB/s.  One token behind 131,071 keys 56 us and four behind 50 to 900 each 10 to 15 us: there
+// requests 85 us, 4.9 TB/s, on 8 bits 109.  One token behind 131,071 keys 54 us and four behind 50 to 900 each 10 us: there
 // the launches, a start of dependent loads, and the joining of parts.
 #include "rs_attn.cuh"
 
