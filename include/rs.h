@@ -602,7 +602,8 @@ typedef struct {
  * stream).  Scores, sums and their joining are fp32; the weights are rounded to
  * bf16 (fp16 for few rows on an 8-bit cache) before they meet the values, y
  * once.  Weights go up to 2^8 within the sums: where values add up to 2^119 and more
- * y may not be finite (few rows on an 8-bit cache take values to the end of the range).
+ * y may not be finite (few rows on an 8-bit cache take values to the end of the
+ * range, but with scores past 2^27 only up to 2^25: y may be 0 there).
  * The batch is the plan's, and rg only checked: after another rs_ragged_plan a
  * new plan is needed.  Rows of requests without attention in the plan, and rows past the
  * batch, are left as they are.  plan: from rs_attn_plan for the same Hq, Hk, type, R,
