@@ -29,8 +29,8 @@
 //
 // Measured (D = 128): a prompt of 32,768 tokens, 16 query heads on 2 key heads, 2.74 to 2.82 ms, 1,560 to 1,600 TFLOP/s, 0.80 to
 // 0.82 of the measured product rate; 16 prompts of 27,711 tokens in all, 32 on 4 heads, 434 to 455 us, 1,170 to 1,230 TFLOP/s
-// (both go with the card's power; about 4 us of each item of 32 tokens and a key head are its start and end).  A key tile of two query tiles takes 2,900 clocks: the products
-// 2,600 of them (34 clocks for each 64 columns, 50 where both operands are in shared memory), the rest the
+// (both go with the card's power; about 4 us of each item of 32 tokens and a key head are its start and end).  A key tile
+// of two query tiles takes 2,900 clocks: the products 2,600 of them (34 clocks for each 64 columns, 50 where both operands are in shared memory), the rest the
 // product warp's waits and commits.  A row's register work is 1,500 clocks a tile.  Where one query tile is all, 1.7 us a key
 // tile of 64 KiB from HBM (1.4 at the copy's rate); from an 8-bit cache 2.0, which the conversion takes.
 #include "rs_attn.cuh"
@@ -578,9 +578,10 @@ __device__ __forceinline__ bool product_role(const Params &p, const PlanView &v,
 }
 
 // ---------------------------------------------------------------- a thread a row
-// A row's weights are 2^(c s - M), M = c m rounded up: 1 at most, all of them relative to the M that there is.  From here
-// on the rounding could leave nothing of the largest.  But there scores that are not equal lie 2^6 and more apart (2^-24 of
-// themselves): with c rounded down to a power of two c m is exact, the largest weight 1, and others 2^-32 at most.
+// A row's weights are 2^(c s - M) with m its reference and M = c m rounded up, so that m's own is 1 at most, and all of
+// them are relative to the M that there is.  From here on the rounding could leave nothing of it.  But there scores that are
+// not equal lie 2^6 and more apart (2^-24 of themselves), so that m is the largest: with c rounded down to a power of two
+// c m is exact, the largest weight is 1, and others are 2^-32 at most.
 constexpr float kFar = 1073741824.f;  // 2^30
 template <class C>
 __device__ __forceinline__ bool row_role(const Params &p, const PlanView &v, int i, Shared *b) {
